@@ -412,11 +412,113 @@ qkv_status qkv_ffn_graph_create(int32_t hidden, int32_t n_ff, int32_t w_dtype, i
 qkv_status qkv_model_graph_kernel_count(const qkv_graph* graph, int32_t* out);
 void qkv_model_graph_destroy(qkv_graph* graph);
 
+/* ---- paged cache: store, attention of one new token, eviction ------------------ */
+
+/* The page "07 · The allocator: liveness, buffer reuse, and the KV cache", §2.5, gives one
+ * contiguous K and V region per layer and sequence.  Serving many sequences, the same rows of
+ * nkt values live in pages of two pools per layer that all sequences share; the pages have no
+ * counterpart of what follows.  Slot s of sequence b is row s % page_size of page
+ * page_table[b * max_pages + s / page_size]; element (head h, d) of a row is at h*hd + d.  A
+ * sequence's capacity is max_pages * page_size slots.  A layer's contiguous regions are the
+ * case of one page of n_ctx slots (n_pages = max_pages = n_seq = 1, page_size = n_ctx, a table
+ * holding 0), so qkv_decode_step and qkv_prefill_step fill a cache that these calls read.
+ *
+ * Only table entries of slots that a call touches are read; the others may hold anything.  An
+ * entry outside [0, n_pages), a length outside [0, capacity] or a sequence index >= n_seq sets
+ * bit 2 (value 4) of the device status flags, a slot outside the capacity bit 0 (see
+ * qkv_check_device_error); what it would have addressed is neither read nor written.
+ * The element type, nkt and hd are the plan's (kv_dtype, n_head_kv, head_dim); its n_ctx is not
+ * used.  All calls are asynchronous, allocate nothing and can be captured. */
+typedef struct qkv_paged_kv {
+    void* k;                   /* device, n_pages pages of page_size rows of nkt elements */
+    void* v;
+    const int32_t* page_table; /* device, n_seq x max_pages */
+    int32_t n_pages;           /* >= 1 */
+    int32_t page_size;         /* >= 1 */
+    int32_t n_seq;             /* >= 1 */
+    int32_t max_pages;         /* >= 1; max_pages * page_size < 2^31 */
+    int64_t page_stride;       /* elements from one page to the next, >= page_size * nkt; 0: that */
+    float* slot_weight;        /* device, n_seq x nkv x capacity, or null: running attention weights */
+    int32_t* slot_pos;         /* device, n_seq x nkv x capacity, or null: position held by each slot */
+} qkv_paged_kv;
+
+/* Finish the projections of nt tokens of any sequences and store them: per token t
+ *   z = Y[t] + bias; with norm weights, each head of q and k becomes
+ *   z * w / sqrt((1/hd) sum_i z_i^2 + eps) (as in qkv_decode_step_qknorm); q and k are rotated at
+ *   d_positions[t]; q goes to row t of q, k and v to slot d_slots[t] of sequence d_seqs[t].
+ * The same f32 operations as qkv_epilogue: without norms the outputs are the same bits.
+ *   Y        device, nt rows q | k | v of R values, y_dtype F32 or BF16, y_stride >= R elements apart.
+ *   bias     device, R floats, or null (no bias).
+ *   q_norm_w, k_norm_w device, hd floats each, or both null (no norm; eps is then ignored).
+ *   d_positions device, nt int32: any values.
+ *   d_seqs   device, nt int32, or null: token t belongs to sequence t (nt <= n_seq).  A negative
+ *            index marks padding: nothing of that token is written.
+ *   d_slots  device, nt int32, or null: the slot is the position.
+ *   q        device, nt rows of nqt floats, q_stride >= nqt apart; may be Y itself (F32, the same stride).
+ * slot_pos, where the cache has it, receives the position for every kv head, slot_weight zero.
+ * A token whose slot, sequence or page is out of range still gets its q row.  Two tokens of a
+ * call must not name the same slot of the same sequence.  nt == 0 returns QKV_OK without a launch.
+ * Errors: INVALID_ARG, UNSUPPORTED (y_dtype), CUDA. */
+qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache, const void* Y, int32_t y_dtype,
+                                int64_t y_stride, int32_t nt, const float* bias, const float* q_norm_w,
+                                const float* k_norm_w, float eps, const int32_t* d_positions,
+                                const int32_t* d_seqs, const int32_t* d_slots, float* q, int64_t q_stride,
+                                void* stream);
+
+/* Attention of one new token per sequence over its cached slots (the new token's own slot, stored
+ * before, among them).  For sequence b and q head h, kv head h / (nh / nkv):
+ *   s_j = scale * sum_d q[b][h][d] K[j][d],  j in [max(0, len - window), len)  (window 0: all),
+ *   out[b][h] = sum_j softmax(s)_j V[j],     lse[b][h] = log sum_j exp(s_j).
+ * A sequence of length 0 gets zeros (lse -inf).  Needs n_head % n_head_kv == 0.
+ *   q       device, n_seq rows of nqt floats, q_stride >= nqt apart.
+ *   d_lens  device, n_seq int32.  An out-of-range length counts as 0.
+ *   out     device, n_seq rows of nqt values, out_dtype F32 or BF16 (rounded once), out_stride apart.
+ *   lse     device, n_seq x nh floats, or null.
+ *   add_weight non-zero: slot_weight[b][kv head][j] += the sum over the kv head's q heads of
+ *           softmax(s)_j, for the j above (the cache must have slot_weight).
+ * Scores, softmax and sums are f32.  A key's products are exact in the tensor cores' terms: q and the
+ * softmax weights are split in two f16 (f16 cache) or tf32 (f32 cache) parts, an f32 cache's rows too.
+ * The length is split over the GPU and joined in the order of the slots: results do not depend on
+ * timing.  d_workspace: device memory of qkv_attn_workspace_bytes bytes, 16-byte aligned, that must be
+ * zero before the first call and belongs to calls that do not overlap on the GPU (one stream, or
+ * graphs replayed one after the other); every completed call leaves it usable for the next, of any
+ * shape that needs no more bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED (out_dtype, n_head % n_head_kv != 0), CUDA. */
+qkv_status qkv_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out);
+qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const float* q, int64_t q_stride,
+                         const int32_t* d_lens, float scale, int32_t window, void* out, int32_t out_dtype,
+                         int64_t out_stride, float* lse, int32_t add_weight, void* d_workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Cut every sequence longer than `budget` slots down to budget, per kv head: kept are the slots
+ * whose position is >= d_next_pos[b] - recent, then those with the largest slot_weight (equal
+ * weights: the lowest slot first; a NaN counts as larger than any number).  The i-th dropped slot
+ * below budget takes what the i-th kept slot at or above it holds: its K and V row (of that head),
+ * weight and position, so no kept row below budget moves and none moves twice.  Attention does not
+ * depend on the order of the slots (but its window counts slots: do not combine the two).
+ *   d_lens     device, n_seq int32; lens_out (n_seq int32, not overlapping d_lens) gets
+ *              min(len, budget).  An out-of-range length is passed on as it is.
+ *   d_next_pos device, n_seq int32: the position that the sequence's next token will have.
+ *   weight_out, pos_out device, as slot_weight and slot_pos, and may be those: slots below
+ *              min(len, budget) are written.  The cache must have both.
+ *   budget >= 1, 0 <= recent <= budget.
+ * Sequences must not share pages (a shared prefix would be changed under the others).  No order of
+ * execution changes the result.  d_workspace: qkv_evict_workspace_bytes bytes, 4-byte aligned, any
+ * contents (null where that is 0), not shared by calls that overlap on the GPU.
+ * Errors: INVALID_ARG, CUDA. */
+qkv_status qkv_evict_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out);
+qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* cache, const int32_t* d_lens,
+                          const int32_t* d_next_pos, int32_t budget, int32_t recent, int32_t* lens_out,
+                          float* weight_out, int32_t* pos_out, void* d_workspace, size_t workspace_bytes,
+                          void* stream);
+
 /* ---- device status ---------------------------------------------------------- */
 
 /* Read (and clear) the device status word on `stream` (synchronises it).
  * flags bit 0: a kernel saw a position outside [0, n_ctx) and skipped its
- * cache stores; *bad_pos_out receives one such position.  Returns
+ * cache stores; *bad_pos_out receives one such position.  Bit 1: a bounded wait
+ * ran out.  Bit 2: a paged call saw a page id, length or sequence index out of
+ * range (*bad_pos_out: one such value).  Returns
  * QKV_ERR_DEVICE_FLAG when any flag was set, QKV_OK otherwise.  The word is
  * per device and shared by all plans. */
 qkv_status qkv_check_device_error(void* stream, uint32_t* flags_out, int32_t* bad_pos_out);

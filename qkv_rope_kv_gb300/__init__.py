@@ -79,6 +79,13 @@ class qkv_ffn_layer(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("x", "w_gate_up", "out")]
 
 
+class qkv_paged_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_seq", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("slot_weight", ctypes.c_void_p), ("slot_pos", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -134,6 +141,11 @@ def _declare(lib):
         "qkv_decode_step_qknorm": ([vp, vp, vp, vp, vp, vp, ctypes.c_float] + [vp] * 8, st),
         "qkv_decode_step_qknorm_noalloc": ([vp, vp, vp, vp, vp, vp, ctypes.c_float] + [vp] * 7, st),
         "qkv_model_graph_create_qknorm": ([vp, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.POINTER(vp)], st),
+        "qkv_paged_store_step": ([vp, vp, vp, i32, i64, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, i64, vp], st),
+        "qkv_attn_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
+        "qkv_attn_step": ([vp, vp, vp, i64, vp, ctypes.c_float, i32, vp, i32, i64, vp, i32, vp, sz, vp], st),
+        "qkv_evict_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
+        "qkv_evict_step": ([vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp], st),
         "qkv_model_graph_destroy": ([vp], None),
         "qkv_check_device_error": ([vp, ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(i32)], st),
         "qkv_test_decode_wait_timeout": ([vp] * 10 + [ctypes.c_uint32, vp], st),
@@ -431,6 +443,133 @@ def qkv_ffn_graph_create(hidden: int, n_ff: int, w_dtype: int, layers, stream) -
     h = ctypes.c_void_p()
     _check(load().qkv_ffn_graph_create(hidden, n_ff, w_dtype, n, arr, _stream(stream), ctypes.byref(h)))
     return ModelGraph(h.value, (layers,))
+
+
+# ---------------------------------------------------------------- paged cache
+
+def _tensor(t, name: str, dtype, shape, device=None, stride=None):
+    """Check a tensor's device, type and shape (rows may be `stride` apart where None in it) and
+    return its address; None passes through."""
+    if t is None:
+        return None
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be on %s, got one on %s" % (name, device or "a GPU", t.device))
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be %s of shape %s, got %s of %s"
+                       % (name, dtype, shape, t.dtype, tuple(t.shape)))
+    if stride is None and not t.is_contiguous() or stride is not None and t.numel() and t.stride(-1) != 1:
+        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be contiguous%s" % (name, "" if stride is None else " in its rows"))
+    return t.data_ptr()
+
+
+class PagedKv:
+    """A ``qkv_paged_kv`` over torch tensors, which it keeps alive: pools ``k`` and ``v``
+    [n_pages, page_size, nkt] of the plan's cache type (pages may be strided, both alike),
+    ``page_table`` int32 [n_seq, max_pages] and, where the cache tracks them, ``slot_weight``
+    (f32) and ``slot_pos`` (int32) [n_seq, n_head_kv, max_pages * page_size]."""
+
+    def __init__(self, plan: Plan, k, v, page_table, slot_weight=None, slot_pos=None):
+        import torch
+        d = plan.desc
+        nkt = d.n_head_kv * d.head_dim
+        if k.dim() != 3 or page_table.dim() != 2:
+            raise QkvError(QKV_ERR_INVALID_ARG, "k, v are [n_pages, page_size, nkt], page_table [n_seq, max_pages]")
+        n_pages, page_size, _ = k.shape
+        n_seq, max_pages = page_table.shape
+        kv = torch.float16 if d.kv_dtype == QKV_F16 else torch.float32
+        self.device = k.device
+        self.capacity = max_pages * page_size
+        tracked = (n_seq, d.n_head_kv, self.capacity)
+        for name, t in (("k", k), ("v", v)):
+            _tensor(t, name, kv, (n_pages, page_size, nkt), self.device, stride=True)
+            if t.stride(1) != nkt and page_size > 1 or t.stride(0) != k.stride(0) and n_pages > 1:
+                raise QkvError(QKV_ERR_INVALID_ARG, "%s: rows of a page must be nkt elements apart, and the pages of "
+                               "k and v equally far" % name)
+        self.struct = qkv_paged_kv(
+            k.data_ptr(), v.data_ptr(), _tensor(page_table, "page_table", torch.int32, (n_seq, max_pages), self.device),
+            n_pages, page_size, n_seq, max_pages, k.stride(0) if n_pages > 1 else 0,
+            _tensor(slot_weight, "slot_weight", torch.float32, tracked, self.device),
+            _tensor(slot_pos, "slot_pos", torch.int32, tracked, self.device))
+        self.n_seq, self.tracked = n_seq, tracked
+        self._keep = (k, v, page_table, slot_weight, slot_pos)
+        self._ref = ctypes.byref(self.struct)
+
+
+def _on_device(cache: PagedKv, stream):
+    """The stream to launch on; the cache's device must be the current one."""
+    import torch
+    if torch.cuda.current_device() != cache.device.index:
+        raise QkvError(QKV_ERR_INVALID_ARG, "the cache is on %s, the current device is cuda:%d: use "
+                       "torch.cuda.device()" % (cache.device, torch.cuda.current_device()))
+    return _stream(stream)
+
+
+def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps: float, positions, seqs, slots,
+                         q, stream=None):
+    """Finish the projections Y [nt, R] (f32 or bf16; rows may be strided) of tokens of any
+    sequences: bias, optional q/k norms, rotation, q [nt, nqt] f32 out, k and v into the cache.
+    ``bias``, the norm weights (together), ``seqs`` and ``slots`` may be None (see qkv.h)."""
+    import torch
+    d = plan.desc
+    nqt = d.n_head * d.head_dim
+    R = nqt + 2 * d.n_head_kv * d.head_dim
+    nt, dev, i32, f32 = Y.shape[0], cache.device, torch.int32, torch.float32
+    bf16 = Y.dtype == torch.bfloat16
+    _check(_lib.qkv_paged_store_step(
+        plan.handle, cache._ref, _tensor(Y, "Y", torch.bfloat16 if bf16 else f32, (nt, R), dev, True),
+        QKV_BF16 if bf16 else QKV_F32, Y.stride(0) if nt > 1 else R, nt, _tensor(bias, "bias", f32, (R,), dev),
+        _tensor(q_norm_w, "q_norm_w", f32, (d.head_dim,), dev), _tensor(k_norm_w, "k_norm_w", f32, (d.head_dim,), dev),
+        eps, _tensor(positions, "positions", i32, (nt,), dev), _tensor(seqs, "seqs", i32, (nt,), dev),
+        _tensor(slots, "slots", i32, (nt,), dev), _tensor(q, "q", f32, (nt, nqt), dev, True),
+        q.stride(0) if nt > 1 else nqt, _on_device(cache, stream)))
+
+
+def qkv_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.qkv_attn_workspace_bytes(plan.handle, cache._ref, ctypes.byref(out)))
+    return out.value
+
+
+def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, workspace, window: int = 0, lse=None,
+                  add_weight: bool = False, stream=None):
+    """Attention of one new token per sequence: q [n_seq, nqt] f32 over the cached slots of each
+    (``lens`` int32 [n_seq]) into out [n_seq, nqt] (f32 or bf16) and lse [n_seq, n_head] (f32).
+    ``workspace``: zeroed device bytes, qkv_attn_workspace_bytes of them; it stays usable."""
+    import torch
+    d = plan.desc
+    B, nqt, dev, f32 = cache.n_seq, d.n_head * d.head_dim, cache.device, torch.float32
+    bf16 = out.dtype == torch.bfloat16
+    _check(_lib.qkv_attn_step(
+        plan.handle, cache._ref, _tensor(q, "q", f32, (B, nqt), dev, True), q.stride(0) if B > 1 else nqt,
+        _tensor(lens, "lens", torch.int32, (B,), dev), scale, window,
+        _tensor(out, "out", torch.bfloat16 if bf16 else f32, (B, nqt), dev, True), QKV_BF16 if bf16 else QKV_F32,
+        out.stride(0) if B > 1 else nqt, _tensor(lse, "lse", f32, (B, d.n_head), dev), add_weight,
+        *_workspace(workspace, dev), _on_device(cache, stream)))
+
+
+def _workspace(t, device):
+    if t is None:
+        return None, 0
+    return _tensor(t, "workspace", t.dtype, tuple(t.shape), device), t.numel() * t.element_size()
+
+
+def qkv_evict_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.qkv_evict_workspace_bytes(plan.handle, cache._ref, ctypes.byref(out)))
+    return out.value
+
+
+def qkv_evict_step(plan: Plan, cache: PagedKv, lens, next_pos, budget: int, recent: int, lens_out, weight_out, pos_out,
+                   workspace, stream=None):
+    """Cut sequences longer than ``budget`` slots to it, per kv head, by slot_weight (and keep the
+    ``recent`` newest positions); weight_out / pos_out may be the cache's own tensors."""
+    import torch
+    B, dev, i32 = cache.n_seq, cache.device, torch.int32
+    _check(_lib.qkv_evict_step(
+        plan.handle, cache._ref, _tensor(lens, "lens", i32, (B,), dev), _tensor(next_pos, "next_pos", i32, (B,), dev),
+        budget, recent, _tensor(lens_out, "lens_out", i32, (B,), dev),
+        _tensor(weight_out, "weight_out", torch.float32, cache.tracked, dev),
+        _tensor(pos_out, "pos_out", i32, cache.tracked, dev), *_workspace(workspace, dev), _on_device(cache, stream)))
 
 
 # ---------------------------------------------------------------- device status

@@ -1,0 +1,241 @@
+// C-ABI layer of the paged-cache entry points: argument validation and workspace layout
+// (include/qkv.h has the contracts; the kernels are in paged_store.cu, paged_attn.cu and
+// paged_evict.cu).
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "qkv_internal.h"
+
+namespace {
+
+#define REQUIRE(cond, ...)                                              \
+    do {                                                                \
+        if (!(cond)) return api_fail(QKV_ERR_INVALID_ARG, __VA_ARGS__); \
+    } while (0)
+
+qkv_status cuda_fail(cudaError_t e, const char* what) {
+    return api_fail(QKV_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int64_t capacity(const qkv_paged_kv* c) { return static_cast<int64_t>(c->max_pages) * c->page_size; }
+
+// Sizes only (what the workspace queries need).
+qkv_status check_shape(const qkv_plan* plan, const qkv_paged_kv* c) {
+    REQUIRE(plan, "plan is null");
+    REQUIRE(c, "cache is null");
+    REQUIRE(c->n_pages >= 1 && c->page_size >= 1 && c->n_seq >= 1 && c->max_pages >= 1,
+            "n_pages, page_size, n_seq and max_pages must be >= 1 (got %d, %d, %d, %d)", c->n_pages, c->page_size,
+            c->n_seq, c->max_pages);
+    REQUIRE(capacity(c) <= INT32_MAX, "max_pages * page_size must be below 2^31");
+    REQUIRE(static_cast<int64_t>(c->n_seq) * (plan->d.n_head + plan->d.n_head_kv) <= (int64_t(1) << 24),
+            "n_seq * heads must be at most 2^24");
+    const int64_t page = static_cast<int64_t>(c->page_size) * plan->nkt;
+    REQUIRE(c->page_stride == 0 || c->page_stride >= page, "page_stride must be 0 or >= page_size * nkt = %lld",
+            static_cast<long long>(page));
+    return QKV_OK;
+}
+
+qkv_status view(const qkv_plan* plan, const qkv_paged_kv* c, PagedView* v) {
+    qkv_status st = check_shape(plan, c);
+    if (st != QKV_OK) return st;
+    REQUIRE(c->k && c->v, "a page pool pointer is null");
+    REQUIRE(c->page_table, "page_table is null");
+    const uintptr_t es = plan->d.kv_dtype == QKV_F16 ? 2 : 4;
+    REQUIRE(aligned(c->k, es) && aligned(c->v, es), "the page pools must be aligned to their elements");
+    REQUIRE(aligned(c->page_table, 4) && aligned(c->slot_weight, 4) && aligned(c->slot_pos, 4),
+            "page_table, slot_weight and slot_pos must be 4-byte aligned");
+    v->k = c->k;
+    v->v = c->v;
+    v->table = c->page_table;
+    v->n_pages = c->n_pages;
+    v->page_size = c->page_size;
+    v->n_seq = c->n_seq;
+    v->max_pages = c->max_pages;
+    v->page_stride = c->page_stride ? c->page_stride : static_cast<int64_t>(c->page_size) * plan->nkt;
+    v->slot_weight = c->slot_weight;
+    v->slot_pos = c->slot_pos;
+    v->nkt = static_cast<int32_t>(plan->nkt);
+    return QKV_OK;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// Byte offsets of the parts of qkv_attn_step's workspace.
+struct AttnLayout {
+    size_t part, lse2, scores, total;
+};
+AttnLayout attn_layout(const qkv_plan* plan, const qkv_paged_kv* c, bool weights) {
+    AttnLayout l;
+    const size_t rows = static_cast<size_t>(c->n_seq) * plan->d.n_head;
+    l.part = up256(kAttnMaxCtas * sizeof(uint32_t));
+    l.lse2 = l.part + up256(sizeof(float) * 2 * kAttnMaxCtas * kAttnHeads * (plan->d.head_dim + 2));
+    l.scores = l.lse2 + (weights ? up256(sizeof(float) * rows) : 0);
+    l.total = l.scores + (weights ? up256(sizeof(float) * rows * capacity(c)) : 0);
+    return l;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache, const void* Y,
+                                           int32_t y_dtype, int64_t y_stride, int32_t nt, const float* bias,
+                                           const float* q_norm_w, const float* k_norm_w, float eps,
+                                           const int32_t* d_positions, const int32_t* d_seqs, const int32_t* d_slots,
+                                           float* q, int64_t q_stride, void* stream) {
+    PagedStoreParams p;
+    std::memset(&p, 0, sizeof p);
+    qkv_status st = view(plan, cache, &p.c);
+    if (st != QKV_OK) return st;
+    REQUIRE(nt >= 0, "nt must be >= 0");
+    if (y_dtype != QKV_F32 && y_dtype != QKV_BF16)
+        return api_fail(QKV_ERR_UNSUPPORTED, "y_dtype %d not supported (F32 or BF16)", y_dtype);
+    REQUIRE(Y && q && d_positions, "Y, q or d_positions is null");
+    REQUIRE(y_stride >= plan->rows, "y_stride must be >= R = %lld", static_cast<long long>(plan->rows));
+    REQUIRE(q_stride >= plan->nqt, "q_stride must be >= nqt = %lld", static_cast<long long>(plan->nqt));
+    REQUIRE((q_norm_w == nullptr) == (k_norm_w == nullptr), "q_norm_w and k_norm_w: both or neither");
+    if (q_norm_w) REQUIRE(eps >= 0.f && eps == eps, "eps must be a number >= 0");
+    REQUIRE(d_seqs || nt <= cache->n_seq, "without d_seqs, nt must be <= n_seq");
+    REQUIRE(aligned(Y, y_dtype == QKV_F32 ? 4 : 2) && aligned(q, 4) && aligned(bias, 4) && aligned(q_norm_w, 4) &&
+                aligned(k_norm_w, 4) && aligned(d_positions, 4) && aligned(d_seqs, 4) && aligned(d_slots, 4),
+            "a pointer is not aligned to its elements");
+    const size_t ybytes = nt ? ((nt - 1) * static_cast<size_t>(y_stride) + plan->rows) * (y_dtype == QKV_F32 ? 4 : 2) : 0;
+    const size_t qbytes = nt ? ((nt - 1) * static_cast<size_t>(q_stride) + plan->nqt) * 4 : 0;
+    REQUIRE((Y == q && y_dtype == QKV_F32 && y_stride == q_stride) || !overlap(Y, ybytes, q, qbytes),
+            "q must be Y itself (F32, the same stride) or not overlap it");
+    if (nt == 0) return QKV_OK;
+    p.y = Y;
+    p.y_stride = y_stride;
+    p.bias = bias;
+    p.norm_w[0] = q_norm_w;
+    p.norm_w[1] = k_norm_w;
+    p.eps = eps;
+    p.positions = d_positions;
+    p.seqs = d_seqs;
+    p.slots = d_slots;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.nt = nt;
+    p.nh = plan->d.n_head;
+    p.nkv = plan->d.n_head_kv;
+    p.hd = plan->d.head_dim;
+    p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
+    std::memcpy(p.inv_freq, plan->inv_freq, sizeof p.inv_freq);
+    const cudaError_t e = launch_paged_store(p, y_dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged store kernel launch");
+    return QKV_OK;
+}
+
+extern "C" qkv_status qkv_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out) {
+    qkv_status st = check_shape(plan, cache);
+    if (st != QKV_OK) return st;
+    REQUIRE(out, "out is null");
+    *out = attn_layout(plan, cache, cache->slot_weight != nullptr).total;
+    return QKV_OK;
+}
+
+extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const float* q, int64_t q_stride,
+                                    const int32_t* d_lens, float scale, int32_t window, void* out, int32_t out_dtype,
+                                    int64_t out_stride, float* lse, int32_t add_weight, void* d_workspace,
+                                    size_t workspace_bytes, void* stream) {
+    PagedAttnParams p;
+    std::memset(&p, 0, sizeof p);
+    qkv_status st = view(plan, cache, &p.c);
+    if (st != QKV_OK) return st;
+    if (plan->d.n_head % plan->d.n_head_kv != 0)
+        return api_fail(QKV_ERR_UNSUPPORTED, "n_head %d is not a multiple of n_head_kv %d", plan->d.n_head,
+                        plan->d.n_head_kv);
+    if (out_dtype != QKV_F32 && out_dtype != QKV_BF16)
+        return api_fail(QKV_ERR_UNSUPPORTED, "out_dtype %d not supported (F32 or BF16)", out_dtype);
+    REQUIRE(q && d_lens && out, "q, d_lens or out is null");
+    REQUIRE(q_stride >= plan->nqt && out_stride >= plan->nqt, "q_stride and out_stride must be >= nqt = %lld",
+            static_cast<long long>(plan->nqt));
+    REQUIRE(std::isfinite(scale), "scale must be finite");
+    REQUIRE(window >= 0, "window must be >= 0");
+    REQUIRE(!add_weight || cache->slot_weight, "add_weight needs a cache with slot_weight");
+    REQUIRE(aligned(q, 4) && aligned(d_lens, 4) && aligned(lse, 4) && aligned(out, out_dtype == QKV_F32 ? 4 : 2),
+            "a pointer is not aligned to its elements");
+    const AttnLayout l = attn_layout(plan, cache, add_weight != 0);
+    REQUIRE(d_workspace && aligned(d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
+    REQUIRE(workspace_bytes >= l.total, "the workspace has %zu bytes, %zu are needed", workspace_bytes, l.total);
+    char* ws = static_cast<char*>(d_workspace);
+    p.q = q;
+    p.q_stride = q_stride;
+    p.lens = d_lens;
+    p.scale = scale;
+    p.window = window;
+    p.out = out;
+    p.out_bf16 = out_dtype == QKV_BF16;
+    p.out_stride = out_stride;
+    p.lse = lse;
+    p.add_weight = add_weight != 0;
+    p.counters = reinterpret_cast<unsigned int*>(ws);
+    p.part = reinterpret_cast<float*>(ws + l.part);
+    p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
+    p.scores = reinterpret_cast<float*>(ws + l.scores);
+    p.nh = plan->d.n_head;
+    p.nkv = plan->d.n_head_kv;
+    p.hd = plan->d.head_dim;
+    p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
+    const cudaError_t e = launch_paged_attn(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
+    return QKV_OK;
+}
+
+extern "C" qkv_status qkv_evict_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out) {
+    qkv_status st = check_shape(plan, cache);
+    if (st != QKV_OK) return st;
+    REQUIRE(out, "out is null");
+    *out = sizeof(int32_t) * 2 * static_cast<size_t>(capacity(cache) / 2) * cache->n_seq * plan->d.n_head_kv;
+    return QKV_OK;
+}
+
+extern "C" qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* cache, const int32_t* d_lens,
+                                     const int32_t* d_next_pos, int32_t budget, int32_t recent, int32_t* lens_out,
+                                     float* weight_out, int32_t* pos_out, void* d_workspace, size_t workspace_bytes,
+                                     void* stream) {
+    PagedEvictParams p;
+    std::memset(&p, 0, sizeof p);
+    qkv_status st = view(plan, cache, &p.c);
+    if (st != QKV_OK) return st;
+    REQUIRE(cache->slot_weight && cache->slot_pos, "the cache must have slot_weight and slot_pos");
+    REQUIRE(d_lens && d_next_pos && lens_out && weight_out && pos_out, "null pointer");
+    REQUIRE(budget >= 1, "budget must be >= 1");
+    REQUIRE(recent >= 0 && recent <= budget, "recent must be in [0, budget]");
+    REQUIRE(aligned(d_lens, 4) && aligned(d_next_pos, 4) && aligned(lens_out, 4) && aligned(weight_out, 4) &&
+                aligned(pos_out, 4),
+            "a pointer is not 4-byte aligned");
+    const size_t nb = sizeof(int32_t) * cache->n_seq;
+    REQUIRE(!overlap(d_lens, nb, lens_out, nb) && !overlap(d_next_pos, nb, lens_out, nb),
+            "lens_out must not overlap d_lens or d_next_pos");
+    const size_t sb = 4 * static_cast<size_t>(capacity(cache)) * cache->n_seq * plan->d.n_head_kv;
+    REQUIRE((weight_out == cache->slot_weight || !overlap(weight_out, sb, cache->slot_weight, sb)) &&
+                (pos_out == cache->slot_pos || !overlap(pos_out, sb, cache->slot_pos, sb)),
+            "weight_out and pos_out must be slot_weight and slot_pos themselves or not overlap them");
+    size_t need = 0;
+    st = qkv_evict_workspace_bytes(plan, cache, &need);
+    if (st != QKV_OK) return st;
+    REQUIRE(workspace_bytes >= need && (d_workspace || need == 0), "the workspace has %zu bytes, %zu are needed",
+            workspace_bytes, need);
+    REQUIRE(aligned(d_workspace, 4), "d_workspace must be 4-byte aligned");
+    p.lens = d_lens;
+    p.next_pos = d_next_pos;
+    p.budget = budget;
+    p.recent = recent;
+    p.lens_out = lens_out;
+    p.weight_out = weight_out;
+    p.pos_out = pos_out;
+    p.lists = static_cast<int32_t*>(d_workspace);
+    p.nkv = plan->d.n_head_kv;
+    p.hd = plan->d.head_dim;
+    p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
+    const cudaError_t e = launch_paged_evict(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "eviction kernel launch");
+    return QKV_OK;
+}

@@ -1,0 +1,63 @@
+// What the paged-cache kernels share: the view of the cache that a launch carries,
+// slot addressing, and each file's device status word (see qkv_check_device_error).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "qkv_internal.h"
+
+namespace qkv_paged {
+
+constexpr unsigned int kFlagSlotRange = 1u;  // a slot outside the sequence's capacity
+constexpr unsigned int kFlagIndexRange = 4u; // a page id, length or sequence index out of range
+
+static __device__ unsigned int g_paged_status[2];  // [0] flags, [1] a bad value
+
+__device__ __forceinline__ void flag_bad(unsigned int bit, int value) {
+    atomicOr(&g_paged_status[0], bit);
+    atomicExch(&g_paged_status[1], static_cast<unsigned int>(value));
+}
+
+// Element offset of the row of slot `slot` of sequence `seq` in the pools, or -1 (and the
+// status flag) where the table names a page that is not there.  64-bit: a pool can hold
+// more than 2^31 elements.
+__device__ __forceinline__ int64_t row_offset(const PagedView& c, int seq, int slot) {
+    const int pg = slot / c.page_size;
+    const int id = __ldg(c.table + static_cast<int64_t>(seq) * c.max_pages + pg);
+    if (static_cast<unsigned int>(id) >= static_cast<unsigned int>(c.n_pages)) {
+        flag_bad(kFlagIndexRange, id);
+        return -1;
+    }
+    return id * c.page_stride + static_cast<int64_t>(slot - pg * c.page_size) * c.nkt;
+}
+
+// Length of sequence b, or 0 (and the status flag) where it is outside [0, capacity].
+__device__ __forceinline__ int checked_len(const PagedView& c, const int32_t* lens, int b) {
+    const int n = __ldg(lens + b);
+    if (n < 0 || n > c.max_pages * c.page_size) {
+        flag_bad(kFlagIndexRange, n);
+        return 0;
+    }
+    return n;
+}
+
+// Read and clear this file's status word (synchronises the stream).
+static inline cudaError_t status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {
+    unsigned int h[2] = {0u, 0u};
+    cudaError_t e = cudaMemcpyFromSymbolAsync(h, g_paged_status, sizeof(h), 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    if (h[0] != 0u) {
+        const unsigned int zero[2] = {0u, 0u};
+        e = cudaMemcpyToSymbolAsync(g_paged_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+        if (e != cudaSuccess) return e;
+        *flags |= h[0];
+        *bad = static_cast<int32_t>(h[1]);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace qkv_paged

@@ -1,0 +1,217 @@
+// qkv_paged_store_step: bias, per-head q / k RMSNorm, neox rotation and the store into the
+// pages, in one pass over the projected rows (include/qkv.h has the contract).
+//
+// Per token and head of q or k:  z = y + b;  n_i = z_i * inv * w_i with
+// inv = 1 / sqrt(sum z^2 / hd + eps);  (n_d, n_{d + hd/2}) rotated by the angle pos * inv_freq[d].
+// Every value is read once and written once, so the pass is bound by memory (or, for a few
+// tokens, by one trip through the latencies of position -> angle and page id -> row).
+#include "epilogue_math.cuh"
+#include "paged_common.cuh"
+
+namespace {
+
+using namespace qkv_epi;
+using namespace qkv_paged;
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 4;  // tokens of one CTA: one sincosf a thread at hd = 128
+
+// Plain loads, not read-only ones: q may be written over Y.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const uint16_t* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) {
+    return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+}
+
+__device__ __forceinline__ void kv_put4(void* kv, int f16, int64_t idx, float4 v) {
+    if (f16) {
+        __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
+        *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(kv) + idx) = *reinterpret_cast<uint2*>(h);
+    } else {
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(kv) + idx) = v;
+    }
+}
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+__device__ __forceinline__ float4 norm4(float4 a, float inv, float4 w) {
+    return make_float4(__fmul_rn(__fmul_rn(a.x, inv), w.x), __fmul_rn(__fmul_rn(a.y, inv), w.y),
+                       __fmul_rn(__fmul_rn(a.z, inv), w.z), __fmul_rn(__fmul_rn(a.w, inv), w.w));
+}
+__device__ __forceinline__ float sq4(float4 a, float s) {
+    return __fmaf_rn(a.x, a.x, __fmaf_rn(a.y, a.y, __fmaf_rn(a.z, a.z, __fmaf_rn(a.w, a.w, s))));
+}
+__device__ __forceinline__ float head_inv(float ss, int hd, float eps) {
+    return __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(hd)), eps)));
+}
+
+// Where the CTA's tokens go: row offsets (-1: not stored), sequences and slots.
+struct Tokens {
+    int64_t row[kMaxTokens];
+    int seq[kMaxTokens], slot[kMaxTokens], pos[kMaxTokens];
+};
+
+// LP lanes work on one head; with VEC a lane holds four neighbouring pairs (LP = hd / 8, a power
+// of two), otherwise a warp strides over the head's pairs one by one (any even hd, any alignment).
+template <typename YT, bool VEC>
+__global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_constant__ PagedStoreParams p, int tokens,
+                                                               int lp, int heads_per_cta) {
+    __shared__ float2 cs_s[kMaxTokens][QKV_MAX_HEAD_DIM / 2];
+    __shared__ Tokens tk;
+    const int half = p.hd >> 1;
+    const int t0 = blockIdx.x * tokens;
+    const int nt = min(tokens, p.nt - t0);
+    const int h0 = blockIdx.y * heads_per_cta;
+    const int nheads = min(heads_per_cta, p.nh + 2 * p.nkv - h0);
+    if (threadIdx.x < nt) {
+        const int t = t0 + threadIdx.x;
+        const int pos = __ldg(p.positions + t);
+        const int seq = p.seqs ? __ldg(p.seqs + t) : t;
+        const int slot = p.slots ? __ldg(p.slots + t) : pos;
+        int64_t row = -1;
+        if (seq >= p.c.n_seq) {
+            flag_bad(kFlagIndexRange, seq);
+        } else if (seq >= 0) {
+            if (slot < 0 || slot >= p.c.max_pages * p.c.page_size) flag_bad(kFlagSlotRange, slot);
+            else row = row_offset(p.c, seq, slot);
+        }
+        tk.row[threadIdx.x] = row;
+        tk.seq[threadIdx.x] = seq;
+        tk.slot[threadIdx.x] = slot;
+        tk.pos[threadIdx.x] = pos;
+    }
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+        const int t = i / half, d = i - t * half;
+        cs_s[t][d] = rope_cos_sin(__ldg(p.positions + t0 + t), p.inv_freq[d]);
+    }
+    __syncthreads();
+
+    const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp;
+    const int items = nt * nheads;
+    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
+    // every group makes the same number of rounds: the lanes of a warp meet in its shuffles
+    for (int i0 = 0; i0 < items; i0 += groups) {
+        const bool live = i0 + g < items;
+        const int i = live ? i0 + g : items - 1;
+        const int t = i / nheads, h = h0 + (i - t * nheads);
+        const int sec = h < p.nh ? 0 : h < p.nh + p.nkv ? 1 : 2;
+        const int j0 = (sec == 0 ? h : sec == 1 ? h - p.nh : h - p.nh - p.nkv) * p.hd;  // within the section
+        const YT* y = static_cast<const YT*>(p.y) + (t0 + t) * p.y_stride + static_cast<int64_t>(h) * p.hd;
+        const float* b = p.bias ? p.bias + static_cast<int64_t>(h) * p.hd : nullptr;
+        const float* w = sec == 2 ? nullptr : p.norm_w[sec];
+        const int64_t row = tk.row[t];
+        const bool write = live && tk.seq[t] >= 0;
+        float* q = p.q + (t0 + t) * p.q_stride + j0;
+        void* kv = sec == 1 ? p.c.k : p.c.v;
+        if constexpr (VEC) {
+            const int d = 4 * l;
+            float4 a0 = load4(y + d), a1 = load4(y + half + d);
+            if (b) {
+                a0 = add4(a0, load4(b + d));
+                a1 = add4(a1, load4(b + half + d));
+            }
+            float inv = 0.f;
+            if (p.norm_w[0]) {  // uniform in the launch; v heads only join the shuffles
+                float ss = sq4(a0, sq4(a1, 0.f));
+                for (int o = lp >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                inv = head_inv(ss, p.hd, p.eps);
+            }
+            if (sec != 2) {
+                if (w) {
+                    a0 = norm4(a0, inv, load4(w + d));
+                    a1 = norm4(a1, inv, load4(w + half + d));
+                }
+                const float2* cs = cs_s[t] + d;
+                float4 r0, r1;
+                rope_rotate_cs(a0.x, a1.x, cs[0], r0.x, r1.x);
+                rope_rotate_cs(a0.y, a1.y, cs[1], r0.y, r1.y);
+                rope_rotate_cs(a0.z, a1.z, cs[2], r0.z, r1.z);
+                rope_rotate_cs(a0.w, a1.w, cs[3], r0.w, r1.w);
+                a0 = r0;
+                a1 = r1;
+            }
+            if (write && sec == 0) {
+                *reinterpret_cast<float4*>(q + d) = a0;
+                *reinterpret_cast<float4*>(q + half + d) = a1;
+            } else if (write && row >= 0) {
+                kv_put4(kv, p.kv_f16, row + j0 + d, a0);
+                kv_put4(kv, p.kv_f16, row + j0 + half + d, a1);
+            }
+        } else {
+            float inv = 0.f;
+            if (p.norm_w[0]) {
+                float ss = 0.f;
+                for (int d = l; d < p.hd; d += lp) {
+                    const float z = b ? __fadd_rn(load1(y + d), __ldg(b + d)) : load1(y + d);
+                    ss = __fmaf_rn(z, z, ss);
+                }
+                for (int o = lp >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                inv = head_inv(ss, p.hd, p.eps);
+            }
+            for (int d = l; d < half; d += lp) {
+                float z0 = load1(y + d), z1 = load1(y + half + d);
+                if (b) {
+                    z0 = __fadd_rn(z0, __ldg(b + d));
+                    z1 = __fadd_rn(z1, __ldg(b + half + d));
+                }
+                if (sec != 2) {
+                    if (w) {
+                        z0 = __fmul_rn(__fmul_rn(z0, inv), __ldg(w + d));
+                        z1 = __fmul_rn(__fmul_rn(z1, inv), __ldg(w + half + d));
+                    }
+                    float r0, r1;
+                    rope_rotate_cs(z0, z1, cs_s[t][d], r0, r1);
+                    z0 = r0;
+                    z1 = r1;
+                }
+                if (write && sec == 0) {
+                    q[d] = z0;
+                    q[half + d] = z1;
+                } else if (write && row >= 0) {
+                    kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + d), z0);
+                    kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + half + d), z1);
+                }
+            }
+        }
+        if (l == 0 && sec == 1 && write && row >= 0) {
+            const int64_t at = (static_cast<int64_t>(tk.seq[t]) * p.nkv + (h - p.nh)) * cap + tk.slot[t];
+            if (p.c.slot_weight) p.c.slot_weight[at] = 0.f;
+            if (p.c.slot_pos) p.c.slot_pos[at] = tk.pos[t];
+        }
+    }
+}
+
+bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+template <typename YT>
+cudaError_t launch_t(const PagedStoreParams& p, cudaStream_t stream) {
+    const int ys = sizeof(YT), es = p.kv_f16 ? 2 : 4;
+    const bool pow2 = p.hd >= 16 && (p.hd & (p.hd - 1)) == 0;
+    const bool vec = pow2 && aligned(p.y, 4 * ys) && p.y_stride % 4 == 0 && aligned(p.bias, 16) &&
+                     aligned(p.norm_w[0], 16) && aligned(p.norm_w[1], 16) && aligned(p.q, 16) &&
+                     p.q_stride % 4 == 0 && aligned(p.c.k, 4 * es) && aligned(p.c.v, 4 * es) &&
+                     p.c.page_stride % 4 == 0;
+    const int lp = vec ? p.hd / 8 : 32;
+    const int heads = p.nh + 2 * p.nkv;
+    int tokens = 1, per = heads;
+    const dim3 grid((p.nt + tokens - 1) / tokens, (heads + per - 1) / per);
+    if (vec) paged_store_kernel<YT, true><<<grid, kThreads, 0, stream>>>(p, tokens, lp, per);
+    else paged_store_kernel<YT, false><<<grid, kThreads, 0, stream>>>(p, tokens, lp, per);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_store(const PagedStoreParams& p, int y_dtype, cudaStream_t stream) {
+    return y_dtype == QKV_BF16 ? launch_t<uint16_t>(p, stream) : launch_t<float>(p, stream);
+}
+
+cudaError_t paged_store_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {
+    return status_read(stream, flags, bad);
+}

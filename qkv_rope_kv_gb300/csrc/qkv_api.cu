@@ -151,6 +151,15 @@ qkv_status run_qknorm(const qkv_plan* plan, const float* x, const void* const w[
 
 }  // namespace
 
+qkv_status api_fail(qkv_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(s, "%s", buf);
+}
+
 // ------------------------------------------------------------------ library
 
 extern "C" int qkv_abi_version(void) { return QKV_ABI_VERSION; }
@@ -951,8 +960,14 @@ extern "C" qkv_status qkv_check_device_error(void* stream, uint32_t* flags_out, 
     if (e != cudaSuccess) return cuda_fail(e, "reading the prefill status word");
     if (!flags) bad = pbad;
     flags |= pflags;
+    for (auto read : {paged_store_status_read, paged_attn_status_read, paged_evict_status_read}) {
+        e = read(static_cast<cudaStream_t>(stream), &flags, &bad);
+        if (e != cudaSuccess) return cuda_fail(e, "reading a paged-cache status word");
+    }
     if (flags_out) *flags_out = flags;
     if (bad_pos_out) *bad_pos_out = bad;
+    if (flags & 4u) return fail(QKV_ERR_DEVICE_FLAG, "device status flags 0x%x (page id, length or sequence index "
+                                                     "out of range: a bad value is %d)", flags, bad);
     if (flags) return fail(QKV_ERR_DEVICE_FLAG, "device status flags 0x%x (position %d outside [0, n_ctx))",
                            flags, bad);
     return QKV_OK;

@@ -88,3 +88,77 @@ struct PrefillParams {
 };
 qkv_status launch_prefill(const PrefillParams& p, bool pdl, cudaStream_t stream, const char** why);
 cudaError_t prefill_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad_pos);
+
+// ---- paged cache (paged_store.cu, paged_attn.cu, paged_evict.cu)
+
+// qkv_paged_kv as a launch carries it, with the plan's row width.
+struct PagedView {
+    void* k;
+    void* v;
+    const int32_t* table;  // [n_seq x max_pages]
+    int32_t n_pages, page_size, n_seq, max_pages;
+    int64_t page_stride;   // elements from page to page
+    float* slot_weight;    // [n_seq x nkv x capacity] or null
+    int32_t* slot_pos;     // the same
+    int32_t nkt;
+};
+
+struct PagedStoreParams {
+    PagedView c;
+    const void* y;
+    int64_t y_stride;
+    const float* bias;       // [R] or null
+    const float* norm_w[2];  // q, k norm weights [hd], or both null
+    float eps;
+    const int32_t* positions;
+    const int32_t* seqs;   // or null: token t belongs to sequence t
+    const int32_t* slots;  // or null: the slot is the position
+    float* q;
+    int64_t q_stride;
+    int32_t nt, nh, nkv, hd, kv_f16;
+    float inv_freq[QKV_MAX_HEAD_DIM / 2];
+};
+cudaError_t launch_paged_store(const PagedStoreParams& p, int y_dtype, cudaStream_t stream);
+cudaError_t paged_store_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
+
+// Workspace of qkv_attn_step.  The counters come first, in a place that no shape moves, so one
+// workspace serves calls of different shapes.
+constexpr int kAttnMaxCtas = 320;  // upper bound of the split grid (two CTAs on each of 152 SMs)
+constexpr int kAttnHeads = 8;      // q heads of one work item
+struct PagedAttnParams {
+    PagedView c;
+    const float* q;
+    int64_t q_stride;
+    const int32_t* lens;
+    float scale;
+    int32_t window;
+    void* out;
+    int32_t out_bf16;
+    int64_t out_stride;
+    float* lse;              // [n_seq x nh] or null
+    int32_t add_weight;
+    unsigned int* counters;  // [kAttnMaxCtas], zero between calls
+    float* part;             // [2 * kAttnMaxCtas][kAttnHeads][hd + 2]
+    float* lse2;             // [n_seq x nh], log2 domain (add_weight)
+    float* scores;           // [n_seq x nh x capacity], log2 domain (add_weight)
+    int32_t nh, nkv, hd, kv_f16;
+};
+cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t paged_attn_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
+
+struct PagedEvictParams {
+    PagedView c;
+    const int32_t* lens;
+    const int32_t* next_pos;
+    int32_t budget, recent;
+    int32_t* lens_out;
+    float* weight_out;
+    int32_t* pos_out;
+    int32_t* lists;  // [n_seq x nkv][2][capacity / 2]: slots freed, slots moved
+    int32_t nkv, hd, kv_f16;
+};
+cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream);
+cudaError_t paged_evict_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
+
+// qkv_api.cu: record the message of a failing call and return its status.
+qkv_status api_fail(qkv_status s, const char* fmt, ...);
