@@ -138,7 +138,7 @@ struct PagedAttnParams {
     float* lse;              // [n_seq x nh] or null
     int32_t add_weight;
     unsigned int* counters;  // [kAttnMaxCtas], zero between calls
-    float* part;             // [2 * kAttnMaxCtas][kAttnHeads][hd + 2]
+    float* part;             // [2 * kAttnMaxCtas][kAttnHeads][hd padded to 64, 128 or 256, + 2]
     float* lse2;             // [n_seq x nh], log2 domain (add_weight)
     float* scores;           // [n_seq x nh x capacity], log2 domain (add_weight)
     int32_t nh, nkv, hd, kv_f16;
