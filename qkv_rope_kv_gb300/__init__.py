@@ -196,6 +196,9 @@ class Plan:
     def __init__(self, handle: int, desc: qkv_plan_desc):
         self.handle = handle
         self.desc = desc
+        self.n_head, self.head_dim = desc.n_head, desc.head_dim
+        self.nqt = desc.n_head * desc.head_dim
+        self.rows = self.nqt + 2 * desc.n_head_kv * desc.head_dim
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
@@ -447,18 +450,16 @@ def qkv_ffn_graph_create(hidden: int, n_ff: int, w_dtype: int, layers, stream) -
 
 # ---------------------------------------------------------------- paged cache
 
-def _tensor(t, name: str, dtype, shape, device=None, stride=None):
-    """Check a tensor's device, type and shape (rows may be `stride` apart where None in it) and
-    return its address; None passes through."""
+def _tensor(t, name: str, dtype, shape: tuple, device: int, rows: bool = False):
+    """Check a tensor's device, type, shape and layout (contiguous, or only in its rows) and return its
+    address; None passes through."""
     if t is None:
         return None
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be on %s, got one on %s" % (name, device or "a GPU", t.device))
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be %s of shape %s, got %s of %s"
-                       % (name, dtype, shape, t.dtype, tuple(t.shape)))
-    if stride is None and not t.is_contiguous() or stride is not None and t.numel() and t.stride(-1) != 1:
-        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be contiguous%s" % (name, "" if stride is None else " in its rows"))
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be %s of shape %s on cuda:%d, got %s of %s on %s"
+                       % (name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
+    if not t.is_contiguous() and not (rows and t.stride(-1) == 1):
+        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be contiguous%s" % (name, " in its rows" if rows else ""))
     return t.data_ptr()
 
 
@@ -472,36 +473,50 @@ class PagedKv:
         import torch
         d = plan.desc
         nkt = d.n_head_kv * d.head_dim
-        if k.dim() != 3 or page_table.dim() != 2:
-            raise QkvError(QKV_ERR_INVALID_ARG, "k, v are [n_pages, page_size, nkt], page_table [n_seq, max_pages]")
+        if k.dim() != 3 or page_table.dim() != 2 or not k.is_cuda:
+            raise QkvError(QKV_ERR_INVALID_ARG, "k, v are CUDA tensors [n_pages, page_size, nkt], page_table is "
+                           "[n_seq, max_pages]")
         n_pages, page_size, _ = k.shape
         n_seq, max_pages = page_table.shape
         kv = torch.float16 if d.kv_dtype == QKV_F16 else torch.float32
-        self.device = k.device
-        self.capacity = max_pages * page_size
-        tracked = (n_seq, d.n_head_kv, self.capacity)
+        dev = self.device = k.get_device()
+        tracked = (n_seq, d.n_head_kv, max_pages * page_size)
         for name, t in (("k", k), ("v", v)):
-            _tensor(t, name, kv, (n_pages, page_size, nkt), self.device, stride=True)
+            _tensor(t, name, kv, (n_pages, page_size, nkt), dev, True)
             if t.stride(1) != nkt and page_size > 1 or t.stride(0) != k.stride(0) and n_pages > 1:
                 raise QkvError(QKV_ERR_INVALID_ARG, "%s: rows of a page must be nkt elements apart, and the pages of "
                                "k and v equally far" % name)
         self.struct = qkv_paged_kv(
-            k.data_ptr(), v.data_ptr(), _tensor(page_table, "page_table", torch.int32, (n_seq, max_pages), self.device),
+            k.data_ptr(), v.data_ptr(), _tensor(page_table, "page_table", torch.int32, (n_seq, max_pages), dev),
             n_pages, page_size, n_seq, max_pages, k.stride(0) if n_pages > 1 else 0,
-            _tensor(slot_weight, "slot_weight", torch.float32, tracked, self.device),
-            _tensor(slot_pos, "slot_pos", torch.int32, tracked, self.device))
-        self.n_seq, self.tracked = n_seq, tracked
+            _tensor(slot_weight, "slot_weight", torch.float32, tracked, dev),
+            _tensor(slot_pos, "slot_pos", torch.int32, tracked, dev))
+        self.address = ctypes.addressof(self.struct)
+        self.plan, self.n_seq, self.tracked = plan, n_seq, tracked
         self._keep = (k, v, page_table, slot_weight, slot_pos)
-        self._ref = ctypes.byref(self.struct)
+
+    def _on(self, plan: Plan, stream):
+        """The stream to launch on; the plan must address rows as this cache's does, and the cache's
+        device be the current one."""
+        if plan is not self.plan:
+            a, b = plan.desc, self.plan.desc
+            if (a.n_head_kv, a.head_dim, a.kv_dtype) != (b.n_head_kv, b.head_dim, b.kv_dtype):
+                raise QkvError(QKV_ERR_INVALID_ARG, "the cache was laid out for another plan's kv heads or type")
+        import torch
+        if torch._C._cuda_getDevice() != self.device:
+            raise QkvError(QKV_ERR_INVALID_ARG, "the cache is on cuda:%d, the current device is cuda:%d: use "
+                           "torch.cuda.device()" % (self.device, torch._C._cuda_getDevice()))
+        return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else _stream(stream)
 
 
-def _on_device(cache: PagedKv, stream):
-    """The stream to launch on; the cache's device must be the current one."""
-    import torch
-    if torch.cuda.current_device() != cache.device.index:
-        raise QkvError(QKV_ERR_INVALID_ARG, "the cache is on %s, the current device is cuda:%d: use "
-                       "torch.cuda.device()" % (cache.device, torch.cuda.current_device()))
-    return _stream(stream)
+def _row_stride(t, width: int) -> int:
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _workspace(t, device: int):
+    if t is None:
+        return None, 0
+    return _tensor(t, "workspace", t.dtype, t.shape, device), t.numel() * t.element_size()
 
 
 def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps: float, positions, seqs, slots,
@@ -510,23 +525,20 @@ def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w
     sequences: bias, optional q/k norms, rotation, q [nt, nqt] f32 out, k and v into the cache.
     ``bias``, the norm weights (together), ``seqs`` and ``slots`` may be None (see qkv.h)."""
     import torch
-    d = plan.desc
-    nqt = d.n_head * d.head_dim
-    R = nqt + 2 * d.n_head_kv * d.head_dim
     nt, dev, i32, f32 = Y.shape[0], cache.device, torch.int32, torch.float32
-    bf16 = Y.dtype == torch.bfloat16
+    bf16, head = Y.dtype is torch.bfloat16, (plan.head_dim,)
     _check(_lib.qkv_paged_store_step(
-        plan.handle, cache._ref, _tensor(Y, "Y", torch.bfloat16 if bf16 else f32, (nt, R), dev, True),
-        QKV_BF16 if bf16 else QKV_F32, Y.stride(0) if nt > 1 else R, nt, _tensor(bias, "bias", f32, (R,), dev),
-        _tensor(q_norm_w, "q_norm_w", f32, (d.head_dim,), dev), _tensor(k_norm_w, "k_norm_w", f32, (d.head_dim,), dev),
-        eps, _tensor(positions, "positions", i32, (nt,), dev), _tensor(seqs, "seqs", i32, (nt,), dev),
-        _tensor(slots, "slots", i32, (nt,), dev), _tensor(q, "q", f32, (nt, nqt), dev, True),
-        q.stride(0) if nt > 1 else nqt, _on_device(cache, stream)))
+        plan.handle, cache.address, _tensor(Y, "Y", torch.bfloat16 if bf16 else f32, (nt, plan.rows), dev, True),
+        QKV_BF16 if bf16 else QKV_F32, _row_stride(Y, plan.rows), nt, _tensor(bias, "bias", f32, (plan.rows,), dev),
+        _tensor(q_norm_w, "q_norm_w", f32, head, dev), _tensor(k_norm_w, "k_norm_w", f32, head, dev), eps,
+        _tensor(positions, "positions", i32, (nt,), dev), _tensor(seqs, "seqs", i32, (nt,), dev),
+        _tensor(slots, "slots", i32, (nt,), dev), _tensor(q, "q", f32, (nt, plan.nqt), dev, True),
+        _row_stride(q, plan.nqt), cache._on(plan, stream)))
 
 
 def qkv_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
     out = ctypes.c_size_t()
-    _check(_lib.qkv_attn_workspace_bytes(plan.handle, cache._ref, ctypes.byref(out)))
+    _check(_lib.qkv_attn_workspace_bytes(plan.handle, cache.address, ctypes.byref(out)))
     return out.value
 
 
@@ -536,26 +548,19 @@ def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, worksp
     (``lens`` int32 [n_seq]) into out [n_seq, nqt] (f32 or bf16) and lse [n_seq, n_head] (f32).
     ``workspace``: zeroed device bytes, qkv_attn_workspace_bytes of them; it stays usable."""
     import torch
-    d = plan.desc
-    B, nqt, dev, f32 = cache.n_seq, d.n_head * d.head_dim, cache.device, torch.float32
-    bf16 = out.dtype == torch.bfloat16
+    B, dev, f32, shape = cache.n_seq, cache.device, torch.float32, (cache.n_seq, plan.nqt)
+    bf16 = out.dtype is torch.bfloat16
     _check(_lib.qkv_attn_step(
-        plan.handle, cache._ref, _tensor(q, "q", f32, (B, nqt), dev, True), q.stride(0) if B > 1 else nqt,
+        plan.handle, cache.address, _tensor(q, "q", f32, shape, dev, True), _row_stride(q, plan.nqt),
         _tensor(lens, "lens", torch.int32, (B,), dev), scale, window,
-        _tensor(out, "out", torch.bfloat16 if bf16 else f32, (B, nqt), dev, True), QKV_BF16 if bf16 else QKV_F32,
-        out.stride(0) if B > 1 else nqt, _tensor(lse, "lse", f32, (B, d.n_head), dev), add_weight,
-        *_workspace(workspace, dev), _on_device(cache, stream)))
-
-
-def _workspace(t, device):
-    if t is None:
-        return None, 0
-    return _tensor(t, "workspace", t.dtype, tuple(t.shape), device), t.numel() * t.element_size()
+        _tensor(out, "out", torch.bfloat16 if bf16 else f32, shape, dev, True), QKV_BF16 if bf16 else QKV_F32,
+        _row_stride(out, plan.nqt), _tensor(lse, "lse", f32, (B, plan.n_head), dev), add_weight,
+        *_workspace(workspace, dev), cache._on(plan, stream)))
 
 
 def qkv_evict_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
     out = ctypes.c_size_t()
-    _check(_lib.qkv_evict_workspace_bytes(plan.handle, cache._ref, ctypes.byref(out)))
+    _check(_lib.qkv_evict_workspace_bytes(plan.handle, cache.address, ctypes.byref(out)))
     return out.value
 
 
@@ -564,12 +569,12 @@ def qkv_evict_step(plan: Plan, cache: PagedKv, lens, next_pos, budget: int, rece
     """Cut sequences longer than ``budget`` slots to it, per kv head, by slot_weight (and keep the
     ``recent`` newest positions); weight_out / pos_out may be the cache's own tensors."""
     import torch
-    B, dev, i32 = cache.n_seq, cache.device, torch.int32
+    B, dev, i32 = (cache.n_seq,), cache.device, torch.int32
     _check(_lib.qkv_evict_step(
-        plan.handle, cache._ref, _tensor(lens, "lens", i32, (B,), dev), _tensor(next_pos, "next_pos", i32, (B,), dev),
-        budget, recent, _tensor(lens_out, "lens_out", i32, (B,), dev),
+        plan.handle, cache.address, _tensor(lens, "lens", i32, B, dev), _tensor(next_pos, "next_pos", i32, B, dev),
+        budget, recent, _tensor(lens_out, "lens_out", i32, B, dev),
         _tensor(weight_out, "weight_out", torch.float32, cache.tracked, dev),
-        _tensor(pos_out, "pos_out", i32, cache.tracked, dev), *_workspace(workspace, dev), _on_device(cache, stream)))
+        _tensor(pos_out, "pos_out", i32, cache.tracked, dev), *_workspace(workspace, dev), cache._on(plan, stream)))
 
 
 # ---------------------------------------------------------------- device status

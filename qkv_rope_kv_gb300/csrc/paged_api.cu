@@ -97,7 +97,7 @@ extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged
     REQUIRE(nt >= 0, "nt must be >= 0");
     if (y_dtype != QKV_F32 && y_dtype != QKV_BF16)
         return api_fail(QKV_ERR_UNSUPPORTED, "y_dtype %d not supported (F32 or BF16)", y_dtype);
-    REQUIRE(Y && q && d_positions, "Y, q or d_positions is null");
+    REQUIRE(nt == 0 || (Y && q && d_positions), "Y, q or d_positions is null");
     REQUIRE(y_stride >= plan->rows, "y_stride must be >= R = %lld", static_cast<long long>(plan->rows));
     REQUIRE(q_stride >= plan->nqt, "q_stride must be >= nqt = %lld", static_cast<long long>(plan->nqt));
     REQUIRE((q_norm_w == nullptr) == (k_norm_w == nullptr), "q_norm_w and k_norm_w: both or neither");

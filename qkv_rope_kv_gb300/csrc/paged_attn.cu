@@ -6,10 +6,12 @@
 #include <math_constants.h>
 
 #include "paged_common.cuh"
+#include "ptx_sync.cuh"
 
 namespace {
 
 using namespace qkv_paged;
+using qkv_ptx::griddep_wait;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -49,6 +51,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
     __shared__ float s_s[kAnyTile];
     __shared__ int64_t row_s[kAnyTile];
     __shared__ float red_s[2 * kAnyThreads / 32];
+    griddep_wait();
     const int b = blockIdx.x / p.nh, h = blockIdx.x - b * p.nh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int j0 = h / (p.nh / p.nkv) * p.hd;
@@ -141,7 +144,8 @@ struct Split {
     static constexpr int kStages = HD < 256 ? 24576 / (2 * kTileBytes) : kF16 ? 3 : 2;
     static constexpr int kRingBytes = kStages * 2 * kTileBytes;
     static constexpr int kORow = HD + 4;                      // floats; + 4 spreads the heads over the banks
-    static constexpr int kMergeFloats = kWarps * kAttnHeads * (kORow + 2);
+    static constexpr int kWarpsFloats = kWarps * kAttnHeads * (kORow + 2);  // the warps' O, m and l
+    static constexpr int kMergeFloats = kWarpsFloats > kAttnHeads * kAttnMaxCtas ? kWarpsFloats : kAttnHeads * kAttnMaxCtas;
     static constexpr int kNT = HD / 8;                        // output column tiles
     static constexpr int kQRegs = kF16 ? HD / 4 : HD / 2;     // A fragments of q
     static constexpr bool kQSmem = kQRegs > 64;               // too many beside O: kept in shared memory
@@ -182,6 +186,12 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ unsigned int atom_add_acq_rel(unsigned int* p, unsigned int v) {
+    unsigned int old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 // Two values rounded to f16 in hi, and the remainders rounded to f16 in lo.
@@ -245,6 +255,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
     constexpr int UK = S::UK;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t red_s[kWarps];
+    __shared__ int longest_s[kWarps];
     __shared__ int64_t start_s;
     __shared__ int b_s;
     __shared__ unsigned int last_s;
@@ -257,14 +268,26 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
     uint32_t* q_s = reinterpret_cast<uint32_t*>(merge + S::kMergeFloats);
     uint32_t* live_s = q_s + (S::kQSmem ? S::kQRegs * 32 : 0) + warp * S::kStages;
 
-    // Total number of units, and the sequence in which this CTA's share begins.
+    griddep_wait();
+    // Total number of units and the longest item; and the sequence in which this CTA's share begins.
+    Walk mine;  // sequence tid of the first 128
     int64_t total = 0;
+    int longest = 0;
     for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
         Walk w;
         w.units = 0;
         if (b0 + tid < B) seq_units<UK>(p, b0 + tid, blockIdx.x == 0, w);
+        if (b0 == 0) mine = w;
         total += w.units;
+        longest = max(longest, w.units);
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) {
+        red_s[warp] = total;
+        longest_s[warp] = longest;
+    }
+    __syncthreads();
     for (int b = blockIdx.x; b < B; b += gridDim.x) {  // an empty sequence has no unit: its rows are written here
         Walk w;
         seq_units<UK>(p, b, false, w);
@@ -273,21 +296,22 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
             for (int h = tid; h < p.nh; h += kSplitThreads) put_lse(p, b, h, 0.f, 0.f, true);
         }
     }
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) red_s[warp] = total;
-    __syncthreads();
     total = (red_s[0] + red_s[1] + red_s[2] + red_s[3]) * items;
+    // A share is at least kMinShare units (each part of an item costs a join), but short items are
+    // not gathered in one CTA while others have none.
+    longest = min(max(max(longest_s[0], longest_s[1]), max(longest_s[2], longest_s[3])), min_share);
     int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    share = share < min_share ? min_share : share;
+    share = share < longest ? longest : share;
     const int64_t f0 = share * blockIdx.x, f1 = f0 + share < total ? f0 + share : total;
     if (f0 >= f1) return;
     int64_t before = 0;  // units of the sequences before this round's
     for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
-        Walk w;
-        w.units = 0;
-        if (b0 + tid < B) seq_units<UK>(p, b0 + tid, false, w);
-        int64_t incl = static_cast<int64_t>(w.units) * items;
-        const int64_t mine = incl;
+        if (b0 > 0) {
+            mine.units = 0;
+            if (b0 + tid < B) seq_units<UK>(p, b0 + tid, false, mine);
+        }
+        const int64_t units = static_cast<int64_t>(mine.units) * items;
+        int64_t incl = units;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
@@ -298,9 +322,9 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         for (int i = 0; i < kWarps; ++i)
             if (i < warp) incl += red_s[i];
         incl += before;
-        if (mine > 0 && incl - mine <= f0 && f0 < incl) {
+        if (units > 0 && incl - units <= f0 && f0 < incl) {
             b_s = b0 + tid;
-            start_s = incl - mine;
+            start_s = incl - units;
         }
         before += red_s[0] + red_s[1] + red_s[2] + red_s[3];
         if (f0 < before) break;  // uniform: every thread has the same sums
@@ -586,27 +610,37 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
 #pragma unroll
             for (int i = 0; i < kPer; ++i) __stcg(reinterpret_cast<float4*>(mine + hh * HD + cc + 64 * i), acc[i]);
             if (cc == 0) __stcg(reinterpret_cast<float2*>(mine + kAttnHeads * HD + 2 * hh), make_float2(M, L));
-            __threadfence();
             __syncthreads();
-            if (tid == 0) last_s = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned int>(c1 - c0);
+            // release this CTA's part (the barrier orders the other threads' writes before) and, in
+            // the last CTA, acquire the others'
+            if (tid == 0) last_s = atom_add_acq_rel(p.counters + c0, 1u);
             __syncthreads();
-            finish = last_s != 0;
+            const int n = c1 - c0 + 1;
+            finish = last_s == static_cast<unsigned int>(n - 1);
             if (finish) {
                 if (tid == 0) p.counters[c0] = 0u;
-                __threadfence();
+                // head hh's 16 threads: maximum, weights and sum over the parts; the weights go to shared memory
                 M = -CUDART_INF_F;
-                for (int c = c0; c <= c1; ++c)
-                    M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(part(c) + kAttnHeads * HD + 2 * hh)).x);
+                for (int i = tid & 15; i < n; i += 16)
+                    M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD + 2 * hh)).x);
+                for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
                 L = 0.f;
-                for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int c = c0; c <= c1; ++c) {
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c) + kAttnHeads * HD + 2 * hh));
+                for (int i = tid & 15; i < n; i += 16) {
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD + 2 * hh));
                     const float k = ml.x == M ? 1.f : ex2(ml.x - M);
+                    merge[hh * kAttnMaxCtas + i] = k;
                     L = fmaf(ml.y, k, L);
+                }
+                for (int o = 8; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                __syncwarp();
+                for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int c = 0; c < n; ++c) {
+                    const float k = merge[hh * kAttnMaxCtas + c];
+                    const float* src = part(c0 + c) + hh * HD + cc;
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
-                        const float4 o = __ldcg(reinterpret_cast<const float4*>(part(c) + hh * HD + cc + 64 * i));
+                        const float4 o = __ldcg(reinterpret_cast<const float4*>(src + 64 * i));
                         acc[i].x = fmaf(o.x, k, acc[i].x);
                         acc[i].y = fmaf(o.y, k, acc[i].y);
                         acc[i].z = fmaf(o.z, k, acc[i].z);
@@ -637,11 +671,12 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
 
 // ---------------------------------------------------------------- running attention weights
 
-constexpr int kWeightThreads = 256;
+constexpr int kWeightThreads = 128, kWeightSlots = 4;  // slots of a thread
 
-// slot_weight[b][kv head][j] += sum over the kv head's q heads of 2^(score - lse): one thread a slot.
+// slot_weight[b][kv head][j] += sum over the kv head's q heads of 2^(score - lse).
 __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const __grid_constant__ PagedAttnParams p,
                                                                            int chunks) {
+    griddep_wait();
     const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
     const int b = item / p.nkv, hk = item - b * p.nkv, G = p.nh / p.nkv;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
@@ -650,11 +685,23 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
     const int first = p.window > 0 ? max(0, n - p.window) : 0;
     const int64_t h0 = static_cast<int64_t>(b) * p.nh + static_cast<int64_t>(hk) * G;
     float* weight = p.c.slot_weight + static_cast<int64_t>(item) * cap;
-    for (int64_t j = first + static_cast<int64_t>(chunk) * kWeightThreads + threadIdx.x; j < n;
-         j += static_cast<int64_t>(chunks) * kWeightThreads) {
-        float w = 0.f;
-        for (int g = 0; g < G; ++g) w += exp2f(p.scores[(h0 + g) * cap + j] - p.lse2[h0 + g]);
-        weight[j] += w;
+    constexpr int kSpan = kWeightThreads * kWeightSlots;
+    for (int64_t j0 = first + static_cast<int64_t>(chunk) * kSpan + threadIdx.x; j0 < n;
+         j0 += static_cast<int64_t>(chunks) * kSpan) {
+        float w[kWeightSlots];
+#pragma unroll
+        for (int k = 0; k < kWeightSlots; ++k) w[k] = 0.f;
+#pragma unroll 4
+        for (int g = 0; g < G; ++g) {
+            const float lse2 = __ldcg(p.lse2 + h0 + g);
+            const float* s = p.scores + (h0 + g) * cap + j0;
+#pragma unroll
+            for (int k = 0; k < kWeightSlots; ++k)
+                if (j0 + k * kWeightThreads < n) w[k] += exp2f(__ldcg(s + k * kWeightThreads) - lse2);
+        }
+#pragma unroll
+        for (int k = 0; k < kWeightSlots; ++k)
+            if (j0 + k * kWeightThreads < n) weight[j0 + k * kWeightThreads] += w[k];
     }
 }
 
@@ -670,8 +717,7 @@ cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int grid = sms * S::kCtas < kAttnMaxCtas ? sms * S::kCtas : kAttnMaxCtas;
     const int blocks_per_head = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
-    kernel<<<grid, kSplitThreads, S::kSmem, stream>>>(p, blocks_per_head, kMinShare);
-    return cudaGetLastError();
+    return launch_dependent(kernel, grid, kSplitThreads, S::kSmem, stream, p, blocks_per_head, kMinShare);
 }
 
 }  // namespace
@@ -682,8 +728,7 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream) {
                            static_cast<uintptr_t>(p.c.page_stride * es) | static_cast<uintptr_t>(p.hd * es);
     cudaError_t e;
     if ((bits & 15u) != 0) {  // rows that 16-byte copies cannot read
-        paged_attn_any_kernel<<<p.c.n_seq * p.nh, kAnyThreads, 0, stream>>>(p);
-        e = cudaGetLastError();
+        e = launch_dependent(paged_attn_any_kernel, p.c.n_seq * p.nh, kAnyThreads, 0, stream, p);
     } else if (p.kv_f16) {
         e = p.hd <= 64 ? launch_split<uint16_t, 64>(p, stream)
                        : p.hd <= 128 ? launch_split<uint16_t, 128>(p, stream) : launch_split<uint16_t, 256>(p, stream);
@@ -693,9 +738,11 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream) {
     }
     if (e != cudaSuccess || !p.add_weight) return e;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    const int chunks = static_cast<int>(cap / kWeightThreads / 8 + 1);
-    paged_attn_weight_kernel<<<p.c.n_seq * p.nkv * chunks, kWeightThreads, 0, stream>>>(p, chunks);
-    return cudaGetLastError();
+    // up to two blocks for every resident one; longer sequences loop
+    const int64_t spans = (cap + kWeightThreads * kWeightSlots - 1) / (kWeightThreads * kWeightSlots);
+    const int64_t most = 4096 / (static_cast<int64_t>(p.c.n_seq) * p.nkv) + 1;
+    const int chunks = static_cast<int>(spans < most ? spans : most);
+    return launch_dependent(paged_attn_weight_kernel, p.c.n_seq * p.nkv * chunks, kWeightThreads, 0, stream, p, chunks);
 }
 
 cudaError_t paged_attn_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {

@@ -43,6 +43,24 @@ __device__ __forceinline__ int checked_len(const PagedView& c, const int32_t* le
     return n;
 }
 
+// Launch after the stream's previous kernel as a programmatic dependent: the blocks are set up while
+// that one drains, and wait for it (griddep_wait) before they read anything.
+template <typename... Params, typename... Args>
+static inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                           const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Read and clear this file's status word (synchronises the stream).
 static inline cudaError_t status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {
     unsigned int h[2] = {0u, 0u};

@@ -6,6 +6,7 @@
 // have to: the i-th dropped slot below the budget takes the i-th kept slot above it.  Sources
 // (>= budget) and destinations (< budget) are disjoint, so the copies need no order.
 #include "paged_common.cuh"
+#include "ptx_sync.cuh"
 
 namespace {
 
@@ -21,160 +22,285 @@ __device__ __forceinline__ uint32_t slot_key(float w, int pos, int64_t protect_f
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix over the warps of one value per warp (all threads get their warp's).
-__device__ __forceinline__ int warp_prefix(int mine, int* buf, int warp, int lane) {
-    if (lane == 0) buf[warp] = mine;
-    __syncthreads();
-    int v = lane < warp ? buf[lane] : 0;
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    return v;
-}
+constexpr int kBins = 2048, kPasses = 3;           // digits of 11, 11 and 10 bits
+constexpr int kBatch = 1024;                       // moves whose rows are looked up at a time
+constexpr int kFixedSmem = kPasses * kBins * 4;    // the histograms, later the batch's row offsets
+constexpr int kMaxCluster = 8;
+static_assert(kFixedSmem >= kBatch * 16, "row offsets fit the histograms' place");
 
-template <bool VEC>
-__device__ __forceinline__ void copy_row(char* base, int64_t to, int64_t from, int bytes, int lane) {
-    if constexpr (VEC) {
-        for (int i = lane * 16; i < bytes; i += 512)
-            *reinterpret_cast<uint4*>(base + to + i) = *reinterpret_cast<const uint4*>(base + from + i);
+__device__ __forceinline__ void cluster_sync(int size) {
+    if (size == 1) {
+        __syncthreads();
     } else {
-        for (int i = lane * 2; i < bytes; i += 64)
-            *reinterpret_cast<uint16_t*>(base + to + i) = *reinterpret_cast<const uint16_t*>(base + from + i);
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 }
 
-// One CTA per (sequence, kv head).
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) paged_evict_kernel(const __grid_constant__ PagedEvictParams p) {
-    __shared__ unsigned int hist_s[256];
-    __shared__ int buf_s[kWarps];
-    __shared__ unsigned int prefix_s;
-    __shared__ int want_s;
-    const int b = blockIdx.x / p.nkv, h = blockIdx.x - b * p.nkv;
+// A 32-bit word of CTA `rank` of a cluster of `size`, at the place of `p` in its shared memory.
+__device__ __forceinline__ uint32_t peer_word(const uint32_t* p, int rank, int size) {
+    if (size == 1) return *p;
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(qkv_ptx::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Count one key's bin: one atomic for the whole warp where its lanes agree (equal weights would
+// otherwise serialise on one address).
+__device__ __forceinline__ void count_bin(uint32_t* hist, uint32_t bin, bool in) {
+    const unsigned int active = __ballot_sync(0xffffffffu, in);
+    if (active == 0u) return;
+    const int leader = __ffs(active) - 1;
+    const uint32_t first = __shfl_sync(0xffffffffu, bin, leader);
+    if (__all_sync(0xffffffffu, !in || bin == first)) {
+        if (static_cast<int>(threadIdx.x & 31) == leader) atomicAdd(hist + first, static_cast<uint32_t>(__popc(active)));
+    } else if (in) {
+        atomicAdd(hist + bin, 1u);
+    }
+}
+
+// A cluster of `size` CTAs per (sequence, kv head); each holds a contiguous run of the slots, their
+// keys in shared memory where they fit (CACHED).  CT is the unit of the row copies.
+template <typename CT, bool CACHED>
+__global__ void __launch_bounds__(kThreads) paged_evict_kernel(const __grid_constant__ PagedEvictParams p, int size) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem + kFixedSmem);
+    __shared__ uint32_t warp_s[kWarps], warp2_s[kWarps];
+    __shared__ uint32_t found_s[3];  // bin, keys still wanted from it, keys in it
+    __shared__ uint32_t publish_s[3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int item = blockIdx.x / size, rank = blockIdx.x - item * size;
+    const int b = item / p.nkv, h = item - b * p.nkv;
     const int cap = p.c.max_pages * p.c.page_size;
+    for (int i = tid; i < kPasses * kBins; i += kThreads) hist[i] = 0u;
+    qkv_ptx::griddep_wait();
     const int len = __ldg(p.lens + b);
     const bool sane = len >= 0 && len <= cap;
-    if (h == 0 && tid == 0) {
+    if (h == 0 && rank == 0 && tid == 0) {
         if (!sane) flag_bad(kFlagIndexRange, len);
         p.lens_out[b] = sane ? min(len, p.budget) : len;
     }
     if (!sane) return;
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * cap;
+    const int64_t base = static_cast<int64_t>(item) * cap;
     const float* w_in = p.c.slot_weight + base;
     const int32_t* pos_in = p.c.slot_pos + base;
     float* w_out = p.weight_out + base;
     int32_t* pos_out = p.pos_out + base;
     if (len <= p.budget) {
-        for (int s = tid; s < len; s += kThreads) {
+        for (int s = rank * kThreads + tid; s < len; s += size * kThreads) {
             w_out[s] = w_in[s];
             pos_out[s] = pos_in[s];
         }
         return;
     }
     const int64_t protect_from = static_cast<int64_t>(__ldg(p.next_pos + b)) - p.recent;
+    const int run = (len + size * kThreads - 1) / (size * kThreads) * 32;  // slots of a warp
+    const int s0 = (rank * kWarps + warp) * run;
+    const int mine = max(0, min(run, len - s0));
+    uint32_t* my_keys = keys + warp * run;
+    auto key_of = [&](int i) -> uint32_t {  // i-th slot of this warp
+        if (CACHED) return my_keys[i];
+        return slot_key(__ldcg(w_in + s0 + i), __ldcg(pos_in + s0 + i), protect_from);
+    };
+    __syncthreads();  // the histograms are clear
 
-    // The budget-th largest key, byte by byte from the top: after a byte, prefix holds the key's
-    // bytes so far and `want` how many of the keys with that prefix are still to be taken.
-    if (tid == 0) {
-        prefix_s = 0u;
-        want_s = p.budget;
-    }
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist_s[tid] = 0u;
-        __syncthreads();
-        const uint32_t prefix = prefix_s, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int s = tid; s < len; s += kThreads) {
-            const uint32_t k = slot_key(w_in[s], pos_in[s], protect_from);
-            if ((k & mask) == prefix) atomicAdd(&hist_s[(k >> shift) & 255u], 1u);
+    // The budget-th largest key, digit by digit: after a digit, `low` is the smallest key with the
+    // digits found so far, and `want` how many of the keys with those digits are kept.
+    uint32_t low = 0u, want = static_cast<uint32_t>(p.budget), in_bin = 0u;
+    int shift = 32;
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const int above = shift;
+        shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        uint32_t* my_hist = hist + pass * kBins;
+#pragma unroll 4
+        for (int i = lane; i < run; i += 32) {
+            uint32_t k = 0u;
+            bool in = i < mine;
+            if (in) {
+                k = CACHED && pass == 0 ? slot_key(w_in[s0 + i], pos_in[s0 + i], protect_from) : key_of(i);
+                if (CACHED && pass == 0) my_keys[i] = k;
+            }
+            in = in && (pass == 0 || k >> above == low >> above);
+            count_bin(my_hist, (k >> shift) & (pass == 2 ? 1023u : 2047u), in);
         }
+        cluster_sync(size);
+        // thread t: bins 2047 - 2t and 2046 - 2t of all CTAs, so that a scan runs from the largest key down
+        uint32_t c0 = 0u, c1 = 0u;
+        for (int r = 0; r < size; ++r) {
+            c0 += peer_word(my_hist + kBins - 1 - 2 * tid, r, size);
+            c1 += peer_word(my_hist + kBins - 2 - 2 * tid, r, size);
+        }
+        uint32_t incl = c0 + c1;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) warp_s[warp] = incl;
+        __syncthreads();
+        incl += __reduce_add_sync(0xffffffffu, lane < warp ? warp_s[lane] : 0u);
+        const uint32_t excl = incl - c0 - c1;
+        if (excl < want && want <= incl) {
+            const bool second = excl + c0 < want;
+            found_s[0] = kBins - 1 - 2 * tid - second;
+            found_s[1] = want - excl - (second ? c0 : 0u);
+            found_s[2] = second ? c1 : c0;
+        }
+        __syncthreads();
+        low |= found_s[0] << shift;
+        want = found_s[1];
+        in_bin = found_s[2];
+        __syncthreads();
+        if (want == in_bin) break;  // all keys from `low` up are kept
+    }
+    // kept: keys above the found digits, and of those with them all, or (whole keys) the first `want`
+    const uint32_t high = shift == 0 ? low : low | ((1u << shift) - 1u);
+    const bool ranked = want != in_bin;
+    uint32_t tie0 = 0u;
+    if (ranked) {
+        uint32_t n = 0u;
+        for (int i = lane; i < run; i += 32) n += __popc(__ballot_sync(0xffffffffu, i < mine && key_of(i) == low));
+        if (lane == 0) warp_s[warp] = n;
         __syncthreads();
         if (warp == 0) {
-            // lane i holds the bytes 255 - 8i .. 248 - 8i, from the largest down
-            unsigned int c[8], sum = 0u;
-            for (int i = 0; i < 8; ++i) sum += c[i] = hist_s[255 - 8 * lane - i];
-            unsigned int incl = sum;
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned int up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
-            }
-            const unsigned int want = static_cast<unsigned int>(want_s);
-            unsigned int above = incl - sum;
-            __syncwarp();
-            if (above < want && want <= incl)
-                for (int i = 0; i < 8; ++i) {
-                    if (above + c[i] >= want) {
-                        prefix_s = prefix | (static_cast<uint32_t>(255 - 8 * lane - i) << shift);
-                        want_s = static_cast<int>(want - above);
-                        break;
-                    }
-                    above += c[i];
-                }
+            n = __reduce_add_sync(0xffffffffu, warp_s[lane]);
+            if (lane == 0) publish_s[0] = n;
         }
+        cluster_sync(size);
+        for (int r = 0; r < rank; ++r) tie0 += peer_word(publish_s, r, size);
+        tie0 += __reduce_add_sync(0xffffffffu, lane < warp ? warp_s[lane] : 0u);
         __syncthreads();
     }
-    const uint32_t T = prefix_s;
-    const int ties = want_s;  // how many slots with key T are kept, lowest first
-
-    // Each warp owns a contiguous run of slots, so ranks follow the slots' order.
-    const int run = (len + kThreads - 1) / kThreads * 32;
-    const int s0 = warp * run, s1 = min(len, s0 + run);
-    int n_tie = 0;
-    for (int s = s0 + lane; s < s0 + run; s += 32) {
-        const bool tie = s < s1 && slot_key(w_in[s], pos_in[s], protect_from) == T;
-        n_tie += __popc(__ballot_sync(0xffffffffu, tie));
-    }
-    const int tie0 = warp_prefix(n_tie, buf_s, warp, lane);
-    int32_t* holes = p.lists + static_cast<int64_t>(blockIdx.x) * 2 * (cap / 2);
+    int32_t* holes = p.lists + static_cast<int64_t>(item) * 2 * (cap / 2);
     int32_t* movers = holes + cap / 2;
-    int hole0 = 0, mover0 = 0, n_pairs = 0;
+    uint32_t hole0 = 0u, mover0 = 0u, pairs = 0u;
+    const bool copy_meta = w_out != w_in || pos_out != pos_in;
     for (int pass = 0; pass < 2; ++pass) {  // count, then write the lists
-        int tie_at = tie0, hole_at = hole0, mover_at = mover0;
-        for (int s = s0 + lane; s < s0 + run; s += 32) {
-            const bool in = s < s1;
-            const uint32_t k = in ? slot_key(w_in[s], pos_in[s], protect_from) : 0u;
-            const unsigned int tied = __ballot_sync(0xffffffffu, in && k == T);
+        uint32_t tie_at = tie0, hole_at = hole0, mover_at = mover0;
+        for (int i = lane; i < run; i += 32) {
+            const bool in = i < mine;
+            const int s = s0 + i;
+            const uint32_t k = in ? key_of(i) : 0u;
             const unsigned int below = (1u << lane) - 1u;
-            const bool kept = in && (k > T || (k == T && tie_at + __popc(tied & below) < ties));
-            tie_at += __popc(tied);
+            bool kept = in && k >= low;
+            if (ranked) {
+                const unsigned int tied = __ballot_sync(0xffffffffu, in && k == low);
+                kept = in && (k > high || (k == low && tie_at + __popc(tied & below) < want));
+                tie_at += __popc(tied);
+            }
             const bool hole = in && !kept && s < p.budget, mover = kept && s >= p.budget;
             const unsigned int hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
             if (pass && hole) holes[hole_at + __popc(hm & below)] = s;
             if (pass && mover) movers[mover_at + __popc(mm & below)] = s;
+            if (pass && copy_meta && kept && s < p.budget) {
+                w_out[s] = w_in[s];
+                pos_out[s] = pos_in[s];
+            }
             hole_at += __popc(hm);
             mover_at += __popc(mm);
         }
         if (pass == 0) {
-            hole0 = warp_prefix(hole_at, buf_s, warp, lane);
-            mover0 = warp_prefix(mover_at, buf_s, warp, lane);
-        } else if (warp == kWarps - 1 && lane == 0) {
-            want_s = hole_at;  // the total
+            if (lane == 0) {
+                warp_s[warp] = hole_at;
+                warp2_s[warp] = mover_at;
+            }
+            __syncthreads();
+            if (warp == 0) {
+                const uint32_t nh = __reduce_add_sync(0xffffffffu, warp_s[lane]);
+                const uint32_t nm = __reduce_add_sync(0xffffffffu, warp2_s[lane]);
+                if (lane == 0) {
+                    publish_s[1] = nh;
+                    publish_s[2] = nm;
+                }
+            }
+            cluster_sync(size);
+            for (int r = 0; r < size; ++r) {
+                const uint32_t nh = peer_word(publish_s + 1, r, size);
+                pairs += nh;
+                if (r < rank) {
+                    hole0 += nh;
+                    mover0 += peer_word(publish_s + 2, r, size);
+                }
+            }
+            hole0 += __reduce_add_sync(0xffffffffu, lane < warp ? warp_s[lane] : 0u);
+            mover0 += __reduce_add_sync(0xffffffffu, lane < warp ? warp2_s[lane] : 0u);
         }
     }
-    __syncthreads();
-    n_pairs = want_s;
+    // The lists are there, and from here on no CTA reads another's shared memory or a key.
+    cluster_sync(size);
 
-    // Kept slots below the budget keep their weight and position; then the moves overwrite the
-    // freed slots (their old values are not needed: sources lie at or above the budget).
-    if (w_out != w_in || pos_out != pos_in)
-        for (int s = tid; s < p.budget; s += kThreads) {
-            w_out[s] = w_in[s];
-            pos_out[s] = pos_in[s];
-        }
-    __syncthreads();
-    const int es = p.kv_f16 ? 2 : 4, bytes = p.hd * es;
-    for (int i = warp; i < n_pairs; i += kWarps) {
-        const int to = holes[i], from = movers[i];
-        const int64_t rt = row_offset(p.c, b, to), rf = row_offset(p.c, b, from);
-        if (rt >= 0 && rf >= 0) {
-            const int64_t bt = (rt + h * p.hd) * es, bf = (rf + h * p.hd) * es;
-            copy_row<VEC>(static_cast<char*>(p.c.k), bt, bf, bytes, lane);
-            copy_row<VEC>(static_cast<char*>(p.c.v), bt, bf, bytes, lane);
-        }
-        if (lane == 0) {
+    // This CTA's share of the moves, a batch at a time: a thread looks up a move's rows and carries its
+    // weight and position; then all threads copy the rows of K and V.
+    int64_t* to_s = reinterpret_cast<int64_t*>(smem);
+    int64_t* from_s = to_s + kBatch;
+    const int share = (static_cast<int>(pairs) + size - 1) / size;
+    const int p1 = min(static_cast<int>(pairs), (rank + 1) * share);
+    const int row_units = p.hd * (p.kv_f16 ? 2 : 4) / static_cast<int>(sizeof(CT));
+    const int elem_per_unit = static_cast<int>(sizeof(CT)) / (p.kv_f16 ? 2 : 4);
+    CT* kp = static_cast<CT*>(p.c.k);
+    CT* vp = static_cast<CT*>(p.c.v);
+    for (int p0 = rank * share; p0 < p1; p0 += kBatch) {
+        const int n = min(kBatch, p1 - p0);
+        for (int i = tid; i < n; i += kThreads) {
+            const int to = __ldcg(holes + p0 + i), from = __ldcg(movers + p0 + i);
+            const int64_t rt = row_offset(p.c, b, to), rf = row_offset(p.c, b, from);
+            to_s[i] = rt >= 0 && rf >= 0 ? (rt + h * p.hd) / elem_per_unit : -1;
+            from_s[i] = (rf + h * p.hd) / elem_per_unit;
             w_out[to] = w_in[from];
             pos_out[to] = pos_in[from];
         }
+        __syncthreads();
+        const int total = n * 2 * row_units;
+        constexpr int kUnroll = 4;
+        for (int e0 = tid; e0 < total; e0 += kThreads * kUnroll) {
+            CT v[kUnroll];
+            CT* dst[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int e = e0 + u * kThreads, i = e / (2 * row_units), c = e - i * 2 * row_units;
+                dst[u] = nullptr;
+                if (e < total && to_s[i] >= 0) {
+                    CT* pool = c < row_units ? kp + c : vp + (c - row_units);
+                    dst[u] = pool + to_s[i];
+                    v[u] = pool[from_s[i]];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (dst[u]) *dst[u] = v[u];
+        }
+        __syncthreads();
     }
+}
+
+template <typename CT>
+cudaError_t launch_t(const PagedEvictParams& p, cudaStream_t stream) {
+    // CTAs of an (sequence, kv head): one for 4096 slots of capacity, while that leaves no more than
+    // two per SM
+    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
+    const int items = p.c.n_seq * p.nkv;
+    int size = 1;
+    while (size < kMaxCluster && cap > 4096 * static_cast<int64_t>(size) && static_cast<int64_t>(items) * size < 304) size *= 2;
+    const int64_t key_bytes = (cap + static_cast<int64_t>(size) * kThreads - 1) / (static_cast<int64_t>(size) * kThreads) * kThreads * 4;
+    const bool cached = key_bytes <= 200 * 1024;
+    auto kernel = cached ? paged_evict_kernel<CT, true> : paged_evict_kernel<CT, false>;
+    const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(key_bytes) : 0);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned int>(items) * size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = size;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = size > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, size);
 }
 
 }  // namespace
@@ -183,10 +309,8 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
     const int es = p.kv_f16 ? 2 : 4;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(p.c.k) | reinterpret_cast<uintptr_t>(p.c.v) |
                            static_cast<uintptr_t>(p.c.page_stride * es) | static_cast<uintptr_t>(p.hd * es);
-    const int grid = p.c.n_seq * p.nkv;
-    if ((bits & 15u) == 0) paged_evict_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-    else paged_evict_kernel<false><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    if ((bits & 15u) == 0) return launch_t<uint4>(p, stream);
+    return p.kv_f16 ? launch_t<uint16_t>(p, stream) : launch_t<uint32_t>(p, stream);
 }
 
 cudaError_t paged_evict_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {

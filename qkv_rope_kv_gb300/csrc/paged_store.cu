@@ -7,6 +7,7 @@
 // tokens, by one trip through the latencies of position -> angle and page id -> row).
 #include "epilogue_math.cuh"
 #include "paged_common.cuh"
+#include "ptx_sync.cuh"
 
 namespace {
 
@@ -14,15 +15,28 @@ using namespace qkv_epi;
 using namespace qkv_paged;
 
 constexpr int kThreads = 256;
+constexpr int kSms = 152;
 constexpr int kMaxTokens = 4;  // tokens of one CTA: one sincosf a thread at hd = 128
 
-// Plain loads, not read-only ones: q may be written over Y.
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const uint16_t* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
+// Four neighbouring values as loaded.  Plain loads, not read-only ones: q may be written over Y.
+template <typename YT>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <>
+struct Raw4<uint16_t> {  // bf16
+    uint2 v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
+    }
+};
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) {
     return __uint_as_float(static_cast<uint32_t>(*p) << 16);
@@ -64,11 +78,25 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_cons
                                                                int lp, int heads_per_cta) {
     __shared__ float2 cs_s[kMaxTokens][QKV_MAX_HEAD_DIM / 2];
     __shared__ Tokens tk;
+    qkv_ptx::griddep_wait();
     const int half = p.hd >> 1;
     const int t0 = blockIdx.x * tokens;
     const int nt = min(tokens, p.nt - t0);
     const int h0 = blockIdx.y * heads_per_cta;
     const int nheads = min(heads_per_cta, p.nh + 2 * p.nkv - h0);
+    const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp;
+    const int items = nt * nheads;
+    // One round's values are loaded a round ahead, the first round's before the angles are there.
+    Raw4<YT> n0, n1;
+    auto fetch = [&](int i) {
+        if (VEC && i < items) {
+            const int t = i / nheads, h = h0 + (i - t * nheads);
+            const YT* y = static_cast<const YT*>(p.y) + (t0 + t) * p.y_stride + static_cast<int64_t>(h) * p.hd + 4 * l;
+            n0.load(y);
+            n1.load(y + half);
+        }
+    };
+    fetch(g);
     if (threadIdx.x < nt) {
         const int t = t0 + threadIdx.x;
         const int pos = __ldg(p.positions + t);
@@ -92,8 +120,6 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_cons
     }
     __syncthreads();
 
-    const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp;
-    const int items = nt * nheads;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
     // every group makes the same number of rounds: the lanes of a warp meet in its shuffles
     for (int i0 = 0; i0 < items; i0 += groups) {
@@ -111,7 +137,8 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_cons
         void* kv = sec == 1 ? p.c.k : p.c.v;
         if constexpr (VEC) {
             const int d = 4 * l;
-            float4 a0 = load4(y + d), a1 = load4(y + half + d);
+            float4 a0 = n0.get(), a1 = n1.get();
+            fetch(i0 + g + groups);
             if (b) {
                 a0 = add4(a0, load4(b + d));
                 a1 = add4(a1, load4(b + half + d));
@@ -199,11 +226,14 @@ cudaError_t launch_t(const PagedStoreParams& p, cudaStream_t stream) {
                      p.c.page_stride % 4 == 0;
     const int lp = vec ? p.hd / 8 : 32;
     const int heads = p.nh + 2 * p.nkv;
-    int tokens = 1, per = heads;
+    // Tokens share a CTA (and its angles' latency) once there are enough for every SM; before that the
+    // heads of a token are spread over CTAs, down to one round each, at the price of more angles.
+    int tokens = p.nt >= kMaxTokens * 4 * kSms ? kMaxTokens : 1, per = heads;
+    while (tokens == 1 && per > kThreads / lp && static_cast<int64_t>(p.nt) * ((heads + per - 1) / per) < kSms)
+        per = (per + 1) / 2;
     const dim3 grid((p.nt + tokens - 1) / tokens, (heads + per - 1) / per);
-    if (vec) paged_store_kernel<YT, true><<<grid, kThreads, 0, stream>>>(p, tokens, lp, per);
-    else paged_store_kernel<YT, false><<<grid, kThreads, 0, stream>>>(p, tokens, lp, per);
-    return cudaGetLastError();
+    return launch_dependent(vec ? paged_store_kernel<YT, true> : paged_store_kernel<YT, false>, grid, kThreads, 0, stream,
+                            p, tokens, lp, per);
 }
 
 }  // namespace
