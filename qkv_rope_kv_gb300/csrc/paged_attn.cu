@@ -115,11 +115,14 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // ---------------------------------------------------------------- split over the length, tensor cores
 
 // Work is counted in units of 16 (f16) or 8 (f32) neighbouring slots of one item, an item being
-// (sequence, kv head, block of up to 8 of its q heads).  The units of all items, in order, are dealt
-// to the CTAs in equal contiguous shares, whatever the lengths are; where a share ends inside an
-// item, its part goes to the workspace and the last CTA to arrive joins the item's parts in order.
+// (sequence, kv head, block of up to 8 of its q heads).  Lengths are on the device, so every CTA finds
+// its own work from them.  With many items, all units in a row are dealt to the CTAs in equal
+// contiguous shares (an item counts kItemCost units more, for its q and its end); with few, each item
+// gets CTAs of its own, so that no CTA has two beginnings and ends on its path.  The part of an item
+// that a CTA does not hold whole goes to the workspace, and the last CTA to arrive joins the item's
+// parts in order.
 //
-// Within a CTA unit f belongs to warp f % 4, and each warp is a stream of its own: it copies its
+// Within a CTA the units go to the four warps in turn, and each warp is a stream of its own: it copies its
 // units into its own ring of stages (cp.async, rows addressed through the page table, rows outside
 // the sequence filled with zeros) and computes them, with no barrier but at the end of an item.
 //
@@ -131,26 +134,33 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // rescaled for every new maximum), both far from f16's ends.
 
 constexpr int kWarps = 4, kSplitThreads = 32 * kWarps;
-constexpr float kPShift = 12.f;  // weights are kept times 2^12
 constexpr int kMinShare = 8;     // units
+constexpr int kItemCost = 4;     // units
+constexpr int kOwnFactor = 4;    // items get CTAs of their own while the grid has four for each
+constexpr float kPShift = 12.f;  // weights are kept times 2^12
 constexpr float kLazy = 3.f;     // and may exceed that by 2^3 before the maximum moves
 
 template <typename KT, int HD>
 struct Split {
     static constexpr bool kF16 = sizeof(KT) == 2;
-    static constexpr int UK = kF16 ? 16 : 8;                  // slots of a unit
+    static constexpr int UK = kF16 ? 16 : 8;               // slots of a unit
     static constexpr int kRowBytes = HD * sizeof(KT);
-    static constexpr int kTileBytes = UK * kRowBytes;         // K or V of a unit
+    static constexpr int kTileBytes = UK * kRowBytes;      // K or V of a unit
     static constexpr int kStages = HD < 256 ? 24576 / (2 * kTileBytes) : kF16 ? 3 : 2;
     static constexpr int kRingBytes = kStages * 2 * kTileBytes;
-    static constexpr int kORow = HD + 4;                      // floats; + 4 spreads the heads over the banks
-    static constexpr int kWarpsFloats = kWarps * kAttnHeads * (kORow + 2);  // the warps' O, m and l
-    static constexpr int kMergeFloats = kWarpsFloats > kAttnHeads * kAttnMaxCtas ? kWarpsFloats : kAttnHeads * kAttnMaxCtas;
-    static constexpr int kNT = HD / 8;                        // output column tiles
-    static constexpr int kQRegs = kF16 ? HD / 4 : HD / 2;     // A fragments of q
-    static constexpr bool kQSmem = kQRegs > 64;               // too many beside O: kept in shared memory
-    static constexpr int kSmem = kWarps * kRingBytes + kMergeFloats * 4 + (kQSmem ? kQRegs * 128 : 0) + kWarps * kStages * 4;
-    static constexpr int kCtas = HD == 256 ? 1 : 2;           // per SM
+    static constexpr int kNT = HD / 8;                     // output column tiles
+    static constexpr int kQuads = HD / 16;                 // a lane's outputs of one head, in fours
+    static constexpr int kQRow = HD + (kF16 ? 8 : 16);     // floats; spreads the heads' rows over the banks
+    static constexpr int kQLoads = kAttnHeads * HD / kSplitThreads;
+    static constexpr bool kQRegs = kF16 || HD < 256;       // q's fragments stay in registers beside O
+    static constexpr bool kQAhead = HD < 256;              // the next item's q too
+    // O of warps 1 to 3; later the weights of an item's parts
+    static constexpr int kOFloats = 3 * kAttnHeads * HD;
+    static constexpr int kMergeFloats = kOFloats > kAttnHeads * kAttnMaxCtas ? kOFloats : kAttnHeads * kAttnMaxCtas;
+    static constexpr int kPartFloats = kAttnHeads * (HD + 2);
+    static constexpr int kSmem = kWarps * kRingBytes +
+                                 4 * (kMergeFloats + 2 * kWarps * kAttnHeads + kAttnHeads * kQRow + kWarps * kStages);
+    static constexpr int kCtas = HD == 256 ? 1 : 2;        // per SM
     static_assert(kStages >= 2, "ring");
 };
 
@@ -227,11 +237,12 @@ __device__ __forceinline__ int swz(int r, int c, int row_bytes) {
 
 // A place in the order of units.
 struct Walk {
-    int b;         // sequence
-    int lo, n;     // its first unit and its length
-    int first;     // its first slot
-    int units;     // units of one of its items
-    int item, u;   // item, and unit within it
+    int b;          // sequence
+    int lo, n;      // its first unit and its length
+    int first;      // its first slot
+    int units;      // units of one of its items
+    int item, u;    // item, and unit within it
+    int64_t start;  // where the item starts in the order (units and item costs)
 };
 
 template <int UK>
@@ -248,14 +259,24 @@ __device__ __forceinline__ void seq_units(const PagedAttnParams& p, int b, bool 
     w.units = n > 0 ? (n + UK - 1) / UK - w.lo : 0;
 }
 
+// Column of value j of a lane's quad i (the layout of O's fragments; four neighbours in the f32 case).
+template <bool F16>
+__device__ __forceinline__ int quad_col(int i, int j, int t) {
+    return F16 ? 8 * (2 * i + (j >> 1)) + 2 * t + (j & 1) : 4 * (2 * t + (i & 1) + 8 * (i >> 1)) + j;
+}
+
+__device__ __forceinline__ float4 fma4(float4 o, float k, float4 a) {
+    return make_float4(fmaf(o.x, k, a.x), fmaf(o.y, k, a.y), fmaf(o.z, k, a.z), fmaf(o.w, k, a.w));
+}
+
 template <typename KT, int HD>
 __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
-    paged_attn_split_kernel(const __grid_constant__ PagedAttnParams p, int blocks_per_head, int min_share) {
+    paged_attn_split_kernel(const __grid_constant__ PagedAttnParams p, int blocks_per_head) {
     using S = Split<KT, HD>;
     constexpr int UK = S::UK;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t red_s[kWarps];
-    __shared__ int longest_s[kWarps];
+    __shared__ int2 counts_s[kWarps];
     __shared__ int64_t start_s;
     __shared__ int b_s;
     __shared__ unsigned int last_s;
@@ -263,16 +284,20 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
     const int B = p.c.n_seq, G = p.nh / p.nkv, items = p.nkv * blocks_per_head;
     unsigned char* ring = smem + warp * S::kRingBytes;
     float* merge = reinterpret_cast<float*>(smem + kWarps * S::kRingBytes);
-    float* merge_m = merge + kWarps * kAttnHeads * S::kORow;
+    float* merge_m = merge + S::kMergeFloats;
     float* merge_l = merge_m + kWarps * kAttnHeads;
-    uint32_t* q_s = reinterpret_cast<uint32_t*>(merge + S::kMergeFloats);
-    uint32_t* live_s = q_s + (S::kQSmem ? S::kQRegs * 32 : 0) + warp * S::kStages;
+    float* q_s = merge_l + kWarps * kAttnHeads;
+    uint32_t* live_s = reinterpret_cast<uint32_t*>(q_s + kAttnHeads * S::kQRow) + warp * S::kStages;
+
+    // columns beyond hd are zeros for good: no copy writes there
+    if (p.hd < HD)
+        for (int i = lane * 16; i < S::kRingBytes; i += 512) *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
 
     griddep_wait();
-    // Total number of units and the longest item; and the sequence in which this CTA's share begins.
+    // How much there is: units, sequences that have any, and the longest item.
     Walk mine;  // sequence tid of the first 128
     int64_t total = 0;
-    int longest = 0;
+    int longest = 0, nonempty = 0;
     for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
         Walk w;
         w.units = 0;
@@ -280,12 +305,14 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         if (b0 == 0) mine = w;
         total += w.units;
         longest = max(longest, w.units);
+        nonempty += w.units > 0;
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
+    nonempty = __reduce_add_sync(0xffffffffu, nonempty);
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) {
         red_s[warp] = total;
-        longest_s[warp] = longest;
+        counts_s[warp] = make_int2(longest, nonempty);
     }
     __syncthreads();
     for (int b = blockIdx.x; b < B; b += gridDim.x) {  // an empty sequence has no unit: its rows are written here
@@ -297,21 +324,30 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         }
     }
     total = (red_s[0] + red_s[1] + red_s[2] + red_s[3]) * items;
-    // A share is at least kMinShare units (each part of an item costs a join), but short items are
-    // not gathered in one CTA while others have none.
-    longest = min(max(max(longest_s[0], longest_s[1]), max(longest_s[2], longest_s[3])), min_share);
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    share = share < longest ? longest : share;
-    const int64_t f0 = share * blockIdx.x, f1 = f0 + share < total ? f0 + share : total;
-    if (f0 >= f1) return;
-    int64_t before = 0;  // units of the sequences before this round's
+    longest = max(max(counts_s[0].x, counts_s[1].x), max(counts_s[2].x, counts_s[3].x));
+    const int64_t n_items = static_cast<int64_t>(counts_s[0].y + counts_s[1].y + counts_s[2].y + counts_s[3].y) * items;
+    // Few items: CTAs of their own, ceil(units / share) each, which are no more than the grid.  A share is
+    // at least kMinShare units (each part costs a join), but not above the longest item.
+    const bool own = n_items * kOwnFactor <= gridDim.x;
+    const int cost = own ? 0 : kItemCost;
+    int64_t share = own ? (total + gridDim.x - n_items - 1) / (gridDim.x - n_items)
+                        : (total + n_items * cost + gridDim.x - 1) / gridDim.x;
+    const int64_t least = min(longest, kMinShare) + cost;
+    share = share < least ? least : share;
+    // The order is counted in CTAs (own) or in units and item costs; this CTA starts at x.
+    const int64_t x = own ? blockIdx.x : share * blockIdx.x;
+    auto extent = [&](int units) -> int64_t {  // of one item
+        return units == 0 ? 0 : own ? (units + static_cast<int>(share) - 1) / static_cast<int>(share) : units + cost;
+    };
+    int64_t before = 0;  // extent of the sequences before this round's
+    if (tid == 0) b_s = -1;
     for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
         if (b0 > 0) {
             mine.units = 0;
             if (b0 + tid < B) seq_units<UK>(p, b0 + tid, false, mine);
         }
-        const int64_t units = static_cast<int64_t>(mine.units) * items;
-        int64_t incl = units;
+        const int64_t size = extent(mine.units) * items;
+        int64_t incl = size;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
@@ -322,56 +358,107 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         for (int i = 0; i < kWarps; ++i)
             if (i < warp) incl += red_s[i];
         incl += before;
-        if (units > 0 && incl - units <= f0 && f0 < incl) {
+        if (size > 0 && incl - size <= x && x < incl) {
             b_s = b0 + tid;
-            start_s = incl - units;
+            start_s = incl - size;
         }
         before += red_s[0] + red_s[1] + red_s[2] + red_s[3];
-        if (f0 < before) break;  // uniform: every thread has the same sums
+        if (x < before) break;  // uniform: every thread has the same sums
     }
-    // columns beyond hd are zeros for good: no copy writes there
-    if (p.hd < HD)
-        for (int i = lane * 16; i < S::kRingBytes; i += 512) *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    if (b_s < 0) return;  // nothing starts here or later
 
-    Walk at;     // the segment being computed
-    seq_units<UK>(p, b_s, false, at);
-    at.item = static_cast<int>((f0 - start_s) / at.units);
-    at.u = static_cast<int>((f0 - start_s) % at.units);
-    auto next_item = [&](Walk& w) {
+    auto next_item = [&](Walk& w) {  // called only where an item follows
+        w.start += w.units + cost;
+        w.u = 0;
         if (++w.item < items) return;
         w.item = 0;
-        do seq_units<UK>(p, w.b + 1, false, w);  // called only where more units follow
+        do seq_units<UK>(p, w.b + 1, false, w);
         while (w.units == 0);
     };
-    Walk ahead = at;            // the unit to be copied next, fa in the flat order
-    int64_t fa = f0 + warp;
-    int skip = warp;            // how far ahead is behind fa
+    Walk at;     // the segment being computed: the CTA's units of one item, from at.u
+    seq_units<UK>(p, b_s, false, at);
+    int64_t end;      // where this CTA's share ends in the order
+    int c0 = 0, c1 = 0;  // first and last CTA of the item (own)
+    {
+        const int64_t e = extent(at.units);
+        at.item = static_cast<int>((x - start_s) / e);
+        const int64_t r = (x - start_s) - at.item * e;
+        if (own) {  // chunk r of e: the order is the item's own units
+            c0 = static_cast<int>(blockIdx.x - r);
+            c1 = static_cast<int>(c0 + e - 1);
+            at.start = 0;
+            at.u = static_cast<int>(at.units * r / e);
+            end = at.units * (r + 1) / e;
+        } else {
+            at.start = start_s + at.item * e;
+            at.u = static_cast<int>(r);
+            end = min(x + share, total + n_items * cost);
+            if (at.u >= at.units) {  // only the item's cost is left here
+                if (at.start + at.units + cost >= end) return;
+                next_item(at);
+            }
+        }
+    }
+
+    // q of the item's heads, scaled to log2 terms: through registers into q_s, zeros where there is none
+    float qx[S::kQLoads];
+    auto load_q = [&](const Walk& w) {
+        const int hk = w.item / blocks_per_head, hb = w.item - hk * blocks_per_head;
+        const int nheads = min(kAttnHeads, G - hb * kAttnHeads);
+        const float* q = p.q + w.b * p.q_stride + static_cast<int64_t>(hk * G + hb * kAttnHeads) * p.hd;
+#pragma unroll
+        for (int i = 0; i < S::kQLoads; ++i) {
+            const int e = tid + i * kSplitThreads, h = e / HD, d = e % HD;
+            qx[i] = h < nheads && d < p.hd ? __ldg(q + h * p.hd + d) : 0.f;
+        }
+    };
+    auto keep_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::kQLoads; ++i) {
+            const int e = tid + i * kSplitThreads;
+            q_s[e / HD * S::kQRow + e % HD] = qx[i] * (p.scale * kLog2e);
+        }
+    };
+    load_q(at);
+
+    Walk ahead = at;  // the unit to be copied next
+    int skip = warp;  // how many units it is behind that
+    bool more = true;
     const int hd_chunks = p.hd * static_cast<int>(sizeof(KT)) / 16;
     constexpr int kChunks = S::kRowBytes / 16;
-
-    // Row offset (lane = slot of the unit; -1: not read) of unit fa, and the column of its kv head.
-    int64_t row = -1;
-    int head_col = 0;
-    auto locate = [&]() {
+    // Move to the warp's next unit: offset of the row (lane = slot of the unit; -1: not read).
+    auto locate = [&](int64_t& row) {
         row = -1;
-        if (fa >= f1) return;
-        for (ahead.u += skip; ahead.u >= ahead.units;) {
-            ahead.u -= ahead.units;
+        if (!more) return;
+        int u = ahead.u + skip;
+        skip = kWarps;
+        while (u >= ahead.units) {
+            u -= ahead.units;
+            if (ahead.start + ahead.units + cost >= end) {
+                more = false;
+                return;
+            }
             next_item(ahead);
         }
-        skip = kWarps;
-        head_col = ahead.item / blocks_per_head * p.hd;
-        const int slot = (ahead.lo + ahead.u) * UK + lane;
-        if (lane < UK && slot >= ahead.first && slot < ahead.n) row = row_offset(p.c, ahead.b, slot);
+        ahead.u = u;
+        if (ahead.start + u >= end) {
+            more = false;
+            return;
+        }
+        const int slot = (ahead.lo + u) * UK + lane;
+        if (lane < UK && slot >= ahead.first && slot < ahead.n) {
+            row = row_offset(p.c, ahead.b, slot);
+            if (row >= 0) row += ahead.item / blocks_per_head * p.hd;
+        }
     };
     int put = 0;  // stage that the next unit goes to
-    auto copy = [&]() {
-        if (fa < f1) {
+    auto copy = [&](int64_t row, bool there) {
+        if (there) {
             const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
             if (lane == 0) live_s[put] = live;
             const uint32_t dst = smem_addr(ring + put * 2 * S::kTileBytes);
-            const int64_t off = row >= 0 ? row + head_col : 0;
+            const int64_t off = row >= 0 ? row : 0;
 #pragma unroll
             for (int i = 0; i < UK * kChunks / 32; ++i) {
                 const int ci = i * 32 + lane, r = ci / kChunks, c = ci % kChunks;
@@ -387,72 +474,79 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         put = put + 1 == S::kStages ? 0 : put + 1;
-        fa += kWarps;
     };
-    for (int i = 0; i < S::kStages - 1; ++i) {
-        locate();
-        copy();
+    int64_t row;
+    bool there;
+    {
+        int64_t rows[S::kStages - 1];
+        bool here[S::kStages - 1];
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) {
+            locate(rows[i]);
+            here[i] = more;
+        }
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) copy(rows[i], here[i]);
+        locate(row);
+        there = more;
     }
-    locate();
+    keep_q();
+    __syncthreads();
 
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    int get = 0;                 // stage of the next unit to compute
-    int64_t f = f0 + warp;       // that unit
-    for (int64_t fs = f0; fs < f1;) {
-        // the segment: the CTA's units of one item
-        const int64_t item_start = fs - at.u, item_end = item_start + at.units;
-        const int64_t fe = item_end < f1 ? item_end : f1;
-        const int item = at.item;
-        const int hk = item / blocks_per_head, hb = item - hk * blocks_per_head;
+    int get = 0;             // stage of the next unit to compute
+    int u = at.u + warp;     // that unit
+    for (;;) {
+        const int us = at.u, ue = end - at.start < at.units ? static_cast<int>(end - at.start) : at.units;
+        const int hk = at.item / blocks_per_head, hb = at.item - hk * blocks_per_head;
         const int h0 = hk * G + hb * kAttnHeads, nheads = min(kAttnHeads, G - hb * kAttnHeads);
+        const bool follows = at.start + at.units + cost < end;
+        Walk next = at;
+        if (follows) next_item(next);
 
         // q of head g as A fragments
-        uint32_t qa[S::kQRegs];
+        uint32_t qa[S::kQRegs ? (S::kF16 ? HD / 4 : HD / 2) : 8];
         float unscale = 1.f;
-        {
-            const float* q = p.q + at.b * p.q_stride + static_cast<int64_t>(h0 + g) * p.hd;
-            float x[HD / 4];
+        const float* qg = q_s + g * S::kQRow;
+        if constexpr (S::kF16) {
             float big = 0.f;
-            const float qs = p.scale * kLog2e;
 #pragma unroll
-            for (int i = 0; i < HD / 4; ++i) {
-                // f16: 16 (i / 4) + 2t + (0, 1, 8, 9); f32: 4 (i / 4) of 16 a round: 16 (i / 4) + 4t + i % 4
-                const int d = S::kF16 ? (i / 4) * 16 + 2 * t + (i & 1) + ((i >> 1) & 1) * 8 : (i / 4) * 16 + 4 * t + (i & 3);
-                x[i] = g < nheads && d < p.hd ? __ldg(q + d) * qs : 0.f;
-                big = fmaxf(big, fabsf(x[i]));
+            for (int s = 0; s < HD / 8; ++s) {
+                const float2 v = *reinterpret_cast<const float2*>(qg + 8 * s + 2 * t);
+                big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
             }
-            if constexpr (S::kF16) {
-                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
-                int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
-                e = e == 128 ? 13 : max(-113, min(e, 126));
-                const float s = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-                unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
+            int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
+            e = e == 128 ? 13 : max(-113, min(e, 126));
+            const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+            unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
 #pragma unroll
-                for (int i = 0; i < HD / 4; i += 2) split_f16(x[i] * s, x[i + 1] * s, qa[i], qa[i + 1]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < HD / 4; ++i) split_tf32(x[i], qa[2 * i], qa[2 * i + 1]);
+            for (int s = 0; s < HD / 8; ++s) {
+                const float2 v = *reinterpret_cast<const float2*>(qg + 8 * s + 2 * t);
+                split_f16(v.x * sc, v.y * sc, qa[2 * s], qa[2 * s + 1]);
             }
-            if constexpr (S::kQSmem) {
-                // every warp has the same fragments; each writes a quarter (the last segment's have
-                // been read: its merge came after)
+        } else if constexpr (S::kQRegs) {
 #pragma unroll
-                for (int i = 0; i < S::kQRegs; i += 4)
-                    if ((i / 4) % kWarps == warp)
-                        *reinterpret_cast<uint4*>(q_s + (i / 4 * 32 + lane) * 4) = make_uint4(qa[i], qa[i + 1], qa[i + 2], qa[i + 3]);
-                __syncthreads();
+            for (int s = 0; s < HD / 16; ++s) {
+                const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
+                split_tf32(v.x, qa[8 * s], qa[8 * s + 1]);
+                split_tf32(v.y, qa[8 * s + 2], qa[8 * s + 3]);
+                split_tf32(v.z, qa[8 * s + 4], qa[8 * s + 5]);
+                split_tf32(v.w, qa[8 * s + 6], qa[8 * s + 7]);
             }
         }
+        if (S::kQAhead && follows) load_q(next);  // waited for at this segment's end
 
         float O[S::kNT][4] = {};
         float m = -CUDART_INF_F, l = 0.f;  // of head g; l over this lane's slots
-        for (; f < fe; f += kWarps) {
+        for (; u < ue; u += kWarps) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
-            __syncwarp();  // unit f is there, and every lane is done with the one before it
-            copy();        // into that one's stage
-            locate();
+            __syncwarp();  // unit u is there, and every lane is done with the one before it
+            copy(row, there);  // into that one's stage
+            locate(row);
+            there = more;
             const uint32_t tile = smem_addr(ring + get * 2 * S::kTileBytes);
             const uint32_t live = live_s[get];
             constexpr int kST = UK / 8;
@@ -474,9 +568,14 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) split_tf32_kv(r[i], hi[i], lo[i]);
-                    uint32_t a[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = S::kQSmem ? q_s[((2 * s + i / 4) * 32 + lane) * 4 + i % 4] : qa[8 * s + i];
+                    uint32_t* a = qa + (S::kQRegs ? 8 * s : 0);
+                    if constexpr (!S::kQRegs) {
+                        const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
+                        split_tf32(v.x, a[0], a[1]);
+                        split_tf32(v.y, a[2], a[3]);
+                        split_tf32(v.z, a[4], a[5]);
+                        split_tf32(v.w, a[6], a[7]);
+                    }
                     mma_tf32(c[0], a, hi[0], hi[1]);
                     mma_tf32(c[0], a + 4, hi[2], hi[3]);
                     mma_tf32(c[0], a, lo[0], lo[1]);
@@ -494,14 +593,14 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
                     mt = fmaxf(mt, sc[2 * j + i]);
                 }
             if (p.add_weight && g < nheads) {
-                const int u = static_cast<int>(f - item_start) + at.lo;
-                float* dst = p.scores + (static_cast<int64_t>(at.b) * p.nh + h0 + g) * cap + static_cast<int64_t>(u) * UK;
+                const int slot0 = (at.lo + u) * UK;
+                float* dst = p.scores + (static_cast<int64_t>(at.b) * p.nh + h0 + g) * cap + slot0;
 #pragma unroll
                 for (int j = 0; j < kST; ++j)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int k = 8 * j + 2 * t + i, slot = u * UK + k;
-                        if (slot >= at.first && slot < at.n) dst[k] = sc[2 * j + i];
+                        const int k = 8 * j + 2 * t + i;
+                        if (slot0 + k >= at.first && slot0 + k < at.n) dst[k] = sc[2 * j + i];
                     }
             }
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
@@ -556,115 +655,128 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
             }
             get = get + 1 == S::kStages ? 0 : get + 1;
         }
+        u -= ue;  // the warp's first unit of the next segment
 
-        // join the four warps
+        // The four warps' sums into warp 0, in lane-linear quads.
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
-        __syncthreads();  // the previous segment's merge has been read
-        if (t == 0) {
-            merge_m[warp * kAttnHeads + g] = m;
-            merge_l[warp * kAttnHeads + g] = l;
+        if (!S::kQAhead && follows) load_q(next);
+        float4 acc[S::kQuads];
+#pragma unroll
+        for (int i = 0; i < S::kQuads; ++i) {
+            if constexpr (S::kF16)
+                acc[i] = make_float4(join_halves(O[2 * i][0], O[2 * i][2]), join_halves(O[2 * i][1], O[2 * i][3]),
+                                     join_halves(O[2 * i + 1][0], O[2 * i + 1][2]),
+                                     join_halves(O[2 * i + 1][1], O[2 * i + 1][3]));
+            else  // tiles 4s .. 4s + 3, column 2t + (i & 1)
+                acc[i] = make_float4(join_halves(O[4 * (i >> 1)][i & 1], O[4 * (i >> 1)][2 + (i & 1)]),
+                                     join_halves(O[4 * (i >> 1) + 1][i & 1], O[4 * (i >> 1) + 1][2 + (i & 1)]),
+                                     join_halves(O[4 * (i >> 1) + 2][i & 1], O[4 * (i >> 1) + 2][2 + (i & 1)]),
+                                     join_halves(O[4 * (i >> 1) + 3][i & 1], O[4 * (i >> 1) + 3][2 + (i & 1)]));
         }
-        float* mo = merge + (warp * kAttnHeads + g) * S::kORow;
-        if constexpr (S::kF16) {
+        __syncthreads();  // the last segment's merge and this one's q have been read
+        if (warp > 0) {
+            if (t == 0) {
+                merge_m[warp * kAttnHeads + g] = m;
+                merge_l[warp * kAttnHeads + g] = l;
+            }
+            float4* mo = reinterpret_cast<float4*>(merge) + (warp - 1) * S::kQuads * 32 + lane;
 #pragma unroll
-            for (int n = 0; n < S::kNT; ++n)
-                *reinterpret_cast<float2*>(mo + 8 * n + 2 * t) =
-                    make_float2(join_halves(O[n][0], O[n][2]), join_halves(O[n][1], O[n][3]));
-        } else {
-#pragma unroll
-            for (int s = 0; s < HD / 32; ++s)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)  // columns of tiles 4s .. 4s + 3: four neighbours
-                    *reinterpret_cast<float4*>(mo + 4 * (2 * t + i + 8 * s)) = make_float4(
-                        join_halves(O[4 * s][i], O[4 * s][2 + i]), join_halves(O[4 * s + 1][i], O[4 * s + 1][2 + i]),
-                        join_halves(O[4 * s + 2][i], O[4 * s + 2][2 + i]),
-                        join_halves(O[4 * s + 3][i], O[4 * s + 3][2 + i]));
+            for (int i = 0; i < S::kQuads; ++i) mo[i * 32] = acc[i];
         }
+        if (follows) keep_q();
         __syncthreads();
-        constexpr int kPer = HD / 64;  // float4 columns of a thread: 16 threads a head
-        const int hh = tid >> 4, cc = (tid & 15) * 4;
-        float M = -CUDART_INF_F, L = 0.f;
-        float4 acc[kPer] = {};
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, merge_m[w * kAttnHeads + hh]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float mw = merge_m[w * kAttnHeads + hh];
-            const float k = mw == M ? 1.f : ex2(mw - M);
-            L = fmaf(merge_l[w * kAttnHeads + hh], k, L);
+        float M = m, L = l;
+        if (warp == 0) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const float4 o = *reinterpret_cast<const float4*>(merge + (w * kAttnHeads + hh) * S::kORow + cc + 64 * i);
-                acc[i].x = fmaf(o.x, k, acc[i].x);
-                acc[i].y = fmaf(o.y, k, acc[i].y);
-                acc[i].z = fmaf(o.z, k, acc[i].z);
-                acc[i].w = fmaf(o.w, k, acc[i].w);
+            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, merge_m[w * kAttnHeads + g]);
+            const float k0 = m == M ? 1.f : ex2(m - M);
+            L = l * k0;
+#pragma unroll
+            for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(acc[i], k0, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const float mw = merge_m[w * kAttnHeads + g], k = mw == M ? 1.f : ex2(mw - M);
+                L = fmaf(merge_l[w * kAttnHeads + g], k, L);
+                const float4* mo = reinterpret_cast<const float4*>(merge) + (w - 1) * S::kQuads * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(mo[i * 32], k, acc[i]);
             }
         }
-        bool finish = fs == item_start && fe == item_end;
-        if (!finish) {
-            // this CTA's part; parts of an item are numbered by their CTAs
-            const int c0 = static_cast<int>(item_start / share), c1 = static_cast<int>((item_end - 1) / share);
-            const int part_floats = kAttnHeads * (HD + 2);
-            auto part = [&](int c) { return p.part + static_cast<int64_t>(2 * c + (c == c0)) * part_floats; };
-            float* mine = part(blockIdx.x);
+        auto finish = [&](int i, float4 o, float inv) {  // no weight at all (every score -inf) gives NaN, as the formula does
+            const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) __stcg(reinterpret_cast<float4*>(mine + hh * HD + cc + 64 * i), acc[i]);
-            if (cc == 0) __stcg(reinterpret_cast<float2*>(mine + kAttnHeads * HD + 2 * hh), make_float2(M, L));
-            __syncthreads();
-            // release this CTA's part (the barrier orders the other threads' writes before) and, in
-            // the last CTA, acquire the others'
-            if (tid == 0) last_s = atom_add_acq_rel(p.counters + c0, 1u);
-            __syncthreads();
+            for (int j = 0; j < 4; ++j)
+                if (quad_col<S::kF16>(i, j, t) < p.hd) put_out(p, at.b, h0 + g, quad_col<S::kF16>(i, j, t), v[j]);
+        };
+        if (us == 0 && ue == at.units) {
+            if (warp == 0 && g < nheads) {
+                const float inv = 1.f / L;
+#pragma unroll
+                for (int i = 0; i < S::kQuads; ++i) finish(i, acc[i], inv);
+                if (t == 0) put_lse(p, at.b, h0 + g, M - kPShift, L, false);
+            }
+        } else {
+            // this CTA's part; an item's parts are those of its CTAs c0 .. c1
+            if (!own) {
+                c0 = static_cast<int>(at.start / share);
+                c1 = static_cast<int>((at.start + at.units - 1) / share);
+            }
             const int n = c1 - c0 + 1;
-            finish = last_s == static_cast<unsigned int>(n - 1);
-            if (finish) {
-                if (tid == 0) p.counters[c0] = 0u;
-                // head hh's 16 threads: maximum, weights and sum over the parts; the weights go to shared memory
-                M = -CUDART_INF_F;
-                for (int i = tid & 15; i < n; i += 16)
-                    M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD + 2 * hh)).x);
-                for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                L = 0.f;
-                for (int i = tid & 15; i < n; i += 16) {
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD + 2 * hh));
-                    const float k = ml.x == M ? 1.f : ex2(ml.x - M);
-                    merge[hh * kAttnMaxCtas + i] = k;
-                    L = fmaf(ml.y, k, L);
-                }
-                for (int o = 8; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-                __syncwarp();
-                for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                for (int c = 0; c < n; ++c) {
-                    const float k = merge[hh * kAttnMaxCtas + c];
-                    const float* src = part(c0 + c) + hh * HD + cc;
+            auto part = [&](int c) { return p.part + static_cast<int64_t>(2 * c + (c == c0)) * S::kPartFloats; };
+            if (warp == 0) {
+                float* to = part(blockIdx.x);
+                if (g < nheads) {
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const float4 o = __ldcg(reinterpret_cast<const float4*>(src + 64 * i));
-                        acc[i].x = fmaf(o.x, k, acc[i].x);
-                        acc[i].y = fmaf(o.y, k, acc[i].y);
-                        acc[i].z = fmaf(o.z, k, acc[i].z);
-                        acc[i].w = fmaf(o.w, k, acc[i].w);
+                    for (int i = 0; i < S::kQuads; ++i) __stcg(reinterpret_cast<float4*>(to) + i * 32 + lane, acc[i]);
+                    if (t == 0) __stcg(reinterpret_cast<float2*>(to + kAttnHeads * HD) + g, make_float2(M, L));
+                }
+                __syncwarp();
+                // release the part (the warp's writes come before, by its barrier) and, in the last CTA,
+                // acquire the others'
+                if (lane == 0) last_s = atom_add_acq_rel(p.counters + c0, 1u);
+            }
+            __syncthreads();
+            if (last_s == static_cast<unsigned int>(n - 1)) {
+                if (tid == 0) p.counters[c0] = 0u;
+                // 16 threads a head: maximum, weights and sum over the parts
+                const int hh = tid >> 4;
+                float Mh = -CUDART_INF_F, Lh = 0.f;
+                if (hh < nheads) {
+                    for (int i = tid & 15; i < n; i += 16)
+                        Mh = fmaxf(Mh, __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD) + hh).x);
+                    for (int o = 8; o; o >>= 1) Mh = fmaxf(Mh, __shfl_xor_sync(0xffffu << (tid & 16), Mh, o));
+                    for (int i = tid & 15; i < n; i += 16) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD) + hh);
+                        const float k = ml.x == Mh ? 1.f : ex2(ml.x - Mh);
+                        merge[i * kAttnHeads + hh] = k;
+                        Lh = fmaf(ml.y, k, Lh);
+                    }
+                    for (int o = 8; o; o >>= 1) Lh += __shfl_xor_sync(0xffffu << (tid & 16), Lh, o);
+                    if ((tid & 15) == 0) {
+                        merge_l[hh] = Lh;
+                        put_lse(p, at.b, h0 + hh, Mh - kPShift, Lh, false);
                     }
                 }
-            }
-        }
-        if (finish && hh < nheads) {
-            const float inv = 1.f / L;  // no weight at all (every score -inf) gives NaN, as the formula does
+                __syncthreads();
+                if (g < nheads) {  // a quarter of the quads for each warp
+                    constexpr int kMine = S::kQuads / kWarps;
+                    float4 sum[kMine] = {};
+#pragma unroll 8
+                    for (int c = 0; c < n; ++c) {
+                        const float k = merge[c * kAttnHeads + g];
+                        const float4* from = reinterpret_cast<const float4*>(part(c0 + c)) + warp * kMine * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int d = cc + 64 * i;
-                const float v[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
-                for (int k = 0; k < 4; ++k)
-                    if (d + k < p.hd) put_out(p, at.b, h0 + hh, d + k, v[k] * inv);
+                        for (int i = 0; i < kMine; ++i) sum[i] = fma4(__ldcg(from + i * 32), k, sum[i]);
+                    }
+                    const float inv = 1.f / merge_l[g];
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) finish(warp * kMine + i, sum[i], inv);
+                }
             }
-            if (cc == 0) put_lse(p, at.b, h0 + hh, M - kPShift, L, false);
         }
-        fs = fe;
-        if (fs < f1) {
-            at.u = 0;
-            next_item(at);
-        }
+        if (!follows) break;
+        at = next;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -717,7 +829,7 @@ cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int grid = sms * S::kCtas < kAttnMaxCtas ? sms * S::kCtas : kAttnMaxCtas;
     const int blocks_per_head = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
-    return launch_dependent(kernel, grid, kSplitThreads, S::kSmem, stream, p, blocks_per_head, kMinShare);
+    return launch_dependent(kernel, grid, kSplitThreads, S::kSmem, stream, p, blocks_per_head);
 }
 
 }  // namespace
