@@ -3,6 +3,7 @@
 //
 // s_j = scale * q.K_j, online softmax (running maximum m and sum l), out = sum p_j V_j / l.
 // Scores are kept in the log2 domain (scale * log2(e) folded into q), so p = 2^(s - m).
+#include <cuda_bf16.h>
 #include <math_constants.h>
 
 #include "paged_common.cuh"
@@ -16,15 +17,42 @@ using qkv_ptx::griddep_wait;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Rounded to nearest even.
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
 __device__ __forceinline__ void put_out(const PagedAttnParams& p, int b, int h, int d, float v) {
     const int64_t at = b * p.out_stride + static_cast<int64_t>(h) * p.hd + d;
     if (p.out_bf16) {
-        const uint32_t u = __float_as_uint(v);  // round to nearest even; NaN stays NaN
-        const uint16_t r = (u & 0x7fffffffu) > 0x7f800000u ? static_cast<uint16_t>(0x7fffu)
-                                                            : static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-        static_cast<uint16_t*>(p.out)[at] = r;
+        static_cast<uint16_t*>(p.out)[at] = bf16_bits(v);
     } else {
         static_cast<float*>(p.out)[at] = v;
+    }
+}
+
+// Four neighbouring values, as one store where the row's address allows it.
+__device__ __forceinline__ void put_out4(const PagedAttnParams& p, int64_t at, float4 v) {
+    if (p.out_bf16) {
+        const uint32_t lo = bf16_bits(v.x) | static_cast<uint32_t>(bf16_bits(v.y)) << 16;
+        const uint32_t hi = bf16_bits(v.z) | static_cast<uint32_t>(bf16_bits(v.w)) << 16;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+        if ((reinterpret_cast<uintptr_t>(o) & 7u) == 0) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+        } else {
+            o[0] = static_cast<uint16_t>(lo);
+            o[1] = static_cast<uint16_t>(lo >> 16);
+            o[2] = static_cast<uint16_t>(hi);
+            o[3] = static_cast<uint16_t>(hi >> 16);
+        }
+    } else {
+        float* o = static_cast<float*>(p.out) + at;
+        if ((reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+            *reinterpret_cast<float4*>(o) = v;
+        } else {
+            o[0] = v.x;
+            o[1] = v.y;
+            o[2] = v.z;
+            o[3] = v.w;
+        }
     }
 }
 
@@ -154,9 +182,7 @@ struct Split {
     static constexpr int kQLoads = kAttnHeads * HD / kSplitThreads;
     static constexpr bool kQRegs = kF16 || HD < 256;       // q's fragments stay in registers beside O
     static constexpr bool kQAhead = HD < 256;              // the next item's q too
-    // O of warps 1 to 3; later the weights of an item's parts
-    static constexpr int kOFloats = 3 * kAttnHeads * HD;
-    static constexpr int kMergeFloats = kOFloats > kAttnHeads * kAttnMaxCtas ? kOFloats : kAttnHeads * kAttnMaxCtas;
+    static constexpr int kMergeFloats = (kWarps - 1) * kAttnHeads * HD;  // O of the warps but the first
     static constexpr int kPartFloats = kAttnHeads * (HD + 2);
     static constexpr int kSmem = kWarps * kRingBytes +
                                  4 * (kMergeFloats + 2 * kWarps * kAttnHeads + kAttnHeads * kQRow + kWarps * kStages);
@@ -259,6 +285,12 @@ __device__ __forceinline__ void seq_units(const PagedAttnParams& p, int b, bool 
     w.units = n > 0 ? (n + UK - 1) / UK - w.lo : 0;
 }
 
+// a / b of non-negative values; 32-bit division where both fit, as they do in all but huge batches.
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // Column of value j of a lane's quad i (the layout of O's fragments; four neighbours in the f32 case).
 template <bool F16>
 __device__ __forceinline__ int quad_col(int i, int j, int t) {
@@ -275,10 +307,6 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
     using S = Split<KT, HD>;
     constexpr int UK = S::UK;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t red_s[kWarps];
-    __shared__ int2 counts_s[kWarps];
-    __shared__ int64_t start_s;
-    __shared__ int b_s;
     __shared__ unsigned int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int B = p.c.n_seq, G = p.nh / p.nkv, items = p.nkv * blocks_per_head;
@@ -294,15 +322,17 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         for (int i = lane * 16; i < S::kRingBytes; i += 512) *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
 
     griddep_wait();
-    // How much there is: units, sequences that have any, and the longest item.
-    Walk mine;  // sequence tid of the first 128
+    // How much there is: units, sequences that have any, and the longest item.  Every warp finds it for
+    // itself (32 lengths at a time), which takes fewer latencies than a barrier would.
+    int units0 = 0;  // of sequence `lane`
     int64_t total = 0;
     int longest = 0, nonempty = 0;
-    for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) {
         Walk w;
         w.units = 0;
-        if (b0 + tid < B) seq_units<UK>(p, b0 + tid, blockIdx.x == 0, w);
-        if (b0 == 0) mine = w;
+        if (b0 + lane < B) seq_units<UK>(p, b0 + lane, blockIdx.x == 0 && warp == 0, w);
+        if (b0 == 0) units0 = w.units;
         total += w.units;
         longest = max(longest, w.units);
         nonempty += w.units > 0;
@@ -310,28 +340,23 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
     longest = __reduce_max_sync(0xffffffffu, longest);
     nonempty = __reduce_add_sync(0xffffffffu, nonempty);
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) {
-        red_s[warp] = total;
-        counts_s[warp] = make_int2(longest, nonempty);
-    }
-    __syncthreads();
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {  // an empty sequence has no unit: its rows are written here
-        Walk w;
-        seq_units<UK>(p, b, false, w);
-        if (w.units == 0) {
-            for (int i = tid; i < p.nh * p.hd; i += kSplitThreads) put_out(p, b, 0, i, 0.f);
-            for (int h = tid; h < p.nh; h += kSplitThreads) put_lse(p, b, h, 0.f, 0.f, true);
+    if (nonempty < B)  // an empty sequence has no unit: its rows are written here
+        for (int b = blockIdx.x; b < B; b += gridDim.x) {
+            Walk w;
+            seq_units<UK>(p, b, false, w);
+            if (w.units == 0) {
+                for (int i = tid; i < p.nh * p.hd; i += kSplitThreads) put_out(p, b, 0, i, 0.f);
+                for (int h = tid; h < p.nh; h += kSplitThreads) put_lse(p, b, h, 0.f, 0.f, true);
+            }
         }
-    }
-    total = (red_s[0] + red_s[1] + red_s[2] + red_s[3]) * items;
-    longest = max(max(counts_s[0].x, counts_s[1].x), max(counts_s[2].x, counts_s[3].x));
-    const int64_t n_items = static_cast<int64_t>(counts_s[0].y + counts_s[1].y + counts_s[2].y + counts_s[3].y) * items;
+    total *= items;
+    const int64_t n_items = static_cast<int64_t>(nonempty) * items;
     // Few items: CTAs of their own, ceil(units / share) each, which are no more than the grid.  A share is
     // at least kMinShare units (each part costs a join), but not above the longest item.
     const bool own = n_items * kOwnFactor <= gridDim.x;
     const int cost = own ? 0 : kItemCost;
-    int64_t share = own ? (total + gridDim.x - n_items - 1) / (gridDim.x - n_items)
-                        : (total + n_items * cost + gridDim.x - 1) / gridDim.x;
+    const int64_t ctas = own ? gridDim.x - n_items : gridDim.x;
+    int64_t share = div_small(total + n_items * cost + ctas - 1, ctas);
     const int64_t least = min(longest, kMinShare) + cost;
     share = share < least ? least : share;
     // The order is counted in CTAs (own) or in units and item costs; this CTA starts at x.
@@ -339,34 +364,32 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
     auto extent = [&](int units) -> int64_t {  // of one item
         return units == 0 ? 0 : own ? (units + static_cast<int>(share) - 1) / static_cast<int>(share) : units + cost;
     };
-    int64_t before = 0;  // extent of the sequences before this round's
-    if (tid == 0) b_s = -1;
-    for (int b0 = 0; b0 < B; b0 += kSplitThreads) {
+    int64_t before = 0, start = 0;  // extent of the sequences before this round's; where x's sequence starts
+    int b_at = -1;
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        Walk w;
+        w.units = units0;
         if (b0 > 0) {
-            mine.units = 0;
-            if (b0 + tid < B) seq_units<UK>(p, b0 + tid, false, mine);
+            w.units = 0;
+            if (b0 + lane < B) seq_units<UK>(p, b0 + lane, false, w);
         }
-        const int64_t size = extent(mine.units) * items;
+        const int64_t size = extent(w.units) * items;
         int64_t incl = size;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        __syncthreads();
-        if (lane == 31) red_s[warp] = incl;
-        __syncthreads();
-        for (int i = 0; i < kWarps; ++i)
-            if (i < warp) incl += red_s[i];
         incl += before;
-        if (size > 0 && incl - size <= x && x < incl) {
-            b_s = b0 + tid;
-            start_s = incl - size;
+        const unsigned int here = __ballot_sync(0xffffffffu, size > 0 && incl - size <= x && x < incl);
+        if (here) {
+            b_at = b0 + __ffs(here) - 1;
+            start = __shfl_sync(0xffffffffu, incl - size, __ffs(here) - 1);
+            break;
         }
-        before += red_s[0] + red_s[1] + red_s[2] + red_s[3];
-        if (x < before) break;  // uniform: every thread has the same sums
+        before = __shfl_sync(0xffffffffu, incl, 31);
     }
-    __syncthreads();
-    if (b_s < 0) return;  // nothing starts here or later
+    if (b_at < 0) return;  // nothing starts here or later
 
     auto next_item = [&](Walk& w) {  // called only where an item follows
         w.start += w.units + cost;
@@ -377,21 +400,22 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         while (w.units == 0);
     };
     Walk at;     // the segment being computed: the CTA's units of one item, from at.u
-    seq_units<UK>(p, b_s, false, at);
+    seq_units<UK>(p, b_at, false, at);
     int64_t end;      // where this CTA's share ends in the order
     int c0 = 0, c1 = 0;  // first and last CTA of the item (own)
     {
         const int64_t e = extent(at.units);
-        at.item = static_cast<int>((x - start_s) / e);
-        const int64_t r = (x - start_s) - at.item * e;
+        at.item = static_cast<int>(div_small(x - start, e));
+        const int64_t r = (x - start) - at.item * e;
         if (own) {  // chunk r of e: the order is the item's own units
             c0 = static_cast<int>(blockIdx.x - r);
             c1 = static_cast<int>(c0 + e - 1);
             at.start = 0;
-            at.u = static_cast<int>(at.units * r / e);
-            end = at.units * (r + 1) / e;
+            const int n = static_cast<int>(e), each = at.units / n, left = at.units - each * n, i = static_cast<int>(r);
+            at.u = i * each + min(i, left);
+            end = at.u + each + (i < left ? 1 : 0);
         } else {
-            at.start = start_s + at.item * e;
+            at.start = start + at.item * e;
             at.u = static_cast<int>(r);
             end = min(x + share, total + n_items * cost);
             if (at.u >= at.units) {  // only the item's cost is left here
@@ -427,34 +451,53 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
     bool more = true;
     const int hd_chunks = p.hd * static_cast<int>(sizeof(KT)) / 16;
     constexpr int kChunks = S::kRowBytes / 16;
-    // Move to the warp's next unit: offset of the row (lane = slot of the unit; -1: not read).
-    auto locate = [&](int64_t& row) {
-        row = -1;
-        if (!more) return;
+    // Move to the warp's next unit and ask the table for its pages (lane = slot of the unit); nothing waits
+    // for the answer before place() makes it the offset of the slot's row (-1: not read).
+    struct Asked {
+        int id, in_page, col;
+        bool in, there;
+    };
+    auto ask = [&]() {
+        Asked a = {0, 0, 0, false, false};
+        if (!more) return a;
         int u = ahead.u + skip;
         skip = kWarps;
         while (u >= ahead.units) {
             u -= ahead.units;
             if (ahead.start + ahead.units + cost >= end) {
                 more = false;
-                return;
+                return a;
             }
             next_item(ahead);
         }
         ahead.u = u;
         if (ahead.start + u >= end) {
             more = false;
-            return;
+            return a;
         }
         const int slot = (ahead.lo + u) * UK + lane;
-        if (lane < UK && slot >= ahead.first && slot < ahead.n) {
-            row = row_offset(p.c, ahead.b, slot);
-            if (row >= 0) row += ahead.item / blocks_per_head * p.hd;
+        a.there = true;
+        a.in = lane < UK && slot >= ahead.first && slot < ahead.n;
+        a.col = ahead.item / blocks_per_head * p.hd;
+        if (a.in) {
+            const int pg = slot / p.c.page_size;
+            a.in_page = slot - pg * p.c.page_size;
+            a.id = __ldg(p.c.table + static_cast<int64_t>(ahead.b) * p.c.max_pages + pg);
         }
+        return a;
+    };
+    auto place = [&](const Asked& a) -> int64_t {
+        if (!a.in) return -1;
+        if (static_cast<unsigned int>(a.id) >= static_cast<unsigned int>(p.c.n_pages)) {
+            flag_bad(kFlagIndexRange, a.id);
+            return -1;
+        }
+        return a.id * p.c.page_stride + static_cast<int64_t>(a.in_page) * p.c.nkt + a.col;
     };
     int put = 0;  // stage that the next unit goes to
-    auto copy = [&](int64_t row, bool there) {
-        if (there) {
+    auto copy = [&](const Asked& a) {
+        if (a.there) {
+            const int64_t row = place(a);
             const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
             if (lane == 0) live_s[put] = live;
             const uint32_t dst = smem_addr(ring + put * 2 * S::kTileBytes);
@@ -475,20 +518,13 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         asm volatile("cp.async.commit_group;" ::: "memory");
         put = put + 1 == S::kStages ? 0 : put + 1;
     };
-    int64_t row;
-    bool there;
-    {
-        int64_t rows[S::kStages - 1];
-        bool here[S::kStages - 1];
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) {
-            locate(rows[i]);
-            here[i] = more;
-        }
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) copy(rows[i], here[i]);
-        locate(row);
-        there = more;
+    // The copies run kStages - 1 units ahead, the questions to the table one more (after the first, they
+    // mostly hit L1: a line of the table names 32 pages).
+    Asked asked = ask();
+#pragma unroll 1
+    for (int i = 0; i < S::kStages - 1; ++i) {
+        copy(asked);
+        asked = ask();
     }
     keep_q();
     __syncthreads();
@@ -544,9 +580,8 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         for (; u < ue; u += kWarps) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
             __syncwarp();  // unit u is there, and every lane is done with the one before it
-            copy(row, there);  // into that one's stage
-            locate(row);
-            there = more;
+            copy(asked);  // into that one's stage
+            asked = ask();
             const uint32_t tile = smem_addr(ring + get * 2 * S::kTileBytes);
             const uint32_t live = live_s[get];
             constexpr int kST = UK / 8;
@@ -703,24 +738,26 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
                 for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(mo[i * 32], k, acc[i]);
             }
         }
-        auto finish = [&](int i, float4 o, float inv) {  // no weight at all (every score -inf) gives NaN, as the formula does
+        // Outputs go through shared memory (the warps' O, read by now) into rows.
+        auto keep_out = [&](int i, float4 o, float inv) {  // no weight at all (every score -inf) gives NaN, as the formula does
             const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (quad_col<S::kF16>(i, j, t) < p.hd) put_out(p, at.b, h0 + g, quad_col<S::kF16>(i, j, t), v[j]);
+            for (int j = 0; j < 4; ++j) merge[g * HD + quad_col<S::kF16>(i, j, t)] = v[j];
         };
-        if (us == 0 && ue == at.units) {
-            if (warp == 0 && g < nheads) {
+        bool done = us == 0 && ue == at.units;
+        if (done) {
+            if (warp == 0) {
+                __syncwarp();
                 const float inv = 1.f / L;
 #pragma unroll
-                for (int i = 0; i < S::kQuads; ++i) finish(i, acc[i], inv);
-                if (t == 0) put_lse(p, at.b, h0 + g, M - kPShift, L, false);
+                for (int i = 0; i < S::kQuads; ++i) keep_out(i, acc[i], inv);
+                if (t == 0 && g < nheads) put_lse(p, at.b, h0 + g, M - kPShift, L, false);
             }
         } else {
             // this CTA's part; an item's parts are those of its CTAs c0 .. c1
             if (!own) {
-                c0 = static_cast<int>(at.start / share);
-                c1 = static_cast<int>((at.start + at.units - 1) / share);
+                c0 = static_cast<int>(div_small(at.start, share));
+                c1 = static_cast<int>(div_small(at.start + at.units - 1, share));
             }
             const int n = c1 - c0 + 1;
             auto part = [&](int c) { return p.part + static_cast<int64_t>(2 * c + (c == c0)) * S::kPartFloats; };
@@ -739,40 +776,57 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
             __syncthreads();
             if (last_s == static_cast<unsigned int>(n - 1)) {
                 if (tid == 0) p.counters[c0] = 0u;
-                // 16 threads a head: maximum, weights and sum over the parts
-                const int hh = tid >> 4;
-                float Mh = -CUDART_INF_F, Lh = 0.f;
-                if (hh < nheads) {
-                    for (int i = tid & 15; i < n; i += 16)
-                        Mh = fmaxf(Mh, __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD) + hh).x);
-                    for (int o = 8; o; o >>= 1) Mh = fmaxf(Mh, __shfl_xor_sync(0xffffu << (tid & 16), Mh, o));
-                    for (int i = tid & 15; i < n; i += 16) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c0 + i) + kAttnHeads * HD) + hh);
-                        const float k = ml.x == Mh ? 1.f : ex2(ml.x - Mh);
-                        merge[i * kAttnHeads + hh] = k;
-                        Lh = fmaf(ml.y, k, Lh);
+                if (g < nheads) {  // a quarter of the quads for each warp, some parts at a time
+                    constexpr int kMine = S::kQuads / kWarps, kBatch = HD == 256 ? 4 : 8;
+                    float4 sum[kMine] = {};
+                    float Mh = -CUDART_INF_F, Lh = 0.f;
+                    for (int b0 = 0; b0 < n; b0 += kBatch) {
+                        float2 ml[kBatch];
+                        float4 o[kBatch][kMine];
+                        float mb = Mh;
+#pragma unroll
+                        for (int c = 0; c < kBatch; ++c) {
+                            ml[c] = make_float2(-CUDART_INF_F, 0.f);
+                            if (b0 + c < n) {
+                                const float4* from = reinterpret_cast<const float4*>(part(c0 + b0 + c));
+                                ml[c] = __ldcg(reinterpret_cast<const float2*>(from + S::kQuads * 32) + g);
+#pragma unroll
+                                for (int i = 0; i < kMine; ++i) o[c][i] = __ldcg(from + (warp * kMine + i) * 32 + lane);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < kBatch; ++c) mb = fmaxf(mb, ml[c].x);
+                        const float keep = Mh == mb ? 1.f : ex2(Mh - mb);
+                        Mh = mb;
+                        Lh *= keep;
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) sum[i] = fma4(sum[i], keep, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+                        for (int c = 0; c < kBatch; ++c)
+                            if (b0 + c < n) {
+                                const float k = ml[c].x == Mh ? 1.f : ex2(ml[c].x - Mh);
+                                Lh = fmaf(ml[c].y, k, Lh);
+#pragma unroll
+                                for (int i = 0; i < kMine; ++i) sum[i] = fma4(o[c][i], k, sum[i]);
+                            }
                     }
-                    for (int o = 8; o; o >>= 1) Lh += __shfl_xor_sync(0xffffu << (tid & 16), Lh, o);
-                    if ((tid & 15) == 0) {
-                        merge_l[hh] = Lh;
-                        put_lse(p, at.b, h0 + hh, Mh - kPShift, Lh, false);
-                    }
+                    const float inv = 1.f / Lh;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) keep_out(warp * kMine + i, sum[i], inv);
+                    if (warp == 0 && t == 0) put_lse(p, at.b, h0 + g, Mh - kPShift, Lh, false);
                 }
                 __syncthreads();
-                if (g < nheads) {  // a quarter of the quads for each warp
-                    constexpr int kMine = S::kQuads / kWarps;
-                    float4 sum[kMine] = {};
-#pragma unroll 8
-                    for (int c = 0; c < n; ++c) {
-                        const float k = merge[c * kAttnHeads + g];
-                        const float4* from = reinterpret_cast<const float4*>(part(c0 + c)) + warp * kMine * 32 + lane;
-#pragma unroll
-                        for (int i = 0; i < kMine; ++i) sum[i] = fma4(__ldcg(from + i * 32), k, sum[i]);
-                    }
-                    const float inv = 1.f / merge_l[g];
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) finish(warp * kMine + i, sum[i], inv);
-                }
+                done = true;
+            }
+        }
+        if (done && warp == 0) {
+            __syncwarp();
+            const int64_t to = at.b * p.out_stride + static_cast<int64_t>(h0) * p.hd;
+#pragma unroll 1
+            for (int e = lane * 4; e < nheads * p.hd; e += 128) {  // hd is a multiple of 4 here
+                const int h = e / p.hd;
+                const float4 v = *reinterpret_cast<const float4*>(merge + h * HD + (e - h * p.hd));
+                put_out4(p, to + e, v);
             }
         }
         if (!follows) break;
