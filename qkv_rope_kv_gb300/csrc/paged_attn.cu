@@ -161,16 +161,18 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // and the weights are 2^(s - m + 12) with m at most 3 below the running maximum (then O need not be
 // rescaled for every new maximum), both far from f16's ends.
 
-constexpr int kWarps = 4, kSplitThreads = 32 * kWarps;
 constexpr int kMinShare = 8;     // units
-constexpr int kItemCost = 4;     // units
+constexpr int kItemCost = 8;     // units
 constexpr int kOwnFactor = 4;    // items get CTAs of their own while the grid has four for each
+constexpr int kJoinParts = 40;   // more parts than this are joined in two levels
 constexpr float kPShift = 12.f;  // weights are kept times 2^12
 constexpr float kLazy = 3.f;     // and may exceed that by 2^3 before the maximum moves
 
 template <typename KT, int HD>
 struct Split {
     static constexpr bool kF16 = sizeof(KT) == 2;
+    static constexpr int kWarps = 4, kThreads = 32 * kWarps;
+    static constexpr int kCtas = HD == 256 ? 1 : 2;        // per SM
     static constexpr int UK = kF16 ? 16 : 8;               // slots of a unit
     static constexpr int kRowBytes = HD * sizeof(KT);
     static constexpr int kTileBytes = UK * kRowBytes;      // K or V of a unit
@@ -179,14 +181,13 @@ struct Split {
     static constexpr int kNT = HD / 8;                     // output column tiles
     static constexpr int kQuads = HD / 16;                 // a lane's outputs of one head, in fours
     static constexpr int kQRow = HD + (kF16 ? 8 : 16);     // floats; spreads the heads' rows over the banks
-    static constexpr int kQLoads = kAttnHeads * HD / kSplitThreads;
+    static constexpr int kQLoads = kAttnHeads * HD / kThreads;
     static constexpr bool kQRegs = kF16 || HD < 256;       // q's fragments stay in registers beside O
     static constexpr bool kQAhead = HD < 256;              // the next item's q too
     static constexpr int kMergeFloats = (kWarps - 1) * kAttnHeads * HD;  // O of the warps but the first
     static constexpr int kPartFloats = kAttnHeads * (HD + 2);
     static constexpr int kSmem = kWarps * kRingBytes +
                                  4 * (kMergeFloats + 2 * kWarps * kAttnHeads + kAttnHeads * kQRow + kWarps * kStages);
-    static constexpr int kCtas = HD == 256 ? 1 : 2;        // per SM
     static_assert(kStages >= 2, "ring");
 };
 
@@ -271,6 +272,16 @@ struct Walk {
     int64_t start;  // where the item starts in the order (units and item costs)
 };
 
+// An item of which a CTA holds a part.
+struct Pending {
+    int b, h0, nheads;
+    int c0, n;             // the first of its CTAs, and how many
+    unsigned int counted;  // parts of the group that were counted before this one
+};
+__device__ __forceinline__ int join_fan(int n) {
+    return n <= kJoinParts ? n : static_cast<int>(ceilf(sqrtf(static_cast<float>(n))));
+}
+
 template <int UK>
 __device__ __forceinline__ void seq_units(const PagedAttnParams& p, int b, bool flag, Walk& w) {
     int n = __ldg(p.lens + b);
@@ -302,19 +313,20 @@ __device__ __forceinline__ float4 fma4(float4 o, float k, float4 a) {
 }
 
 template <typename KT, int HD>
-__global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
+__global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     paged_attn_split_kernel(const __grid_constant__ PagedAttnParams p, int blocks_per_head) {
     using S = Split<KT, HD>;
     constexpr int UK = S::UK;
     extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Pending pending_s[2];
     __shared__ unsigned int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int B = p.c.n_seq, G = p.nh / p.nkv, items = p.nkv * blocks_per_head;
     unsigned char* ring = smem + warp * S::kRingBytes;
-    float* merge = reinterpret_cast<float*>(smem + kWarps * S::kRingBytes);
+    float* merge = reinterpret_cast<float*>(smem + S::kWarps * S::kRingBytes);
     float* merge_m = merge + S::kMergeFloats;
-    float* merge_l = merge_m + kWarps * kAttnHeads;
-    float* q_s = merge_l + kWarps * kAttnHeads;
+    float* merge_l = merge_m + S::kWarps * kAttnHeads;
+    float* q_s = merge_l + S::kWarps * kAttnHeads;
     uint32_t* live_s = reinterpret_cast<uint32_t*>(q_s + kAttnHeads * S::kQRow) + warp * S::kStages;
 
     // columns beyond hd are zeros for good: no copy writes there
@@ -345,8 +357,8 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
             Walk w;
             seq_units<UK>(p, b, false, w);
             if (w.units == 0) {
-                for (int i = tid; i < p.nh * p.hd; i += kSplitThreads) put_out(p, b, 0, i, 0.f);
-                for (int h = tid; h < p.nh; h += kSplitThreads) put_lse(p, b, h, 0.f, 0.f, true);
+                for (int i = tid; i < p.nh * p.hd; i += S::kThreads) put_out(p, b, 0, i, 0.f);
+                for (int h = tid; h < p.nh; h += S::kThreads) put_lse(p, b, h, 0.f, 0.f, true);
             }
         }
     total *= items;
@@ -433,14 +445,14 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         const float* q = p.q + w.b * p.q_stride + static_cast<int64_t>(hk * G + hb * kAttnHeads) * p.hd;
 #pragma unroll
         for (int i = 0; i < S::kQLoads; ++i) {
-            const int e = tid + i * kSplitThreads, h = e / HD, d = e % HD;
+            const int e = tid + i * S::kThreads, h = e / HD, d = e % HD;
             qx[i] = h < nheads && d < p.hd ? __ldg(q + h * p.hd + d) : 0.f;
         }
     };
     auto keep_q = [&]() {
 #pragma unroll
         for (int i = 0; i < S::kQLoads; ++i) {
-            const int e = tid + i * kSplitThreads;
+            const int e = tid + i * S::kThreads;
             q_s[e / HD * S::kQRow + e % HD] = qx[i] * (p.scale * kLog2e);
         }
     };
@@ -461,7 +473,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         Asked a = {0, 0, 0, false, false};
         if (!more) return a;
         int u = ahead.u + skip;
-        skip = kWarps;
+        skip = S::kWarps;
         while (u >= ahead.units) {
             u -= ahead.units;
             if (ahead.start + ahead.units + cost >= end) {
@@ -494,7 +506,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         }
         return a.id * p.c.page_stride + static_cast<int64_t>(a.in_page) * p.c.nkt + a.col;
     };
-    int put = 0;  // stage that the next unit goes to
+    int put = S::kStages - 1;  // stage that the next unit goes to (the first copy is of no unit)
     auto copy = [&](const Asked& a) {
         if (a.there) {
             const int64_t row = place(a);
@@ -518,20 +530,31 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         asm volatile("cp.async.commit_group;" ::: "memory");
         put = put + 1 == S::kStages ? 0 : put + 1;
     };
-    // The copies run kStages - 1 units ahead, the questions to the table one more (after the first, they
-    // mostly hit L1: a line of the table names 32 pages).
-    Asked asked = ask();
+    // Outputs of an item go through shared memory (the place of the warps' O) into its rows.
+    auto keep_out = [&](int i, float4 o, float inv) {  // no weight at all (every score -inf) gives NaN, as the formula does
+        const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) merge[g * HD + quad_col<S::kF16>(i, j, t)] = v[j];
+    };
+    auto put_rows = [&](int b, int h0, int nheads) {
+        const int64_t to = b * p.out_stride + static_cast<int64_t>(h0) * p.hd;
 #pragma unroll 1
-    for (int i = 0; i < S::kStages - 1; ++i) {
-        copy(asked);
-        asked = ask();
-    }
-    keep_q();
-    __syncthreads();
+        for (int e = lane * 4; e < nheads * p.hd; e += 128) {  // hd is a multiple of 4 here
+            const int h = e / p.hd;
+            put_out4(p, to + e, *reinterpret_cast<const float4*>(merge + h * HD + (e - h * p.hd)));
+        }
+    };
+    auto part = [&](const Pending& e, int c) { return p.part + static_cast<int64_t>(2 * c + (c == e.c0)) * S::kPartFloats; };
+    int pendings = 0;  // segments that are not whole items
 
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
     int get = 0;             // stage of the next unit to compute
     int u = at.u + warp;     // that unit
+    // The copies run kStages - 1 units ahead and the questions to the table one more (after the first, most
+    // hit L1: a line of the table names 32 pages).  `warm` counts the rounds that only fill the ring; they
+    // share the loop's code.
+    Asked asked = {0, 0, 0, false, false};
+    int warm = S::kStages;
     for (;;) {
         const int us = at.u, ue = end - at.start < at.units ? static_cast<int>(end - at.start) : at.units;
         const int hk = at.item / blocks_per_head, hb = at.item - hk * blocks_per_head;
@@ -540,48 +563,63 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         Walk next = at;
         if (follows) next_item(next);
 
-        // q of head g as A fragments
-        uint32_t qa[S::kQRegs ? (S::kF16 ? HD / 4 : HD / 2) : 8];
+        uint32_t qa[S::kQRegs ? (S::kF16 ? HD / 4 : HD / 2) : 8];  // q of head g as A fragments
         float unscale = 1.f;
         const float* qg = q_s + g * S::kQRow;
-        if constexpr (S::kF16) {
-            float big = 0.f;
-#pragma unroll
-            for (int s = 0; s < HD / 8; ++s) {
-                const float2 v = *reinterpret_cast<const float2*>(qg + 8 * s + 2 * t);
-                big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
-            int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
-            e = e == 128 ? 13 : max(-113, min(e, 126));
-            const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-            unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-#pragma unroll
-            for (int s = 0; s < HD / 8; ++s) {
-                const float2 v = *reinterpret_cast<const float2*>(qg + 8 * s + 2 * t);
-                split_f16(v.x * sc, v.y * sc, qa[2 * s], qa[2 * s + 1]);
-            }
-        } else if constexpr (S::kQRegs) {
-#pragma unroll
-            for (int s = 0; s < HD / 16; ++s) {
-                const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
-                split_tf32(v.x, qa[8 * s], qa[8 * s + 1]);
-                split_tf32(v.y, qa[8 * s + 2], qa[8 * s + 3]);
-                split_tf32(v.z, qa[8 * s + 4], qa[8 * s + 5]);
-                split_tf32(v.w, qa[8 * s + 6], qa[8 * s + 7]);
-            }
-        }
-        if (S::kQAhead && follows) load_q(next);  // waited for at this segment's end
-
-        float O[S::kNT][4] = {};
+        float O[S::kNT][4];
         float m = -CUDART_INF_F, l = 0.f;  // of head g; l over this lane's slots
-        for (; u < ue; u += kWarps) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
-            __syncwarp();  // unit u is there, and every lane is done with the one before it
+        for (bool fresh = true;;) {
+            if (warm == 0) {
+                if (fresh) {
+                    fresh = false;
+                    if constexpr (S::kF16) {
+                        float big = 0.f;
+#pragma unroll
+                        for (int s = 0; s < HD / 8; ++s) {
+                            const float2 v = *reinterpret_cast<const float2*>(qg + 8 * s + 2 * t);
+                            big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+                        }
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                        // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
+                        int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
+                        e = e == 128 ? 13 : max(-113, min(e, 126));
+                        const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+                        unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+#pragma unroll
+                        for (int s = 0; s < HD / 8; ++s) {
+                            const float2 v = *reinterpret_cast<const float2*>(qg + 8 * s + 2 * t);
+                            split_f16(v.x * sc, v.y * sc, qa[2 * s], qa[2 * s + 1]);
+                        }
+                    } else if constexpr (S::kQRegs) {
+#pragma unroll
+                        for (int s = 0; s < HD / 16; ++s) {
+                            const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
+                            split_tf32(v.x, qa[8 * s], qa[8 * s + 1]);
+                            split_tf32(v.y, qa[8 * s + 2], qa[8 * s + 3]);
+                            split_tf32(v.z, qa[8 * s + 4], qa[8 * s + 5]);
+                            split_tf32(v.w, qa[8 * s + 6], qa[8 * s + 7]);
+                        }
+                    }
+                    if (S::kQAhead && follows) load_q(next);  // waited for at this segment's end
+#pragma unroll
+                    for (int n = 0; n < S::kNT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) O[n][i] = 0.f;
+                }
+                if (u >= ue) break;
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+                __syncwarp();  // unit u is there, and every lane is done with the one before it
+            }
             copy(asked);  // into that one's stage
             asked = ask();
+            if (warm > 0) {
+                if (--warm == 0) {
+                    keep_q();
+                    __syncthreads();
+                }
+                continue;
+            }
             const uint32_t tile = smem_addr(ring + get * 2 * S::kTileBytes);
             const uint32_t live = live_s[get];
             constexpr int kST = UK / 8;
@@ -689,6 +727,7 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
                 }
             }
             get = get + 1 == S::kStages ? 0 : get + 1;
+            u += S::kWarps;
         }
         u -= ue;  // the warp's first unit of the next segment
 
@@ -724,13 +763,13 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
         float M = m, L = l;
         if (warp == 0) {
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, merge_m[w * kAttnHeads + g]);
+            for (int w = 1; w < S::kWarps; ++w) M = fmaxf(M, merge_m[w * kAttnHeads + g]);
             const float k0 = m == M ? 1.f : ex2(m - M);
             L = l * k0;
 #pragma unroll
             for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(acc[i], k0, make_float4(0.f, 0.f, 0.f, 0.f));
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
+            for (int w = 1; w < S::kWarps; ++w) {
                 const float mw = merge_m[w * kAttnHeads + g], k = mw == M ? 1.f : ex2(mw - M);
                 L = fmaf(merge_l[w * kAttnHeads + g], k, L);
                 const float4* mo = reinterpret_cast<const float4*>(merge) + (w - 1) * S::kQuads * 32 + lane;
@@ -738,101 +777,134 @@ __global__ void __launch_bounds__(kSplitThreads, Split<KT, HD>::kCtas)
                 for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(mo[i * 32], k, acc[i]);
             }
         }
-        // Outputs go through shared memory (the warps' O, read by now) into rows.
-        auto keep_out = [&](int i, float4 o, float inv) {  // no weight at all (every score -inf) gives NaN, as the formula does
-            const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) merge[g * HD + quad_col<S::kF16>(i, j, t)] = v[j];
-        };
-        bool done = us == 0 && ue == at.units;
-        if (done) {
+        if (us == 0 && ue == at.units) {
             if (warp == 0) {
-                __syncwarp();
+                __syncwarp();  // the warps' O have been read: their place takes the rows
                 const float inv = 1.f / L;
 #pragma unroll
                 for (int i = 0; i < S::kQuads; ++i) keep_out(i, acc[i], inv);
                 if (t == 0 && g < nheads) put_lse(p, at.b, h0 + g, M - kPShift, L, false);
+                __syncwarp();
+                put_rows(at.b, h0, nheads);
             }
         } else {
-            // this CTA's part; an item's parts are those of its CTAs c0 .. c1
+            // This CTA's part; an item's parts are those of its CTAs c0 .. c1, and the last of a group of
+            // them to be counted will be joined by its CTA, at the end of all its units.  A CTA has two
+            // such segments at most, its first and its last.
             if (!own) {
                 c0 = static_cast<int>(div_small(at.start, share));
                 c1 = static_cast<int>(div_small(at.start + at.units - 1, share));
             }
-            const int n = c1 - c0 + 1;
-            auto part = [&](int c) { return p.part + static_cast<int64_t>(2 * c + (c == c0)) * S::kPartFloats; };
             if (warp == 0) {
-                float* to = part(blockIdx.x);
+                const Pending e = {at.b, h0, nheads, c0, c1 - c0 + 1, 0u};
+                float* to = part(e, blockIdx.x);
                 if (g < nheads) {
 #pragma unroll
                     for (int i = 0; i < S::kQuads; ++i) __stcg(reinterpret_cast<float4*>(to) + i * 32 + lane, acc[i]);
                     if (t == 0) __stcg(reinterpret_cast<float2*>(to + kAttnHeads * HD) + g, make_float2(M, L));
                 }
                 __syncwarp();
-                // release the part (the warp's writes come before, by its barrier) and, in the last CTA,
-                // acquire the others'
-                if (lane == 0) last_s = atom_add_acq_rel(p.counters + c0, 1u);
-            }
-            __syncthreads();
-            if (last_s == static_cast<unsigned int>(n - 1)) {
-                if (tid == 0) p.counters[c0] = 0u;
-                if (g < nheads) {  // a quarter of the quads for each warp, some parts at a time
-                    constexpr int kMine = S::kQuads / kWarps, kBatch = HD == 256 ? 4 : 8;
-                    float4 sum[kMine] = {};
-                    float Mh = -CUDART_INF_F, Lh = 0.f;
-                    for (int b0 = 0; b0 < n; b0 += kBatch) {
-                        float2 ml[kBatch];
-                        float4 o[kBatch][kMine];
-                        float mb = Mh;
-#pragma unroll
-                        for (int c = 0; c < kBatch; ++c) {
-                            ml[c] = make_float2(-CUDART_INF_F, 0.f);
-                            if (b0 + c < n) {
-                                const float4* from = reinterpret_cast<const float4*>(part(c0 + b0 + c));
-                                ml[c] = __ldcg(reinterpret_cast<const float2*>(from + S::kQuads * 32) + g);
-#pragma unroll
-                                for (int i = 0; i < kMine; ++i) o[c][i] = __ldcg(from + (warp * kMine + i) * 32 + lane);
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < kBatch; ++c) mb = fmaxf(mb, ml[c].x);
-                        const float keep = Mh == mb ? 1.f : ex2(Mh - mb);
-                        Mh = mb;
-                        Lh *= keep;
-#pragma unroll
-                        for (int i = 0; i < kMine; ++i) sum[i] = fma4(sum[i], keep, make_float4(0.f, 0.f, 0.f, 0.f));
-#pragma unroll
-                        for (int c = 0; c < kBatch; ++c)
-                            if (b0 + c < n) {
-                                const float k = ml[c].x == Mh ? 1.f : ex2(ml[c].x - Mh);
-                                Lh = fmaf(ml[c].y, k, Lh);
-#pragma unroll
-                                for (int i = 0; i < kMine; ++i) sum[i] = fma4(o[c][i], k, sum[i]);
-                            }
-                    }
-                    const float inv = 1.f / Lh;
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) keep_out(warp * kMine + i, sum[i], inv);
-                    if (warp == 0 && t == 0) put_lse(p, at.b, h0 + g, Mh - kPShift, Lh, false);
+                if (lane == 0) {
+                    const int fan = join_fan(e.n), first = e.c0 + (blockIdx.x - e.c0) / fan * fan;
+                    pending_s[pendings] = e;
+                    // release the part (the warp's writes come before, by its barrier)
+                    pending_s[pendings].counted = atom_add_acq_rel(p.counters + 2 * first + (first == e.c0), 1u);
                 }
-                __syncthreads();
-                done = true;
             }
-        }
-        if (done && warp == 0) {
-            __syncwarp();
-            const int64_t to = at.b * p.out_stride + static_cast<int64_t>(h0) * p.hd;
-#pragma unroll 1
-            for (int e = lane * 4; e < nheads * p.hd; e += 128) {  // hd is a multiple of 4 here
-                const int h = e / p.hd;
-                const float4 v = *reinterpret_cast<const float4*>(merge + h * HD + (e - h * p.hd));
-                put_out4(p, to + e, v);
-            }
+            ++pendings;
         }
         if (!follows) break;
         at = next;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+
+    // Join what this CTA was the last to complete: groups of neighbouring parts first, then the groups
+    // (one group where the parts are few).
+#pragma unroll 1
+    for (int k = 0; k < pendings; ++k) {
+        __syncthreads();  // pending_s is written; the ring and the last join's rows have been read
+        const Pending e = pending_s[k];
+        const int fan = join_fan(e.n), groups = (e.n + fan - 1) / fan, group = (blockIdx.x - e.c0) / fan;
+        int first = e.c0 + group * fan, count = min(fan, e.n - group * fan), stride = 1;
+        unsigned int* counter = p.counters + 2 * first + (first == e.c0);
+        unsigned int counted = e.counted;
+        constexpr int kMine = 2 * HD / S::kThreads;  // fours of one head that a thread joins
+        // Each thread copies its pieces of many parts into shared memory of its own (the ring's place), all
+        // in flight together, then sums them with a short loop: code that runs once is fetched as it runs.
+        constexpr int kPieces = S::kThreads * 16 * (kMine + 1);
+        constexpr int kBatch = S::kWarps * S::kRingBytes / kPieces;
+        float4 sum[kMine];
+        float Mh, Lh;
+#pragma unroll 1
+        while (counted == static_cast<unsigned int>(count - 1)) {
+            if (tid == 0) *counter = 0u;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            Mh = -CUDART_INF_F;
+            Lh = 0.f;
+#pragma unroll 1
+            for (int b0 = 0; b0 < count; b0 += kBatch) {
+                const int nb = min(kBatch, count - b0);
+                if (g < e.nheads) {
+#pragma unroll 1
+                    for (int c = 0; c < nb; ++c) {
+                        const float4* from = reinterpret_cast<const float4*>(part(e, first + (b0 + c) * stride));
+                        const uint32_t to = smem_addr(smem + c * kPieces);
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i)
+                            cp_async16(to + (i * S::kThreads + tid) * 16, from + i * S::kThreads + tid, 16u);
+                        // maximum and sum of heads 2i and 2i + 1
+                        cp_async16(to + (kMine * S::kThreads + tid) * 16, from + S::kQuads * 32 + (g >> 1), 16u);
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    const float2* ml = reinterpret_cast<const float2*>(smem) + 2 * (kMine * S::kThreads + tid) + (g & 1);
+                    float mb = Mh;
+#pragma unroll 4
+                    for (int c = 0; c < nb; ++c) mb = fmaxf(mb, ml[c * (kPieces / 8)].x);
+                    const float keep = Mh == mb ? 1.f : ex2(Mh - mb);
+                    Mh = mb;
+                    Lh *= keep;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) sum[i] = fma4(sum[i], keep, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll 4
+                    for (int c = 0; c < nb; ++c) {
+                        const float2 v = ml[c * (kPieces / 8)];
+                        const float k = v.x == Mh ? 1.f : ex2(v.x - Mh);
+                        Lh = fmaf(v.y, k, Lh);
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i)
+                            sum[i] = fma4(reinterpret_cast<const float4*>(smem + c * kPieces)[i * S::kThreads + tid], k, sum[i]);
+                    }
+                }
+            }
+            if (stride > 1 || groups == 1) {
+                if (g < e.nheads) {
+                    const float inv = 1.f / Lh;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) keep_out(i * S::kWarps + warp, sum[i], inv);
+                    if (warp == 0 && t == 0) put_lse(p, e.b, e.h0 + g, Mh - kPShift, Lh, false);
+                }
+                __syncthreads();
+                if (warp == 0) put_rows(e.b, e.h0, e.nheads);
+                break;
+            }
+            __syncthreads();  // the parts have been read: the first one's place takes the group's
+            if (g < e.nheads) {
+                float4* to = reinterpret_cast<float4*>(part(e, first));
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) __stcg(to + i * S::kThreads + tid, sum[i]);
+                if (warp == 0 && t == 0) __stcg(reinterpret_cast<float2*>(to + S::kQuads * 32) + g, make_float2(Mh, Lh));
+            }
+            first = e.c0;
+            count = groups;
+            stride = fan;
+            counter = p.counters + 2 * kAttnMaxCtas + e.c0;
+            __syncthreads();
+            if (tid == 0) last_s = atom_add_acq_rel(counter, 1u);
+            __syncthreads();
+            counted = last_s;
+        }
+    }
 }
 
 // ---------------------------------------------------------------- running attention weights
@@ -883,7 +955,7 @@ cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int grid = sms * S::kCtas < kAttnMaxCtas ? sms * S::kCtas : kAttnMaxCtas;
     const int blocks_per_head = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
-    return launch_dependent(kernel, grid, kSplitThreads, S::kSmem, stream, p, blocks_per_head);
+    return launch_dependent(kernel, grid, S::kThreads, S::kSmem, stream, p, blocks_per_head);
 }
 
 }  // namespace

@@ -137,7 +137,7 @@ struct PagedAttnParams {
     int64_t out_stride;
     float* lse;              // [n_seq x nh] or null
     int32_t add_weight;
-    unsigned int* counters;  // [kAttnMaxCtas], zero between calls
+    unsigned int* counters;  // [3 * kAttnMaxCtas], zero between calls
     float* part;             // [2 * kAttnMaxCtas][kAttnHeads][hd padded to 64, 128 or 256, + 2]
     float* lse2;             // [n_seq x nh], log2 domain (add_weight)
     float* scores;           // [n_seq x nh x capacity], log2 domain (add_weight)

@@ -255,6 +255,10 @@ def run_attn(nh, nkv, hd, kv, page, lens, window=0, out="f32", weights=False, se
     (4, 2, 64, "f16", 16, [17] * 300, dict(weights=True)),           # more sequences than blocks
     (4, 1, 64, "f16", 16, [40 * (i % 7) for i in range(200)], dict(max_pages=20)),
     (40, 8, 128, "f16", 64, [20011], dict(weights=True)),
+    (5, 1, 128, "f16", 64, [30011], dict(weights=True)),             # one item over the whole GPU
+    (3, 1, 64, "f32", 64, [9000, 50], {}),
+    (8, 1, 256, "f16", 64, [9000], {}),
+    (2, 2, 64, "f16", 16, [12000] + [33] * 60, dict(weights=True)),  # one long among many short
 ], ids=short)
 def test_attn(qkv, nh, nkv, hd, kv, page, lens, kw):
     run_attn(nh, nkv, hd, kv, page, lens, **kw)
