@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
         float w[kWeightSlots];
 #pragma unroll
         for (int k = 0; k < kWeightSlots; ++k) w[k] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int g = 0; g < G; ++g) {
             const float lse2 = __ldcg(p.lse2 + h0 + g);
             const float* s = p.scores + (h0 + g) * cap + j0;

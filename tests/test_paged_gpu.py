@@ -371,11 +371,12 @@ def test_attn_workspace_serves_other_shapes(qkv):
 
 # ---------------------------------------------------------------- eviction
 
-def run_evict(nkv, hd, kv, page, lens, budget, recent, weights, seed=0, pool_off=0, inplace=False, shuffle=True):
+def run_evict(nkv, hd, kv, page, lens, budget, recent, weights, seed=0, pool_off=0, inplace=False, shuffle=True,
+              max_pages=None):
     import torch
     rng = np.random.default_rng(seed)
     B = len(lens)
-    c = ref.Cache(rng, B, nkv, hd, kv, page, max(1, -(-max(lens) // page)), lens=lens, fill=3.0)
+    c = ref.Cache(rng, B, nkv, hd, kv, page, max_pages or max(1, -(-max(lens) // page)), lens=lens, fill=3.0)
     w = weights(rng, (B, nkv, c.cap)).astype(np.float32)
     pos = np.tile(np.arange(c.cap, dtype=np.int32), (B, nkv, 1))
     if shuffle:
@@ -447,6 +448,12 @@ def wild(rng, shape):
     (1, 64, "f16", 256, [40001], 17000, 300, heavy, dict(inplace=True)),
     (1, 8, "f16", 256, [70000], 60000, 300, tied, {}),
     (2, 64, "f16", 16, [30] * 150, 20, 5, tied, {}),
+    (2, 64, "f16", 16, [5000, 9], 4500, 5, heavy, dict(max_pages=400, inplace=True)),
+    (8, 64, "f16", 64, [20000], 700, 5, wild, {}),
+    (160, 2, "f16", 64, [2000, 130], 129, 20, tied, dict(max_pages=520)),        # many heads, large capacity:
+    (160, 2, "f32", 64, [130, 2000], 1500, 0, heavy, dict(max_pages=520, inplace=True)),  # keys made again
+    (1, 2, "f16", 256, [3001], 2000, 7, tied, dict(max_pages=2100)),
+    (1, 2, "f32", 256, [3001], 11, 7, heavy, dict(max_pages=2100, inplace=True)),
 ], ids=short)
 def test_evict(qkv, nkv, hd, kv, page, lens, budget, recent, weights, kw):
     run_evict(nkv, hd, kv, page, lens, budget, recent, weights, **kw)
