@@ -503,8 +503,8 @@ qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const 
  *              min(len, budget) are written.  The cache must have both.
  *   budget >= 1, 0 <= recent <= budget.
  * Sequences must not share pages (a shared prefix would be changed under the others).  No order of
- * execution changes the result.  d_workspace: qkv_evict_workspace_bytes bytes, 4-byte aligned, any
- * contents (null where that is 0), not shared by calls that overlap on the GPU.
+ * execution changes the result.  d_workspace: device memory of qkv_evict_workspace_bytes bytes, 4-byte
+ * aligned, any contents, not shared by calls that overlap on the GPU.
  * Errors: INVALID_ARG, CUDA. */
 qkv_status qkv_evict_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out);
 qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* cache, const int32_t* d_lens,

@@ -193,7 +193,7 @@ extern "C" qkv_status qkv_evict_workspace_bytes(const qkv_plan* plan, const qkv_
     qkv_status st = check_shape(plan, cache);
     if (st != QKV_OK) return st;
     REQUIRE(out, "out is null");
-    *out = sizeof(int32_t) * 2 * static_cast<size_t>(capacity(cache) / 2) * cache->n_seq * plan->d.n_head_kv;
+    *out = sizeof(int32_t) * (1 + 2 * static_cast<size_t>(capacity(cache) / 2)) * cache->n_seq * plan->d.n_head_kv;
     return QKV_OK;
 }
 
@@ -222,7 +222,7 @@ extern "C" qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* c
     size_t need = 0;
     st = qkv_evict_workspace_bytes(plan, cache, &need);
     if (st != QKV_OK) return st;
-    REQUIRE(workspace_bytes >= need && (d_workspace || need == 0), "the workspace has %zu bytes, %zu are needed",
+    REQUIRE(workspace_bytes >= need && d_workspace, "the workspace has %zu bytes, %zu are needed",
             workspace_bytes, need);
     REQUIRE(aligned(d_workspace, 4), "d_workspace must be 4-byte aligned");
     p.lens = d_lens;
@@ -232,7 +232,8 @@ extern "C" qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* c
     p.lens_out = lens_out;
     p.weight_out = weight_out;
     p.pos_out = pos_out;
-    p.lists = static_cast<int32_t*>(d_workspace);
+    p.moves = static_cast<int32_t*>(d_workspace);
+    p.lists = p.moves + static_cast<size_t>(cache->n_seq) * plan->d.n_head_kv;
     p.nkv = plan->d.n_head_kv;
     p.hd = plan->d.head_dim;
     p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;

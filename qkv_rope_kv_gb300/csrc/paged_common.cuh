@@ -20,17 +20,27 @@ __device__ __forceinline__ void flag_bad(unsigned int bit, int value) {
     atomicExch(&g_paged_status[1], static_cast<unsigned int>(value));
 }
 
-// Element offset of the row of slot `slot` of sequence `seq` in the pools, or -1 (and the
-// status flag) where the table names a page that is not there.  64-bit: a pool can hold
-// more than 2^31 elements.
-__device__ __forceinline__ int64_t row_offset(const PagedView& c, int seq, int slot) {
+// A slot's page and its row there; a table entry is asked for here and looked at by row_offset(), so that
+// several can be in flight together.
+struct PageRef {
+    int id, in_page;
+};
+__device__ __forceinline__ PageRef page_ref(const PagedView& c, int seq, int slot) {
     const int pg = slot / c.page_size;
-    const int id = __ldg(c.table + static_cast<int64_t>(seq) * c.max_pages + pg);
-    if (static_cast<unsigned int>(id) >= static_cast<unsigned int>(c.n_pages)) {
-        flag_bad(kFlagIndexRange, id);
+    return {__ldg(c.table + static_cast<int64_t>(seq) * c.max_pages + pg), slot - pg * c.page_size};
+}
+// Element offset of the slot's row in the pools, or -1 (and the status flag) where the table names a page
+// that is not there.  64-bit: a pool can hold more than 2^31 elements.
+__device__ __forceinline__ int64_t row_offset(const PagedView& c, PageRef r) {
+    if (static_cast<unsigned int>(r.id) >= static_cast<unsigned int>(c.n_pages)) {
+        flag_bad(kFlagIndexRange, r.id);
         return -1;
     }
-    return id * c.page_stride + static_cast<int64_t>(slot - pg * c.page_size) * c.nkt;
+    return r.id * c.page_stride + static_cast<int64_t>(r.in_page) * c.nkt;
+}
+
+__device__ __forceinline__ int64_t row_offset(const PagedView& c, int seq, int slot) {
+    return row_offset(c, page_ref(c, seq, slot));
 }
 
 // Length of sequence b, or 0 (and the status flag) where it is outside [0, capacity].

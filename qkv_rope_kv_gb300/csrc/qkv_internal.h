@@ -154,6 +154,7 @@ struct PagedEvictParams {
     int32_t* lens_out;
     float* weight_out;
     int32_t* pos_out;
+    int32_t* moves;  // [n_seq x nkv]: how many moves an item has
     int32_t* lists;  // [n_seq x nkv][2][capacity / 2]: slots freed, slots moved
     int32_t nkv, hd, kv_f16;
 };

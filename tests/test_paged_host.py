@@ -111,7 +111,7 @@ def test_workspace_sizes(lib):
     assert tracked - n.value >= 4 * 3 * 4 * 64 and n.value % 256 == 0
     assert attn(lib, pl, cache(slot_weight=None), ws_bytes=n.value - 1) == q.QKV_ERR_INVALID_ARG
     assert lib.qkv_evict_workspace_bytes(pl.handle, ctypes.byref(cache()), ctypes.byref(n)) == 0
-    assert n.value <= 4 * 3 * 2 * 64
+    assert n.value == 4 * 3 * 2 * (1 + 64)  # a count and two half lists for each sequence and kv head
     assert lib.qkv_evict_workspace_bytes(pl.handle, ctypes.byref(cache()), None) == q.QKV_ERR_INVALID_ARG
     assert lib.qkv_attn_workspace_bytes(None, ctypes.byref(cache()), ctypes.byref(n)) == q.QKV_ERR_INVALID_ARG
 
