@@ -127,6 +127,7 @@ extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged
     p.nkv = plan->d.n_head_kv;
     p.hd = plan->d.head_dim;
     p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
+    p.inv_hd = 1.f / static_cast<float>(p.hd);
     std::memcpy(p.inv_freq, plan->inv_freq, sizeof p.inv_freq);
     const cudaError_t e = launch_paged_store(p, y_dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged store kernel launch");

@@ -61,8 +61,9 @@ __device__ __forceinline__ float4 norm4(float4 a, float inv, float4 w) {
 __device__ __forceinline__ float sq4(float4 a, float s) {
     return __fmaf_rn(a.x, a.x, __fmaf_rn(a.y, a.y, __fmaf_rn(a.z, a.z, __fmaf_rn(a.w, a.w, s))));
 }
-__device__ __forceinline__ float head_inv(float ss, int hd, float eps) {
-    return __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(hd)), eps)));
+// 1 / rms of a head from the sum of its squares.
+__device__ __forceinline__ float head_inv(const PagedStoreParams& p, float ss) {
+    return rsqrtf(__fadd_rn(__fmul_rn(ss, p.inv_hd), p.eps));
 }
 
 // Where the CTA's tokens go: row offsets (-1: not stored), sequences and slots.
@@ -71,32 +72,10 @@ struct Tokens {
     int seq[kMaxTokens], slot[kMaxTokens], pos[kMaxTokens];
 };
 
-// LP lanes work on one head; with VEC a lane holds four neighbouring pairs (LP = hd / 8, a power
-// of two), otherwise a warp strides over the head's pairs one by one (any even hd, any alignment).
-template <typename YT, bool VEC>
-__global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_constant__ PagedStoreParams p, int tokens,
-                                                               int lp, int heads_per_cta) {
-    __shared__ float2 cs_s[kMaxTokens][QKV_MAX_HEAD_DIM / 2];
-    __shared__ Tokens tk;
-    qkv_ptx::griddep_wait();
+// Look up the CTA's tokens and make the (cos, sin) of their pairs.
+__device__ __forceinline__ void token_tables(const PagedStoreParams& p, int t0, int nt, Tokens& tk,
+                                             float2 (*cs_s)[QKV_MAX_HEAD_DIM / 2]) {
     const int half = p.hd >> 1;
-    const int t0 = blockIdx.x * tokens;
-    const int nt = min(tokens, p.nt - t0);
-    const int h0 = blockIdx.y * heads_per_cta;
-    const int nheads = min(heads_per_cta, p.nh + 2 * p.nkv - h0);
-    const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp;
-    const int items = nt * nheads;
-    // One round's values are loaded a round ahead, the first round's before the angles are there.
-    Raw4<YT> n0, n1;
-    auto fetch = [&](int i) {
-        if (VEC && i < items) {
-            const int t = i / nheads, h = h0 + (i - t * nheads);
-            const YT* y = static_cast<const YT*>(p.y) + (t0 + t) * p.y_stride + static_cast<int64_t>(h) * p.hd + 4 * l;
-            n0.load(y);
-            n1.load(y + half);
-        }
-    };
-    fetch(g);
     if (threadIdx.x < nt) {
         const int t = t0 + threadIdx.x;
         const int pos = __ldg(p.positions + t);
@@ -118,99 +97,165 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_cons
         const int t = i / half, d = i - t * half;
         cs_s[t][d] = rope_cos_sin(__ldg(p.positions + t0 + t), p.inv_freq[d]);
     }
-    __syncthreads();
+}
 
-    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
+// A k head's slot starts with no weight.
+__device__ __forceinline__ void track_slot(const PagedStoreParams& p, const Tokens& tk, int t, int kv_head) {
+    const int64_t at = (static_cast<int64_t>(tk.seq[t]) * p.nkv + kv_head) * p.c.max_pages * p.c.page_size + tk.slot[t];
+    if (p.c.slot_weight) p.c.slot_weight[at] = 0.f;
+    if (p.c.slot_pos) p.c.slot_pos[at] = tk.pos[t];
+}
+
+// LP lanes work on one head, four neighbouring pairs a lane (LP: the power of two at or above hd / 8; the
+// lanes beyond idle).  A group keeps its head for the CTA's T tokens, so bias, norm weight and addresses are
+// made once, and the loads of all T (of the next head, as each is used) are in flight together.
+template <typename YT, int T>
+__global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_constant__ PagedStoreParams p, int lp,
+                                                               int heads_per_cta) {
+    __shared__ __align__(16) float2 cs_s[T][QKV_MAX_HEAD_DIM / 2];
+    __shared__ Tokens tk;
+    qkv_ptx::griddep_wait();
+    const int half = p.hd >> 1;
+    const int t0 = blockIdx.x * T, nt = min(T, p.nt - t0);
+    const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
+    const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp, d = 4 * l;
+    int h = blockIdx.y * heads_per_cta + g;
+    const YT* y = static_cast<const YT*>(p.y) + t0 * p.y_stride + static_cast<int64_t>(h) * p.hd + d;
+    Raw4<YT> n0[T], n1[T];
+    const bool wide = d < half;  // a lane that has pairs
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (wide && h < end && t < nt) {
+            n0[t].load(y + t * p.y_stride);
+            n1[t].load(y + t * p.y_stride + half);
+        }
+    token_tables(p, t0, nt, tk, cs_s);
+    __syncthreads();
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     // every group makes the same number of rounds: the lanes of a warp meet in its shuffles
-    for (int i0 = 0; i0 < items; i0 += groups) {
-        const bool live = i0 + g < items;
-        const int i = live ? i0 + g : items - 1;
-        const int t = i / nheads, h = h0 + (i - t * nheads);
+    for (int h_first = blockIdx.y * heads_per_cta; h_first < end; h_first += groups, h += groups) {
+        const bool live = wide && h < end;
         const int sec = h < p.nh ? 0 : h < p.nh + p.nkv ? 1 : 2;
-        const int j0 = (sec == 0 ? h : sec == 1 ? h - p.nh : h - p.nh - p.nkv) * p.hd;  // within the section
-        const YT* y = static_cast<const YT*>(p.y) + (t0 + t) * p.y_stride + static_cast<int64_t>(h) * p.hd;
-        const float* b = p.bias ? p.bias + static_cast<int64_t>(h) * p.hd : nullptr;
-        const float* w = sec == 2 ? nullptr : p.norm_w[sec];
-        const int64_t row = tk.row[t];
-        const bool write = live && tk.seq[t] >= 0;
-        float* q = p.q + (t0 + t) * p.q_stride + j0;
-        void* kv = sec == 1 ? p.c.k : p.c.v;
-        if constexpr (VEC) {
-            const int d = 4 * l;
-            float4 a0 = n0.get(), a1 = n1.get();
-            fetch(i0 + g + groups);
-            if (b) {
-                a0 = add4(a0, load4(b + d));
-                a1 = add4(a1, load4(b + half + d));
+        const int j = (sec == 0 ? h : sec == 1 ? h - p.nh : h - p.nh - p.nkv) * p.hd + d;  // within the section
+        const bool norm = p.norm_w[0] != nullptr;  // v heads then only join the shuffles
+        float4 b0 = zero, b1 = zero, w0 = zero, w1 = zero;
+        if (live && p.bias) {
+            b0 = load4(p.bias + static_cast<int64_t>(h) * p.hd + d);
+            b1 = load4(p.bias + static_cast<int64_t>(h) * p.hd + half + d);
+        }
+        if (live && norm && sec != 2) {
+            w0 = load4(p.norm_w[sec] + d);
+            w1 = load4(p.norm_w[sec] + half + d);
+        }
+        y += static_cast<int64_t>(groups) * p.hd;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float4 a0 = zero, a1 = zero;
+            if (live && t < nt) {
+                a0 = n0[t].get();
+                a1 = n1[t].get();
+            }
+            if (wide && h + groups < end && t < nt) {
+                n0[t].load(y + t * p.y_stride);
+                n1[t].load(y + t * p.y_stride + half);
+            }
+            if (p.bias) {
+                a0 = add4(a0, b0);
+                a1 = add4(a1, b1);
             }
             float inv = 0.f;
-            if (p.norm_w[0]) {  // uniform in the launch; v heads only join the shuffles
+            if (norm) {
                 float ss = sq4(a0, sq4(a1, 0.f));
                 for (int o = lp >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                inv = head_inv(ss, p.hd, p.eps);
+                inv = head_inv(p, ss);
             }
+            if (!live || t >= nt || tk.seq[t] < 0) continue;
             if (sec != 2) {
-                if (w) {
-                    a0 = norm4(a0, inv, load4(w + d));
-                    a1 = norm4(a1, inv, load4(w + half + d));
+                if (norm) {
+                    a0 = norm4(a0, inv, w0);
+                    a1 = norm4(a1, inv, w1);
                 }
-                const float2* cs = cs_s[t] + d;
+                const float4 c0 = *reinterpret_cast<const float4*>(cs_s[t] + d);
+                const float4 c1 = *reinterpret_cast<const float4*>(cs_s[t] + d + 2);
                 float4 r0, r1;
-                rope_rotate_cs(a0.x, a1.x, cs[0], r0.x, r1.x);
-                rope_rotate_cs(a0.y, a1.y, cs[1], r0.y, r1.y);
-                rope_rotate_cs(a0.z, a1.z, cs[2], r0.z, r1.z);
-                rope_rotate_cs(a0.w, a1.w, cs[3], r0.w, r1.w);
+                rope_rotate_cs(a0.x, a1.x, make_float2(c0.x, c0.y), r0.x, r1.x);
+                rope_rotate_cs(a0.y, a1.y, make_float2(c0.z, c0.w), r0.y, r1.y);
+                rope_rotate_cs(a0.z, a1.z, make_float2(c1.x, c1.y), r0.z, r1.z);
+                rope_rotate_cs(a0.w, a1.w, make_float2(c1.z, c1.w), r0.w, r1.w);
                 a0 = r0;
                 a1 = r1;
             }
-            if (write && sec == 0) {
-                *reinterpret_cast<float4*>(q + d) = a0;
-                *reinterpret_cast<float4*>(q + half + d) = a1;
-            } else if (write && row >= 0) {
-                kv_put4(kv, p.kv_f16, row + j0 + d, a0);
-                kv_put4(kv, p.kv_f16, row + j0 + half + d, a1);
-            }
-        } else {
-            float inv = 0.f;
-            if (p.norm_w[0]) {
-                float ss = 0.f;
-                for (int d = l; d < p.hd; d += lp) {
-                    const float z = b ? __fadd_rn(load1(y + d), __ldg(b + d)) : load1(y + d);
-                    ss = __fmaf_rn(z, z, ss);
-                }
-                for (int o = lp >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                inv = head_inv(ss, p.hd, p.eps);
-            }
-            for (int d = l; d < half; d += lp) {
-                float z0 = load1(y + d), z1 = load1(y + half + d);
-                if (b) {
-                    z0 = __fadd_rn(z0, __ldg(b + d));
-                    z1 = __fadd_rn(z1, __ldg(b + half + d));
-                }
-                if (sec != 2) {
-                    if (w) {
-                        z0 = __fmul_rn(__fmul_rn(z0, inv), __ldg(w + d));
-                        z1 = __fmul_rn(__fmul_rn(z1, inv), __ldg(w + half + d));
-                    }
-                    float r0, r1;
-                    rope_rotate_cs(z0, z1, cs_s[t][d], r0, r1);
-                    z0 = r0;
-                    z1 = r1;
-                }
-                if (write && sec == 0) {
-                    q[d] = z0;
-                    q[half + d] = z1;
-                } else if (write && row >= 0) {
-                    kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + d), z0);
-                    kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + half + d), z1);
-                }
+            const int64_t row = tk.row[t];
+            if (sec == 0) {
+                float* q = p.q + (t0 + t) * p.q_stride + j;
+                *reinterpret_cast<float4*>(q) = a0;
+                *reinterpret_cast<float4*>(q + half) = a1;
+            } else if (row >= 0) {
+                void* kv = sec == 1 ? p.c.k : p.c.v;
+                kv_put4(kv, p.kv_f16, row + j, a0);
+                kv_put4(kv, p.kv_f16, row + j + half, a1);
+                if (sec == 1 && l == 0) track_slot(p, tk, t, h - p.nh);
             }
         }
-        if (l == 0 && sec == 1 && write && row >= 0) {
-            const int64_t at = (static_cast<int64_t>(tk.seq[t]) * p.nkv + (h - p.nh)) * cap + tk.slot[t];
-            if (p.c.slot_weight) p.c.slot_weight[at] = 0.f;
-            if (p.c.slot_pos) p.c.slot_pos[at] = tk.pos[t];
+    }
+}
+
+// Any even hd, any alignment: a warp strides over a head's pairs one by one; a token a CTA row.
+template <typename YT>
+__global__ void __launch_bounds__(kThreads) paged_store_any_kernel(const __grid_constant__ PagedStoreParams p,
+                                                                   int heads_per_cta) {
+    __shared__ float2 cs_s[1][QKV_MAX_HEAD_DIM / 2];
+    __shared__ Tokens tk;
+    qkv_ptx::griddep_wait();
+    const int half = p.hd >> 1, t = blockIdx.x, lane = threadIdx.x & 31;
+    const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
+    token_tables(p, t, 1, tk, cs_s);
+    __syncthreads();
+    if (tk.seq[0] < 0) return;
+    const int64_t row = tk.row[0];
+    for (int h = blockIdx.y * heads_per_cta + (threadIdx.x >> 5); h < end; h += kThreads / 32) {
+        const int sec = h < p.nh ? 0 : h < p.nh + p.nkv ? 1 : 2;
+        const int j0 = (sec == 0 ? h : sec == 1 ? h - p.nh : h - p.nh - p.nkv) * p.hd;  // within the section
+        const YT* y = static_cast<const YT*>(p.y) + t * p.y_stride + static_cast<int64_t>(h) * p.hd;
+        const float* b = p.bias ? p.bias + static_cast<int64_t>(h) * p.hd : nullptr;
+        const float* w = sec == 2 ? nullptr : p.norm_w[sec];
+        float* q = p.q + t * p.q_stride + j0;
+        void* kv = sec == 1 ? p.c.k : p.c.v;
+        float inv = 0.f;
+        if (w) {
+            float ss = 0.f;
+            for (int d = lane; d < p.hd; d += 32) {
+                const float z = b ? __fadd_rn(load1(y + d), __ldg(b + d)) : load1(y + d);
+                ss = __fmaf_rn(z, z, ss);
+            }
+            for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            inv = head_inv(p, ss);
         }
+        for (int d = lane; d < half; d += 32) {
+            float z0 = load1(y + d), z1 = load1(y + half + d);
+            if (b) {
+                z0 = __fadd_rn(z0, __ldg(b + d));
+                z1 = __fadd_rn(z1, __ldg(b + half + d));
+            }
+            if (sec != 2) {
+                if (w) {
+                    z0 = __fmul_rn(__fmul_rn(z0, inv), __ldg(w + d));
+                    z1 = __fmul_rn(__fmul_rn(z1, inv), __ldg(w + half + d));
+                }
+                float r0, r1;
+                rope_rotate_cs(z0, z1, cs_s[0][d], r0, r1);
+                z0 = r0;
+                z1 = r1;
+            }
+            if (sec == 0) {
+                q[d] = z0;
+                q[half + d] = z1;
+            } else if (row >= 0) {
+                kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + d), z0);
+                kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + half + d), z1);
+            }
+        }
+        if (lane == 0 && sec == 1 && row >= 0) track_slot(p, tk, 0, h - p.nh);
     }
 }
 
@@ -219,21 +264,22 @@ bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n
 template <typename YT>
 cudaError_t launch_t(const PagedStoreParams& p, cudaStream_t stream) {
     const int ys = sizeof(YT), es = p.kv_f16 ? 2 : 4;
-    const bool pow2 = p.hd >= 16 && (p.hd & (p.hd - 1)) == 0;
-    const bool vec = pow2 && aligned(p.y, 4 * ys) && p.y_stride % 4 == 0 && aligned(p.bias, 16) &&
+    const bool vec = p.hd % 8 == 0 && aligned(p.y, 4 * ys) && p.y_stride % 4 == 0 && aligned(p.bias, 16) &&
                      aligned(p.norm_w[0], 16) && aligned(p.norm_w[1], 16) && aligned(p.q, 16) &&
                      p.q_stride % 4 == 0 && aligned(p.c.k, 4 * es) && aligned(p.c.v, 4 * es) &&
                      p.c.page_stride % 4 == 0;
-    const int lp = vec ? p.hd / 8 : 32;
-    const int heads = p.nh + 2 * p.nkv;
-    // Tokens share a CTA (and its angles' latency) once there are enough for every SM; before that the
+    int lp = 1;
+    while (lp < (vec ? p.hd / 8 : 32)) lp *= 2;
+    // Tokens share a CTA (and what a head needs) once there are enough for every SM; before that the
     // heads of a token are spread over CTAs, down to one round each, at the price of more angles.
-    int tokens = p.nt >= kMaxTokens * 4 * kSms ? kMaxTokens : 1, per = heads;
-    while (tokens == 1 && per > kThreads / lp && static_cast<int64_t>(p.nt) * ((heads + per - 1) / per) < kSms)
-        per = (per + 1) / 2;
+    const bool many = vec && p.nt >= kMaxTokens * 4 * kSms;
+    const int heads = p.nh + 2 * p.nkv, tokens = many ? kMaxTokens : 1;
+    int per = heads;
+    while (!many && per > kThreads / lp && static_cast<int64_t>(p.nt) * ((heads + per - 1) / per) < kSms) per = (per + 1) / 2;
     const dim3 grid((p.nt + tokens - 1) / tokens, (heads + per - 1) / per);
-    return launch_dependent(vec ? paged_store_kernel<YT, true> : paged_store_kernel<YT, false>, grid, kThreads, 0, stream,
-                            p, tokens, lp, per);
+    if (!vec) return launch_dependent(paged_store_any_kernel<YT>, grid, kThreads, 0, stream, p, per);
+    return launch_dependent(many ? paged_store_kernel<YT, kMaxTokens> : paged_store_kernel<YT, 1>, grid, kThreads, 0,
+                            stream, p, lp, per);
 }
 
 }  // namespace

@@ -116,6 +116,7 @@ struct PagedStoreParams {
     float* q;
     int64_t q_stride;
     int32_t nt, nh, nkv, hd, kv_f16;
+    float inv_hd;  // 1 / hd
     float inv_freq[QKV_MAX_HEAD_DIM / 2];
 };
 cudaError_t launch_paged_store(const PagedStoreParams& p, int y_dtype, cudaStream_t stream);
