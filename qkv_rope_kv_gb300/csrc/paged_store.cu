@@ -16,51 +16,84 @@ using namespace qkv_paged;
 
 constexpr int kThreads = 256;
 constexpr int kSms = 152;
-constexpr int kMaxTokens = 4;  // tokens of one CTA: one sincosf a thread at hd = 128
+constexpr int kMaxTokens = 3;  // tokens of one CTA: what fits 64 registers, so four CTAs on an SM
 
-// Four neighbouring values as loaded.  Plain loads, not read-only ones: q may be written over Y.
+// Four neighbouring values as two packed f32 pairs: one instruction works on both of a pair, with each
+// result rounded as its scalar form is.
+using u64 = unsigned long long;
+struct Quad {
+    u64 a, b;
+};
+__device__ __forceinline__ u64 pack(float x, float y) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 add2(u64 x, u64 y) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 x, u64 y) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 x, u64 y, u64 z) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+// (x0 c - x1 s, x0 s + x1 c) of two pairs, each product and the sum rounded.  Both sums are written as
+// x - y = fma(y, -1, x): the assembler joins a packed add with the product before it into one fma.
+__device__ __forceinline__ void rotate2(u64 x0, u64 x1, u64 c, u64 s, u64& r0, u64& r1) {
+    const u64 minus = pack(-1.f, -1.f), neg_s = s ^ 0x8000000080000000ull;
+    r0 = fma2(mul2(x1, s), minus, mul2(x0, c));
+    r1 = fma2(mul2(x0, neg_s), minus, mul2(x1, c));
+}
+__device__ __forceinline__ Quad quad(const float* p) {  // 16-byte aligned
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    return {v.x, v.y};
+}
+
+// Four neighbouring values of Y as loaded.  Plain loads, not read-only ones: q may be written over Y.
 template <typename YT>
 struct Raw4;
 template <>
 struct Raw4<float> {
-    float4 v;
-    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
-    __device__ __forceinline__ float4 get() const { return v; }
+    Quad v;
+    __device__ __forceinline__ void load(const float* p) { v = quad(p); }
+    __device__ __forceinline__ Quad get() const { return v; }
 };
 template <>
 struct Raw4<uint16_t> {  // bf16
     uint2 v;
     __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint2*>(p); }
-    __device__ __forceinline__ float4 get() const {
-        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                           __uint_as_float(v.y & 0xffff0000u));
+    __device__ __forceinline__ Quad get() const {
+        return {pack(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)),
+                pack(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u))};
     }
 };
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) {
     return __uint_as_float(static_cast<uint32_t>(*p) << 16);
 }
 
-__device__ __forceinline__ void kv_put4(void* kv, int f16, int64_t idx, float4 v) {
+__device__ __forceinline__ void kv_put4(void* kv, int f16, int64_t idx, Quad v) {
     if (f16) {
-        __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
+        const float2 x = unpack(v.a), y = unpack(v.b);
+        __half2 h[2] = {__floats2half2_rn(x.x, x.y), __floats2half2_rn(y.x, y.y)};
         *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(kv) + idx) = *reinterpret_cast<uint2*>(h);
     } else {
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(kv) + idx) = v;
+        *reinterpret_cast<ulonglong2*>(reinterpret_cast<float*>(kv) + idx) = make_ulonglong2(v.a, v.b);
     }
 }
 
-__device__ __forceinline__ float4 add4(float4 a, float4 b) {
-    return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
-}
-__device__ __forceinline__ float4 norm4(float4 a, float inv, float4 w) {
-    return make_float4(__fmul_rn(__fmul_rn(a.x, inv), w.x), __fmul_rn(__fmul_rn(a.y, inv), w.y),
-                       __fmul_rn(__fmul_rn(a.z, inv), w.z), __fmul_rn(__fmul_rn(a.w, inv), w.w));
-}
-__device__ __forceinline__ float sq4(float4 a, float s) {
-    return __fmaf_rn(a.x, a.x, __fmaf_rn(a.y, a.y, __fmaf_rn(a.z, a.z, __fmaf_rn(a.w, a.w, s))));
-}
 // 1 / rms of a head from the sum of its squares.
 __device__ __forceinline__ float head_inv(const PagedStoreParams& p, float ss) {
     return rsqrtf(__fadd_rn(__fmul_rn(ss, p.inv_hd), p.eps));
@@ -74,7 +107,8 @@ struct Tokens {
 
 // Look up the CTA's tokens and make the (cos, sin) of their pairs.
 __device__ __forceinline__ void token_tables(const PagedStoreParams& p, int t0, int nt, Tokens& tk,
-                                             float2 (*cs_s)[QKV_MAX_HEAD_DIM / 2]) {
+                                             float (*cos_s)[QKV_MAX_HEAD_DIM / 2],
+                                             float (*sin_s)[QKV_MAX_HEAD_DIM / 2]) {
     const int half = p.hd >> 1;
     if (threadIdx.x < nt) {
         const int t = t0 + threadIdx.x;
@@ -95,7 +129,9 @@ __device__ __forceinline__ void token_tables(const PagedStoreParams& p, int t0, 
     }
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = i / half, d = i - t * half;
-        cs_s[t][d] = rope_cos_sin(__ldg(p.positions + t0 + t), p.inv_freq[d]);
+        const float2 cs = rope_cos_sin(__ldg(p.positions + t0 + t), p.inv_freq[d]);
+        cos_s[t][d] = cs.x;
+        sin_s[t][d] = cs.y;
     }
 }
 
@@ -110,9 +146,9 @@ __device__ __forceinline__ void track_slot(const PagedStoreParams& p, const Toke
 // lanes beyond idle).  A group keeps its head for the CTA's T tokens, so bias, norm weight and addresses are
 // made once, and the loads of all T (of the next head, as each is used) are in flight together.
 template <typename YT, int T>
-__global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_constant__ PagedStoreParams p, int lp,
+__global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_constant__ PagedStoreParams p, int lp,
                                                                int heads_per_cta) {
-    __shared__ __align__(16) float2 cs_s[T][QKV_MAX_HEAD_DIM / 2];
+    __shared__ __align__(16) float cos_s[T][QKV_MAX_HEAD_DIM / 2], sin_s[T][QKV_MAX_HEAD_DIM / 2];
     __shared__ Tokens tk;
     qkv_ptx::griddep_wait();
     const int half = p.hd >> 1;
@@ -129,71 +165,74 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_cons
             n0[t].load(y + t * p.y_stride);
             n1[t].load(y + t * p.y_stride + half);
         }
-    token_tables(p, t0, nt, tk, cs_s);
+    token_tables(p, t0, nt, tk, cos_s, sin_s);
     __syncthreads();
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    int64_t rows[T];
+    bool here[T];  // a token that is no padding
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        here[t] = t < nt && tk.seq[t] >= 0;
+        rows[t] = here[t] ? tk.row[t] : -1;
+    }
+    const bool norm = p.norm_w[0] != nullptr;
     // every group makes the same number of rounds: the lanes of a warp meet in its shuffles
     for (int h_first = blockIdx.y * heads_per_cta; h_first < end; h_first += groups, h += groups) {
-        const bool live = wide && h < end;
+        const bool live = wide && h < end, ahead = wide && h + groups < end;
         const int sec = h < p.nh ? 0 : h < p.nh + p.nkv ? 1 : 2;
         const int j = (sec == 0 ? h : sec == 1 ? h - p.nh : h - p.nh - p.nkv) * p.hd + d;  // within the section
-        const bool norm = p.norm_w[0] != nullptr;  // v heads then only join the shuffles
-        float4 b0 = zero, b1 = zero, w0 = zero, w1 = zero;
+        Quad b0 = {0, 0}, b1 = {0, 0}, w0 = {0, 0}, w1 = {0, 0};
         if (live && p.bias) {
-            b0 = load4(p.bias + static_cast<int64_t>(h) * p.hd + d);
-            b1 = load4(p.bias + static_cast<int64_t>(h) * p.hd + half + d);
+            b0 = quad(p.bias + static_cast<int64_t>(h) * p.hd + d);
+            b1 = quad(p.bias + static_cast<int64_t>(h) * p.hd + half + d);
         }
         if (live && norm && sec != 2) {
-            w0 = load4(p.norm_w[sec] + d);
-            w1 = load4(p.norm_w[sec] + half + d);
+            w0 = quad(p.norm_w[sec] + d);
+            w1 = quad(p.norm_w[sec] + half + d);
         }
         y += static_cast<int64_t>(groups) * p.hd;
+        float* q = p.q + t0 * p.q_stride + j;
+        void* kv = sec == 1 ? p.c.k : p.c.v;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            float4 a0 = zero, a1 = zero;
+            Quad x0 = {0, 0}, x1 = {0, 0};
             if (live && t < nt) {
-                a0 = n0[t].get();
-                a1 = n1[t].get();
+                x0 = n0[t].get();
+                x1 = n1[t].get();
             }
-            if (wide && h + groups < end && t < nt) {
+            if (ahead && t < nt) {
                 n0[t].load(y + t * p.y_stride);
                 n1[t].load(y + t * p.y_stride + half);
             }
             if (p.bias) {
-                a0 = add4(a0, b0);
-                a1 = add4(a1, b1);
+                x0 = {add2(x0.a, b0.a), add2(x0.b, b0.b)};
+                x1 = {add2(x1.a, b1.a), add2(x1.b, b1.b)};
             }
-            float inv = 0.f;
-            if (norm) {
-                float ss = sq4(a0, sq4(a1, 0.f));
+            if (norm) {  // v heads only join the shuffles
+                const float2 sq = unpack(fma2(x0.a, x0.a, fma2(x0.b, x0.b, fma2(x1.a, x1.a, mul2(x1.b, x1.b)))));
+                float ss = sq.x + sq.y;
                 for (int o = lp >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                inv = head_inv(p, ss);
-            }
-            if (!live || t >= nt || tk.seq[t] < 0) continue;
-            if (sec != 2) {
-                if (norm) {
-                    a0 = norm4(a0, inv, w0);
-                    a1 = norm4(a1, inv, w1);
+                if (sec != 2) {
+                    const float inv = head_inv(p, ss);
+                    const u64 i2 = pack(inv, inv);
+                    x0 = {mul2(mul2(x0.a, i2), w0.a), mul2(mul2(x0.b, i2), w0.b)};
+                    x1 = {mul2(mul2(x1.a, i2), w1.a), mul2(mul2(x1.b, i2), w1.b)};
                 }
-                const float4 c0 = *reinterpret_cast<const float4*>(cs_s[t] + d);
-                const float4 c1 = *reinterpret_cast<const float4*>(cs_s[t] + d + 2);
-                float4 r0, r1;
-                rope_rotate_cs(a0.x, a1.x, make_float2(c0.x, c0.y), r0.x, r1.x);
-                rope_rotate_cs(a0.y, a1.y, make_float2(c0.z, c0.w), r0.y, r1.y);
-                rope_rotate_cs(a0.z, a1.z, make_float2(c1.x, c1.y), r0.z, r1.z);
-                rope_rotate_cs(a0.w, a1.w, make_float2(c1.z, c1.w), r0.w, r1.w);
-                a0 = r0;
-                a1 = r1;
             }
-            const int64_t row = tk.row[t];
+            if (!live || !here[t]) continue;
+            if (sec != 2) {
+                const Quad c = quad(cos_s[t] + d), s = quad(sin_s[t] + d);
+                Quad r0, r1;
+                rotate2(x0.a, x1.a, c.a, s.a, r0.a, r1.a);
+                rotate2(x0.b, x1.b, c.b, s.b, r0.b, r1.b);
+                x0 = r0;
+                x1 = r1;
+            }
             if (sec == 0) {
-                float* q = p.q + (t0 + t) * p.q_stride + j;
-                *reinterpret_cast<float4*>(q) = a0;
-                *reinterpret_cast<float4*>(q + half) = a1;
-            } else if (row >= 0) {
-                void* kv = sec == 1 ? p.c.k : p.c.v;
-                kv_put4(kv, p.kv_f16, row + j, a0);
-                kv_put4(kv, p.kv_f16, row + j + half, a1);
+                *reinterpret_cast<ulonglong2*>(q + t * p.q_stride) = make_ulonglong2(x0.a, x0.b);
+                *reinterpret_cast<ulonglong2*>(q + t * p.q_stride + half) = make_ulonglong2(x1.a, x1.b);
+            } else if (rows[t] >= 0) {
+                kv_put4(kv, p.kv_f16, rows[t] + j, x0);
+                kv_put4(kv, p.kv_f16, rows[t] + j + half, x1);
                 if (sec == 1 && l == 0) track_slot(p, tk, t, h - p.nh);
             }
         }
@@ -204,12 +243,12 @@ __global__ void __launch_bounds__(kThreads) paged_store_kernel(const __grid_cons
 template <typename YT>
 __global__ void __launch_bounds__(kThreads) paged_store_any_kernel(const __grid_constant__ PagedStoreParams p,
                                                                    int heads_per_cta) {
-    __shared__ float2 cs_s[1][QKV_MAX_HEAD_DIM / 2];
+    __shared__ float cos_s[1][QKV_MAX_HEAD_DIM / 2], sin_s[1][QKV_MAX_HEAD_DIM / 2];
     __shared__ Tokens tk;
     qkv_ptx::griddep_wait();
     const int half = p.hd >> 1, t = blockIdx.x, lane = threadIdx.x & 31;
     const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
-    token_tables(p, t, 1, tk, cs_s);
+    token_tables(p, t, 1, tk, cos_s, sin_s);
     __syncthreads();
     if (tk.seq[0] < 0) return;
     const int64_t row = tk.row[0];
@@ -243,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) paged_store_any_kernel(const __grid_
                     z1 = __fmul_rn(__fmul_rn(z1, inv), __ldg(w + half + d));
                 }
                 float r0, r1;
-                rope_rotate_cs(z0, z1, cs_s[0][d], r0, r1);
+                rope_rotate_cs(z0, z1, make_float2(cos_s[0][d], sin_s[0][d]), r0, r1);
                 z0 = r0;
                 z1 = r1;
             }
@@ -272,7 +311,7 @@ cudaError_t launch_t(const PagedStoreParams& p, cudaStream_t stream) {
     while (lp < (vec ? p.hd / 8 : 32)) lp *= 2;
     // Tokens share a CTA (and what a head needs) once there are enough for every SM; before that the
     // heads of a token are spread over CTAs, down to one round each, at the price of more angles.
-    const bool many = vec && p.nt >= kMaxTokens * 4 * kSms;
+    const bool many = vec && p.nt >= 16 * kSms;
     const int heads = p.nh + 2 * p.nkv, tokens = many ? kMaxTokens : 1;
     int per = heads;
     while (!many && per > kThreads / lp && static_cast<int64_t>(p.nt) * ((heads + per - 1) / per) < kSms) per = (per + 1) / 2;
