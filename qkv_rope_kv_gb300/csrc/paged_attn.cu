@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "paged_common.cuh"
 #include "ptx_sync.cuh"
 
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 constexpr int kMinShare = 8;     // units
 constexpr int kItemCost = 8;     // units
 constexpr int kOwnFactor = 4;    // items get CTAs of their own while the grid has four for each
+constexpr int kCluster = 8;      // CTAs of a cluster
 constexpr int kJoinParts = 40;   // more parts than this are joined in two levels
 constexpr float kPShift = 12.f;  // weights are kept times 2^12
 constexpr float kLazy = 3.f;     // and may exceed that by 2^3 before the maximum moves
@@ -182,7 +185,7 @@ struct Split {
     static constexpr int kQuads = HD / 16;                 // a lane's outputs of one head, in fours
     static constexpr int kQRow = HD + (kF16 ? 8 : 16);     // floats; spreads the heads' rows over the banks
     static constexpr int kQLoads = kAttnHeads * HD / kThreads;
-    static constexpr bool kQRegs = kF16 || HD < 256;       // q's fragments stay in registers beside O
+    static constexpr bool kQRegs = HD < 256;               // q's fragments stay in registers beside O
     static constexpr bool kQAhead = HD < 256;              // the next item's q too
     static constexpr int kMergeFloats = (kWarps - 1) * kAttnHeads * HD;  // O of the warps but the first
     static constexpr int kPartFloats = kAttnHeads * (HD + 2);
@@ -229,6 +232,27 @@ __device__ __forceinline__ unsigned int atom_add_acq_rel(unsigned int* p, unsign
     unsigned int old;
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
     return old;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What CTA `rank` of the cluster has at the place of `p` in its shared memory.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 peer_float2(const float2* p, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_float4(const float4* p, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_addr(p, rank)) : "memory");
+    return v;
 }
 
 // Two values rounded to f16 in hi, and the remainders rounded to f16 in lo.
@@ -312,7 +336,9 @@ __device__ __forceinline__ float4 fma4(float4 o, float k, float4 a) {
     return make_float4(fmaf(o.x, k, a.x), fmaf(o.y, k, a.y), fmaf(o.z, k, a.z), fmaf(o.w, k, a.w));
 }
 
-template <typename KT, int HD>
+// CLUSTERED: clusters of kCluster CTAs, each with units of one item; the CTAs' parts are joined through
+// their shared memory.
+template <typename KT, int HD, bool CLUSTERED>
 __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     paged_attn_split_kernel(const __grid_constant__ PagedAttnParams p, int blocks_per_head) {
     using S = Split<KT, HD>;
@@ -365,16 +391,19 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     const int64_t n_items = static_cast<int64_t>(nonempty) * items;
     // Few items: CTAs of their own, ceil(units / share) each, which are no more than the grid.  A share is
     // at least kMinShare units (each part costs a join), but not above the longest item.
-    const bool own = n_items * kOwnFactor <= gridDim.x;
+    const bool own = CLUSTERED || n_items * kOwnFactor <= gridDim.x;
+    constexpr int kUnited = CLUSTERED ? kCluster : 1;  // CTAs that an item gets at least, and a multiple of
     const int cost = own ? 0 : kItemCost;
-    const int64_t ctas = own ? gridDim.x - n_items : gridDim.x;
+    const int64_t ctas = own ? gridDim.x - kUnited * n_items : gridDim.x;
     int64_t share = div_small(total + n_items * cost + ctas - 1, ctas);
     const int64_t least = min(longest, kMinShare) + cost;
     share = share < least ? least : share;
     // The order is counted in CTAs (own) or in units and item costs; this CTA starts at x.
     const int64_t x = own ? blockIdx.x : share * blockIdx.x;
     auto extent = [&](int units) -> int64_t {  // of one item
-        return units == 0 ? 0 : own ? (units + static_cast<int>(share) - 1) / static_cast<int>(share) : units + cost;
+        if (units == 0 || !own) return units == 0 ? 0 : units + cost;
+        const int n = (units + static_cast<int>(share) - 1) / static_cast<int>(share);
+        return (n + kUnited - 1) / kUnited * kUnited;
     };
     int64_t before = 0, start = 0;  // extent of the sequences before this round's; where x's sequence starts
     int b_at = -1;
@@ -414,14 +443,15 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     Walk at;     // the segment being computed: the CTA's units of one item, from at.u
     seq_units<UK>(p, b_at, false, at);
     int64_t end;      // where this CTA's share ends in the order
-    int c0 = 0, c1 = 0;  // first and last CTA of the item (own)
+    int c0 = 0, c1 = 0;  // first and last CTA (cluster) of the item (own)
+    const int me = blockIdx.x / kUnited;
     {
         const int64_t e = extent(at.units);
         at.item = static_cast<int>(div_small(x - start, e));
         const int64_t r = (x - start) - at.item * e;
         if (own) {  // chunk r of e: the order is the item's own units
-            c0 = static_cast<int>(blockIdx.x - r);
-            c1 = static_cast<int>(c0 + e - 1);
+            c0 = static_cast<int>(blockIdx.x - r) / kUnited;
+            c1 = c0 + static_cast<int>(e) / kUnited - 1;
             at.start = 0;
             const int n = static_cast<int>(e), each = at.units / n, left = at.units - each * n, i = static_cast<int>(r);
             at.u = i * each + min(i, left);
@@ -586,10 +616,26 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                         e = e == 128 ? 13 : max(-113, min(e, 126));
                         const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
                         unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+                        auto fragment = [&](int s, uint32_t* a) {  // of 16 columns
+                            const float2 v = *reinterpret_cast<const float2*>(qg + 16 * s + 2 * t);
+                            const float2 w = *reinterpret_cast<const float2*>(qg + 16 * s + 8 + 2 * t);
+                            split_f16(v.x * sc, v.y * sc, a[0], a[1]);
+                            split_f16(w.x * sc, w.y * sc, a[2], a[3]);
+                        };
+                        if constexpr (S::kQRegs) {
 #pragma unroll
-                        for (int s = 0; s < HD / 8; ++s) {
-                            const float2 v = *reinterpret_cast<const float2*>(qg + 8 * s + 2 * t);
-                            split_f16(v.x * sc, v.y * sc, qa[2 * s], qa[2 * s + 1]);
+                            for (int s = 0; s < HD / 16; ++s) fragment(s, qa + 4 * s);
+                        } else {  // the fragments take q's place; each warp makes a part of them
+                            constexpr int kPart = HD / 16 / S::kWarps;
+                            uint32_t a[4 * kPart];
+#pragma unroll
+                            for (int s = 0; s < kPart; ++s) fragment(warp * kPart + s, a + 4 * s);
+                            __syncthreads();
+#pragma unroll
+                            for (int s = 0; s < kPart; ++s)
+                                reinterpret_cast<uint4*>(q_s)[(warp * kPart + s) * 32 + lane] =
+                                    make_uint4(a[4 * s], a[4 * s + 1], a[4 * s + 2], a[4 * s + 3]);
+                            __syncthreads();
                         }
                     } else if constexpr (S::kQRegs) {
 #pragma unroll
@@ -630,8 +676,16 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                 for (int s = 0; s < HD / 16; ++s) {
                     uint32_t r[4];
                     ldm4(tile + swz<true, false>(key, 2 * s + half, S::kRowBytes), r);
-                    mma_f16(c[0], qa + 4 * s, r[0], r[1]);
-                    mma_f16(c[kST - 1], qa + 4 * s, r[2], r[3]);
+                    uint32_t* a = qa + (S::kQRegs ? 4 * s : 0);
+                    if constexpr (!S::kQRegs) {
+                        const uint4 v = reinterpret_cast<const uint4*>(q_s)[s * 32 + lane];
+                        a[0] = v.x;
+                        a[1] = v.y;
+                        a[2] = v.z;
+                        a[3] = v.w;
+                    }
+                    mma_f16(c[0], a, r[0], r[1]);
+                    mma_f16(c[kST - 1], a, r[2], r[3]);
                 }
             } else {
 #pragma unroll
@@ -777,7 +831,62 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                 for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(mo[i * 32], k, acc[i]);
             }
         }
-        if (us == 0 && ue == at.units) {
+        if constexpr (CLUSTERED) {
+            // Every CTA's sums to the place of its warps' O, in lane-linear quads; the first CTA reads them.
+            float4* mine = reinterpret_cast<float4*>(merge);
+            float2* ml = reinterpret_cast<float2*>(merge_m);
+            if (warp == 0) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < S::kQuads; ++i) mine[i * 32 + lane] = acc[i];
+                if (t == 0) ml[g] = make_float2(M, L);
+            }
+            cluster_sync();
+            if (blockIdx.x % kCluster == 0) {
+                constexpr int kMine = 2 * HD / S::kThreads;
+                float2 v[kCluster];
+                float4 sum[kMine];
+                float Mh = -CUDART_INF_F, Lh = 0.f;
+#pragma unroll
+                for (int r = 0; r < kCluster; ++r) {
+                    v[r] = peer_float2(ml + g, r);
+                    Mh = fmaxf(Mh, v[r].x);
+                }
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int r = 0; r < kCluster; ++r) {
+                    const float k = v[r].x == Mh ? 1.f : ex2(v[r].x - Mh);
+                    Lh = fmaf(v[r].y, k, Lh);
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) sum[i] = fma4(peer_float4(mine + i * S::kThreads + tid, r), k, sum[i]);
+                }
+                if (c0 == c1) {
+                    __syncthreads();  // the quads have been read: the rows take their place
+                    const float inv = 1.f / Lh;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) keep_out(i * S::kWarps + warp, sum[i], inv);
+                    if (warp == 0 && t == 0 && g < nheads) put_lse(p, at.b, h0 + g, Mh - kPShift, Lh, false);
+                    __syncthreads();
+                    if (warp == 0) put_rows(at.b, h0, nheads);
+                } else {
+                    const Pending e = {at.b, h0, nheads, c0, c1 - c0 + 1, 0u};
+                    float4* to = reinterpret_cast<float4*>(part(e, me));
+                    if (g < nheads) {
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) __stcg(to + i * S::kThreads + tid, sum[i]);
+                        if (warp == 0 && t == 0) __stcg(reinterpret_cast<float2*>(to + S::kQuads * 32) + g, make_float2(Mh, Lh));
+                    }
+                    __syncthreads();
+                    if (tid == 0) {  // counted as below; clusters are few enough for one group
+                        pending_s[0] = e;
+                        pending_s[0].counted = atom_add_acq_rel(p.counters + 2 * c0 + 1, 1u);
+                    }
+                    pendings = 1;
+                }
+            }
+            cluster_sync();  // no CTA leaves while its sums may be read
+        } else if (us == 0 && ue == at.units) {
             if (warp == 0) {
                 __syncwarp();  // the warps' O have been read: their place takes the rows
                 const float inv = 1.f / L;
@@ -797,7 +906,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
             }
             if (warp == 0) {
                 const Pending e = {at.b, h0, nheads, c0, c1 - c0 + 1, 0u};
-                float* to = part(e, blockIdx.x);
+                float* to = part(e, me);
                 if (g < nheads) {
 #pragma unroll
                     for (int i = 0; i < S::kQuads; ++i) __stcg(reinterpret_cast<float4*>(to) + i * 32 + lane, acc[i]);
@@ -805,7 +914,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    const int fan = join_fan(e.n), first = e.c0 + (blockIdx.x - e.c0) / fan * fan;
+                    const int fan = join_fan(e.n), first = e.c0 + (me - e.c0) / fan * fan;
                     pending_s[pendings] = e;
                     // release the part (the warp's writes come before, by its barrier)
                     pending_s[pendings].counted = atom_add_acq_rel(p.counters + 2 * first + (first == e.c0), 1u);
@@ -824,7 +933,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     for (int k = 0; k < pendings; ++k) {
         __syncthreads();  // pending_s is written; the ring and the last join's rows have been read
         const Pending e = pending_s[k];
-        const int fan = join_fan(e.n), groups = (e.n + fan - 1) / fan, group = (blockIdx.x - e.c0) / fan;
+        const int fan = join_fan(e.n), groups = (e.n + fan - 1) / fan, group = (me - e.c0) / fan;
         int first = e.c0 + group * fan, count = min(fan, e.n - group * fan), stride = 1;
         unsigned int* counter = p.counters + 2 * first + (first == e.c0);
         unsigned int counted = e.counted;
@@ -943,19 +1052,60 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
     }
 }
 
+template <typename KT, int HD, bool CLUSTERED>
+cudaError_t launch_split_t(const PagedAttnParams& p, int grid, int blocks_per_head, cudaStream_t stream) {
+    using S = Split<KT, HD>;
+    auto kernel = paged_attn_split_kernel<KT, HD, CLUSTERED>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(grid), S::kThreads, S::kSmem, stream, CLUSTERED ? kCluster : 1, p, blocks_per_head);
+}
+
+// How many clusters of the split kernel a device holds at a time (they need neighbouring SMs).  The same for
+// every context of a device, so it is asked for once.
+template <typename KT, int HD>
+cudaError_t resident_clusters(int* out) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    using S = Split<KT, HD>;
+    auto kernel = paged_attn_split_kernel<KT, HD, true>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (*out > kAttnMaxCtas / kCluster) *out = kAttnMaxCtas / kCluster;
+    if (dev < kMaxDevices) known[dev].store(*out, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
 template <typename KT, int HD>
 cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     using S = Split<KT, HD>;
-    auto kernel = paged_attn_split_kernel<KT, HD>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return e;
-    int dev = 0, sms = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    const int grid = sms * S::kCtas < kAttnMaxCtas ? sms * S::kCtas : kAttnMaxCtas;
     const int blocks_per_head = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
-    return launch_dependent(kernel, grid, S::kThreads, S::kSmem, stream, p, blocks_per_head);
+    // Clusters (as many as fit at a time) while every item can have two of them, and sequences can be
+    // longer than what one CTA does as fast: one 500-slot 7B sequence 9.6 us without, 7.6 us with clusters,
+    // 32000 slots 24.2 and 22.3 us, 16 slots 6.1 and 7.3 us.
+    int clusters = 0;
+    const cudaError_t e = resident_clusters<KT, HD>(&clusters);
+    if (e != cudaSuccess) return e;
+    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
+    if (cap >= 128 && static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks_per_head * 2 <= clusters)
+        return launch_split_t<KT, HD, true>(p, clusters * kCluster, blocks_per_head, stream);
+    return launch_split_t<KT, HD, false>(p, kSms * S::kCtas, blocks_per_head, stream);
 }
 
 }  // namespace
@@ -966,7 +1116,7 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream) {
                            static_cast<uintptr_t>(p.c.page_stride * es) | static_cast<uintptr_t>(p.hd * es);
     cudaError_t e;
     if ((bits & 15u) != 0) {  // rows that 16-byte copies cannot read
-        e = launch_dependent(paged_attn_any_kernel, p.c.n_seq * p.nh, kAnyThreads, 0, stream, p);
+        e = launch_dependent(paged_attn_any_kernel, dim3(p.c.n_seq * p.nh), kAnyThreads, 0, stream, 1, p);
     } else if (p.kv_f16) {
         e = p.hd <= 64 ? launch_split<uint16_t, 64>(p, stream)
                        : p.hd <= 128 ? launch_split<uint16_t, 128>(p, stream) : launch_split<uint16_t, 256>(p, stream);
@@ -980,7 +1130,7 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream) {
     const int64_t spans = (cap + kWeightThreads * kWeightSlots - 1) / (kWeightThreads * kWeightSlots);
     const int64_t most = 4096 / (static_cast<int64_t>(p.c.n_seq) * p.nkv) + 1;
     const int chunks = static_cast<int>(spans < most ? spans : most);
-    return launch_dependent(paged_attn_weight_kernel, p.c.n_seq * p.nkv * chunks, kWeightThreads, 0, stream, p, chunks);
+    return launch_dependent(paged_attn_weight_kernel, dim3(p.c.n_seq * p.nkv * chunks), kWeightThreads, 0, stream, 1, p, chunks);
 }
 
 cudaError_t paged_attn_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {

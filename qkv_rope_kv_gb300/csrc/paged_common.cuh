@@ -53,21 +53,26 @@ __device__ __forceinline__ int checked_len(const PagedView& c, const int32_t* le
     return n;
 }
 
-// Launch after the stream's previous kernel as a programmatic dependent: the blocks are set up while
-// that one drains, and wait for it (griddep_wait) before they read anything.
+constexpr int kSms = 152;  // of a GB300: grids are sized for them
+
+// Launch after the stream's previous kernel as a programmatic dependent (the blocks are set up while that
+// one drains, and wait for it, griddep_wait, before they read anything), in clusters of `cluster` CTAs.
 template <typename... Params, typename... Args>
-static inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                                           const Args&... args) {
+static inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                                           cudaStream_t stream, int cluster, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned int>(cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -17,7 +17,6 @@ namespace {
 using namespace qkv_paged;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kSms = 152;
 constexpr int kBins = 2048, kPasses = 3;               // digits of 11, 11 and 10 bits
 constexpr int kFixedSmem = (kPasses + 1) * kBins * 4;  // a histogram a digit and the cluster's sum of one
 constexpr int kMaxCluster = 16;
@@ -343,20 +342,7 @@ cudaError_t launch_select(const PagedEvictParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned int>(items) * size);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = size;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = size > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, size);
+    return launch_dependent(kernel, dim3(static_cast<unsigned int>(items) * size), kThreads, smem, stream, size, p, size);
 }
 
 template <typename CT>
@@ -368,7 +354,7 @@ cudaError_t launch_move(const PagedEvictParams& p, cudaStream_t stream) {
     int64_t chunks = (4 * kSms + items - 1) / items;
     if (chunks > (most + 15) / 16) chunks = (most + 15) / 16;
     return launch_dependent(paged_evict_move_kernel<CT>, dim3(static_cast<unsigned int>(items * chunks)), kMoveThreads, 0,
-                            stream, p, static_cast<int>(chunks));
+                            stream, 1, p, static_cast<int>(chunks));
 }
 
 }  // namespace

@@ -15,7 +15,6 @@ using namespace qkv_epi;
 using namespace qkv_paged;
 
 constexpr int kThreads = 256;
-constexpr int kSms = 152;
 constexpr int kMaxTokens = 3;  // tokens of one CTA: what fits 64 registers, so four CTAs on an SM
 
 // Four neighbouring values as two packed f32 pairs: one instruction works on both of a pair, with each
@@ -316,9 +315,9 @@ cudaError_t launch_t(const PagedStoreParams& p, cudaStream_t stream) {
     int per = heads;
     while (!many && per > kThreads / lp && static_cast<int64_t>(p.nt) * ((heads + per - 1) / per) < kSms) per = (per + 1) / 2;
     const dim3 grid((p.nt + tokens - 1) / tokens, (heads + per - 1) / per);
-    if (!vec) return launch_dependent(paged_store_any_kernel<YT>, grid, kThreads, 0, stream, p, per);
+    if (!vec) return launch_dependent(paged_store_any_kernel<YT>, grid, kThreads, 0, stream, 1, p, per);
     return launch_dependent(many ? paged_store_kernel<YT, kMaxTokens> : paged_store_kernel<YT, 1>, grid, kThreads, 0,
-                            stream, p, lp, per);
+                            stream, 1, p, lp, per);
 }
 
 }  // namespace
