@@ -63,6 +63,9 @@ qkv_status view(const qkv_plan* plan, const qkv_paged_kv* c, PagedView* v) {
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
+// Floats of a row of scores: whole units of slots, 16-byte aligned rows.
+int64_t score_stride(const qkv_paged_kv* c) { return (capacity(c) + 15) & ~static_cast<int64_t>(15); }
+
 // Byte offsets of the parts of qkv_attn_step's workspace.
 struct AttnLayout {
     size_t part, lse2, scores, total;
@@ -74,7 +77,7 @@ AttnLayout attn_layout(const qkv_plan* plan, const qkv_paged_kv* c, bool weights
     l.part = up256(3 * kAttnMaxCtas * sizeof(uint32_t));
     l.lse2 = l.part + up256(sizeof(float) * 2 * kAttnMaxCtas * kAttnHeads * (hd + 2));
     l.scores = l.lse2 + (weights ? up256(sizeof(float) * rows) : 0);
-    l.total = l.scores + (weights ? up256(sizeof(float) * rows * capacity(c)) : 0);
+    l.total = l.scores + (weights ? up256(sizeof(float) * rows * score_stride(c)) : 0);
     return l;
 }
 
@@ -181,6 +184,7 @@ extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* ca
     p.part = reinterpret_cast<float*>(ws + l.part);
     p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
+    p.score_stride = score_stride(cache);
     p.nh = plan->d.n_head;
     p.nkv = plan->d.n_head_kv;
     p.hd = plan->d.head_dim;

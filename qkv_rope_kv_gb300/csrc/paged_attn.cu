@@ -89,8 +89,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
     const int first = p.window > 0 ? max(0, n - p.window) : 0;
     for (int d = tid; d < p.hd; d += kAnyThreads)
         q_s[d] = p.q[b * p.q_stride + static_cast<int64_t>(h) * p.hd + d] * (p.scale * kLog2e);
-    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    float* scores = p.add_weight ? p.scores + (static_cast<int64_t>(b) * p.nh + h) * cap : nullptr;
+    float* scores = p.add_weight ? p.scores + (static_cast<int64_t>(b) * p.nh + h) * p.score_stride : nullptr;
     float m = -CUDART_INF_F, l = 0.f, acc[QKV_MAX_HEAD_DIM / kAnyThreads] = {};
     for (int j = first; j < n; j += kAnyTile) {
         const int nj = min(kAnyTile, n - j);
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 
 constexpr int kMinShare = 8;     // units
 constexpr int kItemCost = 8;     // units
-constexpr int kOwnFactor = 4;    // items get CTAs of their own while the grid has four for each
+constexpr int kOwnUnits = 8;     // how much larger the largest share may be with CTAs of its own for each item
 constexpr int kCluster = 8;      // CTAs of a cluster
 constexpr int kJoinParts = 40;   // more parts than this are joined in two levels
 constexpr float kPShift = 12.f;  // weights are kept times 2^12
@@ -389,15 +388,17 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
         }
     total *= items;
     const int64_t n_items = static_cast<int64_t>(nonempty) * items;
-    // Few items: CTAs of their own, ceil(units / share) each, which are no more than the grid.  A share is
-    // at least kMinShare units (each part costs a join), but not above the longest item.
-    const bool own = CLUSTERED || n_items * kOwnFactor <= gridDim.x;
+    // CTAs of their own for the items, ceil(units / share) each, which are no more than the grid; or equal
+    // shares of everything, whatever the items, where that makes the largest share clearly smaller.
+    // A share is at least kMinShare units (each part costs a join), but not above the longest item.
     constexpr int kUnited = CLUSTERED ? kCluster : 1;  // CTAs that an item gets at least, and a multiple of
+    const int64_t spare = static_cast<int64_t>(gridDim.x) - kUnited * n_items;
+    const int64_t least = min(longest, kMinShare);
+    const int64_t alone = spare > 0 ? min(max(div_small(total + spare - 1, spare), least), static_cast<int64_t>(longest)) : longest;
+    const int64_t dealt = max(div_small(total + n_items * kItemCost + gridDim.x - 1, gridDim.x), least + kItemCost);
+    const bool own = CLUSTERED || (spare >= 0 && alone <= dealt + kOwnUnits);
     const int cost = own ? 0 : kItemCost;
-    const int64_t ctas = own ? gridDim.x - kUnited * n_items : gridDim.x;
-    int64_t share = div_small(total + n_items * cost + ctas - 1, ctas);
-    const int64_t least = min(longest, kMinShare) + cost;
-    share = share < least ? least : share;
+    const int64_t share = own ? alone : dealt;
     // The order is counted in CTAs (own) or in units and item costs; this CTA starts at x.
     const int64_t x = own ? blockIdx.x : share * blockIdx.x;
     auto extent = [&](int units) -> int64_t {  // of one item
@@ -577,7 +578,6 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     auto part = [&](const Pending& e, int c) { return p.part + static_cast<int64_t>(2 * c + (c == e.c0)) * S::kPartFloats; };
     int pendings = 0;  // segments that are not whole items
 
-    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
     int get = 0;             // stage of the next unit to compute
     int u = at.u + warp;     // that unit
     // The copies run kStages - 1 units ahead and the questions to the table one more (after the first, most
@@ -719,16 +719,10 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                     sc[2 * j + i] = (live >> (8 * j + 2 * t + i)) & 1u ? v : -CUDART_INF_F;
                     mt = fmaxf(mt, sc[2 * j + i]);
                 }
-            if (p.add_weight && g < nheads) {
-                const int slot0 = (at.lo + u) * UK;
-                float* dst = p.scores + (static_cast<int64_t>(at.b) * p.nh + h0 + g) * cap + slot0;
+            if (p.add_weight && g < nheads) {  // whole units: the rows of scores are padded to them
+                float* dst = p.scores + (static_cast<int64_t>(at.b) * p.nh + h0 + g) * p.score_stride + (at.lo + u) * UK + 2 * t;
 #pragma unroll
-                for (int j = 0; j < kST; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = 8 * j + 2 * t + i;
-                        if (slot0 + k >= at.first && slot0 + k < at.n) dst[k] = sc[2 * j + i];
-                    }
+                for (int j = 0; j < kST; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(sc[2 * j], sc[2 * j + 1]);
             }
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
@@ -1018,9 +1012,10 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
 
 // ---------------------------------------------------------------- running attention weights
 
-constexpr int kWeightThreads = 128, kWeightSlots = 4;  // slots of a thread
+constexpr int kWeightThreads = 128, kWeightSpan = 4 * kWeightThreads;  // slots of a CTA
 
-// slot_weight[b][kv head][j] += sum over the kv head's q heads of 2^(score - lse).
+// slot_weight[b][kv head][j] += sum over the kv head's q heads of 2^(score - lse): four neighbouring slots a
+// thread, the rows of all heads in flight together.
 __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const __grid_constant__ PagedAttnParams p,
                                                                            int chunks) {
     griddep_wait();
@@ -1032,23 +1027,23 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
     const int first = p.window > 0 ? max(0, n - p.window) : 0;
     const int64_t h0 = static_cast<int64_t>(b) * p.nh + static_cast<int64_t>(hk) * G;
     float* weight = p.c.slot_weight + static_cast<int64_t>(item) * cap;
-    constexpr int kSpan = kWeightThreads * kWeightSlots;
-    for (int64_t j0 = first + static_cast<int64_t>(chunk) * kSpan + threadIdx.x; j0 < n;
-         j0 += static_cast<int64_t>(chunks) * kSpan) {
-        float w[kWeightSlots];
+    for (int64_t j = (first & ~3) + static_cast<int64_t>(chunk) * kWeightSpan + threadIdx.x * 4; j < n;
+         j += static_cast<int64_t>(chunks) * kWeightSpan) {
+        float old[4], w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < kWeightSlots; ++k) w[k] = 0.f;
+        for (int k = 0; k < 4; ++k) old[k] = j + k >= first && j + k < n ? weight[j + k] : 0.f;
 #pragma unroll 8
         for (int g = 0; g < G; ++g) {
             const float lse2 = __ldcg(p.lse2 + h0 + g);
-            const float* s = p.scores + (h0 + g) * cap + j0;
-#pragma unroll
-            for (int k = 0; k < kWeightSlots; ++k)
-                if (j0 + k * kWeightThreads < n) w[k] += exp2f(__ldcg(s + k * kWeightThreads) - lse2);
+            const float4 s = __ldcg(reinterpret_cast<const float4*>(p.scores + (h0 + g) * p.score_stride + j));
+            w[0] += ex2(s.x - lse2);
+            w[1] += ex2(s.y - lse2);
+            w[2] += ex2(s.z - lse2);
+            w[3] += ex2(s.w - lse2);
         }
 #pragma unroll
-        for (int k = 0; k < kWeightSlots; ++k)
-            if (j0 + k * kWeightThreads < n) weight[j0 + k * kWeightThreads] += w[k];
+        for (int k = 0; k < 4; ++k)
+            if (j + k >= first && j + k < n) weight[j + k] = old[k] + w[k];
     }
 }
 
@@ -1097,13 +1092,13 @@ cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     using S = Split<KT, HD>;
     const int blocks_per_head = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
     // Clusters (as many as fit at a time) while every item can have two of them, and sequences can be
-    // longer than what one CTA does as fast: one 500-slot 7B sequence 9.6 us without, 7.6 us with clusters,
-    // 32000 slots 24.2 and 22.3 us, 16 slots 6.1 and 7.3 us.
+    // longer than what one CTA does as fast (8 units): one 500-slot 7B sequence 9.6 us without, 7.6 us with
+    // clusters, 32000 slots 24.2 and 22.3 us, 16 slots 6.1 and 7.3 us.
     int clusters = 0;
     const cudaError_t e = resident_clusters<KT, HD>(&clusters);
     if (e != cudaSuccess) return e;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    if (cap >= 128 && static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks_per_head * 2 <= clusters)
+    if (cap >= 8 * S::UK && static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks_per_head * 2 <= clusters)
         return launch_split_t<KT, HD, true>(p, clusters * kCluster, blocks_per_head, stream);
     return launch_split_t<KT, HD, false>(p, kSms * S::kCtas, blocks_per_head, stream);
 }
@@ -1126,8 +1121,8 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream) {
     }
     if (e != cudaSuccess || !p.add_weight) return e;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    // up to two blocks for every resident one; longer sequences loop
-    const int64_t spans = (cap + kWeightThreads * kWeightSlots - 1) / (kWeightThreads * kWeightSlots);
+    // a span for each CTA, up to 4096 CTAs or so; longer sequences loop
+    const int64_t spans = (cap + kWeightSpan - 1) / kWeightSpan + 1;  // + 1: a window may begin inside one
     const int64_t most = 4096 / (static_cast<int64_t>(p.c.n_seq) * p.nkv) + 1;
     const int chunks = static_cast<int>(spans < most ? spans : most);
     return launch_dependent(paged_attn_weight_kernel, dim3(p.c.n_seq * p.nkv * chunks), kWeightThreads, 0, stream, 1, p, chunks);
