@@ -14,6 +14,7 @@
 namespace {
 
 using namespace qkv_paged;
+using qkv_ptx::griddep_launch_dependents;
 using qkv_ptx::griddep_wait;
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
     __shared__ int64_t row_s[kAnyTile];
     __shared__ float red_s[2 * kAnyThreads / 32];
     griddep_wait();
+    griddep_launch_dependents();
     const int b = blockIdx.x / p.nh, h = blockIdx.x - b * p.nh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int j0 = h / (p.nh / p.nkv) * p.hd;
@@ -359,6 +361,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
         for (int i = lane * 16; i < S::kRingBytes; i += 512) *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
 
     griddep_wait();
+    griddep_launch_dependents();  // what follows may take the places of CTAs that are done, and wait there
     // How much there is: units, sequences that have any, and the longest item.  Every warp finds it for
     // itself (32 lengths at a time), which takes fewer latencies than a barrier would.
     int units0 = 0;  // of sequence `lane`
@@ -1018,7 +1021,8 @@ constexpr int kWeightThreads = 128, kWeightSpan = 4 * kWeightThreads;  // slots 
 // thread, the rows of all heads in flight together.
 __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const __grid_constant__ PagedAttnParams p,
                                                                            int chunks) {
-    griddep_wait();
+    // Lengths and old weights do not come from the attention kernel, and what comes before that one was done
+    // when it began: they are read while it ends.
     const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
     const int b = item / p.nkv, hk = item - b * p.nkv, G = p.nh / p.nkv;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
@@ -1027,11 +1031,16 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
     const int first = p.window > 0 ? max(0, n - p.window) : 0;
     const int64_t h0 = static_cast<int64_t>(b) * p.nh + static_cast<int64_t>(hk) * G;
     float* weight = p.c.slot_weight + static_cast<int64_t>(item) * cap;
+    bool waited = false;
     for (int64_t j = (first & ~3) + static_cast<int64_t>(chunk) * kWeightSpan + threadIdx.x * 4; j < n;
          j += static_cast<int64_t>(chunks) * kWeightSpan) {
         float old[4], w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 4; ++k) old[k] = j + k >= first && j + k < n ? weight[j + k] : 0.f;
+        if (!waited) {
+            griddep_wait();
+            waited = true;
+        }
 #pragma unroll 8
         for (int g = 0; g < G; ++g) {
             const float lse2 = __ldcg(p.lse2 + h0 + g);
@@ -1045,6 +1054,8 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
         for (int k = 0; k < 4; ++k)
             if (j + k >= first && j + k < n) weight[j + k] = old[k] + w[k];
     }
+    if (!waited) griddep_wait();
+    griddep_launch_dependents();
 }
 
 template <typename KT, int HD, bool CLUSTERED>

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
     const int cap = p.c.max_pages * p.c.page_size;
     for (int i = tid; i < kPasses * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     qkv_ptx::griddep_wait();
+    qkv_ptx::griddep_launch_dependents();
     const int len = __ldg(p.lens + b);
     const int next_pos = __ldg(p.next_pos + b);
     const bool sane = len >= 0 && len <= cap;
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_evict_move_kernel(const __
     const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
     const int b = item / p.nkv, h = item - b * p.nkv, tid = threadIdx.x;
     qkv_ptx::griddep_wait();
+    qkv_ptx::griddep_launch_dependents();
     const int cap = p.c.max_pages * p.c.page_size;
     const int64_t base = static_cast<int64_t>(item) * cap;
     const int32_t* holes = p.lists + static_cast<int64_t>(item) * 2 * (cap / 2);

@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
     __shared__ __align__(16) float cos_s[T][QKV_MAX_HEAD_DIM / 2], sin_s[T][QKV_MAX_HEAD_DIM / 2];
     __shared__ Tokens tk;
     qkv_ptx::griddep_wait();
+    qkv_ptx::griddep_launch_dependents();
     const int half = p.hd >> 1;
     const int t0 = blockIdx.x * T, nt = min(T, p.nt - t0);
     const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(kThreads) paged_store_any_kernel(const __grid_
     __shared__ float cos_s[1][QKV_MAX_HEAD_DIM / 2], sin_s[1][QKV_MAX_HEAD_DIM / 2];
     __shared__ Tokens tk;
     qkv_ptx::griddep_wait();
+    qkv_ptx::griddep_launch_dependents();
     const int half = p.hd >> 1, t = blockIdx.x, lane = threadIdx.x & 31;
     const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
     token_tables(p, t, 1, tk, cos_s, sin_s);
