@@ -436,7 +436,7 @@ typedef struct qkv_paged_kv {
     int32_t n_pages;           /* >= 1 */
     int32_t page_size;         /* >= 1 */
     int32_t n_seq;             /* >= 1 */
-    int32_t max_pages;         /* >= 1; max_pages * page_size < 2^31 */
+    int32_t max_pages;         /* >= 1; max_pages * page_size at most 2^30 */
     int64_t page_stride;       /* elements from one page to the next, >= page_size * nkt; 0: that */
     float* slot_weight;        /* device, n_seq x nkv x capacity, or null: running attention weights */
     int32_t* slot_pos;         /* device, n_seq x nkv x capacity, or null: position held by each slot */
@@ -472,7 +472,8 @@ qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
  * A sequence of length 0 gets zeros (lse -inf).  Needs n_head % n_head_kv == 0.
  *   q       device, n_seq rows of nqt floats, q_stride >= nqt apart.
  *   d_lens  device, n_seq int32.  An out-of-range length counts as 0.
- *   out     device, n_seq rows of nqt values, out_dtype F32 or BF16 (rounded once), out_stride apart.
+ *   out     device, n_seq rows of nqt values, out_dtype F32 or BF16 (rounded once), out_stride apart;
+ *           must not overlap q.
  *   lse     device, n_seq x nh floats, or null.
  *   add_weight non-zero: slot_weight[b][kv head][j] += the sum over the kv head's q heads of
  *           softmax(s)_j, for the j above (the cache must have slot_weight).

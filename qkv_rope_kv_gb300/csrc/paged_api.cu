@@ -1,7 +1,6 @@
 // C-ABI layer of the paged-cache entry points: argument validation and workspace layout
 // (include/qkv.h has the contracts; the kernels are in paged_store.cu, paged_attn.cu and
 // paged_evict.cu).
-#include <climits>
 #include <cmath>
 #include <cstring>
 
@@ -22,6 +21,8 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 int64_t capacity(const qkv_paged_kv* c) { return static_cast<int64_t>(c->max_pages) * c->page_size; }
 
+constexpr int64_t kMaxCapacity = int64_t(1) << 30;  // slots and what kernels round up from them stay in 32 bits
+
 // Sizes only (what the workspace queries need).
 qkv_status check_shape(const qkv_plan* plan, const qkv_paged_kv* c) {
     REQUIRE(plan, "plan is null");
@@ -29,7 +30,7 @@ qkv_status check_shape(const qkv_plan* plan, const qkv_paged_kv* c) {
     REQUIRE(c->n_pages >= 1 && c->page_size >= 1 && c->n_seq >= 1 && c->max_pages >= 1,
             "n_pages, page_size, n_seq and max_pages must be >= 1 (got %d, %d, %d, %d)", c->n_pages, c->page_size,
             c->n_seq, c->max_pages);
-    REQUIRE(capacity(c) <= INT32_MAX, "max_pages * page_size must be below 2^31");
+    REQUIRE(capacity(c) <= kMaxCapacity, "max_pages * page_size must be at most 2^30");
     REQUIRE(static_cast<int64_t>(c->n_seq) * (plan->d.n_head + plan->d.n_head_kv) <= (int64_t(1) << 24),
             "n_seq * heads must be at most 2^24");
     const int64_t page = static_cast<int64_t>(c->page_size) * plan->nkt;
@@ -166,6 +167,10 @@ extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* ca
     REQUIRE(!add_weight || cache->slot_weight, "add_weight needs a cache with slot_weight");
     REQUIRE(aligned(q, 4) && aligned(d_lens, 4) && aligned(lse, 4) && aligned(out, out_dtype == QKV_F32 ? 4 : 2),
             "a pointer is not aligned to its elements");
+    const size_t rows = static_cast<size_t>(cache->n_seq);
+    REQUIRE(!overlap(q, ((rows - 1) * q_stride + plan->nqt) * 4, out,
+                     ((rows - 1) * out_stride + plan->nqt) * (out_dtype == QKV_F32 ? 4 : 2)),
+            "out must not overlap q");
     const AttnLayout l = attn_layout(plan, cache, add_weight != 0);
     REQUIRE(d_workspace && aligned(d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
     REQUIRE(workspace_bytes >= l.total, "the workspace has %zu bytes, %zu are needed", workspace_bytes, l.total);

@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Pending pending_s[2];
     __shared__ unsigned int last_s;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
     const int B = p.c.n_seq, G = p.nh / p.nkv, items = p.nkv * blocks_per_head;
     unsigned char* ring = smem + warp * S::kRingBytes;
     float* merge = reinterpret_cast<float*>(smem + S::kWarps * S::kRingBytes);

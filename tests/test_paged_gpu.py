@@ -244,6 +244,7 @@ def run_attn(nh, nkv, hd, kv, page, lens, window=0, out="f32", weights=False, se
     (10, 2, 96, "f32", 16, [150, 31], dict(weights=True)),
     (6, 3, 8, "f16", 4, [50, 3], {}),
     (6, 3, 24, "f32", 4, [50, 3], {}),
+    (2, 1, 4, "f32", 4, [50, 3], dict(weights=True)),
     (6, 3, 6, "f16", 4, [50, 3], dict(weights=True)),               # rows of no whole 16 bytes
     (5, 5, 2, "f32", 3, [130, 4], dict(weights=True, out="bf16")),
     (28, 4, 128, "f16", 16, [500, 70, 5], dict(window=64, weights=True)),
@@ -264,6 +265,8 @@ def run_attn(nh, nkv, hd, kv, page, lens, window=0, out="f32", weights=False, se
     (3, 1, 64, "f32", 64, [9000, 50], {}),
     (8, 1, 256, "f16", 64, [9000], {}),
     (2, 2, 64, "f16", 16, [12000] + [33] * 60, dict(weights=True)),  # one long among many short
+    (2, 1, 64, "f16", 16, [(7 * i) % 40 if i % 3 else 0 for i in range(1500)], dict(max_pages=3, weights=True)),
+    (2, 2, 64, "f32", 16, [0] * 700 + [300] + [0] * 40, {}),
 ], ids=short)
 def test_attn(qkv, nh, nkv, hd, kv, page, lens, kw):
     run_attn(nh, nkv, hd, kv, page, lens, **kw)
@@ -615,6 +618,80 @@ def test_serving_steps_together(qkv, kv, hd, captured):
                     assert np.array_equal(weight.cpu().numpy()[b, :, :rl[b]], rw[b, :, :rl[b]])
                     assert np.array_equal(spos.cpu().numpy()[b, :, :rl[b]], rp[b, :, :rl[b]])
         assert Q.qkv_check_device_error(stream)[0] == 0
+
+
+def test_two_streams_at_once(qkv):
+    """Calls on two streams, each with its own workspace, over one shared cache: the bits of calls one
+    after the other."""
+    import torch
+    rng = np.random.default_rng(14)
+    nh, nkv, hd = 28, 4, 128
+    c = ref.Cache(rng, 4, nkv, hd, "f16", 16, 130, lens=[2000, 5, 900, 64])
+    plan = make_plan(nh, nkv, hd, "f16")
+    cache, _, _ = gpu_cache(plan, c)
+    lens = dev(c.lens)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.zeros(Q.qkv_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    qs = [dev(rng.standard_normal((4, nh * hd)).astype(np.float32)) for _ in range(2)]
+    outs = [[torch.empty(4, nh * hd, device="cuda") for _ in range(20)] for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for k in range(2):
+            Q.qkv_attn_step(plan, cache, qs[k], lens, 0.09, outs[k][i], ws[k], stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        Q.qkv_attn_step(plan, cache, qs[k], lens, 0.09, outs[2][k], ws[k])
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, outs[2][k]) for o in outs[k])
+    assert not torch.equal(outs[2][0], outs[2][1])
+
+
+FIRST_CALLS = """
+import torch, qkv_rope_kv_gb300 as Q
+torch.manual_seed(0)
+nh, nkv, hd, page = 8, 2, 64, 16
+plan = Q.qkv_plan_create(64, nh, nkv, hd, 1e6, 64)
+k, v = torch.randn(8, page, nkv * hd, device="cuda").half(), torch.randn(8, page, nkv * hd, device="cuda").half()
+table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+w, p = torch.rand(2, nkv, 64, device="cuda"), torch.arange(64, dtype=torch.int32, device="cuda").expand(2, nkv, 64).contiguous()
+cache = Q.PagedKv(plan, k, v, table, slot_weight=w, slot_pos=p)
+ws = torch.zeros(Q.qkv_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+we = torch.zeros(Q.qkv_evict_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+Y = torch.randn(2, (nh + 2 * nkv) * hd, device="cuda")
+q, out = torch.zeros(2, nh * hd, device="cuda"), torch.zeros(2, nh * hd, device="cuda")
+lens, n2 = torch.tensor([50, 63], dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+wo, po = w.clone(), p.clone()
+state = [k, v, w, p, q, out, n2, wo, po]
+saved = [t.clone() for t in state]
+def step():
+    Q.qkv_paged_store_step(plan, cache, Y, None, None, None, 0.0, lens, None, None, q)
+    Q.qkv_attn_step(plan, cache, q, lens, 0.125, out, ws, add_weight=True)
+    Q.qkv_evict_step(plan, cache, lens, lens, 32, 4, n2, wo, po, we)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+for t, s in zip(state, saved): t.copy_(s)
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in state]
+for t, s in zip(state, saved): t.copy_(s)
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, state)) and out.abs().sum() > 0 and n2.tolist() == [32, 32]
+assert Q.qkv_check_device_error()[0] == 0
+print("captured first: ok")
+"""
+
+
+def test_first_calls_inside_a_capture(qkv):
+    """A process whose first calls are captured replays what eager calls do."""
+    import subprocess
+    import sys
+    import os
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured first: ok" in r.stdout, r.stderr[-2000:]
 
 
 def test_attention_reads_what_decode_steps_stored(qkv):

@@ -30,7 +30,7 @@ def cache(**kw):
 
 
 BAD_CACHES = [dict(k=None), dict(v=None), dict(page_table=None), dict(n_pages=0), dict(page_size=0), dict(n_seq=0),
-              dict(max_pages=0), dict(max_pages=1 << 28, page_size=8), dict(page_stride=16 * 128 - 1), dict(k=P + 1),
+              dict(max_pages=0), dict(max_pages=1 << 28, page_size=8), dict(max_pages=(1 << 30) + 1, page_size=1), dict(page_stride=16 * 128 - 1), dict(k=P + 1),
               dict(page_table=P + 2), dict(slot_pos=P + 1), dict(n_seq=1 << 23), dict(page_stride=-5)]
 
 
@@ -42,7 +42,7 @@ def store(lib, pl, c, **kw):
 
 
 def attn(lib, pl, c, **kw):
-    a = dict(q=P, q_stride=256, lens=P, scale=0.125, window=0, out=P, out_dtype=q.QKV_F32, out_stride=256, lse=None,
+    a = dict(q=P, q_stride=256, lens=P, scale=0.125, window=0, out=P << 7, out_dtype=q.QKV_F32, out_stride=256, lse=None,
              add=0, ws=P, ws_bytes=1 << 40)
     a.update(kw)
     return lib.qkv_attn_step(pl.handle if pl else None, ctypes.byref(c) if c else None, *a.values(), None)
@@ -77,8 +77,8 @@ def test_store_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), 1), (dict(lens=None), 1), (dict(out=None), 1), (dict(q_stride=255), 1), (dict(out_stride=1), 1),
     (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(window=-1), 1), (dict(ws=None), 1),
-    (dict(ws=P + 8), 1), (dict(ws_bytes=1024), 1), (dict(out_dtype=q.QKV_F16), 2), (dict(out=P + 2), 1),
-    (dict(lse=P + 2), 1),
+    (dict(ws=P + 8), 1), (dict(ws_bytes=1024), 1), (dict(out_dtype=q.QKV_F16), 2), (dict(out=(P << 7) + 2), 1),
+    (dict(lse=P + 2), 1), (dict(out=P), 1), (dict(out=P + 4 * (2 * 256 + 255)), 1), (dict(out=P - 4 * 767), 1),
 ], ids=str)
 def test_attn_refusals(lib, kw, status):
     assert attn(lib, plan(), cache(), **kw) == status
