@@ -758,3 +758,32 @@ def test_python_refusals(qkv):
         with pytest.raises(Q.QkvError):
             Q.qkv_evict_step(plan, cache, *a)
     assert Q.qkv_check_device_error()[0] == 0
+
+
+def test_readme_example_of_the_paged_cache(qkv):
+    """The README's paged example runs as printed: its last attention is that of the cache, and the
+    eviction leaves the newest positions and the largest weights."""
+    import os
+    import re
+
+    import torch
+    readme = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    code = re.findall(r"```python\n(.*?)```", open(readme).read(), re.S)[0]
+    before, evict = code.split("# Keep 32 slots")
+    env = {}
+    exec(compile(before, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    assert env["lens"].tolist() == [44, 28]
+    c = ref.Cache(np.random.default_rng(0), 2, 8, 128, "f16", 16, 4, lens=[0, 0])
+    c.k, c.v, c.table = env["pool_k"].cpu().numpy(), env["pool_v"].cpu().numpy(), env["table"].cpu().numpy()
+    want = ref.attn_ref(c, env["step_q"].cpu().numpy(), [44, 28], 128 ** -0.5, 0, 40)
+    close(env["attn"].cpu().numpy(), want[0], want[3], "README attention")
+    w, p = env["slot_weight"].cpu().numpy(), env["slot_pos"].cpu().numpy()
+    assert np.allclose(w[0].sum(1), 4 * 5, atol=1e-3) and (p[0, :, :44] == np.arange(44)).all()
+    exec(compile("# Keep 32 slots" + evict, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    rk, rv, rl, rw, rp = ref.evict_ref(c, [44, 28], [44, 28], w, p, 32, 8)
+    assert env["kept"].tolist() == list(rl) == [32, 28]
+    assert np.array_equal(env["pool_k"].cpu().numpy(), rk) and np.array_equal(env["pool_v"].cpu().numpy(), rv)
+    assert np.array_equal(env["slot_pos"].cpu().numpy()[0, :, :32], rp[0, :, :32])
+    assert np.array_equal(env["slot_weight"].cpu().numpy()[0, :, :32], rw[0, :, :32])
