@@ -450,17 +450,28 @@ def qkv_ffn_graph_create(hidden: int, n_ff: int, w_dtype: int, layers, stream) -
 
 # ---------------------------------------------------------------- paged cache
 
-def _tensor(t, name: str, dtype, shape: tuple, device: int, rows: bool = False):
-    """Check a tensor's device, type, shape and layout (contiguous, or only in its rows) and return its
-    address; None passes through."""
+def _refuse(t, name: str, dtype, shape: tuple, device: int, layout: str):
+    raise QkvError(QKV_ERR_INVALID_ARG, "%s must be %s of shape %s on cuda:%d, %s; got %s of %s (strides %s) on %s"
+                   % (name, dtype, shape, device, layout, t.dtype, tuple(t.shape), t.stride(), t.device))
+
+
+def _tensor(t, name: str, dtype, shape: tuple, device: int):
+    """Address of a contiguous tensor of this type, shape and device; None passes through."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be %s of shape %s on cuda:%d, got %s of %s on %s"
-                       % (name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
-    if not t.is_contiguous() and not (rows and t.stride(-1) == 1):
-        raise QkvError(QKV_ERR_INVALID_ARG, "%s must be contiguous%s" % (name, " in its rows" if rows else ""))
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device, "contiguous")
+
+
+def _rows(t, name: str, dtype, shape: tuple, device: int):
+    """Address and row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        if t.stride(1) == 1:
+            return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    _refuse(t, name, dtype, shape, device, "its rows contiguous")
 
 
 class PagedKv:
@@ -481,18 +492,20 @@ class PagedKv:
         kv = torch.float16 if d.kv_dtype == QKV_F16 else torch.float32
         dev = self.device = k.get_device()
         tracked = (n_seq, d.n_head_kv, max_pages * page_size)
+        pools = (n_pages, page_size, nkt)
         for name, t in (("k", k), ("v", v)):
-            _tensor(t, name, kv, (n_pages, page_size, nkt), dev, True)
-            if t.stride(1) != nkt and page_size > 1 or t.stride(0) != k.stride(0) and n_pages > 1:
-                raise QkvError(QKV_ERR_INVALID_ARG, "%s: rows of a page must be nkt elements apart, and the pages of "
-                               "k and v equally far" % name)
+            if t.dtype is not kv or t.shape != pools or t.get_device() != dev or t.stride(2) != 1 and nkt > 1 or \
+                    t.stride(1) != nkt and page_size > 1 or t.stride(0) != k.stride(0) and n_pages > 1:
+                _refuse(t, name, kv, pools, dev, "rows of a page nkt elements apart and the pages of k and v equally far")
         self.struct = qkv_paged_kv(
             k.data_ptr(), v.data_ptr(), _tensor(page_table, "page_table", torch.int32, (n_seq, max_pages), dev),
             n_pages, page_size, n_seq, max_pages, k.stride(0) if n_pages > 1 else 0,
             _tensor(slot_weight, "slot_weight", torch.float32, tracked, dev),
             _tensor(slot_pos, "slot_pos", torch.int32, tracked, dev))
         self.address = ctypes.addressof(self.struct)
-        self.plan, self.n_seq, self.tracked = plan, n_seq, tracked
+        self.plan, self.n_seq, self.per_seq, self.tracked = plan, n_seq, (n_seq,), tracked
+        self.types = torch.float32, torch.int32, torch.bfloat16
+        self._current_device, self._current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self._keep = (k, v, page_table, slot_weight, slot_pos)
 
     def _on(self, plan: Plan, stream):
@@ -502,21 +515,16 @@ class PagedKv:
             a, b = plan.desc, self.plan.desc
             if (a.n_head_kv, a.head_dim, a.kv_dtype) != (b.n_head_kv, b.head_dim, b.kv_dtype):
                 raise QkvError(QKV_ERR_INVALID_ARG, "the cache was laid out for another plan's kv heads or type")
-        import torch
-        if torch._C._cuda_getDevice() != self.device:
+        if self._current_device() != self.device:
             raise QkvError(QKV_ERR_INVALID_ARG, "the cache is on cuda:%d, the current device is cuda:%d: use "
-                           "torch.cuda.device()" % (self.device, torch._C._cuda_getDevice()))
-        return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else _stream(stream)
-
-
-def _row_stride(t, width: int) -> int:
-    return t.stride(0) if t.shape[0] > 1 else width
+                           "torch.cuda.device()" % (self.device, self._current_device()))
+        return self._current_stream(self.device) if stream is None else _stream(stream)
 
 
 def _workspace(t, device: int):
     if t is None:
         return None, 0
-    return _tensor(t, "workspace", t.dtype, t.shape, device), t.numel() * t.element_size()
+    return _tensor(t, "workspace", t.dtype, t.shape, device), t.nbytes
 
 
 def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps: float, positions, seqs, slots,
@@ -524,16 +532,18 @@ def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w
     """Finish the projections Y [nt, R] (f32 or bf16; rows may be strided) of tokens of any
     sequences: bias, optional q/k norms, rotation, q [nt, nqt] f32 out, k and v into the cache.
     ``bias``, the norm weights (together), ``seqs`` and ``slots`` may be None (see qkv.h)."""
-    import torch
-    nt, dev, i32, f32 = Y.shape[0], cache.device, torch.int32, torch.float32
-    bf16, head = Y.dtype is torch.bfloat16, (plan.head_dim,)
+    f32, i32, bf16 = cache.types
+    dev, y_type, head = cache.device, Y.dtype, (plan.head_dim,)
+    nt = Y.shape[0]
+    y, y_stride = _rows(Y, "Y", bf16 if y_type is bf16 else f32, (nt, plan.rows), dev)
+    to, to_stride = _rows(q, "q", f32, (nt, plan.nqt), dev)
+    nt_shape = (nt,)
     _check(_lib.qkv_paged_store_step(
-        plan.handle, cache.address, _tensor(Y, "Y", torch.bfloat16 if bf16 else f32, (nt, plan.rows), dev, True),
-        QKV_BF16 if bf16 else QKV_F32, _row_stride(Y, plan.rows), nt, _tensor(bias, "bias", f32, (plan.rows,), dev),
-        _tensor(q_norm_w, "q_norm_w", f32, head, dev), _tensor(k_norm_w, "k_norm_w", f32, head, dev), eps,
-        _tensor(positions, "positions", i32, (nt,), dev), _tensor(seqs, "seqs", i32, (nt,), dev),
-        _tensor(slots, "slots", i32, (nt,), dev), _tensor(q, "q", f32, (nt, plan.nqt), dev, True),
-        _row_stride(q, plan.nqt), cache._on(plan, stream)))
+        plan.handle, cache.address, y, QKV_BF16 if y_type is bf16 else QKV_F32, y_stride, nt,
+        _tensor(bias, "bias", f32, (plan.rows,), dev), _tensor(q_norm_w, "q_norm_w", f32, head, dev),
+        _tensor(k_norm_w, "k_norm_w", f32, head, dev), eps, _tensor(positions, "positions", i32, nt_shape, dev),
+        _tensor(seqs, "seqs", i32, nt_shape, dev), _tensor(slots, "slots", i32, nt_shape, dev), to, to_stride,
+        cache._on(plan, stream)))
 
 
 def qkv_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
@@ -547,15 +557,14 @@ def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, worksp
     """Attention of one new token per sequence: q [n_seq, nqt] f32 over the cached slots of each
     (``lens`` int32 [n_seq]) into out [n_seq, nqt] (f32 or bf16) and lse [n_seq, n_head] (f32).
     ``workspace``: zeroed device bytes, qkv_attn_workspace_bytes of them; it stays usable."""
-    import torch
-    B, dev, f32, shape = cache.n_seq, cache.device, torch.float32, (cache.n_seq, plan.nqt)
-    bf16 = out.dtype is torch.bfloat16
+    f32, i32, bf16 = cache.types
+    dev, out_type, shape = cache.device, out.dtype, (cache.n_seq, plan.nqt)
+    x, x_stride = _rows(q, "q", f32, shape, dev)
+    to, to_stride = _rows(out, "out", bf16 if out_type is bf16 else f32, shape, dev)
     _check(_lib.qkv_attn_step(
-        plan.handle, cache.address, _tensor(q, "q", f32, shape, dev, True), _row_stride(q, plan.nqt),
-        _tensor(lens, "lens", torch.int32, (B,), dev), scale, window,
-        _tensor(out, "out", torch.bfloat16 if bf16 else f32, shape, dev, True), QKV_BF16 if bf16 else QKV_F32,
-        _row_stride(out, plan.nqt), _tensor(lse, "lse", f32, (B, plan.n_head), dev), add_weight,
-        *_workspace(workspace, dev), cache._on(plan, stream)))
+        plan.handle, cache.address, x, x_stride, _tensor(lens, "lens", i32, cache.per_seq, dev), scale, window, to,
+        QKV_BF16 if out_type is bf16 else QKV_F32, to_stride, _tensor(lse, "lse", f32, (cache.n_seq, plan.n_head), dev),
+        add_weight, *_workspace(workspace, dev), cache._on(plan, stream)))
 
 
 def qkv_evict_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
@@ -568,13 +577,13 @@ def qkv_evict_step(plan: Plan, cache: PagedKv, lens, next_pos, budget: int, rece
                    workspace, stream=None):
     """Cut sequences longer than ``budget`` slots to it, per kv head, by slot_weight (and keep the
     ``recent`` newest positions); weight_out / pos_out may be the cache's own tensors."""
-    import torch
-    B, dev, i32 = (cache.n_seq,), cache.device, torch.int32
+    f32, i32, _ = cache.types
+    dev, B = cache.device, cache.per_seq
     _check(_lib.qkv_evict_step(
         plan.handle, cache.address, _tensor(lens, "lens", i32, B, dev), _tensor(next_pos, "next_pos", i32, B, dev),
         budget, recent, _tensor(lens_out, "lens_out", i32, B, dev),
-        _tensor(weight_out, "weight_out", torch.float32, cache.tracked, dev),
-        _tensor(pos_out, "pos_out", i32, cache.tracked, dev), *_workspace(workspace, dev), cache._on(plan, stream)))
+        _tensor(weight_out, "weight_out", f32, cache.tracked, dev), _tensor(pos_out, "pos_out", i32, cache.tracked, dev),
+        *_workspace(workspace, dev), cache._on(plan, stream)))
 
 
 # ---------------------------------------------------------------- device status
