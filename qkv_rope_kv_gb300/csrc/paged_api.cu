@@ -65,7 +65,7 @@ qkv_status view(const qkv_plan* plan, const qkv_paged_kv* c, PagedView* v) {
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Floats of a row of scores: whole units of slots, 16-byte aligned rows.
-int64_t score_stride(const qkv_paged_kv* c) { return (capacity(c) + 15) & ~static_cast<int64_t>(15); }
+int64_t score_stride(const qkv_paged_kv* c) { return (capacity(c) + 31) & ~static_cast<int64_t>(31); }
 
 // Byte offsets of the parts of qkv_attn_step's workspace.
 struct AttnLayout {

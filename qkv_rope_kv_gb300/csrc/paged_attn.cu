@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 
 // ---------------------------------------------------------------- split over the length, tensor cores
 
-// Work is counted in units of 16 (f16) or 8 (f32) neighbouring slots of one item, an item being
-// (sequence, kv head, block of up to 8 of its q heads).  Lengths are on the device, so every CTA finds
+// Work is counted in units of 8 to 32 neighbouring slots of one item (8 KB of K and V as a rule), an item
+// being (sequence, kv head, block of up to 8 of its q heads).  Lengths are on the device, so every CTA finds
 // its own work from them.  With many items, all units in a row are dealt to the CTAs in equal
 // contiguous shares (an item counts kItemCost units more, for its q and its end); with few, each item
 // gets CTAs of its own, so that no CTA has two beginnings and ends on its path.  The part of an item
@@ -177,7 +177,8 @@ struct Split {
     static constexpr bool kF16 = sizeof(KT) == 2;
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
     static constexpr int kCtas = HD == 256 ? 1 : 2;        // per SM
-    static constexpr int UK = kF16 ? 16 : 8;               // slots of a unit
+    // slots of a unit: 8 KB of K and V, or the fewest that an MMA takes
+    static constexpr int UK = kF16 ? (HD == 64 ? 32 : 16) : (HD == 64 ? 16 : 8);
     static constexpr int kRowBytes = HD * sizeof(KT);
     static constexpr int kTileBytes = UK * kRowBytes;      // K or V of a unit
     static constexpr int kStages = HD < 256 ? 24576 / (2 * kTileBytes) : kF16 ? 3 : 2;
@@ -678,8 +679,6 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                 const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
 #pragma unroll
                 for (int s = 0; s < HD / 16; ++s) {
-                    uint32_t r[4];
-                    ldm4(tile + swz<true, false>(key, 2 * s + half, S::kRowBytes), r);
                     uint32_t* a = qa + (S::kQRegs ? 4 * s : 0);
                     if constexpr (!S::kQRegs) {
                         const uint4 v = reinterpret_cast<const uint4*>(q_s)[s * 32 + lane];
@@ -688,17 +687,17 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                         a[2] = v.z;
                         a[3] = v.w;
                     }
-                    mma_f16(c[0], a, r[0], r[1]);
-                    mma_f16(c[kST - 1], a, r[2], r[3]);
+#pragma unroll
+                    for (int j = 0; j < kST; j += 2) {
+                        uint32_t r[4];
+                        ldm4(tile + swz<true, false>(8 * j + key, 2 * s + half, S::kRowBytes), r);
+                        mma_f16(c[j], a, r[0], r[1]);
+                        mma_f16(c[j + 1], a, r[2], r[3]);
+                    }
                 }
             } else {
 #pragma unroll
                 for (int s = 0; s < HD / 16; ++s) {
-                    float r[4];
-                    lds4(tile + swz<false, false>(g, 4 * s + t, S::kRowBytes), r);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) split_tf32_kv(r[i], hi[i], lo[i]);
                     uint32_t* a = qa + (S::kQRegs ? 8 * s : 0);
                     if constexpr (!S::kQRegs) {
                         const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
@@ -707,10 +706,18 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                         split_tf32(v.z, a[4], a[5]);
                         split_tf32(v.w, a[6], a[7]);
                     }
-                    mma_tf32(c[0], a, hi[0], hi[1]);
-                    mma_tf32(c[0], a + 4, hi[2], hi[3]);
-                    mma_tf32(c[0], a, lo[0], lo[1]);
-                    mma_tf32(c[0], a + 4, lo[2], lo[3]);
+#pragma unroll
+                    for (int j = 0; j < kST; ++j) {
+                        float r[4];
+                        lds4(tile + swz<false, false>(8 * j + g, 4 * s + t, S::kRowBytes), r);
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) split_tf32_kv(r[i], hi[i], lo[i]);
+                        mma_tf32(c[j], a, hi[0], hi[1]);
+                        mma_tf32(c[j], a + 4, hi[2], hi[3]);
+                        mma_tf32(c[j], a, lo[0], lo[1]);
+                        mma_tf32(c[j], a + 4, lo[2], lo[3]);
+                    }
                 }
             }
             float sc[2 * kST];
@@ -741,7 +748,6 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                     for (int i = 0; i < 4; ++i) O[n][i] *= keep;
             }
             const float base = (m == -CUDART_INF_F ? 0.f : m) - kPShift;
-            uint32_t pa[4];
             float pr[2 * kST];
 #pragma unroll
             for (int i = 0; i < 2 * kST; ++i) {
@@ -749,32 +755,40 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                 l += pr[i];
             }
             if constexpr (S::kF16) {
-                split_f16(pr[0], pr[1], pa[0], pa[1]);
-                split_f16(pr[2 * kST - 2], pr[2 * kST - 1], pa[2], pa[3]);
                 const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
 #pragma unroll
-                for (int s = 0; s < HD / 16; ++s) {
-                    uint32_t r[4];
-                    ldm4t(tile + S::kTileBytes + swz<true, true>(key, 2 * s + half, S::kRowBytes), r);
-                    mma_f16(O[2 * s], pa, r[0], r[1]);
-                    mma_f16(O[2 * s + 1], pa, r[2], r[3]);
+                for (int j = 0; j < kST; j += 2) {  // 16 slots
+                    uint32_t pa[4];
+                    split_f16(pr[2 * j], pr[2 * j + 1], pa[0], pa[1]);
+                    split_f16(pr[2 * j + 2], pr[2 * j + 3], pa[2], pa[3]);
+#pragma unroll
+                    for (int s = 0; s < HD / 16; ++s) {
+                        uint32_t r[4];
+                        ldm4t(tile + S::kTileBytes + swz<true, true>(8 * j + key, 2 * s + half, S::kRowBytes), r);
+                        mma_f16(O[2 * s], pa, r[0], r[1]);
+                        mma_f16(O[2 * s + 1], pa, r[2], r[3]);
+                    }
                 }
             } else {
-                split_tf32(pr[0], pa[0], pa[1]);
-                split_tf32(pr[1], pa[2], pa[3]);
 #pragma unroll
-                for (int s = 0; s < HD / 32; ++s) {
-                    // columns 4 (g + 8s) + i are column g of output tile 4s + i
-                    float r0[4], r1[4];
-                    lds4(tile + S::kTileBytes + swz<false, true>(2 * t, g + 8 * s, S::kRowBytes), r0);
-                    lds4(tile + S::kTileBytes + swz<false, true>(2 * t + 1, g + 8 * s, S::kRowBytes), r1);
+                for (int j = 0; j < kST; ++j) {  // 8 slots
+                    uint32_t pa[4];
+                    split_tf32(pr[2 * j], pa[0], pa[1]);
+                    split_tf32(pr[2 * j + 1], pa[2], pa[3]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t h0r, l0r, h1r, l1r;
-                        split_tf32_kv(r0[i], h0r, l0r);
-                        split_tf32_kv(r1[i], h1r, l1r);
-                        mma_tf32(O[4 * s + i], pa, h0r, h1r);
-                        mma_tf32(O[4 * s + i], pa, l0r, l1r);
+                    for (int s = 0; s < HD / 32; ++s) {
+                        // columns 4 (g + 8s) + i are column g of output tile 4s + i
+                        float r0[4], r1[4];
+                        lds4(tile + S::kTileBytes + swz<false, true>(8 * j + 2 * t, g + 8 * s, S::kRowBytes), r0);
+                        lds4(tile + S::kTileBytes + swz<false, true>(8 * j + 2 * t + 1, g + 8 * s, S::kRowBytes), r1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t h0r, l0r, h1r, l1r;
+                            split_tf32_kv(r0[i], h0r, l0r);
+                            split_tf32_kv(r1[i], h1r, l1r);
+                            mma_tf32(O[4 * s + i], pa, h0r, h1r);
+                            mma_tf32(O[4 * s + i], pa, l0r, l1r);
+                        }
                     }
                 }
             }

@@ -142,7 +142,7 @@ struct PagedAttnParams {
     float* part;             // [2 * kAttnMaxCtas][kAttnHeads][hd padded to 64, 128 or 256, + 2]
     float* lse2;             // [n_seq x nh], log2 domain (add_weight)
     float* scores;           // [n_seq x nh x score_stride], log2 domain (add_weight)
-    int64_t score_stride;    // the capacity, rounded up to 16
+    int64_t score_stride;    // the capacity, rounded up to whole units (32)
     int32_t nh, nkv, hd, kv_f16;
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
