@@ -447,22 +447,27 @@ typedef struct qkv_paged_kv {
  *   z * w / sqrt((1/hd) sum_i z_i^2 + eps) (as in qkv_decode_step_qknorm); q and k are rotated at
  *   d_positions[t]; q goes to row t of q, k and v to slot d_slots[t] of sequence d_seqs[t].
  * The same f32 operations as qkv_epilogue: without norms the outputs are the same bits.
- *   Y        device, nt rows q | k | v of R values, y_dtype F32 or BF16, y_stride >= R elements apart.
- *   bias     device, R floats, or null (no bias).
- *   q_norm_w, k_norm_w device, hd floats each, or both null (no norm; eps is then ignored).
- *   d_positions device, nt int32: any values.
- *   d_seqs   device, nt int32, or null: token t belongs to sequence t (nt <= n_seq).  A negative
- *            index marks padding: nothing of that token is written.
- *   d_slots  device, nt int32, or null: the slot is the position.
- *   q        device, nt rows of nqt floats, q_stride >= nqt apart; may be Y itself (F32, the same stride).
  * slot_pos, where the cache has it, receives the position for every kv head, slot_weight zero.
  * A token whose slot, sequence or page is out of range still gets its q row.  Two tokens of a
  * call must not name the same slot of the same sequence.  nt == 0 returns QKV_OK without a launch.
  * Errors: INVALID_ARG, UNSUPPORTED (y_dtype), CUDA. */
-qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache, const void* Y, int32_t y_dtype,
-                                int64_t y_stride, int32_t nt, const float* bias, const float* q_norm_w,
-                                const float* k_norm_w, float eps, const int32_t* d_positions,
-                                const int32_t* d_seqs, const int32_t* d_slots, float* q, int64_t q_stride,
+typedef struct qkv_paged_store_args {
+    const void* Y;              /* device, nt rows q | k | v of R values */
+    int64_t y_stride;           /* elements from row to row, >= R */
+    int32_t y_dtype;            /* QKV_F32 or QKV_BF16 */
+    int32_t nt;
+    const float* bias;          /* device, R floats, or null (no bias) */
+    const float* q_norm_w;      /* device, hd floats, and k_norm_w; or both null (no norm; eps is ignored) */
+    const float* k_norm_w;
+    const int32_t* d_positions; /* device, nt: any values */
+    const int32_t* d_seqs;      /* device, nt, or null: token t belongs to sequence t (nt <= n_seq).  A
+                                 * negative index marks padding: nothing of that token is written. */
+    const int32_t* d_slots;     /* device, nt, or null: the slot is the position */
+    float* q;                   /* device, nt rows of nqt floats; may be Y itself (F32, the same stride) */
+    int64_t q_stride;           /* >= nqt */
+    float eps;
+} qkv_paged_store_args;
+qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_paged_store_args* args,
                                 void* stream);
 
 /* Attention of one new token per sequence over its cached slots (the new token's own slot, stored
@@ -470,48 +475,55 @@ qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
  *   s_j = scale * sum_d q[b][h][d] K[j][d],  j in [max(0, len - window), len)  (window 0: all),
  *   out[b][h] = sum_j softmax(s)_j V[j],     lse[b][h] = log sum_j exp(s_j).
  * A sequence of length 0 gets zeros (lse -inf).  Needs n_head % n_head_kv == 0.
- *   q       device, n_seq rows of nqt floats, q_stride >= nqt apart.
- *   d_lens  device, n_seq int32.  An out-of-range length counts as 0.
- *   out     device, n_seq rows of nqt values, out_dtype F32 or BF16 (rounded once), out_stride apart;
- *           must not overlap q.
- *   lse     device, n_seq x nh floats, or null.
- *   add_weight non-zero: slot_weight[b][kv head][j] += the sum over the kv head's q heads of
- *           softmax(s)_j, for the j above (the cache must have slot_weight).
- * Scores, softmax and sums are f32.  A key's products are exact in the tensor cores' terms: q and the
- * softmax weights are split in two f16 (f16 cache) or tf32 (f32 cache) parts, an f32 cache's rows too.
+ * Scores, softmax and sums are f32.  q and the softmax weights are split in two f16 (f16 cache) or
+ * tf32 (f32 cache) parts for the tensor cores, an f32 cache's rows too: about 22 bits of each.
  * The length is split over the GPU and joined in the order of the slots: results do not depend on
- * timing.  d_workspace: device memory of qkv_attn_workspace_bytes bytes, 16-byte aligned, that must be
- * zero before the first call and belongs to calls that do not overlap on the GPU (one stream, or
- * graphs replayed one after the other); every completed call leaves it usable for the next, of any
- * shape that needs no more bytes.
+ * timing.  The workspace must be zero before the first call and belongs to calls that do not overlap
+ * on the GPU (one stream, or graphs replayed one after the other); every completed call leaves it
+ * usable for the next, of any shape that needs no more bytes.
  * Errors: INVALID_ARG, UNSUPPORTED (out_dtype, n_head % n_head_kv != 0), CUDA. */
+typedef struct qkv_attn_args {
+    const float* q;         /* device, n_seq rows of nqt floats */
+    int64_t q_stride;       /* elements from row to row, >= nqt */
+    const int32_t* d_lens;  /* device, n_seq; an out-of-range length counts as 0 */
+    void* out;              /* device, n_seq rows of nqt values of out_dtype; must not overlap q */
+    int64_t out_stride;     /* >= nqt */
+    float* lse;             /* device, n_seq x nh, or null */
+    void* d_workspace;      /* device, qkv_attn_workspace_bytes bytes, 16-byte aligned */
+    size_t workspace_bytes;
+    float scale;
+    int32_t window;         /* slots, 0: no window */
+    int32_t out_dtype;      /* QKV_F32 or QKV_BF16 (rounded once) */
+    int32_t add_weight;     /* non-zero: slot_weight[b][kv head][j] += the sum over the kv head's q heads of
+                             * softmax(s)_j, for the j above (the cache must have slot_weight) */
+} qkv_attn_args;
 qkv_status qkv_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out);
-qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const float* q, int64_t q_stride,
-                         const int32_t* d_lens, float scale, int32_t window, void* out, int32_t out_dtype,
-                         int64_t out_stride, float* lse, int32_t add_weight, void* d_workspace,
-                         size_t workspace_bytes, void* stream);
+qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_attn_args* args, void* stream);
 
 /* Cut every sequence longer than `budget` slots down to budget, per kv head: kept are the slots
  * whose position is >= d_next_pos[b] - recent, then those with the largest slot_weight (equal
  * weights: the lowest slot first; a NaN counts as larger than any number).  The i-th dropped slot
  * below budget takes what the i-th kept slot at or above it holds: its K and V row (of that head),
  * weight and position, so no kept row below budget moves and none moves twice.  Attention does not
- * depend on the order of the slots (but its window counts slots: do not combine the two).
- *   d_lens     device, n_seq int32; lens_out (n_seq int32, not overlapping d_lens) gets
- *              min(len, budget).  An out-of-range length is passed on as it is.
- *   d_next_pos device, n_seq int32: the position that the sequence's next token will have.
- *   weight_out, pos_out device, as slot_weight and slot_pos, and may be those: slots below
- *              min(len, budget) are written.  The cache must have both.
- *   budget >= 1, 0 <= recent <= budget.
- * Sequences must not share pages (a shared prefix would be changed under the others).  No order of
- * execution changes the result.  d_workspace: device memory of qkv_evict_workspace_bytes bytes, 4-byte
- * aligned, any contents, not shared by calls that overlap on the GPU.
+ * depend on the order of the slots (but its window counts slots: do not combine the two).  The cache
+ * must have slot_weight and slot_pos.  Sequences must not share pages (a shared prefix would be
+ * changed under the others).  No order of execution changes the result.
  * Errors: INVALID_ARG, CUDA. */
+typedef struct qkv_evict_args {
+    const int32_t* d_lens;      /* device, n_seq */
+    const int32_t* d_next_pos;  /* device, n_seq: the position that the sequence's next token will have */
+    int32_t* lens_out;          /* device, n_seq, overlapping neither: min(len, budget); an out-of-range
+                                 * length is passed on as it is */
+    float* weight_out;          /* device, as slot_weight and slot_pos, and may be those: slots below */
+    int32_t* pos_out;           /* min(len, budget) are written */
+    void* d_workspace;          /* device, qkv_evict_workspace_bytes bytes, 4-byte aligned, any contents,
+                                 * not shared by calls that overlap on the GPU */
+    size_t workspace_bytes;
+    int32_t budget;             /* >= 1 */
+    int32_t recent;             /* 0 .. budget */
+} qkv_evict_args;
 qkv_status qkv_evict_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out);
-qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* cache, const int32_t* d_lens,
-                          const int32_t* d_next_pos, int32_t budget, int32_t recent, int32_t* lens_out,
-                          float* weight_out, int32_t* pos_out, void* d_workspace, size_t workspace_bytes,
-                          void* stream);
+qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_evict_args* args, void* stream);
 
 /* ---- device status ---------------------------------------------------------- */
 

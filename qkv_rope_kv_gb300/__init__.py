@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -86,6 +87,12 @@ class qkv_paged_kv(ctypes.Structure):
                 ("slot_weight", ctypes.c_void_p), ("slot_pos", ctypes.c_void_p)]
 
 
+# qkv_paged_store_args, qkv_attn_args and qkv_evict_args, field by field: packing one and passing its
+# bytes costs a third of converting as many ctypes arguments.
+_STORE_ARGS = struct.Struct("@PqiiPPPPPPPqf4x")
+_ATTN_ARGS = struct.Struct("@PqPPqPPNfiii")
+_EVICT_ARGS = struct.Struct("@PPPPPPNii")
+
 _lock = threading.Lock()
 _lib = None
 
@@ -141,11 +148,12 @@ def _declare(lib):
         "qkv_decode_step_qknorm": ([vp, vp, vp, vp, vp, vp, ctypes.c_float] + [vp] * 8, st),
         "qkv_decode_step_qknorm_noalloc": ([vp, vp, vp, vp, vp, vp, ctypes.c_float] + [vp] * 7, st),
         "qkv_model_graph_create_qknorm": ([vp, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.POINTER(vp)], st),
-        "qkv_paged_store_step": ([vp, vp, vp, i32, i64, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, i64, vp], st),
+        # the args structs, packed into bytes (see _STORE_ARGS and the others)
+        "qkv_paged_store_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_attn_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
-        "qkv_attn_step": ([vp, vp, vp, i64, vp, ctypes.c_float, i32, vp, i32, i64, vp, i32, vp, sz, vp], st),
+        "qkv_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_evict_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
-        "qkv_evict_step": ([vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp], st),
+        "qkv_evict_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_model_graph_destroy": ([vp], None),
         "qkv_check_device_error": ([vp, ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(i32)], st),
         "qkv_test_decode_wait_timeout": ([vp] * 10 + [ctypes.c_uint32, vp], st),
@@ -456,9 +464,9 @@ def _refuse(t, name: str, dtype, shape: tuple, device: int, layout: str):
 
 
 def _tensor(t, name: str, dtype, shape: tuple, device: int):
-    """Address of a contiguous tensor of this type, shape and device; None passes through."""
+    """Address of a contiguous tensor of this type, shape and device; 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
     _refuse(t, name, dtype, shape, device, "contiguous")
@@ -523,7 +531,7 @@ class PagedKv:
 
 def _workspace(t, device: int):
     if t is None:
-        return None, 0
+        return 0, 0
     return _tensor(t, "workspace", t.dtype, t.shape, device), t.nbytes
 
 
@@ -538,12 +546,12 @@ def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w
     y, y_stride = _rows(Y, "Y", bf16 if y_type is bf16 else f32, (nt, plan.rows), dev)
     to, to_stride = _rows(q, "q", f32, (nt, plan.nqt), dev)
     nt_shape = (nt,)
-    _check(_lib.qkv_paged_store_step(
-        plan.handle, cache.address, y, QKV_BF16 if y_type is bf16 else QKV_F32, y_stride, nt,
-        _tensor(bias, "bias", f32, (plan.rows,), dev), _tensor(q_norm_w, "q_norm_w", f32, head, dev),
-        _tensor(k_norm_w, "k_norm_w", f32, head, dev), eps, _tensor(positions, "positions", i32, nt_shape, dev),
-        _tensor(seqs, "seqs", i32, nt_shape, dev), _tensor(slots, "slots", i32, nt_shape, dev), to, to_stride,
-        cache._on(plan, stream)))
+    args = _STORE_ARGS.pack(
+        y, y_stride, QKV_BF16 if y_type is bf16 else QKV_F32, nt, _tensor(bias, "bias", f32, (plan.rows,), dev),
+        _tensor(q_norm_w, "q_norm_w", f32, head, dev), _tensor(k_norm_w, "k_norm_w", f32, head, dev),
+        _tensor(positions, "positions", i32, nt_shape, dev), _tensor(seqs, "seqs", i32, nt_shape, dev),
+        _tensor(slots, "slots", i32, nt_shape, dev), to, to_stride, eps)
+    _check(_lib.qkv_paged_store_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 
 def qkv_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
@@ -561,10 +569,11 @@ def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, worksp
     dev, out_type, shape = cache.device, out.dtype, (cache.n_seq, plan.nqt)
     x, x_stride = _rows(q, "q", f32, shape, dev)
     to, to_stride = _rows(out, "out", bf16 if out_type is bf16 else f32, shape, dev)
-    _check(_lib.qkv_attn_step(
-        plan.handle, cache.address, x, x_stride, _tensor(lens, "lens", i32, cache.per_seq, dev), scale, window, to,
-        QKV_BF16 if out_type is bf16 else QKV_F32, to_stride, _tensor(lse, "lse", f32, (cache.n_seq, plan.n_head), dev),
-        add_weight, *_workspace(workspace, dev), cache._on(plan, stream)))
+    args = _ATTN_ARGS.pack(
+        x, x_stride, _tensor(lens, "lens", i32, cache.per_seq, dev), to, to_stride,
+        _tensor(lse, "lse", f32, (cache.n_seq, plan.n_head), dev), *_workspace(workspace, dev), scale, window,
+        QKV_BF16 if out_type is bf16 else QKV_F32, add_weight)
+    _check(_lib.qkv_attn_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 
 def qkv_evict_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
@@ -579,11 +588,11 @@ def qkv_evict_step(plan: Plan, cache: PagedKv, lens, next_pos, budget: int, rece
     ``recent`` newest positions); weight_out / pos_out may be the cache's own tensors."""
     f32, i32, _ = cache.types
     dev, B = cache.device, cache.per_seq
-    _check(_lib.qkv_evict_step(
-        plan.handle, cache.address, _tensor(lens, "lens", i32, B, dev), _tensor(next_pos, "next_pos", i32, B, dev),
-        budget, recent, _tensor(lens_out, "lens_out", i32, B, dev),
-        _tensor(weight_out, "weight_out", f32, cache.tracked, dev), _tensor(pos_out, "pos_out", i32, cache.tracked, dev),
-        *_workspace(workspace, dev), cache._on(plan, stream)))
+    args = _EVICT_ARGS.pack(
+        _tensor(lens, "lens", i32, B, dev), _tensor(next_pos, "next_pos", i32, B, dev),
+        _tensor(lens_out, "lens_out", i32, B, dev), _tensor(weight_out, "weight_out", f32, cache.tracked, dev),
+        _tensor(pos_out, "pos_out", i32, cache.tracked, dev), *_workspace(workspace, dev), budget, recent)
+    _check(_lib.qkv_evict_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 
 # ---------------------------------------------------------------- device status

@@ -89,51 +89,50 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 }  // namespace
 
-extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache, const void* Y,
-                                           int32_t y_dtype, int64_t y_stride, int32_t nt, const float* bias,
-                                           const float* q_norm_w, const float* k_norm_w, float eps,
-                                           const int32_t* d_positions, const int32_t* d_seqs, const int32_t* d_slots,
-                                           float* q, int64_t q_stride, void* stream) {
+extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
+                                           const qkv_paged_store_args* a, void* stream) {
     PagedStoreParams p;
     std::memset(&p, 0, sizeof p);
     qkv_status st = view(plan, cache, &p.c);
     if (st != QKV_OK) return st;
-    REQUIRE(nt >= 0, "nt must be >= 0");
-    if (y_dtype != QKV_F32 && y_dtype != QKV_BF16)
-        return api_fail(QKV_ERR_UNSUPPORTED, "y_dtype %d not supported (F32 or BF16)", y_dtype);
-    REQUIRE(nt == 0 || (Y && q && d_positions), "Y, q or d_positions is null");
-    REQUIRE(y_stride >= plan->rows, "y_stride must be >= R = %lld", static_cast<long long>(plan->rows));
-    REQUIRE(q_stride >= plan->nqt, "q_stride must be >= nqt = %lld", static_cast<long long>(plan->nqt));
-    REQUIRE((q_norm_w == nullptr) == (k_norm_w == nullptr), "q_norm_w and k_norm_w: both or neither");
-    if (q_norm_w) REQUIRE(eps >= 0.f && eps == eps, "eps must be a number >= 0");
-    REQUIRE(d_seqs || nt <= cache->n_seq, "without d_seqs, nt must be <= n_seq");
-    REQUIRE(aligned(Y, y_dtype == QKV_F32 ? 4 : 2) && aligned(q, 4) && aligned(bias, 4) && aligned(q_norm_w, 4) &&
-                aligned(k_norm_w, 4) && aligned(d_positions, 4) && aligned(d_seqs, 4) && aligned(d_slots, 4),
+    REQUIRE(a, "args is null");
+    REQUIRE(a->nt >= 0, "nt must be >= 0");
+    if (a->y_dtype != QKV_F32 && a->y_dtype != QKV_BF16)
+        return api_fail(QKV_ERR_UNSUPPORTED, "y_dtype %d not supported (F32 or BF16)", a->y_dtype);
+    REQUIRE(a->nt == 0 || (a->Y && a->q && a->d_positions), "Y, q or d_positions is null");
+    REQUIRE(a->y_stride >= plan->rows, "y_stride must be >= R = %lld", static_cast<long long>(plan->rows));
+    REQUIRE(a->q_stride >= plan->nqt, "q_stride must be >= nqt = %lld", static_cast<long long>(plan->nqt));
+    REQUIRE((a->q_norm_w == nullptr) == (a->k_norm_w == nullptr), "q_norm_w and k_norm_w: both or neither");
+    if (a->q_norm_w) REQUIRE(a->eps >= 0.f && a->eps == a->eps, "eps must be a number >= 0");
+    REQUIRE(a->d_seqs || a->nt <= cache->n_seq, "without d_seqs, nt must be <= n_seq");
+    const int ys = a->y_dtype == QKV_F32 ? 4 : 2;
+    REQUIRE(aligned(a->Y, ys) && aligned(a->q, 4) && aligned(a->bias, 4) && aligned(a->q_norm_w, 4) &&
+                aligned(a->k_norm_w, 4) && aligned(a->d_positions, 4) && aligned(a->d_seqs, 4) && aligned(a->d_slots, 4),
             "a pointer is not aligned to its elements");
-    const size_t ybytes = nt ? ((nt - 1) * static_cast<size_t>(y_stride) + plan->rows) * (y_dtype == QKV_F32 ? 4 : 2) : 0;
-    const size_t qbytes = nt ? ((nt - 1) * static_cast<size_t>(q_stride) + plan->nqt) * 4 : 0;
-    REQUIRE((Y == q && y_dtype == QKV_F32 && y_stride == q_stride) || !overlap(Y, ybytes, q, qbytes),
+    const size_t ybytes = a->nt ? ((a->nt - 1) * static_cast<size_t>(a->y_stride) + plan->rows) * ys : 0;
+    const size_t qbytes = a->nt ? ((a->nt - 1) * static_cast<size_t>(a->q_stride) + plan->nqt) * 4 : 0;
+    REQUIRE((a->Y == a->q && a->y_dtype == QKV_F32 && a->y_stride == a->q_stride) || !overlap(a->Y, ybytes, a->q, qbytes),
             "q must be Y itself (F32, the same stride) or not overlap it");
-    if (nt == 0) return QKV_OK;
-    p.y = Y;
-    p.y_stride = y_stride;
-    p.bias = bias;
-    p.norm_w[0] = q_norm_w;
-    p.norm_w[1] = k_norm_w;
-    p.eps = eps;
-    p.positions = d_positions;
-    p.seqs = d_seqs;
-    p.slots = d_slots;
-    p.q = q;
-    p.q_stride = q_stride;
-    p.nt = nt;
+    if (a->nt == 0) return QKV_OK;
+    p.y = a->Y;
+    p.y_stride = a->y_stride;
+    p.bias = a->bias;
+    p.norm_w[0] = a->q_norm_w;
+    p.norm_w[1] = a->k_norm_w;
+    p.eps = a->eps;
+    p.positions = a->d_positions;
+    p.seqs = a->d_seqs;
+    p.slots = a->d_slots;
+    p.q = a->q;
+    p.q_stride = a->q_stride;
+    p.nt = a->nt;
     p.nh = plan->d.n_head;
     p.nkv = plan->d.n_head_kv;
     p.hd = plan->d.head_dim;
     p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
     p.inv_hd = 1.f / static_cast<float>(p.hd);
     std::memcpy(p.inv_freq, plan->inv_freq, sizeof p.inv_freq);
-    const cudaError_t e = launch_paged_store(p, y_dtype, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_paged_store(p, a->y_dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged store kernel launch");
     return QKV_OK;
 }
@@ -146,45 +145,45 @@ extern "C" qkv_status qkv_attn_workspace_bytes(const qkv_plan* plan, const qkv_p
     return QKV_OK;
 }
 
-extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const float* q, int64_t q_stride,
-                                    const int32_t* d_lens, float scale, int32_t window, void* out, int32_t out_dtype,
-                                    int64_t out_stride, float* lse, int32_t add_weight, void* d_workspace,
-                                    size_t workspace_bytes, void* stream) {
+extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_attn_args* a,
+                                    void* stream) {
     PagedAttnParams p;
     std::memset(&p, 0, sizeof p);
     qkv_status st = view(plan, cache, &p.c);
     if (st != QKV_OK) return st;
+    REQUIRE(a, "args is null");
     if (plan->d.n_head % plan->d.n_head_kv != 0)
         return api_fail(QKV_ERR_UNSUPPORTED, "n_head %d is not a multiple of n_head_kv %d", plan->d.n_head,
                         plan->d.n_head_kv);
-    if (out_dtype != QKV_F32 && out_dtype != QKV_BF16)
-        return api_fail(QKV_ERR_UNSUPPORTED, "out_dtype %d not supported (F32 or BF16)", out_dtype);
-    REQUIRE(q && d_lens && out, "q, d_lens or out is null");
-    REQUIRE(q_stride >= plan->nqt && out_stride >= plan->nqt, "q_stride and out_stride must be >= nqt = %lld",
+    if (a->out_dtype != QKV_F32 && a->out_dtype != QKV_BF16)
+        return api_fail(QKV_ERR_UNSUPPORTED, "out_dtype %d not supported (F32 or BF16)", a->out_dtype);
+    REQUIRE(a->q && a->d_lens && a->out, "q, d_lens or out is null");
+    REQUIRE(a->q_stride >= plan->nqt && a->out_stride >= plan->nqt, "q_stride and out_stride must be >= nqt = %lld",
             static_cast<long long>(plan->nqt));
-    REQUIRE(std::isfinite(scale), "scale must be finite");
-    REQUIRE(window >= 0, "window must be >= 0");
-    REQUIRE(!add_weight || cache->slot_weight, "add_weight needs a cache with slot_weight");
-    REQUIRE(aligned(q, 4) && aligned(d_lens, 4) && aligned(lse, 4) && aligned(out, out_dtype == QKV_F32 ? 4 : 2),
+    REQUIRE(std::isfinite(a->scale), "scale must be finite");
+    REQUIRE(a->window >= 0, "window must be >= 0");
+    REQUIRE(!a->add_weight || cache->slot_weight, "add_weight needs a cache with slot_weight");
+    const int os = a->out_dtype == QKV_F32 ? 4 : 2;
+    REQUIRE(aligned(a->q, 4) && aligned(a->d_lens, 4) && aligned(a->lse, 4) && aligned(a->out, os),
             "a pointer is not aligned to its elements");
     const size_t rows = static_cast<size_t>(cache->n_seq);
-    REQUIRE(!overlap(q, ((rows - 1) * q_stride + plan->nqt) * 4, out,
-                     ((rows - 1) * out_stride + plan->nqt) * (out_dtype == QKV_F32 ? 4 : 2)),
+    REQUIRE(!overlap(a->q, ((rows - 1) * a->q_stride + plan->nqt) * 4, a->out,
+                     ((rows - 1) * a->out_stride + plan->nqt) * os),
             "out must not overlap q");
-    const AttnLayout l = attn_layout(plan, cache, add_weight != 0);
-    REQUIRE(d_workspace && aligned(d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
-    REQUIRE(workspace_bytes >= l.total, "the workspace has %zu bytes, %zu are needed", workspace_bytes, l.total);
-    char* ws = static_cast<char*>(d_workspace);
-    p.q = q;
-    p.q_stride = q_stride;
-    p.lens = d_lens;
-    p.scale = scale;
-    p.window = window;
-    p.out = out;
-    p.out_bf16 = out_dtype == QKV_BF16;
-    p.out_stride = out_stride;
-    p.lse = lse;
-    p.add_weight = add_weight != 0;
+    const AttnLayout l = attn_layout(plan, cache, a->add_weight != 0);
+    REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
+    REQUIRE(a->workspace_bytes >= l.total, "the workspace has %zu bytes, %zu are needed", a->workspace_bytes, l.total);
+    char* ws = static_cast<char*>(a->d_workspace);
+    p.q = a->q;
+    p.q_stride = a->q_stride;
+    p.lens = a->d_lens;
+    p.scale = a->scale;
+    p.window = a->window;
+    p.out = a->out;
+    p.out_bf16 = a->out_dtype == QKV_BF16;
+    p.out_stride = a->out_stride;
+    p.lse = a->lse;
+    p.add_weight = a->add_weight != 0;
     p.counters = reinterpret_cast<unsigned int*>(ws);
     p.part = reinterpret_cast<float*>(ws + l.part);
     p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
@@ -207,42 +206,41 @@ extern "C" qkv_status qkv_evict_workspace_bytes(const qkv_plan* plan, const qkv_
     return QKV_OK;
 }
 
-extern "C" qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* cache, const int32_t* d_lens,
-                                     const int32_t* d_next_pos, int32_t budget, int32_t recent, int32_t* lens_out,
-                                     float* weight_out, int32_t* pos_out, void* d_workspace, size_t workspace_bytes,
+extern "C" qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_evict_args* a,
                                      void* stream) {
     PagedEvictParams p;
     std::memset(&p, 0, sizeof p);
     qkv_status st = view(plan, cache, &p.c);
     if (st != QKV_OK) return st;
+    REQUIRE(a, "args is null");
     REQUIRE(cache->slot_weight && cache->slot_pos, "the cache must have slot_weight and slot_pos");
-    REQUIRE(d_lens && d_next_pos && lens_out && weight_out && pos_out, "null pointer");
-    REQUIRE(budget >= 1, "budget must be >= 1");
-    REQUIRE(recent >= 0 && recent <= budget, "recent must be in [0, budget]");
-    REQUIRE(aligned(d_lens, 4) && aligned(d_next_pos, 4) && aligned(lens_out, 4) && aligned(weight_out, 4) &&
-                aligned(pos_out, 4),
+    REQUIRE(a->d_lens && a->d_next_pos && a->lens_out && a->weight_out && a->pos_out, "null pointer");
+    REQUIRE(a->budget >= 1, "budget must be >= 1");
+    REQUIRE(a->recent >= 0 && a->recent <= a->budget, "recent must be in [0, budget]");
+    REQUIRE(aligned(a->d_lens, 4) && aligned(a->d_next_pos, 4) && aligned(a->lens_out, 4) && aligned(a->weight_out, 4) &&
+                aligned(a->pos_out, 4),
             "a pointer is not 4-byte aligned");
     const size_t nb = sizeof(int32_t) * cache->n_seq;
-    REQUIRE(!overlap(d_lens, nb, lens_out, nb) && !overlap(d_next_pos, nb, lens_out, nb),
+    REQUIRE(!overlap(a->d_lens, nb, a->lens_out, nb) && !overlap(a->d_next_pos, nb, a->lens_out, nb),
             "lens_out must not overlap d_lens or d_next_pos");
     const size_t sb = 4 * static_cast<size_t>(capacity(cache)) * cache->n_seq * plan->d.n_head_kv;
-    REQUIRE((weight_out == cache->slot_weight || !overlap(weight_out, sb, cache->slot_weight, sb)) &&
-                (pos_out == cache->slot_pos || !overlap(pos_out, sb, cache->slot_pos, sb)),
+    REQUIRE((a->weight_out == cache->slot_weight || !overlap(a->weight_out, sb, cache->slot_weight, sb)) &&
+                (a->pos_out == cache->slot_pos || !overlap(a->pos_out, sb, cache->slot_pos, sb)),
             "weight_out and pos_out must be slot_weight and slot_pos themselves or not overlap them");
     size_t need = 0;
     st = qkv_evict_workspace_bytes(plan, cache, &need);
     if (st != QKV_OK) return st;
-    REQUIRE(workspace_bytes >= need && d_workspace, "the workspace has %zu bytes, %zu are needed",
-            workspace_bytes, need);
-    REQUIRE(aligned(d_workspace, 4), "d_workspace must be 4-byte aligned");
-    p.lens = d_lens;
-    p.next_pos = d_next_pos;
-    p.budget = budget;
-    p.recent = recent;
-    p.lens_out = lens_out;
-    p.weight_out = weight_out;
-    p.pos_out = pos_out;
-    p.moves = static_cast<int32_t*>(d_workspace);
+    REQUIRE(a->workspace_bytes >= need && a->d_workspace, "the workspace has %zu bytes, %zu are needed",
+            a->workspace_bytes, need);
+    REQUIRE(aligned(a->d_workspace, 4), "d_workspace must be 4-byte aligned");
+    p.lens = a->d_lens;
+    p.next_pos = a->d_next_pos;
+    p.budget = a->budget;
+    p.recent = a->recent;
+    p.lens_out = a->lens_out;
+    p.weight_out = a->weight_out;
+    p.pos_out = a->pos_out;
+    p.moves = static_cast<int32_t*>(a->d_workspace);
     p.lists = p.moves + static_cast<size_t>(cache->n_seq) * plan->d.n_head_kv;
     p.nkv = plan->d.n_head_kv;
     p.hd = plan->d.head_dim;

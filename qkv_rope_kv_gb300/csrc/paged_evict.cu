@@ -6,9 +6,11 @@
 // have to: the i-th dropped slot below the budget takes the i-th kept slot above it.  Sources
 // (>= budget) and destinations (< budget) are disjoint, so the copies need no order.
 //
-// Two launches: one finds the moves (a cluster of CTAs per item, bound by its chain of barriers and
+// Two launches: one finds the moves (one or more CTAs per item, bound by their chain of barriers and
 // cluster exchanges), one makes them with the whole GPU (bound by the latency of list, table and
-// row, or by memory).
+// row, or by memory); a single one where items have little to move.
+#include <algorithm>
+
 #include "paged_common.cuh"
 #include "ptx_sync.cuh"
 
@@ -20,8 +22,10 @@ constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kPasses = 3;               // digits of 11, 11 and 10 bits
 constexpr int kFixedSmem = (kPasses + 1) * kBins * 4;  // a histogram a digit and the cluster's sum of one
 constexpr int kMaxCluster = 16;
+constexpr int64_t kOwnMoveBytes = 128 * 1024;
 constexpr int64_t kMaxSlots = 48 * 1024;               // slots of a CTA whose keys fit in shared memory
 constexpr int64_t kClusterSlots = 4096;                // slots of a CTA of a cluster
+static_assert(kFixedSmem >= kThreads * 16, "a batch of moves fits the histograms' place");
 
 // Order-preserving key of a slot: protected slots above everything, NaN above every number.
 __device__ __forceinline__ uint32_t slot_key(float w, int pos, int64_t protect_from) {
@@ -67,9 +71,69 @@ __device__ __forceinline__ void count_bin(uint32_t* hist, uint32_t bin, bool in)
     }
 }
 
+// Make an item's moves chunk, chunk + chunks, ... (which they are does not depend on how many there are, so the
+// list is read together with its length).  A thread looks up a move's rows and carries its weight and position;
+// then all threads copy the rows of K and V, CT by CT, kUnroll of them in flight.  to_s and from_s: THREADS
+// entries of shared memory.
+template <typename CT, int THREADS, int kUnroll>
+__device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, int chunk, int chunks, int64_t* to_s,
+                                           int64_t* from_s) {
+    const int b = item / p.nkv, h = item - b * p.nkv, tid = threadIdx.x;
+    const int cap = p.c.max_pages * p.c.page_size;
+    const int64_t base = static_cast<int64_t>(item) * cap;
+    const int32_t* holes = p.lists + static_cast<int64_t>(item) * 2 * (cap / 2);
+    const int32_t* movers = holes + cap / 2;
+    const int row_units = p.hd * (p.kv_f16 ? 2 : 4) / static_cast<int>(sizeof(CT));
+    const int elem_per_unit = static_cast<int>(sizeof(CT)) / (p.kv_f16 ? 2 : 4);
+    CT* kp = static_cast<CT*>(p.c.k);
+    CT* vp = static_cast<CT*>(p.c.v);
+#pragma unroll 1
+    for (int64_t p0 = chunk;; p0 += static_cast<int64_t>(THREADS) * chunks) {
+        const int64_t at = p0 + static_cast<int64_t>(tid) * chunks;
+        const bool could = at < cap / 2;
+        const int to = could ? __ldcg(holes + at) : 0, from = could ? __ldcg(movers + at) : 0;
+        const int pairs = __ldcg(p.moves + item);
+        if (p0 >= pairs) break;
+        const int n = static_cast<int>(min(static_cast<int64_t>(THREADS), (pairs - p0 + chunks - 1) / chunks));
+        if (tid < n) {
+            // everything the two slots name is asked for before any of it is looked at
+            const float w = p.c.slot_weight[base + from];
+            const int pos = p.c.slot_pos[base + from];
+            const PageRef rt = page_ref(p.c, b, to), rf = page_ref(p.c, b, from);
+            const int64_t ot = row_offset(p.c, rt), of = row_offset(p.c, rf);
+            to_s[tid] = ot >= 0 && of >= 0 ? (ot + h * p.hd) / elem_per_unit : -1;
+            from_s[tid] = (of + h * p.hd) / elem_per_unit;
+            p.weight_out[base + to] = w;
+            p.pos_out[base + to] = pos;
+        }
+        __syncthreads();
+        const int total = n * 2 * row_units;
+#pragma unroll 1
+        for (int e0 = tid; e0 < total; e0 += THREADS * kUnroll) {
+            CT v[kUnroll];
+            CT* dst[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int e = e0 + u * THREADS, i = e / (2 * row_units), c = e - i * 2 * row_units;
+                dst[u] = nullptr;
+                if (e < total && to_s[i] >= 0) {
+                    CT* pool = c < row_units ? kp + c : vp + (c - row_units);
+                    dst[u] = pool + to_s[i];
+                    v[u] = pool[from_s[i]];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (dst[u]) *dst[u] = v[u];
+        }
+        __syncthreads();
+    }
+}
+
 // A cluster of `size` CTAs per (sequence, kv head); each holds a contiguous run of the slots.  CACHED: their
-// keys are kept in shared memory; otherwise they are made again each time.
-template <bool CACHED>
+// keys are kept in shared memory; otherwise they are made again each time.  MOVES (one CTA per item, rows of
+// whole 16 bytes): it makes its moves too.
+template <bool CACHED, bool MOVES>
 __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p,
                                                                       int size) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -260,99 +324,32 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
             mover0 = __reduce_add_sync(0xffffffffu, (lane < rank ? nm : 0u) + (lane < warp ? warp2_s[lane] : 0u));
         }
     }
-    if (size > 1) cluster_sync(size);  // no CTA leaves while another may read its shared memory
+    if constexpr (MOVES) {
+        __syncthreads();  // the list is written, and the histograms have been read
+        int64_t* to_s = reinterpret_cast<int64_t*>(smem);
+        make_moves<uint4, kThreads, 4>(p, item, 0, 1, to_s, to_s + kThreads);
+    } else {
+        if (size > 1) cluster_sync(size);  // no CTA leaves while another may read its shared memory
+    }
 }
 
-// Make the moves: `chunks` CTAs per item share its list.  A thread looks up a move's rows and carries its
-// weight and position; then all threads copy the rows of K and V, CT by CT.
+// The moves, `chunks` CTAs per item.
 constexpr int kMoveThreads = 256;
 
 template <typename CT>
 __global__ void __launch_bounds__(kMoveThreads) paged_evict_move_kernel(const __grid_constant__ PagedEvictParams p,
                                                                         int chunks) {
     __shared__ int64_t to_s[kMoveThreads], from_s[kMoveThreads];
-    const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
-    const int b = item / p.nkv, h = item - b * p.nkv, tid = threadIdx.x;
     qkv_ptx::griddep_wait();
     qkv_ptx::griddep_launch_dependents();
-    const int cap = p.c.max_pages * p.c.page_size;
-    const int64_t base = static_cast<int64_t>(item) * cap;
-    const int32_t* holes = p.lists + static_cast<int64_t>(item) * 2 * (cap / 2);
-    const int32_t* movers = holes + cap / 2;
-    const int row_units = p.hd * (p.kv_f16 ? 2 : 4) / static_cast<int>(sizeof(CT));
-    const int elem_per_unit = static_cast<int>(sizeof(CT)) / (p.kv_f16 ? 2 : 4);
-    CT* kp = static_cast<CT*>(p.c.k);
-    CT* vp = static_cast<CT*>(p.c.v);
-    // This CTA's moves are chunk, chunk + chunks, ...: which they are does not depend on how many there are, so
-    // the list is read together with its length.
-#pragma unroll 1
-    for (int64_t p0 = chunk;; p0 += static_cast<int64_t>(kMoveThreads) * chunks) {
-        const int64_t at = p0 + static_cast<int64_t>(tid) * chunks;
-        const bool could = at < cap / 2;
-        const int to = could ? __ldg(holes + at) : 0, from = could ? __ldg(movers + at) : 0;
-        const int pairs = __ldg(p.moves + item);
-        if (p0 >= pairs) break;
-        const int n = static_cast<int>(min(static_cast<int64_t>(kMoveThreads), (pairs - p0 + chunks - 1) / chunks));
-        if (tid < n) {
-            // everything the two slots name is asked for before any of it is looked at
-            const float w = p.c.slot_weight[base + from];
-            const int pos = p.c.slot_pos[base + from];
-            const PageRef rt = page_ref(p.c, b, to), rf = page_ref(p.c, b, from);
-            const int64_t ot = row_offset(p.c, rt), of = row_offset(p.c, rf);
-            to_s[tid] = ot >= 0 && of >= 0 ? (ot + h * p.hd) / elem_per_unit : -1;
-            from_s[tid] = (of + h * p.hd) / elem_per_unit;
-            p.weight_out[base + to] = w;
-            p.pos_out[base + to] = pos;
-        }
-        __syncthreads();
-        const int total = n * 2 * row_units;
-        constexpr int kUnroll = 8;
-#pragma unroll 1
-        for (int e0 = tid; e0 < total; e0 += kMoveThreads * kUnroll) {
-            CT v[kUnroll];
-            CT* dst[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int e = e0 + u * kMoveThreads, i = e / (2 * row_units), c = e - i * 2 * row_units;
-                dst[u] = nullptr;
-                if (e < total && to_s[i] >= 0) {
-                    CT* pool = c < row_units ? kp + c : vp + (c - row_units);
-                    dst[u] = pool + to_s[i];
-                    v[u] = pool[from_s[i]];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (dst[u]) *dst[u] = v[u];
-        }
-        __syncthreads();
-    }
-}
-
-cudaError_t launch_select(const PagedEvictParams& p, cudaStream_t stream) {
-    // CTAs of a (sequence, kv head): one up to 2 kClusterSlots slots of capacity (the cluster's exchanges cost
-    // 3 us: 8.8 us alone, 11.7 us in twos at 4128 slots), then one for each kClusterSlots (32768 slots in
-    // clusters of 4, 8, 16: 18.1, 15.5, 17.4 us), while that leaves no more than two per SM
-    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    const int items = p.c.n_seq * p.nkv;
-    int size = cap > 2 * kClusterSlots ? 2 : 1;
-    while (size > 1 && size < kMaxCluster && cap > kClusterSlots * size && static_cast<int64_t>(items) * size < 2 * kSms) size *= 2;
-    const int64_t slots = (cap + static_cast<int64_t>(size) * kThreads - 1) / (static_cast<int64_t>(size) * kThreads) * kThreads;
-    const bool cached = slots <= kMaxSlots;
-    auto kernel = cached ? paged_evict_select_kernel<true> : paged_evict_select_kernel<false>;
-    const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(slots) * 4 : 0);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3(static_cast<unsigned int>(items) * size), kThreads, smem, stream, size, p, size);
+    const int item = blockIdx.x / chunks;
+    make_moves<CT, kMoveThreads, 8>(p, item, blockIdx.x - item * chunks, chunks, to_s, from_s);
 }
 
 template <typename CT>
-cudaError_t launch_move(const PagedEvictParams& p, cudaStream_t stream) {
+cudaError_t launch_move(const PagedEvictParams& p, int64_t most, cudaStream_t stream) {
     // enough CTAs for every SM to have four, but none for fewer than 16 of the moves there can be
-    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size, items = static_cast<int64_t>(p.c.n_seq) * p.nkv;
-    const int64_t most = p.budget < cap - p.budget ? p.budget : cap - p.budget;
-    if (most <= 0) return cudaSuccess;  // no sequence can exceed the budget
+    const int64_t items = static_cast<int64_t>(p.c.n_seq) * p.nkv;
     int64_t chunks = (4 * kSms + items - 1) / items;
     if (chunks > (most + 15) / 16) chunks = (most + 15) / 16;
     return launch_dependent(paged_evict_move_kernel<CT>, dim3(static_cast<unsigned int>(items * chunks)), kMoveThreads, 0,
@@ -362,13 +359,33 @@ cudaError_t launch_move(const PagedEvictParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
-    cudaError_t e = launch_select(p, stream);
-    if (e != cudaSuccess) return e;
-    const int es = p.kv_f16 ? 2 : 4;
+    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
+    const int items = p.c.n_seq * p.nkv, es = p.kv_f16 ? 2 : 4;
+    // CTAs of a (sequence, kv head): one up to 2 kClusterSlots slots of capacity (the cluster's exchanges cost
+    // 3 us: 8.8 us alone, 11.7 us in twos at 4128 slots), then one for each kClusterSlots (32768 slots in
+    // clusters of 4, 8, 16: 18.1, 15.5, 17.4 us), while that leaves no more than two per SM
+    int size = cap > 2 * kClusterSlots ? 2 : 1;
+    while (size > 1 && size < kMaxCluster && cap > kClusterSlots * size && static_cast<int64_t>(items) * size < 2 * kSms)
+        size *= 2;
+    const int64_t slots = (cap + static_cast<int64_t>(size) * kThreads - 1) / (static_cast<int64_t>(size) * kThreads) * kThreads;
+    const bool cached = slots <= kMaxSlots;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(p.c.k) | reinterpret_cast<uintptr_t>(p.c.v) |
                            static_cast<uintptr_t>(p.c.page_stride * es) | static_cast<uintptr_t>(p.hd * es);
-    if ((bits & 15u) == 0) return launch_move<uint4>(p, stream);
-    return p.kv_f16 ? launch_move<uint16_t>(p, stream) : launch_move<uint32_t>(p, stream);
+    const bool whole16 = (bits & 15u) == 0;
+    // One launch where no item can have more than kOwnMoveBytes to move (its CTA then takes about as long as
+    // a second launch would), or no item has anything to move.
+    const int64_t most = std::max<int64_t>(0, std::min<int64_t>(p.budget, cap - p.budget));
+    const bool moves = size == 1 && cached && whole16 && most * 2 * p.hd * es <= kOwnMoveBytes;
+    auto kernel = moves ? paged_evict_select_kernel<true, true>
+                        : cached ? paged_evict_select_kernel<true, false> : paged_evict_select_kernel<false, false>;
+    const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(slots) * 4 : 0);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        e = launch_dependent(kernel, dim3(static_cast<unsigned int>(items) * size), kThreads, smem, stream, size, p, size);
+    if (e != cudaSuccess || moves || most == 0) return e;
+    if (whole16) return launch_move<uint4>(p, most, stream);
+    return p.kv_f16 ? launch_move<uint16_t>(p, most, stream) : launch_move<uint32_t>(p, most, stream);
 }
 
 cudaError_t paged_evict_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {

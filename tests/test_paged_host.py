@@ -34,24 +34,59 @@ BAD_CACHES = [dict(k=None), dict(v=None), dict(page_table=None), dict(n_pages=0)
               dict(page_table=P + 2), dict(slot_pos=P + 1), dict(n_seq=1 << 23), dict(page_stride=-5)]
 
 
+def _call(fn, pl, c, layout, values):
+    """The entry point on an args struct (None among the values: a null pointer)."""
+    args = layout.pack(*[0 if v is None else v for v in values])
+    return fn(pl.handle if pl else None, ctypes.byref(c) if c else None, args, None)
+
+
 def store(lib, pl, c, **kw):
-    a = dict(Y=P << 4, y_dtype=q.QKV_F32, y_stride=512, nt=3, bias=P, qw=P, kw=P, eps=1e-6, pos=P, seqs=P, slots=P,
-             q=P << 5, q_stride=256)
-    a.update(kw)
-    return lib.qkv_paged_store_step(pl.handle if pl else None, ctypes.byref(c) if c else None, *a.values(), None)
+    a = dict(Y=P << 4, y_stride=512, y_dtype=q.QKV_F32, nt=3, bias=P, qw=P, kw=P, pos=P, seqs=P, slots=P, q=P << 5,
+             q_stride=256, eps=1e-6)
+    return _call(lib.qkv_paged_store_step, pl, c, q._STORE_ARGS, {**a, **kw}.values())
 
 
 def attn(lib, pl, c, **kw):
-    a = dict(q=P, q_stride=256, lens=P, scale=0.125, window=0, out=P << 7, out_dtype=q.QKV_F32, out_stride=256, lse=None,
-             add=0, ws=P, ws_bytes=1 << 40)
-    a.update(kw)
-    return lib.qkv_attn_step(pl.handle if pl else None, ctypes.byref(c) if c else None, *a.values(), None)
+    a = dict(q=P, q_stride=256, lens=P, out=P << 7, out_stride=256, lse=None, ws=P, ws_bytes=1 << 40, scale=0.125,
+             window=0, out_dtype=q.QKV_F32, add=0)
+    return _call(lib.qkv_attn_step, pl, c, q._ATTN_ARGS, {**a, **kw}.values())
 
 
 def evict(lib, pl, c, **kw):
-    a = dict(lens=P, next=P, budget=8, recent=2, lens_out=P << 6, w=P << 12, pos=P << 13, ws=P, ws_bytes=1 << 40)
-    a.update(kw)
-    return lib.qkv_evict_step(pl.handle if pl else None, ctypes.byref(c) if c else None, *a.values(), None)
+    a = dict(lens=P, next=P, lens_out=P << 6, w=P << 12, pos=P << 13, ws=P, ws_bytes=1 << 40, budget=8, recent=2)
+    return _call(lib.qkv_evict_step, pl, c, q._EVICT_ARGS, {**a, **kw}.values())
+
+
+def test_null_args_are_refused(lib):
+    for fn in (lib.qkv_paged_store_step, lib.qkv_attn_step, lib.qkv_evict_step):
+        assert fn(plan().handle, ctypes.byref(cache()), None, None) == q.QKV_ERR_INVALID_ARG
+
+
+def test_args_layouts_match_the_header(tmp_path):
+    """The packed layouts have the sizes and field offsets that a C compiler gives the header's structs."""
+    import os
+    import subprocess
+    fields = {"qkv_paged_store_args": ("Y y_stride y_dtype nt bias q_norm_w k_norm_w d_positions d_seqs d_slots q "
+                                       "q_stride eps", q._STORE_ARGS),
+              "qkv_attn_args": ("q q_stride d_lens out out_stride lse d_workspace workspace_bytes scale window "
+                                "out_dtype add_weight", q._ATTN_ARGS),
+              "qkv_evict_args": ("d_lens d_next_pos lens_out weight_out pos_out d_workspace workspace_bytes budget "
+                                 "recent", q._EVICT_ARGS)}
+    lines = ['printf("%s %%zu", sizeof(%s));%s puts("");' % (n, n, "".join(
+        'printf(" %%zu", offsetof(%s, %s));' % (n, f) for f in fs.split())) for n, (fs, _) in fields.items()]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include "qkv.h"\nint main(void) {%s return 0; }\n' % "".join(lines))
+    exe = str(tmp_path / "layout")
+    subprocess.check_call(["gcc", "-I", os.path.dirname(q.HEADER), "-o", exe, str(src)])
+    for line in subprocess.check_output([exe], text=True).splitlines():
+        name, size, *offsets = line.split()
+        names, layout = fields[name]
+        assert layout.size == int(size)
+        for i in range(len(offsets)):  # each field alone non-zero shows where it is packed
+            values = [0] * len(offsets)
+            values[i] = 1
+            data = layout.pack(*values)
+            assert min(k for k, byte in enumerate(data) if byte) - int(offsets[i]) in (0, 2), (name, names.split()[i])
 
 
 @pytest.mark.parametrize("bad", BAD_CACHES, ids=str)
