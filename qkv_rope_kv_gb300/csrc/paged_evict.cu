@@ -23,8 +23,10 @@ constexpr int kBins = 2048, kPasses = 3;               // digits of 11, 11 and 1
 constexpr int kFixedSmem = (kPasses + 1) * kBins * 4;  // a histogram a digit and the cluster's sum of one
 constexpr int kMaxCluster = 16;
 constexpr int64_t kOwnMoveBytes = 128 * 1024;
+constexpr uint32_t kCountEverywhere = 4096;            // keys left from which on a digit needs no exchange (24.9 -> 24.1 us)
 constexpr int64_t kMaxSlots = 48 * 1024;               // slots of a CTA whose keys fit in shared memory
 constexpr int64_t kClusterSlots = 4096;                // slots of a CTA of a cluster
+static_assert(2 * kClusterSlots <= kMaxSlots, "a CTA that is alone holds its keys");
 static_assert(kFixedSmem >= kThreads * 16, "a batch of moves fits the histograms' place");
 
 // Order-preserving key of a slot: protected slots above everything, NaN above every number.
@@ -39,6 +41,7 @@ __device__ __forceinline__ void cluster_sync(int size) {
     if (size == 1) {
         __syncthreads();
     } else {
+        __syncwarp();
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 }
@@ -57,17 +60,27 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, int rank, int s
     return v;
 }
 
-// Count one key's bin: one atomic for the whole warp where its lanes agree (equal weights would
+// Add to a counter of the first `to` CTAs of the cluster (1: this CTA's own).
+__device__ __forceinline__ void add_count(uint32_t* counter, uint32_t n, int to) {
+    if (to == 1) {
+        atomicAdd(counter, n);
+        return;
+    }
+    for (int r = 0; r < to; ++r)
+        asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(peer_address(counter, r)), "r"(n) : "memory");
+}
+
+// Count one key's bin: one addition for the whole warp where its lanes agree (equal weights would
 // otherwise serialise on one address).
-__device__ __forceinline__ void count_bin(uint32_t* hist, uint32_t bin, bool in) {
+__device__ __forceinline__ void count_bin(uint32_t* hist, uint32_t bin, bool in, int to) {
     const unsigned int active = __ballot_sync(0xffffffffu, in);
     if (active == 0u) return;
     const int leader = __ffs(active) - 1;
     const uint32_t first = __shfl_sync(0xffffffffu, bin, leader);
     if (__all_sync(0xffffffffu, !in || bin == first)) {
-        if (static_cast<int>(threadIdx.x & 31) == leader) atomicAdd(hist + first, static_cast<uint32_t>(__popc(active)));
+        if (static_cast<int>(threadIdx.x & 31) == leader) add_count(hist + first, static_cast<uint32_t>(__popc(active)), to);
     } else if (in) {
-        atomicAdd(hist + bin, 1u);
+        add_count(hist + bin, 1u, to);
     }
 }
 
@@ -131,11 +144,14 @@ __device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, 
 }
 
 // A cluster of `size` CTAs per (sequence, kv head); each holds a contiguous run of the slots.  CACHED: their
-// keys are kept in shared memory; otherwise they are made again each time.  MOVES (one CTA per item, rows of
-// whole 16 bytes): it makes its moves too.
-template <bool CACHED, bool MOVES>
+// keys are kept in shared memory; otherwise they are made again each time.  ALONE: a cluster is one CTA
+// (11.0 us; 11.8 us where the kernel has to ask).  MOVES (alone, rows of whole 16 bytes): it makes its
+// moves too.
+template <bool CACHED, bool MOVES, bool ALONE>
 __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p,
-                                                                      int size) {
+                                                                      int cluster) {
+    static_assert(ALONE || !MOVES, "a cluster's moves are made by the second kernel");
+    const int size = ALONE ? 1 : cluster;
     extern __shared__ __align__(16) unsigned char smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
     uint32_t* sum = hist + kPasses * kBins;
@@ -197,15 +213,20 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
         const int above = shift;
         shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         uint32_t* my_hist = hist + pass * kBins;
+        // few keys are left: each is counted in every CTA at once, and no exchange of sums has to follow
+        const bool everywhere = size > 1 && pass > 0 && in_bin <= kCountEverywhere;
 #pragma unroll 4
         for (int i = lane; i < run; i += 32) {
             const bool there = i < mine;
             const uint32_t k = there ? key_of(i) : 0u;
-            count_bin(my_hist, (k >> shift) & (pass == 2 ? 1023u : 2047u), there && (pass == 0 || k >> above == low >> above));
+            count_bin(my_hist, (k >> shift) & (pass == 2 ? 1023u : 2047u), there && (pass == 0 || k >> above == low >> above),
+                      everywhere ? size : 1);
         }
         const uint32_t* bins = my_hist;
         if (size == 1) {
             __syncthreads();
+        } else if (everywhere) {
+            cluster_sync(size);
         } else {
             // each CTA adds up its share of the bins over the cluster and hands the sums to every CTA
             cluster_sync(size);
@@ -376,8 +397,10 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
     // a second launch would), or no item has anything to move.
     const int64_t most = std::max<int64_t>(0, std::min<int64_t>(p.budget, cap - p.budget));
     const bool moves = size == 1 && cached && whole16 && most * 2 * p.hd * es <= kOwnMoveBytes;
-    auto kernel = moves ? paged_evict_select_kernel<true, true>
-                        : cached ? paged_evict_select_kernel<true, false> : paged_evict_select_kernel<false, false>;
+    auto kernel = moves       ? paged_evict_select_kernel<true, true, true>
+                  : size == 1 ? paged_evict_select_kernel<true, false, true>  // 2 kClusterSlots < kMaxSlots
+                  : cached    ? paged_evict_select_kernel<true, false, false>
+                              : paged_evict_select_kernel<false, false, false>;
     const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(slots) * 4 : 0);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
