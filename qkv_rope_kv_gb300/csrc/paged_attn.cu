@@ -145,17 +145,28 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 
 // ---------------------------------------------------------------- split over the length, tensor cores
 
+// One new token has as many q rows as a kv head has q heads (5 to 8 here): each byte of the cache takes
+// 5 to 8 flops, so memory bounds a batch, and latencies a short sequence.  Of M = 128 (the least of a
+// tcgen05.mma, whose accumulators would also have to leave TMEM for every softmax step) 8 rows would be used;
+// an mma.sync has 16, all in use here, and its pipe is 13 to 17 % busy.
+// Measured (GPU time, of the copy rate): 64 sequences of 8 x 128 x f16 to 8192 slots 184 us, DRAM at 6.29 TB/s
+// (0.93); one of 32749 slots 29.4 us (0.67: about 10 us of it are launch, lengths, first pages and the join);
+// 32 to 4099 slots with weights 40 us; 14 x 64 x f16, 509 slots 6.2 us, all latency.
+//
 // Work is counted in units of 8 to 32 neighbouring slots of one item (8 KB of K and V as a rule), an item
 // being (sequence, kv head, block of up to 8 of its q heads).  Lengths are on the device, so every CTA finds
-// its own work from them.  With many items, all units in a row are dealt to the CTAs in equal
-// contiguous shares (an item counts kItemCost units more, for its q and its end); with few, each item
-// gets CTAs of its own, so that no CTA has two beginnings and ends on its path.  The part of an item
-// that a CTA does not hold whole goes to the workspace, and the last CTA to arrive joins the item's
-// parts in order.
+// its own work from them.  Each item gets CTAs of its own, so that no CTA has two beginnings and ends on its
+// path, unless the largest share is then more than kOwnUnits units above that of dealing all units in a row
+// to the CTAs in equal contiguous shares (where an item counts kItemCost units more, for its q and its end).
+// The part of an item that a CTA does not hold whole goes to the workspace, and the last CTA to arrive joins
+// the item's parts in order (in a cluster: through shared memory).
 //
 // Within a CTA the units go to the four warps in turn, and each warp is a stream of its own: it copies its
 // units into its own ring of stages (cp.async, rows addressed through the page table, rows outside
-// the sequence filled with zeros) and computes them, with no barrier but at the end of an item.
+// the sequence filled with zeros) and computes them, with no barrier but at the end of an item.  Two CTAs of
+// four warps on an SM: one of eight takes 188 to 194 us for the batch of 184; warps in step, by barriers, add
+// 2.7 us to the 32749 slots; a ring of two stages takes the same.  Code runs few times in a call, so its size
+// counts: the loops that fill the ring and join parts are kept rolled.
 //
 // The 8 q heads of an item take half of the 16 rows of an MMA.  The other half carries what the
 // first loses: rows 0-7 hold q rounded to f16 (tf32), rows 8-15 the rounded remainder, and the same
@@ -310,7 +321,7 @@ __device__ __forceinline__ int join_fan(int n) {
 
 template <int UK>
 __device__ __forceinline__ void seq_units(const PagedAttnParams& p, int b, bool flag, Walk& w) {
-    int n = __ldg(p.lens + b);
+    int n = p.lens[b];
     if (n < 0 || n > p.c.max_pages * p.c.page_size) {
         if (flag) flag_bad(kFlagIndexRange, n);
         n = 0;
@@ -482,7 +493,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
 #pragma unroll
         for (int i = 0; i < S::kQLoads; ++i) {
             const int e = tid + i * S::kThreads, h = e / HD, d = e % HD;
-            qx[i] = h < nheads && d < p.hd ? __ldg(q + h * p.hd + d) : 0.f;
+            qx[i] = h < nheads && d < p.hd ? __ldca(q + h * p.hd + d) : 0.f;  // (a plain load: +1.5 us at 32768 slots)
         }
     };
     auto keep_q = [&]() {
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
         if (a.in) {
             const int pg = slot / p.c.page_size;
             a.in_page = slot - pg * p.c.page_size;
-            a.id = __ldg(p.c.table + static_cast<int64_t>(ahead.b) * p.c.max_pages + pg);
+            a.id = p.c.table[static_cast<int64_t>(ahead.b) * p.c.max_pages + pg];
         }
         return a;
     };
@@ -1033,7 +1044,9 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
 constexpr int kWeightThreads = 128, kWeightSpan = 4 * kWeightThreads;  // slots of a CTA
 
 // slot_weight[b][kv head][j] += sum over the kv head's q heads of 2^(score - lse): four neighbouring slots a
-// thread, the rows of all heads in flight together.
+// thread, the rows of all heads in flight together.  A second pass over 4 bytes a score, since no weight is
+// known before the whole row's sum; the scores come from L2 or DRAM, 8.5 us for 32 x 28 heads to 4099 slots
+// (8.9 MB, 1.0 TB/s: bound by two loads' latency, which the attention's end hides in part).
 __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const __grid_constant__ PagedAttnParams p,
                                                                            int chunks) {
     // Lengths and old weights do not come from the attention kernel, and what comes before that one was done
@@ -1041,7 +1054,7 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
     const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
     const int b = item / p.nkv, hk = item - b * p.nkv, G = p.nh / p.nkv;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    int n = __ldg(p.lens + b);
+    int n = __ldcg(p.lens + b);
     if (n < 0 || n > cap) n = 0;  // flagged by the attention kernel
     const int first = p.window > 0 ? max(0, n - p.window) : 0;
     const int64_t h0 = static_cast<int64_t>(b) * p.nh + static_cast<int64_t>(hk) * G;
@@ -1051,7 +1064,7 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
          j += static_cast<int64_t>(chunks) * kWeightSpan) {
         float old[4], w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) old[k] = j + k >= first && j + k < n ? weight[j + k] : 0.f;
+        for (int k = 0; k < 4; ++k) old[k] = j + k >= first && j + k < n ? __ldcg(weight + j + k) : 0.f;
         if (!waited) {
             griddep_wait();
             waited = true;

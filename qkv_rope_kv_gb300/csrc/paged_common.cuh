@@ -27,7 +27,7 @@ struct PageRef {
 };
 __device__ __forceinline__ PageRef page_ref(const PagedView& c, int seq, int slot) {
     const int pg = slot / c.page_size;
-    return {__ldg(c.table + static_cast<int64_t>(seq) * c.max_pages + pg), slot - pg * c.page_size};
+    return {c.table[static_cast<int64_t>(seq) * c.max_pages + pg], slot - pg * c.page_size};
 }
 // Element offset of the slot's row in the pools, or -1 (and the status flag) where the table names a page
 // that is not there.  64-bit: a pool can hold more than 2^31 elements.
@@ -45,7 +45,7 @@ __device__ __forceinline__ int64_t row_offset(const PagedView& c, int seq, int s
 
 // Length of sequence b, or 0 (and the status flag) where it is outside [0, capacity].
 __device__ __forceinline__ int checked_len(const PagedView& c, const int32_t* lens, int b) {
-    const int n = __ldg(lens + b);
+    const int n = lens[b];
     if (n < 0 || n > c.max_pages * c.page_size) {
         flag_bad(kFlagIndexRange, n);
         return 0;

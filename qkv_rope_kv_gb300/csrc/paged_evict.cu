@@ -8,7 +8,10 @@
 //
 // Two launches: one finds the moves (one or more CTAs per item, bound by their chain of barriers and
 // cluster exchanges), one makes them with the whole GPU (bound by the latency of list, table and
-// row, or by memory); a single one where items have little to move.
+// row, or by memory); a single one where items have little to move.  Measured (GPU time): 8 sequences x 8
+// heads, 2112 -> 2048 slots 11.0 us; 1 x 4, 32749 -> 8192 24.1 us; 32 x 2, to 4099 -> 1024 20.9 us (the bytes
+// would take 0.9, 4.0 and 5.6 us).  256 threads instead of 1024: 14.8 us for the first kernel where 1024 take
+// 9.3; both in one launch for the prompt: 30 us.
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -166,8 +169,8 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
     for (int i = tid; i < kPasses * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     qkv_ptx::griddep_wait();
     qkv_ptx::griddep_launch_dependents();
-    const int len = __ldg(p.lens + b);
-    const int next_pos = __ldg(p.next_pos + b);
+    const int len = p.lens[b];
+    const int next_pos = p.next_pos[b];
     const bool sane = len >= 0 && len <= cap;
     if (rank == 0 && tid == 0) {
         if (h == 0) {
