@@ -272,6 +272,30 @@ def test_attn(qkv, nh, nkv, hd, kv, page, lens, kw):
     run_attn(nh, nkv, hd, kv, page, lens, **kw)
 
 
+@pytest.mark.parametrize("nh,nkv,hd,kv,page,lens,kw", [
+    (96, 8, 128, "f16", 16, [700, 1, 64, 0, 300, 5], dict(weights=True)),
+    (96, 8, 128, "f32", 13, [260, 90, 5, 700], dict(weights=True)),
+    (24, 2, 64, "f16", 16, [200, 0, 33, 1] * 9, dict(out="bf16")),
+    (24, 2, 64, "f32", 16, [100, 31, 0] * 8, dict(weights=True, window=40)),
+    (20, 1, 256, "f16", 16, [100, 31] * 16, dict(weights=True)),     # three blocks of q heads
+    (12, 1, 256, "f32", 16, [100, 31] * 16, {}),
+    (22, 1, 80, "f16", 16, [100, 31] * 16, dict(weights=True)),
+    (17, 1, 96, "f32", 7, [100, 31] * 16, {}),
+    (68, 2, 72, "f32", 16, [90, 300, 2] * 3, dict(stride=4, page_gap=4)),
+    (136, 1, 64, "f16", 16, [90, 31, 0, 200] * 4, dict(weights=True)),  # seventeen
+    (136, 1, 64, "f16", 64, [5000], dict(weights=True)),
+    (40, 2, 128, "f16", 64, [6000, 5000] * 6, {}),
+    (24, 2, 128, "f16", 64, [20000] + [1] * 30, dict(weights=True)),
+    (12, 1, 128, "f16", 64, [20011, 40], dict(weights=True)),
+    (33, 1, 128, "f16", 64, [9000], {}),
+    (12, 1, 64, "f32", 64, [9000, 50], dict(weights=True)),
+    (16, 2, 6, "f16", 4, [50, 3], {}),
+], ids=short)
+def test_attn_with_blocks_of_q_heads(qkv, nh, nkv, hd, kv, page, lens, kw):
+    """More than eight q heads to a kv head."""
+    run_attn(nh, nkv, hd, kv, page, lens, **kw)
+
+
 @pytest.mark.parametrize("kv", ["f16", "f32"])
 def test_attn_with_infinite_values(qkv, kv):
     """A slot whose score is -inf has weight 0; an infinite V element reaches only its column; a NaN
