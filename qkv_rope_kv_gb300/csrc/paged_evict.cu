@@ -9,7 +9,7 @@
 // Two launches: one finds the moves (one or more CTAs per item, bound by their chain of barriers and
 // cluster exchanges), one makes them with the whole GPU (bound by the latency of list, table and
 // row, or by memory); a single one where items have little to move.  Measured (GPU time): 8 sequences x 8
-// heads, 2112 -> 2048 slots 11.0 us; 1 x 4, 32749 -> 8192 24.1 us; 32 x 2, to 4099 -> 1024 20.9 us (the bytes
+// heads, 2112 -> 2048 slots 11.0 us; 1 x 4, 32749 -> 8192 24.1 us; 32 x 2, to 4099 -> 1000 20.9 us (the bytes
 // would take 0.9, 4.0 and 5.6 us).  256 threads instead of 1024: 14.8 us for the first kernel where 1024 take
 // 9.3; both in one launch for the prompt: 30 us.
 #include <algorithm>
