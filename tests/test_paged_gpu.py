@@ -267,6 +267,9 @@ def run_attn(nh, nkv, hd, kv, page, lens, window=0, out="f32", weights=False, se
     (2, 2, 64, "f16", 16, [12000] + [33] * 60, dict(weights=True)),  # one long among many short
     (2, 1, 64, "f16", 16, [(7 * i) % 40 if i % 3 else 0 for i in range(1500)], dict(max_pages=3, weights=True)),
     (2, 2, 64, "f32", 16, [0] * 700 + [300] + [0] * 40, {}),
+    (28, 4, 128, "f16", 16, [40, 0, 7, 33] * 40, dict(weights=True)),  # items dealt whole, several a CTA
+    (14, 2, 64, "f32", 8, [(37 * i) % 90 for i in range(400)], dict(window=50)),
+    (5, 1, 256, "f16", 16, [16, 100, 1] * 150, {}),
 ], ids=short)
 def test_attn(qkv, nh, nkv, hd, kv, page, lens, kw):
     run_attn(nh, nkv, hd, kv, page, lens, **kw)
