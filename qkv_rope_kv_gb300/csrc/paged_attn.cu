@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // tcgen05.mma, whose accumulators would also have to leave TMEM for every softmax step) 8 rows would be used;
 // an mma.sync has 16, all in use here, and its pipe is 13 to 17 % busy.
 // Measured (GPU time, of the copy rate): 64 sequences of 8 x 128 x f16 to 8192 slots 184 us, DRAM at 6.29 TB/s
-// (0.93); one of 32749 slots 29.4 us (0.67: about 10 us of it are launch, lengths, first pages and the join);
-// 32 to 4099 slots with weights 40.7 us; 14 x 64 x f32, 509 slots 6.6 us, all latency.
+// (0.93); one of 32749 slots 28.7 us (0.69: about 9 us of it are launch, lengths, first pages and the join);
+// 32 to 4099 slots with weights 40.7 us; 14 x 64 x f32, 509 slots 6.1 us, all latency.
 //
 // Work is counted in units of 8 to 32 neighbouring slots of one item (8 KB of K and V as a rule), an item
 // being (sequence, kv head, block of up to 8 of its q heads).  Lengths are on the device, so every CTA finds
@@ -205,8 +205,10 @@ struct Split {
     static constexpr int kQuads = HD / 16;                 // a lane's outputs of one head, in fours
     static constexpr int kQRow = HD + (kF16 ? 8 : 16);     // floats; spreads the heads' rows over the banks
     static constexpr int kQLoads = kAttnHeads * HD / kThreads;
-    static constexpr bool kQRegs = HD < 256;               // q's fragments stay in registers beside O
-    static constexpr bool kQAhead = HD < 256;              // the next item's q too
+    // q's fragments stay in registers beside O, and the next item's q is loaded ahead, where that leaves no spills
+    // in the loop (4 x 128 x f32, 32000 slots: 37 us, with fragments in registers 64)
+    static constexpr bool kQRegs = kF16 && HD < 256;
+    static constexpr bool kQAhead = kF16 ? HD < 256 : HD < 128;
     static constexpr int kMergeFloats = (kWarps - 1) * kAttnHeads * HD;  // O of the warps but the first
     static constexpr int kPartFloats = kAttnHeads * (HD + 2);
     static constexpr int kSmem = kWarps * kRingBytes +
@@ -267,6 +269,7 @@ __device__ __forceinline__ unsigned int atom_add_acq_rel(unsigned int* p, unsign
 }
 
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // What CTA `rank` of the cluster has at the place of `p` in its shared memory.
@@ -865,131 +868,195 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                                      join_halves(O[4 * (i >> 1) + 2][i & 1], O[4 * (i >> 1) + 2][2 + (i & 1)]),
                                      join_halves(O[4 * (i >> 1) + 3][i & 1], O[4 * (i >> 1) + 3][2 + (i & 1)]));
         }
-        __syncthreads();  // the last segment's merge and this one's q have been read
-        if (warp > 0) {
-            if (t == 0) {
-                merge_m[warp * kAttnHeads + g] = m;
-                merge_l[warp * kAttnHeads + g] = l;
-            }
-            float4* mo = reinterpret_cast<float4*>(merge) + (warp - 1) * S::kQuads * 32 + lane;
-#pragma unroll
-            for (int i = 0; i < S::kQuads; ++i) mo[i * 32] = acc[i];
-        }
-        if (follows) keep_q();
-        __syncthreads();
-        float M = m, L = l;
-        if (warp == 0) {
-#pragma unroll
-            for (int w = 1; w < S::kWarps; ++w) M = fmaxf(M, merge_m[w * kAttnHeads + g]);
-            const float k0 = m == M ? 1.f : ex2(m - M);
-            L = l * k0;
-#pragma unroll
-            for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(acc[i], k0, make_float4(0.f, 0.f, 0.f, 0.f));
-#pragma unroll
-            for (int w = 1; w < S::kWarps; ++w) {
-                const float mw = merge_m[w * kAttnHeads + g], k = mw == M ? 1.f : ex2(mw - M);
-                L = fmaf(merge_l[w * kAttnHeads + g], k, L);
-                const float4* mo = reinterpret_cast<const float4*>(merge) + (w - 1) * S::kQuads * 32 + lane;
-#pragma unroll
-                for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(mo[i * 32], k, acc[i]);
-            }
-        }
         if constexpr (CLUSTERED) {
-            // Every CTA's sums to the place of its warps' O, in lane-linear quads; the first CTA reads them.
-            float4* mine = reinterpret_cast<float4*>(merge);
+            // All warps' sums to shared memory (the place of their units); then each CTA of the cluster joins its
+            // share of the quads, and so do, where clusters share an item, the CTAs of its last cluster to arrive.
+            // Four threads take a quad: a warp of each CTA one, then a quarter of the clusters.  (Warps joined first,
+            // then CTAs by the cluster's first one: 0.7 us more for 28/4 x 128 x f16, 1641 slots.)
+            constexpr int kPer = S::kQuads * 32 / kCluster;  // quads of a CTA
+            const int rank = blockIdx.x % kCluster, w = tid & 3, clusters = c1 - c0 + 1;
             float2* ml = reinterpret_cast<float2*>(merge_m);
-            if (warp == 0) {
-                __syncwarp();
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < S::kQuads; ++i) mine[i * 32 + lane] = acc[i];
-                if (t == 0) ml[g] = make_float2(M, L);
-            }
+            for (int i = 0; i < S::kQuads; ++i) reinterpret_cast<float4*>(ring)[i * 32 + lane] = acc[i];
+            if (t == 0) ml[warp * kAttnHeads + g] = make_float2(m, l);
             cluster_sync();
-            if (blockIdx.x % kCluster == 0) {
-                constexpr int kMine = 2 * HD / S::kThreads;
+            auto part_of = [&](int c) {  // of the item's cluster c, this CTA's share
+                return p.part + static_cast<int64_t>(2 * ((c * abreast + blk) * kCluster + rank)) * S::kPartFloats;
+            };
+            auto join4 = [&](float& M, float& L, float4& v) {
+                float top = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float k = M == top ? 1.f : ex2(M - top);
+                M = top;
+                L *= k;
+                v = fma4(v, k, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+                for (int x = 1; x < 4; x <<= 1) {
+                    L += __shfl_xor_sync(0xffffffffu, L, x);
+                    v.x += __shfl_xor_sync(0xffffffffu, v.x, x);
+                    v.y += __shfl_xor_sync(0xffffffffu, v.y, x);
+                    v.z += __shfl_xor_sync(0xffffffffu, v.z, x);
+                    v.w += __shfl_xor_sync(0xffffffffu, v.w, x);
+                }
+            };
+            auto emit = [&](int e, float M, float L, float4 v) {  // a column a thread
+                const int h = (e & 31) >> 2, col = quad_col<S::kF16>(e >> 5, w, e & 3);
+                const float mine = w < 2 ? (w == 0 ? v.x : v.y) : (w == 2 ? v.z : v.w);
+                if (h >= nheads) return;
+                if (col < p.hd) put_out(p, at.b, h0 + h, col, mine / L);
+                if ((e & ~28) == 0 && w == 0) put_lse(p, at.b, h0 + h, M - kPShift, L, false);
+            };
+            const float4* theirs = reinterpret_cast<const float4*>(smem + w * S::kRingBytes);
+#pragma unroll 1
+            for (int f = tid >> 2; f < kPer; f += S::kThreads / 4) {
+                const int e = rank * kPer + f;
                 float2 v[kCluster];
-                float4 sum[kMine];
-                float Mh = -CUDART_INF_F, Lh = 0.f;
+                float4 o[kCluster];
 #pragma unroll
                 for (int r = 0; r < kCluster; ++r) {
-                    v[r] = peer_float2(ml + g, r);
-                    Mh = fmaxf(Mh, v[r].x);
+                    v[r] = peer_float2(ml + w * kAttnHeads + ((e & 31) >> 2), r);
+                    o[r] = peer_float4(theirs + e, r);
                 }
+                float M = v[0].x, L = 0.f;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int r = 1; r < kCluster; ++r) M = fmaxf(M, v[r].x);
 #pragma unroll
                 for (int r = 0; r < kCluster; ++r) {
-                    const float k = v[r].x == Mh ? 1.f : ex2(v[r].x - Mh);
-                    Lh = fmaf(v[r].y, k, Lh);
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) sum[i] = fma4(peer_float4(mine + i * S::kThreads + tid, r), k, sum[i]);
+                    const float k = v[r].x == M ? 1.f : ex2(v[r].x - M);
+                    L = fmaf(v[r].y, k, L);
+                    sum = fma4(o[r], k, sum);
                 }
-                if (c0 == c1) {
-                    __syncthreads();  // the quads have been read: the rows take their place
-                    const float inv = 1.f / Lh;
+                join4(M, L, sum);
+                if (clusters == 1) {
+                    emit(e, M, L, sum);
+                } else if (w == 0) {
+                    float4* to = reinterpret_cast<float4*>(part_of(me));
+                    __stcg(to + f, sum);
+                    if ((f & 3) == 0) __stcg(reinterpret_cast<float2*>(to + kPer) + (f >> 2), make_float2(M, L));
+                }
+            }
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            if (clusters > 1) {
+                unsigned int* counter = p.counters + (c0 * abreast + blk) * kCluster + rank;
+                __syncthreads();
+                if (tid == 0) last_s = atom_add_acq_rel(counter, 1u);
+                __syncthreads();
+                if (last_s == static_cast<unsigned int>(clusters - 1)) {
+                    if (tid == 0) *counter = 0u;
+#pragma unroll 1
+                    for (int f = tid >> 2; f < kPer; f += S::kThreads / 4) {
+                        float M = -CUDART_INF_F, L = 0.f;
+                        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                        for (int c = w; c < clusters; c += 16) {
+                            float2 v[4];
+                            float4 o[4];
 #pragma unroll
-                    for (int i = 0; i < kMine; ++i) keep_out(i * S::kWarps + warp, sum[i], inv);
-                    if (warp == 0 && t == 0 && g < nheads) put_lse(p, at.b, h0 + g, Mh - kPShift, Lh, false);
-                    __syncthreads();
-                    if (warp == 0) put_rows(at.b, h0, nheads);
-                } else {
+                            for (int i = 0; i < 4; ++i) {
+                                const float4* from = reinterpret_cast<const float4*>(part_of(c0 + min(c + 4 * i, clusters - 1)));
+                                v[i] = __ldcg(reinterpret_cast<const float2*>(from + kPer) + (f >> 2));
+                                o[i] = __ldcg(from + f);
+                            }
+                            float top = M;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (c + 4 * i < clusters) top = fmaxf(top, v[i].x);
+                            const float keep = M == top ? 1.f : ex2(M - top);
+                            M = top;
+                            L *= keep;
+                            sum = fma4(sum, keep, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (c + 4 * i < clusters) {
+                                    const float k = v[i].x == M ? 1.f : ex2(v[i].x - M);
+                                    L = fmaf(v[i].y, k, L);
+                                    sum = fma4(o[i], k, sum);
+                                }
+                        }
+                        join4(M, L, sum);
+                        emit(rank * kPer + f, M, L, sum);
+                    }
+                }
+            }
+            __syncwarp();
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no CTA leaves while its sums may be read
+        } else {
+            __syncthreads();  // the last segment's merge and this one's q have been read
+            if (warp > 0) {
+                if (t == 0) {
+                    merge_m[warp * kAttnHeads + g] = m;
+                    merge_l[warp * kAttnHeads + g] = l;
+                }
+                float4* mo = reinterpret_cast<float4*>(merge) + (warp - 1) * S::kQuads * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < S::kQuads; ++i) mo[i * 32] = acc[i];
+            }
+            if (follows) keep_q();
+            __syncthreads();
+            float M = m, L = l;
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < S::kWarps; ++w) M = fmaxf(M, merge_m[w * kAttnHeads + g]);
+                const float k0 = m == M ? 1.f : ex2(m - M);
+                L = l * k0;
+#pragma unroll
+                for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(acc[i], k0, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+                for (int w = 1; w < S::kWarps; ++w) {
+                    const float mw = merge_m[w * kAttnHeads + g], k = mw == M ? 1.f : ex2(mw - M);
+                    L = fmaf(merge_l[w * kAttnHeads + g], k, L);
+                    const float4* mo = reinterpret_cast<const float4*>(merge) + (w - 1) * S::kQuads * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < S::kQuads; ++i) acc[i] = fma4(mo[i * 32], k, acc[i]);
+                }
+            }
+            if (us == 0 && ue == at.units) {
+                if (warp == 0) {
+                    __syncwarp();  // the warps' O have been read: their place takes the rows
+                    const float inv = 1.f / L;
+#pragma unroll
+                    for (int i = 0; i < S::kQuads; ++i) keep_out(i, acc[i], inv);
+                    if (t == 0 && g < nheads) put_lse(p, at.b, h0 + g, M - kPShift, L, false);
+                    __syncwarp();
+                    put_rows(at.b, h0, nheads);
+                }
+            } else {
+                // This CTA's part; an item's parts are those of its CTAs c0 .. c1, and the last of a group of
+                // them to be counted will be joined by its CTA, at the end of all its units.  A CTA has two
+                // such segments at most, its first and its last.
+                if (!own) {
+                    c0 = static_cast<int>(div_small(at.start, share));
+                    c1 = static_cast<int>(div_small(at.start + at.units - 1, share));
+                }
+                if (warp == 0) {
                     const Pending e = {at.b, h0, nheads, c0, c1 - c0 + 1, 0u};
-                    float4* to = reinterpret_cast<float4*>(part(e, me));
+                    float* to = part(e, me);
                     if (g < nheads) {
 #pragma unroll
-                        for (int i = 0; i < kMine; ++i) __stcg(to + i * S::kThreads + tid, sum[i]);
-                        if (warp == 0 && t == 0) __stcg(reinterpret_cast<float2*>(to + S::kQuads * 32) + g, make_float2(Mh, Lh));
+                        for (int i = 0; i < S::kQuads; ++i) __stcg(reinterpret_cast<float4*>(to) + i * 32 + lane, acc[i]);
+                        if (t == 0) __stcg(reinterpret_cast<float2*>(to + kAttnHeads * HD) + g, make_float2(M, L));
                     }
-                    __syncthreads();
-                    if (tid == 0) {  // counted as below; clusters are few enough for one group
-                        pending_s[0] = e;
-                        pending_s[0].counted = atom_add_acq_rel(counters + 2 * c0 + 1, 1u);
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int fan = join_fan(e.n), first = e.c0 + (me - e.c0) / fan * fan;
+                        pending_s[pendings] = e;
+                        // release the part (the warp's writes come before, by its barrier)
+                        pending_s[pendings].counted = atom_add_acq_rel(counters + 2 * first + (first == e.c0), 1u);
                     }
-                    pendings = 1;
                 }
+                ++pendings;
             }
-            cluster_sync();  // no CTA leaves while its sums may be read
-        } else if (us == 0 && ue == at.units) {
-            if (warp == 0) {
-                __syncwarp();  // the warps' O have been read: their place takes the rows
-                const float inv = 1.f / L;
-#pragma unroll
-                for (int i = 0; i < S::kQuads; ++i) keep_out(i, acc[i], inv);
-                if (t == 0 && g < nheads) put_lse(p, at.b, h0 + g, M - kPShift, L, false);
-                __syncwarp();
-                put_rows(at.b, h0, nheads);
-            }
-        } else {
-            // This CTA's part; an item's parts are those of its CTAs c0 .. c1, and the last of a group of
-            // them to be counted will be joined by its CTA, at the end of all its units.  A CTA has two
-            // such segments at most, its first and its last.
-            if (!own) {
-                c0 = static_cast<int>(div_small(at.start, share));
-                c1 = static_cast<int>(div_small(at.start + at.units - 1, share));
-            }
-            if (warp == 0) {
-                const Pending e = {at.b, h0, nheads, c0, c1 - c0 + 1, 0u};
-                float* to = part(e, me);
-                if (g < nheads) {
-#pragma unroll
-                    for (int i = 0; i < S::kQuads; ++i) __stcg(reinterpret_cast<float4*>(to) + i * 32 + lane, acc[i]);
-                    if (t == 0) __stcg(reinterpret_cast<float2*>(to + kAttnHeads * HD) + g, make_float2(M, L));
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    const int fan = join_fan(e.n), first = e.c0 + (me - e.c0) / fan * fan;
-                    pending_s[pendings] = e;
-                    // release the part (the warp's writes come before, by its barrier)
-                    pending_s[pendings].counted = atom_add_acq_rel(counters + 2 * first + (first == e.c0), 1u);
-                }
-            }
-            ++pendings;
         }
-        if (!follows) break;
+        if (CLUSTERED || !follows) break;  // a cluster has one item
         at = next;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
+    if constexpr (CLUSTERED) return;
     // Join what this CTA was the last to complete: groups of neighbouring parts first, then the groups
     // (one group where the parts are few).
 #pragma unroll 1
@@ -1177,8 +1244,8 @@ cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     const int blocks = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
     const int abreast = blocks <= kMaxAbreast ? blocks : 1, serial = blocks / abreast;
     // Clusters (as many as fit at a time) while every item can have two of them, and sequences can be
-    // longer than what one CTA does as fast (8 units): one 500-slot 7B sequence 9.6 us without, 7.6 us with
-    // clusters, 32000 slots 24.2 and 22.3 us, 16 slots 6.1 and 7.3 us.
+    // longer than what one CTA does as fast (8 units): one 500-slot 7B sequence 9.6 us without, 6.9 us with
+    // clusters, 32000 slots 24.2 and 20.9 us, 16 slots 6.1 and 7.3 us (before the last step).
     int clusters = 0;
     const cudaError_t e = resident_clusters<KT, HD>(&clusters);
     if (e != cudaSuccess) return e;
