@@ -185,6 +185,7 @@ constexpr int kItemCost = 8;     // units
 constexpr int kJoinCost = 16;    // units
 constexpr int kOwnUnits = 8;     // how much larger the largest share may be with CTAs of its own for each item
 constexpr int kCluster = 8;      // CTAs of a cluster
+constexpr int kOneClusterUnits = 256;  // capacity up to which an item may have just one
 constexpr int kMaxAbreast = 8;   // blocks of q heads that go side by side
 constexpr int kJoinParts = 40;   // more parts than this are joined in two levels
 constexpr float kPShift = 12.f;  // weights are kept times 2^12
@@ -439,7 +440,11 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     // A share is at least kMinShare units (each part costs a join), but not above the longest item.
     const int64_t spare = static_cast<int64_t>(ctas) - kUnited * n_items;
     const int64_t least = min(longest, kMinShare);
-    const int64_t alone = spare > 0 ? min(max(div_small(total + spare - 1, spare), least), static_cast<int64_t>(longest)) : longest;
+    int64_t alone = spare > 0 ? min(max(div_small(total + spare - 1, spare), least), static_cast<int64_t>(longest)) : longest;
+    if (CLUSTERED && n_items > 0) {  // as many clusters for every item as there are for one take less where lengths are alike
+        const int64_t even = div_small(ctas / kUnited, n_items) * kUnited;
+        if (even > 0) alone = min(alone, max(div_small(longest + even - 1, even), least));
+    }
     const int64_t dealt = max(div_small(total + n_items * kItemCost + ctas - 1, ctas), least + kItemCost);
     const bool own = CLUSTERED || (spare >= 0 && alone <= dealt + kOwnUnits);
     // Not own: whole items, the same number for every CTA (each taking the room of the longest), where that makes
@@ -1230,6 +1235,9 @@ cudaError_t resident_clusters(int* out) {
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
     if (e != cudaSuccess) return e;
+    // Only a perfect packing of the SMs holds that many: of 36, a launch behind another kernel had 33 to 36 running
+    // at once, the rest after them (28/4 x 128 x f16, 24000 slots: 25.7 us on 36 clusters, 18.5 on 32).
+    *out = *out * 8 / 9;
     if (*out > kAttnMaxCtas / kCluster) *out = kAttnMaxCtas / kCluster;
     if (dev < kMaxDevices) known[dev].store(*out, std::memory_order_relaxed);
     return cudaSuccess;
@@ -1243,15 +1251,19 @@ cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     // Above 64 q heads a kv head's blocks are items one after another.
     const int blocks = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
     const int abreast = blocks <= kMaxAbreast ? blocks : 1, serial = blocks / abreast;
-    // Clusters (as many as fit at a time) while every item can have two of them, and sequences can be
-    // longer than what one CTA does as fast (8 units): one 500-slot 7B sequence 9.6 us without, 6.9 us with
-    // clusters, 32000 slots 24.2 and 20.9 us, 16 slots 6.1 and 7.3 us (before the last step).
+    // Clusters while every item can have two of them, or one if sequences are short, and sequences can be longer
+    // than what one CTA does as fast (6 units).  No more clusters than can have work.  One 500-slot 7B sequence
+    // 10.1 us without, 6.7 us with clusters, 24000 slots 21.1 and 18.5 us, 64 slots 6.1 and 6.4 us; 24 items
+    // with clusters of their own: 500 slots 10.5 and 8.0 us, 2000 13.5 and 11.3, 24000 55 and 60.
     int clusters = 0;
     const cudaError_t e = resident_clusters<KT, HD>(&clusters);
     if (e != cudaSuccess) return e;
-    const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
-    if (cap >= 8 * S::UK && static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks * 2 <= clusters)
-        return launch_split_t<KT, HD, true>(p, clusters, abreast, serial, stream);
+    const int64_t cap_units = static_cast<int64_t>(p.c.max_pages) * p.c.page_size / S::UK;
+    const int64_t most_items = static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks;
+    if (cap_units >= 6 && most_items * (cap_units <= kOneClusterUnits ? 1 : 2) <= clusters) {
+        const int64_t useful = most_items * (cap_units / (kMinShare * kCluster) + 1);
+        return launch_split_t<KT, HD, true>(p, static_cast<int>(useful < clusters ? useful : clusters), abreast, serial, stream);
+    }
     return launch_split_t<KT, HD, false>(p, kSms * S::kCtas, abreast, serial, stream);
 }
 
