@@ -184,8 +184,6 @@ constexpr int kMinShare = 8;     // units
 constexpr int kItemCost = 8;     // units
 constexpr int kJoinCost = 16;    // units
 constexpr int kOwnUnits = 8;     // how much larger the largest share may be with CTAs of its own for each item
-constexpr int kCluster = 8;      // CTAs of a cluster
-constexpr int kOneClusterUnits = 256;  // capacity up to which an item may have just one
 constexpr int kMaxAbreast = 8;   // blocks of q heads that go side by side
 constexpr int kJoinParts = 40;   // more parts than this are joined in two levels
 constexpr float kPShift = 12.f;  // weights are kept times 2^12
@@ -373,24 +371,24 @@ __device__ __forceinline__ float4 fma4(float4 o, float k, float4 a) {
     return make_float4(fmaf(o.x, k, a.x), fmaf(o.y, k, a.y), fmaf(o.z, k, a.z), fmaf(o.w, k, a.w));
 }
 
-// CLUSTERED: clusters of kCluster CTAs, each with units of one item; the CTAs' parts are joined through
+// C > 1: clusters of C CTAs, each with units of one item; the CTAs' parts are joined through
 // their shared memory.
-template <typename KT, int HD, bool CLUSTERED>
+template <typename KT, int HD, int C>
 __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     paged_attn_split_kernel(const __grid_constant__ PagedAttnParams p, int abreast, int serial) {
     using S = Split<KT, HD>;
     constexpr int UK = S::UK;
+    constexpr bool CLUSTERED = C > 1;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Pending pending_s[2];
     __shared__ unsigned int last_s;
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
     const int B = p.c.n_seq, G = p.nh / p.nkv, items = p.nkv * serial;
-    constexpr int kUnited = CLUSTERED ? kCluster : 1;  // CTAs that an item gets at least, and a multiple of
     // The CTAs (clusters) are dealt to the blocks of q heads that go abreast, which split up their own work alike.
     const int ctas = gridDim.x / abreast;
-    const int me = blockIdx.x / kUnited / abreast, blk = blockIdx.x / kUnited - me * abreast;
-    const int cta = me * kUnited + (CLUSTERED ? blockIdx.x % kUnited : 0);
+    const int me = blockIdx.x / C / abreast, blk = blockIdx.x / C - me * abreast;
+    const int cta = me * C + blockIdx.x % C;
     float* const parts = p.part + static_cast<int64_t>(2 * blk * ctas) * S::kPartFloats;
     unsigned int* const counters = p.counters + 2 * blk * ctas;
     unsigned char* ring = smem + warp * S::kRingBytes;
@@ -438,12 +436,15 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     // CTAs of their own for the items, ceil(units / share) each, which are no more than the grid; or equal
     // shares of everything, whatever the items, where that makes the largest share clearly smaller.
     // A share is at least kMinShare units (each part costs a join), but not above the longest item.
-    const int64_t spare = static_cast<int64_t>(ctas) - kUnited * n_items;
+    const int64_t spare = static_cast<int64_t>(ctas) - C * n_items;
     const int64_t least = min(longest, kMinShare);
     int64_t alone = spare > 0 ? min(max(div_small(total + spare - 1, spare), least), static_cast<int64_t>(longest)) : longest;
-    if (CLUSTERED && n_items > 0) {  // as many clusters for every item as there are for one take less where lengths are alike
-        const int64_t even = div_small(ctas / kUnited, n_items) * kUnited;
+    if (CLUSTERED && n_items > 0) {
+        // as many clusters for every item as there are for one take less where lengths are alike, and one for
+        // each saves a join
+        const int64_t even = div_small(ctas / C, n_items) * C, single = max(div_small(longest + C - 1, C), least);
         if (even > 0) alone = min(alone, max(div_small(longest + even - 1, even), least));
+        if (single <= alone + kOwnUnits) alone = max(alone, single);
     }
     const int64_t dealt = max(div_small(total + n_items * kItemCost + ctas - 1, ctas), least + kItemCost);
     const bool own = CLUSTERED || (spare >= 0 && alone <= dealt + kOwnUnits);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     auto extent = [&](int units) -> int64_t {  // of one item
         if (units == 0 || !own) return units == 0 ? 0 : max(units + cost, room);
         const int n = (units + static_cast<int>(share) - 1) / static_cast<int>(share);
-        return (n + kUnited - 1) / kUnited * kUnited;
+        return (n + C - 1) / C * C;
     };
     int64_t before = 0, start = 0;  // extent of the sequences before this round's; where x's sequence starts
     int b_at = -1;
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
         at.item = static_cast<int>(div_small(x - start, e));
         const int64_t r = (x - start) - at.item * e;
         if (own) {  // chunk r of e: the order is the item's own units
-            c0 = static_cast<int>(cta - r) / kUnited;
-            c1 = c0 + static_cast<int>(e) / kUnited - 1;
+            c0 = static_cast<int>(cta - r) / C;
+            c1 = c0 + static_cast<int>(e) / C - 1;
             at.start = 0;
             const int n = static_cast<int>(e), each = at.units / n, left = at.units - each * n, i = static_cast<int>(r);
             at.u = i * each + min(i, left);
@@ -878,8 +879,8 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
             // share of the quads, and so do, where clusters share an item, the CTAs of its last cluster to arrive.
             // Four threads take a quad: a warp of each CTA one, then a quarter of the clusters.  (Warps joined first,
             // then CTAs by the cluster's first one: 0.7 us more for 28/4 x 128 x f16, 1641 slots.)
-            constexpr int kPer = S::kQuads * 32 / kCluster;  // quads of a CTA
-            const int rank = blockIdx.x % kCluster, w = tid & 3, clusters = c1 - c0 + 1;
+            constexpr int kPer = S::kQuads * 32 / C;  // quads of a CTA
+            const int rank = blockIdx.x % C, w = tid & 3, clusters = c1 - c0 + 1;
             float2* ml = reinterpret_cast<float2*>(merge_m);
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
             if (t == 0) ml[warp * kAttnHeads + g] = make_float2(m, l);
             cluster_sync();
             auto part_of = [&](int c) {  // of the item's cluster c, this CTA's share
-                return p.part + static_cast<int64_t>(2 * ((c * abreast + blk) * kCluster + rank)) * S::kPartFloats;
+                return p.part + static_cast<int64_t>(2 * ((c * abreast + blk) * C + rank)) * S::kPartFloats;
             };
             auto join4 = [&](float& M, float& L, float4& v) {
                 float top = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
@@ -917,19 +918,19 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
 #pragma unroll 1
             for (int f = tid >> 2; f < kPer; f += S::kThreads / 4) {
                 const int e = rank * kPer + f;
-                float2 v[kCluster];
-                float4 o[kCluster];
+                float2 v[C];
+                float4 o[C];
 #pragma unroll
-                for (int r = 0; r < kCluster; ++r) {
+                for (int r = 0; r < C; ++r) {
                     v[r] = peer_float2(ml + w * kAttnHeads + ((e & 31) >> 2), r);
                     o[r] = peer_float4(theirs + e, r);
                 }
                 float M = v[0].x, L = 0.f;
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int r = 1; r < kCluster; ++r) M = fmaxf(M, v[r].x);
+                for (int r = 1; r < C; ++r) M = fmaxf(M, v[r].x);
 #pragma unroll
-                for (int r = 0; r < kCluster; ++r) {
+                for (int r = 0; r < C; ++r) {
                     const float k = v[r].x == M ? 1.f : ex2(v[r].x - M);
                     L = fmaf(v[r].y, k, L);
                     sum = fma4(o[r], k, sum);
@@ -946,7 +947,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
             __syncwarp();
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
             if (clusters > 1) {
-                unsigned int* counter = p.counters + (c0 * abreast + blk) * kCluster + rank;
+                unsigned int* counter = p.counters + (c0 * abreast + blk) * C + rank;
                 __syncthreads();
                 if (tid == 0) last_s = atom_add_acq_rel(counter, 1u);
                 __syncthreads();
@@ -1198,20 +1199,19 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
     griddep_launch_dependents();
 }
 
-template <typename KT, int HD, bool CLUSTERED>
+template <typename KT, int HD, int C>
 cudaError_t launch_split_t(const PagedAttnParams& p, int most, int abreast, int serial, cudaStream_t stream) {
     using S = Split<KT, HD>;
-    auto kernel = paged_attn_split_kernel<KT, HD, CLUSTERED>;
+    auto kernel = paged_attn_split_kernel<KT, HD, C>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    constexpr int kUnited = CLUSTERED ? kCluster : 1;
-    const int grid = most / abreast * abreast * kUnited;
-    return launch_dependent(kernel, dim3(grid), S::kThreads, S::kSmem, stream, kUnited, p, abreast, serial);
+    const int grid = most / abreast * abreast * C;
+    return launch_dependent(kernel, dim3(grid), S::kThreads, S::kSmem, stream, C, p, abreast, serial);
 }
 
 // How many clusters of the split kernel a device holds at a time (they need neighbouring SMs).  The same for
 // every context of a device, so it is asked for once.
-template <typename KT, int HD>
+template <typename KT, int HD, int C>
 cudaError_t resident_clusters(int* out) {
     constexpr int kMaxDevices = 64;
     static std::atomic<int> known[kMaxDevices];
@@ -1220,16 +1220,16 @@ cudaError_t resident_clusters(int* out) {
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
     using S = Split<KT, HD>;
-    auto kernel = paged_attn_split_kernel<KT, HD, true>;
+    auto kernel = paged_attn_split_kernel<KT, HD, C>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
+    cfg.gridDim = dim3(C);
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.x = C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
@@ -1238,9 +1238,28 @@ cudaError_t resident_clusters(int* out) {
     // Only a perfect packing of the SMs holds that many: of 36, a launch behind another kernel had 33 to 36 running
     // at once, the rest after them (28/4 x 128 x f16, 24000 slots: 25.7 us on 36 clusters, 18.5 on 32).
     *out = *out * 8 / 9;
-    if (*out > kAttnMaxCtas / kCluster) *out = kAttnMaxCtas / kCluster;
+    if (*out > kAttnMaxCtas / C) *out = kAttnMaxCtas / C;
     if (dev < kMaxDevices) known[dev].store(*out, std::memory_order_relaxed);
     return cudaSuccess;
+}
+
+// Clusters of C where every item can have two of them (C = 8), or one if sequences are short, and sequences can
+// be longer than what one CTA does as fast (6 units).  No more clusters than can have work.  28/4 x 128 x f16
+// without and with: one sequence of 64 slots 6.1 and 6.4 us, 500 10.1 and 6.8, 24000 21.1 and 18.5; six of 500
+// (C = 8) 10.6 and 8.1, ten of 400 (C = 4) 10.6 and 8.4, 25 of 400 (C = 2) 12.4 and 10.9; beyond the limits one
+// cluster an item loses: ragged 80 items to 1000 slots (C = 2) 12.4 and 15.4, 24 of 24000 (C = 8) 55 and 60.
+template <typename KT, int HD, int C>
+cudaError_t launch_clusters(const PagedAttnParams& p, int blocks, int abreast, int serial, cudaStream_t stream, bool* done) {
+    int clusters = 0;
+    const cudaError_t e = resident_clusters<KT, HD, C>(&clusters);
+    if (e != cudaSuccess) return e;
+    const int64_t units = static_cast<int64_t>(p.c.max_pages) * p.c.page_size / Split<KT, HD>::UK;  // of a full sequence
+    const int64_t items = static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks;
+    if (units < 6 || !((units <= (C == 8 ? 256 : 16 * C) && items <= clusters) || (C == 8 && items * 2 <= clusters)))
+        return cudaSuccess;
+    *done = true;
+    const int64_t useful = items * (units / (kMinShare * C) + 1);
+    return launch_split_t<KT, HD, C>(p, static_cast<int>(useful < clusters ? useful : clusters), abreast, serial, stream);
 }
 
 template <typename KT, int HD>
@@ -1251,20 +1270,12 @@ cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
     // Above 64 q heads a kv head's blocks are items one after another.
     const int blocks = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
     const int abreast = blocks <= kMaxAbreast ? blocks : 1, serial = blocks / abreast;
-    // Clusters while every item can have two of them, or one if sequences are short, and sequences can be longer
-    // than what one CTA does as fast (6 units).  No more clusters than can have work.  One 500-slot 7B sequence
-    // 10.1 us without, 6.7 us with clusters, 24000 slots 21.1 and 18.5 us, 64 slots 6.1 and 6.4 us; 24 items
-    // with clusters of their own: 500 slots 10.5 and 8.0 us, 2000 13.5 and 11.3, 24000 55 and 60.
-    int clusters = 0;
-    const cudaError_t e = resident_clusters<KT, HD>(&clusters);
-    if (e != cudaSuccess) return e;
-    const int64_t cap_units = static_cast<int64_t>(p.c.max_pages) * p.c.page_size / S::UK;
-    const int64_t most_items = static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks;
-    if (cap_units >= 6 && most_items * (cap_units <= kOneClusterUnits ? 1 : 2) <= clusters) {
-        const int64_t useful = most_items * (cap_units / (kMinShare * kCluster) + 1);
-        return launch_split_t<KT, HD, true>(p, static_cast<int>(useful < clusters ? useful : clusters), abreast, serial, stream);
-    }
-    return launch_split_t<KT, HD, false>(p, kSms * S::kCtas, abreast, serial, stream);
+    bool done = false;
+    cudaError_t e = launch_clusters<KT, HD, 8>(p, blocks, abreast, serial, stream, &done);
+    if (e == cudaSuccess && !done) e = launch_clusters<KT, HD, 4>(p, blocks, abreast, serial, stream, &done);
+    if (e == cudaSuccess && !done) e = launch_clusters<KT, HD, 2>(p, blocks, abreast, serial, stream, &done);
+    if (e != cudaSuccess || done) return e;
+    return launch_split_t<KT, HD, 1>(p, kSms * S::kCtas, abreast, serial, stream);
 }
 
 }  // namespace

@@ -268,6 +268,12 @@ def run_attn(nh, nkv, hd, kv, page, lens, window=0, out="f32", weights=False, se
     (2, 1, 64, "f16", 16, [(7 * i) % 40 if i % 3 else 0 for i in range(1500)], dict(max_pages=3, weights=True)),
     (2, 2, 64, "f32", 16, [0] * 700 + [300] + [0] * 40, {}),
     (28, 4, 128, "f16", 16, [40, 0, 7, 33] * 40, dict(weights=True)),  # items dealt whole, several a CTA
+    (28, 4, 128, "f16", 16, [100, 300, 0, 5, 333] * 5, dict(weights=True)),  # clusters of two, and of four
+    (14, 2, 64, "f32", 16, [400, 33, 500] * 15, dict(weights=True, window=300)),
+    (8, 1, 256, "f16", 16, [400, 33, 500] * 15, {}),
+    (10, 2, 80, "f32", 8, [1000, 90, 0, 64] * 5, dict(weights=True, out="bf16")),
+    (20, 4, 128, "f32", 16, [400, 33, 250] * 5, {}),
+    (12, 1, 64, "f16", 16, [900, 33, 250] * 10, {}),
     (14, 2, 64, "f32", 8, [(37 * i) % 90 for i in range(400)], dict(window=50)),
     (5, 1, 256, "f16", 16, [16, 100, 1] * 150, {}),
 ], ids=short)
