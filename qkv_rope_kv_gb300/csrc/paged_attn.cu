@@ -402,6 +402,10 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     if (p.hd < HD)
         for (int i = lane * 16; i < S::kRingBytes; i += 512) *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
 
+    // lengths and page ids on their way to L2 while the launch before this one ends
+    const int64_t line = static_cast<int64_t>(blockIdx.x) * S::kThreads + tid;
+    if (line * 32 < B) prefetch_l2(p.lens + line * 32);
+    if (line * 32 < static_cast<int64_t>(B) * p.c.max_pages) prefetch_l2(p.c.table + line * 32);
     griddep_wait();
     griddep_launch_dependents();  // what follows may take the places of CTAs that are done, and wait there
     // How much there is: units, sequences that have any, and the longest item.  Every warp finds it for

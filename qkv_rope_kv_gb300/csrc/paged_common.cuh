@@ -43,6 +43,9 @@ __device__ __forceinline__ int64_t row_offset(const PagedView& c, int seq, int s
     return row_offset(c, page_ref(c, seq, slot));
 }
 
+// Ask for the line that holds *p.  Only L2 takes it, so this may come before what writes there has ended.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Length of sequence b, or 0 (and the status flag) where it is outside [0, capacity].
 __device__ __forceinline__ int checked_len(const PagedView& c, const int32_t* lens, int b) {
     const int n = lens[b];

@@ -9,7 +9,7 @@
 // Two launches: one finds the moves (one or more CTAs per item, bound by their chain of barriers and
 // cluster exchanges), one makes them with the whole GPU (bound by the latency of list, table and
 // row, or by memory); a single one where items have little to move.  Measured (GPU time): 8 sequences x 8
-// heads, 2112 -> 2048 slots 11.0 us; 1 x 4, 32749 -> 8192 24.1 us; 32 x 2, to 4099 -> 1000 20.9 us (the bytes
+// heads, 2112 -> 2048 slots 10.8 us; 1 x 4, 32749 -> 8192 23.1 us; 32 x 2, to 4099 -> 1000 19.8 us (the bytes
 // would take 0.9, 4.0 and 5.6 us).  256 threads instead of 1024: 14.8 us for the first kernel where 1024 take
 // 9.3; both in one launch for the prompt: 30 us.
 #include <algorithm>
@@ -26,6 +26,7 @@ constexpr int kBins = 2048, kPasses = 3;               // digits of 11, 11 and 1
 constexpr int kFixedSmem = (kPasses + 1) * kBins * 4;  // a histogram a digit and the cluster's sum of one
 constexpr int kMaxCluster = 16;
 constexpr int64_t kOwnMoveBytes = 128 * 1024;
+constexpr int64_t kPrefetchBytes = 4 * 1024 * 1024;
 constexpr uint32_t kCountEverywhere = 4096;            // keys left from which on a digit needs no exchange (24.9 -> 24.1 us)
 constexpr int64_t kMaxSlots = 48 * 1024;               // slots of a CTA whose keys fit in shared memory
 constexpr int64_t kClusterSlots = 4096;                // slots of a CTA of a cluster
@@ -167,6 +168,18 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
     const int b = item / p.nkv, h = item - b * p.nkv;
     const int cap = p.c.max_pages * p.c.page_size;
     for (int i = tid; i < kPasses * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    const int64_t base = static_cast<int64_t>(item) * cap;
+    // Lengths, weights and positions on their way to L2 while the launch before this one ends: of all slots, or if
+    // that is much (0.6 us of bandwidth), of those likely to be in use.  32 sequences x 2 heads to 4099 slots
+    // 20.9 -> 19.8 us, with the likely ones alone 20.6.
+    const bool few = static_cast<int64_t>(p.c.n_seq) * p.nkv * cap * 8 <= kPrefetchBytes;
+    const int64_t likely = few ? cap : min(static_cast<int64_t>(cap), 2 * static_cast<int64_t>(p.budget));
+    if (rank == 0 && tid == 0) prefetch_l2(p.lens + b);
+    if (rank == 0 && tid == 32) prefetch_l2(p.next_pos + b);
+    for (int64_t s = (rank * kThreads + tid) * 32; s < likely; s += size * kThreads * 32) {
+        prefetch_l2(p.c.slot_weight + base + s);
+        prefetch_l2(p.c.slot_pos + base + s);
+    }
     qkv_ptx::griddep_wait();
     qkv_ptx::griddep_launch_dependents();
     const int len = p.lens[b];
@@ -180,7 +193,6 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
         if (!sane || len <= p.budget) p.moves[item] = 0;
     }
     if (!sane) return;
-    const int64_t base = static_cast<int64_t>(item) * cap;
     const float* w_in = p.c.slot_weight + base;
     const int32_t* pos_in = p.c.slot_pos + base;
     float* w_out = p.weight_out + base;
