@@ -33,6 +33,9 @@ constexpr int64_t kClusterSlots = 4096;                // slots of a CTA of a cl
 static_assert(2 * kClusterSlots <= kMaxSlots, "a CTA that is alone holds its keys");
 static_assert(kFixedSmem >= kThreads * 16, "a batch of moves fits the histograms' place");
 
+// Slots of a CTA that is alone, as its keys are kept: whole rounds of its threads.
+__host__ __device__ constexpr int64_t cap_slots(int64_t cap) { return (cap + kThreads - 1) / kThreads * kThreads; }
+
 // Order-preserving key of a slot: protected slots above everything, NaN above every number.
 __device__ __forceinline__ uint32_t slot_key(float w, int pos, int64_t protect_from) {
     if (pos >= protect_from) return 0xffffffffu;
@@ -89,17 +92,15 @@ __device__ __forceinline__ void count_bin(uint32_t* hist, uint32_t bin, bool in,
 }
 
 // Make an item's moves chunk, chunk + chunks, ... (which they are does not depend on how many there are, so the
-// list is read together with its length).  A thread looks up a move's rows and carries its weight and position;
+// list is read together with its length; LISTED: it is in shared memory, `known` long).  A thread looks up a move's rows and carries its weight and position;
 // then all threads copy the rows of K and V, CT by CT, kUnroll of them in flight.  to_s and from_s: THREADS
 // entries of shared memory.
-template <typename CT, int THREADS, int kUnroll>
+template <typename CT, int THREADS, int kUnroll, bool LISTED>
 __device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, int chunk, int chunks, int64_t* to_s,
-                                           int64_t* from_s) {
+                                           int64_t* from_s, const int32_t* holes, const int32_t* movers, int known) {
     const int b = item / p.nkv, h = item - b * p.nkv, tid = threadIdx.x;
     const int cap = p.c.max_pages * p.c.page_size;
     const int64_t base = static_cast<int64_t>(item) * cap;
-    const int32_t* holes = p.lists + static_cast<int64_t>(item) * 2 * (cap / 2);
-    const int32_t* movers = holes + cap / 2;
     const int row_units = p.hd * (p.kv_f16 ? 2 : 4) / static_cast<int>(sizeof(CT));
     const int elem_per_unit = static_cast<int>(sizeof(CT)) / (p.kv_f16 ? 2 : 4);
     CT* kp = static_cast<CT*>(p.c.k);
@@ -107,9 +108,10 @@ __device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, 
 #pragma unroll 1
     for (int64_t p0 = chunk;; p0 += static_cast<int64_t>(THREADS) * chunks) {
         const int64_t at = p0 + static_cast<int64_t>(tid) * chunks;
-        const bool could = at < cap / 2;
-        const int to = could ? __ldcg(holes + at) : 0, from = could ? __ldcg(movers + at) : 0;
-        const int pairs = __ldcg(p.moves + item);
+        const bool could = at < (LISTED ? known : cap / 2);
+        const int to = could ? (LISTED ? holes[at] : __ldcg(holes + at)) : 0;
+        const int from = could ? (LISTED ? movers[at] : __ldcg(movers + at)) : 0;
+        const int pairs = LISTED ? known : __ldcg(p.moves + item);
         if (p0 >= pairs) break;
         const int n = static_cast<int>(min(static_cast<int64_t>(THREADS), (pairs - p0 + chunks - 1) / chunks));
         if (tid < n) {
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
             if (!sane) flag_bad(kFlagIndexRange, len);
             p.lens_out[b] = sane ? min(len, p.budget) : len;
         }
-        if (!sane || len <= p.budget) p.moves[item] = 0;
+        if (!MOVES && (!sane || len <= p.budget)) p.moves[item] = 0;
     }
     if (!sane) return;
     const float* w_in = p.c.slot_weight + base;
@@ -305,8 +307,10 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
                                                   (lane < warp ? warp2_s[lane] : 0u));
         __syncthreads();
     }
-    int32_t* holes = p.lists + static_cast<int64_t>(item) * 2 * (cap / 2);
+    // MOVES: the lists stay here, behind the place of make_moves' rows
+    int32_t* holes = MOVES ? reinterpret_cast<int32_t*>(keys + cap_slots(cap)) : p.lists + static_cast<int64_t>(item) * 2 * (cap / 2);
     int32_t* movers = holes + cap / 2;
+    int pairs = 0;
     uint32_t hole0 = 0u, mover0 = 0u;
     const bool copy_meta = w_out != w_in || pos_out != pos_in;
 #pragma unroll 1
@@ -355,7 +359,8 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
             const uint32_t nh = lane < size ? peer_word(publish_s + 1, lane, size) : 0u;
             const uint32_t nm = lane < size ? peer_word(publish_s + 2, lane, size) : 0u;
             const uint32_t all = __reduce_add_sync(0xffffffffu, nh);
-            if (rank == 0 && tid == 0) p.moves[item] = static_cast<int32_t>(all);
+            pairs = static_cast<int>(all);
+            if (!MOVES && rank == 0 && tid == 0) p.moves[item] = pairs;
             hole0 = __reduce_add_sync(0xffffffffu, (lane < rank ? nh : 0u) + (lane < warp ? warp_s[lane] : 0u));
             mover0 = __reduce_add_sync(0xffffffffu, (lane < rank ? nm : 0u) + (lane < warp ? warp2_s[lane] : 0u));
         }
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
     if constexpr (MOVES) {
         __syncthreads();  // the list is written, and the histograms have been read
         int64_t* to_s = reinterpret_cast<int64_t*>(smem);
-        make_moves<uint4, kThreads, 4>(p, item, 0, 1, to_s, to_s + kThreads);
+        make_moves<uint4, kThreads, 4, true>(p, item, 0, 1, to_s, to_s + kThreads, holes, movers, pairs);
     } else {
         if (size > 1) cluster_sync(size);  // no CTA leaves while another may read its shared memory
     }
@@ -378,8 +383,9 @@ __global__ void __launch_bounds__(kMoveThreads) paged_evict_move_kernel(const __
     __shared__ int64_t to_s[kMoveThreads], from_s[kMoveThreads];
     qkv_ptx::griddep_wait();
     qkv_ptx::griddep_launch_dependents();
-    const int item = blockIdx.x / chunks;
-    make_moves<CT, kMoveThreads, 8>(p, item, blockIdx.x - item * chunks, chunks, to_s, from_s);
+    const int item = blockIdx.x / chunks, half = p.c.max_pages * p.c.page_size / 2;
+    const int32_t* holes = p.lists + static_cast<int64_t>(item) * 2 * half;
+    make_moves<CT, kMoveThreads, 8, false>(p, item, blockIdx.x - item * chunks, chunks, to_s, from_s, holes, holes + half, 0);
 }
 
 template <typename CT>
@@ -416,7 +422,7 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
                   : size == 1 ? paged_evict_select_kernel<true, false, true>  // 2 kClusterSlots < kMaxSlots
                   : cached    ? paged_evict_select_kernel<true, false, false>
                               : paged_evict_select_kernel<false, false, false>;
-    const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(slots) * 4 : 0);
+    const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(slots) * 4 : 0) + (moves ? static_cast<size_t>(cap / 2) * 8 : 0);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)
