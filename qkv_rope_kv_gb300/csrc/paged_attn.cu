@@ -1066,7 +1066,6 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
-    if constexpr (CLUSTERED) return;
     // Join what this CTA was the last to complete: groups of neighbouring parts first, then the groups
     // (one group where the parts are few).
 #pragma unroll 1

@@ -9,7 +9,7 @@
 // Two launches: one finds the moves (one or more CTAs per item, bound by their chain of barriers and
 // cluster exchanges), one makes them with the whole GPU (bound by the latency of list, table and
 // row, or by memory); a single one where items have little to move.  Measured (GPU time): 8 sequences x 8
-// heads, 2112 -> 2048 slots 10.8 us; 1 x 4, 32749 -> 8192 23.1 us; 32 x 2, to 4099 -> 1000 19.8 us (the bytes
+// heads, 2112 -> 2048 slots 9.9 us; 1 x 4, 32749 -> 8192 23.1 us; 32 x 2, to 4099 -> 1000 19.8 us (the bytes
 // would take 0.9, 4.0 and 5.6 us).  256 threads instead of 1024: 14.8 us for the first kernel where 1024 take
 // 9.3; both in one launch for the prompt: 30 us.
 #include <algorithm>
@@ -21,7 +21,7 @@ namespace {
 
 using namespace qkv_paged;
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kThreads = 1024;
 constexpr int kBins = 2048, kPasses = 3;               // digits of 11, 11 and 10 bits
 constexpr int kFixedSmem = (kPasses + 1) * kBins * 4;  // a histogram a digit and the cluster's sum of one
 constexpr int kMaxCluster = 16;
@@ -153,23 +153,24 @@ __device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, 
 // keys are kept in shared memory; otherwise they are made again each time.  ALONE: a cluster is one CTA
 // (11.0 us; 11.8 us where the kernel has to ask).  MOVES (alone, rows of whole 16 bytes): it makes its
 // moves too.
-template <bool CACHED, bool MOVES, bool ALONE>
-__global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p,
+template <bool CACHED, bool MOVES, bool ALONE, int T>
+__global__ void __launch_bounds__(T, kThreads / T) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p,
                                                                       int cluster) {
     static_assert(ALONE || !MOVES, "a cluster's moves are made by the second kernel");
     const int size = ALONE ? 1 : cluster;
+    constexpr int W = T / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem);
     uint32_t* sum = hist + kPasses * kBins;
     uint32_t* keys = reinterpret_cast<uint32_t*>(smem + kFixedSmem);
-    __shared__ uint32_t warp_s[kWarps], warp2_s[kWarps];
+    __shared__ uint32_t warp_s[W], warp2_s[W];
     __shared__ uint32_t found_s[3];  // bin, keys still wanted from it, keys in it
     __shared__ uint32_t publish_s[3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int item = blockIdx.x / size, rank = blockIdx.x - item * size;
     const int b = item / p.nkv, h = item - b * p.nkv;
     const int cap = p.c.max_pages * p.c.page_size;
-    for (int i = tid; i < kPasses * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kPasses * kBins / 4; i += T) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     const int64_t base = static_cast<int64_t>(item) * cap;
     // Lengths, weights and positions on their way to L2 while the launch before this one ends: of all slots, or if
     // that is much (0.6 us of bandwidth), of those likely to be in use.  32 sequences x 2 heads to 4099 slots
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
     const int64_t likely = few ? cap : min(static_cast<int64_t>(cap), 2 * static_cast<int64_t>(p.budget));
     if (rank == 0 && tid == 0) prefetch_l2(p.lens + b);
     if (rank == 0 && tid == 32) prefetch_l2(p.next_pos + b);
-    for (int64_t s = (rank * kThreads + tid) * 32; s < likely; s += size * kThreads * 32) {
+    for (int64_t s = (rank * T + tid) * 32; s < likely; s += size * T * 32) {
         prefetch_l2(p.c.slot_weight + base + s);
         prefetch_l2(p.c.slot_pos + base + s);
     }
@@ -200,15 +201,15 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
     float* w_out = p.weight_out + base;
     int32_t* pos_out = p.pos_out + base;
     if (len <= p.budget) {
-        for (int s = rank * kThreads + tid; s < len; s += size * kThreads) {
+        for (int s = rank * T + tid; s < len; s += size * T) {
             w_out[s] = w_in[s];
             pos_out[s] = pos_in[s];
         }
         return;
     }
     const int64_t protect_from = static_cast<int64_t>(next_pos) - p.recent;
-    const int run = (len + size * kThreads - 1) / (size * kThreads) * 32;  // slots of a warp
-    const int s0 = (rank * kWarps + warp) * run;
+    const int run = (len + size * T - 1) / (size * T) * 32;  // slots of a warp
+    const int s0 = (rank * W + warp) * run;
     const int mine = max(0, min(run, len - s0));
     uint32_t* my_keys = keys + warp * run;
     auto key_of = [&](int i) -> uint32_t {  // i-th slot of this warp
@@ -244,10 +245,10 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
             __syncthreads();
         } else if (everywhere) {
             cluster_sync(size);
-        } else {
+        } else if constexpr (!ALONE) {
             // each CTA adds up its share of the bins over the cluster and hands the sums to every CTA
             cluster_sync(size);
-            const int each = kBins / size, per = kThreads / each;  // bins of a CTA; threads of a bin
+            const int each = kBins / size, per = T / each;  // bins of a CTA; threads of a bin
             const int bin = rank * each + tid / per, part = tid % per;
             uint32_t c = 0u;
             for (int r = part; r < size; r += per) c += peer_word(my_hist + bin, r, size);
@@ -257,12 +258,23 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
             cluster_sync(size);
             bins = sum;
         }
-        // thread t: bins 2047 - 2t and 2046 - 2t, so that a scan runs from the largest key down
-        constexpr int kMine = kBins / kThreads;
-        static_assert(kMine == 2, "two bins a thread");
-        const uint2 two = *reinterpret_cast<const uint2*>(bins + kBins - 2 - 2 * tid);
-        const uint32_t c[kMine] = {two.y, two.x};
-        uint32_t incl = two.x + two.y;
+        // thread t: its share of the bins from the top one down, so that a scan runs from the largest key down
+        constexpr int kMine = kBins / T;
+        static_assert(kMine == 2 || kMine == 4, "one load a thread");
+        uint32_t c[kMine], incl = 0u;
+        if constexpr (kMine == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(bins + kBins - 2 - 2 * tid);
+            c[0] = v.y;
+            c[1] = v.x;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(bins + kBins - 4 - 4 * tid);
+            c[0] = v.w;
+            c[1] = v.z;
+            c[2] = v.y;
+            c[3] = v.x;
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) incl += c[i];
         const uint32_t total = incl;
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
         if (lane == 0) warp2_s[warp] = n;
         __syncthreads();
         if (warp == 0) {
-            n = __reduce_add_sync(0xffffffffu, warp2_s[lane]);
+            n = __reduce_add_sync(0xffffffffu, lane < W ? warp2_s[lane] : 0u);
             if (lane == 0) publish_s[0] = n;
         }
         cluster_sync(size);
@@ -348,8 +360,8 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
             }
             __syncthreads();
             if (warp == 0) {
-                const uint32_t h_all = __reduce_add_sync(0xffffffffu, warp_s[lane]);
-                const uint32_t m_all = __reduce_add_sync(0xffffffffu, warp2_s[lane]);
+                const uint32_t h_all = __reduce_add_sync(0xffffffffu, lane < W ? warp_s[lane] : 0u);
+                const uint32_t m_all = __reduce_add_sync(0xffffffffu, lane < W ? warp2_s[lane] : 0u);
                 if (lane == 0) {
                     publish_s[1] = h_all;
                     publish_s[2] = m_all;
@@ -368,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const __gr
     if constexpr (MOVES) {
         __syncthreads();  // the list is written, and the histograms have been read
         int64_t* to_s = reinterpret_cast<int64_t*>(smem);
-        make_moves<uint4, kThreads, 4, true>(p, item, 0, 1, to_s, to_s + kThreads, holes, movers, pairs);
+        make_moves<uint4, T, 4, true>(p, item, 0, 1, to_s, to_s + T, holes, movers, pairs);
     } else {
         if (size > 1) cluster_sync(size);  // no CTA leaves while another may read its shared memory
     }
@@ -418,15 +430,21 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
     // a second launch would), or no item has anything to move.
     const int64_t most = std::max<int64_t>(0, std::min<int64_t>(p.budget, cap - p.budget));
     const bool moves = size == 1 && cached && whole16 && most * 2 * p.hd * es <= kOwnMoveBytes;
-    auto kernel = moves       ? paged_evict_select_kernel<true, true, true>
-                  : size == 1 ? paged_evict_select_kernel<true, false, true>  // 2 kClusterSlots < kMaxSlots
-                  : cached    ? paged_evict_select_kernel<true, false, false>
-                              : paged_evict_select_kernel<false, false, false>;
+    // A CTA of 1024 threads has an SM to itself: with more items than SMs, half the threads (8 heads x 128 x f16,
+    // 32 sequences 600 -> 550 slots 14.5 us with 1024, 9.6 us with 512; 2112 -> 2048 22.0 and 16.7 us).
+    const bool halves = items > kSms;
+    const int threads = size == 1 && halves ? kThreads / 2 : kThreads;
+    auto kernel = moves       ? (halves ? paged_evict_select_kernel<true, true, true, kThreads / 2>
+                                        : paged_evict_select_kernel<true, true, true, kThreads>)
+                  : size == 1 ? (halves ? paged_evict_select_kernel<true, false, true, kThreads / 2>
+                                        : paged_evict_select_kernel<true, false, true, kThreads>)
+                  : cached    ? paged_evict_select_kernel<true, false, false, kThreads>
+                              : paged_evict_select_kernel<false, false, false, kThreads>;
     const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(slots) * 4 : 0) + (moves ? static_cast<size_t>(cap / 2) * 8 : 0);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)
-        e = launch_dependent(kernel, dim3(static_cast<unsigned int>(items) * size), kThreads, smem, stream, size, p, size);
+        e = launch_dependent(kernel, dim3(static_cast<unsigned int>(items) * size), threads, smem, stream, size, p, size);
     if (e != cudaSuccess || moves || most == 0) return e;
     if (whole16) return launch_move<uint4>(p, most, stream);
     return p.kv_f16 ? launch_move<uint16_t>(p, most, stream) : launch_move<uint32_t>(p, most, stream);

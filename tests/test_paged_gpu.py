@@ -495,6 +495,9 @@ def wild(rng, shape):
     (160, 2, "f32", 64, [130, 2000], 1500, 0, heavy, dict(max_pages=520, inplace=True)),  # keys made again
     (1, 2, "f16", 256, [3001], 2000, 7, tied, dict(max_pages=2100)),
     (1, 2, "f32", 256, [3001], 11, 7, heavy, dict(max_pages=2100, inplace=True)),
+    (8, 128, "f16", 16, [600, 550, 551, 33] * 8, 550, 50, tied, dict(inplace=True)),     # more items than SMs
+    (8, 64, "f32", 32, [2112, 1999, 2048] * 8, 1000, 100, heavy, {}),
+    (8, 16, "f16", 16, [1025, 1024, 1023, 513, 2] * 5, 512, 0, wild, {}),
 ], ids=short)
 def test_evict(qkv, nkv, hd, kv, page, lens, budget, recent, weights, kw):
     run_evict(nkv, hd, kv, page, lens, budget, recent, weights, **kw)
