@@ -477,7 +477,7 @@ qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
  * A sequence of length 0 gets zeros (lse -inf).  Needs n_head % n_head_kv == 0.
  * Scores, softmax and sums are f32.  q and the softmax weights are split in two f16 (f16 cache) or
  * tf32 (f32 cache) parts for the tensor cores, an f32 cache's rows too: about 22 bits of each.
- * The length is split over the GPU and joined in the order of the slots: results do not depend on
+ * The length is split over the GPU and joined in a fixed order: results do not depend on
  * timing.  The workspace must be zero before the first call and belongs to calls that do not overlap
  * on the GPU (one stream, or graphs replayed one after the other); every completed call leaves it
  * usable for the next, of any shape that needs no more bytes.
