@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // an mma.sync has 16, all in use here, and its pipe is 13 to 17 % busy.
 // Measured (GPU time, of the copy rate): 64 sequences of 8 x 128 x f16 to 8192 slots 184 us, DRAM at 6.2 TB/s
 // (0.92); one of 32749 slots 29 us (0.68: about 9 us of it are launch, lengths, first pages and the join);
-// 32 to 4099 slots with weights 40.7 us; 14 x 64 x f32, 509 slots 6.1 us, all latency.
+// 32 to 4099 slots with weights 40.2 us; 14 x 64 x f32, 509 slots 6.1 us, all latency.
 //
 // Work is counted in units of 8 to 32 neighbouring slots of one item (8 KB of K and V as a rule), an item
 // being (sequence, kv head, block of up to 8 of its q heads).  Lengths are on the device, so every CTA finds

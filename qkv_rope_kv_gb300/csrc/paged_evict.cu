@@ -9,7 +9,7 @@
 // Two launches: one finds the moves (one or more CTAs per item, bound by their chain of barriers and
 // cluster exchanges), one makes them with the whole GPU (bound by the latency of list, table and
 // row, or by memory); a single one where items have little to move.  Measured (GPU time): 8 sequences x 8
-// heads, 2112 -> 2048 slots 9.9 us; 1 x 4, 32749 -> 8192 23.1 us; 32 x 2, to 4099 -> 1000 19.8 us (the bytes
+// heads, 2112 -> 2048 slots 9.9 us; 1 x 4, 32749 -> 8192 22.6 us; 32 x 2, to 4099 -> 1000 18.5 us (the bytes
 // would take 0.9, 4.0 and 5.6 us).  256 threads instead of 1024: 14.8 us for the first kernel where 1024 take
 // 9.3; both in one launch for the prompt: 30 us.
 #include <algorithm>
@@ -103,6 +103,8 @@ __device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, 
     const int64_t base = static_cast<int64_t>(item) * cap;
     const int row_units = p.hd * (p.kv_f16 ? 2 : 4) / static_cast<int>(sizeof(CT));
     const int elem_per_unit = static_cast<int>(sizeof(CT)) / (p.kv_f16 ? 2 : 4);
+    const int i0 = tid / (2 * row_units), c0 = tid - i0 * 2 * row_units;
+    const int step_i = THREADS / (2 * row_units), step_c = THREADS - step_i * 2 * row_units;
     CT* kp = static_cast<CT*>(p.c.k);
     CT* vp = static_cast<CT*>(p.c.v);
 #pragma unroll 1
@@ -126,19 +128,25 @@ __device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, 
             p.pos_out[base + to] = pos;
         }
         __syncthreads();
-        const int total = n * 2 * row_units;
+        // unit c of move i, and on by THREADS units a step
+        int i = i0, c = c0;
 #pragma unroll 1
-        for (int e0 = tid; e0 < total; e0 += THREADS * kUnroll) {
+        while (i < n) {
             CT v[kUnroll];
             CT* dst[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int e = e0 + u * THREADS, i = e / (2 * row_units), c = e - i * 2 * row_units;
                 dst[u] = nullptr;
-                if (e < total && to_s[i] >= 0) {
+                if (i < n && to_s[i] >= 0) {
                     CT* pool = c < row_units ? kp + c : vp + (c - row_units);
                     dst[u] = pool + to_s[i];
                     v[u] = pool[from_s[i]];
+                }
+                i += step_i;
+                c += step_c;
+                if (c >= 2 * row_units) {
+                    c -= 2 * row_units;
+                    ++i;
                 }
             }
 #pragma unroll
@@ -380,7 +388,7 @@ __global__ void __launch_bounds__(T, kThreads / T) paged_evict_select_kernel(con
     if constexpr (MOVES) {
         __syncthreads();  // the list is written, and the histograms have been read
         int64_t* to_s = reinterpret_cast<int64_t*>(smem);
-        make_moves<uint4, T, 4, true>(p, item, 0, 1, to_s, to_s + T, holes, movers, pairs);
+        make_moves<uint4, T, T == kThreads ? 2 : 4, true>(p, item, 0, 1, to_s, to_s + T, holes, movers, pairs);
     } else {
         if (size > 1) cluster_sync(size);  // no CTA leaves while another may read its shared memory
     }
