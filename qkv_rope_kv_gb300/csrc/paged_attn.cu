@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // rows are split too (two MMAs).  Before the split q is scaled by a power of two into [2^13, 2^14),
 // and the weights are 2^(s - m + 12) with m at most 3 below the running maximum (then O need not be
 // rescaled for every new maximum), both far from f16's ends.  Sums over many MMAs are made outside of them,
-// rounded to nearest (add4): 20 x 6000 slots x 8 x 128 x f32 come out 9.5e-7 off (2-norms) instead of 6.1e-6,
+// rounded to nearest (add4): 20 x 6000 slots x 8 x 128 x f32 come out 6.2e-7 off (2-norms) instead of 6.1e-6,
 // f16 5e-7 instead of 2.3e-6, at the same times (an f32 batch: 3 % more).
 
 constexpr int kMinShare = 8;     // units
@@ -303,7 +303,7 @@ __device__ __forceinline__ void split_tf32(float a, uint32_t& hi, uint32_t& lo) 
     lo = (__float_as_uint(a - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
 }
 // The same for cache values, cut off (rounding them costs 4 % of a batch's time and takes a third off an error
-// that is a plain f32 sum's already): an infinite one has no remainder (inf - inf is NaN, which max drops).
+// that is below a plain f32 sum's already): an infinite one has no remainder (inf - inf is NaN, which max drops).
 __device__ __forceinline__ void split_tf32_kv(float a, uint32_t& hi, uint32_t& lo) {
     hi = __float_as_uint(a) & 0xffffe000u;
     lo = __float_as_uint(fmaxf(a - __uint_as_float(hi), -1e30f)) & 0xffffe000u;
@@ -771,10 +771,10 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) split_tf32_kv(r[i], hi[i], lo[i]);
                         float sum[4] = {};
+                        mma_tf32(sum, a, lo[0], lo[1]);  // the small products first, as nothing is cut off them
+                        mma_tf32(sum, a + 4, lo[2], lo[3]);
                         mma_tf32(sum, a, hi[0], hi[1]);
                         mma_tf32(sum, a + 4, hi[2], hi[3]);
-                        mma_tf32(sum, a, lo[0], lo[1]);
-                        mma_tf32(sum, a + 4, lo[2], lo[3]);
                         add4(c[j], sum);
                     }
                 }
@@ -849,8 +849,8 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                             split_tf32_kv(r0[i], h0r, l0r);
                             split_tf32_kv(r1[i], h1r, l1r);
                             float tile[4] = {};
-                            mma_tf32(tile, pa, h0r, h1r);
                             mma_tf32(tile, pa, l0r, l1r);
+                            mma_tf32(tile, pa, h0r, h1r);
                             add4(O[4 * s + i], tile);
                         }
                     }
