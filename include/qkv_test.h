@@ -1,5 +1,5 @@
 /* Test hooks of libqkv.so: the device-side failure paths of the decode and
- * prefill kernels.
+ * prefill kernels, and the grid of the paged attention.
  *
  * Not part of the stage.  Every wait of a decode or prefill kernel on a pipeline
  * or exchange barrier is bounded (0.5 s); when it runs out the kernel sets bit 1
@@ -46,6 +46,12 @@ qkv_status qkv_test_decode_wait_timeout(const qkv_plan* plan, const float* x, co
 qkv_status qkv_test_prefill_xchg_timeout(const qkv_plan* plan, const uint16_t* X, int32_t nt, const void* w,
                                          const float* bias, const int32_t* d_positions, float* Y, void* kv_k,
                                          void* kv_v, uint32_t wait_limit_us, void* stream);
+
+/* The grid that qkv_attn_step launches its main kernel on for this plan and cache: CTAs in all, and
+ * CTAs of a cluster (1: none).  The order of the sums follows from it, so it depends on sizes and
+ * alignment alone, and needs no device.
+ * Errors: INVALID_ARG, UNSUPPORTED. */
+qkv_status qkv_test_attn_grid(const qkv_plan* plan, const qkv_paged_kv* cache, int32_t* ctas, int32_t* cluster);
 
 #ifdef __cplusplus
 }

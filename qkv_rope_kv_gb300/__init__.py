@@ -21,7 +21,7 @@ import threading
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqkv.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "qkv.h")
-# every header of the C ABI: the stage (qkv.h) and the test hook of its failure path (qkv_test.h)
+# every header of the C ABI: the stage (qkv.h) and the test hooks (qkv_test.h)
 HEADERS = (HEADER, os.path.join(os.path.dirname(_HERE), "include", "qkv_test.h"))
 
 # ---- constants mirrored from include/qkv.h ----
@@ -157,6 +157,7 @@ def _declare(lib):
         "qkv_model_graph_destroy": ([vp], None),
         "qkv_check_device_error": ([vp, ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(i32)], st),
         "qkv_test_decode_wait_timeout": ([vp] * 10 + [ctypes.c_uint32, vp], st),
+        "qkv_test_attn_grid": ([vp, vp, ctypes.POINTER(i32), ctypes.POINTER(i32)], st),
         "qkv_test_prefill_xchg_timeout": ([vp, vp, ctypes.c_int32] + [vp] * 6 + [ctypes.c_uint32, vp], st),
     }
     for name, (args, res) in sig.items():

@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "qkv_internal.h"
+#include "qkv_test.h"
 
 namespace {
 
@@ -195,6 +196,23 @@ extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* ca
     p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
     const cudaError_t e = launch_paged_attn(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
+    return QKV_OK;
+}
+
+// Test hook (include/qkv_test.h).
+extern "C" qkv_status qkv_test_attn_grid(const qkv_plan* plan, const qkv_paged_kv* cache, int32_t* ctas,
+                                         int32_t* cluster) {
+    PagedAttnParams p;
+    std::memset(&p, 0, sizeof p);
+    qkv_status st = view(plan, cache, &p.c);
+    if (st != QKV_OK) return st;
+    if (plan->d.n_head % plan->d.n_head_kv != 0) return api_fail(QKV_ERR_UNSUPPORTED, "uneven groups of q heads");
+    REQUIRE(ctas && cluster, "ctas or cluster is null");
+    p.nh = plan->d.n_head;
+    p.nkv = plan->d.n_head_kv;
+    p.hd = plan->d.head_dim;
+    p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
+    paged_attn_grid(p, ctas, cluster);
     return QKV_OK;
 }
 

@@ -6,8 +6,6 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
-#include <atomic>
-
 #include "paged_common.cuh"
 #include "ptx_sync.cuh"
 
@@ -191,6 +189,8 @@ constexpr float kLazy = 3.f;     // and may exceed that by 2^3 before the maximu
 
 template <typename KT, int HD>
 struct Split {
+    using Type = KT;
+    static constexpr int kHd = HD;
     static constexpr bool kF16 = sizeof(KT) == 2;
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
     static constexpr int kCtas = HD == 256 ? 1 : 2;        // per SM
@@ -1202,101 +1202,93 @@ __global__ void __launch_bounds__(kWeightThreads) paged_attn_weight_kernel(const
     griddep_launch_dependents();
 }
 
-template <typename KT, int HD, int C>
-cudaError_t launch_split_t(const PagedAttnParams& p, int most, int abreast, int serial, cudaStream_t stream) {
-    using S = Split<KT, HD>;
-    auto kernel = paged_attn_split_kernel<KT, HD, C>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return e;
-    const int grid = most / abreast * abreast * C;
-    return launch_dependent(kernel, dim3(grid), S::kThreads, S::kSmem, stream, C, p, abreast, serial);
+// How many clusters of the split kernel are launched at most: by the kernel's CTAs on an SM and the cluster's size.
+// Clusters need neighbouring SMs, and only a perfect packing holds as many as the occupancy query says: of 36
+// clusters of 8, a launch behind another kernel had 33 to 36 running at once, the rest after them (28/4 x 128 x f16,
+// 24000 slots: 25.7 us on 36 clusters, 18.5 on 32).  So these are 8/9 of what a GB300 holds (36, 74 and 152; with one
+// CTA an SM 15, 36 and 76), and constants: the split of the sums follows from them, and what the query says depends on
+// the device's layout and the process's limits.
+constexpr int sure_clusters(int ctas_per_sm, int size) {
+    return ctas_per_sm == 2 ? (size == 8 ? 32 : size == 4 ? 65 : 135) : (size == 8 ? 13 : size == 4 ? 32 : 67);
 }
 
-// How many clusters of the split kernel a device holds at a time (they need neighbouring SMs).  The same for
-// every context of a device, so it is asked for once.
-template <typename KT, int HD, int C>
-cudaError_t resident_clusters(int* out) {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<int> known[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-    using S = Split<KT, HD>;
-    auto kernel = paged_attn_split_kernel<KT, HD, C>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    // Only a perfect packing of the SMs holds that many: of 36, a launch behind another kernel had 33 to 36 running
-    // at once, the rest after them (28/4 x 128 x f16, 24000 slots: 25.7 us on 36 clusters, 18.5 on 32).
-    *out = *out * 8 / 9;
-    if (*out > kAttnMaxCtas / C) *out = kAttnMaxCtas / C;
-    if (dev < kMaxDevices) known[dev].store(*out, std::memory_order_relaxed);
-    return cudaSuccess;
-}
+struct Grid {
+    int ctas, cluster;    // CTAs in all, and of a cluster
+    int abreast, serial;  // blocks of q heads of a kv head: side by side, and one after another
+};
 
 // Clusters of C where every item can have two of them (C = 8), or one if sequences are short, and sequences can
 // be longer than what one CTA does as fast (6 units).  No more clusters than can have work.  28/4 x 128 x f16
 // without and with: one sequence of 64 slots 6.1 and 6.4 us, 500 10.1 and 6.8, 24000 21.1 and 18.5; six of 500
 // (C = 8) 10.6 and 8.1, ten of 400 (C = 4) 10.6 and 8.4, 25 of 400 (C = 2) 12.4 and 10.9; beyond the limits one
 // cluster an item loses: ragged 80 items to 1000 slots (C = 2) 12.4 and 15.4, 24 of 24000 (C = 8) 55 and 60.
-template <typename KT, int HD, int C>
-cudaError_t launch_clusters(const PagedAttnParams& p, int blocks, int abreast, int serial, cudaStream_t stream, bool* done) {
-    int clusters = 0;
-    const cudaError_t e = resident_clusters<KT, HD, C>(&clusters);
-    if (e != cudaSuccess) return e;
-    const int64_t units = static_cast<int64_t>(p.c.max_pages) * p.c.page_size / Split<KT, HD>::UK;  // of a full sequence
-    const int64_t items = static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks;
-    if (units < 6 || !((units <= (C == 8 ? 256 : 16 * C) && items <= clusters) || (C == 8 && items * 2 <= clusters)))
-        return cudaSuccess;
-    *done = true;
-    const int64_t useful = items * (units / (kMinShare * C) + 1);
-    return launch_split_t<KT, HD, C>(p, static_cast<int>(useful < clusters ? useful : clusters), abreast, serial, stream);
-}
-
-template <typename KT, int HD>
-cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
-    using S = Split<KT, HD>;
+template <typename S>
+Grid split_grid(const PagedAttnParams& p) {
     // Blocks of q heads that read the same rows go abreast, so that all but the first find them in L2 (12 q heads
     // to each of 8 kv heads of 128 x f16, 64 sequences of 8192 slots: 642 us as items of their own, 503 us abreast).
     // Above 64 q heads a kv head's blocks are items one after another.
     const int blocks = (p.nh / p.nkv + kAttnHeads - 1) / kAttnHeads;
     const int abreast = blocks <= kMaxAbreast ? blocks : 1, serial = blocks / abreast;
-    bool done = false;
-    cudaError_t e = launch_clusters<KT, HD, 8>(p, blocks, abreast, serial, stream, &done);
-    if (e == cudaSuccess && !done) e = launch_clusters<KT, HD, 4>(p, blocks, abreast, serial, stream, &done);
-    if (e == cudaSuccess && !done) e = launch_clusters<KT, HD, 2>(p, blocks, abreast, serial, stream, &done);
-    if (e != cudaSuccess || done) return e;
-    return launch_split_t<KT, HD, 1>(p, kSms * S::kCtas, abreast, serial, stream);
+    const int64_t units = static_cast<int64_t>(p.c.max_pages) * p.c.page_size / S::UK;  // of a full sequence
+    const int64_t items = static_cast<int64_t>(p.c.n_seq) * p.nkv * blocks;
+    for (int C = 8; C > 1 && units >= 6; C /= 2) {
+        const int clusters = sure_clusters(S::kCtas, C);
+        if (!((units <= (C == 8 ? 256 : 16 * C) && items <= clusters) || (C == 8 && items * 2 <= clusters))) continue;
+        const int64_t useful = items * (units / (kMinShare * C) + 1);
+        const int most = static_cast<int>(useful < clusters ? useful : clusters);
+        return {most / abreast * abreast * C, C, abreast, serial};
+    }
+    return {kSms * S::kCtas / abreast * abreast, 1, abreast, serial};
+}
+
+template <typename S, int C>
+cudaError_t launch_split_t(const PagedAttnParams& p, const Grid& g, cudaStream_t stream) {
+    auto kernel = paged_attn_split_kernel<typename S::Type, S::kHd, C>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(g.ctas), S::kThreads, S::kSmem, stream, C, p, g.abreast, g.serial);
+}
+
+template <typename S>
+cudaError_t launch_split(const PagedAttnParams& p, cudaStream_t stream) {
+    const Grid g = split_grid<S>(p);
+    switch (g.cluster) {
+        case 8: return launch_split_t<S, 8>(p, g, stream);
+        case 4: return launch_split_t<S, 4>(p, g, stream);
+        case 2: return launch_split_t<S, 2>(p, g, stream);
+        default: return launch_split_t<S, 1>(p, g, stream);
+    }
+}
+
+// fn of the split kernel's instance for the cache.
+template <typename Fn>
+auto with_split(const PagedAttnParams& p, Fn fn) {
+    if (p.kv_f16)
+        return p.hd <= 64 ? fn(Split<uint16_t, 64>()) : p.hd <= 128 ? fn(Split<uint16_t, 128>()) : fn(Split<uint16_t, 256>());
+    return p.hd <= 64 ? fn(Split<float, 64>()) : p.hd <= 128 ? fn(Split<float, 128>()) : fn(Split<float, 256>());
+}
+
+// Whether 16-byte copies can read the rows.
+bool rows_of_16(const PagedAttnParams& p) {
+    const int es = p.kv_f16 ? 2 : 4;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.c.k) | reinterpret_cast<uintptr_t>(p.c.v) |
+                           static_cast<uintptr_t>(p.c.page_stride * es) | static_cast<uintptr_t>(p.hd * es);
+    return (bits & 15u) == 0;
 }
 
 }  // namespace
 
+void paged_attn_grid(const PagedAttnParams& p, int* ctas, int* cluster) {
+    const Grid g = rows_of_16(p) ? with_split(p, [&](auto s) { return split_grid<decltype(s)>(p); })
+                                 : Grid{p.c.n_seq * p.nh, 1, 1, 1};
+    *ctas = g.ctas;
+    *cluster = g.cluster;
+}
+
 cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream) {
-    const int es = p.kv_f16 ? 2 : 4;
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.c.k) | reinterpret_cast<uintptr_t>(p.c.v) |
-                           static_cast<uintptr_t>(p.c.page_stride * es) | static_cast<uintptr_t>(p.hd * es);
-    cudaError_t e;
-    if ((bits & 15u) != 0) {  // rows that 16-byte copies cannot read
-        e = launch_dependent(paged_attn_any_kernel, dim3(p.c.n_seq * p.nh), kAnyThreads, 0, stream, 1, p);
-    } else if (p.kv_f16) {
-        e = p.hd <= 64 ? launch_split<uint16_t, 64>(p, stream)
-                       : p.hd <= 128 ? launch_split<uint16_t, 128>(p, stream) : launch_split<uint16_t, 256>(p, stream);
-    } else {
-        e = p.hd <= 64 ? launch_split<float, 64>(p, stream)
-                       : p.hd <= 128 ? launch_split<float, 128>(p, stream) : launch_split<float, 256>(p, stream);
-    }
+    const cudaError_t e =
+        rows_of_16(p) ? with_split(p, [&](auto s) { return launch_split<decltype(s)>(p, stream); })
+                      : launch_dependent(paged_attn_any_kernel, dim3(p.c.n_seq * p.nh), kAnyThreads, 0, stream, 1, p);
     if (e != cudaSuccess || !p.add_weight) return e;
     const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
     // a span for each CTA, up to 4096 CTAs or so; longer sequences loop

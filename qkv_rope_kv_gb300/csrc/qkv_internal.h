@@ -146,6 +146,8 @@ struct PagedAttnParams {
     int32_t nh, nkv, hd, kv_f16;
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
+// The main kernel's grid for these sizes (and pointers' alignment): CTAs, and CTAs of a cluster.
+void paged_attn_grid(const PagedAttnParams& p, int* ctas, int* cluster);
 cudaError_t paged_attn_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
 
 struct PagedEvictParams {
