@@ -303,10 +303,13 @@ __device__ __forceinline__ void split_tf32(float a, uint32_t& hi, uint32_t& lo) 
     lo = (__float_as_uint(a - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
 }
 // The same for cache values, cut off (rounding them costs 4 % of a batch's time and takes a third off an error
-// that is below a plain f32 sum's already): an infinite one has no remainder (inf - inf is NaN, which max drops).
+// that is below a plain f32 sum's already): an infinite one has no remainder (inf - inf is NaN, which gives way
+// to 0 as the larger magnitude; every other remainder keeps magnitude and sign).
 __device__ __forceinline__ void split_tf32_kv(float a, uint32_t& hi, uint32_t& lo) {
+    float rest;
     hi = __float_as_uint(a) & 0xffffe000u;
-    lo = __float_as_uint(fmaxf(a - __uint_as_float(hi), -1e30f)) & 0xffffe000u;
+    asm("max.xorsign.abs.f32 %0, %1, %2;" : "=f"(rest) : "f"(a - __uint_as_float(hi)), "f"(0.f));
+    lo = __float_as_uint(rest) & 0xffffe000u;
 }
 // The sum of a product's two halves; an infinite or NaN first half stands alone (the second is
 // then a product of the same infinity with a remainder of any sign).
