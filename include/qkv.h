@@ -476,7 +476,8 @@ qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
  *   out[b][h] = sum_j softmax(s)_j V[j],     lse[b][h] = log sum_j exp(s_j).
  * A sequence of length 0 gets zeros (lse -inf).  Needs n_head % n_head_kv == 0.
  * Scores, softmax and sums are f32.  q and the softmax weights are split in two f16 (f16 cache) or
- * tf32 (f32 cache) parts for the tensor cores, an f32 cache's rows too: about 22 bits of each.
+ * tf32 (f32 cache) parts for the tensor cores, an f32 cache's rows too: each is off by 2^-23 of
+ * itself at most, or (f16) by 2^-37 of the largest q element or softmax weight of its row.
  * The length is split over the GPU and joined in a fixed order: results do not depend on
  * timing.  The workspace must be zero before the first call and belongs to calls that do not overlap
  * on the GPU (one stream, or graphs replayed one after the other); every completed call leaves it

@@ -34,3 +34,62 @@ def test_attn_infinite_key_against_a_large_query(qkv, hd, pool_off, sign):
         c.k[c.row(0, 5)][3] = sign * np.inf
 
     base.run_attn(4, 2, hd, "f32", 16, [40, 90], change=change, pool_off=pool_off)
+
+
+@pytest.mark.parametrize("kv,hd,pool_off", [(kv, *x) for kv in ("f32", "f16") for x in LAYOUTS])
+def test_attn_of_one_slot_is_its_value(qkv, kv, hd, pool_off):
+    """One slot has weight 1, kept as a power of two: out is V, off by what the split of an f32 value may
+    lose, 2^-23 of it; an f16 value is exact."""
+    import torch
+    rng = np.random.default_rng(21)
+    n_seq, nh, nkv = 5, 6, 2
+    plan = base.make_plan(nh, nkv, hd, kv)
+    dt = torch.float16 if kv == "f16" else torch.float32
+    k, v = (torch.zeros(n_seq * 16 * nkv * hd + pool_off, dtype=dt, device="cuda")[pool_off:].view(n_seq, 16, nkv * hd)
+            for _ in range(2))
+    host = rng.standard_normal((2, n_seq, 16, nkv * hd)).astype(np.float32)
+    k.copy_(base.dev(host[0]))
+    v.copy_(base.dev(host[1]))
+    cache = base.Q.PagedKv(plan, k, v, torch.arange(n_seq, dtype=torch.int32, device="cuda").view(n_seq, 1))
+    ws = torch.zeros(base.Q.qkv_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+    q = base.dev(rng.standard_normal((n_seq, nh * hd)).astype(np.float32))
+    out = torch.empty(n_seq, nh * hd, device="cuda")
+    base.Q.qkv_attn_step(plan, cache, q, torch.ones(n_seq, dtype=torch.int32, device="cuda"), 0.1, out, ws)
+    want = v[:, 0].double().view(n_seq, nkv, 1, hd).expand(n_seq, nkv, nh // nkv, hd).reshape(n_seq, nh * hd)
+    bound = want.abs() * (2.0 ** -23 if kv == "f32" else 0.0)
+    assert ((out.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("kv", ["f32", "f16"])
+@pytest.mark.parametrize("n_seq,n", [(1, 6000), (4, 6000), (300, 1500)])
+def test_attn_error_over_long_rows(qkv, kv, n_seq, n):
+    """The 2-norm of the error, relative, over rows long enough for sums to lose bits.  With u = 2^-24, standard
+    normal K and V of head size 128 and q of twice that (scores of 2.9 in log2 terms), rms values:
+      scores: q scaled, q and K split 1.2 u of 2.9; eight blocks of columns, each a sum inside two MMAs that cut
+        up to 2 u off a value of 1: 4.5 u; eight additions to nearest 3.3 u; the two halves' sum 1.7 u;
+        the difference to the maximum (4 to 16 in size) 4 u: 8 u together, 5.6 u of a weight;
+      weights and values: 2^s 1.2 u, the two splits 0.7 u each: 5.9 u with the above.  Independent errors of
+        the weights are to the error of the sum as the weights are to the sum;
+      sums: a warp adds at most 6000 / 8 / 4 = 190 units to nearest: sqrt(190 / 2) 0.58 u = 5.7 u, and each
+        unit's own MMAs cut 1.4 u.
+    Together 8.3 u = 5e-7; the bound is twice that.  (Sums left to the MMAs come out at 2.3e-6 and 6.1e-6.)"""
+    import torch
+    nh, nkv, hd = 10, 2, 128
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    plan = base.make_plan(nh, nkv, hd, kv)
+    dt = torch.float16 if kv == "f16" else torch.float32
+    k, v = (torch.randn(n_seq, n, nkv * hd, generator=gen, device="cuda").to(dt) for _ in range(2))
+    q = 2.0 * torch.randn(n_seq, nh * hd, generator=gen, device="cuda")
+    cache = base.Q.PagedKv(plan, k, v, torch.arange(n_seq, dtype=torch.int32, device="cuda").view(n_seq, 1))
+    ws = torch.zeros(base.Q.qkv_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+    out = torch.empty(n_seq, nh * hd, device="cuda")
+    lens = torch.full((n_seq,), n, dtype=torch.int32, device="cuda")
+    base.Q.qkv_attn_step(plan, cache, q, lens, hd ** -0.5, out, ws)
+    off = size = 0.0
+    for b in range(n_seq):
+        K, V = (t[b].double().view(n, nkv, hd).transpose(0, 1) for t in (k, v))
+        p = torch.softmax(q[b].double().view(nkv, nh // nkv, hd) @ K.transpose(1, 2) * hd ** -0.5, -1)
+        want = (p @ V).reshape(-1)
+        off += (out[b].double() - want).square().sum().item()
+        size += want.square().sum().item()
+    assert (off / size) ** 0.5 <= 1e-6
