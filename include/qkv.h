@@ -478,6 +478,8 @@ qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
  * Scores, softmax and sums are f32.  q and the softmax weights are split in two f16 (f16 cache) or
  * tf32 (f32 cache) parts for the tensor cores, an f32 cache's rows too: each is off by 2^-23 of
  * itself at most, or (f16) by 2^-37 of the largest q element or softmax weight of its row.
+ * V is summed before the division by the weights' sum: |V| (f32) times the number of slots is to
+ * stay below the largest f32.
  * The length is split over the GPU and joined in a fixed order: results do not depend on
  * timing.  The workspace must be zero before the first call and belongs to calls that do not overlap
  * on the GPU (one stream, or graphs replayed one after the other); every completed call leaves it

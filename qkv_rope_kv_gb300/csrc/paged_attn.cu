@@ -172,9 +172,10 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // The 8 q heads of an item take half of the 16 rows of an MMA.  The other half carries what the
 // first loses: rows 0-7 hold q rounded to f16 (tf32), rows 8-15 the rounded remainder, and the same
 // with the softmax weights, so both products keep 23 bits at no extra MMA.  An f32 cache's own
-// rows are split too (two MMAs).  Before the split q is scaled by a power of two into [2^13, 2^14),
-// and the weights are 2^(s - m + 12) with m at most 3 below the running maximum (then O need not be
-// rescaled for every new maximum), both far from f16's ends.  Sums over many MMAs are made outside of them,
+// rows are split too (two MMAs).  The weights are 2^(s - m + shift) with m at most 3 below the running
+// maximum (then O need not be rescaled for every new maximum).  f16: before the split q is scaled by a power of
+// two into [2^13, 2^14), and the shift is 12, both far from the type's ends.  f32: the shift is -3, so no weight
+// is above 1 and O stays finite wherever sum p_j |V_j| does.  Sums over many MMAs are made outside of them,
 // rounded to nearest (add4): 20 x 6000 slots x 8 x 128 x f32 come out 6.2e-7 off (2-norms) instead of 6.1e-6,
 // f16 5e-7 instead of 2.3e-6, at the same times (an f32 batch: 3 % more).
 
@@ -184,8 +185,7 @@ constexpr int kJoinCost = 16;    // units
 constexpr int kOwnUnits = 8;     // how much larger the largest share may be with CTAs of its own for each item
 constexpr int kMaxAbreast = 8;   // blocks of q heads that go side by side
 constexpr int kJoinParts = 40;   // more parts than this are joined in two levels
-constexpr float kPShift = 12.f;  // weights are kept times 2^12
-constexpr float kLazy = 3.f;     // and may exceed that by 2^3 before the maximum moves
+constexpr float kLazy = 3.f;     // a weight may be 2^3 above the running maximum's before the maximum moves
 
 template <typename KT, int HD>
 struct Split {
@@ -208,6 +208,7 @@ struct Split {
     // in the loop (4 x 128 x f32, 32000 slots: 37 us, with fragments in registers 64)
     static constexpr bool kQRegs = kF16 && HD < 256;
     static constexpr bool kQAhead = kF16 ? HD < 256 : HD < 128;
+    static constexpr float kPShift = kF16 ? 12.f : -kLazy;  // weights are kept times 2^kPShift
     static constexpr int kMergeFloats = (kWarps - 1) * kAttnHeads * HD;  // O of the warps but the first
     static constexpr int kPartFloats = kAttnHeads * (HD + 2);
     static constexpr int kSmem = kWarps * kRingBytes +
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) O[n][i] *= keep;
             }
-            const float base = (m == -CUDART_INF_F ? 0.f : m) - kPShift;
+            const float base = (m == -CUDART_INF_F ? 0.f : m) - S::kPShift;
             float pr[2 * kST];
 #pragma unroll
             for (int i = 0; i < 2 * kST; ++i) {
@@ -918,7 +919,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                 const float mine = w < 2 ? (w == 0 ? v.x : v.y) : (w == 2 ? v.z : v.w);
                 if (h >= nheads) return;
                 if (col < p.hd) put_out(p, at.b, h0 + h, col, mine / L);
-                if ((e & ~28) == 0 && w == 0) put_lse(p, at.b, h0 + h, M - kPShift, L, false);
+                if ((e & ~28) == 0 && w == 0) put_lse(p, at.b, h0 + h, M - S::kPShift, L, false);
             };
             const float4* theirs = reinterpret_cast<const float4*>(smem + w * S::kRingBytes);
 #pragma unroll 1
@@ -1032,7 +1033,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                     const float inv = 1.f / L;
 #pragma unroll
                     for (int i = 0; i < S::kQuads; ++i) keep_out(i, acc[i], inv);
-                    if (t == 0 && g < nheads) put_lse(p, at.b, h0 + g, M - kPShift, L, false);
+                    if (t == 0 && g < nheads) put_lse(p, at.b, h0 + g, M - S::kPShift, L, false);
                     __syncwarp();
                     put_rows(at.b, h0, nheads);
                 }
@@ -1132,7 +1133,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                     const float inv = 1.f / Lh;
 #pragma unroll
                     for (int i = 0; i < kMine; ++i) keep_out(i * S::kWarps + warp, sum[i], inv);
-                    if (warp == 0 && t == 0) put_lse(p, e.b, e.h0 + g, Mh - kPShift, Lh, false);
+                    if (warp == 0 && t == 0) put_lse(p, e.b, e.h0 + g, Mh - S::kPShift, Lh, false);
                 }
                 __syncthreads();
                 if (warp == 0) put_rows(e.b, e.h0, e.nheads);

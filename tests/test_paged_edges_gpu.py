@@ -93,3 +93,17 @@ def test_attn_error_over_long_rows(qkv, kv, n_seq, n):
         off += (out[b].double() - want).square().sum().item()
         size += want.square().sum().item()
     assert (off / size) ** 0.5 <= 1e-6
+
+
+@pytest.mark.parametrize("hd,pool_off", LAYOUTS)
+def test_attn_of_f32_values_near_the_largest(qkv, hd, pool_off):
+    """Values of either sign around 5e35, whose sum over 90 slots is an f32 number, within the bound of ordinary
+    ones; and one slot of 3.3e38."""
+    def large(c, x):
+        c.v *= np.float32(5e35)
+
+    def one(c, x):
+        c.v[...] = np.where(np.signbit(c.v), np.float32(-3.3e38), np.float32(3.3e38))
+
+    base.run_attn(4, 2, hd, "f32", 16, [40, 90], change=large, pool_off=pool_off, weights=True)
+    base.run_attn(4, 2, hd, "f32", 16, [1, 1, 0], change=one, pool_off=pool_off)
