@@ -442,14 +442,24 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
     // 32 sequences 600 -> 550 slots 14.5 us with 1024, 9.6 us with 512; 2112 -> 2048 22.0 and 16.7 us).
     const bool halves = items > kSms;
     const int threads = size == 1 && halves ? kThreads / 2 : kThreads;
-    auto kernel = moves       ? (halves ? paged_evict_select_kernel<true, true, true, kThreads / 2>
-                                        : paged_evict_select_kernel<true, true, true, kThreads>)
-                  : size == 1 ? (halves ? paged_evict_select_kernel<true, false, true, kThreads / 2>
-                                        : paged_evict_select_kernel<true, false, true, kThreads>)
-                  : cached    ? paged_evict_select_kernel<true, false, false, kThreads>
-                              : paged_evict_select_kernel<false, false, false, kThreads>;
     const size_t smem = kFixedSmem + (cached ? static_cast<size_t>(slots) * 4 : 0) + (moves ? static_cast<size_t>(cap / 2) * 8 : 0);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // A kernel, and the most shared memory that a call of it can need.  That limit belongs to the kernel, not to the
+    // launch: were it set to what this call needs, a call of another thread could lower it before this one's launch.
+    struct Select {
+        void (*kernel)(PagedEvictParams, int);
+        int64_t most_smem;
+    };
+    const Select select =
+        moves       ? Select{halves ? paged_evict_select_kernel<true, true, true, kThreads / 2>
+                                    : paged_evict_select_kernel<true, true, true, kThreads>,
+                             kFixedSmem + 2 * kClusterSlots * (4 + 4)}
+        : size == 1 ? Select{halves ? paged_evict_select_kernel<true, false, true, kThreads / 2>
+                                    : paged_evict_select_kernel<true, false, true, kThreads>,
+                             kFixedSmem + 2 * kClusterSlots * 4}
+        : cached    ? Select{paged_evict_select_kernel<true, false, false, kThreads>, kFixedSmem + kMaxSlots * 4}
+                    : Select{paged_evict_select_kernel<false, false, false, kThreads>, kFixedSmem};
+    auto kernel = select.kernel;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(select.most_smem));
     if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)
         e = launch_dependent(kernel, dim3(static_cast<unsigned int>(items) * size), threads, smem, stream, size, p, size);

@@ -107,3 +107,59 @@ def test_attn_of_f32_values_near_the_largest(qkv, hd, pool_off):
 
     base.run_attn(4, 2, hd, "f32", 16, [40, 90], change=large, pool_off=pool_off, weights=True)
     base.run_attn(4, 2, hd, "f32", 16, [1, 1, 0], change=one, pool_off=pool_off)
+
+
+def run_in_threads(works):
+    """Run the functions at once, a thread each; what they raise."""
+    import threading
+    start, raised = threading.Barrier(len(works)), []
+
+    def body(work):
+        start.wait()
+        try:
+            work()
+        except Exception as e:
+            raised.append(e)
+    threads = [threading.Thread(target=body, args=(w,)) for w in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return raised
+
+
+@pytest.mark.parametrize("caps", [(512, 8192), (16384, 49152, 600000)], ids=str)
+def test_evictions_of_different_capacities_from_several_threads(qkv, caps):
+    """Host threads with caches of different capacities, a stream and a workspace each: no call fails, and each
+    keeps what it keeps alone."""
+    import torch
+    nkv, hd, page, n, budget = 2, 64, 64, 500, 400
+    works, states = [], []
+    rng = np.random.default_rng(23)
+    for cap in caps:
+        plan = base.make_plan(2 * nkv, nkv, hd, "f16")
+        c = base.ref.Cache(rng, 1, nkv, hd, "f16", page, cap // page, lens=[n], table_fill=0)
+        w = torch.zeros(1, nkv, cap, device="cuda")
+        w[..., :n] = base.dev(rng.random((1, nkv, n)).astype(np.float32))
+        pos = torch.arange(cap, dtype=torch.int32, device="cuda").expand(1, nkv, cap).contiguous()
+        k, v = base.dev(c.k), base.dev(c.v)
+        cache = base.Q.PagedKv(plan, k, v, base.dev(c.table), slot_weight=w, slot_pos=pos)
+        lens, out = base.dev(c.lens), torch.zeros(1, dtype=torch.int32, device="cuda")
+        wo, po = torch.zeros_like(w), torch.zeros_like(pos)
+        ws = torch.zeros(base.Q.qkv_evict_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+
+        def work(a=(plan, cache, lens, lens, budget, 7, out, wo, po, ws), stream=stream):
+            for _ in range(1500):
+                base.Q.qkv_evict_step(*a, stream=stream)
+        works.append(work)
+        states.append((c, w.cpu().numpy(), pos.cpu().numpy(), out, wo, po))
+    torch.cuda.synchronize()
+    assert run_in_threads(works) == []
+    torch.cuda.synchronize()
+    for c, w, pos, out, wo, po in states:
+        _, _, rl, rw, rp = base.ref.evict_ref(c, c.lens, c.lens, w, pos, budget, 7)
+        assert out.tolist() == list(rl) == [budget]
+        assert np.array_equal(wo.cpu().numpy()[..., :budget], rw[..., :budget])
+        assert np.array_equal(po.cpu().numpy()[..., :budget], rp[..., :budget])
+    assert base.Q.qkv_check_device_error()[0] == 0
