@@ -1284,6 +1284,19 @@ constexpr int kMaxStages = QKV_DECODE_MAX_STAGES;
 constexpr int kChainSkewPair = QKV_DECODE_CHAIN_SKEW_PAIR;
 constexpr int kChainSkewBlock = QKV_DECODE_CHAIN_SKEW_BLOCK;
 
+// Let a kernel have `bytes` of dynamic shared memory.  The limit belongs to the kernel, not to the launch, so it is
+// never lowered: a call of another thread that needs less would take it from this one before its launch.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+    static std::mutex lock;
+    static size_t most = 0;
+    std::lock_guard<std::mutex> hold(lock);
+    const size_t limit = bytes > most ? bytes : most;
+    const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit));
+    if (e == cudaSuccess) most = limit;
+    return e;
+}
+
 struct RingShape {
     int stages;        // multiple of the group count
     int ctas_per_sm;
@@ -1314,8 +1327,7 @@ template <typename WT, int MODE, int kGroups, int CPL = 0>
 cudaError_t launch_decode_tma(const DecodeParams& p, const RingShape& r, bool pdl, cudaStream_t stream) {
     auto kernel = qkv_decode_tma_kernel<WT, MODE, kGroups, CPL>;
     const size_t smem = r.x_bytes + static_cast<size_t>(r.stages) * r.stage_bytes + 2 * r.stages * sizeof(uint64_t);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = allow_smem<qkv_decode_tma_kernel<WT, MODE, kGroups, CPL>>(smem);
     if (e != cudaSuccess) return e;
     const int units = unit_count(p.nqt, p.nkt, p.hd);
     const int ctas = sm_count() * r.ctas_per_sm;
@@ -1368,8 +1380,7 @@ cudaError_t launch_decode_blk(const DecodeParams& p, int ctas_per_sm, int smem_k
     stages -= stages % kGroups;
     auto kernel = qkv_decode_blk_kernel<WT, MODE, kGroups, EPI, CPL>;
     const size_t smem = x_bytes + static_cast<size_t>(stages) * stage_bytes + 2 * stages * sizeof(uint64_t) + tail;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = allow_smem<qkv_decode_blk_kernel<WT, MODE, kGroups, EPI, CPL>>(smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -1444,8 +1455,7 @@ cudaError_t launch_decode_t(const DecodeParams& p, bool pdl, cudaStream_t stream
     auto kernel = qkv_decode_kernel<WT, VEC, MODE>;
     const size_t smem = static_cast<size_t>(p.H) * sizeof(float);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+        cudaError_t e = allow_smem<qkv_decode_kernel<WT, VEC, MODE>>(smem);
         if (e != cudaSuccess) return e;
     }
     const int units = (p.nqt >> 1) + (p.nkt >> 1) + (p.nkt >> 1);
