@@ -463,7 +463,7 @@ typedef struct qkv_paged_store_args {
     const int32_t* d_seqs;      /* device, nt, or null: token t belongs to sequence t (nt <= n_seq).  A
                                  * negative index marks padding: nothing of that token is written. */
     const int32_t* d_slots;     /* device, nt, or null: the slot is the position */
-    float* q;                   /* device, nt rows of nqt floats; may be Y itself (F32, the same stride) */
+    float* q;                   /* device, nt rows of nqt floats; may be Y itself (F32, and for nt > 1 the same stride) */
     int64_t q_stride;           /* >= nqt */
     float eps;
 } qkv_paged_store_args;

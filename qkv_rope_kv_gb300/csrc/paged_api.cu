@@ -112,8 +112,9 @@ extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged
             "a pointer is not aligned to its elements");
     const size_t ybytes = a->nt ? ((a->nt - 1) * static_cast<size_t>(a->y_stride) + plan->rows) * ys : 0;
     const size_t qbytes = a->nt ? ((a->nt - 1) * static_cast<size_t>(a->q_stride) + plan->nqt) * 4 : 0;
-    REQUIRE((a->Y == a->q && a->y_dtype == QKV_F32 && a->y_stride == a->q_stride) || !overlap(a->Y, ybytes, a->q, qbytes),
-            "q must be Y itself (F32, the same stride) or not overlap it");
+    const bool in_place = a->Y == a->q && a->y_dtype == QKV_F32 && (a->y_stride == a->q_stride || a->nt == 1);
+    REQUIRE(in_place || !overlap(a->Y, ybytes, a->q, qbytes),
+            "q must be Y itself (F32, the same stride where there are rows to step over) or not overlap it");
     if (a->nt == 0) return QKV_OK;
     p.y = a->Y;
     p.y_stride = a->y_stride;

@@ -6,6 +6,7 @@ import pytest
 import test_paged_gpu as base
 
 pytestmark = pytest.mark.gpu
+EPS = base.EPS
 
 # Head sizes and pool alignments that take each of the kernels: tensor cores, and rows of no whole 16 bytes.
 LAYOUTS = [(64, 0), (128, 0), (256, 0), (64, 1)]
@@ -162,4 +163,31 @@ def test_evictions_of_different_capacities_from_several_threads(qkv, caps):
         assert out.tolist() == list(rl) == [budget]
         assert np.array_equal(wo.cpu().numpy()[..., :budget], rw[..., :budget])
         assert np.array_equal(po.cpu().numpy()[..., :budget], rp[..., :budget])
+    assert base.Q.qkv_check_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("hd", [128, 6])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("nt", [1, 2, 500, 2500])
+def test_store_in_place(qkv, nt, norm, hd):
+    """q over Y's own rows, one token or more: the bits of a q of its own, and the rest of Y untouched."""
+    import torch
+    nh, nkv, page = 6, 2, 16
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    plan = base.make_plan(nh, nkv, hd, "f16")
+    k, v = (torch.zeros(160, page, nkv * hd, dtype=torch.float16, device="cuda") for _ in range(2))
+    cache = base.Q.PagedKv(plan, k, v, torch.arange(160, dtype=torch.int32, device="cuda").view(1, 160))
+    Y = torch.randn(nt, (nh + 2 * nkv) * hd, generator=gen, device="cuda")
+    w = (torch.randn(hd, generator=gen, device="cuda"), torch.randn(hd, generator=gen, device="cuda")) if norm else (None, None)
+    at, seqs = torch.arange(nt, dtype=torch.int32, device="cuda"), torch.zeros(nt, dtype=torch.int32, device="cuda")
+    got = []
+    for inplace in (False, True):
+        y = Y.clone()
+        q = y[:, :nh * hd] if inplace else torch.empty(nt, nh * hd, device="cuda")
+        k.zero_()
+        v.zero_()
+        base.Q.qkv_paged_store_step(plan, cache, y, None, *w, EPS, at, seqs, None, q)
+        got.append((q.clone(), k.clone(), v.clone()))
+        assert torch.equal(y[:, nh * hd:], Y[:, nh * hd:])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
     assert base.Q.qkv_check_device_error()[0] == 0

@@ -17,6 +17,21 @@ def plan(nh, nkv, hd, kv):
     return q.qkv_plan_create(64, nh, nkv, hd, 1e6, 64, kv_dtype={"f16": q.QKV_F16, "f32": q.QKV_F32}[kv])
 
 
+def store_args(**kw):
+    a = dict(Y=P << 4, y_stride=512, y_dtype=q.QKV_F32, nt=1, bias=0, qw=0, kw=0, pos=P, seqs=P, slots=P, q=P << 4,
+             q_stride=256, eps=0.0)
+    return q._STORE_ARGS.pack(*{**a, **kw}.values())
+
+
+@pytest.mark.parametrize("kw", [dict(nt=2), dict(y_dtype=q.QKV_BF16), dict(q=(P << 4) + 4), dict(q=(P << 4) + 4 * 511)],
+                         ids=str)
+def test_store_over_parts_of_y_is_refused(lib, kw):
+    """Rows of two strides, of another type, or shifted against Y's."""
+    c = q.qkv_paged_kv(P, P << 8, P, 8, 16, 3, 4, 0, None, None)
+    assert lib.qkv_paged_store_step(plan(4, 2, 64, "f16").handle, ctypes.byref(c), store_args(**kw),
+                                    None) == q.QKV_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("nh,nkv,hd,kv,n_seq,capacity,want", [
     (40, 8, 128, "f16", 1, 32768, (256, 8)),    # four clusters for each kv head
     (28, 4, 128, "f16", 1, 1648, (64, 8)),      # no more clusters than can have work
