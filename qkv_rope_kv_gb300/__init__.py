@@ -504,8 +504,10 @@ class PagedKv:
         pools = (n_pages, page_size, nkt)
         for name, t in (("k", k), ("v", v)):
             if t.dtype is not kv or t.shape != pools or t.get_device() != dev or t.stride(2) != 1 and nkt > 1 or \
-                    t.stride(1) != nkt and page_size > 1 or t.stride(0) != k.stride(0) and n_pages > 1:
-                _refuse(t, name, kv, pools, dev, "rows of a page nkt elements apart and the pages of k and v equally far")
+                    t.stride(1) != nkt and page_size > 1 or \
+                    n_pages > 1 and (t.stride(0) != k.stride(0) or t.stride(0) < page_size * nkt):
+                _refuse(t, name, kv, pools, dev, "rows of a page nkt elements apart, pages of their own, and those of k "
+                        "and v equally far apart")
         self.struct = qkv_paged_kv(
             k.data_ptr(), v.data_ptr(), _tensor(page_table, "page_table", torch.int32, (n_seq, max_pages), dev),
             n_pages, page_size, n_seq, max_pages, k.stride(0) if n_pages > 1 else 0,

@@ -191,3 +191,17 @@ def test_store_in_place(qkv, nt, norm, hd):
         assert torch.equal(y[:, nh * hd:], Y[:, nh * hd:])
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert base.Q.qkv_check_device_error()[0] == 0
+
+
+def test_pools_whose_pages_overlap_are_refused(qkv):
+    """An expanded pool (page stride 0, which means "one after the other" to the C call) or overlapping pages."""
+    import torch
+    plan = base.make_plan(4, 2, 64, "f16")
+    table = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    whole = torch.zeros(8, 16, 128, dtype=torch.float16, device="cuda")
+    one = whole[:1].expand(8, 16, 128)
+    near = whole.as_strided((4, 16, 128), (8 * 128, 128, 1))
+    for k, v in ((one, one), (whole, one), (one, whole), (near, near)):
+        with pytest.raises(base.Q.QkvError, match="pages of their own"):
+            base.Q.PagedKv(plan, k, v, table)
+    base.Q.PagedKv(plan, whole[:1].expand(1, 16, 128), whole[1:2], table)  # one page has no stride
