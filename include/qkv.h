@@ -510,7 +510,8 @@ qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const 
  * weight and position, so no kept row below budget moves and none moves twice.  Attention does not
  * depend on the order of the slots (but its window counts slots: do not combine the two).  The cache
  * must have slot_weight and slot_pos.  Sequences must not share pages (a shared prefix would be
- * changed under the others).  No order of execution changes the result.
+ * changed under the others).  A slot whose page or whose new content's page is out of range keeps its
+ * row, weight and position.  No order of execution changes the result.
  * Errors: INVALID_ARG, CUDA. */
 typedef struct qkv_evict_args {
     const int32_t* d_lens;      /* device, n_seq */

@@ -122,10 +122,11 @@ __device__ __forceinline__ void make_moves(const PagedEvictParams& p, int item, 
             const int pos = p.c.slot_pos[base + from];
             const PageRef rt = page_ref(p.c, b, to), rf = page_ref(p.c, b, from);
             const int64_t ot = row_offset(p.c, rt), of = row_offset(p.c, rf);
-            to_s[tid] = ot >= 0 && of >= 0 ? (ot + h * p.hd) / elem_per_unit : -1;
+            const bool can = ot >= 0 && of >= 0;  // else the slot stays as it is
+            to_s[tid] = can ? (ot + h * p.hd) / elem_per_unit : -1;
             from_s[tid] = (of + h * p.hd) / elem_per_unit;
-            p.weight_out[base + to] = w;
-            p.pos_out[base + to] = pos;
+            p.weight_out[base + to] = can ? w : p.c.slot_weight[base + to];
+            p.pos_out[base + to] = can ? pos : p.c.slot_pos[base + to];
         }
         __syncthreads();
         // unit c of move i, and on by THREADS units a step

@@ -205,3 +205,46 @@ def test_pools_whose_pages_overlap_are_refused(qkv):
         with pytest.raises(base.Q.QkvError, match="pages of their own"):
             base.Q.PagedKv(plan, k, v, table)
     base.Q.PagedKv(plan, whole[:1].expand(1, 16, 128), whole[1:2], table)  # one page has no stride
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("hd,page,max_pages", [(64, 16, 4), (6, 16, 4), (64, 16, 600)])
+def test_evict_leaves_slots_of_bad_pages_as_they_are(qkv, hd, page, max_pages, inplace):
+    """A move from or to a page that is not there is not made, and the slot keeps its weight and position with its
+    row; in one launch, with rows of no whole 16 bytes, and in clusters."""
+    import torch
+    rng = np.random.default_rng(25)
+    nkv, n, budget = 2, 64, 24
+    c = base.ref.Cache(rng, 2, nkv, hd, "f16", page, max_pages, lens=[n, n])
+    plan = base.make_plan(2 * nkv, nkv, hd, "f16")
+    w = rng.random((2, nkv, c.cap)).astype(np.float32)
+    pos = np.tile(rng.permutation(c.cap).astype(np.int32), (2, nkv, 1))
+    bad_slots = set(range(page, 2 * page)) | set(range(2 * page, 3 * page))  # 8 below the budget, others above
+    table = c.table.copy()
+    table[0, 1], table[0, 2] = c.n_pages, -3
+    k, v, dw, dp = base.dev(c.k), base.dev(c.v), base.dev(w), base.dev(pos)
+    cache = base.Q.PagedKv(plan, k, v, base.dev(table), slot_weight=dw, slot_pos=dp)
+    wo, po = (dw, dp) if inplace else (torch.full_like(dw, -8.0), torch.full_like(dp, -8))
+    lo = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(base.Q.qkv_evict_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+    lens = base.dev(c.lens)
+    base.Q.qkv_evict_step(plan, cache, lens, base.dev(np.int32([2 ** 30] * 2)), budget, 0, lo, wo, po, ws)
+    torch.cuda.synchronize()
+    flags, value = base.Q.qkv_check_device_error()
+    assert flags == 4 and value in (c.n_pages, -3) and lo.tolist() == [budget, budget]
+    rk, rv, rw, rp, left = c.k.copy(), c.v.copy(), w.copy(), pos.copy(), 0
+    for b in range(2):
+        for h in range(nkv):
+            kept = set(sorted(range(n), key=lambda s: -w[b, h, s])[:budget])
+            for to, at in zip([s for s in range(budget) if s not in kept], [s for s in range(budget, n) if s in kept]):
+                if b == 0 and (to in bad_slots or at in bad_slots):
+                    left += 1
+                    continue
+                for pool in (rk, rv):
+                    pool[c.row(b, to)][h * hd:(h + 1) * hd] = pool[c.row(b, at)][h * hd:(h + 1) * hd]
+                rw[b, h, to], rp[b, h, to] = w[b, h, at], pos[b, h, at]
+    assert left > 4
+    assert np.array_equal(wo.cpu().numpy()[..., :budget], rw[..., :budget])
+    assert np.array_equal(po.cpu().numpy()[..., :budget], rp[..., :budget])
+    for got, want in ((k, rk), (v, rv)):
+        assert np.array_equal(got.cpu().numpy().view(np.uint16), want.view(np.uint16))
