@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qkv_internal.h"
 
 namespace qkv_paged {
@@ -14,6 +16,7 @@ constexpr unsigned int kFlagSlotRange = 1u;  // a slot outside the sequence's ca
 constexpr unsigned int kFlagIndexRange = 4u; // a page id, length or sequence index out of range
 
 static __device__ unsigned int g_paged_status[2];  // [0] flags, [1] a bad value
+static std::atomic<bool> g_launched{false};        // whether this process launched any of this file's kernels
 
 __device__ __forceinline__ void flag_bad(unsigned int bit, int value) {
     atomicOr(&g_paged_status[0], bit);
@@ -76,11 +79,13 @@ static inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid,
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
+    g_launched.store(true, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Read and clear this file's status word (synchronises the stream).
+// Read and clear this file's status word (synchronises the stream); nothing has set it where nothing was launched.
 static inline cudaError_t status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {
+    if (!g_launched.load(std::memory_order_relaxed)) return cudaSuccess;
     unsigned int h[2] = {0u, 0u};
     cudaError_t e = cudaMemcpyFromSymbolAsync(h, g_paged_status, sizeof(h), 0, cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);

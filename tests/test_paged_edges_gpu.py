@@ -248,3 +248,37 @@ def test_evict_leaves_slots_of_bad_pages_as_they_are(qkv, hd, page, max_pages, i
     assert np.array_equal(po.cpu().numpy()[..., :budget], rp[..., :budget])
     for got, want in ((k, rk), (v, rv)):
         assert np.array_equal(got.cpu().numpy().view(np.uint16), want.view(np.uint16))
+
+
+STATUS_READS = """
+import torch, qkv_rope_kv_gb300 as Q
+from torch.profiler import ProfilerActivity, profile
+plan = Q.qkv_plan_create(64, 4, 2, 64, 1e6, 64)
+k = torch.zeros(4, 16, 128, dtype=torch.float16, device="cuda")
+table = torch.full((1, 4), 9, dtype=torch.int32, device="cuda")
+cache = Q.PagedKv(plan, k, k.clone(), table)
+ws = torch.zeros(Q.qkv_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+q, out, lens = torch.zeros(1, 256, device="cuda"), torch.zeros(1, 256, device="cuda"), torch.ones_like(table[0, :1])
+def reads():
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA, ProfilerActivity.CPU]) as p:
+        got = Q.qkv_check_device_error()
+    return got, sum(e.count for e in p.key_averages() if "Memcpy DtoH" in e.key)
+reads()  # the profiler's first use records nothing
+print(reads())
+Q.qkv_attn_step(plan, cache, q, lens, 0.1, out, ws)
+print(reads())
+print(reads())
+"""
+
+
+def test_status_is_read_only_where_it_can_be_set(qkv):
+    """A process that launched no paged kernel reads the two words of decode and prefill; the attention's follows once
+    it was launched (here on a page that is not there, which sets it)."""
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", STATUS_READS], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    lines = [line for line in r.stdout.splitlines() if line.startswith("((")]
+    assert lines == ["((0, 0), 2)", "((4, 9), 3)", "((0, 0), 3)"], r.stdout + r.stderr[-2000:]
