@@ -532,6 +532,10 @@ class PagedKv:
         return self._current_stream(self.device) if stream is None else _stream(stream)
 
 
+def _unpackable(e: Exception):
+    raise QkvError(QKV_ERR_INVALID_ARG, "a number does not fit its argument: %s" % e) from None
+
+
 def _workspace(t, device: int):
     if t is None:
         return 0, 0
@@ -549,11 +553,14 @@ def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w
     y, y_stride = _rows(Y, "Y", bf16 if y_type is bf16 else f32, (nt, plan.rows), dev)
     to, to_stride = _rows(q, "q", f32, (nt, plan.nqt), dev)
     nt_shape = (nt,)
-    args = _STORE_ARGS.pack(
-        y, y_stride, QKV_BF16 if y_type is bf16 else QKV_F32, nt, _tensor(bias, "bias", f32, (plan.rows,), dev),
-        _tensor(q_norm_w, "q_norm_w", f32, head, dev), _tensor(k_norm_w, "k_norm_w", f32, head, dev),
-        _tensor(positions, "positions", i32, nt_shape, dev), _tensor(seqs, "seqs", i32, nt_shape, dev),
-        _tensor(slots, "slots", i32, nt_shape, dev), to, to_stride, eps)
+    try:
+        args = _STORE_ARGS.pack(
+            y, y_stride, QKV_BF16 if y_type is bf16 else QKV_F32, nt, _tensor(bias, "bias", f32, (plan.rows,), dev),
+            _tensor(q_norm_w, "q_norm_w", f32, head, dev), _tensor(k_norm_w, "k_norm_w", f32, head, dev),
+            _tensor(positions, "positions", i32, nt_shape, dev), _tensor(seqs, "seqs", i32, nt_shape, dev),
+            _tensor(slots, "slots", i32, nt_shape, dev), to, to_stride, eps)
+    except (struct.error, OverflowError) as e:
+        _unpackable(e)
     _check(_lib.qkv_paged_store_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 
@@ -572,10 +579,13 @@ def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, worksp
     dev, out_type, shape = cache.device, out.dtype, (cache.n_seq, plan.nqt)
     x, x_stride = _rows(q, "q", f32, shape, dev)
     to, to_stride = _rows(out, "out", bf16 if out_type is bf16 else f32, shape, dev)
-    args = _ATTN_ARGS.pack(
-        x, x_stride, _tensor(lens, "lens", i32, cache.per_seq, dev), to, to_stride,
-        _tensor(lse, "lse", f32, (cache.n_seq, plan.n_head), dev), *_workspace(workspace, dev), scale, window,
-        QKV_BF16 if out_type is bf16 else QKV_F32, add_weight)
+    try:
+        args = _ATTN_ARGS.pack(
+            x, x_stride, _tensor(lens, "lens", i32, cache.per_seq, dev), to, to_stride,
+            _tensor(lse, "lse", f32, (cache.n_seq, plan.n_head), dev), *_workspace(workspace, dev), scale, window,
+            QKV_BF16 if out_type is bf16 else QKV_F32, add_weight)
+    except (struct.error, OverflowError) as e:
+        _unpackable(e)
     _check(_lib.qkv_attn_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 
@@ -591,10 +601,13 @@ def qkv_evict_step(plan: Plan, cache: PagedKv, lens, next_pos, budget: int, rece
     ``recent`` newest positions); weight_out / pos_out may be the cache's own tensors."""
     f32, i32, _ = cache.types
     dev, B = cache.device, cache.per_seq
-    args = _EVICT_ARGS.pack(
-        _tensor(lens, "lens", i32, B, dev), _tensor(next_pos, "next_pos", i32, B, dev),
-        _tensor(lens_out, "lens_out", i32, B, dev), _tensor(weight_out, "weight_out", f32, cache.tracked, dev),
-        _tensor(pos_out, "pos_out", i32, cache.tracked, dev), *_workspace(workspace, dev), budget, recent)
+    try:
+        args = _EVICT_ARGS.pack(
+            _tensor(lens, "lens", i32, B, dev), _tensor(next_pos, "next_pos", i32, B, dev),
+            _tensor(lens_out, "lens_out", i32, B, dev), _tensor(weight_out, "weight_out", f32, cache.tracked, dev),
+            _tensor(pos_out, "pos_out", i32, cache.tracked, dev), *_workspace(workspace, dev), budget, recent)
+    except (struct.error, OverflowError) as e:
+        _unpackable(e)
     _check(_lib.qkv_evict_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 

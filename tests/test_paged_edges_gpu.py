@@ -282,3 +282,30 @@ def test_status_is_read_only_where_it_can_be_set(qkv):
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     lines = [line for line in r.stdout.splitlines() if line.startswith("((")]
     assert lines == ["((0, 0), 2)", "((4, 9), 3)", "((0, 0), 3)"], r.stdout + r.stderr[-2000:]
+
+
+def test_numbers_that_fit_no_argument_are_refused(qkv):
+    """As any other bad argument, by the framework's error."""
+    import torch
+    plan = base.make_plan(4, 2, 64, "f16")
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    i32 = torch.int32
+    k = z(4, 16, 128, dtype=torch.float16)
+    w, p, lens = z(1, 2, 64), z(1, 2, 64, dtype=i32), z(1, dtype=i32)
+    cache = base.Q.PagedKv(plan, k, k.clone(), z(1, 4, dtype=i32), slot_weight=w, slot_pos=p)
+    ws = z(base.Q.qkv_attn_workspace_bytes(plan, cache), dtype=torch.uint8)
+    we = z(base.Q.qkv_evict_workspace_bytes(plan, cache), dtype=torch.uint8)
+    q, out = z(1, 256), z(1, 256)
+    for scale, window in ((0.1, 1 << 31), (0.1, -1), (0.1, 1.5), (0.1, None), (1e39, 0), (None, 0), (float("nan"), 0)):
+        with pytest.raises(base.Q.QkvError) as e:
+            base.Q.qkv_attn_step(plan, cache, q, lens, scale, out, ws, window=window)
+        assert e.value.status == base.Q.QKV_ERR_INVALID_ARG
+    for budget, recent in ((1 << 31, 0), (1 << 40, 0), (4, -1), (4, 1 << 40), (2.5, 0)):
+        with pytest.raises(base.Q.QkvError) as e:
+            base.Q.qkv_evict_step(plan, cache, lens, lens, budget, recent, lens.clone(), w, p, we)
+        assert e.value.status == base.Q.QKV_ERR_INVALID_ARG
+    for eps in (1e39, None, -1.0):
+        with pytest.raises(base.Q.QkvError) as e:
+            base.Q.qkv_paged_store_step(plan, cache, z(1, 512), None, z(64), z(64), eps, lens, None, None, q)
+        assert e.value.status == base.Q.QKV_ERR_INVALID_ARG
+    assert base.Q.qkv_check_device_error()[0] == 0
