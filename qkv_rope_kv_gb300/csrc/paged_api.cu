@@ -246,6 +246,9 @@ extern "C" qkv_status qkv_evict_step(const qkv_plan* plan, const qkv_paged_kv* c
     REQUIRE((a->weight_out == cache->slot_weight || !overlap(a->weight_out, sb, cache->slot_weight, sb)) &&
                 (a->pos_out == cache->slot_pos || !overlap(a->pos_out, sb, cache->slot_pos, sb)),
             "weight_out and pos_out must be slot_weight and slot_pos themselves or not overlap them");
+    REQUIRE(!overlap(a->weight_out, sb, a->pos_out, sb) && !overlap(a->weight_out, sb, cache->slot_pos, sb) &&
+                !overlap(a->pos_out, sb, cache->slot_weight, sb),
+            "weight_out must not overlap pos_out or slot_pos, nor pos_out slot_weight");
     size_t need = 0;
     st = qkv_evict_workspace_bytes(plan, cache, &need);
     if (st != QKV_OK) return st;

@@ -54,3 +54,12 @@ def test_attention_grid_follows_from_sizes_alone(lib, nh, nkv, hd, kv, n_seq, ca
     assert lib.qkv_test_attn_grid(plan(nh, nkv, hd, kv).handle, ctypes.byref(c), ctypes.byref(ctas),
                                   ctypes.byref(cluster)) == q.QKV_OK
     assert (ctas.value, cluster.value) == want
+
+
+@pytest.mark.parametrize("w,pos", [(P << 13, P << 14), (P << 14, P << 12), (P << 14, P << 14), (P << 14, (P << 14) + 1532),
+                                   (P << 12, (P << 12) + 4)], ids=str)
+def test_eviction_outputs_over_each_other_are_refused(lib, w, pos):
+    """weight_out over slot_pos, pos_out over slot_weight, and one over the other."""
+    c = q.qkv_paged_kv(P, P << 8, P, 8, 16, 3, 4, 0, P << 12, P << 13)
+    args = q._EVICT_ARGS.pack(P, P, P << 6, w, pos, P, 1 << 40, 8, 2)
+    assert lib.qkv_evict_step(plan(4, 2, 64, "f16").handle, ctypes.byref(c), args, None) == q.QKV_ERR_INVALID_ARG
