@@ -104,7 +104,7 @@ extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged
     REQUIRE(a->y_stride >= plan->rows, "y_stride must be >= R = %lld", static_cast<long long>(plan->rows));
     REQUIRE(a->q_stride >= plan->nqt, "q_stride must be >= nqt = %lld", static_cast<long long>(plan->nqt));
     REQUIRE((a->q_norm_w == nullptr) == (a->k_norm_w == nullptr), "q_norm_w and k_norm_w: both or neither");
-    if (a->q_norm_w) REQUIRE(a->eps >= 0.f && a->eps == a->eps, "eps must be a number >= 0");
+    if (a->q_norm_w) REQUIRE(a->eps >= 0.f && std::isfinite(a->eps), "eps must be finite and >= 0");
     REQUIRE(a->d_seqs || a->nt <= cache->n_seq, "without d_seqs, nt must be <= n_seq");
     const int ys = a->y_dtype == QKV_F32 ? 4 : 2;
     REQUIRE(aligned(a->Y, ys) && aligned(a->q, 4) && aligned(a->bias, 4) && aligned(a->q_norm_w, 4) &&

@@ -63,3 +63,11 @@ def test_eviction_outputs_over_each_other_are_refused(lib, w, pos):
     c = q.qkv_paged_kv(P, P << 8, P, 8, 16, 3, 4, 0, P << 12, P << 13)
     args = q._EVICT_ARGS.pack(P, P, P << 6, w, pos, P, 1 << 40, 8, 2)
     assert lib.qkv_evict_step(plan(4, 2, 64, "f16").handle, ctypes.byref(c), args, None) == q.QKV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("eps", [float("inf"), float("nan"), -1.0, -float("inf")])
+def test_store_eps_is_finite_and_not_negative(lib, eps):
+    """A norm with an infinite eps has no value but 0."""
+    c = q.qkv_paged_kv(P, P << 8, P, 8, 16, 3, 4, 0, None, None)
+    args = store_args(qw=P, kw=P, q=P << 5, eps=eps)
+    assert lib.qkv_paged_store_step(plan(4, 2, 64, "f16").handle, ctypes.byref(c), args, None) == q.QKV_ERR_INVALID_ARG
