@@ -481,9 +481,10 @@ qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
  * V is summed before the division by the weights' sum: |V| (f32) times the number of slots is to
  * stay below the largest f32.
  * The length is split over the GPU and joined in a fixed order: results do not depend on
- * timing.  The workspace must be zero before the first call and belongs to calls that do not overlap
- * on the GPU (one stream, or graphs replayed one after the other); every completed call leaves it
- * usable for the next, of any shape that needs no more bytes.
+ * timing.  The workspace's first 4096 bytes must be zero before the first call (the others may hold
+ * anything), and it belongs to calls that do not overlap on the GPU (one stream, or graphs replayed one
+ * after the other); every completed call leaves it usable for the next, of any shape that needs no more
+ * bytes.
  * Errors: INVALID_ARG, UNSUPPORTED (out_dtype, n_head % n_head_kv != 0), CUDA. */
 typedef struct qkv_attn_args {
     const float* q;         /* device, n_seq rows of nqt floats */

@@ -574,7 +574,7 @@ def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, worksp
                   add_weight: bool = False, stream=None):
     """Attention of one new token per sequence: q [n_seq, nqt] f32 over the cached slots of each
     (``lens`` int32 [n_seq]) into out [n_seq, nqt] (f32 or bf16) and lse [n_seq, n_head] (f32).
-    ``workspace``: zeroed device bytes, qkv_attn_workspace_bytes of them; it stays usable."""
+    ``workspace``: qkv_attn_workspace_bytes device bytes, the first 4096 of them zero; it stays usable."""
     f32, i32, bf16 = cache.types
     dev, out_type, shape = cache.device, out.dtype, (cache.n_seq, plan.nqt)
     x, x_stride = _rows(q, "q", f32, shape, dev)

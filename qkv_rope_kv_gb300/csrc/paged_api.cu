@@ -77,6 +77,7 @@ AttnLayout attn_layout(const qkv_plan* plan, const qkv_paged_kv* c, bool weights
     const size_t rows = static_cast<size_t>(c->n_seq) * plan->d.n_head;
     const size_t hd = plan->d.head_dim <= 64 ? 64 : plan->d.head_dim <= 128 ? 128 : 256;  // as the kernels pad it
     l.part = up256(3 * kAttnMaxCtas * sizeof(uint32_t));
+    static_assert(3 * kAttnMaxCtas * sizeof(uint32_t) <= 4096, "the counters are in what a caller has to zero");
     l.lse2 = l.part + up256(sizeof(float) * 2 * kAttnMaxCtas * kAttnHeads * (hd + 2));
     l.scores = l.lse2 + (weights ? up256(sizeof(float) * rows) : 0);
     l.total = l.scores + (weights ? up256(sizeof(float) * rows * score_stride(c)) : 0);

@@ -309,3 +309,30 @@ def test_numbers_that_fit_no_argument_are_refused(qkv):
             base.Q.qkv_paged_store_step(plan, cache, z(1, 512), None, z(64), z(64), eps, lens, None, None, q)
         assert e.value.status == base.Q.QKV_ERR_INVALID_ARG
     assert base.Q.qkv_check_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("nh,nkv,hd,kv,lens,kw", [
+    (28, 4, 128, "f16", [3000], {}), (28, 4, 128, "f16", [700, 1, 0, 2000] * 9, dict(window=65)),
+    (14, 2, 64, "f32", [509, 33], {}), (5, 1, 128, "f16", [30011], {}), (136, 1, 64, "f16", [90, 31, 0, 200] * 4, {}),
+    (8, 1, 256, "f16", [900] * 20, {}), (6, 3, 6, "f16", [50, 3], dict(window=7)),
+], ids=str)
+def test_attn_workspace_needs_its_head_zero_alone(qkv, nh, nkv, hd, kv, lens, kw):
+    """Behind the first 4096 bytes the workspace may hold anything (here NaN)."""
+    import torch
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    ws[:4096] = 0
+    base.run_attn(nh, nkv, hd, kv, 16, lens, weights=True, workspace=ws, **kw)
+
+
+@pytest.mark.filterwarnings("ignore:invalid value")  # a signalling NaN on its way to 64 bits
+@pytest.mark.parametrize("bits", [0x7f800001, 0xff800001, 0x7f801fff, 0x7fffffff], ids=hex)
+@pytest.mark.parametrize("hd,pool_off", LAYOUTS)
+def test_attn_f32_nan_of_any_payload(qkv, hd, pool_off, bits):
+    """A NaN whose payload is in its lowest bits is one as any other: in V it stays in its column, in K in its heads."""
+    nan = np.array(bits, np.uint32).view(np.float32)
+
+    def change(c, x):
+        c.v[c.row(0, 9)][4] = nan
+        c.k[c.row(1, 11)][hd + 2] = nan
+
+    base.run_attn(4, 2, hd, "f32", 16, [40, 90], change=change, pool_off=pool_off)
