@@ -204,8 +204,9 @@ struct Split {
     static constexpr int kQuads = HD / 16;                 // a lane's outputs of one head, in fours
     static constexpr int kQRow = HD + (kF16 ? 8 : 16);     // floats; spreads the heads' rows over the banks
     static constexpr int kQLoads = kAttnHeads * HD / kThreads;
-    // q's fragments stay in registers beside O, and the next item's q is loaded ahead, where that leaves no spills
-    // in the loop (4 x 128 x f32, 32000 slots: 37 us, with fragments in registers 64)
+    // q's fragments stay in registers beside O, and the next item's q is loaded ahead, where there is room (4 x 128 x
+    // f32, 32000 slots: 37 us, with fragments in registers, and spilled, 64).  What the compiler still spills: head
+    // size 256 without clusters 144 bytes (f32) and 132 (f16), in clusters 8 (f32); f32 of 128 without clusters 12.
     static constexpr bool kQRegs = kF16 && HD < 256;
     static constexpr bool kQAhead = kF16 ? HD < 256 : HD < 128;
     static constexpr float kPShift = kF16 ? 12.f : -kLazy;  // weights are kept times 2^kPShift
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
         Walk next = at;
         if (follows) next_item(next);
 
-        uint32_t qa[S::kQRegs ? (S::kF16 ? HD / 4 : HD / 2) : 8];  // q of head g as A fragments
+        uint32_t qa[S::kQRegs ? HD / 4 : 8];  // q of head g as A fragments
         float unscale = 1.f;
         const float* qg = q_s + g * S::kQRow;
         float O[S::kNT][4];
@@ -698,15 +699,6 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
                                 reinterpret_cast<uint4*>(q_s)[(warp * kPart + s) * 32 + lane] =
                                     make_uint4(a[4 * s], a[4 * s + 1], a[4 * s + 2], a[4 * s + 3]);
                             __syncthreads();
-                        }
-                    } else if constexpr (S::kQRegs) {
-#pragma unroll
-                        for (int s = 0; s < HD / 16; ++s) {
-                            const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
-                            split_tf32(v.x, qa[8 * s], qa[8 * s + 1]);
-                            split_tf32(v.y, qa[8 * s + 2], qa[8 * s + 3]);
-                            split_tf32(v.z, qa[8 * s + 4], qa[8 * s + 5]);
-                            split_tf32(v.w, qa[8 * s + 6], qa[8 * s + 7]);
                         }
                     }
                     if (S::kQAhead && follows) load_q(next);  // waited for at this segment's end
@@ -758,14 +750,12 @@ __global__ void __launch_bounds__(Split<KT, HD>::kThreads, Split<KT, HD>::kCtas)
             } else {
 #pragma unroll
                 for (int s = 0; s < HD / 16; ++s) {
-                    uint32_t* a = qa + (S::kQRegs ? 8 * s : 0);
-                    if constexpr (!S::kQRegs) {
-                        const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
-                        split_tf32(v.x, a[0], a[1]);
-                        split_tf32(v.y, a[2], a[3]);
-                        split_tf32(v.z, a[4], a[5]);
-                        split_tf32(v.w, a[6], a[7]);
-                    }
+                    uint32_t* a = qa;
+                    const float4 v = *reinterpret_cast<const float4*>(qg + 16 * s + 4 * t);
+                    split_tf32(v.x, a[0], a[1]);
+                    split_tf32(v.y, a[2], a[3]);
+                    split_tf32(v.z, a[4], a[5]);
+                    split_tf32(v.w, a[6], a[7]);
 #pragma unroll
                     for (int j = 0; j < kST; ++j) {
                         float r[4];
