@@ -505,8 +505,9 @@ qkv_status qkv_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* ca
 qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_attn_args* args, void* stream);
 
 /* Cut every sequence longer than `budget` slots down to budget, per kv head: kept are the slots
- * whose position is >= d_next_pos[b] - recent, then those with the largest slot_weight (equal
- * weights: the lowest slot first; a NaN counts as larger than any number).  The i-th dropped slot
+ * whose position is >= d_next_pos[b] - recent (of more than budget such: the lowest slots), then those
+ * with the largest slot_weight (equal weights: the lowest slot first; a NaN counts as larger than any
+ * number).  The i-th dropped slot
  * below budget takes what the i-th kept slot at or above it holds: its K and V row (of that head),
  * weight and position, so no kept row below budget moves and none moves twice.  Attention does not
  * depend on the order of the slots (but its window counts slots: do not combine the two).  The cache

@@ -336,3 +336,24 @@ def test_attn_f32_nan_of_any_payload(qkv, hd, pool_off, bits):
         c.k[c.row(1, 11)][hd + 2] = nan
 
     base.run_attn(4, 2, hd, "f32", 16, [40, 90], change=change, pool_off=pool_off)
+
+
+@pytest.mark.parametrize("max_pages", [4, 600])
+def test_evict_with_more_newest_slots_than_the_budget(qkv, max_pages):
+    """Positions that all count as newest: the lowest slots stay, and nothing moves."""
+    import torch
+    rng = np.random.default_rng(26)
+    c = base.ref.Cache(rng, 1, 2, 64, "f16", 16, max_pages, lens=[64])
+    plan = base.make_plan(4, 2, 64, "f16")
+    w, pos = base.dev(rng.random((1, 2, c.cap)).astype(np.float32)), base.dev(np.tile(np.arange(c.cap, dtype=np.int32), (1, 2, 1)))
+    k, v = base.dev(c.k), base.dev(c.v)
+    cache = base.Q.PagedKv(plan, k, v, base.dev(c.table), slot_weight=w, slot_pos=pos)
+    wo, po, lo = torch.full_like(w, -8.0), torch.full_like(pos, -8), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(base.Q.qkv_evict_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+    for nxt in (-2 ** 31, 0, 5):
+        base.Q.qkv_evict_step(plan, cache, base.dev(c.lens), base.dev(np.int32([nxt])), 20, 9, lo, wo, po, ws)
+        assert lo.tolist() == [20] and torch.equal(wo[..., :20], w[..., :20]) and torch.equal(po[..., :20], pos[..., :20])
+        assert (wo[..., 20:] == -8).all() and (po[..., 20:] == -8).all()
+        assert np.array_equal(k.cpu().numpy().view(np.uint16), c.k.view(np.uint16))
+        assert np.array_equal(v.cpu().numpy().view(np.uint16), c.v.view(np.uint16))
+    assert base.Q.qkv_check_device_error()[0] == 0
