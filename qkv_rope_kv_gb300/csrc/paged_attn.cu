@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // an mma.sync has 16, all in use here, and its pipe is 13 to 17 % busy.
 // Measured (GPU time, of the copy rate): 64 sequences of 8 x 128 x f16 to 8192 slots 184 us, DRAM at 6.2 TB/s
 // (0.92); one of 32749 slots 29 us (0.68: about 9 us of it are launch, lengths, first pages and the join);
-// 32 to 4099 slots with weights 40.2 us; 14 x 64 x f32, 509 slots 6.1 us, all latency.
+// 32 to 4099 slots with weights 40.2 us; 14 x 64 x f32, 509 slots 5.9 us, all latency.
 //
 // Work is counted in units of 8 to 32 neighbouring slots of one item (8 KB of K and V as a rule), an item
 // being (sequence, kv head, block of up to 8 of its q heads).  Lengths are on the device, so every CTA finds
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
 // maximum (then O need not be rescaled for every new maximum).  f16: before the split q is scaled by a power of
 // two into [2^13, 2^14), and the shift is 12, both far from the type's ends.  f32: the shift is -3, so no weight
 // is above 1 and O stays finite wherever sum p_j |V_j| does.  Sums over many MMAs are made outside of them,
-// rounded to nearest (add4): 20 x 6000 slots x 8 x 128 x f32 come out 6.2e-7 off (2-norms) instead of 6.1e-6,
-// f16 5e-7 instead of 2.3e-6, at the same times (an f32 batch: 3 % more).
+// rounded to nearest (add4): 20 x 6000 slots x 8 x 128 x f32 come out 5e-7 off (2-norms) instead of 6.1e-6,
+// f16 4e-7 instead of 2.3e-6, at the same times (an f32 batch: 3 % more).
 
 constexpr int kMinShare = 8;     // units
 constexpr int kItemCost = 8;     // units
@@ -205,8 +205,9 @@ struct Split {
     static constexpr int kQRow = HD + (kF16 ? 8 : 16);     // floats; spreads the heads' rows over the banks
     static constexpr int kQLoads = kAttnHeads * HD / kThreads;
     // q's fragments stay in registers beside O, and the next item's q is loaded ahead, where there is room (4 x 128 x
-    // f32, 32000 slots: 37 us, with fragments in registers, and spilled, 64).  What the compiler still spills: head
-    // size 256 without clusters 144 bytes (f32) and 132 (f16), in clusters 8 (f32); f32 of 128 without clusters 12.
+    // f32, 32000 slots, values split by masks: 37 us, with fragments in registers, and spilled, 64).  What the
+    // compiler still spills: head size 256 without clusters 144 bytes (f32) and 132 (f16), in clusters 8 (f32); f32
+    // of 128 without clusters 12.
     static constexpr bool kQRegs = kF16 && HD < 256;
     static constexpr bool kQAhead = kF16 ? HD < 256 : HD < 128;
     static constexpr float kPShift = kF16 ? 12.f : -kLazy;  // weights are kept times 2^kPShift
