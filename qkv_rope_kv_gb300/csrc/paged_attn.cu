@@ -306,9 +306,9 @@ __device__ __forceinline__ void split_tf32(float a, uint32_t& hi, uint32_t& lo) 
     asm("cvt.rn.tf32.f32 %0, %1;" : "=r"(hi) : "f"(a));
     asm("cvt.rn.tf32.f32 %0, %1;" : "=r"(lo) : "f"(a - __uint_as_float(hi)));
 }
-// The same for cache values, the rest cut off, which has the same bound: the splits bound an f32 batch
-// (100 x 4000 slots of 28/4 x 128: 272 us; the rest rounded 276; both cut by a mask, which loses two bits, 297).
-// An infinite value becomes the largest number and an infinite rest, whose products have the same sign; a NaN is two.
+// The same for cache values, the rest cut off, which has the same bound and takes the least time (100 x 4000 slots
+// of 28/4 x 128: 272 us; the rest rounded 276; both cut by a mask, which loses two bits, 297).  An infinite value
+// becomes the largest number and an infinite rest, whose products have the same sign; a NaN becomes two.
 __device__ __forceinline__ void split_tf32_kv(float a, uint32_t& hi, uint32_t& lo) {
     asm("cvt.rn.satfinite.tf32.f32 %0, %1;" : "=r"(hi) : "f"(a));
     lo = __float_as_uint(a - __uint_as_float(hi)) & 0xffffe000u;
