@@ -412,6 +412,63 @@ qkv_status qkv_ffn_graph_create(int32_t hidden, int32_t n_ff, int32_t w_dtype, i
 qkv_status qkv_model_graph_kernel_count(const qkv_graph* graph, int32_t* out);
 void qkv_model_graph_destroy(qkv_graph* graph);
 
+/* ---- rotary positions in other forms --------------------------------------------- */
+
+/* The plan's rotation is the pages' (neox pairs of a whole head, frequencies from one base).  The forms that
+ * other models and longer contexts take, which the pages have no counterpart of, are a qkv_rope:
+ *   pairs d < rot_dim/2 of a head are elements (d, d + rot_dim/2) (QKV_ROPE_NEOX) or (2d, 2d + 1)
+ *   (QKV_ROPE_INTERLEAVED); elements from rot_dim on pass unchanged;
+ *   (x0, x1) -> magnitude * (x0 cos a - x1 sin a, x0 sin a + x1 cos a),  a = position * f_d.
+ * f_d comes from theta^(-2d/rot_dim) by the scaling:
+ *   NONE    itself
+ *   LINEAR  / factor
+ *   BASE    with theta * factor^(rot_dim / (rot_dim - 2)) for theta (rot_dim >= 4)
+ *   RAMP    f / factor * g + f * (1 - g), g rising from 0 to 1 over pair indexes: from floor(at(high)), not below 0,
+ *           to ceil(at(low)), not above rot_dim - 1, at(t) = rot_dim ln(orig_ctx / (2 pi t)) / (2 ln theta) being the
+ *           index whose pair makes t turns over orig_ctx positions (theta > 1; a ramp shorter than 0.001 is that long)
+ *   BANDS   (1 - g) f / factor + g f, g = (orig_ctx f / (2 pi) - low) / (high - low) held within [0, 1]
+ *   TABLE   / divisors[d]
+ * computed in 64 bits and kept as turns a position in units of 2^-64 turn, so the angle, an integer product without its
+ * whole turns, is that of f_d itself at every position, off by 2^-25 of half a turn at most.  (The plan's rotation
+ * rounds position * f_d to f32 first, so the two differ at far positions.)  magnitude is folded into cos and sin. */
+enum { QKV_ROPE_SCALE_NONE = 0, QKV_ROPE_SCALE_LINEAR = 1, QKV_ROPE_SCALE_BASE = 2, QKV_ROPE_SCALE_RAMP = 3,
+       QKV_ROPE_SCALE_BANDS = 4, QKV_ROPE_SCALE_TABLE = 5 };
+typedef struct qkv_rope_desc {
+    int32_t head_dim;  /* 2 .. QKV_MAX_HEAD_DIM */
+    int32_t rot_dim;   /* even, 2 .. head_dim */
+    int32_t layout;    /* QKV_ROPE_NEOX or QKV_ROPE_INTERLEAVED */
+    int32_t scaling;
+    double theta;      /* > 0 */
+    double factor;     /* > 0 (LINEAR, BASE, RAMP, BANDS) */
+    double orig_ctx;   /* > 0 (RAMP, BANDS) */
+    double low, high;  /* 0 < low < high (RAMP, BANDS) */
+    double magnitude;  /* finite, > 0 */
+    const double* divisors; /* host, rot_dim/2 values > 0 (TABLE) */
+} qkv_rope_desc;
+typedef struct qkv_rope qkv_rope;
+/* Host state only, as a plan.  Errors: INVALID_ARG. */
+qkv_status qkv_rope_create(const qkv_rope_desc* desc, qkv_rope** out);
+void qkv_rope_destroy(qkv_rope* rope);
+/* Copy the rot_dim/2 frequencies (radians a position) to host memory. */
+qkv_status qkv_rope_freqs(const qkv_rope* rope, double* out_host, int32_t n);
+
+/* Turn the heads of nt rows by their rows' positions (q and k heads that lie side by side in one call).
+ * inverse: by the opposite angle, with the same magnitude; as the rotation is linear and this its transpose, it takes
+ * the gradient of out to that of x.  f32 arithmetic, one rounding to dtype.  nt == 0 returns QKV_OK without a launch.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype), CUDA. */
+typedef struct qkv_rope_args {
+    const void* x;              /* device, nt rows of n_heads heads of head_dim values */
+    int64_t x_stride;           /* elements from row to row, >= n_heads * head_dim */
+    void* out;                  /* as x; may be x itself (with the same stride where nt > 1) or not overlap it */
+    int64_t out_stride;
+    const int32_t* d_positions; /* device, nt: any values */
+    int32_t dtype;              /* QKV_F32, QKV_BF16 or QKV_F16: of x and out */
+    int32_t nt;
+    int32_t n_heads;            /* >= 1 */
+    int32_t inverse;
+} qkv_rope_args;
+qkv_status qkv_rope_step(const qkv_rope* rope, const qkv_rope_args* args, void* stream);
+
 /* ---- paged cache: store, attention of one new token, eviction ------------------ */
 
 /* The page "07 · The allocator: liveness, buffer reuse, and the KV cache", §2.5, gives one
@@ -469,6 +526,9 @@ typedef struct qkv_paged_store_args {
 } qkv_paged_store_args;
 qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_paged_store_args* args,
                                 void* stream);
+/* The same with `rope` (of the plan's head_dim) in place of the plan's rotation. */
+qkv_status qkv_paged_store_rope_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_rope* rope,
+                                     const qkv_paged_store_args* args, void* stream);
 
 /* Attention of one new token per sequence over its cached slots (the new token's own slot, stored
  * before, among them).  For sequence b and q head h, kv head h / (nh / nkv):

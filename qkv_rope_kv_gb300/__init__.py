@@ -30,6 +30,8 @@ QKV_OK, QKV_ERR_INVALID_ARG, QKV_ERR_UNSUPPORTED, QKV_ERR_POS_RANGE, QKV_ERR_CUD
 QKV_F32, QKV_BF16, QKV_F16 = 0, 1, 2
 QKV_CLASS_CONCAT, QKV_CLASS_MIXED = 0, 1
 QKV_ROPE_NEOX, QKV_ROPE_INTERLEAVED = 0, 1
+QKV_ROPE_SCALE_NONE, QKV_ROPE_SCALE_LINEAR, QKV_ROPE_SCALE_BASE, QKV_ROPE_SCALE_RAMP, QKV_ROPE_SCALE_BANDS, \
+    QKV_ROPE_SCALE_TABLE = range(6)
 QKV_MAX_HEAD_DIM = 256
 
 
@@ -87,8 +89,16 @@ class qkv_paged_kv(ctypes.Structure):
                 ("slot_weight", ctypes.c_void_p), ("slot_pos", ctypes.c_void_p)]
 
 
+class qkv_rope_desc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_ctx", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("magnitude", ctypes.c_double), ("divisors", ctypes.c_void_p)]
+
+
 # qkv_paged_store_args, qkv_attn_args and qkv_evict_args, field by field: packing one and passing its
 # bytes costs a third of converting as many ctypes arguments.
+_ROPE_ARGS = struct.Struct("@PqPqPiiii")
 _STORE_ARGS = struct.Struct("@PqiiPPPPPPPqf4x")
 _ATTN_ARGS = struct.Struct("@PqPPqPPNfiii")
 _EVICT_ARGS = struct.Struct("@PPPPPPNii")
@@ -150,6 +160,11 @@ def _declare(lib):
         "qkv_model_graph_create_qknorm": ([vp, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.POINTER(vp)], st),
         # the args structs, packed into bytes (see _STORE_ARGS and the others)
         "qkv_paged_store_step": ([vp, vp, ctypes.c_char_p, vp], st),
+        "qkv_paged_store_rope_step": ([vp, vp, vp, ctypes.c_char_p, vp], st),
+        "qkv_rope_create": ([ctypes.POINTER(qkv_rope_desc), ctypes.POINTER(vp)], st),
+        "qkv_rope_destroy": ([vp], None),
+        "qkv_rope_freqs": ([vp, vp, i32], st),
+        "qkv_rope_step": ([vp, ctypes.c_char_p, vp], st),
         "qkv_attn_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
         "qkv_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_evict_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
@@ -483,6 +498,73 @@ def _rows(t, name: str, dtype, shape: tuple, device: int):
     _refuse(t, name, dtype, shape, device, "its rows contiguous")
 
 
+def _unpackable(e: Exception):
+    raise QkvError(QKV_ERR_INVALID_ARG, "a number does not fit its argument: %s" % e) from None
+
+
+class Rope:
+    """Owner of a ``qkv_rope*``; destroyed with the object."""
+
+    def __init__(self, handle: int, desc: qkv_rope_desc):
+        import torch
+        self.handle = handle
+        self.head_dim, self.rot_dim = desc.head_dim, desc.rot_dim
+        self.types = {torch.float32: QKV_F32, torch.bfloat16: QKV_BF16, torch.float16: QKV_F16}
+        self.index_type = torch.int32
+        self.current_device, self.current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.qkv_rope_destroy(self.handle)
+            self.handle = None
+
+    def freqs(self):
+        """The frequencies (radians a position) of the rot_dim/2 pairs, numpy float64."""
+        import numpy as np
+        out = np.empty(self.rot_dim // 2, np.float64)
+        _check(_lib.qkv_rope_freqs(self.handle, out.ctypes.data, out.size))
+        return out
+
+
+def qkv_rope_create(head_dim: int, theta: float, rot_dim: int | None = None, layout: int = QKV_ROPE_NEOX,
+                    scaling: int = QKV_ROPE_SCALE_NONE, factor: float = 1.0, orig_ctx: float = 0.0, low: float = 0.0,
+                    high: float = 0.0, magnitude: float = 1.0, divisors=None) -> Rope:
+    """Rotary positions in a form of their own (see qkv.h): all of a head (``rot_dim`` None) or its first part, half or
+    interleaved pairs, frequencies scaled; ``divisors``: rot_dim/2 numbers (QKV_ROPE_SCALE_TABLE)."""
+    load()
+    rot_dim = head_dim if rot_dim is None else rot_dim
+    table = None
+    if divisors is not None:
+        table = (ctypes.c_double * len(divisors))(*divisors)
+        if len(divisors) != rot_dim // 2:
+            raise QkvError(QKV_ERR_INVALID_ARG, "divisors must be rot_dim/2 = %d numbers (got %d)" % (rot_dim // 2,
+                                                                                                 len(divisors)))
+    d = qkv_rope_desc(head_dim, rot_dim, layout, scaling, theta, factor, orig_ctx, low, high, magnitude,
+                      ctypes.cast(table, ctypes.c_void_p))
+    h = ctypes.c_void_p()
+    _check(_lib.qkv_rope_create(ctypes.byref(d), ctypes.byref(h)))
+    return Rope(h.value, d)
+
+
+def qkv_rope_step(rope: Rope, x, positions, out, inverse: bool = False, stream=None):
+    """Turn the heads of x [nt, n_heads * head_dim] (f32, bf16 or f16; rows may be strided) by ``positions`` (int32
+    [nt]) into out, which may be x itself; ``inverse`` turns back, which takes out's gradient to x's."""
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    kind = rope.types.get(dtype)
+    if kind is None or dev < 0 or len(shape) != 2 or shape[1] == 0 or shape[1] % rope.head_dim:
+        raise QkvError(QKV_ERR_INVALID_ARG, "x must be a CUDA tensor [nt, n_heads * %d] of f32, bf16 or f16; got %s of %s "
+                       "on %s" % (rope.head_dim, dtype, tuple(shape), x.device))
+    if rope.current_device() != dev:
+        raise QkvError(QKV_ERR_INVALID_ARG, "x is on cuda:%d, the current device is cuda:%d: use torch.cuda.device()"
+                       % (dev, rope.current_device()))
+    nt, width = shape
+    src, src_stride = _rows(x, "x", dtype, shape, dev)
+    to, to_stride = _rows(out, "out", dtype, shape, dev)
+    args = _ROPE_ARGS.pack(src, src_stride, to, to_stride, _tensor(positions, "positions", rope.index_type, (nt,), dev),
+                           kind, nt, width // rope.head_dim, bool(inverse))
+    _check(_lib.qkv_rope_step(rope.handle, args, rope.current_stream(dev) if stream is None else _stream(stream)))
+
+
 class PagedKv:
     """A ``qkv_paged_kv`` over torch tensors, which it keeps alive: pools ``k`` and ``v``
     [n_pages, page_size, nkt] of the plan's cache type (pages may be strided, both alike),
@@ -532,21 +614,13 @@ class PagedKv:
         return self._current_stream(self.device) if stream is None else _stream(stream)
 
 
-def _unpackable(e: Exception):
-    raise QkvError(QKV_ERR_INVALID_ARG, "a number does not fit its argument: %s" % e) from None
-
-
 def _workspace(t, device: int):
     if t is None:
         return 0, 0
     return _tensor(t, "workspace", t.dtype, t.shape, device), t.nbytes
 
 
-def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps: float, positions, seqs, slots,
-                         q, stream=None):
-    """Finish the projections Y [nt, R] (f32 or bf16; rows may be strided) of tokens of any
-    sequences: bias, optional q/k norms, rotation, q [nt, nqt] f32 out, k and v into the cache.
-    ``bias``, the norm weights (together), ``seqs`` and ``slots`` may be None (see qkv.h)."""
+def _store_args(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q) -> bytes:
     f32, i32, bf16 = cache.types
     dev, y_type, head = cache.device, Y.dtype, (plan.head_dim,)
     nt = Y.shape[0]
@@ -554,14 +628,29 @@ def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w
     to, to_stride = _rows(q, "q", f32, (nt, plan.nqt), dev)
     nt_shape = (nt,)
     try:
-        args = _STORE_ARGS.pack(
+        return _STORE_ARGS.pack(
             y, y_stride, QKV_BF16 if y_type is bf16 else QKV_F32, nt, _tensor(bias, "bias", f32, (plan.rows,), dev),
             _tensor(q_norm_w, "q_norm_w", f32, head, dev), _tensor(k_norm_w, "k_norm_w", f32, head, dev),
             _tensor(positions, "positions", i32, nt_shape, dev), _tensor(seqs, "seqs", i32, nt_shape, dev),
             _tensor(slots, "slots", i32, nt_shape, dev), to, to_stride, eps)
     except (struct.error, OverflowError) as e:
         _unpackable(e)
+
+
+def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps: float, positions, seqs, slots,
+                         q, stream=None):
+    """Finish the projections Y [nt, R] (f32 or bf16; rows may be strided) of tokens of any
+    sequences: bias, optional q/k norms, rotation, q [nt, nqt] f32 out, k and v into the cache.
+    ``bias``, the norm weights (together), ``seqs`` and ``slots`` may be None (see qkv.h)."""
+    args = _store_args(plan, cache, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q)
     _check(_lib.qkv_paged_store_step(plan.handle, cache.address, args, cache._on(plan, stream)))
+
+
+def qkv_paged_store_rope_step(plan: Plan, cache: PagedKv, rope: Rope, Y, bias, q_norm_w, k_norm_w, eps: float, positions,
+                              seqs, slots, q, stream=None):
+    """qkv_paged_store_step with ``rope`` in place of the plan's rotation."""
+    args = _store_args(plan, cache, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q)
+    _check(_lib.qkv_paged_store_rope_step(plan.handle, cache.address, rope.handle, args, cache._on(plan, stream)))
 
 
 def qkv_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:

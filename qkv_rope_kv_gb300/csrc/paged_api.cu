@@ -91,8 +91,10 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 }  // namespace
 
-extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
-                                           const qkv_paged_store_args* a, void* stream) {
+namespace {
+
+qkv_status paged_store(const qkv_plan* plan, const qkv_paged_kv* cache, const RopeTable* rope,
+                       const qkv_paged_store_args* a, void* stream) {
     PagedStoreParams p;
     std::memset(&p, 0, sizeof p);
     qkv_status st = view(plan, cache, &p.c);
@@ -135,9 +137,25 @@ extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged
     p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
     p.inv_hd = 1.f / static_cast<float>(p.hd);
     std::memcpy(p.inv_freq, plan->inv_freq, sizeof p.inv_freq);
-    const cudaError_t e = launch_paged_store(p, a->y_dtype, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_paged_store(p, rope, a->y_dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged store kernel launch");
     return QKV_OK;
+}
+
+}  // namespace
+
+extern "C" qkv_status qkv_paged_store_step(const qkv_plan* plan, const qkv_paged_kv* cache,
+                                           const qkv_paged_store_args* a, void* stream) {
+    return paged_store(plan, cache, nullptr, a, stream);
+}
+
+extern "C" qkv_status qkv_paged_store_rope_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_rope* rope,
+                                                const qkv_paged_store_args* a, void* stream) {
+    REQUIRE(plan, "plan is null");
+    REQUIRE(rope, "rope is null");
+    REQUIRE(rope->head_dim == plan->d.head_dim, "the rope is for heads of %d, the plan has heads of %d", rope->head_dim,
+            plan->d.head_dim);
+    return paged_store(plan, cache, &rope->table, a, stream);
 }
 
 extern "C" qkv_status qkv_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out) {

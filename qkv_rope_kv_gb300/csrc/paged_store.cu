@@ -11,58 +11,17 @@
 #include "epilogue_math.cuh"
 #include "paged_common.cuh"
 #include "ptx_sync.cuh"
+#include "rope_math.cuh"
 
 namespace {
 
 using namespace qkv_epi;
 using namespace qkv_paged;
+using namespace qkv_rope_math;
 
 constexpr int kThreads = 256;
 // Tokens of one CTA: what fits 64 registers, so four CTAs on an SM (bf16 rows 62; f32 rows spill 76 bytes).
 constexpr int kMaxTokens = 3;
-
-// Four neighbouring values as two packed f32 pairs: one instruction works on both of a pair, with each
-// result rounded as its scalar form is.
-using u64 = unsigned long long;
-struct Quad {
-    u64 a, b;
-};
-__device__ __forceinline__ u64 pack(float x, float y) {
-    u64 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 unpack(u64 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ u64 add2(u64 x, u64 y) {
-    u64 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ u64 mul2(u64 x, u64 y) {
-    u64 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ u64 fma2(u64 x, u64 y, u64 z) {
-    u64 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-// (x0 c - x1 s, x0 s + x1 c) of two pairs, each product and the sum rounded.  Both sums are written as
-// x - y = fma(y, -1, x): the assembler joins a packed add with the product before it into one fma.
-__device__ __forceinline__ void rotate2(u64 x0, u64 x1, u64 c, u64 s, u64& r0, u64& r1) {
-    const u64 minus = pack(-1.f, -1.f), neg_s = s ^ 0x8000000080000000ull;
-    r0 = fma2(mul2(x1, s), minus, mul2(x0, c));
-    r1 = fma2(mul2(x0, neg_s), minus, mul2(x1, c));
-}
-__device__ __forceinline__ Quad quad(const float* p) {  // 16-byte aligned
-    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
-    return {v.x, v.y};
-}
 
 // Four neighbouring values of Y as loaded.  Plain loads, not read-only ones: q may be written over Y.
 template <typename YT>
@@ -102,6 +61,22 @@ __device__ __forceinline__ float head_inv(const PagedStoreParams& p, float ss) {
     return rsqrtf(__fadd_rn(__fmul_rn(ss, p.inv_hd), p.eps));
 }
 
+// The rotation: the plan's, or a qkv_rope's with its pairs half a head apart or neighbours.
+enum Form { kPlan, kHalves, kNeighbours };
+template <Form F>
+struct Rotation {  // what the parameters do not hold of it
+    RopeTable table;
+    __device__ __forceinline__ int rot(const PagedStoreParams&) const { return table.rot; }
+    __device__ __forceinline__ float2 at(const PagedStoreParams&, int pos, int d) const { return cos_sin(table, pos, d); }
+};
+template <>
+struct Rotation<kPlan> {
+    __device__ __forceinline__ int rot(const PagedStoreParams& p) const { return p.hd; }
+    __device__ __forceinline__ float2 at(const PagedStoreParams& p, int pos, int d) const {
+        return rope_cos_sin(pos, p.inv_freq[d]);
+    }
+};
+
 // Where the CTA's tokens go: row offsets (-1: not stored), sequences and slots.
 struct Tokens {
     int64_t row[kMaxTokens];
@@ -109,10 +84,11 @@ struct Tokens {
 };
 
 // Look up the CTA's tokens and make the (cos, sin) of their pairs.
-__device__ __forceinline__ void token_tables(const PagedStoreParams& p, int t0, int nt, Tokens& tk,
+template <Form F>
+__device__ __forceinline__ void token_tables(const PagedStoreParams& p, const Rotation<F>& r, int t0, int nt, Tokens& tk,
                                              float (*cos_s)[QKV_MAX_HEAD_DIM / 2],
                                              float (*sin_s)[QKV_MAX_HEAD_DIM / 2]) {
-    const int half = p.hd >> 1;
+    const int half = r.rot(p) >> 1;
     if (threadIdx.x < nt) {
         const int t = t0 + threadIdx.x;
         const int pos = p.positions[t];
@@ -132,7 +108,7 @@ __device__ __forceinline__ void token_tables(const PagedStoreParams& p, int t0, 
     }
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = i / half, d = i - t * half;
-        const float2 cs = rope_cos_sin(p.positions[t0 + t], p.inv_freq[d]);
+        const float2 cs = r.at(p, p.positions[t0 + t], d);
         cos_s[t][d] = cs.x;
         sin_s[t][d] = cs.y;
     }
@@ -148,28 +124,34 @@ __device__ __forceinline__ void track_slot(const PagedStoreParams& p, const Toke
 // LP lanes work on one head, four neighbouring pairs a lane (LP: the power of two at or above hd / 8; the
 // lanes beyond idle).  A group keeps its head for the CTA's T tokens, so bias, norm weight and addresses are
 // made once, and the loads of all T (of the next head, as each is used) are in flight together.
-template <typename YT, int T>
-__global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_constant__ PagedStoreParams p, int lp,
+// (Of a qkv_rope's halves, the values that pass go by eight neighbours a lane; so do all where pairs are neighbours.)
+template <typename YT, int T, Form F>
+__global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_constant__ PagedStoreParams p,
+                                                               const __grid_constant__ Rotation<F> r, int lp,
                                                                int heads_per_cta) {
     __shared__ __align__(16) float cos_s[T][QKV_MAX_HEAD_DIM / 2], sin_s[T][QKV_MAX_HEAD_DIM / 2];
     __shared__ Tokens tk;
     qkv_ptx::griddep_wait();
     qkv_ptx::griddep_launch_dependents();
-    const int half = p.hd >> 1;
+    const int rot = r.rot(p);
     const int t0 = blockIdx.x * T, nt = min(T, p.nt - t0);
     const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
-    const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp, d = 4 * l;
+    const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp;
     int h = blockIdx.y * heads_per_cta + g;
-    const YT* y = static_cast<const YT*>(p.y) + t0 * p.y_stride + static_cast<int64_t>(h) * p.hd + d;
+    const bool wide = 8 * l < p.hd;  // a lane that has values
+    const bool turned = 8 * l < rot;
+    int d0 = 4 * l, d1 = rot / 2 + 4 * l;  // its two quads
+    if (F != kPlan) lane_quads<F == kNeighbours>(l, rot, d0, d1);
+    const int apart = d1 - d0;
+    const YT* y = static_cast<const YT*>(p.y) + t0 * p.y_stride + static_cast<int64_t>(h) * p.hd + d0;
     Raw4<YT> n0[T], n1[T];
-    const bool wide = d < half;  // a lane that has pairs
 #pragma unroll
     for (int t = 0; t < T; ++t)
         if (wide && h < end && t < nt) {
             n0[t].load(y + t * p.y_stride);
-            n1[t].load(y + t * p.y_stride + half);
+            n1[t].load(y + t * p.y_stride + apart);
         }
-    token_tables(p, t0, nt, tk, cos_s, sin_s);
+    token_tables(p, r, t0, nt, tk, cos_s, sin_s);
     __syncthreads();
     int64_t rows[T];
     bool here[T];  // a token that is no padding
@@ -183,15 +165,15 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
     for (int h_first = blockIdx.y * heads_per_cta; h_first < end; h_first += groups, h += groups) {
         const bool live = wide && h < end, ahead = wide && h + groups < end;
         const int sec = h < p.nh ? 0 : h < p.nh + p.nkv ? 1 : 2;
-        const int j = (sec == 0 ? h : sec == 1 ? h - p.nh : h - p.nh - p.nkv) * p.hd + d;  // within the section
+        const int j = (sec == 0 ? h : sec == 1 ? h - p.nh : h - p.nh - p.nkv) * p.hd + d0;  // within the section
         Quad b0 = {0, 0}, b1 = {0, 0}, w0 = {0, 0}, w1 = {0, 0};
         if (live && p.bias) {
-            b0 = quad(p.bias + static_cast<int64_t>(h) * p.hd + d);
-            b1 = quad(p.bias + static_cast<int64_t>(h) * p.hd + half + d);
+            b0 = quad(p.bias + static_cast<int64_t>(h) * p.hd + d0);
+            b1 = quad(p.bias + static_cast<int64_t>(h) * p.hd + d1);
         }
         if (live && norm && sec != 2) {
-            w0 = quad(p.norm_w[sec] + d);
-            w1 = quad(p.norm_w[sec] + half + d);
+            w0 = quad(p.norm_w[sec] + d0);
+            w1 = quad(p.norm_w[sec] + d1);
         }
         y += static_cast<int64_t>(groups) * p.hd;
         float* q = p.q + t0 * p.q_stride + j;
@@ -205,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
             }
             if (ahead && t < nt) {
                 n0[t].load(y + t * p.y_stride);
-                n1[t].load(y + t * p.y_stride + half);
+                n1[t].load(y + t * p.y_stride + apart);
             }
             if (p.bias) {
                 x0 = {add2(x0.a, b0.a), add2(x0.b, b0.b)};
@@ -223,20 +205,24 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
                 }
             }
             if (!live || !here[t]) continue;
-            if (sec != 2) {
-                const Quad c = quad(cos_s[t] + d), s = quad(sin_s[t] + d);
-                Quad r0, r1;
-                rotate2(x0.a, x1.a, c.a, s.a, r0.a, r1.a);
-                rotate2(x0.b, x1.b, c.b, s.b, r0.b, r1.b);
-                x0 = r0;
-                x1 = r1;
+            if (sec != 2 && (F == kPlan || turned)) {
+                const Quad c = quad(cos_s[t] + 4 * l), s = quad(sin_s[t] + 4 * l);
+                if (F == kNeighbours) {
+                    rotate_neighbours(x0, x1, c, s);
+                } else {
+                    Quad r0, r1;
+                    rotate2(x0.a, x1.a, c.a, s.a, r0.a, r1.a);
+                    rotate2(x0.b, x1.b, c.b, s.b, r0.b, r1.b);
+                    x0 = r0;
+                    x1 = r1;
+                }
             }
             if (sec == 0) {
                 *reinterpret_cast<ulonglong2*>(q + t * p.q_stride) = make_ulonglong2(x0.a, x0.b);
-                *reinterpret_cast<ulonglong2*>(q + t * p.q_stride + half) = make_ulonglong2(x1.a, x1.b);
+                *reinterpret_cast<ulonglong2*>(q + t * p.q_stride + apart) = make_ulonglong2(x1.a, x1.b);
             } else if (rows[t] >= 0) {
                 kv_put4(kv, p.kv_f16, rows[t] + j, x0);
-                kv_put4(kv, p.kv_f16, rows[t] + j + half, x1);
+                kv_put4(kv, p.kv_f16, rows[t] + j + apart, x1);
                 if (sec == 1 && l == 0) track_slot(p, tk, t, h - p.nh);
             }
         }
@@ -244,16 +230,17 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
 }
 
 // Any even hd, any alignment: a warp strides over a head's pairs one by one; a token a CTA row.
-template <typename YT>
+template <typename YT, Form F>
 __global__ void __launch_bounds__(kThreads) paged_store_any_kernel(const __grid_constant__ PagedStoreParams p,
+                                                                   const __grid_constant__ Rotation<F> r,
                                                                    int heads_per_cta) {
     __shared__ float cos_s[1][QKV_MAX_HEAD_DIM / 2], sin_s[1][QKV_MAX_HEAD_DIM / 2];
     __shared__ Tokens tk;
     qkv_ptx::griddep_wait();
     qkv_ptx::griddep_launch_dependents();
-    const int half = p.hd >> 1, t = blockIdx.x, lane = threadIdx.x & 31;
+    const int half = p.hd >> 1, turn = r.rot(p) >> 1, t = blockIdx.x, lane = threadIdx.x & 31;
     const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
-    token_tables(p, t, 1, tk, cos_s, sin_s);
+    token_tables(p, r, t, 1, tk, cos_s, sin_s);
     __syncthreads();
     if (tk.seq[0] < 0) return;
     const int64_t row = tk.row[0];
@@ -276,27 +263,35 @@ __global__ void __launch_bounds__(kThreads) paged_store_any_kernel(const __grid_
             inv = head_inv(p, ss);
         }
         for (int d = lane; d < half; d += 32) {
-            float z0 = load1(y + d), z1 = load1(y + half + d);
+            // the pair's two values; behind the last pair, two that pass
+            int d0 = d, d1 = turn + d;
+            if (F == kNeighbours || (F == kHalves && d >= turn)) {
+                d0 = 2 * d;
+                d1 = 2 * d + 1;
+            }
+            float z0 = load1(y + d0), z1 = load1(y + d1);
             if (b) {
-                z0 = __fadd_rn(z0, __ldg(b + d));
-                z1 = __fadd_rn(z1, __ldg(b + half + d));
+                z0 = __fadd_rn(z0, __ldg(b + d0));
+                z1 = __fadd_rn(z1, __ldg(b + d1));
             }
             if (sec != 2) {
                 if (w) {
-                    z0 = __fmul_rn(__fmul_rn(z0, inv), __ldg(w + d));
-                    z1 = __fmul_rn(__fmul_rn(z1, inv), __ldg(w + half + d));
+                    z0 = __fmul_rn(__fmul_rn(z0, inv), __ldg(w + d0));
+                    z1 = __fmul_rn(__fmul_rn(z1, inv), __ldg(w + d1));
                 }
-                float r0, r1;
-                rope_rotate_cs(z0, z1, make_float2(cos_s[0][d], sin_s[0][d]), r0, r1);
-                z0 = r0;
-                z1 = r1;
+                if (F == kPlan || d < turn) {
+                    float r0, r1;
+                    rope_rotate_cs(z0, z1, make_float2(cos_s[0][d], sin_s[0][d]), r0, r1);
+                    z0 = r0;
+                    z1 = r1;
+                }
             }
             if (sec == 0) {
-                q[d] = z0;
-                q[half + d] = z1;
+                q[d0] = z0;
+                q[d1] = z1;
             } else if (row >= 0) {
-                kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + d), z0);
-                kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + half + d), z1);
+                kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + d0), z0);
+                kv_put(kv, p.kv_f16, static_cast<size_t>(row + j0 + d1), z1);
             }
         }
         if (lane == 0 && sec == 1 && row >= 0) track_slot(p, tk, 0, h - p.nh);
@@ -305,10 +300,10 @@ __global__ void __launch_bounds__(kThreads) paged_store_any_kernel(const __grid_
 
 bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-template <typename YT>
-cudaError_t launch_t(const PagedStoreParams& p, cudaStream_t stream) {
+template <typename YT, Form F>
+cudaError_t launch_t(const PagedStoreParams& p, const Rotation<F>& r, bool eights, cudaStream_t stream) {
     const int ys = sizeof(YT), es = p.kv_f16 ? 2 : 4;
-    const bool vec = p.hd % 8 == 0 && aligned(p.y, 4 * ys) && p.y_stride % 4 == 0 && aligned(p.bias, 16) &&
+    const bool vec = p.hd % 8 == 0 && eights && aligned(p.y, 4 * ys) && p.y_stride % 4 == 0 && aligned(p.bias, 16) &&
                      aligned(p.norm_w[0], 16) && aligned(p.norm_w[1], 16) && aligned(p.q, 16) &&
                      p.q_stride % 4 == 0 && aligned(p.c.k, 4 * es) && aligned(p.c.v, 4 * es) &&
                      p.c.page_stride % 4 == 0;
@@ -321,15 +316,20 @@ cudaError_t launch_t(const PagedStoreParams& p, cudaStream_t stream) {
     int per = heads;
     while (!many && per > kThreads / lp && static_cast<int64_t>(p.nt) * ((heads + per - 1) / per) < kSms) per = (per + 1) / 2;
     const dim3 grid((p.nt + tokens - 1) / tokens, (heads + per - 1) / per);
-    if (!vec) return launch_dependent(paged_store_any_kernel<YT>, grid, kThreads, 0, stream, 1, p, per);
-    return launch_dependent(many ? paged_store_kernel<YT, kMaxTokens> : paged_store_kernel<YT, 1>, grid, kThreads, 0,
-                            stream, 1, p, lp, per);
+    if (!vec) return launch_dependent(paged_store_any_kernel<YT, F>, grid, kThreads, 0, stream, 1, p, r, per);
+    return launch_dependent(many ? paged_store_kernel<YT, kMaxTokens, F> : paged_store_kernel<YT, 1, F>, grid, kThreads,
+                            0, stream, 1, p, r, lp, per);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_store(const PagedStoreParams& p, int y_dtype, cudaStream_t stream) {
-    return y_dtype == QKV_BF16 ? launch_t<uint16_t>(p, stream) : launch_t<float>(p, stream);
+cudaError_t launch_paged_store(const PagedStoreParams& p, const RopeTable* rope, int y_dtype, cudaStream_t stream) {
+    const bool bf16 = y_dtype == QKV_BF16;
+    if (!rope) return (bf16 ? launch_t<uint16_t, kPlan> : launch_t<float, kPlan>)(p, {}, true, stream);
+    const bool eights = rope->rot % 8 == 0;  // a lane's eight values all turn or all pass
+    if (rope->neighbours)
+        return (bf16 ? launch_t<uint16_t, kNeighbours> : launch_t<float, kNeighbours>)(p, {*rope}, eights, stream);
+    return (bf16 ? launch_t<uint16_t, kHalves> : launch_t<float, kHalves>)(p, {*rope}, eights, stream);
 }
 
 cudaError_t paged_store_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {

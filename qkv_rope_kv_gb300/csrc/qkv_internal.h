@@ -14,6 +14,19 @@ struct qkv_plan {
     float inv_freq[QKV_MAX_HEAD_DIM / 2];
 };
 
+// A qkv_rope as a launch carries it.
+struct RopeTable {
+    unsigned long long turns[QKV_MAX_HEAD_DIM / 2];  // of each pair a position, in 2^-64 turn
+    float magnitude;
+    int32_t rot;         // values of a head that are turned, from the first on
+    int32_t neighbours;  // pairs (2d, 2d + 1), else (d, d + rot / 2)
+};
+struct qkv_rope {
+    RopeTable table;
+    int32_t head_dim;
+    double freq[QKV_MAX_HEAD_DIM / 2];
+};
+
 // Everything one decode-layer launch needs, passed by value (__grid_constant__),
 // so a captured graph node carries its own copy.
 struct DecodeParams {
@@ -89,6 +102,17 @@ struct PrefillParams {
 qkv_status launch_prefill(const PrefillParams& p, bool pdl, cudaStream_t stream, const char** why);
 cudaError_t prefill_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad_pos);
 
+// rope.cu
+struct RopeParams {
+    RopeTable rope;
+    const void* x;
+    void* out;
+    int64_t x_stride, out_stride;
+    const int32_t* positions;
+    int32_t nt, n_heads, hd, inverse;
+};
+cudaError_t launch_rope(const RopeParams& p, int dtype, cudaStream_t stream);
+
 // ---- paged cache (paged_store.cu, paged_attn.cu, paged_evict.cu)
 
 // qkv_paged_kv as a launch carries it, with the plan's row width.
@@ -119,7 +143,8 @@ struct PagedStoreParams {
     float inv_hd;  // 1 / hd
     float inv_freq[QKV_MAX_HEAD_DIM / 2];
 };
-cudaError_t launch_paged_store(const PagedStoreParams& p, int y_dtype, cudaStream_t stream);
+// With `rope` (or null) in place of the plan's rotation.
+cudaError_t launch_paged_store(const PagedStoreParams& p, const RopeTable* rope, int y_dtype, cudaStream_t stream);
 cudaError_t paged_store_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
 
 // Workspace of qkv_attn_step.  The counters come first, in a place that no shape moves, so one
