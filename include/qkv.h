@@ -564,6 +564,67 @@ typedef struct qkv_attn_args {
 qkv_status qkv_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out);
 qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_attn_args* args, void* stream);
 
+/* Attention of several new tokens per sequence over its cached slots (the new tokens' own slots, stored before, among
+ * them): a prompt, a part of one behind what is cached, or drafted tokens.  Sequence b's new tokens are rows
+ * d_first[b] .. d_first[b + 1] - 1 of q and its last slots: of n new tokens and a length of len, token i sees
+ *   the slots j in [max(0, e - window), e),  e = len - n + i + 1  (window 0: from 0),
+ * and out and lse are those of qkv_attn_step, row by row.  A token with e <= 0 gets zeros (lse -inf).  What lies in slots
+ * that a token does not see, infinities and NaN too, does not change its row.
+ * d_first must not decrease; a pair that does, or lies outside [0, nt], is flagged (bit 2) and its sequence skipped.
+ * Rows before d_first[0] and from d_first[n_seq] on are left as they were.
+ * Scores, softmax and sums are f32.  With out F32, q, the softmax weights and an f32 cache's rows keep 22 bits or more;
+ * with out BF16 and an f16 cache, q (scaled by a power of two for each row) and the softmax weights are rounded to f16,
+ * 2^-11 of themselves at most: less than out's own rounding as long as |scale| * sum_d |q_d K_d| stays below about 8.
+ * |V| (f32) times the number of slots is to stay below the largest f32.
+ * Work is split over the GPU and joined in a fixed order: results do not depend on timing.  The workspace may hold
+ * anything and is not shared by calls that overlap on the GPU.
+ * Errors: INVALID_ARG, UNSUPPORTED (out_dtype, n_head % n_head_kv != 0), CUDA. */
+typedef struct qkv_prompt_attn_args {
+    const float* q;         /* device, nt rows of nqt floats */
+    int64_t q_stride;       /* elements from row to row, >= nqt */
+    const int32_t* d_first; /* device, n_seq + 1 */
+    const int32_t* d_lens;  /* device, n_seq; an out-of-range length counts as 0 */
+    void* out;              /* device, nt rows of nqt values of out_dtype; must not overlap q */
+    int64_t out_stride;     /* >= nqt */
+    float* lse;             /* device, nt x nh, or null */
+    void* d_workspace;      /* device, qkv_prompt_attn_workspace_bytes bytes, 16-byte aligned */
+    size_t workspace_bytes;
+    float scale;
+    int32_t window;         /* slots, 0: no window */
+    int32_t out_dtype;      /* QKV_F32 or QKV_BF16 (rounded once) */
+    int32_t nt;             /* >= 0; 0 returns QKV_OK without a launch */
+} qkv_prompt_attn_args;
+qkv_status qkv_prompt_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, int32_t nt, size_t* out);
+qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* args,
+                                void* stream);
+
+/* qkv_attn_step (without window and add_weight) for sequences that begin alike: the first d_prefix_len[b] slots of
+ * sequence b are those of sequence d_share[b] and are read through that one's row of the page table, once for all
+ * neighbouring sequences with the same d_share (a sequence that shares nothing names itself, with any prefix length).
+ * The slots from there to d_lens[b] are read through b's own row, whose entries below may hold anything.  A prefix
+ * need not end on a page's border, nor a sequence's length reach its prefix's end: it then sees only so many of its slots.
+ * A d_prefix_len outside [0, capacity] is flagged (bit 2) and counts as 0; a d_share outside [0, n_seq) is flagged and
+ * the prefix's slots are not seen.  Numerics as qkv_prompt_attn_step for the prefix, as qkv_attn_step for the rest.  The
+ * workspace's first 4096 bytes are as in qkv_attn_step: zero before the first call, and left usable.
+ * Errors: INVALID_ARG, UNSUPPORTED (out_dtype, n_head % n_head_kv != 0), CUDA. */
+typedef struct qkv_prefix_attn_args {
+    const float* q;         /* device, n_seq rows of nqt floats */
+    int64_t q_stride;       /* elements from row to row, >= nqt */
+    const int32_t* d_lens;  /* device, n_seq: slots of each, the prefix's among them; an out-of-range length counts as 0 */
+    const int32_t* d_share; /* device, n_seq */
+    const int32_t* d_prefix_len; /* device, n_seq */
+    void* out;              /* device, n_seq rows of nqt values of out_dtype; must not overlap q */
+    int64_t out_stride;     /* >= nqt */
+    float* lse;             /* device, n_seq x nh, or null */
+    void* d_workspace;      /* device, qkv_prefix_attn_workspace_bytes bytes, 16-byte aligned */
+    size_t workspace_bytes;
+    float scale;
+    int32_t out_dtype;      /* QKV_F32 or QKV_BF16 (rounded once) */
+} qkv_prefix_attn_args;
+qkv_status qkv_prefix_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out);
+qkv_status qkv_prefix_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prefix_attn_args* args,
+                                void* stream);
+
 /* Cut every sequence longer than `budget` slots down to budget, per kv head: kept are the slots
  * whose position is >= d_next_pos[b] - recent (of more than budget such: the lowest slots), then those
  * with the largest slot_weight (equal weights: the lowest slot first; a NaN counts as larger than any

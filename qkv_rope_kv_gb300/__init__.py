@@ -101,6 +101,8 @@ class qkv_rope_desc(ctypes.Structure):
 _ROPE_ARGS = struct.Struct("@PqPqPiiii")
 _STORE_ARGS = struct.Struct("@PqiiPPPPPPPqf4x")
 _ATTN_ARGS = struct.Struct("@PqPPqPPNfiii")
+_PROMPT_ARGS = struct.Struct("@PqPPPqPPNfiii")
+_PREFIX_ARGS = struct.Struct("@PqPPPPqPPNfi")
 _EVICT_ARGS = struct.Struct("@PPPPPPNii")
 
 _lock = threading.Lock()
@@ -167,6 +169,10 @@ def _declare(lib):
         "qkv_rope_step": ([vp, ctypes.c_char_p, vp], st),
         "qkv_attn_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
         "qkv_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
+        "qkv_prompt_attn_workspace_bytes": ([vp, vp, i32, ctypes.POINTER(sz)], st),
+        "qkv_prompt_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
+        "qkv_prefix_attn_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
+        "qkv_prefix_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_evict_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
         "qkv_evict_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_model_graph_destroy": ([vp], None),
@@ -676,6 +682,57 @@ def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, worksp
     except (struct.error, OverflowError) as e:
         _unpackable(e)
     _check(_lib.qkv_attn_step(plan.handle, cache.address, args, cache._on(plan, stream)))
+
+
+def qkv_prompt_attn_workspace_bytes(plan: Plan, cache: PagedKv, nt: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.qkv_prompt_attn_workspace_bytes(plan.handle, cache.address, nt, ctypes.byref(out)))
+    return out.value
+
+
+def qkv_prompt_attn_step(plan: Plan, cache: PagedKv, q, first, lens, scale: float, out, workspace, window: int = 0,
+                         lse=None, stream=None):
+    """Attention of several new tokens per sequence, each up to its own slot: q [nt, nqt] f32, sequence b's tokens in rows
+    first[b] .. first[b + 1] - 1 (int32 [n_seq + 1]), over the cached slots of each (``lens`` int32 [n_seq]) into out
+    [nt, nqt] (f32 or bf16) and lse [nt, n_head] (f32).  ``workspace``: qkv_prompt_attn_workspace_bytes device bytes."""
+    f32, i32, bf16 = cache.types
+    dev, out_type, nt = cache.device, out.dtype, q.shape[0]
+    x, x_stride = _rows(q, "q", f32, (nt, plan.nqt), dev)
+    to, to_stride = _rows(out, "out", bf16 if out_type is bf16 else f32, (nt, plan.nqt), dev)
+    try:
+        args = _PROMPT_ARGS.pack(
+            x, x_stride, _tensor(first, "first", i32, (cache.n_seq + 1,), dev),
+            _tensor(lens, "lens", i32, cache.per_seq, dev), to, to_stride, _tensor(lse, "lse", f32, (nt, plan.n_head), dev),
+            *_workspace(workspace, dev), scale, window, QKV_BF16 if out_type is bf16 else QKV_F32, nt)
+    except (struct.error, OverflowError) as e:
+        _unpackable(e)
+    _check(_lib.qkv_prompt_attn_step(plan.handle, cache.address, args, cache._on(plan, stream)))
+
+
+def qkv_prefix_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.qkv_prefix_attn_workspace_bytes(plan.handle, cache.address, ctypes.byref(out)))
+    return out.value
+
+
+def qkv_prefix_attn_step(plan: Plan, cache: PagedKv, q, lens, share, prefix_len, scale: float, out, workspace, lse=None,
+                         stream=None):
+    """qkv_attn_step for sequences that begin alike: the first ``prefix_len[b]`` slots of sequence b are those of sequence
+    ``share[b]`` (int32 [n_seq] each) and are read once for neighbours with the same ``share``.  ``workspace``:
+    qkv_prefix_attn_workspace_bytes device bytes, the first 4096 of them zero; it stays usable."""
+    f32, i32, bf16 = cache.types
+    dev, out_type, B, shape = cache.device, out.dtype, cache.per_seq, (cache.n_seq, plan.nqt)
+    x, x_stride = _rows(q, "q", f32, shape, dev)
+    to, to_stride = _rows(out, "out", bf16 if out_type is bf16 else f32, shape, dev)
+    try:
+        args = _PREFIX_ARGS.pack(
+            x, x_stride, _tensor(lens, "lens", i32, B, dev), _tensor(share, "share", i32, B, dev),
+            _tensor(prefix_len, "prefix_len", i32, B, dev), to, to_stride,
+            _tensor(lse, "lse", f32, (cache.n_seq, plan.n_head), dev), *_workspace(workspace, dev), scale,
+            QKV_BF16 if out_type is bf16 else QKV_F32)
+    except (struct.error, OverflowError) as e:
+        _unpackable(e)
+    _check(_lib.qkv_prefix_attn_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 
 def qkv_evict_workspace_bytes(plan: Plan, cache: PagedKv) -> int:

@@ -1,6 +1,6 @@
 // C-ABI layer of the paged-cache entry points: argument validation and workspace layout
-// (include/qkv.h has the contracts; the kernels are in paged_store.cu, paged_attn.cu and
-// paged_evict.cu).
+// (include/qkv.h has the contracts; the kernels are in paged_store.cu, paged_attn.cu,
+// paged_evict.cu and paged_rows*.cu).
 #include <cmath>
 #include <cstring>
 
@@ -216,6 +216,223 @@ extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* ca
     p.kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
     const cudaError_t e = launch_paged_attn(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel launch");
+    return QKV_OK;
+}
+
+namespace {
+
+// What the attention of many rows takes from plan and cache; `nt` q rows.
+void rows_params(const qkv_plan* plan, int32_t nt, PagedRowsParams* p) {
+    p->nt = nt;
+    p->nh = plan->d.n_head;
+    p->nkv = plan->d.n_head_kv;
+    p->hd = plan->d.head_dim;
+    p->kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
+}
+
+// The kernel's shape, and byte offsets of the workspace's parts.
+struct RowsLayout {
+    RowsShape shape;
+    int32_t per_block, blocks, max_tiles;
+    size_t attn, total, tiles, starts, row_end, row_tile, pieces, part, prefix_out, prefix_lse, own_out, own_lse, bytes;
+};
+// attn_bytes: of qkv_attn_step's workspace in front (prefix); 0: prompt.
+RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t attn_bytes) {
+    RowsLayout l;
+    const bool prefix = attn_bytes > 0;
+    const int32_t G = p.nh / p.nkv;
+    l.shape = paged_rows_shape(p);
+    l.per_block = G < l.shape.rows ? G : l.shape.rows;
+    l.blocks = (G + l.per_block - 1) / l.per_block;
+    const int64_t tiles = prefix ? c->n_seq : p.nt / (l.shape.rows / l.per_block) + static_cast<int64_t>(c->n_seq);
+    l.max_tiles = static_cast<int32_t>(tiles);
+    size_t at = up256(attn_bytes);
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += up256(n);
+        return here;
+    };
+    const size_t rows = static_cast<size_t>(c->n_seq) * p.nh;
+    l.attn = 0;
+    l.total = take(2 * sizeof(int64_t));
+    l.tiles = take(tiles * sizeof(RowTile));
+    l.starts = take(prefix ? 4 * static_cast<size_t>(c->n_seq) : 0);
+    l.row_end = take(prefix ? 4 * static_cast<size_t>(c->n_seq) : 0);
+    l.row_tile = take(prefix ? 4 * static_cast<size_t>(c->n_seq) : 0);
+    l.pieces = take(kRowsMaxCtas * sizeof(RowPiece));
+    l.part = take(4 * 2 * static_cast<size_t>(l.shape.ctas) * l.shape.rows * (p.hd + 2));
+    l.prefix_out = take(prefix ? 4 * rows * p.hd : 0);
+    l.prefix_lse = take(prefix ? 4 * rows : 0);
+    l.own_out = take(prefix ? 4 * rows * p.hd : 0);
+    l.own_lse = take(prefix ? 4 * rows : 0);
+    l.bytes = at;
+    return l;
+}
+void rows_workspace(const RowsLayout& l, char* ws, PagedRowsParams* p) {
+    p->rows = l.shape.rows;
+    p->block = l.shape.block;
+    p->per_block = l.per_block;
+    p->blocks = l.blocks;
+    p->max_tiles = l.max_tiles;
+    p->total = reinterpret_cast<int64_t*>(ws + l.total);
+    p->tiles = reinterpret_cast<RowTile*>(ws + l.tiles);
+    p->starts = reinterpret_cast<int32_t*>(ws + l.starts);
+    p->row_end = reinterpret_cast<int32_t*>(ws + l.row_end);
+    p->row_tile = reinterpret_cast<int32_t*>(ws + l.row_tile);
+    p->pieces = reinterpret_cast<RowPiece*>(ws + l.pieces);
+    p->part = reinterpret_cast<float*>(ws + l.part);
+    p->prefix_out = reinterpret_cast<float*>(ws + l.prefix_out);
+    p->prefix_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
+    p->own_out = reinterpret_cast<const float*>(ws + l.own_out);
+    p->own_lse = reinterpret_cast<const float*>(ws + l.own_lse);
+}
+
+qkv_status check_rows(const qkv_plan* plan, int32_t out_dtype, const float* q, int64_t q_stride, const void* out,
+                      int64_t out_stride, const float* lse, float scale, int64_t rows) {
+    if (plan->d.n_head % plan->d.n_head_kv != 0)
+        return api_fail(QKV_ERR_UNSUPPORTED, "n_head %d is not a multiple of n_head_kv %d", plan->d.n_head,
+                        plan->d.n_head_kv);
+    if (out_dtype != QKV_F32 && out_dtype != QKV_BF16)
+        return api_fail(QKV_ERR_UNSUPPORTED, "out_dtype %d not supported (F32 or BF16)", out_dtype);
+    REQUIRE(q_stride >= plan->nqt && out_stride >= plan->nqt, "q_stride and out_stride must be >= nqt = %lld",
+            static_cast<long long>(plan->nqt));
+    REQUIRE(std::isfinite(scale), "scale must be finite");
+    const int os = out_dtype == QKV_F32 ? 4 : 2;
+    if (rows == 0) return QKV_OK;
+    REQUIRE(q && out, "q or out is null");
+    REQUIRE(aligned(q, 4) && aligned(out, os) && aligned(lse, 4), "a pointer is not aligned to its elements");
+    REQUIRE(!overlap(q, ((rows - 1) * q_stride + plan->nqt) * 4, out, ((rows - 1) * out_stride + plan->nqt) * os),
+            "out must not overlap q");
+    return QKV_OK;
+}
+
+// Sizes that the workspaces are computed from; n_head * rows fits what the kernels count in.
+qkv_status check_prompt_shape(const qkv_plan* plan, const qkv_paged_kv* c, int32_t nt) {
+    qkv_status st = check_shape(plan, c);
+    if (st != QKV_OK) return st;
+    REQUIRE(nt >= 0, "nt must be >= 0");
+    REQUIRE(static_cast<int64_t>(nt) * plan->d.n_head <= (int64_t(1) << 30), "nt * n_head must be at most 2^30");
+    return QKV_OK;
+}
+
+}  // namespace
+
+extern "C" qkv_status qkv_prompt_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, int32_t nt,
+                                                      size_t* out) {
+    qkv_status st = check_prompt_shape(plan, cache, nt);
+    if (st != QKV_OK) return st;
+    REQUIRE(out, "out is null");
+    if (plan->d.n_head % plan->d.n_head_kv != 0) return api_fail(QKV_ERR_UNSUPPORTED, "uneven groups of q heads");
+    PagedRowsParams p;
+    std::memset(&p, 0, sizeof p);
+    rows_params(plan, nt, &p);
+    *out = rows_layout(p, cache, 0).bytes;
+    return QKV_OK;
+}
+
+extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a,
+                                           void* stream) {
+    PagedRowsParams p;
+    std::memset(&p, 0, sizeof p);
+    qkv_status st = view(plan, cache, &p.c);
+    if (st != QKV_OK) return st;
+    REQUIRE(a, "args is null");
+    st = check_prompt_shape(plan, cache, a->nt);
+    if (st != QKV_OK) return st;
+    st = check_rows(plan, a->out_dtype, a->q, a->q_stride, a->out, a->out_stride, a->lse, a->scale, a->nt);
+    if (st != QKV_OK) return st;
+    REQUIRE(a->window >= 0, "window must be >= 0");
+    if (a->nt == 0) return QKV_OK;
+    REQUIRE(a->d_first && a->d_lens, "d_first or d_lens is null");
+    REQUIRE(aligned(a->d_first, 4) && aligned(a->d_lens, 4), "a pointer is not aligned to its elements");
+    rows_params(plan, a->nt, &p);
+    const RowsLayout l = rows_layout(p, cache, 0);
+    REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
+    REQUIRE(a->workspace_bytes >= l.bytes, "the workspace has %zu bytes, %zu are needed", a->workspace_bytes, l.bytes);
+    rows_workspace(l, static_cast<char*>(a->d_workspace), &p);
+    p.q = a->q;
+    p.q_stride = a->q_stride;
+    p.first = a->d_first;
+    p.lens = a->d_lens;
+    p.scale = a->scale;
+    p.window = a->window;
+    p.out = a->out;
+    p.out_bf16 = a->out_dtype == QKV_BF16;
+    p.out_stride = a->out_stride;
+    p.lse = a->lse;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_paged_rows_plan(p, s);
+    if (e == cudaSuccess) e = launch_paged_rows(p, s);
+    if (e == cudaSuccess) e = launch_paged_rows_join(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention kernel launch");
+    return QKV_OK;
+}
+
+extern "C" qkv_status qkv_prefix_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out) {
+    qkv_status st = check_shape(plan, cache);
+    if (st != QKV_OK) return st;
+    REQUIRE(out, "out is null");
+    if (plan->d.n_head % plan->d.n_head_kv != 0) return api_fail(QKV_ERR_UNSUPPORTED, "uneven groups of q heads");
+    PagedRowsParams p;
+    std::memset(&p, 0, sizeof p);
+    rows_params(plan, cache->n_seq, &p);
+    *out = rows_layout(p, cache, attn_layout(plan, cache, false).total).bytes;
+    return QKV_OK;
+}
+
+extern "C" qkv_status qkv_prefix_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prefix_attn_args* a,
+                                           void* stream) {
+    PagedRowsParams p;
+    std::memset(&p, 0, sizeof p);
+    qkv_status st = view(plan, cache, &p.c);
+    if (st != QKV_OK) return st;
+    REQUIRE(a, "args is null");
+    st = check_rows(plan, a->out_dtype, a->q, a->q_stride, a->out, a->out_stride, a->lse, a->scale, cache->n_seq);
+    if (st != QKV_OK) return st;
+    REQUIRE(a->d_lens && a->d_share && a->d_prefix_len, "d_lens, d_share or d_prefix_len is null");
+    REQUIRE(aligned(a->d_lens, 4) && aligned(a->d_share, 4) && aligned(a->d_prefix_len, 4),
+            "a pointer is not aligned to its elements");
+    rows_params(plan, cache->n_seq, &p);
+    const AttnLayout al = attn_layout(plan, cache, false);
+    const RowsLayout l = rows_layout(p, cache, al.total);
+    REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
+    REQUIRE(a->workspace_bytes >= l.bytes, "the workspace has %zu bytes, %zu are needed", a->workspace_bytes, l.bytes);
+    char* ws = static_cast<char*>(a->d_workspace);
+    rows_workspace(l, ws, &p);
+    p.q = a->q;
+    p.q_stride = a->q_stride;
+    p.lens = a->d_lens;
+    p.share = a->d_share;
+    p.prefix_len = a->d_prefix_len;
+    p.scale = a->scale;
+    p.out = a->out;
+    p.out_bf16 = a->out_dtype == QKV_BF16;
+    p.out_stride = a->out_stride;
+    p.lse = a->lse;
+    // the rows' own slots: the attention of one new token each, from where the prefix ends
+    PagedAttnParams o;
+    std::memset(&o, 0, sizeof o);
+    o.c = p.c;
+    o.q = a->q;
+    o.q_stride = a->q_stride;
+    o.lens = a->d_lens;
+    o.starts = p.starts;
+    o.scale = a->scale;
+    o.out = ws + l.own_out;
+    o.out_stride = plan->nqt;
+    o.lse = reinterpret_cast<float*>(ws + l.own_lse);
+    o.counters = reinterpret_cast<unsigned int*>(ws);
+    o.part = reinterpret_cast<float*>(ws + al.part);
+    o.nh = p.nh;
+    o.nkv = p.nkv;
+    o.hd = p.hd;
+    o.kv_f16 = p.kv_f16;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_paged_rows_plan(p, s);
+    if (e == cudaSuccess) e = launch_paged_attn(o, s);
+    if (e == cudaSuccess) e = launch_paged_rows(p, s);
+    if (e == cudaSuccess) e = launch_paged_rows_join(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix attention kernel launch");
     return QKV_OK;
 }
 

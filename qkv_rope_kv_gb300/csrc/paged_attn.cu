@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int j0 = h / (p.nh / p.nkv) * p.hd;
     const int n = checked_len(p.c, p.lens, b);
-    const int first = p.window > 0 ? max(0, n - p.window) : 0;
+    const int first = p.starts ? min(p.starts[b], n) : p.window > 0 ? max(0, n - p.window) : 0;
     for (int d = tid; d < p.hd; d += kAnyThreads)
         q_s[d] = p.q[b * p.q_stride + static_cast<int64_t>(h) * p.hd + d] * (p.scale * kLog2e);
     float* scores = p.add_weight ? p.scores + (static_cast<int64_t>(b) * p.nh + h) * p.score_stride : nullptr;
@@ -355,9 +355,9 @@ __device__ __forceinline__ void seq_units(const PagedAttnParams& p, int b, bool 
     }
     w.b = b;
     w.n = n;
-    w.first = p.window > 0 ? max(0, n - p.window) : 0;
+    w.first = p.starts ? min(p.starts[b], n) : p.window > 0 ? max(0, n - p.window) : 0;
     w.lo = w.first / UK;
-    w.units = n > 0 ? (n + UK - 1) / UK - w.lo : 0;
+    w.units = n > w.first ? (n + UK - 1) / UK - w.lo : 0;
 }
 
 // a / b of non-negative values; 32-bit division where both fit, as they do in all but huge batches.

@@ -1,0 +1,237 @@
+// Attention of many q rows over a paged cache (qkv_prompt_attn_step, and the prefix of qkv_prefix_attn_step; include/qkv.h
+// has the contracts): any head size, cache type and alignment, in f32.
+//
+// s_j = scale * q.K_j, running maximum m and sum l of each row, out = sum p_j V_j / l, scores in log2 terms.  A tile of 64
+// rows goes over blocks of 64 slots: both products are made by plain f32 multiply-adds from shared memory, each thread 4 x 4
+// scores and 4 rows x hd / 16 columns of the sums.
+#include "paged_rows.cuh"
+
+namespace {
+
+using namespace qkv_rows;
+using qkv_ptx::griddep_launch_dependents;
+using qkv_ptx::griddep_wait;
+
+constexpr int kThreads = 256, kRows = 64, kBlock = 64;
+constexpr int kPStride = kBlock + 4;
+
+template <int HDP>
+struct Shape {
+    static constexpr int kStride = HDP + 4;  // floats of a row: sixteen rows' quads fall into different banks
+    static constexpr int kCols = HDP / 64;   // quads of columns of a thread
+    static constexpr int kSmem = 4 * (2 * 64 * kStride + kRows * kPStride);
+    static constexpr int kCtas = HDP == 256 ? 1 : 2;  // an SM
+};
+
+__device__ __forceinline__ float get(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float get(const __half* p) { return __half2float(__ldg(p)); }
+
+// One block of K or V into shared memory; slots that are not there, and columns behind hd, are zeros.
+template <typename KT, int HDP>
+__device__ __forceinline__ void load_block(const PagedRowsParams& p, const void* pool, const int64_t* row_s, float* to) {
+    const KT* src = static_cast<const KT*>(pool);
+#pragma unroll 4
+    for (int e = threadIdx.x; e < kBlock * HDP; e += kThreads) {
+        const int r = e / HDP, d = e % HDP;
+        const int64_t at = row_s[r];
+        to[r * Shape<HDP>::kStride + d] = at >= 0 && d < p.hd ? get(src + at + d) : 0.f;
+    }
+}
+
+template <typename KT, int HDP>
+__global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_kernel(const __grid_constant__ PagedRowsParams p) {
+    using S = Shape<HDP>;
+    extern __shared__ __align__(16) float smem[];
+    float *q_s = smem, *kv_s = q_s + kRows * S::kStride, *p_s = kv_s + kBlock * S::kStride;
+    __shared__ int64_t row_s[kBlock];
+    __shared__ int lo_s[kRows], hi_s[kRows];
+    __shared__ int all_lo_s, all_hi_s;  // slots that every row sees
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = p.nh / p.nkv;
+    Walk w;
+    if (!w.begin(p)) return;
+    Piece x;
+    while (w.next(p, x)) {
+        const RowTile& t = x.t;
+        const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
+        const int rows = t.ntok * heads;
+        __syncthreads();  // the last piece's rows have been read
+        if (tid == 0) {
+            note_piece(p, w, x, w.u >= w.end);
+            all_lo_s = 0;
+            all_hi_s = 0x7fffffff;
+        }
+        __syncthreads();
+        if (tid < kRows) {
+            int lo = 0, hi = 0;
+            if (tid < rows) {
+                row_span(p, t, tid / heads, lo, hi);
+                atomicMax(&all_lo_s, lo);
+                atomicMin(&all_hi_s, hi);
+            }
+            lo_s[tid] = lo;
+            hi_s[tid] = hi;
+        }
+        const float scale = p.scale * kLog2e;
+        for (int e = tid; e < kRows * HDP; e += kThreads) {
+            const int r = e / HDP, d = e % HDP, i = r / heads;
+            q_s[r * S::kStride + d] =
+                r < rows && d < p.hd
+                    ? __ldcg(p.q + (t.row0 + i) * p.q_stride + static_cast<int64_t>(kv * G + g0 + r - i * heads) * p.hd + d) * scale
+                    : 0.f;
+        }
+        float m[4], l[4];
+        float4 o[4][S::kCols];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -CUDART_INF_F;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < S::kCols; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int u = x.from; u < x.to; ++u) {
+            const int j0 = t.lo + u * kBlock;
+            if (tid < kBlock) {
+                const int64_t row = j0 + tid < t.hi ? row_offset(p.c, t.seq, j0 + tid) : -1;
+                row_s[tid] = row < 0 ? -1 : row + static_cast<int64_t>(kv) * p.hd;
+            }
+            __syncthreads();
+            load_block<KT, HDP>(p, p.c.k, row_s, kv_s);
+            __syncthreads();
+            float s[4][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < HDP; d += 4) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = *reinterpret_cast<const float4*>(q_s + (ty + 16 * i) * S::kStride + d);
+                    b[i] = *reinterpret_cast<const float4*>(kv_s + (tx + 16 * i) * S::kStride + d);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
+            }
+            // a weight below zero marks a slot that the row does not see
+            const bool mixed = j0 < all_lo_s || j0 + kBlock > all_hi_s;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = ty + 16 * i, lo = lo_s[r], hi = hi_s[r];
+                bool in[4];
+                float mt = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int slot = j0 + tx + 16 * j;
+                    in[j] = row_s[tx + 16 * j] >= 0 && slot >= lo && slot < hi;
+                    if (!in[j]) s[i][j] = -CUDART_INF_F;
+                    mt = fmaxf(mt, s[i][j]);
+                }
+#pragma unroll
+                for (int k = 1; k < 16; k <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, k));
+                const float keep = m[i] == mt ? 1.f : exp2f(m[i] - mt), base = mt == -CUDART_INF_F ? 0.f : mt;
+                m[i] = mt;
+                l[i] *= keep;
+#pragma unroll
+                for (int c = 0; c < S::kCols; ++c)
+                    o[i][c] = make_float4(o[i][c].x * keep, o[i][c].y * keep, o[i][c].z * keep, o[i][c].w * keep);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = exp2f(s[i][j] - base);
+                    l[i] += e;
+                    p_s[r * kPStride + tx + 16 * j] = mixed && !in[j] ? -1.f : e;
+                }
+            }
+            __syncthreads();
+            load_block<KT, HDP>(p, p.c.v, row_s, kv_s);
+            __syncthreads();
+#pragma unroll 2
+            for (int j = 0; j < kBlock; j += 4) {
+                float4 e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const float4*>(p_s + (ty + 16 * i) * kPStride + j);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int c = 0; c < S::kCols; ++c) {
+                        const float4 v = *reinterpret_cast<const float4*>(kv_s + (j + k) * S::kStride + 4 * tx + 64 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float f = k == 0 ? e[i].x : k == 1 ? e[i].y : k == 2 ? e[i].z : e[i].w;
+                            if (mixed && f < 0.f) continue;  // whatever V holds there
+                            o[i][c] = make_float4(fmaf(f, v.x, o[i][c].x), fmaf(f, v.y, o[i][c].y), fmaf(f, v.z, o[i][c].z),
+                                                  fmaf(f, v.w, o[i][c].w));
+                        }
+                    }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int k = 1; k < 16; k <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
+            const int r = ty + 16 * i;
+            if (r >= rows) continue;
+            const int row = t.row0 + r / heads, h = kv * G + g0 + r % heads;
+            if (x.whole()) {
+                const bool empty = lo_s[r] >= hi_s[r];
+                const float inv = empty ? 0.f : 1.f / l[i];
+                const int64_t at = p.first ? row * p.out_stride + static_cast<int64_t>(h) * p.hd
+                                           : (static_cast<int64_t>(row) * p.nh + h) * p.hd;
+#pragma unroll
+                for (int c = 0; c < S::kCols; ++c) {
+                    const float v[4] = {o[i][c].x, o[i][c].y, o[i][c].z, o[i][c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int d = 4 * tx + 64 * c + k;
+                        if (d >= p.hd) continue;
+                        const float y = empty ? 0.f : v[k] * inv;
+                        if (p.first) put_out(p, at + d, y);
+                        else p.prefix_out[at + d] = y;
+                    }
+                }
+                float* lse = p.first ? p.lse : p.prefix_lse;
+                if (tx == 0 && lse) lse[static_cast<int64_t>(row) * p.nh + h] = lse_of(m[i], l[i], empty);
+            } else {
+                float* part = part_of(p, blockIdx.x, x.first);
+                float* to = part_o(p, part, r);
+                if (tx == 0) *part_ml(part, r) = make_float2(m[i], l[i]);
+#pragma unroll
+                for (int c = 0; c < S::kCols; ++c) {
+                    const float v[4] = {o[i][c].x, o[i][c].y, o[i][c].z, o[i][c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (4 * tx + 64 * c + k < p.hd) to[4 * tx + 64 * c + k] = v[k];
+                }
+            }
+        }
+    }
+}
+
+template <typename KT, int HDP>
+cudaError_t launch_t(const PagedRowsParams& p, cudaStream_t stream) {
+    auto kernel = paged_rows_any_kernel<KT, HDP>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<HDP>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(kSms * Shape<HDP>::kCtas), kThreads, Shape<HDP>::kSmem, stream, 1, p);
+}
+
+template <typename KT>
+cudaError_t launch_any(const PagedRowsParams& p, cudaStream_t stream) {
+    return p.hd <= 64 ? launch_t<KT, 64>(p, stream) : p.hd <= 128 ? launch_t<KT, 128>(p, stream) : launch_t<KT, 256>(p, stream);
+}
+
+}  // namespace
+
+RowsShape paged_rows_shape(const PagedRowsParams& p) {
+    return {kRows, kBlock, kSms * (p.hd <= 128 ? Shape<128>::kCtas : Shape<256>::kCtas)};
+}
+
+cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream) {
+    return p.kv_f16 ? launch_any<__half>(p, stream) : launch_any<float>(p, stream);
+}
+
+cudaError_t paged_rows_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {
+    return status_read(stream, flags, bad);
+}

@@ -1,0 +1,142 @@
+// What the kernels of attention with many q rows share: the walk over a CTA's units, and where its results go.
+#pragma once
+
+#include <math_constants.h>
+
+#include "paged_common.cuh"
+#include "ptx_sync.cuh"
+
+namespace qkv_rows {
+
+using namespace qkv_paged;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMinUnits = 2;  // of a CTA: a part costs its write and its join
+
+__device__ __forceinline__ int64_t units_per_cta(int64_t total, int ctas) {
+    const int64_t even = (total + ctas - 1) / ctas;
+    return even > kMinUnits ? even : kMinUnits;
+}
+
+// Some units [from, to) of one tile, and the first q head.
+struct Piece {
+    RowTile t;
+    int tile, head;  // head: kv head and block of its q heads
+    int from, to;
+    bool first;      // of the CTA's pieces
+    __device__ __forceinline__ bool whole() const { return from == 0 && to == t.units; }
+};
+
+__device__ __forceinline__ RowTile load_tile(const PagedRowsParams& p, int i) {
+    RowTile t;
+    const int4* s = reinterpret_cast<const int4*>(p.tiles + i);
+    int4* d = reinterpret_cast<int4*>(&t);
+    static_assert(sizeof(RowTile) == 48, "three loads");
+    d[0] = __ldcg(s);
+    d[1] = __ldcg(s + 1);
+    d[2] = __ldcg(s + 2);
+    return t;
+}
+
+// The units of one CTA, piece by piece.  Every warp walks for itself; all its lanes call together.
+struct Walk {
+    int64_t u, end, per_head, total, share;
+    int tiles, tile, head;
+    bool first;
+    __device__ __forceinline__ bool begin(const PagedRowsParams& p) {
+        per_head = __ldcg(p.total);
+        tiles = static_cast<int>(__ldcg(p.total + 1));
+        total = per_head * p.nkv * p.blocks;
+        share = units_per_cta(total, gridDim.x);
+        u = share * blockIdx.x;
+        end = min(total, u + share);
+        first = true;
+        if (u >= end) return false;
+        head = static_cast<int>(u / per_head);
+        const int64_t r = u - head * per_head;
+        // the last tile that begins at or before r: 32 candidates at a time
+        int lo = 0, n = tiles;
+        const int lane = threadIdx.x & 31;
+        while (n > 1) {
+            const int step = (n + 31) / 32, at = lo + lane * step;
+            const bool ok = lane * step < n && __ldcg(&p.tiles[at].unit0) <= r;
+            const int last = 31 - __clz(__ballot_sync(0xffffffffu, ok));
+            lo += last * step;
+            n = min(step, n - last * step);
+        }
+        tile = lo;
+        return true;
+    }
+    __device__ __forceinline__ bool next(const PagedRowsParams& p, Piece& x) {
+        if (u >= end) return false;
+        for (;;) {
+            if (tile >= tiles) {
+                tile = 0;
+                ++head;
+            }
+            x.t = load_tile(p, tile);
+            if (x.t.units > 0) break;
+            ++tile;
+        }
+        x.tile = tile;
+        x.head = head;
+        const int64_t start = head * per_head + x.t.unit0;
+        x.from = static_cast<int>(u - start);
+        x.to = static_cast<int>(min(static_cast<int64_t>(x.t.units), end - start));
+        x.first = first;
+        first = false;
+        u = start + x.to;
+        ++tile;
+        return true;
+    }
+};
+
+// What row i of a tile sees.
+__device__ __forceinline__ void row_span(const PagedRowsParams& p, const RowTile& t, int i, int& lo, int& hi) {
+    if (p.first) {
+        hi = max(0, t.base + i);
+        lo = p.window > 0 ? max(0, t.base + i - p.window) : 0;
+    } else {
+        hi = __ldcg(p.row_end + t.row0 + i);
+        lo = 0;
+    }
+}
+
+__device__ __forceinline__ float* part_of(const PagedRowsParams& p, int cta, bool first) {
+    return p.part + static_cast<int64_t>(2 * cta + (first ? 0 : 1)) * p.rows * (p.hd + 2);
+}
+// Maximum and sum of a part's row; the rows' sums of V come behind all of these.
+__device__ __forceinline__ float2* part_ml(float* part, int row) { return reinterpret_cast<float2*>(part) + row; }
+__device__ __forceinline__ float* part_o(const PagedRowsParams& p, float* part, int row) {
+    return part + 2 * p.rows + static_cast<int64_t>(row) * p.hd;
+}
+
+// For the join: the CTA in which a tile begins notes how many CTAs have parts of it.
+__device__ __forceinline__ void note_piece(const PagedRowsParams& p, const Walk& w, const Piece& x, bool last) {
+    if (!last) return;
+    RowPiece r = {};
+    if (x.from == 0 && x.to < x.t.units) {
+        r.start = x.head * w.per_head + x.t.unit0;
+        r.tile = x.tile;
+        r.head = x.head;
+        r.parts = static_cast<int>((r.start + x.t.units - 1) / w.share - blockIdx.x) + 1;
+    }
+    p.pieces[blockIdx.x] = r;
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+    uint16_t r;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void put_out(const PagedRowsParams& p, int64_t at, float v) {
+    if (p.out_bf16) static_cast<uint16_t*>(p.out)[at] = bf16_bits(v);
+    else static_cast<float*>(p.out)[at] = v;
+}
+// log(l 2^m); an empty row has none.
+__device__ __forceinline__ float lse_of(float m, float l, bool empty) {
+    return empty ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+}
+
+}  // namespace qkv_rows

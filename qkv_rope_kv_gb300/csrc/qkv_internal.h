@@ -158,6 +158,7 @@ struct PagedAttnParams {
     const int32_t* lens;
     float scale;
     int32_t window;
+    const int32_t* starts;   // [n_seq] or null: the first slot of each, >= 0 (then no window and no weights)
     void* out;
     int32_t out_bf16;
     int64_t out_stride;
@@ -174,6 +175,66 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
 // The main kernel's grid for these sizes (and pointers' alignment): CTAs, and CTAs of a cluster.
 void paged_attn_grid(const PagedAttnParams& p, int* ctas, int* cluster);
 cudaError_t paged_attn_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
+
+// Attention of many q rows over the same slots (paged_rows*.cu).  The rows (tokens x q heads of a kv head) go in tiles; the
+// slots that any of a tile's rows sees, in blocks, are its units.  A kernel's CTAs get equal shares of all tiles' units in
+// a row, kv head by kv head, so a tile's blocks can be spread over several CTAs: their parts are joined afterwards.
+struct alignas(16) RowTile {
+    int64_t unit0;  // units of one kv head before this tile's
+    int32_t units;
+    int32_t seq;    // whose row of the page table
+    int32_t row0, ntok;  // q rows
+    int32_t lo, hi;      // slots that are read: lo a multiple of the block
+    int32_t base;        // row i sees [max(0, base + i - window), base + i); prefix: [0, row_end[row0 + i])
+};
+struct RowPiece {  // for each CTA, its last tile where that goes on in other CTAs and began in this one
+    int64_t start;  // the tile's first unit, over all heads
+    int32_t tile, head;
+    int32_t parts;  // 0: none
+    int32_t pad;
+};
+constexpr int kRowsMaxCtas = 304;
+struct PagedRowsParams {
+    PagedView c;
+    const float* q;
+    int64_t q_stride;
+    const int32_t* first;       // prompt: [n_seq + 1]; prefix: null
+    const int32_t* lens;
+    const int32_t* share;       // prefix: [n_seq] each
+    const int32_t* prefix_len;
+    float scale;
+    int32_t window;
+    void* out;
+    int32_t out_bf16;
+    int64_t out_stride;
+    float* lse;
+    int32_t nt, nh, nkv, hd, kv_f16;
+    // the plan, made on the device
+    int32_t rows, block;        // of a tile, of a unit
+    int32_t per_block, blocks;  // q heads of a kv head in a tile, and how many such blocks it has
+    int32_t max_tiles;
+    int64_t* total;             // [0] units of one block of q heads, [1] tiles
+    RowTile* tiles;
+    int32_t* starts;            // prefix: [n_seq] each: where the rows' own slots begin, ...
+    int32_t* row_end;           // ... how many of the prefix are seen, ...
+    int32_t* row_tile;          // ... and in which tile
+    RowPiece* pieces;           // [kRowsMaxCtas]
+    float* part;                // [2 * kRowsMaxCtas][rows][hd + 2]
+    float* prefix_out;          // prefix: [n_seq][nqt] and [n_seq][nh]: of whole tiles
+    float* prefix_lse;
+    const float* own_out;       // the same of the rows' own slots
+    const float* own_lse;
+};
+cudaError_t launch_paged_rows_plan(const PagedRowsParams& p, cudaStream_t stream);
+cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream);
+cudaError_t launch_paged_rows_join(const PagedRowsParams& p, cudaStream_t stream);
+// Rows of a tile, slots of a block and CTAs of the kernel that these sizes and addresses get.
+struct RowsShape {
+    int32_t rows, block, ctas;
+};
+RowsShape paged_rows_shape(const PagedRowsParams& p);
+cudaError_t paged_rows_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
+cudaError_t paged_rows_plan_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
 
 struct PagedEvictParams {
     PagedView c;
