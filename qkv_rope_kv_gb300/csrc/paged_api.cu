@@ -237,11 +237,11 @@ struct RowsLayout {
     size_t attn, total, tiles, starts, row_end, row_tile, pieces, part, prefix_out, prefix_lse, own_out, own_lse, bytes;
 };
 // attn_bytes: of qkv_attn_step's workspace in front (prefix); 0: prompt.
-RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t attn_bytes) {
+RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t attn_bytes, const RowsShape& shape) {
     RowsLayout l;
     const bool prefix = attn_bytes > 0;
     const int32_t G = p.nh / p.nkv;
-    l.shape = paged_rows_shape(p);
+    l.shape = shape;
     l.per_block = G < l.shape.rows ? G : l.shape.rows;
     l.blocks = (G + l.per_block - 1) / l.per_block;
     const int64_t tiles = prefix ? c->n_seq : p.nt / (l.shape.rows / l.per_block) + static_cast<int64_t>(c->n_seq);
@@ -266,6 +266,15 @@ RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t a
     l.own_out = take(prefix ? 4 * rows * p.hd : 0);
     l.own_lse = take(prefix ? 4 * rows : 0);
     l.bytes = at;
+    return l;
+}
+// What the call's kernel needs.  The size is that of the larger kind of kernel: which one it is depends on addresses too.
+RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t attn_bytes) {
+    RowsLayout l = rows_layout(p, c, attn_bytes, paged_rows_shape(p));
+    for (const RowsShape& shape : {paged_rows_any_shape(p), paged_rows_tc_shape()}) {
+        const size_t n = rows_layout(p, c, attn_bytes, shape).bytes;
+        if (n > l.bytes) l.bytes = n;
+    }
     return l;
 }
 void rows_workspace(const RowsLayout& l, char* ws, PagedRowsParams* p) {

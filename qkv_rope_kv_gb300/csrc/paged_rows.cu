@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
     float *q_s = smem, *kv_s = q_s + kRows * S::kStride, *p_s = kv_s + kBlock * S::kStride;
     __shared__ int64_t row_s[kBlock];
     __shared__ int lo_s[kRows], hi_s[kRows];
-    __shared__ int all_lo_s, all_hi_s;  // slots that every row sees
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = p.nh / p.nkv;
@@ -57,19 +56,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
         const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
         const int rows = t.ntok * heads;
         __syncthreads();  // the last piece's rows have been read
-        if (tid == 0) {
-            note_piece(p, w, x, w.u >= w.end);
-            all_lo_s = 0;
-            all_hi_s = 0x7fffffff;
-        }
-        __syncthreads();
+        if (tid == 0) note_piece(p, w, x, w.u >= w.end);
         if (tid < kRows) {
             int lo = 0, hi = 0;
-            if (tid < rows) {
-                row_span(p, t, tid / heads, lo, hi);
-                atomicMax(&all_lo_s, lo);
-                atomicMin(&all_hi_s, hi);
-            }
+            if (tid < rows) row_span(p, t, tid / heads, lo, hi);
             lo_s[tid] = lo;
             hi_s[tid] = hi;
         }
@@ -115,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
                         s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
             }
             // a weight below zero marks a slot that the row does not see
-            const bool mixed = j0 < all_lo_s || j0 + kBlock > all_hi_s;
+            const bool mixed = j0 < t.all_lo || j0 + kBlock > t.all_hi;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = ty + 16 * i, lo = lo_s[r], hi = hi_s[r];
@@ -224,11 +214,23 @@ cudaError_t launch_any(const PagedRowsParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-RowsShape paged_rows_shape(const PagedRowsParams& p) {
+RowsShape paged_rows_any_shape(const PagedRowsParams& p) {
     return {kRows, kBlock, kSms * (p.hd <= 128 ? Shape<128>::kCtas : Shape<256>::kCtas)};
 }
 
+// f16 rows that 16-byte copies can read, of whole steps of 16 columns that fit tensor memory beside the scores.
+bool paged_rows_on_tensor_cores(const PagedRowsParams& p) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.c.k) | reinterpret_cast<uintptr_t>(p.c.v) |
+                           static_cast<uintptr_t>(p.c.page_stride * 2);
+    return p.kv_f16 && p.hd <= 128 && p.hd % 16 == 0 && (bits & 15u) == 0;
+}
+
+RowsShape paged_rows_shape(const PagedRowsParams& p) {
+    return paged_rows_on_tensor_cores(p) ? paged_rows_tc_shape() : paged_rows_any_shape(p);
+}
+
 cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream) {
+    if (paged_rows_on_tensor_cores(p)) return launch_paged_rows_tc(p, stream);
     return p.kv_f16 ? launch_any<__half>(p, stream) : launch_any<float>(p, stream);
 }
 

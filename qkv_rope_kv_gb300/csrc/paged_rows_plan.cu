@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prompt_kernel(const __grid_
                 x.base = len_s[lo] - n_s[lo] + tok + 1;
                 x.hi = max(0, x.base + x.ntok - 1);
                 const int see = p.window > 0 ? max(0, x.base - p.window) : 0;
+                x.all_lo = p.window > 0 ? max(0, x.base + x.ntok - 1 - p.window) : 0;
+                x.all_hi = max(0, x.base);
                 x.lo = see < x.hi ? see / p.block * p.block : 0;
                 x.units = max(1, (x.hi - x.lo + p.block - 1) / p.block);  // rows that see nothing are written too
             }
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prompt_kernel(const __grid_
 
 // One new token of each sequence, the beginnings shared: tiles of neighbouring sequences with the same d_share.
 __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_constant__ PagedRowsParams p) {
-    __shared__ int hi_s[kPlanThreads], n_s[kPlanThreads], start_s[kPlanThreads], run_s[kPlanThreads];
+    __shared__ int hi_s[kPlanThreads], all_s[kPlanThreads], n_s[kPlanThreads], start_s[kPlanThreads], run_s[kPlanThreads];
     __shared__ int64_t warp_s[kPlanThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
         __syncthreads();
         if (lane == 31) run_s[i >> 5] = run;
         hi_s[i] = 0;
+        all_s[i] = 0x7fffffff;
         n_s[i] = 0;
         __syncthreads();
         for (int w = 0; w < i >> 5; ++w) run = max(run, run_s[w]);
@@ -147,6 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
         __syncthreads();
         if (b < p.c.n_seq) {
             atomicMax(&hi_s[mine], seen);
+            atomicMin(&all_s[mine], seen);
             atomicAdd(&n_s[mine], 1);
         }
         __syncthreads();
@@ -163,6 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
             x.seq = p.share[x.row0];
             x.ntok = n_s[i];
             x.hi = x.ntok == 1 && x.seq == x.row0 ? 0 : hi_s[i];
+            x.all_hi = all_s[i];
             x.units = (x.hi + p.block - 1) / p.block;
         }
         int64_t sum;

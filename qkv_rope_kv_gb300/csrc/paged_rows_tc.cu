@@ -1,0 +1,676 @@
+// Attention of many q rows over a paged f16 cache on the 5th-generation tensor cores (qkv_prompt_attn_step, and the prefix of
+// qkv_prefix_attn_step; include/qkv.h has the contracts).
+//
+// s_j = scale * q.K_j, running maximum m and sum l of each row, out = sum p_j V_j / l, scores in log2 terms.  A tile of 256
+// q rows, as two halves of 128 (the rows of a tcgen05.mma), goes over blocks of 128 slots: S = Q K^T and O += P V with both
+// accumulators in tensor memory, 128 columns each for a half.  P, in f16, takes the place of S there and is the second
+// product's A operand.  While one half's softmax runs, the tensor cores work for the other half, and K and V are read once
+// for both.
+//   warps 0-3, 4-7   softmax of the halves, a row a thread: S out of tensor memory, P back into it, O rescaled
+//                    where the maximum moved by more than 2^kLazy; at the end O / l to memory
+//   warp 8           issues the MMAs
+//   warps 9-12       copy K and V through the page table into a ring of chunks of 128 slots x 64 columns (cp.async, so pages
+//                    of any size; the 128-byte swizzle that the MMA reads)
+// SPLIT (out F32): q is kept as the sum of two f16 (rounded, and the remainder rounded) and so are the weights, both
+// products are made twice, and 22 bits of each are kept.  Otherwise (out BF16) once, of the rounded values: 2^-11, an
+// eighth of what out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are
+// 2^(s - m + kShift), far from f16's ends on both sides.
+#include "paged_rows.cuh"
+
+namespace {
+
+using namespace qkv_rows;
+using namespace qkv_ptx;
+
+constexpr int kTileRows = 256, kHalf = 128, kBlock = 128;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarps = 4, kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+constexpr int kChunkBytes = kBlock * 128;  // 128 slots (or q rows) x 64 columns
+constexpr unsigned int kFlagTimeout = 2u;
+constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
+
+template <bool SPLIT, int NCH>  // NCH chunks of 64 columns a head
+struct Shape {
+    static constexpr int kQBytes = 2 * NCH * (SPLIT ? 2 : 1) * kChunkBytes;
+    static constexpr int kStages = SPLIT ? (NCH == 2 ? 6 : 10) : (NCH == 2 ? 10 : 12);  // even: a head's chunks are neighbours
+    // Copies in flight ahead of the one that is waited for.  The MMAs free a block's V only after the next block's K is
+    // there, so that many chunks must fit behind those in flight.
+    static constexpr int kLag = kStages - 2 * NCH > 5 ? 5 : kStages - 2 * NCH;
+    static constexpr int kSmem = 1024 + kQBytes + kStages * kChunkBytes;
+    static constexpr float kShift = SPLIT ? 12.f : 6.f, kLazy = SPLIT ? 3.f : 8.f;  // weights stay below 2^15
+    static_assert(kSmem + 1024 <= 227 * 1024 && kStages <= kMaxStages && kStages % 2 == 0, "shared memory");
+};
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Shared-memory descriptors of chunks of 128-byte rows in the 128-byte swizzle (eight rows, 1024 bytes, an atom; version 1,
+// layout type 2).  K-major (Q, K): the stride offset leads to the next eight rows, the leading one is not used.
+// MN-major (V: rows are slots, the summed dimension): the stride offset leads to the next eight slots, the leading one
+// to the next 64 columns, a chunk further.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+    return (static_cast<uint64_t>(addr) & 0x3FFFFull) >> 4 | 1ull << 16 | (1024ull >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    return (static_cast<uint64_t>(addr) & 0x3FFFFull) >> 4 | (static_cast<uint64_t>(kChunkBytes) >> 4) << 16 |
+           (1024ull >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// kind::f16, D f32, A and B f16, M = 128; bit 16: B is MN-major.
+__device__ __forceinline__ uint32_t idesc(int n, bool b_mn) {
+    return 1u << 4 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(kHalf >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(accumulate)
+                 : "memory");
+}
+
+// N consecutive columns of this warp's 32 lanes: thread l has lane l's.
+__device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ uint32_t tm_ld1(uint32_t a) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(a));
+    tc_wait_ld();
+    return r;
+}
+__device__ __forceinline__ void tm_st1(uint32_t a, uint32_t r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(a), "r"(r) : "memory");
+}
+
+// ---------------------------------------------------------------- arithmetic
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+using u64 = unsigned long long;
+__device__ __forceinline__ u64 pack2(float x, float y) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 x, u64 y, u64 z) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ u64 add2(u64 x, u64 y) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two values rounded to f16, and the remainders rounded to f16.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = f16x2(a, b);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = f16x2(a - f.x, b - f.y);
+}
+// Byte offset of 16 bytes of a 128-byte row within a chunk.
+__device__ __forceinline__ uint32_t swz(int row, int c16) { return row * 128 + ((c16 ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool finite_f16x2(uint32_t w) {
+    return (w & 0x7c00u) != 0x7c00u && (w & 0x7c000000u) != 0x7c000000u;
+}
+
+// A score in f32 from memory, in log2 terms: for K with infinities or NaN, whose products with the two parts of q need not
+// be those with q (0 * inf where the remainder is zero).
+__device__ __noinline__ float plain_score(const PagedRowsParams& p, const float* q, int seq, int slot, int kv) {
+    const int64_t row = row_offset(p.c, seq, slot);
+    if (row < 0) return -CUDART_INF_F;
+    const __half* k = static_cast<const __half*>(p.c.k) + row + static_cast<int64_t>(kv) * p.hd;
+    float s = 0.f;
+    for (int d = 0; d < p.hd; ++d) s = fmaf(__ldcg(q + d) * (p.scale * kLog2e), __half2float(k[d]), s);
+    return s;
+}
+
+// What the infinities and NaN of V that a row sees, in slots [lo, hi), add to 16 columns of its sum: the copies put
+// zeros in their place, since a weight of zero (a slot that the row does not see) times them is NaN.
+__device__ __noinline__ void add_non_finite(const PagedRowsParams& p, int seq, int kv, int lo, int hi, int c, float* o) {
+    for (int s = lo; s < hi; ++s) {
+        const int64_t row = row_offset(p.c, seq, s);
+        if (row < 0) continue;
+        const __half* v = static_cast<const __half*>(p.c.v) + row + static_cast<int64_t>(kv) * p.hd + c;
+        for (int d = 0; d < 16; ++d) {
+            const float x = __half2float(v[d]);
+            if (!(fabsf(x) < CUDART_INF_F)) o[d] += x;
+        }
+    }
+}
+
+struct Control {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], drained;
+    uint32_t live[kLiveRing][4];   // slots of a block that are there
+    uint32_t poison[kPoisonRing];  // n: in piece n - 1, V had infinities or NaN that were replaced
+    uint32_t tmem;
+};
+
+template <bool SPLIT, int NCH>
+__global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid_constant__ PagedRowsParams p) {
+    using S = Shape<SPLIT, NCH>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Control ctl;
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t q_at = smem_u32(smem), ring_at = q_at + S::kQBytes;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    constexpr int kParts = SPLIT ? 2 : 1;
+    // chunk c of part `part` (0: rounded, 1: remainder) of half t of q
+    auto q_chunk = [&](int t, int part, int c) { return q_at + ((t * kParts + part) * NCH + c) * kChunkBytes; };
+    auto chunk_at = [&](uint32_t n) { return ring_at + n % S::kStages * kChunkBytes; };
+
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid < kPoisonRing) ctl.poison[tid] = 0;
+    if (tid == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&ctl.full[s], kLoadWarps);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&ctl.q_ready[t], 4);
+            mbar_init(&ctl.s_full[t], 1);
+            mbar_init(&ctl.p_ready[t], 4);
+            mbar_init(&ctl.o_full[t], 1);
+        }
+        mbar_init(&ctl.drained, 1);
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const int G = p.nh / p.nkv;
+    Walk w;
+    Piece x;
+    const bool work = w.begin(p);
+    if (work && warp < kSoftWarps) {
+        // ---- softmax: thread `lane` of warp w has row 32 (w % 4) + lane of half w / 4
+        const int t = warp >> 2, quarter = warp & 3;
+        const uint32_t s_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 128 * t, o_at = s_at + 256;
+        uint32_t s_phase = 0, o_phase = 0;
+        int piece = 0, block = 0;
+        bool ok = true;
+        while (ok && w.next(p, x)) {
+            const RowTile& tile = x.t;
+            const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
+            const int rows = tile.ntok * heads, row0 = t * kHalf + 32 * quarter, r = row0 + lane;
+            ++piece;
+            if (tid == 0) note_piece(p, w, x, w.u >= w.end);
+            if (t == 1 && rows <= kHalf) {  // nothing for this half
+                block += x.to - x.from;
+                continue;
+            }
+            // q of the warp's rows, a row at a time
+            float unscale = 1.f;
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const int row = row0 + i, tok = row / heads;
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+                if (row < rows && 4 * lane < p.hd) {
+                    const float* src = p.q + (tile.row0 + tok) * p.q_stride +
+                                       static_cast<int64_t>(kv * G + g0 + row - tok * heads) * p.hd + 4 * lane;
+                    if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+                        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+                        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = __ldcg(src + k);
+                    }
+                }
+                float big = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] *= p.scale * kLog2e;
+                    big = fmaxf(big, fabsf(v[k]));
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
+                int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
+                e = e == 128 ? 13 : max(-113, min(e, 126));
+                const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+                if (lane == i) unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+                if (4 * lane < 64 * NCH) {
+                    uint32_t hi[2], lo[2];
+                    split2(v[0] * sc, v[1] * sc, hi[0], lo[0]);
+                    split2(v[2] * sc, v[3] * sc, hi[1], lo[1]);
+                    const int c = lane >> 4, in = (lane & 15) >> 1;  // chunk, and 16 bytes of its row
+                    const uint32_t at = swz(32 * quarter + i, in) + 8 * (lane & 1);
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, 0, c) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
+                    if (SPLIT)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, kParts - 1, c) + at), "r"(lo[0]),
+                                     "r"(lo[1])
+                                     : "memory");
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.q_ready[t]);
+
+            const bool busy = row0 < rows, mine = r < rows;
+            int see_lo = 0, see_hi = 0;
+            if (mine) row_span(p, tile, r / heads, see_lo, see_hi);
+            float m = -CUDART_INF_F, l = 0.f;
+            for (int u = x.from; u < x.to; ++u, ++block) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.s_full[t], s_phase));
+                s_phase ^= 1;
+                if (!ok) break;
+                tc_fence_after();
+                if (busy) {
+                    const int j0 = tile.lo + u * kBlock;
+                    const uint32_t* live = ctl.live[block % kLiveRing];
+                    const bool mixed = j0 < tile.all_lo || j0 + kBlock > tile.all_hi ||
+                                       (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
+                    // the slots of columns 32 c .. 32 c + 31 that the row sees
+                    auto seen = [&](int c) {
+                        const int a = see_lo - j0 - 32 * c, b = see_hi - j0 - 32 * c;
+                        const uint32_t below = b >= 32 ? 0xffffffffu : b <= 0 ? 0u : (1u << b) - 1u;
+                        const uint32_t from = a <= 0 ? 0xffffffffu : a >= 32 ? 0u : 0xffffffffu << a;
+                        return below & from & live[c];
+                    };
+                    float top;
+                    for (int round = 0;; ++round) {
+                        top = -CUDART_INF_F;
+                        u64 odd = 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t v[32];
+                            tm_ld32(s_at + 32 * c, v);
+                            tc_wait_ld();
+                            if (SPLIT) {
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2)
+                                    odd = fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), 0, odd);
+                            }
+                            if (mixed) {
+                                const uint32_t in = seen(c);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!((in >> k) & 1u)) v[k] = 0xff800000u;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+                                top = fmaxf(top, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                        }
+                        if (!SPLIT || round == 1) break;
+                        const float2 bad = unpack2(odd);
+                        if (!__any_sync(0xffffffffu, !(bad.x + bad.y == 0.f))) break;
+                        const float* q_row = p.q + static_cast<int64_t>(tile.row0 + r / heads) * p.q_stride +
+                                             static_cast<int64_t>(kv * G + g0 + r % heads) * p.hd;
+                        for (int k = 0; k < kBlock; ++k) {
+                            float v = __uint_as_float(tm_ld1(s_at + k));
+                            if (mine && !(fabsf(v) < CUDART_INF_F) && ((seen(k >> 5) >> (k & 31)) & 1u))
+                                v = plain_score(p, q_row, tile.seq, j0 + k, kv) * (1.f / unscale);
+                            __syncwarp();
+                            tm_st1(s_at + k, __float_as_uint(v));
+                        }
+                        tc_wait_st();
+                    }
+                    top *= unscale;
+                    if (__any_sync(0xffffffffu, top > m + S::kLazy)) {
+                        const float next = fmaxf(m, top), keep = m == next ? 1.f : ex2(m - next);
+                        m = next;
+                        l *= keep;
+                        if (u > x.from)
+                            for (int c = 0; c < p.hd; c += 16) {
+                                uint32_t o[16];
+                                tm_ld16(o_at + c, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                                tm_st16(o_at + c, o);
+                            }
+                    }
+                    const float base = (m == -CUDART_INF_F ? 0.f : m) - S::kShift;
+                    const u64 by = pack2(unscale, unscale), minus = pack2(-base, -base);
+                    u64 sum = 0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32], h[16], low[16];
+                        tm_ld32(s_at + 32 * c, v);
+                        tc_wait_ld();
+                        if (mixed) {
+                            const uint32_t in = seen(c);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((in >> k) & 1u)) v[k] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 y = unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), by, minus));
+                            const float a = ex2(y.x), b = ex2(y.y);
+                            sum = add2(sum, pack2(a, b));
+                            if (SPLIT) split2(a, b, h[k / 2], low[k / 2]);
+                            else h[k / 2] = f16x2(a, b);
+                        }
+                        tm_st16(s_at + 32 * c, h);
+                        if (SPLIT) tm_st16(s_at + 32 * c + 16, low);
+                    }
+                    const float2 both = unpack2(sum);
+                    l += both.x + both.y;
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_ready[t]);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.o_full[t], o_phase));
+            o_phase ^= 1;
+            if (!ok) break;
+            tc_fence_after();
+            if (!busy) continue;
+            const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
+            const int i = r / heads, row = tile.row0 + i, h = kv * G + g0 + r - i * heads;
+            const bool whole = x.whole(), empty = see_lo >= see_hi;
+            const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;
+            float* part = part_of(p, blockIdx.x, x.first);
+            const int64_t out_at = row * p.out_stride + static_cast<int64_t>(h) * p.hd;
+            float* to = nullptr;  // bf16
+            if (!whole) to = part_o(p, part, r);
+            else if (!p.first) to = p.prefix_out + (static_cast<int64_t>(row) * p.nh + h) * p.hd;
+            else if (!p.out_bf16) to = static_cast<float*>(p.out) + out_at;
+            for (int c = 0; c < p.hd; c += 16) {
+                uint32_t v[16];
+                float o[16];
+                tm_ld16(o_at + c, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(v[k]);
+                if (poison && mine) {
+                    float more[16] = {};
+                    add_non_finite(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock),
+                                   min(see_hi, tile.lo + x.to * kBlock), c, more);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] += more[k];
+                }
+                if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = whole && empty ? 0.f : o[k] * inv;
+                    if (to) {
+                        if ((reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
+#pragma unroll
+                            for (int k = 0; k < 16; k += 4)
+                                *reinterpret_cast<float4*>(to + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) to[c + k] = o[k];
+                        }
+                    } else {
+                        uint16_t* b = static_cast<uint16_t*>(p.out) + out_at + c;
+                        if ((reinterpret_cast<uintptr_t>(b) & 15u) == 0) {
+                            uint32_t d[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d[k]) : "f"(o[2 * k + 1]), "f"(o[2 * k]));
+                            *reinterpret_cast<uint4*>(b) = make_uint4(d[0], d[1], d[2], d[3]);
+                            *reinterpret_cast<uint4*>(b + 8) = make_uint4(d[4], d[5], d[6], d[7]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) b[k] = bf16_bits(o[k]);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (mine) {
+                float* lse = p.first ? p.lse : p.prefix_lse;
+                if (!whole) *part_ml(part, r) = make_float2(m - S::kShift, l);
+                else if (lse) lse[static_cast<int64_t>(row) * p.nh + h] = lse_of(m - S::kShift, l, empty);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) flag_bad(kFlagTimeout, 0);
+    } else if (work && warp == kMmaWarp) {
+        // ---- MMAs, issued by one lane (the walk is made by all of them)
+        const int steps = p.hd / 16;
+        const uint32_t id_s = idesc(kBlock, false), id_o = idesc(p.hd, true);
+        uint32_t item = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        bool ok = true;
+        auto wait_full = [&](uint32_t first) {  // a block's chunks of K or V
+            for (int c = 0; c < NCH; ++c)
+                if (ok) ok = mbar_wait_bounded(&ctl.full[(first + c) % S::kStages], ((first + c) / S::kStages) & 1);
+            tc_fence_after();
+        };
+        auto release = [&](uint32_t first) {
+            for (int c = 0; c < NCH; ++c) tc_commit(&ctl.empty[(first + c) % S::kStages]);
+        };
+        auto scores = [&](int t, uint32_t first) {
+            uint32_t acc = 0;
+            for (int part = kParts - 1; part >= 0; --part)  // the small products first
+                for (int k = 0; k < steps; ++k) {
+                    const int c = k >> 2, in = (k & 3) * 32;
+                    mma_ss(tmem + 128 * t, desc_k(q_chunk(t, part, c) + in), desc_k(chunk_at(first + c) + in), id_s, acc);
+                    acc = 1;
+                }
+            tc_commit(&ctl.s_full[t]);
+        };
+        auto sums = [&](int t, uint32_t first, uint32_t acc) {
+            const uint32_t v = chunk_at(first);
+            for (int k = 0; k < kBlock / 16; ++k)
+                for (int part = kParts - 1; part >= 0; --part) {
+                    mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 32 * (k >> 1) + 16 * part + 8 * (k & 1), desc_mn(v + k * 2048),
+                           id_o, acc);
+                    acc = 1;
+                }
+        };
+        while (__all_sync(0xffffffffu, ok) && w.next(p, x)) {
+            const int kv = x.head / p.blocks, heads = min(p.per_block, G - (x.head - kv * p.blocks) * p.per_block);
+            const int halves = x.t.ntok * heads > kHalf ? 2 : 1;
+            if (lane == 0) {
+                for (int t = 0; t < halves; ++t) {
+                    if (ok) ok = mbar_wait_bounded(&ctl.q_ready[t], q_phase[t]);
+                    q_phase[t] ^= 1;
+                }
+                wait_full(item);
+                if (ok) {
+                    for (int t = 0; t < halves; ++t) scores(t, item);
+                    release(item);
+                }
+                for (int u = x.from; ok && u < x.to; ++u) {
+                    const uint32_t v = item + NCH, next = item + 2 * NCH;
+                    const bool last = u + 1 == x.to;
+                    wait_full(v);
+                    for (int t = 0; ok && t < halves; ++t) {
+                        ok = mbar_wait_bounded(&ctl.p_ready[t], p_phase[t]);
+                        p_phase[t] ^= 1;
+                        if (!ok) break;
+                        tc_fence_after();
+                        sums(t, v, u > x.from);
+                        if (t + 1 == halves) release(v);
+                        if (last) {
+                            tc_commit(&ctl.o_full[t]);
+                        } else {
+                            if (t == 0) wait_full(next);
+                            if (ok) scores(t, next);
+                        }
+                    }
+                    if (ok && !last) release(next);
+                    item = next;
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0 && !ok) {  // what was issued ends before tensor memory is freed
+            tc_commit(&ctl.drained);
+            mbar_wait_bounded(&ctl.drained, 0);
+            flag_bad(kFlagTimeout, 0);
+        }
+        __syncwarp();
+    } else if (work) {
+        // ---- copies: warp i of four has slots 32 i .. 32 i + 31 of a block
+        const int i = warp - kMmaWarp - 1;
+        uint32_t item = 0, done = 0;  // chunks asked for, chunks handed over
+        int piece = 0, block = 0;
+        bool ok = true;
+        const int chunks16 = p.hd / 8;  // 16-byte pieces of a row
+        // of the chunks in flight: which hold V to be looked at (bit n % 32 of chunk n), and their pieces (four bits each)
+        uint32_t look = 0;
+        u64 pieces = 0;
+        auto hand_over = [&]() {
+            const uint32_t n = done++;
+            if ((look >> (n % 32)) & 1u) {
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (static_cast<int>(n % NCH) * 8 + (lane & 7) >= chunks16) continue;
+                    const uint32_t at = chunk_at(n) + swz(32 * i + 4 * k + (lane >> 3), lane & 7);
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+                    if (finite_f16x2(v[0]) && finite_f16x2(v[1]) && finite_f16x2(v[2]) && finite_f16x2(v[3])) continue;
+                    bad = true;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if ((v[j] & 0x7c00u) == 0x7c00u) v[j] &= 0xffff0000u;
+                        if ((v[j] & 0x7c000000u) == 0x7c000000u) v[j] &= 0x0000ffffu;
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                 : "memory");
+                }
+                // pieces in flight are few: the number's last four bits tell which
+                if (bad) {
+                    const uint32_t low = static_cast<uint32_t>(pieces >> (4 * (n % 16))) & 15u;
+                    ctl.poison[low] = piece - ((piece - low) & 15u);
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.full[n % S::kStages]);
+        };
+        while (ok && w.next(p, x)) {
+            const RowTile& tile = x.t;
+            const int kv = x.head / p.blocks;
+            ++piece;
+            for (int u = x.from; ok && u < x.to; ++u, ++block) {
+                const int j0 = tile.lo + u * kBlock, slot = j0 + 32 * i + lane;
+                const int64_t at = slot < tile.hi ? row_offset(p.c, tile.seq, slot) : -1;
+                const uint32_t there = __ballot_sync(0xffffffffu, at >= 0);
+                const int64_t base = at >= 0 ? at + static_cast<int64_t>(kv) * p.hd : 0;
+                const bool check = SPLIT || j0 < tile.all_lo || j0 + kBlock > tile.all_hi;
+                int64_t off[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) off[k] = __shfl_sync(0xffffffffu, base, 4 * k + (lane >> 3));
+#pragma unroll
+                for (int kc = 0; kc < 2 * NCH; ++kc) {  // K's chunks, then V's
+                    const bool is_v = kc >= NCH;
+                    const int c = kc % NCH;
+                    const __half* pool = static_cast<const __half*>(is_v ? p.c.v : p.c.k);
+                    const uint32_t n = item;
+                    if (ok && n >= S::kStages)
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
+                    if (!ok) break;
+                    ++item;
+                    if (kc == 0 && lane == 0) ctl.live[block % kLiveRing][i] = there;
+                    pieces = (pieces & ~(15ull << (4 * (n % 16)))) | static_cast<u64>(piece & 15) << (4 * (n % 16));
+                    look = is_v && check ? look | 1u << (n % 32) : look & ~(1u << (n % 32));
+                    if (8 * c + (lane & 7) < chunks16) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int row = 4 * k + (lane >> 3);
+                            cp_async16(chunk_at(n) + swz(32 * i + row, lane & 7), pool + off[k] + 64 * c + 8 * (lane & 7),
+                                       (there >> row) & 1u ? 16u : 0u);
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (item > S::kLag) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(S::kLag) : "memory");
+                        hand_over();
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (ok) {
+            while (done < item) hand_over();
+        } else if (lane == 0) {
+            flag_bad(kFlagTimeout, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <bool SPLIT, int NCH>
+cudaError_t launch_t(const PagedRowsParams& p, cudaStream_t stream) {
+    auto kernel = paged_rows_tc_kernel<SPLIT, NCH>;
+    constexpr int smem = Shape<SPLIT, NCH>::kSmem;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(kSms), kThreads, smem, stream, 1, p);
+}
+
+}  // namespace
+
+RowsShape paged_rows_tc_shape() { return {kTileRows, kBlock, kSms}; }
+
+cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream) {
+    if (p.out_bf16) return p.hd <= 64 ? launch_t<false, 1>(p, stream) : launch_t<false, 2>(p, stream);
+    return p.hd <= 64 ? launch_t<true, 1>(p, stream) : launch_t<true, 2>(p, stream);
+}
+
+cudaError_t paged_rows_tc_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {
+    return status_read(stream, flags, bad);
+}

@@ -961,7 +961,7 @@ extern "C" qkv_status qkv_check_device_error(void* stream, uint32_t* flags_out, 
     if (!flags) bad = pbad;
     flags |= pflags;
     for (auto read : {paged_store_status_read, paged_attn_status_read, paged_evict_status_read, paged_rows_plan_status_read,
-                      paged_rows_status_read}) {
+                      paged_rows_status_read, paged_rows_tc_status_read}) {
         e = read(static_cast<cudaStream_t>(stream), &flags, &bad);
         if (e != cudaSuccess) return cuda_fail(e, "reading a paged-cache status word");
     }

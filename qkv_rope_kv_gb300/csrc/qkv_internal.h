@@ -186,6 +186,7 @@ struct alignas(16) RowTile {
     int32_t row0, ntok;  // q rows
     int32_t lo, hi;      // slots that are read: lo a multiple of the block
     int32_t base;        // row i sees [max(0, base + i - window), base + i); prefix: [0, row_end[row0 + i])
+    int32_t all_lo, all_hi;  // slots that every row sees
 };
 struct RowPiece {  // for each CTA, its last tile where that goes on in other CTAs and began in this one
     int64_t start;  // the tile's first unit, over all heads
@@ -233,7 +234,12 @@ struct RowsShape {
     int32_t rows, block, ctas;
 };
 RowsShape paged_rows_shape(const PagedRowsParams& p);
+RowsShape paged_rows_tc_shape();
+RowsShape paged_rows_any_shape(const PagedRowsParams& p);
+bool paged_rows_on_tensor_cores(const PagedRowsParams& p);
+cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream);
 cudaError_t paged_rows_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
+cudaError_t paged_rows_tc_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
 cudaError_t paged_rows_plan_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
 
 struct PagedEvictParams {
