@@ -222,8 +222,10 @@ extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* ca
 namespace {
 
 // What the attention of many rows takes from plan and cache; `nt` q rows.
-void rows_params(const qkv_plan* plan, int32_t nt, PagedRowsParams* p) {
+void rows_params(const qkv_plan* plan, const qkv_paged_kv* c, int32_t nt, bool prefix, PagedRowsParams* p) {
+    p->c.n_seq = c->n_seq;
     p->nt = nt;
+    p->prefix = prefix;
     p->nh = plan->d.n_head;
     p->nkv = plan->d.n_head_kv;
     p->hd = plan->d.head_dim;
@@ -271,7 +273,7 @@ RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t a
 // What the call's kernel needs.  The size is that of the larger kind of kernel: which one it is depends on addresses too.
 RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t attn_bytes) {
     RowsLayout l = rows_layout(p, c, attn_bytes, paged_rows_shape(p));
-    for (const RowsShape& shape : {paged_rows_any_shape(p), paged_rows_tc_shape()}) {
+    for (const RowsShape& shape : {paged_rows_any_shape(p), paged_rows_tc_shape(true), paged_rows_tc_shape(false)}) {
         const size_t n = rows_layout(p, c, attn_bytes, shape).bytes;
         if (n > l.bytes) l.bytes = n;
     }
@@ -334,7 +336,7 @@ extern "C" qkv_status qkv_prompt_attn_workspace_bytes(const qkv_plan* plan, cons
     if (plan->d.n_head % plan->d.n_head_kv != 0) return api_fail(QKV_ERR_UNSUPPORTED, "uneven groups of q heads");
     PagedRowsParams p;
     std::memset(&p, 0, sizeof p);
-    rows_params(plan, nt, &p);
+    rows_params(plan, cache, nt, false, &p);
     *out = rows_layout(p, cache, 0).bytes;
     return QKV_OK;
 }
@@ -354,7 +356,7 @@ extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged
     if (a->nt == 0) return QKV_OK;
     REQUIRE(a->d_first && a->d_lens, "d_first or d_lens is null");
     REQUIRE(aligned(a->d_first, 4) && aligned(a->d_lens, 4), "a pointer is not aligned to its elements");
-    rows_params(plan, a->nt, &p);
+    rows_params(plan, cache, a->nt, false, &p);
     const RowsLayout l = rows_layout(p, cache, 0);
     REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
     REQUIRE(a->workspace_bytes >= l.bytes, "the workspace has %zu bytes, %zu are needed", a->workspace_bytes, l.bytes);
@@ -384,7 +386,7 @@ extern "C" qkv_status qkv_prefix_attn_workspace_bytes(const qkv_plan* plan, cons
     if (plan->d.n_head % plan->d.n_head_kv != 0) return api_fail(QKV_ERR_UNSUPPORTED, "uneven groups of q heads");
     PagedRowsParams p;
     std::memset(&p, 0, sizeof p);
-    rows_params(plan, cache->n_seq, &p);
+    rows_params(plan, cache, cache->n_seq, true, &p);
     *out = rows_layout(p, cache, attn_layout(plan, cache, false).total).bytes;
     return QKV_OK;
 }
@@ -401,7 +403,7 @@ extern "C" qkv_status qkv_prefix_attn_step(const qkv_plan* plan, const qkv_paged
     REQUIRE(a->d_lens && a->d_share && a->d_prefix_len, "d_lens, d_share or d_prefix_len is null");
     REQUIRE(aligned(a->d_lens, 4) && aligned(a->d_share, 4) && aligned(a->d_prefix_len, 4),
             "a pointer is not aligned to its elements");
-    rows_params(plan, cache->n_seq, &p);
+    rows_params(plan, cache, cache->n_seq, true, &p);
     const AttnLayout al = attn_layout(plan, cache, false);
     const RowsLayout l = rows_layout(p, cache, al.total);
     REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");

@@ -1,20 +1,29 @@
 // Attention of many q rows over a paged f16 cache on the 5th-generation tensor cores (qkv_prompt_attn_step, and the prefix of
 // qkv_prefix_attn_step; include/qkv.h has the contracts).
 //
-// s_j = scale * q.K_j, running maximum m and sum l of each row, out = sum p_j V_j / l, scores in log2 terms.  A tile of 256
-// q rows, as two halves of 128 (the rows of a tcgen05.mma), goes over blocks of 128 slots: S = Q K^T and O += P V with both
-// accumulators in tensor memory, 128 columns each for a half.  P, in f16, takes the place of S there and is the second
-// product's A operand.  While one half's softmax runs, the tensor cores work for the other half, and K and V are read once
-// for both.
-//   warps 0-3, 4-7   softmax of the halves, a row a thread: S out of tensor memory, P back into it, O rescaled
-//                    where the maximum moved by more than 2^kLazy; at the end O / l to memory
-//   warp 8           issues the MMAs
-//   warps 9-12       copy K and V through the page table into a ring of chunks of 128 slots x 64 columns (cp.async, so pages
-//                    of any size; the 128-byte swizzle that the MMA reads)
+// s_j = scale * q.K_j, running maximum m and sum l of each row, out = sum p_j V_j / l, scores in log2 terms.  128 q rows (the
+// rows of a tcgen05.mma) go over blocks of 128 slots: S = Q K^T and O += P V with both accumulators in tensor memory, 128
+// columns each.  P, in f16, takes the place of S there and is the second product's A operand.  Two such streams go side by
+// side, each with S and O of its own: while one's softmax runs, the tensor cores work for the other.
+//   wide    a tile has 256 rows, a stream takes 128 of them over all blocks, and K and V are read once for both
+//   NARROW  a tile has 128 rows, the streams take the even and the odd blocks, and their sums are joined at the end
+// A block of a wide tile takes 2048 cycles of the tensor cores (8192 multiply-adds in 64 cycles each way), twice that SPLIT.
+//   warps 0-3, 4-7   softmax of the streams, a row a thread: S out of tensor memory, P back into it (in two halves, so
+//                    that its product begins early), O rescaled where the maximum moved by more than 2^kLazy; at
+//                    the end O / l to memory
+//   warp 8           issues the MMAs (9-11 only fill up its warpgroup)
+//   warps 12-15      copy K and V into a ring of chunks of 128 slots x 64 columns in the 128-byte swizzle that the MMA reads.
+//                    Pages of a multiple of 8 slots: 12 asks for boxes of a page's rows by TMA, 13-15 hand them on and
+//                    look at V where that is needed.  Others: all four by cp.async, a row at a time.
 // SPLIT (out F32): q is kept as the sum of two f16 (rounded, and the remainder rounded) and so are the weights, both
 // products are made twice, and 22 bits of each are kept.  Otherwise (out BF16) once, of the rounded values: 2^-11, an
 // eighth of what out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are
 // 2^(s - m + kShift), far from f16's ends on both sides.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
 #include "paged_rows.cuh"
 
 namespace {
@@ -22,22 +31,28 @@ namespace {
 using namespace qkv_rows;
 using namespace qkv_ptx;
 
-constexpr int kTileRows = 256, kHalf = 128, kBlock = 128;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarps = 4, kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+constexpr int kHalf = 128, kBlock = 128;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12, kLoadWarps = 4, kThreads = 32 * (kLoadWarp + kLoadWarps);
+// Registers: 128 a thread at launch, of which the copying and issuing warpgroups give up what the two with a row of scores
+// in registers take: 2 * 128 * (72 + 184) = 512 * 128.
+constexpr int kLaunchRegs = 128, kFewRegs = 72, kManyRegs = 184;
+static_assert(2 * 128 * (kFewRegs + kManyRegs) <= kThreads * kLaunchRegs, "registers");
 constexpr int kChunkBytes = kBlock * 128;  // 128 slots (or q rows) x 64 columns
 constexpr unsigned int kFlagTimeout = 2u;
+constexpr int kControlBytes = 2560;  // barriers and small tables, behind the chunks
 constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
 
-template <bool SPLIT, int NCH>  // NCH chunks of 64 columns a head
+template <bool SPLIT, int NCH, bool NARROW>  // NCH chunks of 64 columns a head
 struct Shape {
-    static constexpr int kQBytes = 2 * NCH * (SPLIT ? 2 : 1) * kChunkBytes;
-    static constexpr int kStages = SPLIT ? (NCH == 2 ? 6 : 10) : (NCH == 2 ? 10 : 12);  // even: a head's chunks are neighbours
-    // Copies in flight ahead of the one that is waited for.  The MMAs free a block's V only after the next block's K is
-    // there, so that many chunks must fit behind those in flight.
+    static constexpr int kQChunks = (NARROW ? 1 : 2) * NCH * (SPLIT ? 2 : 1);
+    static constexpr int kRoom = 14 - kQChunks;
+    static constexpr int kStages = kRoom > kMaxStages ? kMaxStages : kRoom;  // even: a head's chunks are neighbours
+    // Copies in flight ahead of the one that is waited for (cp.async).  The MMAs free a block's V only after the next
+    // block's K is there, so that many chunks must fit behind those in flight.
     static constexpr int kLag = kStages - 2 * NCH > 5 ? 5 : kStages - 2 * NCH;
-    static constexpr int kSmem = 1024 + kQBytes + kStages * kChunkBytes;
+    static constexpr int kControlAt = (kQChunks + kStages) * kChunkBytes, kSmem = kControlAt + kControlBytes;
     static constexpr float kShift = SPLIT ? 12.f : 6.f, kLazy = SPLIT ? 3.f : 8.f;  // weights stay below 2^15
-    static_assert(kSmem + 1024 <= 227 * 1024 && kStages <= kMaxStages && kStages % 2 == 0, "shared memory");
+    static_assert(kSmem <= 227 * 1024 && kStages % 2 == 0 && kStages % NCH == 0, "shared memory");
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -74,6 +89,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(accumulate)
                  : "memory");
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int col, int row, int page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row), "r"(page), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // N consecutive columns of this warp's 32 lanes: thread l has lane l's.
@@ -188,26 +210,43 @@ __device__ __noinline__ void add_non_finite(const PagedRowsParams& p, int seq, i
 }
 
 struct Control {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], drained;
+    uint64_t landed[kMaxStages], full[kMaxStages], empty[kMaxStages];
+    uint64_t q_ready[2], s_full[2], p_half[2], p_ready[2], o_full[2], joined, drained;
     uint32_t live[kLiveRing][4];   // slots of a block that are there
-    uint32_t poison[kPoisonRing];  // n: in piece n - 1, V had infinities or NaN that were replaced
+    uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
+    float unscale[kHalf];          // NARROW: of the rows of q
+    float2 ml[kHalf];              // NARROW: maxima and sums of the second stream
     uint32_t tmem;
 };
+static_assert(sizeof(Control) <= kControlBytes, "control");
 
-template <bool SPLIT, int NCH>
-__global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid_constant__ PagedRowsParams p) {
-    using S = Shape<SPLIT, NCH>;
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ Control ctl;
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const uint32_t q_at = smem_u32(smem), ring_at = q_at + S::kQBytes;
+// Replace infinities and NaN among 16 bytes of V by zeros.
+__device__ __forceinline__ bool clean16(uint32_t at) {
+    uint32_t v[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+    if (finite_f16x2(v[0]) && finite_f16x2(v[1]) && finite_f16x2(v[2]) && finite_f16x2(v[3])) return false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if ((v[j] & 0x7c00u) == 0x7c00u) v[j] &= 0xffff0000u;
+        if ((v[j] & 0x7c000000u) == 0x7c000000u) v[j] &= 0x0000ffffu;
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    return true;
+}
+
+template <bool SPLIT, int NCH, bool NARROW>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_rows_tc_kernel(const __grid_constant__ PagedRowsParams p, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v, int box) {
+    using S = Shape<SPLIT, NCH, NARROW>;
+    extern __shared__ __align__(1024) unsigned char smem[];  // atoms of the swizzle: no other shared memory before it
+    Control& ctl = *reinterpret_cast<Control*>(smem + S::kControlAt);
+    const uint32_t q_at = smem_u32(smem), ring_at = q_at + S::kQChunks * kChunkBytes;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     constexpr int kParts = SPLIT ? 2 : 1;
-    // chunk c of part `part` (0: rounded, 1: remainder) of half t of q
-    auto q_chunk = [&](int t, int part, int c) { return q_at + ((t * kParts + part) * NCH + c) * kChunkBytes; };
+    // chunk c of part `part` (0: rounded, 1: remainder) of stream t's q
+    auto q_chunk = [&](int t, int part, int c) { return q_at + (((NARROW ? 0 : t) * kParts + part) * NCH + c) * kChunkBytes; };
     auto chunk_at = [&](uint32_t n) { return ring_at + n % S::kStages * kChunkBytes; };
 
     if (warp == kMmaWarp) {
@@ -218,15 +257,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
     if (tid < kPoisonRing) ctl.poison[tid] = 0;
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(&ctl.full[s], kLoadWarps);
+            mbar_init(&ctl.landed[s], 1);
+            mbar_init(&ctl.full[s], box ? kLoadWarps - 1 : kLoadWarps);
             mbar_init(&ctl.empty[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&ctl.q_ready[t], 4);
+            mbar_init(&ctl.q_ready[t], NARROW ? 8 : 4);
             mbar_init(&ctl.s_full[t], 1);
+            mbar_init(&ctl.p_half[t], 4);
             mbar_init(&ctl.p_ready[t], 4);
             mbar_init(&ctl.o_full[t], 1);
         }
+        mbar_init(&ctl.joined, 4);
         mbar_init(&ctl.drained, 1);
         mbar_fence_init();
     }
@@ -241,83 +283,104 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
     Walk w;
     Piece x;
     const bool work = w.begin(p);
+    if (work) {
+        if (warp < kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    }
     if (work && warp < kSoftWarps) {
-        // ---- softmax: thread `lane` of warp w has row 32 (w % 4) + lane of half w / 4
+        // ---- softmax: thread `lane` of warp w has row 32 (w % 4) + lane of stream w / 4
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t s_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 128 * t, o_at = s_at + 256;
-        uint32_t s_phase = 0, o_phase = 0;
-        int piece = 0, block = 0;
+        uint32_t s_phase = 0, o_phase = 0, join_phase = 0;  // o_phase: bit t
+        int piece = 0, block0 = 0;
         bool ok = true;
         while (ok && w.next(p, x)) {
             const RowTile& tile = x.t;
             const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
-            const int rows = tile.ntok * heads, row0 = t * kHalf + 32 * quarter, r = row0 + lane;
+            const int rows = tile.ntok * heads, row0 = (NARROW ? 0 : t * kHalf) + 32 * quarter, r = row0 + lane;
+            const int first_block = block0;
+            block0 += x.to - x.from;
             ++piece;
             if (tid == 0) note_piece(p, w, x, w.u >= w.end);
-            if (t == 1 && rows <= kHalf) {  // nothing for this half
-                block += x.to - x.from;
-                continue;
-            }
-            // q of the warp's rows, a row at a time
+            if (!NARROW && t == 1 && rows <= kHalf) continue;  // nothing for this stream
+            // q of the warp's rows (NARROW: every other one, the rest is the other stream's warp's), a row at a time
             float unscale = 1.f;
-#pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const int row = row0 + i, tok = row / heads;
-                float v[4] = {0.f, 0.f, 0.f, 0.f};
-                if (row < rows && 4 * lane < p.hd) {
-                    const float* src = p.q + (tile.row0 + tok) * p.q_stride +
-                                       static_cast<int64_t>(kv * G + g0 + row - tok * heads) * p.hd + 4 * lane;
-                    if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-                        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-                    } else {
+            constexpr int kStep = NARROW ? 2 : 1, kAhead = 8;
+#pragma unroll 1
+            for (int i0 = NARROW ? t : 0; i0 < 32; i0 += kAhead * kStep) {
+                float v[kAhead][4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = __ldcg(src + k);
+                for (int j = 0; j < kAhead; ++j) {
+                    const int row = row0 + i0 + j * kStep, tok = row / heads;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[j][k] = 0.f;
+                    if (row < rows && 4 * lane < p.hd) {
+                        const float* src = p.q + (tile.row0 + tok) * p.q_stride +
+                                           static_cast<int64_t>(kv * G + g0 + row - tok * heads) * p.hd + 4 * lane;
+                        if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+                            const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+                            v[j][0] = f.x, v[j][1] = f.y, v[j][2] = f.z, v[j][3] = f.w;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) v[j][k] = __ldcg(src + k);
+                        }
                     }
                 }
-                float big = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[k] *= p.scale * kLog2e;
-                    big = fmaxf(big, fabsf(v[k]));
-                }
+                for (int j = 0; j < kAhead; ++j) {
+                    const int i = i0 + j * kStep;
+                    float big = 0.f;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
-                int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
-                e = e == 128 ? 13 : max(-113, min(e, 126));
-                const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-                if (lane == i) unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-                if (4 * lane < 64 * NCH) {
-                    uint32_t hi[2], lo[2];
-                    split2(v[0] * sc, v[1] * sc, hi[0], lo[0]);
-                    split2(v[2] * sc, v[3] * sc, hi[1], lo[1]);
-                    const int c = lane >> 4, in = (lane & 15) >> 1;  // chunk, and 16 bytes of its row
-                    const uint32_t at = swz(32 * quarter + i, in) + 8 * (lane & 1);
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, 0, c) + at), "r"(hi[0]), "r"(hi[1]) : "memory");
-                    if (SPLIT)
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, kParts - 1, c) + at), "r"(lo[0]),
-                                     "r"(lo[1])
+                    for (int k = 0; k < 4; ++k) {
+                        v[j][k] *= p.scale * kLog2e;
+                        big = fmaxf(big, fabsf(v[j][k]));
+                    }
+                    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));  // not below zero
+                    // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
+                    int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
+                    e = e == 128 ? 13 : max(-113, min(e, 126));
+                    const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+                    const float un = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+                    if (NARROW) {
+                        if (lane == 0) ctl.unscale[row0 + i] = un;
+                    } else if (lane == i) {
+                        unscale = un;
+                    }
+                    if (4 * lane < 64 * NCH) {
+                        uint32_t hi[2], lo[2];
+                        split2(v[j][0] * sc, v[j][1] * sc, hi[0], lo[0]);
+                        split2(v[j][2] * sc, v[j][3] * sc, hi[1], lo[1]);
+                        const int c = lane >> 4, in = (lane & 15) >> 1;  // chunk, and 16 bytes of its row
+                        const uint32_t at = swz(32 * quarter + i, in) + 8 * (lane & 1);
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, 0, c) + at), "r"(hi[0]), "r"(hi[1])
                                      : "memory");
+                        if (SPLIT)
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, kParts - 1, c) + at), "r"(lo[0]),
+                                         "r"(lo[1])
+                                         : "memory");
+                    }
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.q_ready[t]);
+            if (lane == 0) mbar_arrive(&ctl.q_ready[NARROW ? 0 : t]);
 
             const bool busy = row0 < rows, mine = r < rows;
+            const bool both = NARROW ? x.to - x.from > 1 : true;  // NARROW: the second stream has blocks
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, r / heads, see_lo, see_hi);
             float m = -CUDART_INF_F, l = 0.f;
-            for (int u = x.from; u < x.to; ++u, ++block) {
+            for (int u = x.from + (NARROW ? t : 0); u < x.to; u += NARROW ? 2 : 1) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.s_full[t], s_phase));
                 s_phase ^= 1;
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
+                    const bool begun = u >= x.from + (NARROW ? 2 : 1);  // O holds sums
+                    if (NARROW && !begun) unscale = ctl.unscale[r];
                     const int j0 = tile.lo + u * kBlock;
-                    const uint32_t* live = ctl.live[block % kLiveRing];
+                    const uint32_t* live = ctl.live[(first_block + u - x.from) % kLiveRing];
                     const bool mixed = j0 < tile.all_lo || j0 + kBlock > tile.all_hi ||
                                        (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
                     // the slots of columns 32 c .. 32 c + 31 that the row sees
@@ -327,29 +390,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
                         const uint32_t from = a <= 0 ? 0xffffffffu : a >= 32 ? 0u : 0xffffffffu << a;
                         return below & from & live[c];
                     };
-                    float top;
+                    uint32_t v[kBlock / 32][32];
                     for (int round = 0;; ++round) {
-                        top = -CUDART_INF_F;
+#pragma unroll
+                        for (int c = 0; c < kBlock / 32; ++c) tm_ld32(s_at + 32 * c, v[c]);
+                        tc_wait_ld();
                         u64 odd = 0;
+                        if (mixed) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t v[32];
-                            tm_ld32(s_at + 32 * c, v);
-                            tc_wait_ld();
-                            if (SPLIT) {
-#pragma unroll
-                                for (int k = 0; k < 32; k += 2)
-                                    odd = fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), 0, odd);
-                            }
-                            if (mixed) {
+                            for (int c = 0; c < kBlock / 32; ++c) {
                                 const uint32_t in = seen(c);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!((in >> k) & 1u)) v[k] = 0xff800000u;
+                                for (int k = 0; k < 32; ++k) {
+                                    const bool sees = (in >> k) & 1u;
+                                    if (SPLIT && sees && !(fabsf(__uint_as_float(v[c][k])) < CUDART_INF_F)) odd = ~0ull;
+                                    if (!sees) v[c][k] = 0xff800000u;
+                                }
                             }
+                        } else if (SPLIT) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2)
-                                top = fmaxf(top, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                            for (int c = 0; c < kBlock / 32; ++c)
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2)
+                                    odd = fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), 0, odd);
                         }
                         if (!SPLIT || round == 1) break;
                         const float2 bad = unpack2(odd);
@@ -357,20 +420,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
                         const float* q_row = p.q + static_cast<int64_t>(tile.row0 + r / heads) * p.q_stride +
                                              static_cast<int64_t>(kv * G + g0 + r % heads) * p.hd;
                         for (int k = 0; k < kBlock; ++k) {
-                            float v = __uint_as_float(tm_ld1(s_at + k));
-                            if (mine && !(fabsf(v) < CUDART_INF_F) && ((seen(k >> 5) >> (k & 31)) & 1u))
-                                v = plain_score(p, q_row, tile.seq, j0 + k, kv) * (1.f / unscale);
+                            float f = __uint_as_float(tm_ld1(s_at + k));
+                            if (mine && !(fabsf(f) < CUDART_INF_F) && ((seen(k >> 5) >> (k & 31)) & 1u))
+                                f = plain_score(p, q_row, tile.seq, j0 + k, kv) * (1.f / unscale);
                             __syncwarp();
-                            tm_st1(s_at + k, __float_as_uint(v));
+                            tm_st1(s_at + k, __float_as_uint(f));
                         }
                         tc_wait_st();
                     }
-                    top *= unscale;
+                    float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+#pragma unroll
+                        for (int c = 0; c < kBlock / 32; ++c)
+                            tops[c] = fmaxf(fmaxf(tops[c], __uint_as_float(v[c][k])), __uint_as_float(v[c][k + 1]));
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * unscale;
                     if (__any_sync(0xffffffffu, top > m + S::kLazy)) {
                         const float next = fmaxf(m, top), keep = m == next ? 1.f : ex2(m - next);
                         m = next;
                         l *= keep;
-                        if (u > x.from)
+                        if (begun)
+#pragma unroll 1
                             for (int c = 0; c < p.hd; c += 16) {
                                 uint32_t o[16];
                                 tm_ld16(o_at + c, o);
@@ -382,43 +452,66 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
                     }
                     const float base = (m == -CUDART_INF_F ? 0.f : m) - S::kShift;
                     const u64 by = pack2(unscale, unscale), minus = pack2(-base, -base);
-                    u64 sum = 0;
+                    u64 sum[2] = {0, 0};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32], h[16], low[16];
-                        tm_ld32(s_at + 32 * c, v);
-                        tc_wait_ld();
-                        if (mixed) {
-                            const uint32_t in = seen(c);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!((in >> k) & 1u)) v[k] = 0xff800000u;
-                        }
+                    for (int c = 0; c < kBlock / 32; ++c) {
+                        uint32_t h[16], low[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const float2 y = unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), by, minus));
+                            const float2 y =
+                                unpack2(fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), by, minus));
                             const float a = ex2(y.x), b = ex2(y.y);
-                            sum = add2(sum, pack2(a, b));
+                            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
                             if (SPLIT) split2(a, b, h[k / 2], low[k / 2]);
                             else h[k / 2] = f16x2(a, b);
                         }
                         tm_st16(s_at + 32 * c, h);
                         if (SPLIT) tm_st16(s_at + 32 * c + 16, low);
+                        if (c == 1) {
+                            tc_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&ctl.p_half[t]);
+                        }
                     }
-                    const float2 both = unpack2(sum);
-                    l += both.x + both.y;
+                    const float2 part = unpack2(add2(sum[0], sum[1]));
+                    l += part.x + part.y;
                     tc_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(&ctl.p_half[t]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.p_ready[t]);
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.o_full[t], o_phase));
-            o_phase ^= 1;
+            if (NARROW && t == 1 && both) {
+                ctl.ml[r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.joined);
+            }
+            // NARROW: both streams read the one q, so both wait for both
+            for (int k = 0; k < 2; ++k) {
+                if (NARROW ? k == 1 && !both : k != t) continue;
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.o_full[k], (o_phase >> k) & 1));
+                o_phase ^= 1u << k;
+            }
+            if (NARROW && t == 0 && both) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.joined, join_phase));
+                join_phase ^= 1;
+            }
             if (!ok) break;
             tc_fence_after();
-            if (!busy) continue;
+            if (!busy || (NARROW && t == 1)) continue;
+            float k0 = 1.f, k1 = 0.f;
+            if (NARROW && both) {
+                const float2 other = ctl.ml[r];
+                const float top = fmaxf(m, other.x);
+                k0 = m == top ? 1.f : ex2(m - top);
+                k1 = other.x == top ? 1.f : ex2(other.x - top);
+                m = top;
+                l = l * k0 + other.y * k1;
+            }
             const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
             const int i = r / heads, row = tile.row0 + i, h = kv * G + g0 + r - i * heads;
             const bool whole = x.whole(), empty = see_lo >= see_hi;
@@ -429,13 +522,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
             if (!whole) to = part_o(p, part, r);
             else if (!p.first) to = p.prefix_out + (static_cast<int64_t>(row) * p.nh + h) * p.hd;
             else if (!p.out_bf16) to = static_cast<float*>(p.out) + out_at;
+#pragma unroll 1
             for (int c = 0; c < p.hd; c += 16) {
-                uint32_t v[16];
+                uint32_t v[16], y[16];
                 float o[16];
                 tm_ld16(o_at + c, v);
+                if (NARROW && both) tm_ld16(o_at + 128 + c, y);
                 tc_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(v[k]);
+                for (int k = 0; k < 16; ++k) {
+                    o[k] = __uint_as_float(v[k]);
+                    if (NARROW && both) o[k] = fmaf(o[k], k0, __uint_as_float(y[k]) * k1);
+                }
                 if (poison && mine) {
                     float more[16] = {};
                     add_non_finite(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock),
@@ -484,58 +582,105 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
         // ---- MMAs, issued by one lane (the walk is made by all of them)
         const int steps = p.hd / 16;
         const uint32_t id_s = idesc(kBlock, false), id_o = idesc(p.hd, true);
-        uint32_t item = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        uint32_t item = 0, q_phase = 0, h_phase = 0, p_phase = 0;  // item: the piece's first chunk; phases: bit t
         bool ok = true;
         auto wait_full = [&](uint32_t first) {  // a block's chunks of K or V
+#pragma unroll
             for (int c = 0; c < NCH; ++c)
                 if (ok) ok = mbar_wait_bounded(&ctl.full[(first + c) % S::kStages], ((first + c) / S::kStages) & 1);
             tc_fence_after();
         };
         auto release = [&](uint32_t first) {
+#pragma unroll
             for (int c = 0; c < NCH; ++c) tc_commit(&ctl.empty[(first + c) % S::kStages]);
         };
         auto scores = [&](int t, uint32_t first) {
             uint32_t acc = 0;
+#pragma unroll
             for (int part = kParts - 1; part >= 0; --part)  // the small products first
-                for (int k = 0; k < steps; ++k) {
-                    const int c = k >> 2, in = (k & 3) * 32;
-                    mma_ss(tmem + 128 * t, desc_k(q_chunk(t, part, c) + in), desc_k(chunk_at(first + c) + in), id_s, acc);
-                    acc = 1;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    const uint64_t a = desc_k(q_chunk(t, part, c)), b = desc_k(chunk_at(first + c));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 16 columns are 32 bytes
+                        if (4 * c + k < steps) {
+                            mma_ss(tmem + 128 * t, a + 2 * k, b + 2 * k, id_s, acc);
+                            acc = 1;
+                        }
                 }
             tc_commit(&ctl.s_full[t]);
         };
+        // O of stream t: the first half of the slots as soon as their weights are there
         auto sums = [&](int t, uint32_t first, uint32_t acc) {
-            const uint32_t v = chunk_at(first);
-            for (int k = 0; k < kBlock / 16; ++k)
-                for (int part = kParts - 1; part >= 0; --part) {
-                    mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 32 * (k >> 1) + 16 * part + 8 * (k & 1), desc_mn(v + k * 2048),
-                           id_o, acc);
-                    acc = 1;
+            const uint64_t v = desc_mn(chunk_at(first));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!ok) break;
+                if (half == 0) {
+                    ok = mbar_wait_bounded(&ctl.p_half[t], (h_phase >> t) & 1);
+                    h_phase ^= 1u << t;
+                } else {
+                    ok = mbar_wait_bounded(&ctl.p_ready[t], (p_phase >> t) & 1);
+                    p_phase ^= 1u << t;
                 }
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = half * kBlock / 32; k < (half + 1) * kBlock / 32; ++k)  // 16 slots are 2048 bytes
+#pragma unroll
+                    for (int part = kParts - 1; part >= 0; --part) {
+                        mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 32 * (k >> 1) + 16 * part + 8 * (k & 1), v + 128 * k, id_o,
+                               acc);
+                        acc = 1;
+                    }
+            }
         };
         while (__all_sync(0xffffffffu, ok) && w.next(p, x)) {
             const int kv = x.head / p.blocks, heads = min(p.per_block, G - (x.head - kv * p.blocks) * p.per_block);
-            const int halves = x.t.ntok * heads > kHalf ? 2 : 1;
-            if (lane == 0) {
-                for (int t = 0; t < halves; ++t) {
-                    if (ok) ok = mbar_wait_bounded(&ctl.q_ready[t], q_phase[t]);
-                    q_phase[t] ^= 1;
+            const int n = x.to - x.from;
+            if (lane == 0 && NARROW) {
+                auto k_of = [&](int b) { return item + 2 * b * NCH; };
+                ok = mbar_wait_bounded(&ctl.q_ready[0], q_phase & 1);
+                q_phase ^= 1u;
+                for (int b = 0; ok && b < n && b < 2; ++b) {
+                    wait_full(k_of(b));
+                    if (ok) {
+                        scores(b, k_of(b));
+                        release(k_of(b));
+                    }
                 }
-                wait_full(item);
-                if (ok) {
-                    for (int t = 0; t < halves; ++t) scores(t, item);
-                    release(item);
+                for (int b = 0; ok && b < n; ++b) {
+                    const int t = b & 1;
+                    wait_full(k_of(b) + NCH);
+                    sums(t, k_of(b) + NCH, b >= 2);
+                    if (!ok) break;
+                    release(k_of(b) + NCH);
+                    if (b + 2 >= n) {
+                        tc_commit(&ctl.o_full[t]);
+                    } else {
+                        wait_full(k_of(b + 2));
+                        if (ok) {
+                            scores(t, k_of(b + 2));
+                            release(k_of(b + 2));
+                        }
+                    }
                 }
-                for (int u = x.from; ok && u < x.to; ++u) {
-                    const uint32_t v = item + NCH, next = item + 2 * NCH;
-                    const bool last = u + 1 == x.to;
+            } else if (lane == 0) {
+                const int halves = x.t.ntok * heads > kHalf ? 2 : 1;
+                for (int t = 0; ok && t < halves; ++t) {
+                    ok = mbar_wait_bounded(&ctl.q_ready[t], (q_phase >> t) & 1);
+                    q_phase ^= 1u << t;
+                    if (t == 0) wait_full(item);
+                    if (ok) scores(t, item);
+                }
+                if (ok) release(item);
+                for (int b = 0; ok && b < n; ++b) {
+                    const uint32_t v = item + (2 * b + 1) * NCH, next = v + NCH;
+                    const bool last = b + 1 == n;
                     wait_full(v);
                     for (int t = 0; ok && t < halves; ++t) {
-                        ok = mbar_wait_bounded(&ctl.p_ready[t], p_phase[t]);
-                        p_phase[t] ^= 1;
+                        sums(t, v, b > 0);
                         if (!ok) break;
-                        tc_fence_after();
-                        sums(t, v, u > x.from);
                         if (t + 1 == halves) release(v);
                         if (last) {
                             tc_commit(&ctl.o_full[t]);
@@ -545,9 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
                         }
                     }
                     if (ok && !last) release(next);
-                    item = next;
                 }
             }
+            item += 2 * n * NCH;
             __syncwarp();
         }
         if (lane == 0 && !ok) {  // what was issued ends before tensor memory is freed
@@ -556,9 +701,90 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
             flag_bad(kFlagTimeout, 0);
         }
         __syncwarp();
-    } else if (work) {
-        // ---- copies: warp i of four has slots 32 i .. 32 i + 31 of a block
-        const int i = warp - kMmaWarp - 1;
+    } else if (work && warp >= kLoadWarp && box) {
+        // ---- copies by TMA: boxes of `box` rows of a page, lane b of warp 12 the b-th of a block
+        uint32_t item = 0;
+        int piece = 0, block = 0;
+        bool ok = true;
+        if (warp == kLoadWarp) {
+            while (ok && w.next(p, x)) {
+                const RowTile& tile = x.t;
+                const int col = x.head / p.blocks * p.hd, per = kBlock / box;
+                // page ids are asked for a block ahead
+                auto ask = [&](int u) {
+                    const int slot = tile.lo + u * kBlock + lane * box;
+                    return u < x.to && lane < per && slot < tile.hi ? page_ref(p.c, tile.seq, slot) : PageRef{0, -1};
+                };
+                PageRef asked = ask(x.from);
+                for (int u = x.from; ok && u < x.to; ++u, ++block) {
+                    const PageRef at = asked;
+                    asked = ask(u + 1);
+                    bool valid = at.in_page >= 0;
+                    if (valid && static_cast<unsigned int>(at.id) >= static_cast<unsigned int>(p.c.n_pages)) {
+                        flag_bad(kFlagIndexRange, at.id);
+                        valid = false;
+                    }
+                    const uint32_t boxes = __ballot_sync(0xffffffffu, valid);
+                    const int j0 = tile.lo + u * kBlock;
+#pragma unroll
+                    for (int kc = 0; kc < 2 * NCH; ++kc) {  // K's chunks, then V's
+                        const uint32_t n = item;
+                        if (ok && n >= S::kStages)
+                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
+                        if (!ok) break;
+                        ++item;
+                        if (kc == 0) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int s = 32 * c + lane;
+                                const uint32_t there = __ballot_sync(0xffffffffu, j0 + s < tile.hi && ((boxes >> (s / box)) & 1u));
+                                if (lane == 0) ctl.live[block % kLiveRing][c] = there;
+                            }
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&ctl.landed[n % S::kStages], __popc(boxes) * box * 128);
+                        __syncwarp();
+                        if (valid)
+                            tma_box(chunk_at(n) + lane * box * 128, kc < NCH ? &map_k : &map_v, col + 64 * (kc % NCH), at.in_page,
+                                    at.id, &ctl.landed[n % S::kStages]);
+                    }
+                }
+            }
+            if (!ok) {  // no copy is in flight when the CTA ends
+                for (uint32_t n = item > S::kStages ? item - S::kStages : 0; n < item; ++n)
+                    mbar_wait_bounded(&ctl.landed[n % S::kStages], (n / S::kStages) & 1);
+                if (lane == 0) flag_bad(kFlagTimeout, 0);
+            }
+        } else {
+            const int chunks16 = p.hd / 8, me = (warp - kLoadWarp - 1) * 32 + lane;
+            while (ok && w.next(p, x)) {
+                ++piece;
+                for (int u = x.from; ok && u < x.to; ++u) {
+                    const int j0 = x.t.lo + u * kBlock;
+                    const bool check = SPLIT || j0 < x.t.all_lo || j0 + kBlock > x.t.all_hi;
+#pragma unroll 1
+                    for (int kc = 0; kc < 2 * NCH; ++kc) {
+                        const uint32_t n = item++;
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.landed[n % S::kStages], (n / S::kStages) & 1));
+                        if (!ok) break;
+                        if (kc >= NCH && check) {
+                            const int width = min(8, chunks16 - 8 * (kc - NCH));  // 16-byte pieces of a row here
+                            bool bad = false;
+#pragma unroll 4
+                            for (int e = me; e < 8 * kBlock; e += 32 * (kLoadWarps - 1))
+                                if ((e & 7) < width) bad |= clean16(chunk_at(n) + swz(e >> 3, e & 7));
+                            if (bad) ctl.poison[piece % kPoisonRing] = piece;
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl.full[n % S::kStages]);
+                    }
+                }
+            }
+            if (!ok && lane == 0) flag_bad(kFlagTimeout, 0);
+        }
+    } else if (work && warp >= kLoadWarp) {
+        // ---- copies by cp.async: warp i of four has slots 32 i .. 32 i + 31 of a block
+        const int i = warp - kLoadWarp;
         uint32_t item = 0, done = 0;  // chunks asked for, chunks handed over
         int piece = 0, block = 0;
         bool ok = true;
@@ -571,22 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
             if ((look >> (n % 32)) & 1u) {
                 bool bad = false;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (static_cast<int>(n % NCH) * 8 + (lane & 7) >= chunks16) continue;
-                    const uint32_t at = chunk_at(n) + swz(32 * i + 4 * k + (lane >> 3), lane & 7);
-                    uint32_t v[4];
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
-                    if (finite_f16x2(v[0]) && finite_f16x2(v[1]) && finite_f16x2(v[2]) && finite_f16x2(v[3])) continue;
-                    bad = true;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if ((v[j] & 0x7c00u) == 0x7c00u) v[j] &= 0xffff0000u;
-                        if ((v[j] & 0x7c000000u) == 0x7c000000u) v[j] &= 0x0000ffffu;
-                    }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                                 : "memory");
-                }
+                for (int k = 0; k < 8; ++k)
+                    if (static_cast<int>(n % NCH) * 8 + (lane & 7) < chunks16)
+                        bad |= clean16(chunk_at(n) + swz(32 * i + 4 * k + (lane >> 3), lane & 7));
                 // pieces in flight are few: the number's last four bits tell which
                 if (bad) {
                     const uint32_t low = static_cast<uint32_t>(pieces >> (4 * (n % 16))) & 15u;
@@ -601,9 +814,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
             const RowTile& tile = x.t;
             const int kv = x.head / p.blocks;
             ++piece;
+            auto ask = [&](int u) {
+                const int slot = tile.lo + u * kBlock + 32 * i + lane;
+                return u < x.to && slot < tile.hi ? page_ref(p.c, tile.seq, slot) : PageRef{0, -1};
+            };
+            PageRef asked = ask(x.from);
             for (int u = x.from; ok && u < x.to; ++u, ++block) {
-                const int j0 = tile.lo + u * kBlock, slot = j0 + 32 * i + lane;
-                const int64_t at = slot < tile.hi ? row_offset(p.c, tile.seq, slot) : -1;
+                const int j0 = tile.lo + u * kBlock;
+                const int64_t at = asked.in_page >= 0 ? row_offset(p.c, asked) : -1;
+                asked = ask(u + 1);
                 const uint32_t there = __ballot_sync(0xffffffffu, at >= 0);
                 const int64_t base = at >= 0 ? at + static_cast<int64_t>(kv) * p.hd : 0;
                 const bool check = SPLIT || j0 < tile.all_lo || j0 + kBlock > tile.all_hi;
@@ -653,22 +872,64 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_tc_kernel(const __grid
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <bool SPLIT, int NCH>
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+    }();
+    return fn;
+}
+
+// A pool as columns x rows of a page x pages, read in boxes of 64 columns and `box` rows.
+bool encode(CUtensorMap* map, const PagedRowsParams& p, void* pool, int box) {
+    if (!encoder()) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.c.nkt), static_cast<cuuint64_t>(p.c.page_size),
+                                static_cast<cuuint64_t>(p.c.n_pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.c.nkt) * 2, static_cast<cuuint64_t>(p.c.page_stride) * 2};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 1}, steps[3] = {1, 1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, pool, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool SPLIT, int NCH, bool NARROW>
 cudaError_t launch_t(const PagedRowsParams& p, cudaStream_t stream) {
-    auto kernel = paged_rows_tc_kernel<SPLIT, NCH>;
-    constexpr int smem = Shape<SPLIT, NCH>::kSmem;
+    auto kernel = paged_rows_tc_kernel<SPLIT, NCH, NARROW>;
+    constexpr int smem = Shape<SPLIT, NCH, NARROW>::kSmem;
+    // fewer registers at launch than the warpgroups share out would leave some of them waiting for ever
+    static const bool enough = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs >= kLaunchRegs;
+    }();
+    if (!enough) return cudaErrorInvalidKernelImage;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3(kSms), kThreads, smem, stream, 1, p);
+    // Boxes of as many rows, a power of two, as divide a page and a block; eight rows are an atom of the swizzle.
+    int box = 1;
+    while (box < kBlock && p.c.page_size % (2 * box) == 0) box *= 2;
+    CUtensorMap k, v;
+    std::memset(&k, 0, sizeof k);
+    std::memset(&v, 0, sizeof v);
+    if (box < 8 || p.c.nkt < 64 || !encode(&k, p, p.c.k, box) || !encode(&v, p, p.c.v, box)) box = 0;
+    return launch_dependent(kernel, dim3(kSms), kThreads, smem, stream, 1, p, k, v, box);
+}
+
+template <bool SPLIT, int NCH>
+cudaError_t launch_n(const PagedRowsParams& p, cudaStream_t stream) {
+    return p.rows == kHalf ? launch_t<SPLIT, NCH, true>(p, stream) : launch_t<SPLIT, NCH, false>(p, stream);
 }
 
 }  // namespace
 
-RowsShape paged_rows_tc_shape() { return {kTileRows, kBlock, kSms}; }
+RowsShape paged_rows_tc_shape(bool narrow) { return {narrow ? kHalf : 2 * kHalf, kBlock, kSms}; }
 
 cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream) {
-    if (p.out_bf16) return p.hd <= 64 ? launch_t<false, 1>(p, stream) : launch_t<false, 2>(p, stream);
-    return p.hd <= 64 ? launch_t<true, 1>(p, stream) : launch_t<true, 2>(p, stream);
+    if (p.out_bf16) return p.hd <= 64 ? launch_n<false, 1>(p, stream) : launch_n<false, 2>(p, stream);
+    return p.hd <= 64 ? launch_n<true, 1>(p, stream) : launch_n<true, 2>(p, stream);
 }
 
 cudaError_t paged_rows_tc_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {

@@ -210,6 +210,7 @@ struct PagedRowsParams {
     int64_t out_stride;
     float* lse;
     int32_t nt, nh, nkv, hd, kv_f16;
+    int32_t prefix;             // which of the two calls
     // the plan, made on the device
     int32_t rows, block;        // of a tile, of a unit
     int32_t per_block, blocks;  // q heads of a kv head in a tile, and how many such blocks it has
@@ -234,7 +235,7 @@ struct RowsShape {
     int32_t rows, block, ctas;
 };
 RowsShape paged_rows_shape(const PagedRowsParams& p);
-RowsShape paged_rows_tc_shape();
+RowsShape paged_rows_tc_shape(bool narrow);
 RowsShape paged_rows_any_shape(const PagedRowsParams& p);
 bool paged_rows_on_tensor_cores(const PagedRowsParams& p);
 cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream);
