@@ -235,8 +235,8 @@ void rows_params(const qkv_plan* plan, const qkv_paged_kv* c, int32_t nt, bool p
 // The kernel's shape, and byte offsets of the workspace's parts.
 struct RowsLayout {
     RowsShape shape;
-    int32_t per_block, blocks, max_tiles;
-    size_t attn, total, tiles, starts, row_end, row_tile, pieces, part, prefix_out, prefix_lse, own_out, own_lse, bytes;
+    int32_t per_block, blocks, part_tokens, tile_tokens, max_tiles;
+    size_t attn, total, q_high, q_low, q_unscale, tiles, starts, row_end, row_tile, pieces, part, prefix_out, prefix_lse, own_out, own_lse, bytes;
 };
 // attn_bytes: of qkv_attn_step's workspace in front (prefix); 0: prompt.
 RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t attn_bytes, const RowsShape& shape) {
@@ -244,9 +244,11 @@ RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t a
     const bool prefix = attn_bytes > 0;
     const int32_t G = p.nh / p.nkv;
     l.shape = shape;
-    l.per_block = G < l.shape.rows ? G : l.shape.rows;
+    l.per_block = G < l.shape.part_rows ? G : l.shape.part_rows;
     l.blocks = (G + l.per_block - 1) / l.per_block;
-    const int64_t tiles = prefix ? c->n_seq : p.nt / (l.shape.rows / l.per_block) + static_cast<int64_t>(c->n_seq);
+    l.part_tokens = l.shape.part_rows / l.per_block;
+    l.tile_tokens = l.part_tokens * (l.shape.rows / l.shape.part_rows);
+    const int64_t tiles = prefix ? c->n_seq : p.nt / l.tile_tokens + static_cast<int64_t>(c->n_seq);
     l.max_tiles = static_cast<int32_t>(tiles);
     size_t at = up256(attn_bytes);
     auto take = [&](size_t n) {
@@ -261,6 +263,10 @@ RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t a
     l.starts = take(prefix ? 4 * static_cast<size_t>(c->n_seq) : 0);
     l.row_end = take(prefix ? 4 * static_cast<size_t>(c->n_seq) : 0);
     l.row_tile = take(prefix ? 4 * static_cast<size_t>(c->n_seq) : 0);
+    const size_t q = l.shape.tensor ? static_cast<size_t>(p.nt) * p.nh : 0;
+    l.q_high = take(2 * q * p.hd);
+    l.q_low = take(2 * q * p.hd);
+    l.q_unscale = take(4 * q);
     l.pieces = take(kRowsMaxCtas * sizeof(RowPiece));
     l.part = take(4 * 2 * static_cast<size_t>(l.shape.ctas) * l.shape.rows * (p.hd + 2));
     l.prefix_out = take(prefix ? 4 * rows * p.hd : 0);
@@ -284,7 +290,14 @@ void rows_workspace(const RowsLayout& l, char* ws, PagedRowsParams* p) {
     p->block = l.shape.block;
     p->per_block = l.per_block;
     p->blocks = l.blocks;
+    p->part_rows = l.shape.part_rows;
+    p->part_tokens = l.part_tokens;
+    p->tile_tokens = l.tile_tokens;
+    p->tile_cost = l.shape.tile_cost;
     p->max_tiles = l.max_tiles;
+    p->q_high = reinterpret_cast<uint16_t*>(ws + l.q_high);
+    p->q_low = reinterpret_cast<uint16_t*>(ws + l.q_low);
+    p->q_unscale = reinterpret_cast<float*>(ws + l.q_unscale);
     p->total = reinterpret_cast<int64_t*>(ws + l.total);
     p->tiles = reinterpret_cast<RowTile*>(ws + l.tiles);
     p->starts = reinterpret_cast<int32_t*>(ws + l.starts);

@@ -50,25 +50,26 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = p.nh / p.nkv;
     Walk w;
     if (!w.begin(p)) return;
+    if (tid == 0) note_none(p);
     Piece x;
     while (w.next(p, x)) {
         const RowTile& t = x.t;
         const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
-        const int rows = t.ntok * heads;
+        const int rows = t.ntok * p.per_block;
         __syncthreads();  // the last piece's rows have been read
-        if (tid == 0) note_piece(p, w, x, w.u >= w.end);
+        if (tid == 0) note_piece(p, w, x);
         if (tid < kRows) {
             int lo = 0, hi = 0;
-            if (tid < rows) row_span(p, t, tid / heads, lo, hi);
+            if (tid < rows) row_span(p, t, tid / p.per_block, lo, hi);
             lo_s[tid] = lo;
             hi_s[tid] = hi;
         }
         const float scale = p.scale * kLog2e;
         for (int e = tid; e < kRows * HDP; e += kThreads) {
-            const int r = e / HDP, d = e % HDP, i = r / heads;
+            const int r = e / HDP, d = e % HDP, i = r / p.per_block, g = r - i * p.per_block;
             q_s[r * S::kStride + d] =
-                r < rows && d < p.hd
-                    ? __ldcg(p.q + (t.row0 + i) * p.q_stride + static_cast<int64_t>(kv * G + g0 + r - i * heads) * p.hd + d) * scale
+                r < rows && g < heads && d < p.hd
+                    ? __ldcg(p.q + (t.row0 + i) * p.q_stride + static_cast<int64_t>(kv * G + g0 + g) * p.hd + d) * scale
                     : 0.f;
         }
         float m[4], l[4];
@@ -162,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
 #pragma unroll
             for (int k = 1; k < 16; k <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
             const int r = ty + 16 * i;
-            if (r >= rows) continue;
-            const int row = t.row0 + r / heads, h = kv * G + g0 + r % heads;
+            const int row = t.row0 + r / p.per_block, g = r % p.per_block, h = kv * G + g0 + g;
+            if (r >= rows || g >= heads) continue;
             if (x.whole()) {
                 const bool empty = lo_s[r] >= hi_s[r];
                 const float inv = empty ? 0.f : 1.f / l[i];
@@ -215,7 +216,7 @@ cudaError_t launch_any(const PagedRowsParams& p, cudaStream_t stream) {
 }  // namespace
 
 RowsShape paged_rows_any_shape(const PagedRowsParams& p) {
-    return {kRows, kBlock, kSms * (p.hd <= 128 ? Shape<128>::kCtas : Shape<256>::kCtas)};
+    return {kRows, kRows, kBlock, kSms * (p.hd <= 128 ? Shape<128>::kCtas : Shape<256>::kCtas), 1, false};
 }
 
 // f16 rows that 16-byte copies can read, of whole steps of 16 columns that fit tensor memory beside the scores.

@@ -12,9 +12,9 @@ using namespace qkv_paged;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMinUnits = 2;  // of a CTA: a part costs its write and its join
+constexpr int kMinUnits = 3;  // of a CTA's share: a part costs its write and its join
 
-__device__ __forceinline__ int64_t units_per_cta(int64_t total, int ctas) {
+__device__ __forceinline__ int64_t share_of(int64_t total, int ctas) {
     const int64_t even = (total + ctas - 1) / ctas;
     return even > kMinUnits ? even : kMinUnits;
 }
@@ -24,7 +24,7 @@ struct Piece {
     RowTile t;
     int tile, head;  // head: kv head and block of its q heads
     int from, to;
-    bool first;      // of the CTA's pieces
+    bool first;      // the tile lies over the CTA's beginning
     __device__ __forceinline__ bool whole() const { return from == 0 && to == t.units; }
 };
 
@@ -41,26 +41,24 @@ __device__ __forceinline__ RowTile load_tile(const PagedRowsParams& p, int i) {
 
 // The units of one CTA, piece by piece.  Every warp walks for itself; all its lanes call together.
 struct Walk {
-    int64_t u, end, per_head, total, share;
+    int64_t at, end, per_head, share;
     int tiles, tile, head;
-    bool first;
     __device__ __forceinline__ bool begin(const PagedRowsParams& p) {
         per_head = __ldcg(p.total);
         tiles = static_cast<int>(__ldcg(p.total + 1));
-        total = per_head * p.nkv * p.blocks;
-        share = units_per_cta(total, gridDim.x);
-        u = share * blockIdx.x;
-        end = min(total, u + share);
-        first = true;
-        if (u >= end) return false;
-        head = static_cast<int>(u / per_head);
-        const int64_t r = u - head * per_head;
+        const int64_t total = per_head * p.nkv * p.blocks;
+        share = share_of(total, gridDim.x);
+        at = share * blockIdx.x;
+        end = min(total, at + share);
+        if (at >= end) return false;
+        head = static_cast<int>(at / per_head);
+        const int64_t r = at - head * per_head;
         // the last tile that begins at or before r: 32 candidates at a time
         int lo = 0, n = tiles;
         const int lane = threadIdx.x & 31;
         while (n > 1) {
-            const int step = (n + 31) / 32, at = lo + lane * step;
-            const bool ok = lane * step < n && __ldcg(&p.tiles[at].unit0) <= r;
+            const int step = (n + 31) / 32, i = lo + lane * step;
+            const bool ok = lane * step < n && __ldcg(&p.tiles[i].start) <= r;
             const int last = 31 - __clz(__ballot_sync(0xffffffffu, ok));
             lo += last * step;
             n = min(step, n - last * step);
@@ -69,28 +67,31 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ bool next(const PagedRowsParams& p, Piece& x) {
-        if (u >= end) return false;
-        for (;;) {
+        while (at < end) {
             if (tile >= tiles) {
                 tile = 0;
                 ++head;
             }
             x.t = load_tile(p, tile);
-            if (x.t.units > 0) break;
-            ++tile;
+            const int64_t start = head * per_head + x.t.start;
+            x.tile = tile++;
+            if (x.t.units == 0) continue;
+            x.head = head;
+            x.from = static_cast<int>(min(at - start, static_cast<int64_t>(x.t.units)));
+            x.to = static_cast<int>(min(static_cast<int64_t>(x.t.units), end - start));
+            x.first = start <= share * blockIdx.x;
+            at = start + x.t.units + p.tile_cost;
+            if (x.from < x.to) return true;  // else only the tile's end is this CTA's
         }
-        x.tile = tile;
-        x.head = head;
-        const int64_t start = head * per_head + x.t.unit0;
-        x.from = static_cast<int>(u - start);
-        x.to = static_cast<int>(min(static_cast<int64_t>(x.t.units), end - start));
-        x.first = first;
-        first = false;
-        u = start + x.to;
-        ++tile;
-        return true;
+        return false;
     }
 };
+
+// Row of a tile for its token i and q head g of the block.
+__device__ __forceinline__ int row_of(const PagedRowsParams& p, int i, int g) {
+    const int part = i / p.part_tokens;
+    return part * p.part_rows + (i - part * p.part_tokens) * p.per_block + g;
+}
 
 // What row i of a tile sees.
 __device__ __forceinline__ void row_span(const PagedRowsParams& p, const RowTile& t, int i, int& lo, int& hi) {
@@ -112,16 +113,15 @@ __device__ __forceinline__ float* part_o(const PagedRowsParams& p, float* part, 
     return part + 2 * p.rows + static_cast<int64_t>(row) * p.hd;
 }
 
-// For the join: the CTA in which a tile begins notes how many CTAs have parts of it.
-__device__ __forceinline__ void note_piece(const PagedRowsParams& p, const Walk& w, const Piece& x, bool last) {
-    if (!last) return;
+// For the join: the CTA in which a tile begins notes how many CTAs have parts of it; one thread, first for no piece.
+__device__ __forceinline__ void note_none(const PagedRowsParams& p) { p.pieces[blockIdx.x].parts = 0; }
+__device__ __forceinline__ void note_piece(const PagedRowsParams& p, const Walk& w, const Piece& x) {
+    if (x.from > 0 || x.to == x.t.units) return;
     RowPiece r = {};
-    if (x.from == 0 && x.to < x.t.units) {
-        r.start = x.head * w.per_head + x.t.unit0;
-        r.tile = x.tile;
-        r.head = x.head;
-        r.parts = static_cast<int>((r.start + x.t.units - 1) / w.share - blockIdx.x) + 1;
-    }
+    r.start = x.head * w.per_head + x.t.start;
+    r.tile = x.tile;
+    r.head = x.head;
+    r.parts = static_cast<int>((r.start + x.t.units - 1) / w.share - blockIdx.x) + 1;
     p.pieces[blockIdx.x] = r;
 }
 

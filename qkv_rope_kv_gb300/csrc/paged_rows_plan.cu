@@ -33,14 +33,62 @@ __device__ __forceinline__ T scan(T v, T& sum, T* warp_s) {
     return before + incl - v;
 }
 
+// For the tensor cores: q as f16, scaled by a power of two for each row into [2^13, 2^14) where the remainders are far from
+// f16's subnormals, and the remainders; and by what scores are to be multiplied to be in log2 terms.  A warp a row, as
+// many bytes as q has (or half as many again); rows that belong to no sequence too.
+__device__ __forceinline__ void convert_q(const PagedRowsParams& p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = static_cast<int64_t>(p.nt) * p.nh, step = static_cast<int64_t>(gridDim.x - 1) * (kPlanThreads / 32);
+    const float by = fabsf(p.scale) * kLog2e;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5); r < rows; r += step) {
+        const int64_t tok = r / p.nh;
+        const float* q = p.q + tok * p.q_stride + (r - tok * p.nh) * p.hd + 4 * lane;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (4 * lane < p.hd) {
+            if ((reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(q));
+                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = __ldcg(q + k);
+            }
+        }
+        float big = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+        big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));  // not below zero
+        // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
+        int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
+        e = e == 128 ? 13 : max(-113, min(e, 126));
+        // scores are compared before they are multiplied: by a number above zero, the sign goes into q
+        float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+        if (p.scale < 0.f) sc = -sc;
+        const float unscale = by == 0.f ? 1.f : fmaxf(by * __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23), 1.1754944e-38f);
+        if (by == 0.f) sc = 0.f;
+        if (4 * lane < p.hd) {
+            __half2 h[2], l[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float a = v[2 * k] * sc, b = v[2 * k + 1] * sc;
+                h[k] = __floats2half2_rn(a, b);
+                const float2 f = __half22float2(h[k]);
+                l[k] = __floats2half2_rn(a - f.x, b - f.y);
+            }
+            const int64_t at = r * p.hd + 4 * lane;
+            *reinterpret_cast<uint2*>(p.q_high + at) = *reinterpret_cast<uint2*>(h);
+            if (!p.out_bf16) *reinterpret_cast<uint2*>(p.q_low + at) = *reinterpret_cast<uint2*>(l);
+        }
+        if (lane == 0) p.q_unscale[r] = unscale;
+    }
+}
+
 // Several new tokens of each sequence: tiles of neighbouring tokens.
 __global__ void __launch_bounds__(kPlanThreads) plan_prompt_kernel(const __grid_constant__ PagedRowsParams p) {
     __shared__ int off_s[kPlanThreads + 1], first_s[kPlanThreads], n_s[kPlanThreads], len_s[kPlanThreads];
     __shared__ int64_t warp_s[kPlanThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
-    const int per_tile = p.rows / p.per_block;
-    int64_t units = 0, tiles = 0;
+    if (blockIdx.x > 0) return convert_q(p);
+    const int per_tile = p.tile_tokens;
+    int64_t length = 0, tiles = 0;
     for (int b0 = 0; b0 < p.c.n_seq; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
         int count = 0;
@@ -88,15 +136,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prompt_kernel(const __grid_
                 x.units = max(1, (x.hi - x.lo + p.block - 1) / p.block);  // rows that see nothing are written too
             }
             int64_t sum;
-            x.unit0 = units + scan<int64_t>(x.units, sum, warp_s);
+            x.start = length + scan<int64_t>(x.units ? x.units + p.tile_cost : 0, sum, warp_s);
             if (t < here) p.tiles[tiles + t] = x;
-            units += sum;
+            length += sum;
         }
         tiles += here;
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        p.total[0] = units;
+        p.total[0] = length;
         p.total[1] = tiles;
     }
 }
@@ -107,8 +155,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
     __shared__ int64_t warp_s[kPlanThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
-    const int per_tile = p.rows / p.per_block;
-    int64_t units = 0, tiles = 0;
+    if (blockIdx.x > 0) return convert_q(p);
+    const int per_tile = p.tile_tokens;
+    int64_t length = 0, tiles = 0;
     // a tile ends where a round does
     for (int b0 = 0; b0 < p.c.n_seq; b0 += kPlanThreads) {
         const int i = threadIdx.x, b = b0 + i;
@@ -171,14 +220,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
             x.units = (x.hi + p.block - 1) / p.block;
         }
         int64_t sum;
-        x.unit0 = units + scan<int64_t>(x.units, sum, warp_s);
+        x.start = length + scan<int64_t>(x.units ? x.units + p.tile_cost : 0, sum, warp_s);
         if (i < here) p.tiles[tiles + i] = x;
-        units += sum;
+        length += sum;
         tiles += here;
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        p.total[0] = units;
+        p.total[0] = length;
         p.total[1] = tiles;
     }
 }
@@ -217,7 +266,7 @@ __device__ __forceinline__ void join_row(const PagedRowsParams& p, int64_t start
 __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_constant__ PagedRowsParams p, int ctas) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = units_per_cta(total, ctas);
+    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = share_of(total, ctas);
     if (share * blockIdx.x >= total) return;
     const RowPiece* s = p.pieces + blockIdx.x;
     const int parts = __ldcg(&s->parts);
@@ -227,9 +276,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_
     const int g0 = (head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
     const RowTile t = load_tile(p, __ldcg(&s->tile));
     for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < t.ntok * heads; r += gridDim.y * kJoinRows) {
-        const int i = r / heads, h = kv * G + g0 + r - i * heads;
+        const int i = r / heads, g = r - i * heads, h = kv * G + g0 + g;
         Joined j;
-        join_row(p, start, share, blockIdx.x, parts, r, j);
+        join_row(p, start, share, blockIdx.x, parts, row_of(p, i, g), j);
         int lo, hi;
         row_span(p, t, i, lo, hi);
         const bool empty = lo >= hi;
@@ -261,12 +310,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
     for (int k = 0; k < kMaxCols; ++k) j.o[k] = 0.f;
     if (prefix) {
         const RowTile t = load_tile(p, __ldcg(p.row_tile + b));
-        const int64_t per_head = __ldcg(p.total), share = units_per_cta(per_head * p.nkv * p.blocks, ctas);
-        const int blk = (h - kv * G) / p.per_block, heads = min(p.per_block, G - blk * p.per_block);
-        const int64_t start = (static_cast<int64_t>(kv) * p.blocks + blk) * per_head + t.unit0;
+        const int64_t per_head = __ldcg(p.total), share = share_of(per_head * p.nkv * p.blocks, ctas);
+        const int blk = (h - kv * G) / p.per_block;
+        const int64_t start = (static_cast<int64_t>(kv) * p.blocks + blk) * per_head + t.start;
         const int c0 = static_cast<int>(start / share), c1 = static_cast<int>((start + t.units - 1) / share);
         if (c0 < c1) {
-            join_row(p, start, share, c0, c1 - c0 + 1, (b - t.row0) * heads + h - kv * G - blk * p.per_block, j);
+            join_row(p, start, share, c0, c1 - c0 + 1, row_of(p, b - t.row0, h - kv * G - blk * p.per_block), j);
             const float inv = 1.f / j.l;
 #pragma unroll
             for (int k = 0; k < kMaxCols; ++k) j.o[k] *= inv;
@@ -299,7 +348,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
 }  // namespace
 
 cudaError_t launch_paged_rows_plan(const PagedRowsParams& p, cudaStream_t stream) {
-    return launch_dependent(p.first ? plan_prompt_kernel : plan_prefix_kernel, dim3(1), kPlanThreads, 0, stream, 1, p);
+    int converting = 0;
+    if (paged_rows_shape(p).tensor) {  // a CTA for every 4 rows a warp, up to four on an SM
+        const int64_t each = 4 * (kPlanThreads / 32), want = (static_cast<int64_t>(p.nt) * p.nh + each - 1) / each;
+        converting = static_cast<int>(want < 4 * kSms ? want : 4 * kSms);
+    }
+    return launch_dependent(p.first ? plan_prompt_kernel : plan_prefix_kernel, dim3(1 + converting), kPlanThreads, 0, stream, 1, p);
 }
 
 cudaError_t launch_paged_rows_join(const PagedRowsParams& p, cudaStream_t stream) {

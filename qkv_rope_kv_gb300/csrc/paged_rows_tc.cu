@@ -40,6 +40,7 @@ static_assert(2 * 128 * (kFewRegs + kManyRegs) <= kThreads * kLaunchRegs, "regis
 constexpr int kChunkBytes = kBlock * 128;  // 128 slots (or q rows) x 64 columns
 constexpr unsigned int kFlagTimeout = 2u;
 constexpr int kControlBytes = 2560;  // barriers and small tables, behind the chunks
+constexpr int kTileCost = 2;  // units that a tile's beginning and end take
 constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
 
 template <bool SPLIT, int NCH, bool NARROW>  // NCH chunks of 64 columns a head
@@ -61,36 +62,47 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// One lane of a warp whose lanes are all here.  The warp that issues MMAs runs as a whole and elects for each instruction, so
+// that the compiler knows all operands to be the same in its lanes, as the instructions want them (issued by `if (lane == 0)`,
+// an MMA took about 100 cycles to issue instead of the 64 that it runs).
+__device__ __forceinline__ bool elect() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    if (elect())
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Shared-memory descriptors of chunks of 128-byte rows in the 128-byte swizzle (eight rows, 1024 bytes, an atom; version 1,
 // layout type 2).  K-major (Q, K): the stride offset leads to the next eight rows, the leading one is not used.
 // MN-major (V: rows are slots, the summed dimension): the stride offset leads to the next eight slots, the leading one
 // to the next 64 columns, a chunk further.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
-    return (static_cast<uint64_t>(addr) & 0x3FFFFull) >> 4 | 1ull << 16 | (1024ull >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-    return (static_cast<uint64_t>(addr) & 0x3FFFFull) >> 4 | (static_cast<uint64_t>(kChunkBytes) >> 4) << 16 |
-           (1024ull >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// The upper halves are the same; these are the lower ones, which grow by 1 for 16 bytes.
+constexpr uint32_t kDescHigh = 1024u >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr & 0x3FFFFu) >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
+    return (addr & 0x3FFFFu) >> 4 | static_cast<uint32_t>(kChunkBytes >> 4) << 16;
 }
 // kind::f16, D f32, A and B f16, M = 128; bit 16: B is MN-major.
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn) {
     return 1u << 4 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(kHalf >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(accumulate)
-                 : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accumulate) {
+    if (elect())
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(accumulate),
+                     "r"(kDescHigh)
+                     : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(accumulate)
-                 : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accumulate) {
+    if (elect())
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(accumulate),
+                     "r"(kDescHigh)
+                     : "memory");
 }
-
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int col, int row, int page, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -136,12 +148,34 @@ __device__ __forceinline__ void tm_st1(uint32_t a, uint32_t r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(a), "r"(r) : "memory");
 }
 
+// As mbar_wait_bounded, without asking to be suspended: these waits are short, and there are many.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+    const uint32_t at = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (int i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(at), "r"(parity) : "memory");
+        if (ok) return true;
+        if ((i & 63) == 63) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitTimeoutNs) return false;
+        }
+    }
+}
+
 // ---------------------------------------------------------------- arithmetic
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 using u64 = unsigned long long;
 __device__ __forceinline__ u64 pack2(float x, float y) {
@@ -211,10 +245,9 @@ __device__ __noinline__ void add_non_finite(const PagedRowsParams& p, int seq, i
 
 struct Control {
     uint64_t landed[kMaxStages], full[kMaxStages], empty[kMaxStages];
-    uint64_t q_ready[2], s_full[2], p_half[2], p_ready[2], o_full[2], joined, drained;
+    uint64_t q_ready[2], q_free[2], s_full[2], p_half[2], p_ready[2], o_full[2], joined, drained;
     uint32_t live[kLiveRing][4];   // slots of a block that are there
     uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
-    float unscale[kHalf];          // NARROW: of the rows of q
     float2 ml[kHalf];              // NARROW: maxima and sums of the second stream
     uint32_t tmem;
 };
@@ -237,7 +270,8 @@ __device__ __forceinline__ bool clean16(uint32_t at) {
 template <bool SPLIT, int NCH, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_rows_tc_kernel(const __grid_constant__ PagedRowsParams p, const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v, int box) {
+                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q,
+                         const __grid_constant__ CUtensorMap map_ql, int box) {
     using S = Shape<SPLIT, NCH, NARROW>;
     extern __shared__ __align__(1024) unsigned char smem[];  // atoms of the swizzle: no other shared memory before it
     Control& ctl = *reinterpret_cast<Control*>(smem + S::kControlAt);
@@ -262,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.empty[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&ctl.q_ready[t], NARROW ? 8 : 4);
+            mbar_init(&ctl.q_ready[t], 1);
+            mbar_init(&ctl.q_free[t], 4);
             mbar_init(&ctl.s_full[t], 1);
             mbar_init(&ctl.p_half[t], 4);
             mbar_init(&ctl.p_ready[t], 4);
@@ -283,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w;
     Piece x;
     const bool work = w.begin(p);
+    if (work && tid == 0) note_none(p);
     if (work) {
         if (warp < kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -297,88 +333,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && w.next(p, x)) {
             const RowTile& tile = x.t;
             const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
-            const int rows = tile.ntok * heads, row0 = (NARROW ? 0 : t * kHalf) + 32 * quarter, r = row0 + lane;
             const int first_block = block0;
             block0 += x.to - x.from;
             ++piece;
-            if (tid == 0) note_piece(p, w, x, w.u >= w.end);
-            if (!NARROW && t == 1 && rows <= kHalf) continue;  // nothing for this stream
-            // q of the warp's rows (NARROW: every other one, the rest is the other stream's warp's), a row at a time
-            float unscale = 1.f;
-            constexpr int kStep = NARROW ? 2 : 1, kAhead = 8;
-#pragma unroll 1
-            for (int i0 = NARROW ? t : 0; i0 < 32; i0 += kAhead * kStep) {
-                float v[kAhead][4];
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int row = row0 + i0 + j * kStep, tok = row / heads;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[j][k] = 0.f;
-                    if (row < rows && 4 * lane < p.hd) {
-                        const float* src = p.q + (tile.row0 + tok) * p.q_stride +
-                                           static_cast<int64_t>(kv * G + g0 + row - tok * heads) * p.hd + 4 * lane;
-                        if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-                            const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                            v[j][0] = f.x, v[j][1] = f.y, v[j][2] = f.z, v[j][3] = f.w;
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v[j][k] = __ldcg(src + k);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int i = i0 + j * kStep;
-                    float big = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        v[j][k] *= p.scale * kLog2e;
-                        big = fmaxf(big, fabsf(v[j][k]));
-                    }
-                    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));  // not below zero
-                    // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
-                    int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
-                    e = e == 128 ? 13 : max(-113, min(e, 126));
-                    const float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-                    const float un = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-                    if (NARROW) {
-                        if (lane == 0) ctl.unscale[row0 + i] = un;
-                    } else if (lane == i) {
-                        unscale = un;
-                    }
-                    if (4 * lane < 64 * NCH) {
-                        uint32_t hi[2], lo[2];
-                        split2(v[j][0] * sc, v[j][1] * sc, hi[0], lo[0]);
-                        split2(v[j][2] * sc, v[j][3] * sc, hi[1], lo[1]);
-                        const int c = lane >> 4, in = (lane & 15) >> 1;  // chunk, and 16 bytes of its row
-                        const uint32_t at = swz(32 * quarter + i, in) + 8 * (lane & 1);
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, 0, c) + at), "r"(hi[0]), "r"(hi[1])
-                                     : "memory");
-                        if (SPLIT)
-                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_chunk(t, kParts - 1, c) + at), "r"(lo[0]),
-                                         "r"(lo[1])
-                                         : "memory");
-                    }
-                }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.q_ready[NARROW ? 0 : t]);
-
-            const bool busy = row0 < rows, mine = r < rows;
+            if (tid == 0) note_piece(p, w, x);
+            const int token0 = NARROW ? 0 : t * p.part_tokens;  // the stream's first
+            if (token0 >= tile.ntok) continue;                  // nothing for this stream
+            const int r = 32 * quarter + lane, in_part = r / p.per_block, g = r - in_part * p.per_block;
+            const int i = token0 + in_part, row = tile.row0 + i, h = kv * G + g0 + g;
+            const bool mine = in_part < p.part_tokens && i < tile.ntok && g < heads;
+            const bool busy = 32 * quarter < min(p.part_tokens, tile.ntok - token0) * p.per_block;
+            const float unscale = mine ? __ldcg(p.q_unscale + static_cast<int64_t>(row) * p.nh + h) : 1.f;
             const bool both = NARROW ? x.to - x.from > 1 : true;  // NARROW: the second stream has blocks
             int see_lo = 0, see_hi = 0;
-            if (mine) row_span(p, tile, r / heads, see_lo, see_hi);
+            if (mine) row_span(p, tile, i, see_lo, see_hi);
             float m = -CUDART_INF_F, l = 0.f;
             for (int u = x.from + (NARROW ? t : 0); u < x.to; u += NARROW ? 2 : 1) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.s_full[t], s_phase));
+                ok = __all_sync(0xffffffffu, wait_for(&ctl.s_full[t], s_phase));
                 s_phase ^= 1;
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
                     const bool begun = u >= x.from + (NARROW ? 2 : 1);  // O holds sums
-                    if (NARROW && !begun) unscale = ctl.unscale[r];
                     const int j0 = tile.lo + u * kBlock;
                     const uint32_t* live = ctl.live[(first_block + u - x.from) % kLiveRing];
                     const bool mixed = j0 < tile.all_lo || j0 + kBlock > tile.all_hi ||
@@ -416,13 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (!SPLIT || round == 1) break;
                         const float2 bad = unpack2(odd);
-                        if (!__any_sync(0xffffffffu, !(bad.x + bad.y == 0.f))) break;
-                        const float* q_row = p.q + static_cast<int64_t>(tile.row0 + r / heads) * p.q_stride +
-                                             static_cast<int64_t>(kv * G + g0 + r % heads) * p.hd;
+                        if (!__any_sync(0xffffffffu, mine && !(bad.x + bad.y == 0.f))) break;
+                        const float* q_row = p.q + row * p.q_stride + static_cast<int64_t>(h) * p.hd;
                         for (int k = 0; k < kBlock; ++k) {
                             float f = __uint_as_float(tm_ld1(s_at + k));
                             if (mine && !(fabsf(f) < CUDART_INF_F) && ((seen(k >> 5) >> (k & 31)) & 1u))
-                                f = plain_score(p, q_row, tile.seq, j0 + k, kv) * (1.f / unscale);
+                                f = plain_score(p, q_row, tile.seq, j0 + k, kv) / unscale;
                             __syncwarp();
                             tm_st1(s_at + k, __float_as_uint(f));
                         }
@@ -433,8 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 32; k += 2)
 #pragma unroll
                         for (int c = 0; c < kBlock / 32; ++c)
-                            tops[c] = fmaxf(fmaxf(tops[c], __uint_as_float(v[c][k])), __uint_as_float(v[c][k + 1]));
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * unscale;
+                            tops[c] = max3(tops[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
+                    // rows that are none (what is in q's place there varies) have no say in the warp's votes
+                    const float top =
+                        mine ? fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * unscale : -CUDART_INF_F;
                     if (__any_sync(0xffffffffu, top > m + S::kLazy)) {
                         const float next = fmaxf(m, top), keep = m == next ? 1.f : ex2(m - next);
                         m = next;
@@ -493,114 +470,159 @@ __global__ void __launch_bounds__(kThreads, 1)
             // NARROW: both streams read the one q, so both wait for both
             for (int k = 0; k < 2; ++k) {
                 if (NARROW ? k == 1 && !both : k != t) continue;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.o_full[k], (o_phase >> k) & 1));
+                ok = ok && __all_sync(0xffffffffu, wait_for(&ctl.o_full[k], (o_phase >> k) & 1));
                 o_phase ^= 1u << k;
             }
             if (NARROW && t == 0 && both) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.joined, join_phase));
+                ok = ok && __all_sync(0xffffffffu, wait_for(&ctl.joined, join_phase));
                 join_phase ^= 1;
             }
             if (!ok) break;
             tc_fence_after();
-            if (!busy || (NARROW && t == 1)) continue;
-            float k0 = 1.f, k1 = 0.f;
-            if (NARROW && both) {
-                const float2 other = ctl.ml[r];
-                const float top = fmaxf(m, other.x);
-                k0 = m == top ? 1.f : ex2(m - top);
-                k1 = other.x == top ? 1.f : ex2(other.x - top);
-                m = top;
-                l = l * k0 + other.y * k1;
-            }
-            const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
-            const int i = r / heads, row = tile.row0 + i, h = kv * G + g0 + r - i * heads;
-            const bool whole = x.whole(), empty = see_lo >= see_hi;
-            const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;
-            float* part = part_of(p, blockIdx.x, x.first);
-            const int64_t out_at = row * p.out_stride + static_cast<int64_t>(h) * p.hd;
-            float* to = nullptr;  // bf16
-            if (!whole) to = part_o(p, part, r);
-            else if (!p.first) to = p.prefix_out + (static_cast<int64_t>(row) * p.nh + h) * p.hd;
-            else if (!p.out_bf16) to = static_cast<float*>(p.out) + out_at;
+            if (NARROW && t == 1) continue;
+            if (busy) {
+                float k0 = 1.f, k1 = 0.f;
+                if (NARROW && both) {
+                    const float2 other = ctl.ml[r];
+                    const float top = fmaxf(m, other.x);
+                    k0 = m == top ? 1.f : ex2(m - top);
+                    k1 = other.x == top ? 1.f : ex2(other.x - top);
+                    m = top;
+                    l = l * k0 + other.y * k1;
+                }
+                const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
+                const bool whole = x.whole(), empty = see_lo >= see_hi;
+                if (whole) k0 *= empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
+                if (NARROW && both && whole) k1 *= empty ? 0.f : 1.f / l;
+                float* part = part_of(p, blockIdx.x, x.first);
+                // Results go to memory through q's place, by whole rows of a warp: 16 bytes a lane of neighbouring lanes
+                // instead of a row a lane, which took 7000 cycles of a tile.
+                const bool bf16 = whole && p.first && p.out_bf16;
+                char* to;
+                if (!whole) to = reinterpret_cast<char*>(part_o(p, part, t * kHalf + r));
+                else if (!p.first) to = reinterpret_cast<char*>(p.prefix_out + (static_cast<int64_t>(row) * p.nh + h) * p.hd);
+                else to = static_cast<char*>(p.out) + (row * p.out_stride + static_cast<int64_t>(h) * p.hd) * (bf16 ? 2 : 4);
+                constexpr int kRowBytes = 128 * NCH;  // of a row and round
+                const uint32_t mine_at = q_chunk(t, 0, 0) + (32 * quarter) * kRowBytes;
+                const int bytes = p.hd * (bf16 ? 2 : 4), columns = kRowBytes / (bf16 ? 2 : 4);
 #pragma unroll 1
-            for (int c = 0; c < p.hd; c += 16) {
-                uint32_t v[16], y[16];
-                float o[16];
-                tm_ld16(o_at + c, v);
-                if (NARROW && both) tm_ld16(o_at + 128 + c, y);
-                tc_wait_ld();
+                for (int c0 = 0; c0 < p.hd; c0 += columns) {
+#pragma unroll 1
+                    for (int c = c0; c < min(p.hd, c0 + columns); c += 16) {
+                        uint32_t v[16], y[16];
+                        tm_ld16(o_at + c, v);
+                        if (NARROW && both) tm_ld16(o_at + 128 + c, y);
+                        tc_wait_ld();
+                        float o[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    o[k] = __uint_as_float(v[k]);
-                    if (NARROW && both) o[k] = fmaf(o[k], k0, __uint_as_float(y[k]) * k1);
-                }
-                if (poison && mine) {
-                    float more[16] = {};
-                    add_non_finite(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock),
-                                   min(see_hi, tile.lo + x.to * kBlock), c, more);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] += more[k];
-                }
-                if (mine) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = whole && empty ? 0.f : o[k] * inv;
-                    if (to) {
-                        if ((reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
-#pragma unroll
-                            for (int k = 0; k < 16; k += 4)
-                                *reinterpret_cast<float4*>(to + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) to[c + k] = o[k];
+                        for (int k = 0; k < 16; ++k) {
+                            o[k] = __uint_as_float(v[k]) * k0;
+                            if (NARROW && both) o[k] = fmaf(__uint_as_float(y[k]), k1, o[k]);
+                            if (whole && empty) o[k] = 0.f;
                         }
-                    } else {
-                        uint16_t* b = static_cast<uint16_t*>(p.out) + out_at + c;
-                        if ((reinterpret_cast<uintptr_t>(b) & 15u) == 0) {
-                            uint32_t d[8];
+                        if (poison && mine) {
+                            float more[16] = {};
+                            add_non_finite(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock),
+                                           min(see_hi, tile.lo + x.to * kBlock), c, more);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] += more[k];
+                        }
+                        uint32_t d[16];
+                        if (bf16) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d[k]) : "f"(o[2 * k + 1]), "f"(o[2 * k]));
-                            *reinterpret_cast<uint4*>(b) = make_uint4(d[0], d[1], d[2], d[3]);
-                            *reinterpret_cast<uint4*>(b + 8) = make_uint4(d[4], d[5], d[6], d[7]);
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) b[k] = bf16_bits(o[k]);
+                            for (int k = 0; k < 16; ++k) d[k] = __float_as_uint(o[k]);
+                        }
+                        const int first = (c - c0) * (bf16 ? 2 : 4) / 16;  // 16-byte piece of the row
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (!bf16 || k < 2)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                                 mine_at + lane * kRowBytes + (((first + k) ^ (lane & 7)) << 4)),
+                                             "r"(d[4 * k]), "r"(d[4 * k + 1]), "r"(d[4 * k + 2]), "r"(d[4 * k + 3])
+                                             : "memory");
+                    }
+                    __syncwarp();
+                    constexpr int kPieces = kRowBytes / 16, kRowsAtOnce = 32 / kPieces;
+                    const int piece16 = lane % kPieces, skip = c0 * (bf16 ? 2 : 4);
+#pragma unroll 2
+                    for (int k = 0; k < 32; k += kRowsAtOnce) {
+                        const int from = k + lane / kPieces;
+                        char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(to), from)) + skip + 16 * piece16;
+                        const bool there = __shfl_sync(0xffffffffu, mine, from);
+                        if (!there || skip + 16 * piece16 >= bytes) continue;
+                        uint4 v;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(mine_at + from * kRowBytes + ((piece16 ^ (from & 7)) << 4))
+                                     : "memory");
+                        if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+                            *reinterpret_cast<uint4*>(dst) = v;
+                        } else {
+                            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if (bf16) {
+                                    reinterpret_cast<uint16_t*>(dst)[2 * j] = static_cast<uint16_t>(e[j]);
+                                    reinterpret_cast<uint16_t*>(dst)[2 * j + 1] = static_cast<uint16_t>(e[j] >> 16);
+                                } else {
+                                    reinterpret_cast<uint32_t*>(dst)[j] = e[j];
+                                }
+                            }
                         }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
-            if (mine) {
-                float* lse = p.first ? p.lse : p.prefix_lse;
-                if (!whole) *part_ml(part, r) = make_float2(m - S::kShift, l);
-                else if (lse) lse[static_cast<int64_t>(row) * p.nh + h] = lse_of(m - S::kShift, l, empty);
+                if (mine) {
+                    float* lse = p.first ? p.lse : p.prefix_lse;
+                    if (!whole) *part_ml(part, t * kHalf + r) = make_float2(m - S::kShift, l);
+                    else if (lse) lse[static_cast<int64_t>(row) * p.nh + h] = lse_of(m - S::kShift, l, empty);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_fence_before();
             }
             __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.q_free[t]);
         }
         if (!ok && lane == 0) flag_bad(kFlagTimeout, 0);
     } else if (work && warp == kMmaWarp) {
-        // ---- MMAs, issued by one lane (the walk is made by all of them)
+        // ---- MMAs
         const int steps = p.hd / 16;
         const uint32_t id_s = idesc(kBlock, false), id_o = idesc(p.hd, true);
-        uint32_t item = 0, q_phase = 0, h_phase = 0, p_phase = 0;  // item: the piece's first chunk; phases: bit t
+        // The next block's K and V: stages of their first chunks, and the phases that they wait for.
+        uint32_t k_at = 0, k_phase = 0, v_at = NCH, v_phase = 0;
+        uint32_t q_phase = 0, h_phase = 0, p_phase = 0;  // bit t
         bool ok = true;
-        auto wait_full = [&](uint32_t first) {  // a block's chunks of K or V
-#pragma unroll
-            for (int c = 0; c < NCH; ++c)
-                if (ok) ok = mbar_wait_bounded(&ctl.full[(first + c) % S::kStages], ((first + c) / S::kStages) & 1);
+        auto wait = [&](uint64_t* bar, uint32_t phase) {
+            if (ok) ok = __all_sync(0xffffffffu, wait_for(bar, phase));
             tc_fence_after();
         };
-        auto release = [&](uint32_t first) {
+        auto wait_full = [&](uint32_t at, uint32_t phase) {  // a block's chunks of K or V
 #pragma unroll
-            for (int c = 0; c < NCH; ++c) tc_commit(&ctl.empty[(first + c) % S::kStages]);
+            for (int c = 0; c < NCH; ++c) wait(&ctl.full[at + c], phase);
         };
-        auto scores = [&](int t, uint32_t first) {
+        auto release = [&](uint32_t at) {
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) tc_commit(&ctl.empty[at + c]);
+        };
+        auto next_block = [&](uint32_t& at, uint32_t& phase) {
+            at += 2 * NCH;
+            if (at >= S::kStages) {
+                at -= S::kStages;
+                phase ^= 1u;
+            }
+        };
+        const uint32_t ring = desc_k(ring_at), ring_v = desc_mn(ring_at);
+        auto scores = [&](int t) {  // of stream t and the next block
             uint32_t acc = 0;
 #pragma unroll
             for (int part = kParts - 1; part >= 0; --part)  // the small products first
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
-                    const uint64_t a = desc_k(q_chunk(t, part, c)), b = desc_k(chunk_at(first + c));
+                    const uint32_t a = desc_k(q_chunk(t, part, c)), b = ring + (k_at + c) * (kChunkBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // 16 columns are 32 bytes
                         if (4 * c + k < steps) {
@@ -611,96 +633,124 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(&ctl.s_full[t]);
         };
         // O of stream t: the first half of the slots as soon as their weights are there
-        auto sums = [&](int t, uint32_t first, uint32_t acc) {
-            const uint64_t v = desc_mn(chunk_at(first));
+        auto sums = [&](int t, uint32_t acc) {
+            const uint32_t v = ring_v + v_at * (kChunkBytes >> 4), o = tmem + 256 + 128 * t, w0 = tmem + 128 * t;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                if (!ok) break;
                 if (half == 0) {
-                    ok = mbar_wait_bounded(&ctl.p_half[t], (h_phase >> t) & 1);
+                    wait(&ctl.p_half[t], (h_phase >> t) & 1);
                     h_phase ^= 1u << t;
                 } else {
-                    ok = mbar_wait_bounded(&ctl.p_ready[t], (p_phase >> t) & 1);
+                    wait(&ctl.p_ready[t], (p_phase >> t) & 1);
                     p_phase ^= 1u << t;
                 }
-                if (!ok) break;
-                tc_fence_after();
+                if (!ok) return;
 #pragma unroll
                 for (int k = half * kBlock / 32; k < (half + 1) * kBlock / 32; ++k)  // 16 slots are 2048 bytes
 #pragma unroll
                     for (int part = kParts - 1; part >= 0; --part) {
-                        mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 32 * (k >> 1) + 16 * part + 8 * (k & 1), v + 128 * k, id_o,
-                               acc);
+                        mma_ts(o, w0 + 32 * (k >> 1) + 16 * part + 8 * (k & 1), v + 128 * k, id_o, acc);
                         acc = 1;
                     }
             }
         };
-        while (__all_sync(0xffffffffu, ok) && w.next(p, x)) {
-            const int kv = x.head / p.blocks, heads = min(p.per_block, G - (x.head - kv * p.blocks) * p.per_block);
+        while (ok && w.next(p, x)) {
             const int n = x.to - x.from;
-            if (lane == 0 && NARROW) {
-                auto k_of = [&](int b) { return item + 2 * b * NCH; };
-                ok = mbar_wait_bounded(&ctl.q_ready[0], q_phase & 1);
+            if (NARROW) {
+                wait(&ctl.q_ready[0], q_phase);
                 q_phase ^= 1u;
-                for (int b = 0; ok && b < n && b < 2; ++b) {
-                    wait_full(k_of(b));
-                    if (ok) {
-                        scores(b, k_of(b));
-                        release(k_of(b));
-                    }
-                }
-                for (int b = 0; ok && b < n; ++b) {
-                    const int t = b & 1;
-                    wait_full(k_of(b) + NCH);
-                    sums(t, k_of(b) + NCH, b >= 2);
+                for (int b = 0; b < min(n, 2) && ok; ++b) {
+                    wait_full(k_at, k_phase);
                     if (!ok) break;
-                    release(k_of(b) + NCH);
+                    scores(b);
+                    release(k_at);
+                    next_block(k_at, k_phase);
+                }
+                for (int b = 0; b < n && ok; ++b) {
+                    const int t = b & 1;
+                    wait_full(v_at, v_phase);
+                    if (ok) sums(t, b >= 2);
+                    if (!ok) break;
+                    release(v_at);
+                    next_block(v_at, v_phase);
                     if (b + 2 >= n) {
                         tc_commit(&ctl.o_full[t]);
-                    } else {
-                        wait_full(k_of(b + 2));
-                        if (ok) {
-                            scores(t, k_of(b + 2));
-                            release(k_of(b + 2));
-                        }
+                        continue;
                     }
+                    wait_full(k_at, k_phase);
+                    if (!ok) break;
+                    scores(t);
+                    release(k_at);
+                    next_block(k_at, k_phase);
                 }
-            } else if (lane == 0) {
-                const int halves = x.t.ntok * heads > kHalf ? 2 : 1;
-                for (int t = 0; ok && t < halves; ++t) {
-                    ok = mbar_wait_bounded(&ctl.q_ready[t], (q_phase >> t) & 1);
+            } else {
+                const int halves = x.t.ntok > p.part_tokens ? 2 : 1;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= halves || !ok) break;
+                    wait(&ctl.q_ready[t], (q_phase >> t) & 1);
                     q_phase ^= 1u << t;
-                    if (t == 0) wait_full(item);
-                    if (ok) scores(t, item);
+                    if (t == 0) wait_full(k_at, k_phase);
+                    if (ok) scores(t);
                 }
-                if (ok) release(item);
-                for (int b = 0; ok && b < n; ++b) {
-                    const uint32_t v = item + (2 * b + 1) * NCH, next = v + NCH;
+                if (!ok) break;
+                release(k_at);
+                next_block(k_at, k_phase);
+                for (int b = 0; b < n && ok; ++b) {
                     const bool last = b + 1 == n;
-                    wait_full(v);
-                    for (int t = 0; ok && t < halves; ++t) {
-                        sums(t, v, b > 0);
+                    wait_full(v_at, v_phase);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= halves) break;
+                        if (ok) sums(t, b > 0);
                         if (!ok) break;
-                        if (t + 1 == halves) release(v);
+                        if (t + 1 == halves) release(v_at);
                         if (last) {
                             tc_commit(&ctl.o_full[t]);
                         } else {
-                            if (t == 0) wait_full(next);
-                            if (ok) scores(t, next);
+                            if (t == 0) wait_full(k_at, k_phase);
+                            if (ok) scores(t);
                         }
                     }
-                    if (ok && !last) release(next);
+                    if (!ok) break;
+                    next_block(v_at, v_phase);
+                    if (!last) {
+                        release(k_at);
+                        next_block(k_at, k_phase);
+                    }
                 }
             }
-            item += 2 * n * NCH;
-            __syncwarp();
         }
-        if (lane == 0 && !ok) {  // what was issued ends before tensor memory is freed
+        if (!ok) {  // what was issued ends before tensor memory is freed
             tc_commit(&ctl.drained);
-            mbar_wait_bounded(&ctl.drained, 0);
-            flag_bad(kFlagTimeout, 0);
+            wait_for(&ctl.drained, 0);
+            if (lane == 0) flag_bad(kFlagTimeout, 0);
         }
         __syncwarp();
+    } else if (work && warp == kMmaWarp + 1) {
+        // ---- q of the next piece, as soon as the last one's results have left its place
+        uint32_t phase = 3;  // bit t: nothing to wait for at first
+        bool ok = true;
+        const uint32_t bytes = kParts * NCH * 128 * p.per_block * p.part_tokens;
+        while (ok && w.next(p, x)) {
+            const int kv = x.head / p.blocks, h0 = kv * G + (x.head - kv * p.blocks) * p.per_block;
+            for (int t = 0; t < (NARROW ? 1 : 2); ++t) {
+                const int token = t * p.part_tokens;
+                if (!ok || token >= x.t.ntok) break;
+                ok = __all_sync(0xffffffffu, wait_for(&ctl.q_free[t], (phase >> t) & 1));
+                phase ^= 1u << t;
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&ctl.q_ready[t], bytes);
+                    for (int c = 0; c < NCH; ++c) {
+                        tma_box(q_chunk(t, 0, c), &map_q, 64 * c, h0, x.t.row0 + token, &ctl.q_ready[t]);
+                        if (SPLIT) tma_box(q_chunk(t, kParts - 1, c), &map_ql, 64 * c, h0, x.t.row0 + token, &ctl.q_ready[t]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) flag_bad(kFlagTimeout, 0);
     } else if (work && warp >= kLoadWarp && box) {
         // ---- copies by TMA: boxes of `box` rows of a page, lane b of warp 12 the b-th of a block
         uint32_t item = 0;
@@ -730,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kc = 0; kc < 2 * NCH; ++kc) {  // K's chunks, then V's
                         const uint32_t n = item;
                         if (ok && n >= S::kStages)
-                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
+                            ok = __all_sync(0xffffffffu, wait_for(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
                         if (!ok) break;
                         ++item;
                         if (kc == 0) {
@@ -751,27 +801,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) {  // no copy is in flight when the CTA ends
                 for (uint32_t n = item > S::kStages ? item - S::kStages : 0; n < item; ++n)
-                    mbar_wait_bounded(&ctl.landed[n % S::kStages], (n / S::kStages) & 1);
+                    wait_for(&ctl.landed[n % S::kStages], (n / S::kStages) & 1);
                 if (lane == 0) flag_bad(kFlagTimeout, 0);
             }
         } else {
             const int chunks16 = p.hd / 8, me = (warp - kLoadWarp - 1) * 32 + lane;
             while (ok && w.next(p, x)) {
                 ++piece;
-                for (int u = x.from; ok && u < x.to; ++u) {
+                for (int u = x.from; ok && u < x.to; ++u, ++block) {
                     const int j0 = x.t.lo + u * kBlock;
                     const bool check = SPLIT || j0 < x.t.all_lo || j0 + kBlock > x.t.all_hi;
 #pragma unroll 1
                     for (int kc = 0; kc < 2 * NCH; ++kc) {
                         const uint32_t n = item++;
-                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.landed[n % S::kStages], (n / S::kStages) & 1));
+                        ok = __all_sync(0xffffffffu, wait_for(&ctl.landed[n % S::kStages], (n / S::kStages) & 1));
                         if (!ok) break;
-                        if (kc >= NCH && check) {
+                        const uint32_t* live = ctl.live[block % kLiveRing];
+                        if (kc >= NCH && (check || (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu)) {
                             const int width = min(8, chunks16 - 8 * (kc - NCH));  // 16-byte pieces of a row here
                             bool bad = false;
 #pragma unroll 4
-                            for (int e = me; e < 8 * kBlock; e += 32 * (kLoadWarps - 1))
-                                if ((e & 7) < width) bad |= clean16(chunk_at(n) + swz(e >> 3, e & 7));
+                            for (int e = me; e < 8 * kBlock; e += 32 * (kLoadWarps - 1)) {
+                                if ((e & 7) >= width) continue;
+                                const uint32_t to = chunk_at(n) + swz(e >> 3, e & 7);
+                                // slots that are not there: whatever the page, or the ring before, holds
+                                if ((live[e >> 8] >> ((e >> 3) & 31)) & 1u) bad |= clean16(to);
+                                else asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+                            }
                             if (bad) ctl.poison[piece % kPoisonRing] = piece;
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         }
@@ -836,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __half* pool = static_cast<const __half*>(is_v ? p.c.v : p.c.k);
                     const uint32_t n = item;
                     if (ok && n >= S::kStages)
-                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
+                        ok = __all_sync(0xffffffffu, wait_for(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
                     if (!ok) break;
                     ++item;
                     if (kc == 0 && lane == 0) ctl.live[block % kLiveRing][i] = there;
@@ -884,15 +940,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// A pool as columns x rows of a page x pages, read in boxes of 64 columns and `box` rows.
-bool encode(CUtensorMap* map, const PagedRowsParams& p, void* pool, int box) {
+// Three dimensions of f16 values, read in boxes of 64 values of the first.
+bool encode(CUtensorMap* map, const void* base, int64_t n0, int64_t n1, int64_t n2, int64_t stride1, int64_t stride2, int box1,
+            int box2) {
     if (!encoder()) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.c.nkt), static_cast<cuuint64_t>(p.c.page_size),
-                                static_cast<cuuint64_t>(p.c.n_pages)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.c.nkt) * 2, static_cast<cuuint64_t>(p.c.page_stride) * 2};
-    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 1}, steps[3] = {1, 1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, pool, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n0), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride1) * 2, static_cast<cuuint64_t>(stride2) * 2};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2)}, steps[3] = {1, 1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, steps,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -911,11 +967,17 @@ cudaError_t launch_t(const PagedRowsParams& p, cudaStream_t stream) {
     // Boxes of as many rows, a power of two, as divide a page and a block; eight rows are an atom of the swizzle.
     int box = 1;
     while (box < kBlock && p.c.page_size % (2 * box) == 0) box *= 2;
-    CUtensorMap k, v;
-    std::memset(&k, 0, sizeof k);
-    std::memset(&v, 0, sizeof v);
-    if (box < 8 || p.c.nkt < 64 || !encode(&k, p, p.c.k, box) || !encode(&v, p, p.c.v, box)) box = 0;
-    return launch_dependent(kernel, dim3(kSms), kThreads, smem, stream, 1, p, k, v, box);
+    CUtensorMap maps[4];  // pools as columns x rows of a page x pages, q as columns x heads x tokens
+    std::memset(maps, 0, sizeof maps);
+    for (int i = 0; i < 2 && box; ++i)
+        if (box < 8 || p.c.nkt < 64 ||
+            !encode(&maps[i], i ? p.c.v : p.c.k, p.c.nkt, p.c.page_size, p.c.n_pages, p.c.nkt, p.c.page_stride, box, 1))
+            box = 0;
+    const int64_t nqt = static_cast<int64_t>(p.nh) * p.hd;
+    for (int i = 0; i < (SPLIT ? 2 : 1); ++i)
+        if (!encode(&maps[2 + i], i ? p.q_low : p.q_high, p.hd, p.nh, p.nt, p.hd, nqt, p.per_block, p.part_tokens))
+            return cudaErrorInvalidValue;
+    return launch_dependent(kernel, dim3(kSms), kThreads, smem, stream, 1, p, maps[0], maps[1], maps[2], maps[3], box);
 }
 
 template <bool SPLIT, int NCH>
@@ -925,7 +987,7 @@ cudaError_t launch_n(const PagedRowsParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-RowsShape paged_rows_tc_shape(bool narrow) { return {narrow ? kHalf : 2 * kHalf, kBlock, kSms}; }
+RowsShape paged_rows_tc_shape(bool narrow) { return {narrow ? kHalf : 2 * kHalf, kHalf, kBlock, kSms, kTileCost, true}; }
 
 cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream) {
     if (p.out_bf16) return p.hd <= 64 ? launch_n<false, 1>(p, stream) : launch_n<false, 2>(p, stream);

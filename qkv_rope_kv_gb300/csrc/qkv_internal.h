@@ -177,10 +177,11 @@ void paged_attn_grid(const PagedAttnParams& p, int* ctas, int* cluster);
 cudaError_t paged_attn_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad);
 
 // Attention of many q rows over the same slots (paged_rows*.cu).  The rows (tokens x q heads of a kv head) go in tiles; the
-// slots that any of a tile's rows sees, in blocks, are its units.  A kernel's CTAs get equal shares of all tiles' units in
-// a row, kv head by kv head, so a tile's blocks can be spread over several CTAs: their parts are joined afterwards.
+// slots that any of a tile's rows sees, in blocks, are its units.  A kernel's CTAs get equal shares of all tiles in
+// a row, kv head by kv head, each tile as long as its units and a constant for its beginning and end; so a tile's blocks can
+// be spread over several CTAs, and their parts are joined afterwards.
 struct alignas(16) RowTile {
-    int64_t unit0;  // units of one kv head before this tile's
+    int64_t start;  // where it begins, within its kv head
     int32_t units;
     int32_t seq;    // whose row of the page table
     int32_t row0, ntok;  // q rows
@@ -188,8 +189,8 @@ struct alignas(16) RowTile {
     int32_t base;        // row i sees [max(0, base + i - window), base + i); prefix: [0, row_end[row0 + i])
     int32_t all_lo, all_hi;  // slots that every row sees
 };
-struct RowPiece {  // for each CTA, its last tile where that goes on in other CTAs and began in this one
-    int64_t start;  // the tile's first unit, over all heads
+struct RowPiece {  // for each CTA, the tile that begins in it and goes on in others
+    int64_t start;  // of the tile, over all heads
     int32_t tile, head;
     int32_t parts;  // 0: none
     int32_t pad;
@@ -214,12 +215,17 @@ struct PagedRowsParams {
     // the plan, made on the device
     int32_t rows, block;        // of a tile, of a unit
     int32_t per_block, blocks;  // q heads of a kv head in a tile, and how many such blocks it has
-    int32_t max_tiles;
-    int64_t* total;             // [0] units of one block of q heads, [1] tiles
+    int32_t part_rows, part_tokens;  // a tile's rows come in one or two parts, of whole tokens each (see row_of)
+    int32_t tile_tokens, tile_cost, max_tiles;
+    int64_t* total;             // [0] how long the tiles of one block of q heads are, [1] tiles
     RowTile* tiles;
     int32_t* starts;            // prefix: [n_seq] each: where the rows' own slots begin, ...
     int32_t* row_end;           // ... how many of the prefix are seen, ...
     int32_t* row_tile;          // ... and in which tile
+    // tensor cores: q in f16 as [nt][nqt] rounded values times a power of two, the remainders, and what gives scores back
+    uint16_t* q_high;
+    uint16_t* q_low;            // (out F32)
+    float* q_unscale;           // [nt][nh]
     RowPiece* pieces;           // [kRowsMaxCtas]
     float* part;                // [2 * kRowsMaxCtas][rows][hd + 2]
     float* prefix_out;          // prefix: [n_seq][nqt] and [n_seq][nh]: of whole tiles
@@ -232,7 +238,8 @@ cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream);
 cudaError_t launch_paged_rows_join(const PagedRowsParams& p, cudaStream_t stream);
 // Rows of a tile, slots of a block and CTAs of the kernel that these sizes and addresses get.
 struct RowsShape {
-    int32_t rows, block, ctas;
+    int32_t rows, part_rows, block, ctas, tile_cost;
+    bool tensor;  // the kernel on the tensor cores
 };
 RowsShape paged_rows_shape(const PagedRowsParams& p);
 RowsShape paged_rows_tc_shape(bool narrow);

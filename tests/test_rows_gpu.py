@@ -47,7 +47,7 @@ def check(c, x, places, nh, scale, out, o, lse, nqt):
 
 
 def run_prompt(nh, nkv, hd, kv, page, new, cached, window=0, out="f32", seed=0, q_scale=1.5, change=None, stride=0,
-               pool_off=0, page_gap=0, behind=0, ahead=0, lens=None, plan=None, workspace=None, twice=True):
+               pool_off=0, page_gap=0, behind=0, ahead=0, lens=None, plan=None, workspace=None, twice=True, scale=None):
     import torch
     rng = np.random.default_rng(seed)
     B = len(new)
@@ -64,7 +64,7 @@ def run_prompt(nh, nkv, hd, kv, page, new, cached, window=0, out="f32", seed=0, 
     lse = torch.full((nt, nh), 55.0, device="cuda")
     if workspace is None:
         workspace = torch.full((Q.qkv_prompt_attn_workspace_bytes(plan, cache, nt),), 0xa5, dtype=torch.uint8, device="cuda")
-    scale = hd ** -0.5
+    scale = hd ** -0.5 if scale is None else scale
     args = (plan, cache, q, dev(first), dev(lens), scale, o[:, :nh * hd], workspace)
     Q.qkv_prompt_attn_step(*args, window=window, lse=lse)
     torch.cuda.synchronize()
@@ -113,6 +113,11 @@ def run_prompt(nh, nkv, hd, kv, page, new, cached, window=0, out="f32", seed=0, 
     (28, 4, 128, "f16", 16, [40, 9], [5, 300], dict(pool_off=1)),
     (28, 4, 128, "f16", 16, [40, 9], [5, 300], dict(page_gap=1)),
     (28, 4, 128, "f16", 16, [40, 9], [5, 300], dict(q_scale=12.0)),
+    (28, 4, 128, "f16", 16, [40, 9], [5, 300], dict(scale=-0.11, out="bf16")),
+    (28, 4, 128, "f16", 16, [40, 9], [5, 300], dict(scale=0.0)),
+    (4, 4, 16, "f16", 16, [40, 9], [5, 300], {}),                # heads narrower than a chunk, rows narrower than a box
+    (3, 1, 32, "f16", 24, [200, 9], [5, 300], dict(out="bf16")),
+    (6, 2, 48, "f16", 8, [70, 9], [5, 300], {}),
     (2, 1, 128, "f16", 64, [1500], [0], dict(out="bf16")),
     (2, 1, 128, "f16", 64, [2], [9000], {}),                     # one tile over many CTAs
     (2, 1, 64, "f32", 64, [2], [9000], {}),
