@@ -229,8 +229,9 @@ __device__ __noinline__ float plain_score(const PagedRowsParams& p, const float*
     return s;
 }
 
-// What the infinities and NaN of V that a row sees, in slots [lo, hi), add to 16 columns of its sum: the copies put
-// zeros in their place, since a weight of zero (a slot that the row does not see) times them is NaN.
+// What the infinities and NaN of V that a row sees, in slots [lo, hi), add to 16 columns of its sum.  The products do not
+// tell: a weight of zero (of a slot that the row does not see; or rounded, or a remainder) times them is NaN.  So blocks
+// with slots that only some rows see get zeros in their place, and rows that come out infinite or NaN look here.
 __device__ __noinline__ void add_non_finite(const PagedRowsParams& p, int seq, int kv, int lo, int hi, int c, float* o) {
     for (int s = lo; s < hi; ++s) {
         const int64_t row = row_offset(p.c, seq, s);
@@ -253,17 +254,20 @@ struct Control {
 };
 static_assert(sizeof(Control) <= kControlBytes, "control");
 
-// Replace infinities and NaN among 16 bytes of V by zeros.
-__device__ __forceinline__ bool clean16(uint32_t at) {
-    uint32_t v[4];
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
-    if (finite_f16x2(v[0]) && finite_f16x2(v[1]) && finite_f16x2(v[2]) && finite_f16x2(v[3])) return false;
+// 16 bytes of V, zeros in the place of infinities and NaN.
+__device__ __forceinline__ void keep_finite(uint32_t at, uint32_t (&v)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if ((v[j] & 0x7c00u) == 0x7c00u) v[j] &= 0xffff0000u;
         if ((v[j] & 0x7c000000u) == 0x7c000000u) v[j] &= 0x0000ffffu;
     }
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ bool clean16(uint32_t at) {
+    uint32_t v[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+    if (finite_f16x2(v[0]) && finite_f16x2(v[1]) && finite_f16x2(v[2]) && finite_f16x2(v[3])) return false;
+    keep_finite(at, v);
     return true;
 }
 
@@ -520,12 +524,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (NARROW && both) o[k] = fmaf(__uint_as_float(y[k]), k1, o[k]);
                             if (whole && empty) o[k] = 0.f;
                         }
-                        if (poison && mine) {
+                        float odd = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) odd = fmaf(o[k], 0.f, odd);
+                        if (mine && (poison || !(odd == 0.f))) {
                             float more[16] = {};
                             add_non_finite(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock),
                                            min(see_hi, tile.lo + x.to * kBlock), c, more);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] += more[k];
+                            for (int k = 0; k < 16; ++k)
+                                if (!(more[k] == 0.f)) o[k] = more[k];
                         }
                         uint32_t d[16];
                         if (bf16) {
@@ -810,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++piece;
                 for (int u = x.from; ok && u < x.to; ++u, ++block) {
                     const int j0 = x.t.lo + u * kBlock;
-                    const bool check = SPLIT || j0 < x.t.all_lo || j0 + kBlock > x.t.all_hi;
+                    const bool check = j0 < x.t.all_lo || j0 + kBlock > x.t.all_hi;
 #pragma unroll 1
                     for (int kc = 0; kc < 2 * NCH; ++kc) {
                         const uint32_t n = item++;
@@ -820,13 +828,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kc >= NCH && (check || (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu)) {
                             const int width = min(8, chunks16 - 8 * (kc - NCH));  // 16-byte pieces of a row here
                             bool bad = false;
-#pragma unroll 4
-                            for (int e = me; e < 8 * kBlock; e += 32 * (kLoadWarps - 1)) {
-                                if ((e & 7) >= width) continue;
-                                const uint32_t to = chunk_at(n) + swz(e >> 3, e & 7);
-                                // slots that are not there: whatever the page, or the ring before, holds
-                                if ((live[e >> 8] >> ((e >> 3) & 31)) & 1u) bad |= clean16(to);
-                                else asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+                            constexpr int kSkip = 32 * (kLoadWarps - 1) / 8, kBatch = 4;  // rows from one piece of a thread to the next
+                            const uint32_t col = me & 7;
+#pragma unroll 1
+                            for (int r0 = me >> 3; r0 < kBlock; r0 += kBatch * kSkip) {
+                                uint32_t v[kBatch][4], at[kBatch];
+                                bool there[kBatch];
+#pragma unroll
+                                for (int k = 0; k < kBatch; ++k) {
+                                    const int row = min(r0 + k * kSkip, kBlock - 1);
+                                    at[k] = chunk_at(n) + swz(row, col);
+                                    there[k] = (live[row >> 5] >> (row & 31)) & 1u;
+                                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                                 : "=r"(v[k][0]), "=r"(v[k][1]), "=r"(v[k][2]), "=r"(v[k][3]) : "r"(at[k]) : "memory");
+                                }
+#pragma unroll
+                                for (int k = 0; k < kBatch; ++k) {
+                                    if (static_cast<int>(col) >= width || r0 + k * kSkip >= kBlock) continue;
+                                    // slots that are not there: whatever the page, or the ring before, holds
+                                    if (!there[k]) v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0;
+                                    else if (finite_f16x2(v[k][0]) && finite_f16x2(v[k][1]) && finite_f16x2(v[k][2]) &&
+                                             finite_f16x2(v[k][3]))
+                                        continue;
+                                    else bad = true;
+                                    keep_finite(at[k], v[k]);
+                                }
                             }
                             if (bad) ctl.poison[piece % kPoisonRing] = piece;
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -881,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asked = ask(u + 1);
                 const uint32_t there = __ballot_sync(0xffffffffu, at >= 0);
                 const int64_t base = at >= 0 ? at + static_cast<int64_t>(kv) * p.hd : 0;
-                const bool check = SPLIT || j0 < tile.all_lo || j0 + kBlock > tile.all_hi;
+                const bool check = j0 < tile.all_lo || j0 + kBlock > tile.all_hi;
                 int64_t off[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) off[k] = __shfl_sync(0xffffffffu, base, 4 * k + (lane >> 3));
