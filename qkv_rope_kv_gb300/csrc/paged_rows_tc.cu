@@ -9,8 +9,7 @@
 //   NARROW  a tile has 128 rows, the streams take the even and the odd blocks, and their sums are joined at the end
 // A block of a wide tile takes 2048 cycles of the tensor cores (8192 multiply-adds in 64 cycles each way), twice that SPLIT.
 //   warps 0-3, 4-7   softmax of the streams, a row a thread: S out of tensor memory, P back into it (in two halves, so
-//                    that its product begins early), O rescaled where the maximum moved by more than 2^kLazy; at
-//                    the end O / l to memory
+//                    that its product begins early), O rescaled where the maximum has to move; at the end O / l to memory
 //   warp 8           issues the MMAs (9-11 only fill up its warpgroup)
 //   warps 12-15      copy K and V into a ring of chunks of 128 slots x 64 columns in the 128-byte swizzle that the MMA reads.
 //                    Pages of a multiple of 8 slots: 12 asks for boxes of a page's rows by TMA, 13-15 hand them on and
@@ -18,7 +17,7 @@
 // SPLIT (out F32): q is kept as the sum of two f16 (rounded, and the remainder rounded) and so are the weights, both
 // products are made twice, and 22 bits of each are kept.  Otherwise (out BF16) once, of the rounded values: 2^-11, an
 // eighth of what out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are
-// 2^(s - m + kShift), far from f16's ends on both sides.
+// 2^(s - m + kShift), m being the maximum or up to some 2^9 below it.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -40,6 +39,8 @@ static_assert(2 * 128 * (kFewRegs + kManyRegs) <= kThreads * kLaunchRegs, "regis
 constexpr int kChunkBytes = kBlock * 128;  // 128 slots (or q rows) x 64 columns
 constexpr unsigned int kFlagTimeout = 2u;
 constexpr int kControlBytes = 2560;  // barriers and small tables, behind the chunks
+// Weights are kept times 2^kShift; the maximum moves where 64 of a row are together above kMostWeight.
+constexpr float kShift = 6.f, kMostWeight = 32768.f;
 constexpr int kTileCost = 2;  // units that a tile's beginning and end take
 constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
 
@@ -52,7 +53,6 @@ struct Shape {
     // block's K is there, so that many chunks must fit behind those in flight.
     static constexpr int kLag = kStages - 2 * NCH > 5 ? 5 : kStages - 2 * NCH;
     static constexpr int kControlAt = (kQChunks + kStages) * kChunkBytes, kSmem = kControlAt + kControlBytes;
-    static constexpr float kShift = SPLIT ? 12.f : 6.f, kLazy = SPLIT ? 3.f : 8.f;  // weights stay below 2^15
     static_assert(kSmem <= 227 * 1024 && kStages % 2 == 0 && kStages % NCH == 0, "shared memory");
 };
 
@@ -246,7 +246,7 @@ __device__ __noinline__ void add_non_finite(const PagedRowsParams& p, int seq, i
 
 struct Control {
     uint64_t landed[kMaxStages], full[kMaxStages], empty[kMaxStages];
-    uint64_t q_ready[2], q_free[2], s_full[2], p_half[2], p_ready[2], o_full[2], joined, drained;
+    uint64_t q_ready[2], q_free[2], s_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], joined, drained;
     uint32_t live[kLiveRing][4];   // slots of a block that are there
     uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
     float2 ml[kHalf];              // NARROW: maxima and sums of the second stream
@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.q_free[t], 4);
             mbar_init(&ctl.s_full[t], 1);
             mbar_init(&ctl.p_half[t], 4);
+            mbar_init(&ctl.half_done[t], 1);
             mbar_init(&ctl.p_ready[t], 4);
             mbar_init(&ctl.o_full[t], 1);
         }
@@ -344,10 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int token0 = NARROW ? 0 : t * p.part_tokens;  // the stream's first
             if (token0 >= tile.ntok) continue;                  // nothing for this stream
             const int r = 32 * quarter + lane, in_part = r / p.per_block, g = r - in_part * p.per_block;
-            const int i = token0 + in_part, row = tile.row0 + i, h = kv * G + g0 + g;
+            const int i = token0 + in_part, row = tile.row0 + i, h_row = kv * G + g0 + g;
             const bool mine = in_part < p.part_tokens && i < tile.ntok && g < heads;
             const bool busy = 32 * quarter < min(p.part_tokens, tile.ntok - token0) * p.per_block;
-            const float unscale = mine ? __ldcg(p.q_unscale + static_cast<int64_t>(row) * p.nh + h) : 1.f;
+            const float unscale = mine ? __ldcg(p.q_unscale + static_cast<int64_t>(row) * p.nh + h_row) : 1.f;
             const bool both = NARROW ? x.to - x.from > 1 : true;  // NARROW: the second stream has blocks
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, i, see_lo, see_hi);
@@ -357,113 +358,110 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s_phase ^= 1;
                 if (!ok) break;
                 tc_fence_after();
-                if (busy) {
-                    const bool begun = u >= x.from + (NARROW ? 2 : 1);  // O holds sums
-                    const int j0 = tile.lo + u * kBlock;
-                    const uint32_t* live = ctl.live[(first_block + u - x.from) % kLiveRing];
-                    const bool mixed = j0 < tile.all_lo || j0 + kBlock > tile.all_hi ||
-                                       (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
-                    // the slots of columns 32 c .. 32 c + 31 that the row sees
-                    auto seen = [&](int c) {
-                        const int a = see_lo - j0 - 32 * c, b = see_hi - j0 - 32 * c;
-                        const uint32_t below = b >= 32 ? 0xffffffffu : b <= 0 ? 0u : (1u << b) - 1u;
-                        const uint32_t from = a <= 0 ? 0xffffffffu : a >= 32 ? 0u : 0xffffffffu << a;
-                        return below & from & live[c];
-                    };
-                    uint32_t v[kBlock / 32][32];
-                    for (int round = 0;; ++round) {
+                const int j0 = tile.lo + u * kBlock;
+                const uint32_t* live = ctl.live[(first_block + u - x.from) % kLiveRing];
+                const bool mixed = j0 < tile.all_lo || j0 + kBlock > tile.all_hi ||
+                                   (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
+                // the slots of columns 32 c .. 32 c + 31 that the row sees
+                auto seen = [&](int c) {
+                    const int a = see_lo - j0 - 32 * c, b = see_hi - j0 - 32 * c;
+                    const uint32_t below = b >= 32 ? 0xffffffffu : b <= 0 ? 0u : (1u << b) - 1u;
+                    const uint32_t from = a <= 0 ? 0xffffffffu : a >= 32 ? 0u : 0xffffffffu << a;
+                    return below & from & live[c];
+                };
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (busy) {
+                        const uint32_t at = s_at + 64 * half;
+                        uint32_t h[2][16], low[2][16];
+                        float total;
+                        // The weights are made with the maximum as it was.  Their sum tells whether that will do (none is then
+                        // above f16's largest): the maximum itself is looked for only at first and where the sum has grown.
+                        // Rows that are none (what is in q's place there varies) have no say in the warp's votes.
+#pragma unroll 1
+                        for (int round = 0;; ++round) {
+                            uint32_t v[2][32];
+                            tm_ld32(at, v[0]);
+                            tm_ld32(at + 32, v[1]);
+                            tc_wait_ld();
+                            if (mixed) {
 #pragma unroll
-                        for (int c = 0; c < kBlock / 32; ++c) tm_ld32(s_at + 32 * c, v[c]);
-                        tc_wait_ld();
-                        u64 odd = 0;
-                        if (mixed) {
+                                for (int c = 0; c < 2; ++c) {
+                                    const uint32_t in = seen(2 * half + c);
 #pragma unroll
-                            for (int c = 0; c < kBlock / 32; ++c) {
-                                const uint32_t in = seen(c);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    const bool sees = (in >> k) & 1u;
-                                    if (SPLIT && sees && !(fabsf(__uint_as_float(v[c][k])) < CUDART_INF_F)) odd = ~0ull;
-                                    if (!sees) v[c][k] = 0xff800000u;
+                                    for (int k = 0; k < 32; ++k)
+                                        if (!((in >> k) & 1u)) v[c][k] = 0xff800000u;
                                 }
                             }
-                        } else if (SPLIT) {
+                            const float base = (m == -CUDART_INF_F ? 0.f : m) - kShift;
+                            const u64 by = pack2(unscale, unscale), minus = pack2(-base, -base);
+                            u64 sum[2] = {0, 0};
 #pragma unroll
-                            for (int c = 0; c < kBlock / 32; ++c)
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                                for (int k = 0; k < 32; k += 2)
-                                    odd = fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), 0, odd);
+                                for (int k = 0; k < 32; k += 2) {
+                                    const float2 y =
+                                        unpack2(fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), by, minus));
+                                    const float a = ex2(y.x), b = ex2(y.y);
+                                    sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
+                                    if (SPLIT) split2(a, b, h[c][k / 2], low[c][k / 2]);
+                                    else h[c][k / 2] = f16x2(a, b);
+                                }
+                            const float2 s2 = unpack2(add2(sum[0], sum[1]));
+                            total = s2.x + s2.y;
+                            if (round == 2 || !__any_sync(0xffffffffu, mine && (m == -CUDART_INF_F || !(total <= kMostWeight)))) break;
+                            if (SPLIT && round == 0 && __any_sync(0xffffffffu, mine && total != total)) {
+                                const float* q_row = p.q + row * p.q_stride + static_cast<int64_t>(h_row) * p.hd;
+#pragma unroll 1
+                                for (int k = 0; k < 64; ++k) {
+                                    float f = __uint_as_float(tm_ld1(at + k));
+                                    if (mine && f != f && ((seen(2 * half + (k >> 5)) >> (k & 31)) & 1u))
+                                        f = plain_score(p, q_row, tile.seq, j0 + 64 * half + k, kv) / unscale;
+                                    __syncwarp();
+                                    tm_st1(at + k, __float_as_uint(f));
+                                }
+                                tc_wait_st();
+                                continue;
+                            }
+                            float tops[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    tops[c] = max3(tops[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
+                            const float next = mine ? fmaxf(m, fmaxf(tops[0], tops[1]) * unscale) : m;
+                            const float keep = m == next ? 1.f : ex2(m - next);
+                            m = next;
+                            l *= keep;
+                            round = 1;  // the next one is the last
+                            if (half == 1) {  // the first half's weights are on their way into O
+                                ok = __all_sync(0xffffffffu, wait_for(&ctl.half_done[t], s_phase ^ 1));
+                                tc_fence_after();
+                            }
+                            if (half == 1 || u >= x.from + (NARROW ? 2 : 1))
+#pragma unroll 1
+                                for (int c = 0; c < p.hd; c += 16) {
+                                    uint32_t o[16];
+                                    tm_ld16(o_at + c, o);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                                    tm_st16(o_at + c, o);
+                                }
                         }
-                        if (!SPLIT || round == 1) break;
-                        const float2 bad = unpack2(odd);
-                        if (!__any_sync(0xffffffffu, mine && !(bad.x + bad.y == 0.f))) break;
-                        const float* q_row = p.q + row * p.q_stride + static_cast<int64_t>(h) * p.hd;
-                        for (int k = 0; k < kBlock; ++k) {
-                            float f = __uint_as_float(tm_ld1(s_at + k));
-                            if (mine && !(fabsf(f) < CUDART_INF_F) && ((seen(k >> 5) >> (k & 31)) & 1u))
-                                f = plain_score(p, q_row, tile.seq, j0 + k, kv) / unscale;
-                            __syncwarp();
-                            tm_st1(s_at + k, __float_as_uint(f));
+                        l += total;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            tm_st16(at + 32 * c, h[c]);
+                            if (SPLIT) tm_st16(at + 32 * c + 16, low[c]);
                         }
                         tc_wait_st();
                     }
-                    float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-#pragma unroll
-                        for (int c = 0; c < kBlock / 32; ++c)
-                            tops[c] = max3(tops[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
-                    // rows that are none (what is in q's place there varies) have no say in the warp's votes
-                    const float top =
-                        mine ? fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * unscale : -CUDART_INF_F;
-                    if (__any_sync(0xffffffffu, top > m + S::kLazy)) {
-                        const float next = fmaxf(m, top), keep = m == next ? 1.f : ex2(m - next);
-                        m = next;
-                        l *= keep;
-                        if (begun)
-#pragma unroll 1
-                            for (int c = 0; c < p.hd; c += 16) {
-                                uint32_t o[16];
-                                tm_ld16(o_at + c, o);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-                                tm_st16(o_at + c, o);
-                            }
-                    }
-                    const float base = (m == -CUDART_INF_F ? 0.f : m) - S::kShift;
-                    const u64 by = pack2(unscale, unscale), minus = pack2(-base, -base);
-                    u64 sum[2] = {0, 0};
-#pragma unroll
-                    for (int c = 0; c < kBlock / 32; ++c) {
-                        uint32_t h[16], low[16];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            const float2 y =
-                                unpack2(fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), by, minus));
-                            const float a = ex2(y.x), b = ex2(y.y);
-                            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
-                            if (SPLIT) split2(a, b, h[k / 2], low[k / 2]);
-                            else h[k / 2] = f16x2(a, b);
-                        }
-                        tm_st16(s_at + 32 * c, h);
-                        if (SPLIT) tm_st16(s_at + 32 * c + 16, low);
-                        if (c == 1) {
-                            tc_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&ctl.p_half[t]);
-                        }
-                    }
-                    const float2 part = unpack2(add2(sum[0], sum[1]));
-                    l += part.x + part.y;
-                    tc_wait_st();
-                } else if (lane == 0) {
-                    mbar_arrive(&ctl.p_half[t]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(half ? &ctl.p_ready[t] : &ctl.p_half[t]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_ready[t]);
+                if (!ok) break;
             }
             if (!ok) break;
             if (NARROW && t == 1 && both) {
@@ -504,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool bf16 = whole && p.first && p.out_bf16;
                 char* to;
                 if (!whole) to = reinterpret_cast<char*>(part_o(p, part, t * kHalf + r));
-                else if (!p.first) to = reinterpret_cast<char*>(p.prefix_out + (static_cast<int64_t>(row) * p.nh + h) * p.hd);
-                else to = static_cast<char*>(p.out) + (row * p.out_stride + static_cast<int64_t>(h) * p.hd) * (bf16 ? 2 : 4);
+                else if (!p.first) to = reinterpret_cast<char*>(p.prefix_out + (static_cast<int64_t>(row) * p.nh + h_row) * p.hd);
+                else to = static_cast<char*>(p.out) + (row * p.out_stride + static_cast<int64_t>(h_row) * p.hd) * (bf16 ? 2 : 4);
                 constexpr int kRowBytes = 128 * NCH;  // of a row and round
                 const uint32_t mine_at = q_chunk(t, 0, 0) + (32 * quarter) * kRowBytes;
                 const int bytes = p.hd * (bf16 ? 2 : 4), columns = kRowBytes / (bf16 ? 2 : 4);
@@ -586,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (mine) {
                     float* lse = p.first ? p.lse : p.prefix_lse;
-                    if (!whole) *part_ml(part, t * kHalf + r) = make_float2(m - S::kShift, l);
-                    else if (lse) lse[static_cast<int64_t>(row) * p.nh + h] = lse_of(m - S::kShift, l, empty);
+                    if (!whole) *part_ml(part, t * kHalf + r) = make_float2(m - kShift, l);
+                    else if (lse) lse[static_cast<int64_t>(row) * p.nh + h_row] = lse_of(m - kShift, l, empty);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
@@ -660,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_ts(o, w0 + 32 * (k >> 1) + 16 * part + 8 * (k & 1), v + 128 * k, id_o, acc);
                         acc = 1;
                     }
+                if (half == 0) tc_commit(&ctl.half_done[t]);
             }
         };
         while (ok && w.next(p, x)) {
