@@ -37,46 +37,60 @@ __device__ __forceinline__ T scan(T v, T& sum, T* warp_s) {
 // f16's subnormals, and the remainders; and by what scores are to be multiplied to be in log2 terms.  A warp a row, as
 // many bytes as q has (or half as many again); rows that belong to no sequence too.
 __device__ __forceinline__ void convert_q(const PagedRowsParams& p) {
+    constexpr int kAhead = 4;  // rows of a warp in flight
     const int lane = threadIdx.x & 31;
     const int64_t rows = static_cast<int64_t>(p.nt) * p.nh, step = static_cast<int64_t>(gridDim.x - 1) * (kPlanThreads / 32);
     const float by = fabsf(p.scale) * kLog2e;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5); r < rows; r += step) {
-        const int64_t tok = r / p.nh;
-        const float* q = p.q + tok * p.q_stride + (r - tok * p.nh) * p.hd + 4 * lane;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (4 * lane < p.hd) {
-            if ((reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
-                const float4 f = __ldcg(reinterpret_cast<const float4*>(q));
-                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-            } else {
+    const bool quads = ((reinterpret_cast<uintptr_t>(p.q) | static_cast<uintptr_t>(p.q_stride * 4)) & 15u) == 0;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5); r0 < rows; r0 += kAhead * step) {
+        float v[kAhead][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = __ldcg(q + k);
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t r = r0 + j * step;
+            const int tok = static_cast<int>(r / p.nh);
+            const float* q = p.q + tok * p.q_stride + (r - static_cast<int64_t>(tok) * p.nh) * p.hd + 4 * lane;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[j][k] = 0.f;
+            if (r < rows && 4 * lane < p.hd) {
+                if (quads) {
+                    const float4 f = __ldcg(reinterpret_cast<const float4*>(q));
+                    v[j][0] = f.x, v[j][1] = f.y, v[j][2] = f.z, v[j][3] = f.w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[j][k] = __ldcg(q + k);
+                }
             }
         }
-        float big = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-        big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));  // not below zero
-        // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
-        int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
-        e = e == 128 ? 13 : max(-113, min(e, 126));
-        // scores are compared before they are multiplied: by a number above zero, the sign goes into q
-        float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-        if (p.scale < 0.f) sc = -sc;
-        const float unscale = by == 0.f ? 1.f : fmaxf(by * __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23), 1.1754944e-38f);
-        if (by == 0.f) sc = 0.f;
-        if (4 * lane < p.hd) {
-            __half2 h[2], l[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float a = v[2 * k] * sc, b = v[2 * k + 1] * sc;
-                h[k] = __floats2half2_rn(a, b);
-                const float2 f = __half22float2(h[k]);
-                l[k] = __floats2half2_rn(a - f.x, b - f.y);
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t r = r0 + j * step;
+            if (r >= rows) break;
+            float big = fmaxf(fmaxf(fabsf(v[j][0]), fabsf(v[j][1])), fmaxf(fabsf(v[j][2]), fabsf(v[j][3])));
+            big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));  // not below zero
+            // exponent of the largest |q|, kept where both 2^(13 - e) and 2^(e - 13) are normal
+            int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127;
+            e = e == 128 ? 13 : max(-113, min(e, 126));
+            // scores are compared before they are multiplied: by a number above zero, the sign goes into q
+            float sc = __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+            if (p.scale < 0.f) sc = -sc;
+            if (by == 0.f) sc = 0.f;
+            const float unscale =
+                by == 0.f ? 1.f : fmaxf(by * __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23), 1.1754944e-38f);
+            if (4 * lane < p.hd) {
+                __half2 h[2], l[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float a = v[j][2 * k] * sc, b = v[j][2 * k + 1] * sc;
+                    h[k] = __floats2half2_rn(a, b);
+                    const float2 f = __half22float2(h[k]);
+                    l[k] = __floats2half2_rn(a - f.x, b - f.y);
+                }
+                const int64_t at = r * p.hd + 4 * lane;
+                *reinterpret_cast<uint2*>(p.q_high + at) = *reinterpret_cast<uint2*>(h);
+                if (!p.out_bf16) *reinterpret_cast<uint2*>(p.q_low + at) = *reinterpret_cast<uint2*>(l);
             }
-            const int64_t at = r * p.hd + 4 * lane;
-            *reinterpret_cast<uint2*>(p.q_high + at) = *reinterpret_cast<uint2*>(h);
-            if (!p.out_bf16) *reinterpret_cast<uint2*>(p.q_low + at) = *reinterpret_cast<uint2*>(l);
+            if (lane == 0) p.q_unscale[r] = unscale;
         }
-        if (lane == 0) p.q_unscale[r] = unscale;
     }
 }
 
@@ -233,32 +247,92 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
 }
 
 constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32;
-constexpr int kMaxCols = QKV_MAX_HEAD_DIM / 32;
+constexpr int kQuads = QKV_MAX_HEAD_DIM / 128;  // of a lane's columns: four from 4 * lane, and from 128 + 4 * lane
 
-// The parts of a row, in the order of its slots: the lane's columns lane, lane + 32, ...
+// Columns [d, d + 4) of a row, as far as there are any.
+__device__ __forceinline__ float4 get4(const float* row, int d, int hd) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d + 4 <= hd && (reinterpret_cast<uintptr_t>(row + d) & 15u) == 0) return __ldcg(reinterpret_cast<const float4*>(row + d));
+    if (d < hd) v.x = __ldcg(row + d);
+    if (d + 1 < hd) v.y = __ldcg(row + d + 1);
+    if (d + 2 < hd) v.z = __ldcg(row + d + 2);
+    if (d + 3 < hd) v.w = __ldcg(row + d + 3);
+    return v;
+}
+__device__ __forceinline__ void put4(const PagedRowsParams& p, int64_t at, int d, float4 v) {
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    if (p.out_bf16) {
+        uint16_t* o = static_cast<uint16_t*>(p.out) + at + d;
+        uint32_t two[2];
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(two[0]) : "f"(v.y), "f"(v.x));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(two[1]) : "f"(v.w), "f"(v.z));
+        if (d + 4 <= p.hd && (reinterpret_cast<uintptr_t>(o) & 7u) == 0) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(two[0], two[1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (d + k < p.hd) o[k] = static_cast<uint16_t>(two[k >> 1] >> (16 * (k & 1)));
+        }
+    } else {
+        float* o = static_cast<float*>(p.out) + at + d;
+        if (d + 4 <= p.hd && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+            *reinterpret_cast<float4*>(o) = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (d + k < p.hd) o[k] = x[k];
+        }
+    }
+}
+__device__ __forceinline__ float4 fma4(float4 a, float k, float4 b) {
+    return make_float4(fmaf(a.x, k, b.x), fmaf(a.y, k, b.y), fmaf(a.z, k, b.z), fmaf(a.w, k, b.w));
+}
+
+// The parts of a row, in the order of its slots, a few at a time, all of whose loads are in flight together.
 struct Joined {
-    float m, l, o[kMaxCols];
+    float m, l;
+    float4 o[kQuads];
 };
 __device__ __forceinline__ void join_row(const PagedRowsParams& p, int64_t start, int64_t share, int c0, int parts, int row,
                                          Joined& j) {
+    constexpr int kAhead = 4;
     const int lane = threadIdx.x & 31;
     j.m = -CUDART_INF_F;
     j.l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMaxCols; ++k) j.o[k] = 0.f;
+    for (int k = 0; k < kQuads; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool first = start == share * c0;  // the tile is the first of its first CTA
-    for (int c = lane; c < parts; c += 32) j.m = fmaxf(j.m, __ldcg(part_ml(part_of(p, c0 + c, c > 0 || first), row)).x);
-    for (int o = 16; o; o >>= 1) j.m = fmaxf(j.m, __shfl_xor_sync(0xffffffffu, j.m, o));
-#pragma unroll 4
-    for (int c = 0; c < parts; ++c) {
-        float* part = part_of(p, c0 + c, c > 0 || first);
-        const float2 ml = __ldcg(part_ml(part, row));
-        const float k = ml.x == j.m ? 1.f : exp2f(ml.x - j.m);
-        const float* o = part_o(p, part, row);
-        j.l = fmaf(ml.y, k, j.l);
+#pragma unroll 1
+    for (int b = 0; b < parts; b += kAhead) {
+        float2 ml[kAhead];
+        float4 o[kAhead][kQuads];
 #pragma unroll
-        for (int i = 0; i < kMaxCols; ++i)
-            if (lane + 32 * i < p.hd) j.o[i] = fmaf(__ldcg(o + lane + 32 * i), k, j.o[i]);
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = min(b + i, parts - 1);
+            float* part = part_of(p, c0 + c, c > 0 || first);
+            ml[i] = __ldcg(part_ml(part, row));
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k)
+                if (k == 0 || p.hd > 128) o[i][k] = get4(part_o(p, part, row), 128 * k + 4 * lane, p.hd);
+        }
+        float top = j.m;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (b + i < parts) top = fmaxf(top, ml[i].x);
+        const float keep = j.m == top ? 1.f : exp2f(j.m - top);
+        j.m = top;
+        j.l *= keep;
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) j.o[k] = fma4(j.o[k], keep, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (b + i >= parts) continue;
+            const float f = ml[i].x == top ? 1.f : exp2f(ml[i].x - top);
+            j.l = fmaf(ml[i].y, f, j.l);
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k)
+                if (k == 0 || p.hd > 128) j.o[k] = fma4(o[i][k], f, j.o[k]);
+        }
     }
 }
 
@@ -266,15 +340,14 @@ __device__ __forceinline__ void join_row(const PagedRowsParams& p, int64_t start
 __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_constant__ PagedRowsParams p, int ctas) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = share_of(total, ctas);
-    if (share * blockIdx.x >= total) return;
     const RowPiece* s = p.pieces + blockIdx.x;
-    const int parts = __ldcg(&s->parts);
-    if (parts == 0) return;
-    const int64_t start = __ldcg(&s->start);
-    const int head = __ldcg(&s->head), kv = head / p.blocks, G = p.nh / p.nkv;
+    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = share_of(total, ctas);
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(s)), y = __ldcg(reinterpret_cast<const int4*>(s) + 1);
+    if (share * blockIdx.x >= total || y.x == 0) return;  // (what was loaded is none)
+    const int64_t start = static_cast<uint32_t>(x.x) | static_cast<int64_t>(x.y) << 32;
+    const int parts = y.x, head = x.w, kv = head / p.blocks, G = p.nh / p.nkv;
     const int g0 = (head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
-    const RowTile t = load_tile(p, __ldcg(&s->tile));
+    const RowTile t = load_tile(p, x.z);
     for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < t.ntok * heads; r += gridDim.y * kJoinRows) {
         const int i = r / heads, g = r - i * heads, h = kv * G + g0 + g;
         Joined j;
@@ -282,14 +355,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_
         int lo, hi;
         row_span(p, t, i, lo, hi);
         const bool empty = lo >= hi;
-        const float inv = empty ? 0.f : 1.f / j.l;
+        const float inv = 1.f / j.l;
         const int64_t at = (t.row0 + i) * p.out_stride + static_cast<int64_t>(h) * p.hd;
+        const int d = 4 * (threadIdx.x & 31);
 #pragma unroll
-        for (int k = 0; k < kMaxCols; ++k) {
-            const int d = (threadIdx.x & 31) + 32 * k;
-            if (d < p.hd) put_out(p, at + d, empty ? 0.f : j.o[k] * inv);
+        for (int k = 0; k < kQuads; ++k) {
+            const float4 o = make_float4(j.o[k].x * inv, j.o[k].y * inv, j.o[k].z * inv, j.o[k].w * inv);
+            put4(p, at, 128 * k + d, empty ? make_float4(0.f, 0.f, 0.f, 0.f) : o);
         }
-        if ((threadIdx.x & 31) == 0 && p.lse) p.lse[static_cast<int64_t>(t.row0 + i) * p.nh + h] = lse_of(j.m, j.l, empty);
+        if (d == 0 && p.lse) p.lse[static_cast<int64_t>(t.row0 + i) * p.nh + h] = lse_of(j.m, j.l, empty);
     }
 }
 
@@ -300,17 +374,23 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
     const int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 5);
     const int b = static_cast<int>(x / p.nh), h = static_cast<int>(x - static_cast<int64_t>(b) * p.nh);
     if (b >= p.c.n_seq) return;
-    const int lane = threadIdx.x & 31, G = p.nh / p.nkv, kv = h / G;
-    const bool prefix = __ldcg(p.row_end + b) > 0;
+    const int d = 4 * (threadIdx.x & 31), G = p.nh / p.nkv, kv = h / G;
     const int64_t row = static_cast<int64_t>(b) * p.nh + h;
+    // all that is needed whatever the case, in flight together
+    const int seen = __ldcg(p.row_end + b), tile = __ldcg(p.row_tile + b);
+    const int64_t per_head = __ldcg(p.total);
     const float own = __ldcg(p.own_lse + row);
+    float4 mine[kQuads];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) mine[k] = get4(p.own_out + row * p.hd, 128 * k + d, p.hd);
+    const bool prefix = seen > 0;
     float theirs = -CUDART_INF_F;
     Joined j;
 #pragma unroll
-    for (int k = 0; k < kMaxCols; ++k) j.o[k] = 0.f;
+    for (int k = 0; k < kQuads; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (prefix) {
-        const RowTile t = load_tile(p, __ldcg(p.row_tile + b));
-        const int64_t per_head = __ldcg(p.total), share = share_of(per_head * p.nkv * p.blocks, ctas);
+        const RowTile t = load_tile(p, tile);
+        const int64_t share = share_of(per_head * p.nkv * p.blocks, ctas);
         const int blk = (h - kv * G) / p.per_block;
         const int64_t start = (static_cast<int64_t>(kv) * p.blocks + blk) * per_head + t.start;
         const int c0 = static_cast<int>(start / share), c1 = static_cast<int>((start + t.units - 1) / share);
@@ -318,31 +398,26 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
             join_row(p, start, share, c0, c1 - c0 + 1, row_of(p, b - t.row0, h - kv * G - blk * p.per_block), j);
             const float inv = 1.f / j.l;
 #pragma unroll
-            for (int k = 0; k < kMaxCols; ++k) j.o[k] *= inv;
+            for (int k = 0; k < kQuads; ++k) j.o[k] = fma4(j.o[k], inv, make_float4(0.f, 0.f, 0.f, 0.f));
             theirs = lse_of(j.m, j.l, false);
         } else {
             theirs = __ldcg(p.prefix_lse + row);
 #pragma unroll
-            for (int k = 0; k < kMaxCols; ++k)
-                if (lane + 32 * k < p.hd) j.o[k] = __ldcg(p.prefix_out + row * p.hd + lane + 32 * k);
+            for (int k = 0; k < kQuads; ++k) j.o[k] = get4(p.prefix_out + row * p.hd, 128 * k + d, p.hd);
         }
     }
     // One that is empty (-inf) leaves the other as it is.  A NaN, or +inf (whose own row is NaN already), stays.
     const bool none = own == -CUDART_INF_F, alone = !prefix;
     const float top = fmaxf(own, theirs);
-    float a = alone ? 0.f : expf(theirs - top), z = none && !alone && theirs > -CUDART_INF_F ? 0.f : expf(own - top);
-    if (alone) z = 1.f;
+    const float a = alone ? 0.f : expf(theirs - top), z = alone ? 1.f : none && theirs > -CUDART_INF_F ? 0.f : expf(own - top);
     const float inv = 1.f / (a + z);
     const int64_t at = b * p.out_stride + static_cast<int64_t>(h) * p.hd;
 #pragma unroll
-    for (int k = 0; k < kMaxCols; ++k) {
-        const int d = lane + 32 * k;
-        if (d >= p.hd) break;
-        const float mine = __ldcg(p.own_out + row * p.hd + d);
-        const float v = alone ? mine : z == 0.f ? j.o[k] : a == 0.f ? mine : (j.o[k] * a + mine * z) * inv;
-        put_out(p, at + d, v);
+    for (int k = 0; k < kQuads; ++k) {
+        const float4 s = fma4(mine[k], z, fma4(j.o[k], a, make_float4(0.f, 0.f, 0.f, 0.f)));
+        put4(p, at, 128 * k + d, alone || a == 0.f ? mine[k] : z == 0.f ? j.o[k] : fma4(s, inv, make_float4(0.f, 0.f, 0.f, 0.f)));
     }
-    if (lane == 0 && p.lse) p.lse[row] = alone || top == -CUDART_INF_F ? own : z == 0.f ? theirs : a == 0.f ? own : top + logf(a + z);
+    if (d == 0 && p.lse) p.lse[row] = alone || top == -CUDART_INF_F ? own : z == 0.f ? theirs : a == 0.f ? own : top + logf(a + z);
 }
 
 }  // namespace
@@ -359,7 +434,7 @@ cudaError_t launch_paged_rows_plan(const PagedRowsParams& p, cudaStream_t stream
 cudaError_t launch_paged_rows_join(const PagedRowsParams& p, cudaStream_t stream) {
     const int ctas = paged_rows_shape(p).ctas;
     if (p.first) {
-        const int each = (p.rows + 4 * kJoinRows - 1) / (4 * kJoinRows);  // four rows a warp
+        const int each = (p.rows + 2 * kJoinRows - 1) / (2 * kJoinRows);  // two rows a warp
         return launch_dependent(join_prompt_kernel, dim3(ctas, each), kJoinThreads, 0, stream, 1, p, ctas);
     }
     const int64_t rows = static_cast<int64_t>(p.c.n_seq) * p.nh;

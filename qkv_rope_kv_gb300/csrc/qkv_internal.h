@@ -189,11 +189,10 @@ struct alignas(16) RowTile {
     int32_t base;        // row i sees [max(0, base + i - window), base + i); prefix: [0, row_end[row0 + i])
     int32_t all_lo, all_hi;  // slots that every row sees
 };
-struct RowPiece {  // for each CTA, the tile that begins in it and goes on in others
+struct alignas(16) RowPiece {  // for each CTA, the tile that begins in it and goes on in others
     int64_t start;  // of the tile, over all heads
     int32_t tile, head;
     int32_t parts;  // 0: none
-    int32_t pad;
 };
 constexpr int kRowsMaxCtas = 304;
 struct PagedRowsParams {
