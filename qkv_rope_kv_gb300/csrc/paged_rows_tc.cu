@@ -229,19 +229,36 @@ __device__ __noinline__ float plain_score(const PagedRowsParams& p, const float*
     return s;
 }
 
-// What the infinities and NaN of V that a row sees, in slots [lo, hi), add to 16 columns of its sum.  The products do not
-// tell: a weight of zero (of a slot that the row does not see; or rounded, or a remainder) times them is NaN.  So blocks
-// with slots that only some rows see get zeros in their place, and rows that come out infinite or NaN look here.
-__device__ __noinline__ void add_non_finite(const PagedRowsParams& p, int seq, int kv, int lo, int hi, int c, float* o) {
-    for (int s = lo; s < hi; ++s) {
-        const int64_t row = row_offset(p.c, seq, s);
-        if (row < 0) continue;
-        const __half* v = static_cast<const __half*>(p.c.v) + row + static_cast<int64_t>(kv) * p.hd + c;
-        for (int d = 0; d < 16; ++d) {
-            const float x = __half2float(v[d]);
-            if (!(fabsf(x) < CUDART_INF_F)) o[d] += x;
+// What the infinities and NaN of V that a row sees, in slots [lo, hi), make of its result.  The products do not tell: a
+// weight of zero (of a slot that the row does not see; or rounded, or a remainder) times them is NaN.  So blocks with
+// slots that only some rows see get zeros in their place, and rows that come out infinite or NaN look here.
+__device__ __noinline__ void fix_row(const PagedRowsParams& p, int seq, int kv, int lo, int hi, char* to, int es) {
+    for (int d = 0; d < p.hd; ++d) {
+        float more = 0.f;
+        for (int s = lo; s < hi; ++s) {
+            const int64_t row = row_offset(p.c, seq, s);
+            if (row < 0) continue;
+            const float v = __half2float(static_cast<const __half*>(p.c.v)[row + static_cast<int64_t>(kv) * p.hd + d]);
+            if (!(fabsf(v) < CUDART_INF_F)) more += v;
         }
+        if (more == 0.f) continue;
+        if (es == 2) reinterpret_cast<uint16_t*>(to)[d] = bf16_bits(more);
+        else reinterpret_cast<float*>(to)[d] = more;
     }
+}
+
+// 16 bytes of values of es bytes, to any address of such values.
+__device__ __noinline__ void store_any(char* to, uint4 v, int es) {
+    const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    for (int j = 0; j < 16; j += es) {
+        const uint32_t x = j < 4 ? e[0] : j < 8 ? e[1] : j < 12 ? e[2] : e[3];
+        if (es == 2) *reinterpret_cast<uint16_t*>(to + j) = static_cast<uint16_t>(x >> (8 * (j & 3)));
+        else *reinterpret_cast<uint32_t*>(to + j) = x;
+    }
+}
+__device__ __forceinline__ void store16(char* to, uint4 v, int es) {
+    if ((reinterpret_cast<uintptr_t>(to) & 15u) == 0) *reinterpret_cast<uint4*>(to) = v;
+    else store_any(to, v, es);
 }
 
 struct Control {
@@ -494,19 +511,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
                 const bool whole = x.whole(), empty = see_lo >= see_hi;
-                if (whole) k0 *= empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
-                if (NARROW && both && whole) k1 *= empty ? 0.f : 1.f / l;
+                const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
+                k0 *= inv;
+                k1 *= inv;
                 float* part = part_of(p, blockIdx.x, x.first);
-                // Results go to memory through q's place, by whole rows of a warp: 16 bytes a lane of neighbouring lanes
-                // instead of a row a lane, which took 7000 cycles of a tile.
-                const bool bf16 = whole && p.first && p.out_bf16;
+                // Results go to memory through q's place, by rows of a warp: 16 bytes a lane of neighbouring lanes instead of a
+                // row a lane, which took 7000 cycles of a tile.
+                const int es = whole && p.first && p.out_bf16 ? 2 : 4;
                 char* to;
                 if (!whole) to = reinterpret_cast<char*>(part_o(p, part, t * kHalf + r));
                 else if (!p.first) to = reinterpret_cast<char*>(p.prefix_out + (static_cast<int64_t>(row) * p.nh + h_row) * p.hd);
-                else to = static_cast<char*>(p.out) + (row * p.out_stride + static_cast<int64_t>(h_row) * p.hd) * (bf16 ? 2 : 4);
-                constexpr int kRowBytes = 128 * NCH;  // of a row and round
-                const uint32_t mine_at = q_chunk(t, 0, 0) + (32 * quarter) * kRowBytes;
-                const int bytes = p.hd * (bf16 ? 2 : 4), columns = kRowBytes / (bf16 ? 2 : 4);
+                else to = static_cast<char*>(p.out) + (row * p.out_stride + static_cast<int64_t>(h_row) * p.hd) * es;
+                constexpr int kRowBytes = 128;  // of 32 rows: a round's
+                const uint32_t stage = q_chunk(t, 0, 0) + quarter * 32 * kRowBytes;
+                const int columns = kRowBytes / es;
+                float odd = 0.f;
 #pragma unroll 1
                 for (int c0 = 0; c0 < p.hd; c0 += columns) {
 #pragma unroll 1
@@ -515,71 +534,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tm_ld16(o_at + c, v);
                         if (NARROW && both) tm_ld16(o_at + 128 + c, y);
                         tc_wait_ld();
+                        uint32_t d[16];
                         float o[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             o[k] = __uint_as_float(v[k]) * k0;
                             if (NARROW && both) o[k] = fmaf(__uint_as_float(y[k]), k1, o[k]);
-                            if (whole && empty) o[k] = 0.f;
+                            odd = fmaf(o[k], 0.f, odd);
+                            d[k] = __float_as_uint(o[k]);
                         }
-                        float odd = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) odd = fmaf(o[k], 0.f, odd);
-                        if (mine && (poison || !(odd == 0.f))) {
-                            float more[16] = {};
-                            add_non_finite(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock),
-                                           min(see_hi, tile.lo + x.to * kBlock), c, more);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if (!(more[k] == 0.f)) o[k] = more[k];
-                        }
-                        uint32_t d[16];
-                        if (bf16) {
+                        if (es == 2) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d[k]) : "f"(o[2 * k + 1]), "f"(o[2 * k]));
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) d[k] = __float_as_uint(o[k]);
                         }
-                        const int first = (c - c0) * (bf16 ? 2 : 4) / 16;  // 16-byte piece of the row
+                        const uint32_t dst = stage + lane * kRowBytes, first = (c - c0) * es / 16;  // 16-byte piece of the row
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (!bf16 || k < 2)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                 mine_at + lane * kRowBytes + (((first + k) ^ (lane & 7)) << 4)),
+                            if (es == 4 || k < 2)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((first + k) ^ (lane & 7)) << 4)),
                                              "r"(d[4 * k]), "r"(d[4 * k + 1]), "r"(d[4 * k + 2]), "r"(d[4 * k + 3])
                                              : "memory");
                     }
                     __syncwarp();
-                    constexpr int kPieces = kRowBytes / 16, kRowsAtOnce = 32 / kPieces;
-                    const int piece16 = lane % kPieces, skip = c0 * (bf16 ? 2 : 4);
-#pragma unroll 2
-                    for (int k = 0; k < 32; k += kRowsAtOnce) {
-                        const int from = k + lane / kPieces;
-                        char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(to), from)) + skip + 16 * piece16;
-                        const bool there = __shfl_sync(0xffffffffu, mine, from);
-                        if (!there || skip + 16 * piece16 >= bytes) continue;
-                        uint4 v;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                     : "r"(mine_at + from * kRowBytes + ((piece16 ^ (from & 7)) << 4))
-                                     : "memory");
-                        if ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-                            *reinterpret_cast<uint4*>(dst) = v;
-                        } else {
-                            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                    // eight lanes a row
+                    const int skip = c0 * es + 16 * (lane & 7);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (bf16) {
-                                    reinterpret_cast<uint16_t*>(dst)[2 * j] = static_cast<uint16_t>(e[j]);
-                                    reinterpret_cast<uint16_t*>(dst)[2 * j + 1] = static_cast<uint16_t>(e[j] >> 16);
-                                } else {
-                                    reinterpret_cast<uint32_t*>(dst)[j] = e[j];
-                                }
-                            }
-                        }
+                    for (int k = 0; k < 32; k += 4) {
+                        const int from = k + (lane >> 3);
+                        char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(to), from)) + skip;
+                        const bool has = __shfl_sync(0xffffffffu, mine, from);
+                        uint4 w4;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w)
+                                     : "r"(stage + from * kRowBytes + (((lane & 7) ^ (from & 7)) << 4))
+                                     : "memory");
+                        if (has && skip < p.hd * es) store16(dst, w4, es);
                     }
+                    __syncwarp();
+                }
+                if (__any_sync(0xffffffffu, mine && (poison || !(odd == 0.f)))) {
+                    if (mine)
+                        fix_row(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock), min(see_hi, tile.lo + x.to * kBlock), to, es);
                     __syncwarp();
                 }
                 if (mine) {
