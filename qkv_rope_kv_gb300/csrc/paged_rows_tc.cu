@@ -138,6 +138,15 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&r)[16]) {
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
+    uint32_t x[16];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = r[16 * i + k];
+        tm_st16(a + 16 * i, x);
+    }
+}
 __device__ __forceinline__ uint32_t tm_ld1(uint32_t a) {
     uint32_t r;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(a));
@@ -390,17 +399,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int half = 0; half < 2; ++half) {
                     if (busy) {
                         const uint32_t at = s_at + 64 * half;
-                        uint32_t h[2][16], low[2][16];
                         float total;
+                        uint32_t v[2][32];
+                        tm_ld32(at, v[0]);
+                        tm_ld32(at + 32, v[1]);
+                        tc_wait_ld();
                         // The weights are made with the maximum as it was.  Their sum tells whether that will do (none is then
                         // above f16's largest): the maximum itself is looked for only at first and where the sum has grown.
                         // Rows that are none (what is in q's place there varies) have no say in the warp's votes.
 #pragma unroll 1
                         for (int round = 0;; ++round) {
-                            uint32_t v[2][32];
-                            tm_ld32(at, v[0]);
-                            tm_ld32(at + 32, v[1]);
-                            tc_wait_ld();
                             if (mixed) {
 #pragma unroll
                                 for (int c = 0; c < 2; ++c) {
@@ -414,21 +422,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const u64 by = pack2(unscale, unscale), minus = pack2(-base, -base);
                             u64 sum[2] = {0, 0};
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t h[16], low[16];
 #pragma unroll
                                 for (int k = 0; k < 32; k += 2) {
                                     const float2 y =
                                         unpack2(fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), by, minus));
                                     const float a = ex2(y.x), b = ex2(y.y);
                                     sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
-                                    if (SPLIT) split2(a, b, h[c][k / 2], low[c][k / 2]);
-                                    else h[c][k / 2] = f16x2(a, b);
+                                    if (SPLIT) split2(a, b, h[k / 2], low[k / 2]);
+                                    else h[k / 2] = f16x2(a, b);
                                 }
+                                tm_st16(at + 32 * c, h);
+                                if (SPLIT) tm_st16(at + 32 * c + 16, low);
+                            }
                             const float2 s2 = unpack2(add2(sum[0], sum[1]));
                             total = s2.x + s2.y;
                             if (round == 2 || !__any_sync(0xffffffffu, mine && (m == -CUDART_INF_F || !(total <= kMostWeight)))) break;
                             if (SPLIT && round == 0 && __any_sync(0xffffffffu, mine && total != total)) {
                                 const float* q_row = p.q + row * p.q_stride + static_cast<int64_t>(h_row) * p.hd;
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) tm_st32(at + 32 * c, v[c]);
+                                tc_wait_st();
 #pragma unroll 1
                                 for (int k = 0; k < 64; ++k) {
                                     float f = __uint_as_float(tm_ld1(at + k));
@@ -438,6 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     tm_st1(at + k, __float_as_uint(f));
                                 }
                                 tc_wait_st();
+                                tm_ld32(at, v[0]);
+                                tm_ld32(at + 32, v[1]);
+                                tc_wait_ld();
                                 continue;
                             }
                             float tops[2] = {-CUDART_INF_F, -CUDART_INF_F};
@@ -467,11 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                         }
                         l += total;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            tm_st16(at + 32 * c, h[c]);
-                            if (SPLIT) tm_st16(at + 32 * c + 16, low[c]);
-                        }
                         tc_wait_st();
                     }
                     tc_fence_before();
