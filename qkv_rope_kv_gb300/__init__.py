@@ -626,7 +626,12 @@ def _workspace(t, device: int):
     return _tensor(t, "workspace", t.dtype, t.shape, device), t.nbytes
 
 
-def _store_args(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q) -> bytes:
+def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps: float, positions, seqs, slots,
+                         q, stream=None, rope: Rope | None = None):
+    """Finish the projections Y [nt, R] (f32 or bf16; rows may be strided) of tokens of any
+    sequences: bias, optional q/k norms, rotation, q [nt, nqt] f32 out, k and v into the cache.
+    ``bias``, the norm weights (together), ``seqs`` and ``slots`` may be None (see qkv.h); with
+    ``rope`` this is qkv_paged_store_rope_step."""
     f32, i32, bf16 = cache.types
     dev, y_type, head = cache.device, Y.dtype, (plan.head_dim,)
     nt = Y.shape[0]
@@ -634,29 +639,23 @@ def _store_args(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps, po
     to, to_stride = _rows(q, "q", f32, (nt, plan.nqt), dev)
     nt_shape = (nt,)
     try:
-        return _STORE_ARGS.pack(
+        args = _STORE_ARGS.pack(
             y, y_stride, QKV_BF16 if y_type is bf16 else QKV_F32, nt, _tensor(bias, "bias", f32, (plan.rows,), dev),
             _tensor(q_norm_w, "q_norm_w", f32, head, dev), _tensor(k_norm_w, "k_norm_w", f32, head, dev),
             _tensor(positions, "positions", i32, nt_shape, dev), _tensor(seqs, "seqs", i32, nt_shape, dev),
             _tensor(slots, "slots", i32, nt_shape, dev), to, to_stride, eps)
     except (struct.error, OverflowError) as e:
         _unpackable(e)
-
-
-def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w, eps: float, positions, seqs, slots,
-                         q, stream=None):
-    """Finish the projections Y [nt, R] (f32 or bf16; rows may be strided) of tokens of any
-    sequences: bias, optional q/k norms, rotation, q [nt, nqt] f32 out, k and v into the cache.
-    ``bias``, the norm weights (together), ``seqs`` and ``slots`` may be None (see qkv.h)."""
-    args = _store_args(plan, cache, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q)
-    _check(_lib.qkv_paged_store_step(plan.handle, cache.address, args, cache._on(plan, stream)))
+    if rope is not None:
+        _check(_lib.qkv_paged_store_rope_step(plan.handle, cache.address, rope.handle, args, cache._on(plan, stream)))
+    else:
+        _check(_lib.qkv_paged_store_step(plan.handle, cache.address, args, cache._on(plan, stream)))
 
 
 def qkv_paged_store_rope_step(plan: Plan, cache: PagedKv, rope: Rope, Y, bias, q_norm_w, k_norm_w, eps: float, positions,
                               seqs, slots, q, stream=None):
     """qkv_paged_store_step with ``rope`` in place of the plan's rotation."""
-    args = _store_args(plan, cache, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q)
-    _check(_lib.qkv_paged_store_rope_step(plan.handle, cache.address, rope.handle, args, cache._on(plan, stream)))
+    qkv_paged_store_step(plan, cache, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q, stream, rope)
 
 
 def qkv_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:

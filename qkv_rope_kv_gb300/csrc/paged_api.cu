@@ -441,6 +441,7 @@ extern "C" qkv_status qkv_prefix_attn_step(const qkv_plan* plan, const qkv_paged
     o.q_stride = a->q_stride;
     o.lens = a->d_lens;
     o.starts = p.starts;
+    o.window = -1;
     o.scale = a->scale;
     o.out = ws + l.own_out;
     o.out_stride = plan->nqt;

@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kAnyThreads) paged_attn_any_kernel(const __gri
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int j0 = h / (p.nh / p.nkv) * p.hd;
     const int n = checked_len(p.c, p.lens, b);
-    const int first = p.starts ? min(p.starts[b], n) : p.window > 0 ? max(0, n - p.window) : 0;
+    int first = 0;
+    if (p.window != 0) first = p.window > 0 ? max(0, n - p.window) : min(p.starts[b], n);
     for (int d = tid; d < p.hd; d += kAnyThreads)
         q_s[d] = p.q[b * p.q_stride + static_cast<int64_t>(h) * p.hd + d] * (p.scale * kLog2e);
     float* scores = p.add_weight ? p.scores + (static_cast<int64_t>(b) * p.nh + h) * p.score_stride : nullptr;
@@ -355,7 +356,8 @@ __device__ __forceinline__ void seq_units(const PagedAttnParams& p, int b, bool 
     }
     w.b = b;
     w.n = n;
-    w.first = p.starts ? min(p.starts[b], n) : p.window > 0 ? max(0, n - p.window) : 0;
+    w.first = 0;
+    if (p.window != 0) w.first = p.window > 0 ? max(0, n - p.window) : min(p.starts[b], n);
     w.lo = w.first / UK;
     w.units = n > w.first ? (n + UK - 1) / UK - w.lo : 0;
 }

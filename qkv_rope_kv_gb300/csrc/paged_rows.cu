@@ -26,11 +26,48 @@ struct Shape {
 __device__ __forceinline__ float get(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float get(const __half* p) { return __half2float(__ldg(p)); }
 
-// One block of K or V into shared memory; slots that are not there, and columns behind hd, are zeros.
+// A block of K or V on its way to shared memory: all 16-byte pieces of a thread in flight together.  Slots that are not
+// there, and columns behind hd, are zeros.
 template <typename KT, int HDP>
-__device__ __forceinline__ void load_block(const PagedRowsParams& p, const void* pool, const int64_t* row_s, float* to) {
+struct Block {
+    static constexpr int kPer = 16 / sizeof(KT);                          // values of a piece
+    static constexpr int kPieces = kBlock * HDP / (kPer * kThreads);      // of a thread
+    static constexpr int kBatch = kPieces > 8 ? 8 : kPieces;
+    uint4 v[kBatch];
+    __device__ __forceinline__ void load(const PagedRowsParams& p, const void* pool, const int64_t* row_s, int from) {
+        const KT* src = static_cast<const KT*>(pool);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int e = threadIdx.x + (from + k) * kThreads, r = e / (HDP / kPer), d = e % (HDP / kPer) * kPer;
+            const int64_t at = row_s[r];
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (at >= 0 && d < p.hd) v[k] = __ldg(reinterpret_cast<const uint4*>(src + at + d));
+        }
+    }
+    __device__ __forceinline__ void store(float* to, int from) const {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int e = threadIdx.x + (from + k) * kThreads, r = e / (HDP / kPer), d = e % (HDP / kPer) * kPer;
+            float4* dst = reinterpret_cast<float4*>(to + r * Shape<HDP>::kStride + d);
+            if constexpr (kPer == 4) {
+                *dst = *reinterpret_cast<const float4*>(&v[k]);
+            } else {
+                const __half2* h = reinterpret_cast<const __half2*>(&v[k]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 x = __half22float2(h[2 * i]), y = __half22float2(h[2 * i + 1]);
+                    dst[i] = make_float4(x.x, x.y, y.x, y.y);
+                }
+            }
+        }
+    }
+};
+
+// The same for rows that 16-byte loads cannot read (hd or addresses).
+template <typename KT, int HDP>
+__device__ __forceinline__ void load_any(const PagedRowsParams& p, const void* pool, const int64_t* row_s, float* to) {
     const KT* src = static_cast<const KT*>(pool);
-#pragma unroll 4
+#pragma unroll 8
     for (int e = threadIdx.x; e < kBlock * HDP; e += kThreads) {
         const int r = e / HDP, d = e % HDP;
         const int64_t at = row_s[r];
@@ -48,16 +85,21 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, G = p.nh / p.nkv;
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.c.k) | reinterpret_cast<uintptr_t>(p.c.v) |
+                       static_cast<uintptr_t>(p.c.page_stride * sizeof(KT)) | static_cast<uintptr_t>(p.hd * sizeof(KT))) & 15u) == 0;
+    const bool q_vec = ((reinterpret_cast<uintptr_t>(p.q) | static_cast<uintptr_t>(p.q_stride * 4) | static_cast<uintptr_t>(p.hd * 4)) & 15u) == 0;
+    using B = Block<KT, HDP>;
+    constexpr bool kAhead = B::kPieces <= 4;  // there are registers for it
     Walk w;
     if (!w.begin(p)) return;
     if (tid == 0) note_none(p);
-    Piece x;
-    while (w.next(p, x)) {
-        const RowTile& t = x.t;
-        const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
+    Piece piece;
+    while (w.next(p, piece)) {
+        const RowTile& t = piece.t;
+        const int kv = piece.head / p.blocks, g0 = (piece.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
         const int rows = t.ntok * p.per_block;
         __syncthreads();  // the last piece's rows have been read
-        if (tid == 0) note_piece(p, w, x);
+        if (tid == 0) note_piece(p, w, piece);
         if (tid < kRows) {
             int lo = 0, hi = 0;
             if (tid < rows) row_span(p, t, tid / p.per_block, lo, hi);
@@ -65,12 +107,17 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
             hi_s[tid] = hi;
         }
         const float scale = p.scale * kLog2e;
-        for (int e = tid; e < kRows * HDP; e += kThreads) {
-            const int r = e / HDP, d = e % HDP, i = r / p.per_block, g = r - i * p.per_block;
-            q_s[r * S::kStride + d] =
-                r < rows && g < heads && d < p.hd
-                    ? __ldcg(p.q + (t.row0 + i) * p.q_stride + static_cast<int64_t>(kv * G + g0 + g) * p.hd + d) * scale
-                    : 0.f;
+#pragma unroll 4
+        for (int e = tid; e < kRows * HDP / 4; e += kThreads) {
+            const int r = e / (HDP / 4), d = e % (HDP / 4) * 4, i = r / p.per_block, g = r - i * p.per_block;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows && g < heads && d < p.hd) {
+                const float* src = p.q + (t.row0 + i) * p.q_stride + static_cast<int64_t>(kv * G + g0 + g) * p.hd + d;
+                if (q_vec) y = __ldcg(reinterpret_cast<const float4*>(src));
+                else y = make_float4(__ldcg(src), d + 1 < p.hd ? __ldcg(src + 1) : 0.f, d + 2 < p.hd ? __ldcg(src + 2) : 0.f,
+                                     d + 3 < p.hd ? __ldcg(src + 3) : 0.f);
+            }
+            *reinterpret_cast<float4*>(q_s + r * S::kStride + d) = make_float4(y.x * scale, y.y * scale, y.z * scale, y.w * scale);
         }
         float m[4], l[4];
         float4 o[4][S::kCols];
@@ -81,14 +128,24 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
 #pragma unroll
             for (int c = 0; c < S::kCols; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        for (int u = x.from; u < x.to; ++u) {
+        for (int u = piece.from; u < piece.to; ++u) {
             const int j0 = t.lo + u * kBlock;
             if (tid < kBlock) {
                 const int64_t row = j0 + tid < t.hi ? row_offset(p.c, t.seq, j0 + tid) : -1;
                 row_s[tid] = row < 0 ? -1 : row + static_cast<int64_t>(kv) * p.hd;
             }
             __syncthreads();
-            load_block<KT, HDP>(p, p.c.k, row_s, kv_s);
+            B x;
+            if (vec) {
+#pragma unroll
+                for (int k = 0; k < B::kPieces; k += B::kBatch) {
+                    x.load(p, p.c.k, row_s, k);
+                    x.store(kv_s, k);
+                }
+                if (kAhead) x.load(p, p.c.v, row_s, 0);  // V is on its way while the scores are made
+            } else {
+                load_any<KT, HDP>(p, p.c.k, row_s, kv_s);
+            }
             __syncthreads();
             float s[4][4] = {};
 #pragma unroll 4
@@ -135,7 +192,15 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
                 }
             }
             __syncthreads();
-            load_block<KT, HDP>(p, p.c.v, row_s, kv_s);
+            if (vec) {
+#pragma unroll
+                for (int k = 0; k < B::kPieces; k += B::kBatch) {
+                    if (!kAhead) x.load(p, p.c.v, row_s, k);
+                    x.store(kv_s, k);
+                }
+            } else {
+                load_any<KT, HDP>(p, p.c.v, row_s, kv_s);
+            }
             __syncthreads();
 #pragma unroll 2
             for (int j = 0; j < kBlock; j += 4) {
@@ -165,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
             const int r = ty + 16 * i;
             const int row = t.row0 + r / p.per_block, g = r % p.per_block, h = kv * G + g0 + g;
             if (r >= rows || g >= heads) continue;
-            if (x.whole()) {
+            if (piece.whole()) {
                 const bool empty = lo_s[r] >= hi_s[r];
                 const float inv = empty ? 0.f : 1.f / l[i];
                 const int64_t at = p.first ? row * p.out_stride + static_cast<int64_t>(h) * p.hd
@@ -185,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
                 float* lse = p.first ? p.lse : p.prefix_lse;
                 if (tx == 0 && lse) lse[static_cast<int64_t>(row) * p.nh + h] = lse_of(m[i], l[i], empty);
             } else {
-                float* part = part_of(p, blockIdx.x, x.first);
+                float* part = part_of(p, blockIdx.x, piece.first);
                 float* to = part_o(p, part, r);
                 if (tx == 0) *part_ml(part, r) = make_float2(m[i], l[i]);
 #pragma unroll

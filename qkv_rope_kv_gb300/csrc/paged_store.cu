@@ -133,16 +133,20 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
     __shared__ Tokens tk;
     qkv_ptx::griddep_wait();
     qkv_ptx::griddep_launch_dependents();
-    const int rot = r.rot(p);
+    const int half = p.hd >> 1, rot = r.rot(p);
     const int t0 = blockIdx.x * T, nt = min(T, p.nt - t0);
     const int end = min(p.nh + 2 * p.nkv, static_cast<int>(blockIdx.y + 1) * heads_per_cta);
     const int groups = kThreads / lp, g = threadIdx.x / lp, l = threadIdx.x % lp;
     int h = blockIdx.y * heads_per_cta + g;
-    const bool wide = 8 * l < p.hd;  // a lane that has values
-    const bool turned = 8 * l < rot;
-    int d0 = 4 * l, d1 = rot / 2 + 4 * l;  // its two quads
-    if (F != kPlan) lane_quads<F == kNeighbours>(l, rot, d0, d1);
-    const int apart = d1 - d0;
+    // a lane's two quads, and whether it has any
+    int d0 = 4 * l, apart = half;
+    bool wide = d0 < half;
+    if constexpr (F != kPlan) {
+        int d1;
+        lane_quads<F == kNeighbours>(l, rot, d0, d1);
+        apart = d1 - d0;
+        wide = 8 * l < p.hd;
+    }
     const YT* y = static_cast<const YT*>(p.y) + t0 * p.y_stride + static_cast<int64_t>(h) * p.hd + d0;
     Raw4<YT> n0[T], n1[T];
 #pragma unroll
@@ -169,11 +173,11 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
         Quad b0 = {0, 0}, b1 = {0, 0}, w0 = {0, 0}, w1 = {0, 0};
         if (live && p.bias) {
             b0 = quad(p.bias + static_cast<int64_t>(h) * p.hd + d0);
-            b1 = quad(p.bias + static_cast<int64_t>(h) * p.hd + d1);
+            b1 = quad(p.bias + static_cast<int64_t>(h) * p.hd + apart + d0);
         }
         if (live && norm && sec != 2) {
             w0 = quad(p.norm_w[sec] + d0);
-            w1 = quad(p.norm_w[sec] + d1);
+            w1 = quad(p.norm_w[sec] + apart + d0);
         }
         y += static_cast<int64_t>(groups) * p.hd;
         float* q = p.q + t0 * p.q_stride + j;
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_store_kernel(const __grid_c
                 }
             }
             if (!live || !here[t]) continue;
-            if (sec != 2 && (F == kPlan || turned)) {
+            if (sec != 2 && (F == kPlan || 8 * l < rot)) {
                 const Quad c = quad(cos_s[t] + 4 * l), s = quad(sin_s[t] + 4 * l);
                 if (F == kNeighbours) {
                     rotate_neighbours(x0, x1, c, s);

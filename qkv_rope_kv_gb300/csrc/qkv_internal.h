@@ -157,8 +157,7 @@ struct PagedAttnParams {
     int64_t q_stride;
     const int32_t* lens;
     float scale;
-    int32_t window;
-    const int32_t* starts;   // [n_seq] or null: the first slot of each, >= 0 (then no window and no weights)
+    int32_t window;          // -1: each sequence's first slot is in starts (and no weights)
     void* out;
     int32_t out_bf16;
     int64_t out_stride;
@@ -170,6 +169,7 @@ struct PagedAttnParams {
     float* scores;           // [n_seq x nh x score_stride], log2 domain (add_weight)
     int64_t score_stride;    // the capacity, rounded up to whole units (32)
     int32_t nh, nkv, hd, kv_f16;
+    const int32_t* starts;   // [n_seq], >= 0
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t stream);
 // The main kernel's grid for these sizes (and pointers' alignment): CTAs, and CTAs of a cluster.
