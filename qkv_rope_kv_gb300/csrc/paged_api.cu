@@ -294,6 +294,7 @@ void rows_workspace(const RowsLayout& l, char* ws, PagedRowsParams* p) {
     p->part_tokens = l.part_tokens;
     p->tile_tokens = l.tile_tokens;
     p->tile_cost = l.shape.tile_cost;
+    p->min_share = l.shape.min_share;
     p->max_tiles = l.max_tiles;
     p->q_high = reinterpret_cast<uint16_t*>(ws + l.q_high);
     p->q_low = reinterpret_cast<uint16_t*>(ws + l.q_low);

@@ -281,7 +281,7 @@ cudaError_t launch_any(const PagedRowsParams& p, cudaStream_t stream) {
 }  // namespace
 
 RowsShape paged_rows_any_shape(const PagedRowsParams& p) {
-    return {kRows, kRows, kBlock, kSms * (p.hd <= 128 ? Shape<128>::kCtas : Shape<256>::kCtas), 1, false};
+    return {kRows, kRows, kBlock, kSms * (p.hd <= 128 ? Shape<128>::kCtas : Shape<256>::kCtas), 1, 1, false};
 }
 
 // f16 rows that 16-byte copies can read, of whole steps of 16 columns that fit tensor memory beside the scores.

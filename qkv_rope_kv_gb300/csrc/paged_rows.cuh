@@ -12,11 +12,10 @@ using namespace qkv_paged;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMinUnits = 3;  // of a CTA's share: a part costs its write and its join
 
-__device__ __forceinline__ int64_t share_of(int64_t total, int ctas) {
+__device__ __forceinline__ int64_t share_of(const PagedRowsParams& p, int64_t total, int ctas) {
     const int64_t even = (total + ctas - 1) / ctas;
-    return even > kMinUnits ? even : kMinUnits;
+    return even > p.min_share ? even : p.min_share;
 }
 
 // Some units [from, to) of one tile, and the first q head.
@@ -47,7 +46,7 @@ struct Walk {
         per_head = __ldcg(p.total);
         tiles = static_cast<int>(__ldcg(p.total + 1));
         const int64_t total = per_head * p.nkv * p.blocks;
-        share = share_of(total, gridDim.x);
+        share = share_of(p, total, gridDim.x);
         at = share * blockIdx.x;
         end = min(total, at + share);
         if (at >= end) return false;

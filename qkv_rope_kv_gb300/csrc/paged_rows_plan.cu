@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_
     griddep_wait();
     griddep_launch_dependents();
     const RowPiece* s = p.pieces + blockIdx.x;
-    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = share_of(total, ctas);
+    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = share_of(p, total, ctas);
     const int4 x = __ldcg(reinterpret_cast<const int4*>(s)), y = __ldcg(reinterpret_cast<const int4*>(s) + 1);
     if (share * blockIdx.x >= total || y.x == 0) return;  // (what was loaded is none)
     const int64_t start = static_cast<uint32_t>(x.x) | static_cast<int64_t>(x.y) << 32;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
     for (int k = 0; k < kQuads; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (prefix) {
         const RowTile t = load_tile(p, tile);
-        const int64_t share = share_of(per_head * p.nkv * p.blocks, ctas);
+        const int64_t share = share_of(p, per_head * p.nkv * p.blocks, ctas);
         const int blk = (h - kv * G) / p.per_block;
         const int64_t start = (static_cast<int64_t>(kv) * p.blocks + blk) * per_head + t.start;
         const int c0 = static_cast<int>(start / share), c1 = static_cast<int>((start + t.units - 1) / share);

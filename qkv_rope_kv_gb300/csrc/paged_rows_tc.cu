@@ -41,7 +41,8 @@ constexpr unsigned int kFlagTimeout = 2u;
 constexpr int kControlBytes = 2560;  // barriers and small tables, behind the chunks
 // Weights are kept times 2^kShift; the maximum moves where 64 of a row are together above kMostWeight.
 constexpr float kShift = 6.f, kMostWeight = 32768.f;
-constexpr int kTileCost = 2;  // units that a tile's beginning and end take
+constexpr int kTileCost = 3;  // units that a tile's beginning and end take
+constexpr int kMinShare = 3;  // of a CTA: a part costs its write and its join
 constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
 
 template <bool SPLIT, int NCH, bool NARROW>  // NCH chunks of 64 columns a head
@@ -1021,7 +1022,7 @@ cudaError_t launch_n(const PagedRowsParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-RowsShape paged_rows_tc_shape(bool narrow) { return {narrow ? kHalf : 2 * kHalf, kHalf, kBlock, kSms, kTileCost, true}; }
+RowsShape paged_rows_tc_shape(bool narrow) { return {narrow ? kHalf : 2 * kHalf, kHalf, kBlock, kSms, kTileCost, kMinShare, true}; }
 
 cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream) {
     if (p.out_bf16) return p.hd <= 64 ? launch_n<false, 1>(p, stream) : launch_n<false, 2>(p, stream);
