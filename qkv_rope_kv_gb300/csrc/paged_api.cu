@@ -371,6 +371,7 @@ extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged
     REQUIRE(a->d_first && a->d_lens, "d_first or d_lens is null");
     REQUIRE(aligned(a->d_first, 4) && aligned(a->d_lens, 4), "a pointer is not aligned to its elements");
     rows_params(plan, cache, a->nt, false, &p);
+    p.out_bf16 = a->out_dtype == QKV_BF16;
     const RowsLayout l = rows_layout(p, cache, 0);
     REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
     REQUIRE(a->workspace_bytes >= l.bytes, "the workspace has %zu bytes, %zu are needed", a->workspace_bytes, l.bytes);
@@ -382,7 +383,6 @@ extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged
     p.scale = a->scale;
     p.window = a->window;
     p.out = a->out;
-    p.out_bf16 = a->out_dtype == QKV_BF16;
     p.out_stride = a->out_stride;
     p.lse = a->lse;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -418,6 +418,7 @@ extern "C" qkv_status qkv_prefix_attn_step(const qkv_plan* plan, const qkv_paged
     REQUIRE(aligned(a->d_lens, 4) && aligned(a->d_share, 4) && aligned(a->d_prefix_len, 4),
             "a pointer is not aligned to its elements");
     rows_params(plan, cache, cache->n_seq, true, &p);
+    p.out_bf16 = a->out_dtype == QKV_BF16;
     const AttnLayout al = attn_layout(plan, cache, false);
     const RowsLayout l = rows_layout(p, cache, al.total);
     REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
@@ -431,7 +432,6 @@ extern "C" qkv_status qkv_prefix_attn_step(const qkv_plan* plan, const qkv_paged
     p.prefix_len = a->d_prefix_len;
     p.scale = a->scale;
     p.out = a->out;
-    p.out_bf16 = a->out_dtype == QKV_BF16;
     p.out_stride = a->out_stride;
     p.lse = a->lse;
     // the rows' own slots: the attention of one new token each, from where the prefix ends

@@ -293,9 +293,10 @@ bool paged_rows_on_tensor_cores(const PagedRowsParams& p) {
 
 RowsShape paged_rows_shape(const PagedRowsParams& p) {
     if (!paged_rows_on_tensor_cores(p)) return paged_rows_any_shape(p);
-    // Narrow tiles where a sequence (all, of a prefix) has no more rows for a kv head than those hold, on average.
+    // Narrow tiles for out F32 (whose kernel has no others), and where a sequence (all, of a prefix) has no more rows for a
+    // kv head than those hold, on average.
     const int64_t rows = static_cast<int64_t>(p.nt) * (p.nh / p.nkv);
-    return paged_rows_tc_shape(rows <= static_cast<int64_t>(paged_rows_tc_shape(true).rows) * (p.prefix ? 1 : p.c.n_seq));
+    return paged_rows_tc_shape(!p.out_bf16 || rows <= static_cast<int64_t>(paged_rows_tc_shape(true).rows) * (p.prefix ? 1 : p.c.n_seq));
 }
 
 cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream) {

@@ -39,8 +39,10 @@ static_assert(2 * 128 * (kFewRegs + kManyRegs) <= kThreads * kLaunchRegs, "regis
 constexpr int kChunkBytes = kBlock * 128;  // 128 slots (or q rows) x 64 columns
 constexpr unsigned int kFlagTimeout = 2u;
 constexpr int kControlBytes = 2560;  // barriers and small tables, behind the chunks
-// Weights are kept times 2^kShift; the maximum moves where 64 of a row are together above kMostWeight.
-constexpr float kShift = 6.f, kMostWeight = 32768.f;
+// Weights are kept times 2^kShift; the maximum moves where 64 of a row are together above kMostWeight (64 times the
+// largest are not).
+constexpr float kMostWeight = 60000.f;
+constexpr int kFold = 2;       // SPLIT: blocks that are summed in one accumulator before it is added to the others' sum
 constexpr int kTileCost = 3;  // units that a tile's beginning and end take
 constexpr int kMinShare = 3;  // of a CTA: a part costs its write and its join
 constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
@@ -53,6 +55,7 @@ struct Shape {
     // Copies in flight ahead of the one that is waited for (cp.async).  The MMAs free a block's V only after the next
     // block's K is there, so that many chunks must fit behind those in flight.
     static constexpr int kLag = kStages - 2 * NCH > 5 ? 5 : kStages - 2 * NCH;
+    static constexpr float kShift = SPLIT ? 9.f : 6.f;  // SPLIT: remainders of weights 2^-10 of the largest keep 23 bits
     static constexpr int kControlAt = (kQChunks + kStages) * kChunkBytes, kSmem = kControlAt + kControlBytes;
     static_assert(kSmem <= 227 * 1024 && kStages % 2 == 0 && kStages % NCH == 0, "shared memory");
 };
@@ -208,6 +211,19 @@ __device__ __forceinline__ u64 add2(u64 x, u64 y) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
+__device__ __forceinline__ u64 mul2(u64 x, u64 y) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ void scale16(uint32_t at, float by) {
+    uint32_t o[16];
+    tm_ld16(at, o);
+    tc_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+    tm_st16(at, o);
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -241,9 +257,11 @@ __device__ __noinline__ float plain_score(const PagedRowsParams& p, const float*
 
 // What the infinities and NaN of V that a row sees, in slots [lo, hi), make of its result.  The products do not tell: a
 // weight of zero (of a slot that the row does not see; or rounded, or a remainder) times them is NaN.  So blocks with
-// slots that only some rows see get zeros in their place, and rows that come out infinite or NaN look here.
-__device__ __noinline__ void fix_row(const PagedRowsParams& p, int seq, int kv, int lo, int hi, char* to, int es) {
+// slots that only some rows see get zeros in their place, and rows that come out infinite or NaN look here.  side: the
+// columns of every other 16 (-1: all).
+__device__ __noinline__ void fix_row(const PagedRowsParams& p, int seq, int kv, int lo, int hi, int side, char* to, int es) {
     for (int d = 0; d < p.hd; ++d) {
+        if (side >= 0 && ((d >> 4) & 1) != side) continue;
         float more = 0.f;
         for (int s = lo; s < hi; ++s) {
             const int64_t row = row_offset(p.c, seq, s);
@@ -271,12 +289,23 @@ __device__ __forceinline__ void store16(char* to, uint4 v, int es) {
     else store_any(to, v, es);
 }
 
+// Whether `yes` holds in any lane of the two softmax warps that have the same rows; they meet here.
+__device__ __forceinline__ bool pair_any(int quarter, bool yes) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(static_cast<uint32_t>(yes)), "r"(1 + quarter) : "memory");
+    return any != 0;
+}
+
 struct Control {
     uint64_t landed[kMaxStages], full[kMaxStages], empty[kMaxStages];
-    uint64_t q_ready[2], q_free[2], s_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], joined, drained;
+    uint64_t q_ready[2], q_free[2], s_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], joined, pv_done, o_free, drained;
     uint32_t live[kLiveRing][4];   // slots of a block that are there
     uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
-    float2 ml[kHalf];              // NARROW: maxima and sums of the second stream
+    union {
+        float2 ml[kHalf];      // NARROW: maxima and sums of the second stream
+        float top[2][kHalf];   // SPLIT: of the rows, by side
+    };
     uint32_t tmem;
 };
 static_assert(sizeof(Control) <= kControlBytes, "control");
@@ -304,6 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_ql, int box) {
     using S = Shape<SPLIT, NCH, NARROW>;
+    static_assert(!SPLIT || NARROW, "one stream");
+    constexpr float kShift = S::kShift;
     extern __shared__ __align__(1024) unsigned char smem[];  // atoms of the swizzle: no other shared memory before it
     Control& ctl = *reinterpret_cast<Control*>(smem + S::kControlAt);
     const uint32_t q_at = smem_u32(smem), ring_at = q_at + S::kQChunks * kChunkBytes;
@@ -328,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&ctl.q_ready[t], 1);
-            mbar_init(&ctl.q_free[t], 4);
+            mbar_init(&ctl.q_free[t], SPLIT ? 8 : 4);
             mbar_init(&ctl.s_full[t], 1);
             mbar_init(&ctl.p_half[t], 4);
             mbar_init(&ctl.half_done[t], 1);
@@ -336,6 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.o_full[t], 1);
         }
         mbar_init(&ctl.joined, 4);
+        mbar_init(&ctl.pv_done, 1);
+        mbar_init(&ctl.o_free, 8);
         mbar_init(&ctl.drained, 1);
         mbar_fence_init();
     }
@@ -356,6 +389,256 @@ __global__ void __launch_bounds__(kThreads, 1)
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     }
     if (work && warp < kSoftWarps) {
+      if constexpr (SPLIT) {
+        // ---- softmax, SPLIT: thread `lane` of warp w has row 32 (w % 4) + lane and columns 64 (w / 4) .. + 63 of every block; the
+        // warps of a pair, w and w + 4, have the same rows
+        const int quarter = warp & 3, side = warp >> 2;
+        const uint32_t lanes_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16), o_at = lanes_at + 256, sum_at = lanes_at + 384;
+        uint32_t s_phase = 0;  // bit t
+        int piece = 0, block0 = 0;
+        bool ok = true;
+        // Block number `block`'s weights are in O.
+        auto wait_pv = [&](int block) {
+            const bool there = __all_sync(0xffffffffu, wait_for(&ctl.pv_done, block & 1));
+            tc_fence_after();
+            return there;
+        };
+        while (ok && w.next(p, x)) {
+            const RowTile& tile = x.t;
+            const int kv = x.head / p.blocks, g0 = (x.head - kv * p.blocks) * p.per_block, heads = min(p.per_block, G - g0);
+            const int first_block = block0, n = x.to - x.from;
+            block0 += n;
+            ++piece;
+            if (tid == 0) note_piece(p, w, x);
+            const int r = 32 * quarter + lane, i = r / p.per_block, g = r - i * p.per_block;
+            const int h_row = kv * G + g0 + g;
+            const int64_t row = tile.row0 + i;
+            const bool mine = i < tile.ntok && g < heads, busy = 32 * quarter < tile.ntok * p.per_block;
+            const float unscale = mine ? __ldcg(p.q_unscale + row * p.nh + h_row) : 1.f;
+            int see_lo = 0, see_hi = 0;
+            if (mine) row_span(p, tile, i, see_lo, see_hi);
+            float m = -CUDART_INF_F, l = 0.f;  // l: of this side's columns
+#pragma unroll 1
+            for (int b = 0; b < n; ++b) {
+                const int t = b & 1;
+                ok = __all_sync(0xffffffffu, wait_for(&ctl.s_full[t], (s_phase >> t) & 1)) && ok;
+                s_phase ^= 1u << t;
+                tc_fence_after();
+                if (busy) {
+                    const uint32_t at = lanes_at + 128 * t + 64 * side;
+                    const int j0 = tile.lo + (x.from + b) * kBlock;
+                    const uint32_t* live = ctl.live[(first_block + b) % kLiveRing];
+                    const bool mixed = j0 < tile.all_lo || j0 + kBlock > tile.all_hi ||
+                                       (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
+                    // the slots of columns 32 c .. 32 c + 31 that the row sees
+                    auto seen = [&](int c) {
+                        const int a = see_lo - j0 - 32 * c, e = see_hi - j0 - 32 * c;
+                        const uint32_t below = e >= 32 ? 0xffffffffu : e <= 0 ? 0u : (1u << e) - 1u;
+                        const uint32_t from = a <= 0 ? 0xffffffffu : a >= 32 ? 0u : 0xffffffffu << a;
+                        return below & from & live[c];
+                    };
+                    uint32_t v[2][32];
+                    tm_ld32(at, v[0]);
+                    tm_ld32(at + 32, v[1]);
+                    tc_wait_ld();
+                    float total;
+                    // The weights are made with the maximum as it was.  Their sum tells whether that will do (none is then above
+                    // f16's largest): the maximum itself is looked for only at first and where the sum has grown, by both
+                    // warps of the pair.  Rows that are none (what is in q's place there varies) have no say.
+#pragma unroll 1
+                    for (int round = 0;; ++round) {
+                        if (mixed) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t in = seen(2 * side + c);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!((in >> k) & 1u)) v[c][k] = 0xff800000u;
+                            }
+                        }
+                        // 2^(s - m) first: its argument is small where it counts, and so is its rounding
+                        const float base = m == -CUDART_INF_F ? 0.f : m;
+                        const u64 by = pack2(unscale, unscale), minus = pack2(-base, -base);
+                        constexpr float kTimes = 512.f;  // 2^kShift
+                        const u64 up = pack2(kTimes, kTimes);
+                        u64 sum[2] = {0, 0};
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t h[16], low[16];
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 y =
+                                    unpack2(fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), by, minus));
+                                const u64 e = mul2(pack2(ex2(y.x), ex2(y.y)), up);
+                                sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], e);
+                                const float2 f = unpack2(e);
+                                split2(f.x, f.y, h[k / 2], low[k / 2]);
+                            }
+                            tm_st16(at + 32 * c, h);
+                            tm_st16(at + 32 * c + 16, low);
+                        }
+                        const float2 s2 = unpack2(add2(sum[0], sum[1]));
+                        total = s2.x + s2.y;
+                        if (round == 2 || !pair_any(quarter, !ok || (mine && (m == -CUDART_INF_F || !(total <= kMostWeight))))) break;
+                        if (pair_any(quarter, !ok)) {  // a wait ran out: both leave
+                            ok = false;
+                            break;
+                        }
+                        if (round == 0) {
+                            const bool odd = __any_sync(0xffffffffu, mine && total != total);
+                            if (odd) {  // K with infinities or NaN: scores from memory, in the place of those that are NaN
+                                const float* q_row = p.q + row * p.q_stride + static_cast<int64_t>(h_row) * p.hd;
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) tm_st32(at + 32 * c, v[c]);
+                                tc_wait_st();
+#pragma unroll 1
+                                for (int k = 0; k < 64; ++k) {
+                                    float f = __uint_as_float(tm_ld1(at + k));
+                                    if (mine && f != f && ((seen(2 * side + (k >> 5)) >> (k & 31)) & 1u))
+                                        f = plain_score(p, q_row, tile.seq, j0 + 64 * side + k, kv) / unscale;
+                                    __syncwarp();
+                                    tm_st1(at + k, __float_as_uint(f));
+                                }
+                                tc_wait_st();
+                                tm_ld32(at, v[0]);
+                                tm_ld32(at + 32, v[1]);
+                                tc_wait_ld();
+                            }
+                            if (pair_any(quarter, odd)) continue;
+                        }
+                        float tops[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                tops[c] = max3(tops[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
+                        const float top = fmaxf(tops[0], tops[1]) * unscale;
+                        ctl.top[side][r] = top;
+                        pair_any(quarter, false);
+                        const float next = mine ? fmaxf(m, fmaxf(top, ctl.top[side ^ 1][r])) : m;
+                        const float keep = m == next ? 1.f : ex2(m - next);
+                        m = next;
+                        l *= keep;
+                        if (b > 0) {
+                            ok = wait_pv(first_block + b - 1) && ok;  // the weights before these are in O
+#pragma unroll 1
+                            for (int c = 16 * side; c < p.hd; c += 32) {
+                                scale16(o_at + c, keep);
+                                if (b > kFold) scale16(sum_at + c, keep);
+                            }
+                        }
+                        tc_wait_st();
+                        tc_fence_before();
+                        pair_any(quarter, false);  // all of O is as it is to be before either side's weights go into it
+                        round = 1;                 // the next one is the last
+                    }
+                    l += total;
+                    tc_wait_st();
+                }
+                if (!ok) break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(side ? &ctl.p_ready[t] : &ctl.p_half[t]);
+                // The tensor cores cut bits off every sum, always towards zero: 5e-6 of 4096 slots' sums in one accumulator
+                // were lost.  So the sums of kFold blocks are added to the others' here, rounded to nearest.
+                if (b > 0 && b % kFold == 0) {
+                    if (busy) {
+                        ok = wait_pv(first_block + b - 1);
+#pragma unroll 1
+                        for (int c = 16 * side; c < p.hd; c += 32) {
+                            uint32_t o[16], y[16];
+                            tm_ld16(o_at + c, o);
+                            if (b > kFold) tm_ld16(sum_at + c, y);
+                            tc_wait_ld();
+                            if (b > kFold) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(y[k]));
+                            }
+                            tm_st16(sum_at + c, o);
+                        }
+                        tc_wait_st();
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.o_free);
+                }
+            }
+            const bool there = ok && wait_pv(first_block + n - 1);
+            ok = !pair_any(quarter, !there);
+            if (!ok) break;
+            if (busy) {
+                const bool both = n > kFold;
+                ctl.top[side][r] = l;
+                pair_any(quarter, false);
+                l += ctl.top[side ^ 1][r];
+                const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
+                const bool whole = x.whole(), empty = see_lo >= see_hi;
+                const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
+                float* part = part_of(p, blockIdx.x, x.first);
+                float* to;
+                if (!whole) to = part_o(p, part, r);
+                else if (!p.first) to = p.prefix_out + (row * p.nh + h_row) * p.hd;
+                else to = static_cast<float*>(p.out) + row * p.out_stride + static_cast<int64_t>(h_row) * p.hd;
+                // through q's place, by rows of a warp; the sides take 16 columns in turn
+                constexpr int kRowBytes = 64;  // of 32 rows: a round's
+                const uint32_t stage = q_chunk(0, 0, 0) + warp * 32 * kRowBytes;
+                float odd = 0.f;
+#pragma unroll 1
+                for (int c = 16 * side; c < p.hd; c += 32) {
+                    uint32_t v[16], y[16];
+                    tm_ld16(o_at + c, v);
+                    if (both) tm_ld16(sum_at + c, y);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float o = __uint_as_float(v[k]);
+                        if (both) o += __uint_as_float(y[k]);
+                        o *= inv;
+                        odd = fmaf(o, 0.f, odd);
+                        v[k] = __float_as_uint(o);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * kRowBytes +
+                                                                                      ((k ^ ((lane >> 1) & 3)) << 4)),
+                                     "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                                     : "memory");
+                    __syncwarp();
+                    // four lanes a row
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        const int from = k + (lane >> 2);
+                        char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(to), from)) + 4 * c +
+                                    16 * (lane & 3);
+                        const bool has = __shfl_sync(0xffffffffu, mine, from);
+                        uint4 w4;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w)
+                                     : "r"(stage + from * kRowBytes + (((lane & 3) ^ ((from >> 1) & 3)) << 4))
+                                     : "memory");
+                        if (has) store16(dst, w4, 4);
+                    }
+                    __syncwarp();
+                }
+                if (__any_sync(0xffffffffu, mine && (poison || !(odd == 0.f)))) {
+                    if (mine)
+                        fix_row(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock), min(see_hi, tile.lo + x.to * kBlock), side,
+                                reinterpret_cast<char*>(to), 4);
+                    __syncwarp();
+                }
+                if (mine && side == 0) {
+                    float* lse = p.first ? p.lse : p.prefix_lse;
+                    if (!whole) *part_ml(part, r) = make_float2(m - kShift, l);
+                    else if (lse) lse[row * p.nh + h_row] = lse_of(m - kShift, l, empty);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.q_free[0]);
+        }
+        if (!ok && lane == 0) flag_bad(kFlagTimeout, 0);
+      } else {
         // ---- softmax: thread `lane` of warp w has row 32 (w % 4) + lane of stream w / 4
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t s_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 128 * t, o_at = s_at + 256;
@@ -424,41 +707,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             u64 sum[2] = {0, 0};
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                uint32_t h[16], low[16];
+                                uint32_t h[16];
 #pragma unroll
                                 for (int k = 0; k < 32; k += 2) {
                                     const float2 y =
                                         unpack2(fma2(pack2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), by, minus));
                                     const float a = ex2(y.x), b = ex2(y.y);
                                     sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
-                                    if (SPLIT) split2(a, b, h[k / 2], low[k / 2]);
-                                    else h[k / 2] = f16x2(a, b);
+                                    h[k / 2] = f16x2(a, b);
                                 }
                                 tm_st16(at + 32 * c, h);
-                                if (SPLIT) tm_st16(at + 32 * c + 16, low);
                             }
                             const float2 s2 = unpack2(add2(sum[0], sum[1]));
                             total = s2.x + s2.y;
                             if (round == 2 || !__any_sync(0xffffffffu, mine && (m == -CUDART_INF_F || !(total <= kMostWeight)))) break;
-                            if (SPLIT && round == 0 && __any_sync(0xffffffffu, mine && total != total)) {
-                                const float* q_row = p.q + row * p.q_stride + static_cast<int64_t>(h_row) * p.hd;
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) tm_st32(at + 32 * c, v[c]);
-                                tc_wait_st();
-#pragma unroll 1
-                                for (int k = 0; k < 64; ++k) {
-                                    float f = __uint_as_float(tm_ld1(at + k));
-                                    if (mine && f != f && ((seen(2 * half + (k >> 5)) >> (k & 31)) & 1u))
-                                        f = plain_score(p, q_row, tile.seq, j0 + 64 * half + k, kv) / unscale;
-                                    __syncwarp();
-                                    tm_st1(at + k, __float_as_uint(f));
-                                }
-                                tc_wait_st();
-                                tm_ld32(at, v[0]);
-                                tm_ld32(at + 32, v[1]);
-                                tc_wait_ld();
-                                continue;
-                            }
                             float tops[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                             for (int k = 0; k < 32; k += 2)
@@ -589,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (__any_sync(0xffffffffu, mine && (poison || !(odd == 0.f)))) {
                     if (mine)
-                        fix_row(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock), min(see_hi, tile.lo + x.to * kBlock), to, es);
+                        fix_row(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock), min(see_hi, tile.lo + x.to * kBlock), -1, to, es);
                     __syncwarp();
                 }
                 if (mine) {
@@ -604,13 +866,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&ctl.q_free[t]);
         }
         if (!ok && lane == 0) flag_bad(kFlagTimeout, 0);
+      }
     } else if (work && warp == kMmaWarp) {
         // ---- MMAs
         const int steps = p.hd / 16;
         const uint32_t id_s = idesc(kBlock, false), id_o = idesc(p.hd, true);
         // The next block's K and V: stages of their first chunks, and the phases that they wait for.
         uint32_t k_at = 0, k_phase = 0, v_at = NCH, v_phase = 0;
-        uint32_t q_phase = 0, h_phase = 0, p_phase = 0;  // bit t
+        uint32_t q_phase = 0, h_phase = 0, p_phase = 0, o_phase = 0;  // bit t
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t phase) {
             if (ok) ok = __all_sync(0xffffffffu, wait_for(bar, phase));
@@ -650,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // O of stream t: the first half of the slots as soon as their weights are there
         auto sums = [&](int t, uint32_t acc) {
-            const uint32_t v = ring_v + v_at * (kChunkBytes >> 4), o = tmem + 256 + 128 * t, w0 = tmem + 128 * t;
+            const uint32_t v = ring_v + v_at * (kChunkBytes >> 4), o = tmem + 256 + (SPLIT ? 0 : 128 * t), w0 = tmem + 128 * t;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (half == 0) {
@@ -668,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_ts(o, w0 + 32 * (k >> 1) + 16 * part + 8 * (k & 1), v + 128 * k, id_o, acc);
                         acc = 1;
                     }
-                if (half == 0) tc_commit(&ctl.half_done[t]);
+                if (!SPLIT && half == 0) tc_commit(&ctl.half_done[t]);
             }
         };
         while (ok && w.next(p, x)) {
@@ -686,12 +949,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < n && ok; ++b) {
                     const int t = b & 1;
                     wait_full(v_at, v_phase);
-                    if (ok) sums(t, b >= 2);
+                    if (SPLIT && b > 0 && b % kFold == 0) {  // the accumulator's sums have been added to the others
+                        wait(&ctl.o_free, o_phase);
+                        o_phase ^= 1u;
+                    }
+                    if (ok) sums(t, SPLIT ? b % kFold != 0 : b >= 2);
                     if (!ok) break;
+                    if (SPLIT) tc_commit(&ctl.pv_done);
                     release(v_at);
                     next_block(v_at, v_phase);
                     if (b + 2 >= n) {
-                        tc_commit(&ctl.o_full[t]);
+                        if (!SPLIT) tc_commit(&ctl.o_full[t]);
                         continue;
                     }
                     wait_full(k_at, k_phase);
@@ -1017,7 +1285,8 @@ cudaError_t launch_t(const PagedRowsParams& p, cudaStream_t stream) {
 
 template <bool SPLIT, int NCH>
 cudaError_t launch_n(const PagedRowsParams& p, cudaStream_t stream) {
-    return p.rows == kHalf ? launch_t<SPLIT, NCH, true>(p, stream) : launch_t<SPLIT, NCH, false>(p, stream);
+    if constexpr (SPLIT) return launch_t<SPLIT, NCH, true>(p, stream);
+    else return p.rows == kHalf ? launch_t<SPLIT, NCH, true>(p, stream) : launch_t<SPLIT, NCH, false>(p, stream);
 }
 
 }  // namespace
