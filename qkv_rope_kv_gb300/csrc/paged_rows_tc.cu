@@ -394,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warps of a pair, w and w + 4, have the same rows
         const int quarter = warp & 3, side = warp >> 2;
         const uint32_t lanes_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16), o_at = lanes_at + 256, sum_at = lanes_at + 384;
-        uint32_t s_phase = 0;  // bit t
+        uint32_t s_phase = 0, o_phase = 0;  // s_phase: bit t
         int piece = 0, block0 = 0;
         bool ok = true;
-        // Block number `block`'s weights are in O.
+        // Block number `block`'s weights are in O; those of the block before it are known to be.
         auto wait_pv = [&](int block) {
             const bool there = __all_sync(0xffffffffu, wait_for(&ctl.pv_done, block & 1));
             tc_fence_after();
@@ -414,7 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h_row = kv * G + g0 + g;
             const int64_t row = tile.row0 + i;
             const bool mine = i < tile.ntok && g < heads, busy = 32 * quarter < tile.ntok * p.per_block;
-            const float unscale = mine ? __ldcg(p.q_unscale + row * p.nh + h_row) : 1.f;
+            // The tensor cores cut bits off a score's sums too, each towards zero: 2^-23 of it are missing on average (128
+            // columns; log sum exp comes out 6e-7 too small), and given back here.
+            const float unscale = mine ? __ldcg(p.q_unscale + row * p.nh + h_row) * (1.f + 1.1920929e-7f) : 1.f;
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, i, see_lo, see_hi);
             float m = -CUDART_INF_F, l = 0.f;  // l: of this side's columns
@@ -563,9 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&ctl.o_free);
                 }
             }
-            const bool there = ok && wait_pv(first_block + n - 1);
+            // (not by pv_done, whose last phase but one may be under way or over: a barrier tells a phase only from the next)
+            const bool there = ok && __all_sync(0xffffffffu, wait_for(&ctl.o_full[0], o_phase));
+            o_phase ^= 1u;
             ok = !pair_any(quarter, !there);
             if (!ok) break;
+            tc_fence_after();
             if (busy) {
                 const bool both = n > kFold;
                 ctl.top[side][r] = l;
@@ -959,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     release(v_at);
                     next_block(v_at, v_phase);
                     if (b + 2 >= n) {
-                        if (!SPLIT) tc_commit(&ctl.o_full[t]);
+                        if (!SPLIT || b + 1 == n) tc_commit(&ctl.o_full[SPLIT ? 0 : t]);
                         continue;
                     }
                     wait_full(k_at, k_phase);

@@ -313,6 +313,89 @@ def test_prefix_equals_plain_decode(qkv):
     assert (np.abs(a.cpu().numpy() - b.cpu().numpy()) <= 2 * bo).all()
 
 
+# ---------------------------------------------------------------- many blocks for a CTA
+
+def attend64(q, K, V, hi, scale):
+    """q [rows, G, hd] f32 over K, V [n, hd] f16, row i up to hi[i]: out in 64 bits, and the bound of rows_reference.py
+    (with sum p |V| in the place of each column's)."""
+    import torch
+    s = torch.einsum("rgd,nd->rgn", q.double(), K.double()) * scale
+    s.masked_fill_(torch.arange(K.shape[0], device="cuda") >= hi[:, None, None], -float("inf"))
+    p = torch.softmax(s, -1)
+    size = torch.einsum("rgd,nd->rgn", q.double().abs(), K.double().abs()).amax(-1, keepdim=True) * scale
+    return torch.einsum("rgn,nd->rgd", p, V.double()), torch.einsum("rgn,nd->rgd", p, V.double().abs()), size
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("nh,nkv,hd,new,cached", [(32, 8, 128, 700, 3900), (16, 8, 64, 1500, 2000), (40, 8, 128, 3, 20000)])
+def test_long_prompts(qkv, nh, nkv, hd, new, cached, out):
+    """Pieces of tens of blocks, which sums of several accumulators and rescaled ones go through."""
+    import torch
+    torch.manual_seed(1)
+    n, page, G = new + cached, 64, nh // nkv
+    per = -(-n // page)
+    plan = make_plan(nh, nkv, hd, "f16")
+    k, v = (torch.randn(per, page, nkv * hd, device="cuda").half() for _ in range(2))
+    k.view(-1, nkv, hd)[cached // 2:] *= 1.5  # maxima move on the way
+    table = torch.randperm(per, device="cuda").int()[None].contiguous()
+    cache = Q.PagedKv(plan, k, v, table)
+    q = 2 * torch.randn(new, nh * hd, device="cuda")
+    o = torch.empty(new, nh * hd, device="cuda", dtype=torch.bfloat16 if out == "bf16" else torch.float32)
+    ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, new), dtype=torch.uint8, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    scale = hd ** -0.5
+    for _ in range(4):
+        o.fill_(float("nan"))
+        Q.qkv_prompt_attn_step(plan, cache, q, i32(0, new), i32(n), scale, o, ws)
+        K, V = (x[table[0].long()].view(-1, nkv, hd)[:n] for x in (k, v))
+        hi = torch.arange(cached + 1, n + 1, device="cuda")
+        for h in range(nkv):
+            want, most, size = attend64(q.view(new, nkv, G, hd)[:, h], K[:, h], V[:, h], hi, scale)
+            ds = (hd + 8) * 2 * ref.U * size + 2 * 4 * ref.U * size
+            rel = torch.expm1(2 * (ds + (2.0 ** -11 * size if out == "bf16" else 0))) + (n / 8 + 64) * 2 * ref.U
+            bound = rel * most
+            if out == "bf16":
+                bound = bound + 2.0 ** -11 * most + 2.0 ** -8 * (want.abs() + bound)
+            got = o.view(new, nkv, G, hd)[:, h].double()
+            assert ((got - want).abs() <= bound).all()
+            if out == "f32":  # sums of many values are not worse than those of f32 adds one by one: sqrt(n) u of them
+                assert (got - want).norm() <= (n ** 0.5 + hd ** 0.5 * size.max()) * ref.U * most.norm()
+    assert Q.qkv_check_device_error()[0] == 0
+
+
+def test_long_shared_prefix(qkv):
+    import torch
+    torch.manual_seed(2)
+    nh, nkv, hd, page, B, P = 28, 4, 128, 64, 60, 12800
+    G, per, own = nh // nkv, P // page, 3
+    plan = make_plan(nh, nkv, hd, "f16")
+    k, v = (torch.randn(per + B, page, nkv * hd, device="cuda").half() for _ in range(2))
+    table = torch.full((B, per + 1), -1, dtype=torch.int32, device="cuda")
+    table[0, :per] = torch.randperm(per, device="cuda").int()
+    table[:, per] = torch.arange(per, per + B, device="cuda").int()
+    cache = Q.PagedKv(plan, k, v, table)
+    ws = torch.zeros(Q.qkv_prefix_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+    q = 2 * torch.randn(B, nh * hd, device="cuda")
+    full = lambda x: torch.full((B,), x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for dtype in (torch.float32, torch.bfloat16):
+        for _ in range(4):
+            torch.zeros(1 << 28, device="cuda")  # caches hold something else: warps of a CTA run further apart
+            o = torch.full((B, nh * hd), float("nan"), device="cuda", dtype=dtype)
+            Q.qkv_prefix_attn_step(plan, cache, q, full(P + own), full(0), full(P), hd ** -0.5, o, ws)
+            for h in range(nkv):
+                Kp, Vp = (x[table[0, :per].long()].view(-1, nkv, hd)[:, h] for x in (k, v))
+                Ko, Vo = (x[per:].view(B, page, nkv, hd)[:, :own, h] for x in (k, v))
+                x = q.view(B, nkv, G, hd)[:, h]
+                s = torch.cat([torch.einsum("bgd,nd->bgn", x.double(), Kp.double()),
+                               torch.einsum("bgd,bnd->bgn", x.double(), Ko.double())], -1) * hd ** -0.5
+                p = torch.softmax(s, -1)
+                want = torch.einsum("bgn,nd->bgd", p[..., :P], Vp.double()) + torch.einsum("bgn,bnd->bgd", p[..., P:], Vo.double())
+                got = o.view(B, nkv, G, hd)[:, h].double()
+                # 2-norms: weights off by 2^-11 at random, and bf16's half step; f32 as in test_long_prompts
+                assert (got - want).norm() <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -18) * want.norm()
+    assert Q.qkv_check_device_error()[0] == 0
+
+
 # ---------------------------------------------------------------- as they are used
 
 def test_graphs_streams_and_shapes_share_a_workspace(qkv):
