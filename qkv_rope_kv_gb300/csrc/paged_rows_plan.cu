@@ -39,16 +39,24 @@ __device__ __forceinline__ T scan(T v, T& sum, T* warp_s) {
 __device__ __forceinline__ void convert_q(const PagedRowsParams& p) {
     constexpr int kAhead = 4;  // rows of a warp in flight
     const int lane = threadIdx.x & 31;
-    const int64_t rows = static_cast<int64_t>(p.nt) * p.nh, step = static_cast<int64_t>(gridDim.x - 1) * (kPlanThreads / 32);
+    const int64_t rows = static_cast<int64_t>(p.nt) * p.nh;
+    const int step = static_cast<int>(gridDim.x - 1) * (kPlanThreads / 32), step_tok = step / p.nh, step_head = step - step_tok * p.nh;
     const float by = fabsf(p.scale) * kLog2e;
     const bool quads = ((reinterpret_cast<uintptr_t>(p.q) | static_cast<uintptr_t>(p.q_stride * 4)) & 15u) == 0;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5); r0 < rows; r0 += kAhead * step) {
+    const int begin = static_cast<int>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5);
+    int tok = begin / p.nh, head = begin - tok * p.nh;  // (counted on: a division of 64 bits a row took as long as the copying)
+    for (int64_t r0 = begin; r0 < rows; r0 += static_cast<int64_t>(kAhead) * step) {
         float v[kAhead][4];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int64_t r = r0 + j * step;
-            const int tok = static_cast<int>(r / p.nh);
-            const float* q = p.q + tok * p.q_stride + (r - static_cast<int64_t>(tok) * p.nh) * p.hd + 4 * lane;
+            const int64_t r = r0 + static_cast<int64_t>(j) * step;
+            const float* q = p.q + tok * p.q_stride + head * p.hd + 4 * lane;
+            tok += step_tok;
+            head += step_head;
+            if (head >= p.nh) {
+                head -= p.nh;
+                ++tok;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[j][k] = 0.f;
             if (r < rows && 4 * lane < p.hd) {
@@ -63,7 +71,7 @@ __device__ __forceinline__ void convert_q(const PagedRowsParams& p) {
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int64_t r = r0 + j * step;
+            const int64_t r = r0 + static_cast<int64_t>(j) * step;
             if (r >= rows) break;
             float big = fmaxf(fmaxf(fabsf(v[j][0]), fabsf(v[j][1])), fmaxf(fabsf(v[j][2]), fabsf(v[j][3])));
             big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));  // not below zero
@@ -247,7 +255,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
 }
 
 constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32;
-constexpr int kQuads = QKV_MAX_HEAD_DIM / 128;  // of a lane's columns: four from 4 * lane, and from 128 + 4 * lane
+// Q quads of columns of a lane: four from 4 * lane, and for heads above 128 from 128 + 4 * lane.  With one, four CTAs fit on an
+// SM, and all of a call's run at once; as the kernel of both, whose two did not, joins of 36 MB took 34 us.
+static_assert(QKV_MAX_HEAD_DIM <= 256, "columns of a lane");
+constexpr int kJoinCtas = 4;
 
 // Columns [d, d + 4) of a row, as far as there are any.
 __device__ __forceinline__ float4 get4(const float* row, int d, int hd) {
@@ -289,31 +300,32 @@ __device__ __forceinline__ float4 fma4(float4 a, float k, float4 b) {
 }
 
 // The parts of a row, in the order of its slots, a few at a time, all of whose loads are in flight together.
+template <int Q>
 struct Joined {
     float m, l;
-    float4 o[kQuads];
+    float4 o[Q];
 };
+template <int Q>
 __device__ __forceinline__ void join_row(const PagedRowsParams& p, int64_t start, int64_t share, int c0, int parts, int row,
-                                         Joined& j) {
+                                         Joined<Q>& j) {
     constexpr int kAhead = 4;
     const int lane = threadIdx.x & 31;
     j.m = -CUDART_INF_F;
     j.l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < Q; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool first = start == share * c0;  // the tile is the first of its first CTA
 #pragma unroll 1
     for (int b = 0; b < parts; b += kAhead) {
         float2 ml[kAhead];
-        float4 o[kAhead][kQuads];
+        float4 o[kAhead][Q];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int c = min(b + i, parts - 1);
-            float* part = part_of(p, c0 + c, c > 0 || first);
+            if (b + i >= parts) continue;
+            float* part = part_of(p, c0 + b + i, b + i > 0 || first);
             ml[i] = __ldcg(part_ml(part, row));
 #pragma unroll
-            for (int k = 0; k < kQuads; ++k)
-                if (k == 0 || p.hd > 128) o[i][k] = get4(part_o(p, part, row), 128 * k + 4 * lane, p.hd);
+            for (int k = 0; k < Q; ++k) o[i][k] = get4(part_o(p, part, row), 128 * k + 4 * lane, p.hd);
         }
         float top = j.m;
 #pragma unroll
@@ -323,21 +335,21 @@ __device__ __forceinline__ void join_row(const PagedRowsParams& p, int64_t start
         j.m = top;
         j.l *= keep;
 #pragma unroll
-        for (int k = 0; k < kQuads; ++k) j.o[k] = fma4(j.o[k], keep, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int k = 0; k < Q; ++k) j.o[k] = fma4(j.o[k], keep, make_float4(0.f, 0.f, 0.f, 0.f));
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (b + i >= parts) continue;
             const float f = ml[i].x == top ? 1.f : exp2f(ml[i].x - top);
             j.l = fmaf(ml[i].y, f, j.l);
 #pragma unroll
-            for (int k = 0; k < kQuads; ++k)
-                if (k == 0 || p.hd > 128) j.o[k] = fma4(o[i][k], f, j.o[k]);
+            for (int k = 0; k < Q; ++k) j.o[k] = fma4(o[i][k], f, j.o[k]);
         }
     }
 }
 
 // Prompt: CTA x takes rows of the tile that CTA x of the attention began and others went on with; a warp a row.
-__global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_constant__ PagedRowsParams p, int ctas) {
+template <int Q>
+__global__ void __launch_bounds__(kJoinThreads, Q == 1 ? kJoinCtas : 2) join_prompt_kernel(const __grid_constant__ PagedRowsParams p, int ctas) {
     griddep_wait();
     griddep_launch_dependents();
     const RowPiece* s = p.pieces + blockIdx.x;
@@ -350,7 +362,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_
     const RowTile t = load_tile(p, x.z);
     for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < t.ntok * heads; r += gridDim.y * kJoinRows) {
         const int i = r / heads, g = r - i * heads, h = kv * G + g0 + g;
-        Joined j;
+        Joined<Q> j;
         join_row(p, start, share, blockIdx.x, parts, row_of(p, i, g), j);
         int lo, hi;
         row_span(p, t, i, lo, hi);
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_
         const int64_t at = (t.row0 + i) * p.out_stride + static_cast<int64_t>(h) * p.hd;
         const int d = 4 * (threadIdx.x & 31);
 #pragma unroll
-        for (int k = 0; k < kQuads; ++k) {
+        for (int k = 0; k < Q; ++k) {
             const float4 o = make_float4(j.o[k].x * inv, j.o[k].y * inv, j.o[k].z * inv, j.o[k].w * inv);
             put4(p, at, 128 * k + d, empty ? make_float4(0.f, 0.f, 0.f, 0.f) : o);
         }
@@ -368,7 +380,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_prompt_kernel(const __grid_
 }
 
 // Prefix: a warp for each sequence and q head joins the prefix's result, from parts or whole, and the own slots'.
-__global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_constant__ PagedRowsParams p, int ctas) {
+template <int Q>
+__global__ void __launch_bounds__(kJoinThreads, Q == 1 ? kJoinCtas : 2) join_prefix_kernel(const __grid_constant__ PagedRowsParams p, int ctas) {
     griddep_wait();
     griddep_launch_dependents();
     const int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 5);
@@ -380,14 +393,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
     const int seen = __ldcg(p.row_end + b), tile = __ldcg(p.row_tile + b);
     const int64_t per_head = __ldcg(p.total);
     const float own = __ldcg(p.own_lse + row);
-    float4 mine[kQuads];
+    float4 mine[Q];
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) mine[k] = get4(p.own_out + row * p.hd, 128 * k + d, p.hd);
+    for (int k = 0; k < Q; ++k) mine[k] = get4(p.own_out + row * p.hd, 128 * k + d, p.hd);
     const bool prefix = seen > 0;
     float theirs = -CUDART_INF_F;
-    Joined j;
+    Joined<Q> j;
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < Q; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (prefix) {
         const RowTile t = load_tile(p, tile);
         const int64_t share = share_of(p, per_head * p.nkv * p.blocks, ctas);
@@ -398,12 +411,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
             join_row(p, start, share, c0, c1 - c0 + 1, row_of(p, b - t.row0, h - kv * G - blk * p.per_block), j);
             const float inv = 1.f / j.l;
 #pragma unroll
-            for (int k = 0; k < kQuads; ++k) j.o[k] = fma4(j.o[k], inv, make_float4(0.f, 0.f, 0.f, 0.f));
+            for (int k = 0; k < Q; ++k) j.o[k] = fma4(j.o[k], inv, make_float4(0.f, 0.f, 0.f, 0.f));
             theirs = lse_of(j.m, j.l, false);
         } else {
             theirs = __ldcg(p.prefix_lse + row);
 #pragma unroll
-            for (int k = 0; k < kQuads; ++k) j.o[k] = get4(p.prefix_out + row * p.hd, 128 * k + d, p.hd);
+            for (int k = 0; k < Q; ++k) j.o[k] = get4(p.prefix_out + row * p.hd, 128 * k + d, p.hd);
         }
     }
     // One that is empty (-inf) leaves the other as it is.  A NaN, or +inf (whose own row is NaN already), stays.
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
     const float inv = 1.f / (a + z);
     const int64_t at = b * p.out_stride + static_cast<int64_t>(h) * p.hd;
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
+    for (int k = 0; k < Q; ++k) {
         const float4 s = fma4(mine[k], z, fma4(j.o[k], a, make_float4(0.f, 0.f, 0.f, 0.f)));
         put4(p, at, 128 * k + d, alone || a == 0.f ? mine[k] : z == 0.f ? j.o[k] : fma4(s, inv, make_float4(0.f, 0.f, 0.f, 0.f)));
     }
@@ -433,13 +446,14 @@ cudaError_t launch_paged_rows_plan(const PagedRowsParams& p, cudaStream_t stream
 
 cudaError_t launch_paged_rows_join(const PagedRowsParams& p, cudaStream_t stream) {
     const int ctas = paged_rows_shape(p).ctas;
+    const bool wide = p.hd > 128;
     if (p.first) {
-        const int each = (p.rows + 2 * kJoinRows - 1) / (2 * kJoinRows);  // two rows a warp
-        return launch_dependent(join_prompt_kernel, dim3(ctas, each), kJoinThreads, 0, stream, 1, p, ctas);
+        // four CTAs a tile: a row or two a warp where tiles are small
+        return launch_dependent(wide ? join_prompt_kernel<2> : join_prompt_kernel<1>, dim3(ctas, 4), kJoinThreads, 0, stream, 1, p, ctas);
     }
     const int64_t rows = static_cast<int64_t>(p.c.n_seq) * p.nh;
-    return launch_dependent(join_prefix_kernel, dim3(static_cast<unsigned int>((rows + kJoinRows - 1) / kJoinRows)),
-                            kJoinThreads, 0, stream, 1, p, ctas);
+    return launch_dependent(wide ? join_prefix_kernel<2> : join_prefix_kernel<1>,
+                            dim3(static_cast<unsigned int>((rows + kJoinRows - 1) / kJoinRows)), kJoinThreads, 0, stream, 1, p, ctas);
 }
 
 cudaError_t paged_rows_plan_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {
