@@ -3,21 +3,27 @@
 //
 // s_j = scale * q.K_j, running maximum m and sum l of each row, out = sum p_j V_j / l, scores in log2 terms.  128 q rows (the
 // rows of a tcgen05.mma) go over blocks of 128 slots: S = Q K^T and O += P V with both accumulators in tensor memory, 128
-// columns each.  P, in f16, takes the place of S there and is the second product's A operand.  Two such streams go side by
-// side, each with S and O of its own: while one's softmax runs, the tensor cores work for the other.
-//   wide    a tile has 256 rows, a stream takes 128 of them over all blocks, and K and V are read once for both
-//   NARROW  a tile has 128 rows, the streams take the even and the odd blocks, and their sums are joined at the end
-// A block of a wide tile takes 2048 cycles of the tensor cores (8192 multiply-adds in 64 cycles each way), twice that SPLIT.
-//   warps 0-3, 4-7   softmax of the streams, a row a thread: S out of tensor memory, P back into it (in two halves, so
-//                    that its product begins early), O rescaled where the maximum has to move; at the end O / l to memory
-//   warp 8           issues the MMAs (9-11 only fill up its warpgroup)
+// columns each.  P, in f16, takes the place of S there and is the second product's A operand.  While the softmax is at one
+// block, the tensor cores work on another:
+//   wide    a tile has 256 rows in two streams of 128, each with S and O of its own, and K and V are read once for both
+//   NARROW  a tile has 128 rows; not SPLIT, the streams take the even and the odd blocks and their sums are joined at the end
+//   SPLIT   (always NARROW) one stream whose S is there twice, so that a block's scores are made during the last one's softmax
+// SPLIT is for out F32: q is kept as the sum of two f16 (rounded, and the remainder rounded), so are the weights, both
+// products are made twice, and 22 bits of each are kept.  For out BF16 everything is rounded once: 2^-11, an eighth of what
+// out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are 2^(s - m + kShift), m
+// being the maximum or up to some 2^9 below it.
+//   warps 0-3, 4-7   softmax: S out of tensor memory, P back into it, O rescaled where the maximum has to move; at the end O / l
+//                    to memory.  A row a thread of a stream each, P in two halves so that its product begins early; SPLIT: a
+//                    row is two threads', of warps w and w + 4 and of 64 columns each, which meet at barriers of their own.
+//   warp 8           issues the MMAs; 9 copies q; 10 and 11 only fill up the warpgroup
 //   warps 12-15      copy K and V into a ring of chunks of 128 slots x 64 columns in the 128-byte swizzle that the MMA reads.
 //                    Pages of a multiple of 8 slots: 12 asks for boxes of a page's rows by TMA, 13-15 hand them on and
 //                    look at V where that is needed.  Others: all four by cp.async, a row at a time.
-// SPLIT (out F32): q is kept as the sum of two f16 (rounded, and the remainder rounded) and so are the weights, both
-// products are made twice, and 22 bits of each are kept.  Otherwise (out BF16) once, of the rounded values: 2^-11, an
-// eighth of what out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are
-// 2^(s - m + kShift), m being the maximum or up to some 2^9 below it.
+// An MMA of 128 x 128 x 16 takes 64 cycles, so a block of 128 rows takes 1024, and 2048 SPLIT.  What it takes in fact: 1800 for
+// 8191 new tokens of 40 heads over 8 (510 us; the tensor pipe is busy for 60 % of them), by the chain of a stream's S, softmax
+// (of which twice 230 cycles bring the scores, 600 make the weights, 270 hand them on) and products; SPLIT about 3800 for 96
+// rows over 32704 slots (79 us, 49 %), by the same chain and the warp that asks for copies.  A CTA's first piece begins some
+// 20000 cycles late: its instructions are in no cache yet.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -888,10 +894,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < NCH; ++c) wait(&ctl.full[at + c], phase);
         };
-        auto release = [&](uint32_t at) {
-#pragma unroll
-            for (int c = 0; c < NCH; ++c) tc_commit(&ctl.empty[at + c]);
-        };
+        // (one commit for a head's chunks: each takes the issuing thread 65 to 115 cycles)
+        auto release = [&](uint32_t at) { tc_commit(&ctl.empty[at]); };
         auto next_block = [&](uint32_t& at, uint32_t& phase) {
             at += 2 * NCH;
             if (at >= S::kStages) {
@@ -988,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next_block(k_at, k_phase);
                 for (int b = 0; b < n && ok; ++b) {
                     const bool last = b + 1 == n;
+                    if (!last) wait_full(k_at, k_phase);  // (here rather than between weights that are there and scores)
                     wait_full(v_at, v_phase);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
@@ -998,8 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (last) {
                             tc_commit(&ctl.o_full[t]);
                         } else {
-                            if (t == 0) wait_full(k_at, k_phase);
-                            if (ok) scores(t);
+                            scores(t);
                         }
                     }
                     if (!ok) break;
@@ -1069,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kc = 0; kc < 2 * NCH; ++kc) {  // K's chunks, then V's
                         const uint32_t n = item;
-                        if (ok && n >= S::kStages)
+                        if (ok && n >= S::kStages && kc % NCH == 0)  // a head's chunks are freed together
                             ok = __all_sync(0xffffffffu, wait_for(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
                         if (!ok) break;
                         ++item;
@@ -1199,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int c = kc % NCH;
                     const __half* pool = static_cast<const __half*>(is_v ? p.c.v : p.c.k);
                     const uint32_t n = item;
-                    if (ok && n >= S::kStages)
+                    if (ok && n >= S::kStages && c == 0)  // a head's chunks are freed together
                         ok = __all_sync(0xffffffffu, wait_for(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
                     if (!ok) break;
                     ++item;
