@@ -222,10 +222,9 @@ extern "C" qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* ca
 namespace {
 
 // What the attention of many rows takes from plan and cache; `nt` q rows.
-void rows_params(const qkv_plan* plan, const qkv_paged_kv* c, int32_t nt, bool prefix, PagedRowsParams* p) {
+void rows_params(const qkv_plan* plan, const qkv_paged_kv* c, int32_t nt, PagedRowsParams* p) {
     p->c.n_seq = c->n_seq;
     p->nt = nt;
-    p->prefix = prefix;
     p->nh = plan->d.n_head;
     p->nkv = plan->d.n_head_kv;
     p->hd = plan->d.head_dim;
@@ -294,7 +293,6 @@ void rows_workspace(const RowsLayout& l, char* ws, PagedRowsParams* p) {
     p->part_tokens = l.part_tokens;
     p->tile_tokens = l.tile_tokens;
     p->tile_cost = l.shape.tile_cost;
-    p->min_share = l.shape.min_share;
     p->max_tiles = l.max_tiles;
     p->q_high = reinterpret_cast<uint16_t*>(ws + l.q_high);
     p->q_low = reinterpret_cast<uint16_t*>(ws + l.q_low);
@@ -350,7 +348,7 @@ extern "C" qkv_status qkv_prompt_attn_workspace_bytes(const qkv_plan* plan, cons
     if (plan->d.n_head % plan->d.n_head_kv != 0) return api_fail(QKV_ERR_UNSUPPORTED, "uneven groups of q heads");
     PagedRowsParams p;
     std::memset(&p, 0, sizeof p);
-    rows_params(plan, cache, nt, false, &p);
+    rows_params(plan, cache, nt, &p);
     *out = rows_layout(p, cache, 0).bytes;
     return QKV_OK;
 }
@@ -370,7 +368,7 @@ extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged
     if (a->nt == 0) return QKV_OK;
     REQUIRE(a->d_first && a->d_lens, "d_first or d_lens is null");
     REQUIRE(aligned(a->d_first, 4) && aligned(a->d_lens, 4), "a pointer is not aligned to its elements");
-    rows_params(plan, cache, a->nt, false, &p);
+    rows_params(plan, cache, a->nt, &p);
     p.out_bf16 = a->out_dtype == QKV_BF16;
     const RowsLayout l = rows_layout(p, cache, 0);
     REQUIRE(a->d_workspace && aligned(a->d_workspace, 16), "d_workspace must be a 16-byte aligned pointer");
@@ -400,7 +398,7 @@ extern "C" qkv_status qkv_prefix_attn_workspace_bytes(const qkv_plan* plan, cons
     if (plan->d.n_head % plan->d.n_head_kv != 0) return api_fail(QKV_ERR_UNSUPPORTED, "uneven groups of q heads");
     PagedRowsParams p;
     std::memset(&p, 0, sizeof p);
-    rows_params(plan, cache, cache->n_seq, true, &p);
+    rows_params(plan, cache, cache->n_seq, &p);
     *out = rows_layout(p, cache, attn_layout(plan, cache, false).total).bytes;
     return QKV_OK;
 }
@@ -417,7 +415,7 @@ extern "C" qkv_status qkv_prefix_attn_step(const qkv_plan* plan, const qkv_paged
     REQUIRE(a->d_lens && a->d_share && a->d_prefix_len, "d_lens, d_share or d_prefix_len is null");
     REQUIRE(aligned(a->d_lens, 4) && aligned(a->d_share, 4) && aligned(a->d_prefix_len, 4),
             "a pointer is not aligned to its elements");
-    rows_params(plan, cache, cache->n_seq, true, &p);
+    rows_params(plan, cache, cache->n_seq, &p);
     p.out_bf16 = a->out_dtype == QKV_BF16;
     const AttnLayout al = attn_layout(plan, cache, false);
     const RowsLayout l = rows_layout(p, cache, al.total);

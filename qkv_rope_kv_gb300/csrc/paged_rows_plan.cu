@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prompt_kernel(const __grid_
                 x.units = max(1, (x.hi - x.lo + p.block - 1) / p.block);  // rows that see nothing are written too
             }
             int64_t sum;
-            x.start = length + scan<int64_t>(x.units ? x.units + p.tile_cost : 0, sum, warp_s);
+            x.start = length + scan<int64_t>(x.units ? x.units + tile_cost(p, x) : 0, sum, warp_s);
             if (t < here) p.tiles[tiles + t] = x;
             length += sum;
         }
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefix_kernel(const __grid_
             x.units = (x.hi + p.block - 1) / p.block;
         }
         int64_t sum;
-        x.start = length + scan<int64_t>(x.units ? x.units + p.tile_cost : 0, sum, warp_s);
+        x.start = length + scan<int64_t>(x.units ? x.units + tile_cost(p, x) : 0, sum, warp_s);
         if (i < here) p.tiles[tiles + i] = x;
         length += sum;
         tiles += here;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kJoinThreads, Q == 1 ? kJoinCtas : 2) join_pro
     griddep_wait();
     griddep_launch_dependents();
     const RowPiece* s = p.pieces + blockIdx.x;
-    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = share_of(p, total, ctas);
+    const int64_t total = __ldcg(p.total) * p.nkv * p.blocks, share = share_of(total, ctas);
     const int4 x = __ldcg(reinterpret_cast<const int4*>(s)), y = __ldcg(reinterpret_cast<const int4*>(s) + 1);
     if (share * blockIdx.x >= total || y.x == 0) return;  // (what was loaded is none)
     const int64_t start = static_cast<uint32_t>(x.x) | static_cast<int64_t>(x.y) << 32;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kJoinThreads, Q == 1 ? kJoinCtas : 2) join_pre
     for (int k = 0; k < Q; ++k) j.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (prefix) {
         const RowTile t = load_tile(p, tile);
-        const int64_t share = share_of(p, per_head * p.nkv * p.blocks, ctas);
+        const int64_t share = share_of(per_head * p.nkv * p.blocks, ctas);
         const int blk = (h - kv * G) / p.per_block;
         const int64_t start = (static_cast<int64_t>(kv) * p.blocks + blk) * per_head + t.start;
         const int c0 = static_cast<int>(start / share), c1 = static_cast<int>((start + t.units - 1) / share);

@@ -5,10 +5,9 @@
 // rows of a tcgen05.mma) go over blocks of 128 slots: S = Q K^T and O += P V with both accumulators in tensor memory, 128
 // columns each.  P, in f16, takes the place of S there and is the second product's A operand.  While the softmax is at one
 // block, the tensor cores work on another:
-//   wide    a tile has 256 rows in two streams of 128, each with S and O of its own, and K and V are read once for both
-//   NARROW  a tile has 128 rows; not SPLIT, the streams take the even and the odd blocks and their sums are joined at the end
-//   SPLIT   (always NARROW) one stream whose S is there twice, so that a block's scores are made during the last one's softmax
-// SPLIT is for out F32: q is kept as the sum of two f16 (rounded, and the remainder rounded), so are the weights, both
+//   out BF16          a tile has 256 rows in two streams of 128, each with S and O of its own; K and V are read once for both
+//   out F32, "SPLIT"  a tile has 128 rows, one stream, whose S is there twice: a block's scores are made during the last one's softmax
+// SPLIT, q is kept as the sum of two f16 (rounded, and the remainder rounded), so are the weights, both
 // products are made twice, and 22 bits of each are kept.  For out BF16 everything is rounded once: 2^-11, an eighth of what
 // out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are 2^(s - m + kShift), m
 // being the maximum or up to some 2^9 below it.
@@ -49,15 +48,15 @@ constexpr int kControlBytes = 2560;  // barriers and small tables, behind the ch
 // largest are not).
 constexpr float kMostWeight = 60000.f;
 constexpr int kFold = 2;       // SPLIT: blocks that are summed in one accumulator before it is added to the others' sum
-constexpr int kTileCost = 3;  // units that a tile's beginning and end take
-constexpr int kMinShare = 3;  // of a CTA: a part costs its write and its join
+// Units that a tile's beginning and end take for 128 rows.  (0, 3 and 6 gave 71, 60 and 65 us for 32 sequences of four tokens, and for
+// 8191 tokens, whose tiles have twice as many rows, 679, 550 and 566.)
+constexpr int kTileCost = 3;
 constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
 
-template <bool SPLIT, int NCH, bool NARROW>  // NCH chunks of 64 columns a head
+template <bool SPLIT, int NCH>  // NCH chunks of 64 columns a head
 struct Shape {
-    static constexpr int kQChunks = (NARROW ? 1 : 2) * NCH * (SPLIT ? 2 : 1);
-    static constexpr int kRoom = 14 - kQChunks;
-    static constexpr int kStages = kRoom > kMaxStages ? kMaxStages : kRoom;  // even: a head's chunks are neighbours
+    static constexpr int kQChunks = 2 * NCH;  // two streams, or two parts
+    static constexpr int kStages = 14 - kQChunks < kMaxStages ? 14 - kQChunks : kMaxStages;  // even: a head's chunks are neighbours
     // Copies in flight ahead of the one that is waited for (cp.async).  The MMAs free a block's V only after the next
     // block's K is there, so that many chunks must fit behind those in flight.
     static constexpr int kLag = kStages - 2 * NCH > 5 ? 5 : kStages - 2 * NCH;
@@ -305,13 +304,10 @@ __device__ __forceinline__ bool pair_any(int quarter, bool yes) {
 
 struct Control {
     uint64_t landed[kMaxStages], full[kMaxStages], empty[kMaxStages];
-    uint64_t q_ready[2], q_free[2], s_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], joined, pv_done, o_free, drained;
+    uint64_t q_ready[2], q_free[2], s_full[2], p_half[2], half_done[2], p_ready[2], o_full[2], pv_done, o_free, drained;
     uint32_t live[kLiveRing][4];   // slots of a block that are there
     uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
-    union {
-        float2 ml[kHalf];      // NARROW: maxima and sums of the second stream
-        float top[2][kHalf];   // SPLIT: of the rows, by side
-    };
+    float top[2][kHalf];           // SPLIT: of the rows, by side
     uint32_t tmem;
 };
 static_assert(sizeof(Control) <= kControlBytes, "control");
@@ -333,13 +329,12 @@ __device__ __forceinline__ bool clean16(uint32_t at) {
     return true;
 }
 
-template <bool SPLIT, int NCH, bool NARROW>
+template <bool SPLIT, int NCH>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_rows_tc_kernel(const __grid_constant__ PagedRowsParams p, const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_ql, int box) {
-    using S = Shape<SPLIT, NCH, NARROW>;
-    static_assert(!SPLIT || NARROW, "one stream");
+    using S = Shape<SPLIT, NCH>;
     constexpr float kShift = S::kShift;
     extern __shared__ __align__(1024) unsigned char smem[];  // atoms of the swizzle: no other shared memory before it
     Control& ctl = *reinterpret_cast<Control*>(smem + S::kControlAt);
@@ -348,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     constexpr int kParts = SPLIT ? 2 : 1;
     // chunk c of part `part` (0: rounded, 1: remainder) of stream t's q
-    auto q_chunk = [&](int t, int part, int c) { return q_at + (((NARROW ? 0 : t) * kParts + part) * NCH + c) * kChunkBytes; };
+    auto q_chunk = [&](int t, int part, int c) { return q_at + (((SPLIT ? 0 : t) * kParts + part) * NCH + c) * kChunkBytes; };
     auto chunk_at = [&](uint32_t n) { return ring_at + n % S::kStages * kChunkBytes; };
 
     if (warp == kMmaWarp) {
@@ -372,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.p_ready[t], 4);
             mbar_init(&ctl.o_full[t], 1);
         }
-        mbar_init(&ctl.joined, 4);
         mbar_init(&ctl.pv_done, 1);
         mbar_init(&ctl.o_free, 8);
         mbar_init(&ctl.drained, 1);
@@ -653,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- softmax: thread `lane` of warp w has row 32 (w % 4) + lane of stream w / 4
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t s_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 128 * t, o_at = s_at + 256;
-        uint32_t s_phase = 0, o_phase = 0, join_phase = 0;  // o_phase: bit t
+        uint32_t s_phase = 0, o_phase = 0;
         int piece = 0, block0 = 0;
         bool ok = true;
         while (ok && w.next(p, x)) {
@@ -663,18 +657,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             block0 += x.to - x.from;
             ++piece;
             if (tid == 0) note_piece(p, w, x);
-            const int token0 = NARROW ? 0 : t * p.part_tokens;  // the stream's first
+            const int token0 = t * p.part_tokens;  // the stream's first
             if (token0 >= tile.ntok) continue;                  // nothing for this stream
             const int r = 32 * quarter + lane, in_part = r / p.per_block, g = r - in_part * p.per_block;
             const int i = token0 + in_part, row = tile.row0 + i, h_row = kv * G + g0 + g;
             const bool mine = in_part < p.part_tokens && i < tile.ntok && g < heads;
             const bool busy = 32 * quarter < min(p.part_tokens, tile.ntok - token0) * p.per_block;
             const float unscale = mine ? __ldcg(p.q_unscale + static_cast<int64_t>(row) * p.nh + h_row) : 1.f;
-            const bool both = NARROW ? x.to - x.from > 1 : true;  // NARROW: the second stream has blocks
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, i, see_lo, see_hi);
             float m = -CUDART_INF_F, l = 0.f;
-            for (int u = x.from + (NARROW ? t : 0); u < x.to; u += NARROW ? 2 : 1) {
+            for (int u = x.from; u < x.to; ++u) {
                 ok = __all_sync(0xffffffffu, wait_for(&ctl.s_full[t], s_phase));
                 s_phase ^= 1;
                 if (!ok) break;
@@ -747,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ok = __all_sync(0xffffffffu, wait_for(&ctl.half_done[t], s_phase ^ 1));
                                 tc_fence_after();
                             }
-                            if (half == 1 || u >= x.from + (NARROW ? 2 : 1))
+                            if (half == 1 || u > x.from)
 #pragma unroll 1
                                 for (int c = 0; c < p.hd; c += 16) {
                                     uint32_t o[16];
@@ -768,39 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
             }
             if (!ok) break;
-            if (NARROW && t == 1 && both) {
-                ctl.ml[r] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.joined);
-            }
-            // NARROW: both streams read the one q, so both wait for both
-            for (int k = 0; k < 2; ++k) {
-                if (NARROW ? k == 1 && !both : k != t) continue;
-                ok = ok && __all_sync(0xffffffffu, wait_for(&ctl.o_full[k], (o_phase >> k) & 1));
-                o_phase ^= 1u << k;
-            }
-            if (NARROW && t == 0 && both) {
-                ok = ok && __all_sync(0xffffffffu, wait_for(&ctl.joined, join_phase));
-                join_phase ^= 1;
-            }
+            ok = __all_sync(0xffffffffu, wait_for(&ctl.o_full[t], o_phase));
+            o_phase ^= 1u;
             if (!ok) break;
             tc_fence_after();
-            if (NARROW && t == 1) continue;
             if (busy) {
-                float k0 = 1.f, k1 = 0.f;
-                if (NARROW && both) {
-                    const float2 other = ctl.ml[r];
-                    const float top = fmaxf(m, other.x);
-                    k0 = m == top ? 1.f : ex2(m - top);
-                    k1 = other.x == top ? 1.f : ex2(other.x - top);
-                    m = top;
-                    l = l * k0 + other.y * k1;
-                }
                 const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
                 const bool whole = x.whole(), empty = see_lo >= see_hi;
                 const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
-                k0 *= inv;
-                k1 *= inv;
                 float* part = part_of(p, blockIdx.x, x.first);
                 // Results go to memory through q's place, by rows of a warp: 16 bytes a lane of neighbouring lanes instead of a
                 // row a lane, which took 7000 cycles of a tile.
@@ -817,16 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c0 = 0; c0 < p.hd; c0 += columns) {
 #pragma unroll 1
                     for (int c = c0; c < min(p.hd, c0 + columns); c += 16) {
-                        uint32_t v[16], y[16];
+                        uint32_t v[16];
                         tm_ld16(o_at + c, v);
-                        if (NARROW && both) tm_ld16(o_at + 128 + c, y);
                         tc_wait_ld();
                         uint32_t d[16];
                         float o[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            o[k] = __uint_as_float(v[k]) * k0;
-                            if (NARROW && both) o[k] = fmaf(__uint_as_float(y[k]), k1, o[k]);
+                            o[k] = __uint_as_float(v[k]) * inv;
                             odd = fmaf(o[k], 0.f, odd);
                             d[k] = __float_as_uint(o[k]);
                         }
@@ -945,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         while (ok && w.next(p, x)) {
             const int n = x.to - x.from;
-            if (NARROW) {
+            if (SPLIT) {
                 wait(&ctl.q_ready[0], q_phase);
                 q_phase ^= 1u;
                 for (int b = 0; b < min(n, 2) && ok; ++b) {
@@ -958,19 +924,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < n && ok; ++b) {
                     const int t = b & 1;
                     wait_full(v_at, v_phase);
-                    if (SPLIT && b > 0 && b % kFold == 0) {  // the accumulator's sums have been added to the others
+                    if (b > 0 && b % kFold == 0) {  // the accumulator's sums have been added to the others
                         wait(&ctl.o_free, o_phase);
                         o_phase ^= 1u;
                     }
-                    if (ok) sums(t, SPLIT ? b % kFold != 0 : b >= 2);
+                    if (ok) sums(t, b % kFold != 0);
                     if (!ok) break;
-                    if (SPLIT) tc_commit(&ctl.pv_done);
+                    tc_commit(&ctl.pv_done);
                     release(v_at);
                     next_block(v_at, v_phase);
-                    if (b + 2 >= n) {
-                        if (!SPLIT || b + 1 == n) tc_commit(&ctl.o_full[SPLIT ? 0 : t]);
-                        continue;
-                    }
+                    if (b + 1 == n) tc_commit(&ctl.o_full[0]);
+                    if (b + 2 >= n) continue;
                     wait_full(k_at, k_phase);
                     if (!ok) break;
                     scores(t);
@@ -1028,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = kParts * NCH * 128 * p.per_block * p.part_tokens;
         while (ok && w.next(p, x)) {
             const int kv = x.head / p.blocks, h0 = kv * G + (x.head - kv * p.blocks) * p.per_block;
-            for (int t = 0; t < (NARROW ? 1 : 2); ++t) {
+            for (int t = 0; t < (SPLIT ? 1 : 2); ++t) {
                 const int token = t * p.part_tokens;
                 if (!ok || token >= x.t.ntok) break;
                 ok = __all_sync(0xffffffffu, wait_for(&ctl.q_free[t], (phase >> t) & 1));
@@ -1264,10 +1228,10 @@ bool encode(CUtensorMap* map, const void* base, int64_t n0, int64_t n1, int64_t 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool SPLIT, int NCH, bool NARROW>
+template <bool SPLIT, int NCH>
 cudaError_t launch_t(const PagedRowsParams& p, cudaStream_t stream) {
-    auto kernel = paged_rows_tc_kernel<SPLIT, NCH, NARROW>;
-    constexpr int smem = Shape<SPLIT, NCH, NARROW>::kSmem;
+    auto kernel = paged_rows_tc_kernel<SPLIT, NCH>;
+    constexpr int smem = Shape<SPLIT, NCH>::kSmem;
     // fewer registers at launch than the warpgroups share out would leave some of them waiting for ever
     static const bool enough = [&] {
         cudaFuncAttributes a;
@@ -1292,19 +1256,15 @@ cudaError_t launch_t(const PagedRowsParams& p, cudaStream_t stream) {
     return launch_dependent(kernel, dim3(kSms), kThreads, smem, stream, 1, p, maps[0], maps[1], maps[2], maps[3], box);
 }
 
-template <bool SPLIT, int NCH>
-cudaError_t launch_n(const PagedRowsParams& p, cudaStream_t stream) {
-    if constexpr (SPLIT) return launch_t<SPLIT, NCH, true>(p, stream);
-    else return p.rows == kHalf ? launch_t<SPLIT, NCH, true>(p, stream) : launch_t<SPLIT, NCH, false>(p, stream);
-}
-
 }  // namespace
 
-RowsShape paged_rows_tc_shape(bool narrow) { return {narrow ? kHalf : 2 * kHalf, kHalf, kBlock, kSms, kTileCost, kMinShare, true}; }
+RowsShape paged_rows_tc_shape(bool split) {
+    return {split ? kHalf : 2 * kHalf, kHalf, kBlock, kSms, kTileCost, true};
+}
 
 cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream) {
-    if (p.out_bf16) return p.hd <= 64 ? launch_n<false, 1>(p, stream) : launch_n<false, 2>(p, stream);
-    return p.hd <= 64 ? launch_n<true, 1>(p, stream) : launch_n<true, 2>(p, stream);
+    if (p.out_bf16) return p.hd <= 64 ? launch_t<false, 1>(p, stream) : launch_t<false, 2>(p, stream);
+    return p.hd <= 64 ? launch_t<true, 1>(p, stream) : launch_t<true, 2>(p, stream);
 }
 
 cudaError_t paged_rows_tc_status_read(cudaStream_t stream, uint32_t* flags, int32_t* bad) {

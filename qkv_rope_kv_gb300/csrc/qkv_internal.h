@@ -210,12 +210,11 @@ struct PagedRowsParams {
     int64_t out_stride;
     float* lse;
     int32_t nt, nh, nkv, hd, kv_f16;
-    int32_t prefix;             // which of the two calls
     // the plan, made on the device
     int32_t rows, block;        // of a tile, of a unit
     int32_t per_block, blocks;  // q heads of a kv head in a tile, and how many such blocks it has
     int32_t part_rows, part_tokens;  // a tile's rows come in one or two parts, of whole tokens each (see row_of)
-    int32_t tile_tokens, tile_cost, min_share, max_tiles;
+    int32_t tile_tokens, tile_cost, max_tiles;
     int64_t* total;             // [0] how long the tiles of one block of q heads are, [1] tiles
     RowTile* tiles;
     int32_t* starts;            // prefix: [n_seq] each: where the rows' own slots begin, ...
@@ -237,11 +236,11 @@ cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream);
 cudaError_t launch_paged_rows_join(const PagedRowsParams& p, cudaStream_t stream);
 // Rows of a tile, slots of a block and CTAs of the kernel that these sizes and addresses get.
 struct RowsShape {
-    int32_t rows, part_rows, block, ctas, tile_cost, min_share;
+    int32_t rows, part_rows, block, ctas, tile_cost;
     bool tensor;  // the kernel on the tensor cores
 };
 RowsShape paged_rows_shape(const PagedRowsParams& p);
-RowsShape paged_rows_tc_shape(bool narrow);
+RowsShape paged_rows_tc_shape(bool split);
 RowsShape paged_rows_any_shape(const PagedRowsParams& p);
 bool paged_rows_on_tensor_cores(const PagedRowsParams& p);
 cudaError_t launch_paged_rows_tc(const PagedRowsParams& p, cudaStream_t stream);
