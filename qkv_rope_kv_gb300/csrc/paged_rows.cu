@@ -3,7 +3,8 @@
 //
 // s_j = scale * q.K_j, running maximum m and sum l of each row, out = sum p_j V_j / l, scores in log2 terms.  A tile of 64
 // rows goes over blocks of 64 slots: both products are made by plain f32 multiply-adds from shared memory, each thread 4 x 4
-// scores and 4 rows x hd / 16 columns of the sums.
+// scores and 4 rows x hd / 16 columns of the sums.  Multiply-adds bound it (and their operands' reads from shared memory) where
+// there are many rows; a few, 17 tokens of 14 heads over 2, take 17.7 us with the plan and the join: a chain of latencies.
 #include "paged_rows.cuh"
 
 namespace {
@@ -284,8 +285,8 @@ RowsShape paged_rows_any_shape(const PagedRowsParams& p) {
     return {kRows, kRows, kBlock, kSms * (p.hd <= 128 ? Shape<128>::kCtas : Shape<256>::kCtas), 1, false};
 }
 
-// f16 rows that 16-byte copies can read, of whole steps of 16 columns that fit tensor memory beside the scores.  (4 x 509 tokens of
-// 28 heads over 4: 94 us, and 2050 by f32 multiply-adds; 17 tokens of 14 over 2, the smallest, 19.5 and 23.6.)
+// f16 rows that 16-byte copies can read, of whole steps of 16 columns that fit tensor memory beside the scores.  (4 x 509
+// tokens of 28 heads over 4: 94 us, and 2050 by f32 multiply-adds; 17 tokens of 14 over 2, the smallest, 19.5 and 23.6.)
 bool paged_rows_on_tensor_cores(const PagedRowsParams& p) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(p.c.k) | reinterpret_cast<uintptr_t>(p.c.v) |
                            static_cast<uintptr_t>(p.c.page_stride * 2);

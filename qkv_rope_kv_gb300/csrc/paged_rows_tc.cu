@@ -6,7 +6,8 @@
 // columns each.  P, in f16, takes the place of S there and is the second product's A operand.  While the softmax is at one
 // block, the tensor cores work on another:
 //   out BF16          a tile has 256 rows in two streams of 128, each with S and O of its own; K and V are read once for both
-//   out F32, "SPLIT"  a tile has 128 rows, one stream, whose S is there twice: a block's scores are made during the last one's softmax
+//   out F32, "SPLIT"  a tile has 128 rows, one stream, whose S is there twice: a block's scores are made during the softmax of
+//                     the last one's
 // SPLIT, q is kept as the sum of two f16 (rounded, and the remainder rounded), so are the weights, both
 // products are made twice, and 22 bits of each are kept.  For out BF16 everything is rounded once: 2^-11, an eighth of what
 // out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are 2^(s - m + kShift), m
@@ -48,15 +49,16 @@ constexpr int kControlBytes = 2560;  // barriers and small tables, behind the ch
 // largest are not).
 constexpr float kMostWeight = 60000.f;
 constexpr int kFold = 2;       // SPLIT: blocks that are summed in one accumulator before it is added to the others' sum
-// Units that a tile's beginning and end take for 128 rows.  (0, 3 and 6 gave 71, 60 and 65 us for 32 sequences of four tokens, and for
-// 8191 tokens, whose tiles have twice as many rows, 679, 550 and 566.)
+// Units that a tile's beginning and end take for 128 rows.  (0, 3 and 6 gave 71, 60 and 65 us for 32 sequences of four tokens;
+// 0, 3 and 5 of them 679, 550 and 566 for 8191 tokens, whose tiles have twice as many rows.)
 constexpr int kTileCost = 3;
 constexpr int kMaxStages = 12, kPoisonRing = 16, kLiveRing = 8;
 
 template <bool SPLIT, int NCH>  // NCH chunks of 64 columns a head
 struct Shape {
     static constexpr int kQChunks = 2 * NCH;  // two streams, or two parts
-    static constexpr int kStages = 14 - kQChunks < kMaxStages ? 14 - kQChunks : kMaxStages;  // even: a head's chunks are neighbours
+    // (even: a head's chunks are neighbours)
+    static constexpr int kStages = 14 - kQChunks < kMaxStages ? 14 - kQChunks : kMaxStages;
     // Copies in flight ahead of the one that is waited for (cp.async).  The MMAs free a block's V only after the next
     // block's K is there, so that many chunks must fit behind those in flight.
     static constexpr int kLag = kStages - 2 * NCH > 5 ? 5 : kStages - 2 * NCH;
