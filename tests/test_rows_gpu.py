@@ -327,12 +327,13 @@ def attend64(q, K, V, hi, scale):
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("page", [64, 7])  # copied by boxes, and row by row
 @pytest.mark.parametrize("nh,nkv,hd,new,cached", [(32, 8, 128, 700, 3900), (16, 8, 64, 1500, 2000), (40, 8, 128, 3, 20000)])
-def test_long_prompts(qkv, nh, nkv, hd, new, cached, out):
+def test_long_prompts(qkv, nh, nkv, hd, new, cached, page, out):
     """Pieces of tens of blocks, which sums of several accumulators and rescaled ones go through."""
     import torch
     torch.manual_seed(1)
-    n, page, G = new + cached, 64, nh // nkv
+    n, G = new + cached, nh // nkv
     per = -(-n // page)
     plan = make_plan(nh, nkv, hd, "f16")
     k, v = (torch.randn(per, page, nkv * hd, device="cuda").half() for _ in range(2))
@@ -393,6 +394,41 @@ def test_long_shared_prefix(qkv):
                 got = o.view(B, nkv, G, hd)[:, h].double()
                 # 2-norms: weights off by 2^-11 at random, and bf16's half step; f32 as in test_long_prompts
                 assert (got - want).norm() <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -18) * want.norm()
+    assert Q.qkv_check_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_calls_at_the_same_time(qkv, out):
+    """Calls on two streams, each with a workspace of its own, give the bits of calls one after the other."""
+    import torch
+    torch.manual_seed(3)
+    nh, nkv, hd, page, new = 28, 4, 128, 16, 300
+    plan = make_plan(nh, nkv, hd, "f16")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    dtype = torch.bfloat16 if out == "bf16" else torch.float32
+    sides = []
+    for k in range(2):
+        n = new + 700 * (k + 1)
+        pools = [torch.randn(-(-n // page), page, nkv * hd, device="cuda").half() for _ in range(2)]
+        table = torch.randperm(pools[0].shape[0], device="cuda").int()[None].contiguous()
+        cache = Q.PagedKv(plan, *pools, table)
+        ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, new), dtype=torch.uint8, device="cuda")
+        sides.append((cache, torch.randn(new, nh * hd, device="cuda"), i32(0, new), i32(n), ws, torch.cuda.Stream(), pools, table))
+
+    def call(s, o, stream=None):
+        Q.qkv_prompt_attn_step(plan, s[0], s[1], s[2], s[3], hd ** -0.5, o, s[4], stream=stream)
+    want = [torch.empty(new, nh * hd, device="cuda", dtype=dtype) for _ in sides]
+    for s, o in zip(sides, want):
+        call(s, o)
+        torch.cuda.synchronize()
+    got = [[torch.full_like(o, float("nan")) for _ in range(6)] for o in want]
+    torch.cuda.synchronize()
+    for k in range(6):
+        for s, o in zip(sides, got):
+            call(s, o[k], s[5])
+    torch.cuda.synchronize()
+    for o, w in zip(got, want):
+        assert all(torch.equal(x, w) for x in o)
     assert Q.qkv_check_device_error()[0] == 0
 
 
