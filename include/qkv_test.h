@@ -1,7 +1,7 @@
 /* Test hooks of libqkv.so: the device-side failure paths of the decode and
- * prefill kernels, and the grid of the paged attention.
+ * prefill kernels and of the attention of many query rows, and the grid of the paged attention.
  *
- * Not part of the stage.  Every wait of a decode or prefill kernel on a pipeline
+ * Not part of the stage.  Every wait of these kernels on a pipeline
  * or exchange barrier is bounded (0.5 s); when it runs out the kernel sets bit 1
  * (value 2) of the device status word, lets its own copies in flight land, and
  * returns, so the context stays usable and the host learns of the failure from
@@ -46,6 +46,16 @@ qkv_status qkv_test_decode_wait_timeout(const qkv_plan* plan, const float* x, co
 qkv_status qkv_test_prefill_xchg_timeout(const qkv_plan* plan, const uint16_t* X, int32_t nt, const void* w,
                                          const float* bias, const int32_t* d_positions, float* Y, void* kv_k,
                                          void* kv_v, uint32_t wait_limit_us, void* stream);
+
+/* qkv_prompt_attn_step with every wait of the tensor cores' kernel (f16 caches; the others have no such waits) limited
+ * to wait_limit_us microseconds (1 .. 1000) in which the CTA asks for no further block of slots, and, with withhold_end
+ * non-zero, with the warps that write results never told that a piece's sums are complete: their wait runs out, they set
+ * the device status flag 2 and leave (out and lse then hold nothing of use).  Without it the results are those of qkv_prompt_attn_step, however much
+ * longer than the limit a CTA's pieces last.  Returns after the launches; read the flag with qkv_check_device_error,
+ * which also clears it.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+qkv_status qkv_test_prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* args,
+                                uint32_t wait_limit_us, int32_t withhold_end, void* stream);
 
 /* The grid that qkv_attn_step launches its main kernel on for this plan and cache: CTAs in all, and
  * CTAs of a cluster (1: none).  The order of the sums follows from it, so it depends on sizes and

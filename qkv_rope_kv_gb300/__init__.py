@@ -171,6 +171,7 @@ def _declare(lib):
         "qkv_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_prompt_attn_workspace_bytes": ([vp, vp, i32, ctypes.POINTER(sz)], st),
         "qkv_prompt_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
+        "qkv_test_prompt_attn": ([vp, vp, ctypes.c_char_p, ctypes.c_uint32, i32, vp], st),
         "qkv_prefix_attn_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
         "qkv_prefix_attn_step": ([vp, vp, ctypes.c_char_p, vp], st),
         "qkv_evict_workspace_bytes": ([vp, vp, ctypes.POINTER(sz)], st),
@@ -689,23 +690,36 @@ def qkv_prompt_attn_workspace_bytes(plan: Plan, cache: PagedKv, nt: int) -> int:
     return out.value
 
 
-def qkv_prompt_attn_step(plan: Plan, cache: PagedKv, q, first, lens, scale: float, out, workspace, window: int = 0,
-                         lse=None, stream=None):
-    """Attention of several new tokens per sequence, each up to its own slot: q [nt, nqt] f32, sequence b's tokens in rows
-    first[b] .. first[b + 1] - 1 (int32 [n_seq + 1]), over the cached slots of each (``lens`` int32 [n_seq]) into out
-    [nt, nqt] (f32 or bf16) and lse [nt, n_head] (f32).  ``workspace``: qkv_prompt_attn_workspace_bytes device bytes."""
+def _prompt_args(plan, cache, q, first, lens, scale, out, workspace, window, lse):
     f32, i32, bf16 = cache.types
     dev, out_type, nt = cache.device, out.dtype, q.shape[0]
     x, x_stride = _rows(q, "q", f32, (nt, plan.nqt), dev)
     to, to_stride = _rows(out, "out", bf16 if out_type is bf16 else f32, (nt, plan.nqt), dev)
     try:
-        args = _PROMPT_ARGS.pack(
+        return _PROMPT_ARGS.pack(
             x, x_stride, _tensor(first, "first", i32, (cache.n_seq + 1,), dev),
             _tensor(lens, "lens", i32, cache.per_seq, dev), to, to_stride, _tensor(lse, "lse", f32, (nt, plan.n_head), dev),
             *_workspace(workspace, dev), scale, window, QKV_BF16 if out_type is bf16 else QKV_F32, nt)
     except (struct.error, OverflowError) as e:
         _unpackable(e)
+
+
+def qkv_prompt_attn_step(plan: Plan, cache: PagedKv, q, first, lens, scale: float, out, workspace, window: int = 0,
+                         lse=None, stream=None):
+    """Attention of several new tokens per sequence, each up to its own slot: q [nt, nqt] f32, sequence b's tokens in rows
+    first[b] .. first[b + 1] - 1 (int32 [n_seq + 1]), over the cached slots of each (``lens`` int32 [n_seq]) into out
+    [nt, nqt] (f32 or bf16) and lse [nt, n_head] (f32).  ``workspace``: qkv_prompt_attn_workspace_bytes device bytes."""
+    args = _prompt_args(plan, cache, q, first, lens, scale, out, workspace, window, lse)
     _check(_lib.qkv_prompt_attn_step(plan.handle, cache.address, args, cache._on(plan, stream)))
+
+
+def qkv_test_prompt_attn(plan: Plan, cache: PagedKv, q, first, lens, scale: float, out, workspace, window: int = 0,
+                         lse=None, wait_limit_us: int = 200, withhold_end: bool = False, stream=None):
+    """Test hook (include/qkv_test.h): qkv_prompt_attn_step with every wait limited to wait_limit_us without progress, and
+    with the end of every piece withheld, so the device status flag 2 gets set."""
+    args = _prompt_args(plan, cache, q, first, lens, scale, out, workspace, window, lse)
+    _check(_lib.qkv_test_prompt_attn(plan.handle, cache.address, args, int(wait_limit_us), int(withhold_end),
+                                     cache._on(plan, stream)))
 
 
 def qkv_prefix_attn_workspace_bytes(plan: Plan, cache: PagedKv) -> int:

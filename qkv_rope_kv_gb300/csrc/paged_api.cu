@@ -353,8 +353,10 @@ extern "C" qkv_status qkv_prompt_attn_workspace_bytes(const qkv_plan* plan, cons
     return QKV_OK;
 }
 
-extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a,
-                                           void* stream) {
+namespace {
+
+qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a, uint64_t wait_limit_ns,
+                       bool withhold_end, void* stream) {
     PagedRowsParams p;
     std::memset(&p, 0, sizeof p);
     qkv_status st = view(plan, cache, &p.c);
@@ -383,12 +385,28 @@ extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged
     p.out = a->out;
     p.out_stride = a->out_stride;
     p.lse = a->lse;
+    p.wait_limit_ns = wait_limit_ns;
+    p.withhold_end = withhold_end;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_paged_rows_plan(p, s);
     if (e == cudaSuccess) e = launch_paged_rows(p, s);
     if (e == cudaSuccess) e = launch_paged_rows_join(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "prompt attention kernel launch");
     return QKV_OK;
+}
+
+}  // namespace
+
+extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a,
+                                           void* stream) {
+    return prompt_attn(plan, cache, a, 0, false, stream);
+}
+
+// Test hook (include/qkv_test.h).
+extern "C" qkv_status qkv_test_prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a,
+                                           uint32_t wait_limit_us, int32_t withhold_end, void* stream) {
+    REQUIRE(wait_limit_us >= 1 && wait_limit_us <= 1000, "wait_limit_us must be in [1, 1000] (got %u)", wait_limit_us);
+    return prompt_attn(plan, cache, a, wait_limit_us * 1000ull, withhold_end != 0, stream);
 }
 
 extern "C" qkv_status qkv_prefix_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out) {

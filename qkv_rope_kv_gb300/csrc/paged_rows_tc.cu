@@ -168,10 +168,13 @@ __device__ __forceinline__ void tm_st1(uint32_t a, uint32_t r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(a), "r"(r) : "memory");
 }
 
-// As mbar_wait_bounded, without asking to be suspended: these waits are short, and there are many.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+// As mbar_wait_bounded, without asking to be suspended: these waits are short, and there are many.  Some last for a whole
+// piece or, where a stream has no rows in the pieces before, for several; so one that has lasted for the limit gives up only
+// if no block was asked for meanwhile (a CTA's blocks are counted in *moved, and they come to an end).
+__device__ __forceinline__ bool wait_moving(uint64_t* bar, uint32_t parity, const uint32_t* moved, uint64_t limit_ns) {
     const uint32_t at = smem_u32(bar);
     uint64_t t0 = 0;
+    uint32_t seen = 0;
     for (int i = 0;; ++i) {
         uint32_t ok;
         asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -179,8 +182,12 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
         if (ok) return true;
         if ((i & 63) == 63) {
             const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitTimeoutNs) return false;
+            const uint32_t n = *static_cast<const volatile uint32_t*>(moved);
+            if (t0 == 0 || (now - t0 > limit_ns && n != seen)) {
+                t0 = now;
+                seen = n;
+            }
+            if (now - t0 > limit_ns) return false;
         }
     }
 }
@@ -310,6 +317,7 @@ struct Control {
     uint32_t live[kLiveRing][4];   // slots of a block that are there
     uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
     float top[2][kHalf];           // SPLIT: of the rows, by side
+    uint32_t moved;                // blocks that were asked for
     uint32_t tmem;
 };
 static_assert(sizeof(Control) <= kControlBytes, "control");
@@ -347,6 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunk c of part `part` (0: rounded, 1: remainder) of stream t's q
     auto q_chunk = [&](int t, int part, int c) { return q_at + (((SPLIT ? 0 : t) * kParts + part) * NCH + c) * kChunkBytes; };
     auto chunk_at = [&](uint32_t n) { return ring_at + n % S::kStages * kChunkBytes; };
+    auto wait_for = [&](uint64_t* bar, uint32_t parity) {
+        return wait_moving(bar, parity, &ctl.moved, p.wait_limit_ns ? p.wait_limit_ns : kWaitTimeoutNs);
+    };
+    auto note_moved = [&](int block) { *static_cast<volatile uint32_t*>(&ctl.moved) = static_cast<uint32_t>(block) + 1u; };
 
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(512u)
@@ -355,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid < kPoisonRing) ctl.poison[tid] = 0;
     if (tid == 0) {
+        ctl.moved = 0;
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&ctl.landed[s], 1);
             mbar_init(&ctl.full[s], box ? kLoadWarps - 1 : kLoadWarps);
@@ -935,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(&ctl.pv_done);
                     release(v_at);
                     next_block(v_at, v_phase);
-                    if (b + 1 == n) tc_commit(&ctl.o_full[0]);
+                    if (b + 1 == n && !p.withhold_end) tc_commit(&ctl.o_full[0]);
                     if (b + 2 >= n) continue;
                     wait_full(k_at, k_phase);
                     if (!ok) break;
@@ -966,11 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (ok) sums(t, b > 0);
                         if (!ok) break;
                         if (t + 1 == halves) release(v_at);
-                        if (last) {
-                            tc_commit(&ctl.o_full[t]);
-                        } else {
-                            scores(t);
-                        }
+                        if (!last) scores(t);
+                        else if (!p.withhold_end) tc_commit(&ctl.o_full[t]);
                     }
                     if (!ok) break;
                     next_block(v_at, v_phase);
@@ -1044,6 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         ++item;
                         if (kc == 0) {
+                            if (lane == 0) note_moved(block);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 const int s = 32 * c + lane;
@@ -1173,7 +1184,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = __all_sync(0xffffffffu, wait_for(&ctl.empty[n % S::kStages], (n / S::kStages - 1) & 1));
                     if (!ok) break;
                     ++item;
-                    if (kc == 0 && lane == 0) ctl.live[block % kLiveRing][i] = there;
+                    if (kc == 0 && lane == 0) {
+                        if (i == 0) note_moved(block);
+                        ctl.live[block % kLiveRing][i] = there;
+                    }
                     pieces = (pieces & ~(15ull << (4 * (n % 16)))) | static_cast<u64>(piece & 15) << (4 * (n % 16));
                     look = is_v && check ? look | 1u << (n % 32) : look & ~(1u << (n % 32));
                     if (8 * c + (lane & 7) < chunks16) {

@@ -230,6 +230,10 @@ struct PagedRowsParams {
     float* prefix_lse;
     const float* own_out;       // the same of the rows' own slots
     const float* own_lse;
+    // Test hook of the tensor cores' bounded waits (zero in every product call): a non-zero limit replaces the default, and
+    // withhold_end makes no piece's end known to the warps that wait for it.
+    uint64_t wait_limit_ns;
+    int32_t withhold_end;
 };
 cudaError_t launch_paged_rows_plan(const PagedRowsParams& p, cudaStream_t stream);
 cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream);

@@ -1,0 +1,78 @@
+"""Bounded waits of the attention of many query rows on the tensor cores: none runs out while its CTA gets on, however long
+a piece of work lasts; one whose end never comes sets the flag and leaves the context usable."""
+import time
+
+import pytest
+
+import qkv_rope_kv_gb300 as Q
+from test_paged_gpu import make_plan
+
+pytestmark = pytest.mark.gpu
+
+
+def dtypes(out):
+    import torch
+    return torch.bfloat16 if out == "bf16" else torch.float32
+
+
+def problem(new, slots, nh, nkv, hd, out, pages=64, page=64):
+    """Sequences of new[b] tokens at the end of slots[b] slots, of `pages` pages that their rows of the table name again and
+    again, and a call of them."""
+    import torch
+    torch.manual_seed(1)
+    plan = make_plan(nh, nkv, hd, "f16")
+    k, v = (torch.randn(pages, page, nkv * hd, device="cuda").half() for _ in range(2))
+    per = -(-max(slots) // page)
+    table = (torch.arange(per, device="cuda") % pages).int()[None].repeat(len(new), 1).contiguous()
+    cache = Q.PagedKv(plan, k, v, table)
+    first = [0]
+    for n in new:
+        first.append(first[-1] + n)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.randn(first[-1], nh * hd, device="cuda")
+    ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, first[-1]), dtype=torch.uint8, device="cuda")
+    o = torch.full((first[-1], nh * hd), float("nan"), dtype=dtypes(out), device="cuda")
+
+    def call(fn, o, **kw):
+        fn(plan, cache, q, i32(first), i32(slots), hd ** -0.5, o, ws, **kw)
+        torch.cuda.synchronize()
+        return Q.qkv_check_device_error()[0]
+    return call, o
+
+
+# pieces of 320 blocks, which take some 300 us and more: the warp that copies q waits for the last one's end; and tiles of
+# one stream before those of two, whose second stream's warps wait all that time
+LONG = {"whole tiles": dict(new=[4864], slots=[40960]), "one stream, then two": dict(new=[128] * 18 + [256], slots=[40960] * 19)}
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("name", list(LONG))
+def test_pieces_longer_than_the_limit(qkv, name, out):
+    import torch
+    call, want = problem(nh=8, nkv=8, hd=64, out=out, **LONG[name])
+    assert call(Q.qkv_prompt_attn_step, want) == 0
+    for _ in range(3):
+        got = torch.full_like(want, float("nan"))
+        assert call(Q.qkv_test_prompt_attn, got, wait_limit_us=100) == 0
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("page", [64, 12])  # copied by boxes, and row by row
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_withheld_end_is_flagged(qkv, out, page):
+    import torch
+    call, want = problem([700], [3000], 8, 2, 128, out, page=page)
+    assert call(Q.qkv_prompt_attn_step, want) == 0
+    got = torch.full_like(want, 5.0)
+    t0 = time.perf_counter()
+    assert call(Q.qkv_test_prompt_attn, got, wait_limit_us=500, withhold_end=True) == 2
+    assert time.perf_counter() - t0 < 10.0
+    assert call(Q.qkv_prompt_attn_step, got) == 0  # the context is usable, the workspace too
+    assert torch.equal(got, want)
+
+
+def test_hook_refusals(qkv):
+    for limit in (0, 1001):
+        call, o = problem([3], [40], 2, 1, 64, "f32")
+        with pytest.raises(Q.QkvError):
+            call(Q.qkv_test_prompt_attn, o, wait_limit_us=limit)
