@@ -48,14 +48,15 @@ qkv_status qkv_test_prefill_xchg_timeout(const qkv_plan* plan, const uint16_t* X
                                          void* kv_v, uint32_t wait_limit_us, void* stream);
 
 /* qkv_prompt_attn_step with every wait of the tensor cores' kernel (f16 caches; the others have no such waits) limited
- * to wait_limit_us microseconds (1 .. 1000) in which the CTA asks for no further block of slots, and, with withhold_end
- * non-zero, with the warps that write results never told that a piece's sums are complete: their wait runs out, they set
- * the device status flag 2 and leave (out and lse then hold nothing of use).  Without it the results are those of qkv_prompt_attn_step, however much
- * longer than the limit a CTA's pieces last.  Returns after the launches; read the flag with qkv_check_device_error,
- * which also clears it.
+ * to wait_limit_us microseconds (1 .. 1000) in which the CTA asks for no further block of slots.
+ *   fail 0: the results are those of qkv_prompt_attn_step, however much longer than the limit a CTA's pieces last;
+ *   fail 1: the warps that write results are never told that a piece's sums are complete, so their waits run out;
+ *   fail 2: one warp's waits for the sums of a block before another (out F32) count as run out, its partner's do not.
+ * Where a wait runs out the device status flag 2 is set, all warps leave, and out and lse hold nothing of use.
+ * Returns after the launches; read the flag with qkv_check_device_error, which also clears it.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 qkv_status qkv_test_prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* args,
-                                uint32_t wait_limit_us, int32_t withhold_end, void* stream);
+                                uint32_t wait_limit_us, int32_t fail, void* stream);
 
 /* The grid that qkv_attn_step launches its main kernel on for this plan and cache: CTAs in all, and
  * CTAs of a cluster (1: none).  The order of the sums follows from it, so it depends on sizes and

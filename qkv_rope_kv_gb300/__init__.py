@@ -714,11 +714,11 @@ def qkv_prompt_attn_step(plan: Plan, cache: PagedKv, q, first, lens, scale: floa
 
 
 def qkv_test_prompt_attn(plan: Plan, cache: PagedKv, q, first, lens, scale: float, out, workspace, window: int = 0,
-                         lse=None, wait_limit_us: int = 200, withhold_end: bool = False, stream=None):
-    """Test hook (include/qkv_test.h): qkv_prompt_attn_step with every wait limited to wait_limit_us without progress, and
-    with the end of every piece withheld, so the device status flag 2 gets set."""
+                         lse=None, wait_limit_us: int = 200, fail: int = 0, stream=None):
+    """Test hook (include/qkv_test.h): qkv_prompt_attn_step with every wait limited to wait_limit_us without progress; fail:
+    1 with the end of every piece withheld, 2 with some of one warp's waits taken for run out."""
     args = _prompt_args(plan, cache, q, first, lens, scale, out, workspace, window, lse)
-    _check(_lib.qkv_test_prompt_attn(plan.handle, cache.address, args, int(wait_limit_us), int(withhold_end),
+    _check(_lib.qkv_test_prompt_attn(plan.handle, cache.address, args, int(wait_limit_us), int(fail),
                                      cache._on(plan, stream)))
 
 

@@ -356,7 +356,7 @@ extern "C" qkv_status qkv_prompt_attn_workspace_bytes(const qkv_plan* plan, cons
 namespace {
 
 qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a, uint64_t wait_limit_ns,
-                       bool withhold_end, void* stream) {
+                       int32_t fail, void* stream) {
     PagedRowsParams p;
     std::memset(&p, 0, sizeof p);
     qkv_status st = view(plan, cache, &p.c);
@@ -386,7 +386,7 @@ qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qk
     p.out_stride = a->out_stride;
     p.lse = a->lse;
     p.wait_limit_ns = wait_limit_ns;
-    p.withhold_end = withhold_end;
+    p.fail = fail;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_paged_rows_plan(p, s);
     if (e == cudaSuccess) e = launch_paged_rows(p, s);
@@ -399,14 +399,15 @@ qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qk
 
 extern "C" qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a,
                                            void* stream) {
-    return prompt_attn(plan, cache, a, 0, false, stream);
+    return prompt_attn(plan, cache, a, 0, 0, stream);
 }
 
 // Test hook (include/qkv_test.h).
 extern "C" qkv_status qkv_test_prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a,
-                                           uint32_t wait_limit_us, int32_t withhold_end, void* stream) {
+                                           uint32_t wait_limit_us, int32_t fail, void* stream) {
     REQUIRE(wait_limit_us >= 1 && wait_limit_us <= 1000, "wait_limit_us must be in [1, 1000] (got %u)", wait_limit_us);
-    return prompt_attn(plan, cache, a, wait_limit_us * 1000ull, withhold_end != 0, stream);
+    REQUIRE(fail >= 0 && fail <= 2, "fail must be 0, 1 or 2 (got %d)", fail);
+    return prompt_attn(plan, cache, a, wait_limit_us * 1000ull, fail, stream);
 }
 
 extern "C" qkv_status qkv_prefix_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out) {

@@ -44,6 +44,7 @@ constexpr int kLaunchRegs = 128, kFewRegs = 72, kManyRegs = 184;
 static_assert(2 * 128 * (kFewRegs + kManyRegs) <= kThreads * kLaunchRegs, "registers");
 constexpr int kChunkBytes = kBlock * 128;  // 128 slots (or q rows) x 64 columns
 constexpr unsigned int kFlagTimeout = 2u;
+constexpr int kFailEnd = 1, kFailOneOfTwo = 2;  // p.fail
 constexpr int kControlBytes = 2560;  // barriers and small tables, behind the chunks
 // Weights are kept times 2^kShift; the maximum moves where 64 of a row are together above kMostWeight (64 times the
 // largest are not).
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         // Block number `block`'s weights are in O; those of the block before it are known to be.
         auto wait_pv = [&](int block) {
-            const bool there = __all_sync(0xffffffffu, wait_for(&ctl.pv_done, block & 1));
+            const bool there = __all_sync(0xffffffffu, wait_for(&ctl.pv_done, block & 1)) && (p.fail != kFailOneOfTwo || warp != 0);
             tc_fence_after();
             return there;
         };
@@ -546,7 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc_wait_st();
                         tc_fence_before();
-                        pair_any(quarter, false);  // all of O is as it is to be before either side's weights go into it
+                        // all of O is as it is to be before either side's weights go into it; and where one's wait ran out both
+                        // leave, or the other would stay at the next barrier
+                        ok = !pair_any(quarter, !ok);
                         round = 1;                 // the next one is the last
                     }
                     l += total;
@@ -948,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(&ctl.pv_done);
                     release(v_at);
                     next_block(v_at, v_phase);
-                    if (b + 1 == n && !p.withhold_end) tc_commit(&ctl.o_full[0]);
+                    if (b + 1 == n && p.fail != kFailEnd) tc_commit(&ctl.o_full[0]);
                     if (b + 2 >= n) continue;
                     wait_full(k_at, k_phase);
                     if (!ok) break;
@@ -980,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         if (t + 1 == halves) release(v_at);
                         if (!last) scores(t);
-                        else if (!p.withhold_end) tc_commit(&ctl.o_full[t]);
+                        else if (p.fail != kFailEnd) tc_commit(&ctl.o_full[t]);
                     }
                     if (!ok) break;
                     next_block(v_at, v_phase);

@@ -231,9 +231,10 @@ struct PagedRowsParams {
     const float* own_out;       // the same of the rows' own slots
     const float* own_lse;
     // Test hook of the tensor cores' bounded waits (zero in every product call): a non-zero limit replaces the default, and
-    // withhold_end makes no piece's end known to the warps that wait for it.
+    // fail 1 makes no piece's end known to the warps that wait for it, 2 (out F32) takes one warp's waits for a block's sums
+    // for run out.
     uint64_t wait_limit_ns;
-    int32_t withhold_end;
+    int32_t fail;
 };
 cudaError_t launch_paged_rows_plan(const PagedRowsParams& p, cudaStream_t stream);
 cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t stream);

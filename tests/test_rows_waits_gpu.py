@@ -15,13 +15,14 @@ def dtypes(out):
     return torch.bfloat16 if out == "bf16" else torch.float32
 
 
-def problem(new, slots, nh, nkv, hd, out, pages=64, page=64):
+def problem(new, slots, nh, nkv, hd, out, pages=64, page=64, grow=1.0):
     """Sequences of new[b] tokens at the end of slots[b] slots, of `pages` pages that their rows of the table name again and
-    again, and a call of them."""
+    again, and a call of them.  K of the second half of the pages is larger by `grow`."""
     import torch
     torch.manual_seed(1)
     plan = make_plan(nh, nkv, hd, "f16")
     k, v = (torch.randn(pages, page, nkv * hd, device="cuda").half() for _ in range(2))
+    k[pages // 2:] *= grow
     per = -(-max(slots) // page)
     table = (torch.arange(per, device="cuda") % pages).int()[None].repeat(len(new), 1).contiguous()
     cache = Q.PagedKv(plan, k, v, table)
@@ -65,14 +66,28 @@ def test_withheld_end_is_flagged(qkv, out, page):
     assert call(Q.qkv_prompt_attn_step, want) == 0
     got = torch.full_like(want, 5.0)
     t0 = time.perf_counter()
-    assert call(Q.qkv_test_prompt_attn, got, wait_limit_us=500, withhold_end=True) == 2
+    assert call(Q.qkv_test_prompt_attn, got, wait_limit_us=500, fail=1) == 2
     assert time.perf_counter() - t0 < 10.0
     assert call(Q.qkv_prompt_attn_step, got) == 0  # the context is usable, the workspace too
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("slots,pages", [(256, 4), (640, 10)])  # where sums are rescaled; where they are added to others too
+def test_one_of_two_warps_gives_up(qkv, slots, pages):
+    """A row's two warps, which meet at barriers of their own, leave together."""
+    import torch
+    call, want = problem([700], [slots], 32, 8, 128, "f32", pages=pages, grow=8.0)
+    assert call(Q.qkv_prompt_attn_step, want) == 0
+    got = torch.full_like(want, 5.0)
+    t0 = time.perf_counter()
+    assert call(Q.qkv_test_prompt_attn, got, wait_limit_us=500, fail=2) == 2
+    assert time.perf_counter() - t0 < 10.0
+    assert call(Q.qkv_prompt_attn_step, got) == 0
+    assert torch.equal(got, want)
+
+
 def test_hook_refusals(qkv):
-    for limit in (0, 1001):
-        call, o = problem([3], [40], 2, 1, 64, "f32")
+    call, o = problem([3], [40], 2, 1, 64, "f32")
+    for kw in (dict(wait_limit_us=0), dict(wait_limit_us=1001), dict(fail=3), dict(fail=-1)):
         with pytest.raises(Q.QkvError):
-            call(Q.qkv_test_prompt_attn, o, wait_limit_us=limit)
+            call(Q.qkv_test_prompt_attn, o, **kw)
