@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "ptx_sync.cuh"
 #include "qkv_internal.h"
 #include "qkv_test.h"
 
@@ -229,6 +230,7 @@ void rows_params(const qkv_plan* plan, const qkv_paged_kv* c, int32_t nt, PagedR
     p->nkv = plan->d.n_head_kv;
     p->hd = plan->d.head_dim;
     p->kv_f16 = plan->d.kv_dtype == QKV_F16 ? 1 : 0;
+    p->wait_limit_ns = static_cast<int32_t>(qkv_ptx::kWaitTimeoutNs);
 }
 
 // The kernel's shape, and byte offsets of the workspace's parts.
@@ -355,7 +357,7 @@ extern "C" qkv_status qkv_prompt_attn_workspace_bytes(const qkv_plan* plan, cons
 
 namespace {
 
-qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a, uint64_t wait_limit_ns,
+qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qkv_prompt_attn_args* a, int32_t wait_limit_ns,
                        int32_t fail, void* stream) {
     PagedRowsParams p;
     std::memset(&p, 0, sizeof p);
@@ -385,7 +387,7 @@ qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qk
     p.out = a->out;
     p.out_stride = a->out_stride;
     p.lse = a->lse;
-    p.wait_limit_ns = wait_limit_ns;
+    if (wait_limit_ns) p.wait_limit_ns = wait_limit_ns;
     p.fail = fail;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_paged_rows_plan(p, s);
@@ -407,7 +409,7 @@ extern "C" qkv_status qkv_test_prompt_attn(const qkv_plan* plan, const qkv_paged
                                            uint32_t wait_limit_us, int32_t fail, void* stream) {
     REQUIRE(wait_limit_us >= 1 && wait_limit_us <= 1000, "wait_limit_us must be in [1, 1000] (got %u)", wait_limit_us);
     REQUIRE(fail >= 0 && fail <= 2, "fail must be 0, 1 or 2 (got %d)", fail);
-    return prompt_attn(plan, cache, a, wait_limit_us * 1000ull, fail, stream);
+    return prompt_attn(plan, cache, a, static_cast<int32_t>(wait_limit_us) * 1000, fail, stream);
 }
 
 extern "C" qkv_status qkv_prefix_attn_workspace_bytes(const qkv_plan* plan, const qkv_paged_kv* cache, size_t* out) {

@@ -170,25 +170,20 @@ __device__ __forceinline__ void tm_st1(uint32_t a, uint32_t r) {
 }
 
 // As mbar_wait_bounded, without asking to be suspended: these waits are short, and there are many.  Some last for a whole
-// piece or, where a stream has no rows in the pieces before, for several; so one that has lasted for the limit gives up only
-// if no block was asked for meanwhile (a CTA's blocks are counted in *moved, and they come to an end).
-__device__ __forceinline__ bool wait_moving(uint64_t* bar, uint32_t parity, const uint32_t* moved, uint64_t limit_ns) {
+// piece or, where a stream has no rows in the pieces before, for several; so the limit counts from when the CTA last asked
+// for a block, which *moved holds (and blocks come to an end).  Nothing is kept of a wait's own beginning: code that is
+// inlined at every wait costs time (noting when it began and what *moved was then: 2.5 % of all calls).
+__device__ __forceinline__ uint32_t now_ns() { return static_cast<uint32_t>(globaltimer_ns()); }
+__device__ __forceinline__ bool wait_moving(uint64_t* bar, uint32_t parity, const uint32_t* moved, int32_t limit_ns) {
     const uint32_t at = smem_u32(bar);
-    uint64_t t0 = 0;
-    uint32_t seen = 0;
     for (int i = 0;; ++i) {
         uint32_t ok;
         asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok) : "r"(at), "r"(parity) : "memory");
         if (ok) return true;
         if ((i & 63) == 63) {
-            const uint64_t now = globaltimer_ns();
-            const uint32_t n = *static_cast<const volatile uint32_t*>(moved);
-            if (t0 == 0 || (now - t0 > limit_ns && n != seen)) {
-                t0 = now;
-                seen = n;
-            }
-            if (now - t0 > limit_ns) return false;
+            const uint32_t now = now_ns();  // (what is read after it may be later)
+            if (static_cast<int32_t>(now - *static_cast<const volatile uint32_t*>(moved)) > limit_ns) return false;
         }
     }
 }
@@ -318,7 +313,7 @@ struct Control {
     uint32_t live[kLiveRing][4];   // slots of a block that are there
     uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
     float top[2][kHalf];           // SPLIT: of the rows, by side
-    uint32_t moved;                // blocks that were asked for
+    uint32_t moved;                // when a block was last asked for, in ns
     uint32_t tmem;
 };
 static_assert(sizeof(Control) <= kControlBytes, "control");
@@ -356,10 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunk c of part `part` (0: rounded, 1: remainder) of stream t's q
     auto q_chunk = [&](int t, int part, int c) { return q_at + (((SPLIT ? 0 : t) * kParts + part) * NCH + c) * kChunkBytes; };
     auto chunk_at = [&](uint32_t n) { return ring_at + n % S::kStages * kChunkBytes; };
-    auto wait_for = [&](uint64_t* bar, uint32_t parity) {
-        return wait_moving(bar, parity, &ctl.moved, p.wait_limit_ns ? p.wait_limit_ns : kWaitTimeoutNs);
-    };
-    auto note_moved = [&](int block) { *static_cast<volatile uint32_t*>(&ctl.moved) = static_cast<uint32_t>(block) + 1u; };
+    auto wait_for = [&](uint64_t* bar, uint32_t parity) { return wait_moving(bar, parity, &ctl.moved, p.wait_limit_ns); };
+    auto note_moved = [&]() { *static_cast<volatile uint32_t*>(&ctl.moved) = now_ns(); };
 
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(512u)
@@ -368,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid < kPoisonRing) ctl.poison[tid] = 0;
     if (tid == 0) {
-        ctl.moved = 0;
+        ctl.moved = now_ns();
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&ctl.landed[s], 1);
             mbar_init(&ctl.full[s], box ? kLoadWarps - 1 : kLoadWarps);
@@ -1057,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         ++item;
                         if (kc == 0) {
-                            if (lane == 0) note_moved(block);
+                            if (lane == 0) note_moved();
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 const int s = 32 * c + lane;
@@ -1188,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     ++item;
                     if (kc == 0 && lane == 0) {
-                        if (i == 0) note_moved(block);
+                        if (i == 0) note_moved();
                         ctl.live[block % kLiveRing][i] = there;
                     }
                     pieces = (pieces & ~(15ull << (4 * (n % 16)))) | static_cast<u64>(piece & 15) << (4 * (n % 16));

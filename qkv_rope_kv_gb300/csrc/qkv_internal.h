@@ -230,10 +230,9 @@ struct PagedRowsParams {
     float* prefix_lse;
     const float* own_out;       // the same of the rows' own slots
     const float* own_lse;
-    // Test hook of the tensor cores' bounded waits (zero in every product call): a non-zero limit replaces the default, and
-    // fail 1 makes no piece's end known to the warps that wait for it, 2 (out F32) takes one warp's waits for a block's sums
-    // for run out.
-    uint64_t wait_limit_ns;
+    int32_t wait_limit_ns;      // of the tensor cores' bounded waits
+    // Test hook (zero in every product call): 1 makes no piece's end known to the warps that wait for it, 2 (out F32) takes one
+    // warp's waits for a block's sums for run out.
     int32_t fail;
 };
 cudaError_t launch_paged_rows_plan(const PagedRowsParams& p, cudaStream_t stream);
