@@ -44,6 +44,8 @@ constexpr int kLaunchRegs = 128, kFewRegs = 72, kManyRegs = 184;
 static_assert(2 * 128 * (kFewRegs + kManyRegs) <= kThreads * kLaunchRegs, "registers");
 constexpr int kChunkBytes = kBlock * 128;  // 128 slots (or q rows) x 64 columns
 constexpr unsigned int kFlagTimeout = 2u;
+// Named barriers: 1 to 4 of pairs of warps, then one for each stream's warps that have rows, and one for all of its warps.
+constexpr int kStreamBarrier = 5, kEndBarrier = 7;
 constexpr int kFailEnd = 1, kFailOneOfTwo = 2;  // p.fail
 constexpr int kControlBytes = 2560;  // barriers and small tables, behind the chunks
 // Weights are kept times 2^kShift; the maximum moves where 64 of a row are together above kMostWeight (64 times the
@@ -265,24 +267,19 @@ __device__ __noinline__ float plain_score(const PagedRowsParams& p, const float*
     return s;
 }
 
-// What the infinities and NaN of V that a row sees, in slots [lo, hi), make of its result.  The products do not tell: a
-// weight of zero (of a slot that the row does not see; or rounded, or a remainder) times them is NaN.  So blocks with
-// slots that only some rows see get zeros in their place, and rows that come out infinite or NaN look here.  side: the
-// columns of every other 16 (-1: all).
-__device__ __noinline__ void fix_row(const PagedRowsParams& p, int seq, int kv, int lo, int hi, int side, char* to, int es) {
-    for (int d = 0; d < p.hd; ++d) {
-        if (side >= 0 && ((d >> 4) & 1) != side) continue;
-        float more = 0.f;
-        for (int s = lo; s < hi; ++s) {
-            const int64_t row = row_offset(p.c, seq, s);
-            if (row < 0) continue;
-            const float v = __half2float(static_cast<const __half*>(p.c.v)[row + static_cast<int64_t>(kv) * p.hd + d]);
-            if (!(fabsf(v) < CUDART_INF_F)) more += v;
-        }
-        if (more == 0.f) continue;
-        if (es == 2) reinterpret_cast<uint16_t*>(to)[d] = bf16_bits(more);
-        else reinterpret_cast<float*>(to)[d] = more;
+__device__ __forceinline__ bool finite_f16x8(const uint4& v) {
+    return finite_f16x2(v.x) && finite_f16x2(v.y) && finite_f16x2(v.z) && finite_f16x2(v.w);
+}
+// The kinds of eight values of f16: bit j of the low byte for +inf in value j, of the next -inf, of the third NaN.
+__device__ __forceinline__ uint32_t kinds_of(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t h = w[j >> 1] >> (16 * (j & 1));
+        if ((h & 0x7c00u) == 0x7c00u) r |= ((h & 0x3ffu) != 0 ? 0x10000u : (h & 0x8000u) != 0 ? 0x100u : 1u) << j;
     }
+    return r;
 }
 
 // 16 bytes of values of es bytes, to any address of such values.
@@ -304,6 +301,14 @@ __device__ __forceinline__ bool pair_any(int quarter, bool yes) {
     uint32_t any;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(any) : "r"(static_cast<uint32_t>(yes)), "r"(1 + quarter) : "memory");
+    return any != 0;
+}
+
+// Whether `yes` holds in any lane of `warps` warps, which meet here.
+__device__ __forceinline__ bool stream_any(int barrier, int warps, bool yes) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(static_cast<uint32_t>(yes)), "r"(barrier), "r"(32 * warps) : "memory");
     return any != 0;
 }
 
@@ -333,6 +338,108 @@ __device__ __forceinline__ bool clean16(uint32_t at) {
     if (finite_f16x2(v[0]) && finite_f16x2(v[1]) && finite_f16x2(v[2]) && finite_f16x2(v[3])) return false;
     keep_finite(at, v);
     return true;
+}
+
+// What the infinities and NaN of V that a row sees in slots [lo, hi) make of its result.  The products do not tell: a
+// weight of zero (of a slot that the row does not see; or rounded, or a remainder) times them is NaN.  So blocks with
+// slots that only some rows see get zeros in their place, and where any row of a stream came out infinite or NaN, or had
+// such zeros, the stream's `warps` warps that have rows look here, together: each reads every warps-th 32 slots of V, 16 bytes a
+// lane, and notes kind and column of what it finds, once for all rows where all see the slot and else for each row that
+// does; then every row takes its own.  A row's span is empty where it takes no part; SPLIT, a row's two threads have the
+// columns of every other 16.  8191 tokens of 10 heads over 2 with one infinity in an early slot take 0.36 ms instead of 0.17, out
+// F32 0.57 instead of 0.32.  (A search by each row for itself, a value at a time, would take a second for 32768 slots.)
+constexpr int kKindWords = 3 * 128 / 32, kCommon = kHalf;  // of a row: a bit for each kind and column
+constexpr int kSpansAt = 4 * (kHalf + 1) * kKindWords;
+static_assert(kSpansAt % 16 == 0 && kSpansAt + kHalf * sizeof(int2) <= kChunkBytes, "what the rows' warps leave each other");
+template <bool SPLIT, int NCH>
+__device__ __noinline__ void mend_rows(const PagedRowsParams& p, int warps, int seq, int kv, int lo, int hi, char* to, int es) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = SPLIT ? 0 : warp >> 2, side = SPLIT ? warp >> 2 : -1, row = 32 * (warp & 3) + lane;
+    const int rows = SPLIT ? 16 * warps : 32 * warps, rank = SPLIT ? (warp & 3) + side * (warps / 2) : warp & 3;
+    const int barrier = kStreamBarrier + t;
+    unsigned char* scratch = smem + t * NCH * kChunkBytes;  // q's place
+    uint32_t* kinds = reinterpret_cast<uint32_t*>(scratch);
+    int2* spans = reinterpret_cast<int2*>(scratch + kSpansAt);
+    volatile uint32_t* moved = &reinterpret_cast<Control*>(smem + Shape<SPLIT, NCH>::kControlAt)->moved;
+    const bool live = lo < hi;
+    if (side <= 0) {  // (a row's two sides see the same)
+        spans[row] = make_int2(lo, hi);
+        for (int k = 0; k < kKindWords; ++k) kinds[row * kKindWords + k] = 0;
+        if (row < kKindWords) kinds[kCommon * kKindWords + row] = 0;
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * warps) : "memory");
+    int from = 0x7fffffff, to_all = 0x7fffffff, from_all = 0, end = 0;  // slots that any row sees, and that all do
+    for (int r = lane; r < rows; r += 32) {
+        const int2 s = spans[r];
+        if (s.x >= s.y) continue;
+        from = min(from, s.x), from_all = max(from_all, s.x), to_all = min(to_all, s.y), end = max(end, s.y);
+    }
+    from = __reduce_min_sync(0xffffffffu, from), from_all = __reduce_max_sync(0xffffffffu, from_all);
+    to_all = __reduce_min_sync(0xffffffffu, to_all), end = __reduce_max_sync(0xffffffffu, end);
+    constexpr int kLanes = 8 * NCH, kSlots = 32 / kLanes, kLoads = 32 / kSlots;  // of a slot; slots of a load; loads of 32 slots
+    const int c = lane % kLanes, which = lane / kLanes;
+    const bool has = 8 * c < p.hd;
+    const uint4* v0 = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.c.v) + static_cast<int64_t>(kv) * p.hd + (has ? 8 * c : 0));
+    auto ask = [&](int at) { return at + lane < end ? page_ref(p.c, seq, at + lane) : PageRef{0, -1}; };
+    uint32_t common = 0;
+    if (end > 0) {
+        from += 32 * rank;
+        PageRef asked = ask(from);
+        for (; from < end; from += 32 * warps) {
+            const int64_t off = asked.in_page >= 0 ? row_offset(p.c, asked) : -1;
+            asked = ask(min(from, end) + 32 * warps);
+            if (lane == 0) *moved = now_ns();
+            uint4 v[kLoads];
+            bool clean = true;
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int64_t o = __shfl_sync(0xffffffffu, off, kSlots * k + which);
+                v[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (o >= 0 && has) v[k] = __ldg(v0 + o / 8);
+            }
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) clean = clean && finite_f16x8(v[k]);
+            if (__all_sync(0xffffffffu, clean)) continue;
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int slot = from + kSlots * k + which;
+                uint32_t found = finite_f16x8(v[k]) ? 0u : kinds_of(v[k]);
+                if (slot >= from_all && slot < to_all) {
+                    common |= found;
+                    found = 0;
+                }
+                for (uint32_t lanes = __ballot_sync(0xffffffffu, found != 0); lanes; lanes &= lanes - 1) {
+                    const int l = __ffs(lanes) - 1, at = l % kLanes, s = from + kSlots * k + l / kLanes;
+                    const uint32_t f = __shfl_sync(0xffffffffu, found, l);
+                    for (int r = lane; r < rows; r += 32) {
+                        const int2 see = spans[r];
+                        if (s < see.x || s >= see.y) continue;
+                        for (int kind = 0; kind < 3; ++kind)
+                            if ((f >> (8 * kind)) & 255u)
+                                atomicOr(&kinds[r * kKindWords + 4 * kind + (at >> 2)], ((f >> (8 * kind)) & 255u) << (8 * (at & 3)));
+                    }
+                }
+            }
+        }
+    }
+    for (int kind = 0; kind < 3; ++kind)
+        if ((common >> (8 * kind)) & 255u)
+            atomicOr(&kinds[kCommon * kKindWords + 4 * kind + (c >> 2)], ((common >> (8 * kind)) & 255u) << (8 * (c & 3)));
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * warps) : "memory");
+    if (!live) return;
+    for (int w = 0; 32 * w < p.hd; ++w) {
+        uint32_t any[3];
+        for (int kind = 0; kind < 3; ++kind) any[kind] = kinds[row * kKindWords + 4 * kind + w] | kinds[kCommon * kKindWords + 4 * kind + w];
+        for (uint32_t left = any[0] | any[1] | any[2]; left; left &= left - 1) {
+            const int b = __ffs(left) - 1, d = 32 * w + b;
+            if (side >= 0 && ((d >> 4) & 1) != side) continue;
+            const bool plus = (any[0] >> b) & 1u, minus = (any[1] >> b) & 1u, nan = ((any[2] >> b) & 1u) || (plus && minus);
+            const uint32_t bits = nan ? 0x7fc00000u : plus ? 0x7f800000u : 0xff800000u;
+            if (es == 2) reinterpret_cast<uint16_t*>(to)[d] = static_cast<uint16_t>(bits >> 16);
+            else reinterpret_cast<uint32_t*>(to)[d] = bits;
+        }
+    }
 }
 
 template <bool SPLIT, int NCH>
@@ -422,7 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 32 * quarter + lane, i = r / p.per_block, g = r - i * p.per_block;
             const int h_row = kv * G + g0 + g;
             const int64_t row = tile.row0 + i;
-            const bool mine = i < tile.ntok && g < heads, busy = 32 * quarter < tile.ntok * p.per_block;
+            const bool mine = i < tile.ntok && g < heads;
+            const int busy_pairs = (tile.ntok * p.per_block + 31) / 32;
+            const bool busy = quarter < busy_pairs;
             // The tensor cores cut bits off a score's sums too, each towards zero: 2^-23 of it are missing on average (128
             // columns; log sum exp comes out 6e-7 too small), and given back here.
             const float unscale = mine ? __ldcg(p.q_unscale + row * p.nh + h_row) * (1.f + 1.1920929e-7f) : 1.f;
@@ -580,9 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool there = ok && __all_sync(0xffffffffu, wait_for(&ctl.o_full[0], o_phase));
             o_phase ^= 1u;
             ok = !pair_any(quarter, !there);
-            if (!ok) break;
             tc_fence_after();
             if (busy) {
+                const bool put = mine && ok;  // (nothing is written where a wait ran out)
+                float* to;
                 const bool both = n > kFold;
                 ctl.top[side][r] = l;
                 pair_any(quarter, false);
@@ -591,7 +701,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool whole = x.whole(), empty = see_lo >= see_hi;
                 const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
                 float* part = part_of(p, blockIdx.x, x.first);
-                float* to;
                 if (!whole) to = part_o(p, part, r);
                 else if (!p.first) to = p.prefix_out + (row * p.nh + h_row) * p.hd;
                 else to = static_cast<float*>(p.out) + row * p.out_stride + static_cast<int64_t>(h_row) * p.hd;
@@ -626,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int from = k + (lane >> 2);
                         char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(to), from)) + 4 * c +
                                     16 * (lane & 3);
-                        const bool has = __shfl_sync(0xffffffffu, mine, from);
+                        const bool has = __shfl_sync(0xffffffffu, put, from);
                         uint4 w4;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w)
@@ -636,20 +745,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (__any_sync(0xffffffffu, mine && (poison || !(odd == 0.f)))) {
-                    if (mine)
-                        fix_row(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock), min(see_hi, tile.lo + x.to * kBlock), side,
-                                reinterpret_cast<char*>(to), 4);
-                    __syncwarp();
-                }
-                if (mine && side == 0) {
+                if (put && side == 0) {
                     float* lse = p.first ? p.lse : p.prefix_lse;
                     if (!whole) *part_ml(part, r) = make_float2(m - kShift, l);
                     else if (lse) lse[row * p.nh + h_row] = lse_of(m - kShift, l, empty);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                const bool live = put && l > 0.f;
+                // (a sum of weights that is NaN makes all of the row NaN already)
+                if (stream_any(kStreamBarrier, 2 * busy_pairs, live && (poison || !(odd == 0.f))))
+                    mend_rows<SPLIT, NCH>(p, 2 * busy_pairs, tile.seq, kv, live ? max(see_lo, tile.lo + x.from * kBlock) : 0,
+                                          live ? min(see_hi, tile.lo + x.to * kBlock) : 0, reinterpret_cast<char*>(to), 4);
                 tc_fence_before();
             }
+            // all warps come here, whatever became of their waits, and leave together
+            if (stream_any(kEndBarrier, kSoftWarps, !ok)) {
+                ok = false;
+                break;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.q_free[0]);
         }
@@ -673,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 32 * quarter + lane, in_part = r / p.per_block, g = r - in_part * p.per_block;
             const int i = token0 + in_part, row = tile.row0 + i, h_row = kv * G + g0 + g;
             const bool mine = in_part < p.part_tokens && i < tile.ntok && g < heads;
-            const bool busy = 32 * quarter < min(p.part_tokens, tile.ntok - token0) * p.per_block;
+            const int busy_warps = (min(p.part_tokens, tile.ntok - token0) * p.per_block + 31) / 32;
+            const bool busy = quarter < busy_warps;
             const float unscale = mine ? __ldcg(p.q_unscale + static_cast<int64_t>(row) * p.nh + h_row) : 1.f;
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, i, see_lo, see_hi);
@@ -771,12 +885,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
             }
-            if (!ok) break;
-            ok = __all_sync(0xffffffffu, wait_for(&ctl.o_full[t], o_phase));
+            ok = ok && __all_sync(0xffffffffu, wait_for(&ctl.o_full[t], o_phase));
             o_phase ^= 1u;
-            if (!ok) break;
             tc_fence_after();
             if (busy) {
+                const bool put = mine && ok;  // (nothing is written where a wait ran out)
                 const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
                 const bool whole = x.whole(), empty = see_lo >= see_hi;
                 const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
@@ -827,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 32; k += 4) {
                         const int from = k + (lane >> 3);
                         char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(to), from)) + skip;
-                        const bool has = __shfl_sync(0xffffffffu, mine, from);
+                        const bool has = __shfl_sync(0xffffffffu, put, from);
                         uint4 w4;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w)
@@ -837,19 +950,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (__any_sync(0xffffffffu, mine && (poison || !(odd == 0.f)))) {
-                    if (mine)
-                        fix_row(p, tile.seq, kv, max(see_lo, tile.lo + x.from * kBlock), min(see_hi, tile.lo + x.to * kBlock), -1, to, es);
-                    __syncwarp();
-                }
-                if (mine) {
+                // (a sum of weights that is NaN makes all of the row NaN already)
+                const bool live = put && l > 0.f;
+                // (a sum of weights that is NaN makes all of the row NaN already)
+                if (stream_any(kStreamBarrier + t, busy_warps, live && (poison || !(odd == 0.f))))
+                    mend_rows<SPLIT, NCH>(p, busy_warps, tile.seq, kv, live ? max(see_lo, tile.lo + x.from * kBlock) : 0,
+                                          live ? min(see_hi, tile.lo + x.to * kBlock) : 0, to, es);
+                if (put) {
                     float* lse = p.first ? p.lse : p.prefix_lse;
                     if (!whole) *part_ml(part, t * kHalf + r) = make_float2(m - kShift, l);
                     else if (lse) lse[static_cast<int64_t>(row) * p.nh + h_row] = lse_of(m - kShift, l, empty);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
             }
+            // all warps of the stream come here, whatever became of their waits
+            // all warps of the stream come here, whatever became of their waits, and leave together
+            if (stream_any(kEndBarrier + t, 4, !ok)) {
+                ok = false;
+                break;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.q_free[t]);
         }
