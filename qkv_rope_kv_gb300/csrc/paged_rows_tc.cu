@@ -318,6 +318,7 @@ struct Control {
     uint32_t live[kLiveRing][4];   // slots of a block that are there
     uint32_t poison[kPoisonRing];  // n: in piece n, V had infinities or NaN that were replaced
     float top[2][kHalf];           // SPLIT: of the rows, by side
+    bool grow[2][kHalf];           // whether a row's maximum is to be looked for
     uint32_t moved;                // when a block was last asked for, in ns
     uint32_t tmem;
 };
@@ -599,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const float2 s2 = unpack2(add2(sum[0], sum[1]));
                         total = s2.x + s2.y;
-                        if (round == 2 || !pair_any(quarter, !ok || (mine && (m == -CUDART_INF_F || !(total <= kMostWeight))))) break;
+                        const bool grow = mine && (m == -CUDART_INF_F || !(total <= kMostWeight));
+                        if (round == 2 || !pair_any(quarter, !ok || grow)) break;
                         if (pair_any(quarter, !ok)) {  // a wait ran out: both leave
                             ok = false;
                             break;
@@ -633,9 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int c = 0; c < 2; ++c)
                                 tops[c] = max3(tops[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
                         const float top = fmaxf(tops[0], tops[1]) * unscale;
+                        // (moved only where the row's own sums ask for it: its bits do not depend on what other rows see)
                         ctl.top[side][r] = top;
+                        ctl.grow[side][r] = grow;
                         pair_any(quarter, false);
-                        const float next = mine ? fmaxf(m, fmaxf(top, ctl.top[side ^ 1][r])) : m;
+                        const float next = grow || ctl.grow[side ^ 1][r] ? fmaxf(m, fmaxf(top, ctl.top[side ^ 1][r])) : m;
                         const float keep = m == next ? 1.f : ex2(m - next);
                         m = next;
                         l *= keep;
@@ -849,14 +853,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             const float2 s2 = unpack2(add2(sum[0], sum[1]));
                             total = s2.x + s2.y;
-                            if (round == 2 || !__any_sync(0xffffffffu, mine && (m == -CUDART_INF_F || !(total <= kMostWeight)))) break;
+                            const bool grow = mine && (m == -CUDART_INF_F || !(total <= kMostWeight));
+                            if (round == 2 || !__any_sync(0xffffffffu, grow)) break;
                             float tops[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                             for (int k = 0; k < 32; k += 2)
 #pragma unroll
                                 for (int c = 0; c < 2; ++c)
                                     tops[c] = max3(tops[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
-                            const float next = mine ? fmaxf(m, fmaxf(tops[0], tops[1]) * unscale) : m;
+                            // (moved only where the row's own sum asks for it: its bits do not depend on what other rows see)
+                            const float next = grow ? fmaxf(m, fmaxf(tops[0], tops[1]) * unscale) : m;
                             const float keep = m == next ? 1.f : ex2(m - next);
                             m = next;
                             l *= keep;

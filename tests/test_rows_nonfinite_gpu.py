@@ -143,3 +143,25 @@ def test_shared_prefix(qkv, out):
     expect = want.clone()
     expect[:, 0, :, 2], expect[9, 1, :, 4] = INF, -INF
     assert same(got, expect)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("new,slots,hd,window", [(700, 900, 128, 0), (700, 5000, 64, 0), (2000, 6000, 128, 1500), (900, 1500, 96, 40)])
+def test_large_scores_of_others(qkv, out, new, slots, hd, window):
+    """K that grows much in slots that a row does not see, but its neighbours do, leaves the row's bits alone."""
+    import torch
+    call = Call(new, slots, hd, out, page=16, window=window)
+    want, lse, _ = call.run()
+    half = slots - new // 2
+    rows, checked = call.k.clone(), 0
+    for changed in (range(half, slots), range(0, half)):  # later slots, and earlier ones, which only a window hides
+        call.k.copy_(rows)
+        at = torch.tensor([int(call.table[0, s // call.page]) * call.page + s % call.page for s in changed], device="cuda")
+        call.k.view(-1, call.nkv * hd)[at] *= 20
+        got, lse2, _ = call.run()
+        free = ~torch.stack([call.sees(changed[0]), call.sees(changed[-1])]).any(0)
+        end = torch.arange(slots - new + 1, slots + 1, device="cuda")
+        free &= (end <= changed[0]) | ((end - window > changed[-1]) if window else False)
+        checked += int(free.sum())
+        assert same(got[free], want[free]) and same(lse[free], lse2[free])
+    assert checked
