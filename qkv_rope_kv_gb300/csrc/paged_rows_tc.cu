@@ -256,17 +256,6 @@ __device__ __forceinline__ bool finite_f16x2(uint32_t w) {
     return (w & 0x7c00u) != 0x7c00u && (w & 0x7c000000u) != 0x7c000000u;
 }
 
-// A score in f32 from memory, in log2 terms: for K with infinities or NaN, whose products with the two parts of q need not
-// be those with q (0 * inf where the remainder is zero).
-__device__ __noinline__ float plain_score(const PagedRowsParams& p, const float* q, int seq, int slot, int kv) {
-    const int64_t row = row_offset(p.c, seq, slot);
-    if (row < 0) return -CUDART_INF_F;
-    const __half* k = static_cast<const __half*>(p.c.k) + row + static_cast<int64_t>(kv) * p.hd;
-    float s = 0.f;
-    for (int d = 0; d < p.hd; ++d) s = fmaf(__ldcg(q + d) * (p.scale * kLog2e), __half2float(k[d]), s);
-    return s;
-}
-
 __device__ __forceinline__ bool finite_f16x8(const uint4& v) {
     return finite_f16x2(v.x) && finite_f16x2(v.y) && finite_f16x2(v.z) && finite_f16x2(v.w);
 }
@@ -280,6 +269,56 @@ __device__ __forceinline__ uint32_t kinds_of(const uint4& v) {
         if ((h & 0x7c00u) == 0x7c00u) r |= ((h & 0x3ffu) != 0 ? 0x10000u : (h & 0x8000u) != 0 ? 0x100u : 1u) << j;
     }
     return r;
+}
+
+// SPLIT: scores of 64 slots from `slot0` on, in tensor memory at `at`, of which some are NaN in some rows.  For K with infinities
+// the products with the two parts of q need not be those with q (0 * inf where the remainder is zero), so those
+// scores are made anew: an infinity of that sign, or NaN where K or q have one, signs differ or q has a zero there.  A
+// warp reads K of all slots together, 8 bytes a lane; a lane looks at its own row's q only where K is infinite.  q_row:
+// null for rows that have no say; seen: slots that the row sees.  (One such slot costs next to nothing, an infinity in
+// every slot of 40000 20 to 30 times the call's time; each score by its own thread from memory took a millisecond a block.)
+__device__ __noinline__ void mend_scores(const PagedRowsParams& p, uint32_t at, const float* q_row, int seq, int kv, int slot0,
+                                         uint32_t seen0, uint32_t seen1) {
+    const int lane = threadIdx.x & 31;
+    const bool mine = q_row != nullptr;
+    const uint32_t any0 = __reduce_or_sync(0xffffffffu, mine ? seen0 : 0u), any1 = __reduce_or_sync(0xffffffffu, mine ? seen1 : 0u);
+    const int64_t off0 = (any0 >> lane) & 1u ? row_offset(p.c, seq, slot0 + lane) : -1;
+    const int64_t off1 = (any1 >> lane) & 1u ? row_offset(p.c, seq, slot0 + 32 + lane) : -1;
+    const __half* pool = static_cast<const __half*>(p.c.k) + static_cast<int64_t>(kv) * p.hd + 4 * lane;
+#pragma unroll 1
+    for (int k0 = 0; k0 < 64; k0 += 8) {
+        uint2 w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t o = __shfl_sync(0xffffffffu, k0 < 32 ? off0 : off1, (k0 + k) & 31);
+            w[k] = make_uint2(0u, 0u);
+            if (o >= 0 && 4 * lane < p.hd) w[k] = __ldg(reinterpret_cast<const uint2*>(pool + o));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t lanes = __ballot_sync(0xffffffffu, !finite_f16x2(w[k].x) || !finite_f16x2(w[k].y));
+            if (!lanes) continue;  // q is at fault
+            float f = __uint_as_float(tm_ld1(at + k0 + k));
+            const bool need = mine && f != f && (((k0 < 32 ? seen0 : seen1) >> ((k0 + k) & 31)) & 1u);
+            bool plus = false, minus = false, nan = false;
+            for (; lanes; lanes &= lanes - 1) {
+                const int l = __ffs(lanes) - 1;
+                const uint32_t x = __shfl_sync(0xffffffffu, w[k].x, l), y = __shfl_sync(0xffffffffu, w[k].y, l);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t h = (j < 2 ? x : y) >> (16 * (j & 1));
+                    if (!need || (h & 0x7c00u) != 0x7c00u) continue;
+                    const float q = __ldcg(q_row + 4 * l + j);
+                    if ((h & 0x3ffu) != 0 || !(fabsf(q) > 0.f) || p.scale == 0.f) nan = true;
+                    else if ((q < 0.f) != (p.scale < 0.f) != ((h & 0x8000u) != 0)) minus = true;
+                    else plus = true;
+                }
+                if (__all_sync(0xffffffffu, !need || nan || (plus && minus))) break;
+            }
+            if (need && !nan && plus != minus) f = plus ? CUDART_INF_F : -CUDART_INF_F;
+            __syncwarp();
+            tm_st1(at + k0 + k, __float_as_uint(f));
+        }
+    }
 }
 
 // 16 bytes of values of es bytes, to any address of such values.
@@ -539,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, i, see_lo, see_hi);
             float m = -CUDART_INF_F, l = 0.f;  // l: of this side's columns
+            bool live_row = mine;              // a row that has come to NaN has no say any more
 #pragma unroll 1
             for (int b = 0; b < n; ++b) {
                 const int t = b & 1;
@@ -600,27 +640,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const float2 s2 = unpack2(add2(sum[0], sum[1]));
                         total = s2.x + s2.y;
-                        const bool grow = mine && (m == -CUDART_INF_F || !(total <= kMostWeight));
+                        const bool grow = live_row && (m == -CUDART_INF_F || !(total <= kMostWeight));
                         if (round == 2 || !pair_any(quarter, !ok || grow)) break;
                         if (pair_any(quarter, !ok)) {  // a wait ran out: both leave
                             ok = false;
                             break;
                         }
                         if (round == 0) {
-                            const bool odd = __any_sync(0xffffffffu, mine && total != total);
-                            if (odd) {  // K with infinities or NaN: scores from memory, in the place of those that are NaN
+                            const bool odd = __any_sync(0xffffffffu, live_row && total != total);
+                            if (odd) {  // K with infinities, or NaN
                                 const float* q_row = p.q + row * p.q_stride + static_cast<int64_t>(h_row) * p.hd;
 #pragma unroll
                                 for (int c = 0; c < 2; ++c) tm_st32(at + 32 * c, v[c]);
                                 tc_wait_st();
-#pragma unroll 1
-                                for (int k = 0; k < 64; ++k) {
-                                    float f = __uint_as_float(tm_ld1(at + k));
-                                    if (mine && f != f && ((seen(2 * side + (k >> 5)) >> (k & 31)) & 1u))
-                                        f = plain_score(p, q_row, tile.seq, j0 + 64 * side + k, kv) / unscale;
-                                    __syncwarp();
-                                    tm_st1(at + k, __float_as_uint(f));
-                                }
+                                mend_scores(p, at, live_row ? q_row : nullptr, tile.seq, kv, j0 + 64 * side, seen(2 * side), seen(2 * side + 1));
                                 tc_wait_st();
                                 tm_ld32(at, v[0]);
                                 tm_ld32(at + 32, v[1]);
@@ -659,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         round = 1;                 // the next one is the last
                     }
                     l += total;
+                    live_row = live_row && total == total;
                     tc_wait_st();
                 }
                 if (!ok) break;
@@ -796,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, i, see_lo, see_hi);
             float m = -CUDART_INF_F, l = 0.f;
+            bool live_row = mine;  // a row that has come to NaN has no say any more
             for (int u = x.from; u < x.to; ++u) {
                 ok = __all_sync(0xffffffffu, wait_for(&ctl.s_full[t], s_phase));
                 s_phase ^= 1;
@@ -853,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             const float2 s2 = unpack2(add2(sum[0], sum[1]));
                             total = s2.x + s2.y;
-                            const bool grow = mine && (m == -CUDART_INF_F || !(total <= kMostWeight));
+                            const bool grow = live_row && (m == -CUDART_INF_F || !(total <= kMostWeight));
                             if (round == 2 || !__any_sync(0xffffffffu, grow)) break;
                             float tops[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -883,6 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                         }
                         l += total;
+                        live_row = live_row && total == total;
                         tc_wait_st();
                     }
                     tc_fence_before();

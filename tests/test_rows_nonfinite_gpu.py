@@ -3,7 +3,9 @@ bits alone, raise no flag, and cost about as much as the call itself."""
 import pytest
 
 import qkv_rope_kv_gb300 as Q
+import rows_reference as ref
 from test_paged_gpu import make_plan
+from test_rows_gpu import attend64
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +167,67 @@ def test_large_scores_of_others(qkv, out, new, slots, hd, window):
         checked += int(free.sum())
         assert same(got[free], want[free]) and same(lse[free], lse2[free])
     assert checked
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("new,slots,hd,kw", [
+    (8191, 8191, 128, {}),
+    (300, 40000, 64, dict(page=12)),
+    (2000, 6000, 128, dict(window=1500)),
+], ids=str)
+def test_nan_scores(qkv, new, slots, hd, kw, out):
+    """A NaN in K makes the rows that see it NaN, one in q (or an infinity) its row; the others keep their bits."""
+    import torch
+    call = Call(new, slots, hd, out, **kw)
+    want, lse, t0 = call.run()
+    dead = torch.zeros(new, call.nkv, call.G, dtype=torch.bool, device="cuda")
+    for slot in (5, slots - new // 2):
+        call.k[call.row(slot)][7] = NAN
+        dead[:, 0] |= call.sees(slot)[:, None]
+    got, lse2, t1 = call.run()
+    q = call.q.view(new, call.nkv, call.G, hd)
+    q[3, 1, 2, 5], q[new // 2, 1, 0, 0], q[new - 1, 1, 1, hd - 1] = NAN, INF, -INF
+    got3, lse3, t2 = call.run()
+    for dead, o, l in ((dead, got, lse2), (dead | ~torch.isfinite(q).all(-1), got3, lse3)):
+        assert torch.isnan(o[dead]).all() and torch.isnan(l[dead]).all()
+        assert same(o[~dead], want[~dead]) and same(l[~dead], lse[~dead])
+    assert max(t1, t2) < 5 * t0 + 0.5, "%.3f and %.3f ms, %.3f without" % (t1, t2, t0)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("value,d", [(INF, 0), (-INF, 63)])
+def test_infinite_k(qkv, out, value, d):
+    """A row whose q has the other sign there sees the slot with no weight, one of the same sign is NaN."""
+    import torch
+    new, slots, hd, slot = 700, 5000, 64, 1234
+    call = Call(new, slots, hd, out, page=16)
+    _, _, t0 = call.run()
+    call.k[call.row(slot)][d] = value
+    got, lse, t1 = call.run()
+    q = call.q.view(new, call.nkv, call.G, hd)[:, 0]
+    dead = (q[..., d] < 0) == (value < 0)
+    assert dead.any() and not dead.all()
+    assert torch.isnan(got[:, 0][dead]).all() and torch.isnan(lse[:, 0][dead]).all()
+    at = [i for i in range(slots) if i != slot]
+    K, V = (x[call.table[0].long()].view(-1, call.nkv, hd)[at][:, 0] for x in (call.k, call.v))
+    hi = torch.arange(slots - new + 1, slots + 1, device="cuda") - 1
+    want, most, size = attend64(q, K, V, hi, hd ** -0.5)
+    ds = (hd + 16) * 2 * ref.U * size + (2.0 ** -11 * size if out == "bf16" else 0)
+    bound = (torch.expm1(2 * ds) + (slots / 8 + 64) * 2 * ref.U) * most
+    if out == "bf16":
+        bound = bound + 2.0 ** -11 * most + 2.0 ** -8 * (want.abs() + bound)
+    assert ((got[:, 0].double() - want).abs() <= bound)[~dead].all()
+    assert t1 < 5 * t0 + 0.5, "%.3f ms, %.3f without" % (t1, t0)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_every_k_infinite(qkv, out):
+    """Every row is NaN, by +inf or by nothing else than -inf."""
+    import torch
+    call = Call(600, 5000, 128, out)
+    _, _, t0 = call.run()
+    call.k[..., 3] = INF
+    call.k[..., 128 + 3] = -INF
+    got, _, t1 = call.run()
+    assert torch.isnan(got).all()
+    assert t1 < 40 * t0 + 0.5, "%.3f ms, %.3f without" % (t1, t0)
