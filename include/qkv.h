@@ -579,7 +579,8 @@ qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const 
  * slots at a time, whose sums are added to each other rounded to nearest; 1e-6 of the result over 30000 slots).
  * |V| (f32) times the number of slots is to stay below the largest f32.
  * Work is split over the GPU and joined in a fixed order: results do not depend on timing.  The workspace may hold
- * anything and is not shared by calls that overlap on the GPU.
+ * anything and is not shared by calls that overlap on the GPU; its first 4096 bytes are left as they are, so it may be that of
+ * qkv_attn_step or qkv_prefix_attn_step in turn.
  * Errors: INVALID_ARG, UNSUPPORTED (out_dtype, n_head % n_head_kv != 0), CUDA. */
 typedef struct qkv_prompt_attn_args {
     const float* q;         /* device, nt rows of nqt floats */
@@ -645,8 +646,9 @@ typedef struct qkv_evict_args {
                                  * length is passed on as it is */
     float* weight_out;          /* device, as slot_weight and slot_pos, and may be those: slots below */
     int32_t* pos_out;           /* min(len, budget) are written */
-    void* d_workspace;          /* device, qkv_evict_workspace_bytes bytes, 4-byte aligned, any contents,
-                                 * not shared by calls that overlap on the GPU */
+    void* d_workspace;          /* device, qkv_evict_workspace_bytes bytes, 4-byte aligned, any contents, all of
+                                 * which is overwritten (so not an attention's workspace), not shared by
+                                 * calls that overlap on the GPU */
     size_t workspace_bytes;
     int32_t budget;             /* >= 1 */
     int32_t recent;             /* 0 .. budget */

@@ -66,6 +66,10 @@ qkv_status view(const qkv_plan* plan, const qkv_paged_kv* c, PagedView* v) {
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
+// What a caller zeroes of a workspace once: the counters of the attention of one token, which it leaves zero.  The attention of
+// many rows keeps off them, so that one workspace serves both.
+constexpr size_t kCounterBytes = 4096;
+
 // Floats of a row of scores: whole units of slots, 16-byte aligned rows.
 int64_t score_stride(const qkv_paged_kv* c) { return (capacity(c) + 31) & ~static_cast<int64_t>(31); }
 
@@ -78,7 +82,7 @@ AttnLayout attn_layout(const qkv_plan* plan, const qkv_paged_kv* c, bool weights
     const size_t rows = static_cast<size_t>(c->n_seq) * plan->d.n_head;
     const size_t hd = plan->d.head_dim <= 64 ? 64 : plan->d.head_dim <= 128 ? 128 : 256;  // as the kernels pad it
     l.part = up256(3 * kAttnMaxCtas * sizeof(uint32_t));
-    static_assert(3 * kAttnMaxCtas * sizeof(uint32_t) <= 4096, "the counters are in what a caller has to zero");
+    static_assert(3 * kAttnMaxCtas * sizeof(uint32_t) <= kCounterBytes, "the counters are in what a caller has to zero");
     l.lse2 = l.part + up256(sizeof(float) * 2 * kAttnMaxCtas * kAttnHeads * (hd + 2));
     l.scores = l.lse2 + (weights ? up256(sizeof(float) * rows) : 0);
     l.total = l.scores + (weights ? up256(sizeof(float) * rows * score_stride(c)) : 0);
@@ -237,7 +241,7 @@ void rows_params(const qkv_plan* plan, const qkv_paged_kv* c, int32_t nt, PagedR
 struct RowsLayout {
     RowsShape shape;
     int32_t per_block, blocks, part_tokens, tile_tokens, max_tiles;
-    size_t attn, total, q_high, q_low, q_unscale, tiles, starts, row_end, row_tile, pieces, part, prefix_out, prefix_lse, own_out, own_lse, bytes;
+    size_t total, q_high, q_low, q_unscale, tiles, starts, row_end, row_tile, pieces, part, prefix_out, prefix_lse, own_out, own_lse, bytes;
 };
 // attn_bytes: of qkv_attn_step's workspace in front (prefix); 0: prompt.
 RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t attn_bytes, const RowsShape& shape) {
@@ -251,14 +255,13 @@ RowsLayout rows_layout(const PagedRowsParams& p, const qkv_paged_kv* c, size_t a
     l.tile_tokens = l.part_tokens * (l.shape.rows / l.shape.part_rows);
     const int64_t tiles = prefix ? c->n_seq : p.nt / l.tile_tokens + static_cast<int64_t>(c->n_seq);
     l.max_tiles = static_cast<int32_t>(tiles);
-    size_t at = up256(attn_bytes);
+    size_t at = prefix ? up256(attn_bytes) : kCounterBytes;
     auto take = [&](size_t n) {
         const size_t here = at;
         at += up256(n);
         return here;
     };
     const size_t rows = static_cast<size_t>(c->n_seq) * p.nh;
-    l.attn = 0;
     l.total = take(2 * sizeof(int64_t));
     l.tiles = take(tiles * sizeof(RowTile));
     l.starts = take(prefix ? 4 * static_cast<size_t>(c->n_seq) : 0);
