@@ -570,7 +570,8 @@ qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const 
  *   the slots j in [max(0, e - window), e),  e = len - n + i + 1  (window 0: from 0),
  * and out and lse are those of qkv_attn_step, row by row.  A token with e <= 0 gets zeros (lse -inf).  What lies in slots
  * that a token does not see, infinities and NaN too, does not change its row.
- * d_first must not decrease; a pair that does, or lies outside [0, nt], is flagged (bit 2) and its sequence skipped.
+ * d_first must not decrease; a pair that does, lies outside [0, nt] or begins below an earlier entry (whose rows might be
+ * another sequence's) is flagged (bit 2) and its sequence skipped.
  * Rows before d_first[0] and from d_first[n_seq] on are left as they were.
  * Scores, softmax and sums are f32.  With out F32, q, the softmax weights and an f32 cache's rows keep 22 bits or more;
  * with out BF16 and an f16 cache, q (scaled by a power of two for each row) and the softmax weights are rounded to f16,

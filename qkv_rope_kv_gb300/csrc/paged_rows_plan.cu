@@ -35,6 +35,25 @@ __device__ __forceinline__ T scan(T v, T& sum, T* warp_s) {
     return before + incl - v;
 }
 
+// The largest value of the CTA's threads up to this one, and of all (in `all`); all threads call.
+__device__ __forceinline__ int max_scan(int v, int& all, int* warp_s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = max(v, up);
+    }
+    __syncthreads();  // the last call's values have been read
+    if (lane == 31) warp_s[warp] = v;
+    __syncthreads();
+    all = warp_s[0];
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) v = max(v, warp_s[w]);
+        all = max(all, warp_s[w]);
+    }
+    return v;
+}
+
 // For the tensor cores: q as f16, scaled by a power of two for each row into [2^13, 2^14) where the remainders are far from
 // f16's subnormals, and the remainders; and by what scores are to be multiplied to be in log2 terms.  A warp a row, as
 // many bytes as q has (or half as many again); rows that belong to no sequence too.
@@ -108,19 +127,36 @@ __device__ __forceinline__ void convert_q(const PagedRowsParams& p) {
 __global__ void __launch_bounds__(kPlanThreads) plan_prompt_kernel(const __grid_constant__ PagedRowsParams p) {
     __shared__ int off_s[kPlanThreads + 1], first_s[kPlanThreads], n_s[kPlanThreads], len_s[kPlanThreads];
     __shared__ int64_t warp_s[kPlanThreads / 32];
+    __shared__ int top_s[kPlanThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x > 0) return convert_q(p);
     const int per_tile = p.tile_tokens;
     int64_t length = 0, tiles = 0;
+    int top = 0;        // the largest of d_first before this round
+    bool fell = false;  // whether it has decreased
     for (int b0 = 0; b0 < p.c.n_seq; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
-        int count = 0;
+        int count = 0, a = 0, e = 0;
         if (b < p.c.n_seq) {
-            const int a = p.first[b], e = p.first[b + 1];
+            a = p.first[b];
+            e = p.first[b + 1];
+        }
+        // Behind a decrease a pair may be in order and still begin below where another ended: two sequences with the same rows.
+        // (Only looked for there: a prefix maximum of every call's d_first.)
+        int over = a;
+        if (__syncthreads_or(e < a && b < p.c.n_seq) || fell) {
+            int all;
+            over = max(max_scan(b < p.c.n_seq ? a : 0, all, top_s), top);
+            top = max(top, all);
+            fell = true;
+        } else if (b0 + kPlanThreads < p.c.n_seq) {
+            top = p.first[b0 + kPlanThreads - 1];
+        }
+        if (b < p.c.n_seq) {
             int n = e - a;
-            if (a < 0 || e < a || e > p.nt) {
-                flag_bad(kFlagIndexRange, a < 0 ? a : e);
+            if (a < 0 || e < a || e > p.nt || a < over) {
+                flag_bad(kFlagIndexRange, a < 0 || a < over ? a : e);
                 n = 0;
             }
             first_s[threadIdx.x] = a;
@@ -132,11 +168,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prompt_kernel(const __grid_
         off_s[threadIdx.x] = static_cast<int>(scan<int64_t>(count, here, warp_s));
         if (threadIdx.x == 0) off_s[kPlanThreads] = static_cast<int>(here);
         __syncthreads();
-        // d_first that goes up and down could name more tiles than rows: no more than there is room for
-        if (here > p.max_tiles - tiles) {
-            if (threadIdx.x == 0) flag_bad(kFlagIndexRange, p.first[b0]);
-            here = p.max_tiles - tiles;
-        }
         for (int64_t t0 = 0; t0 < here; t0 += kPlanThreads) {
             const int t = static_cast<int>(t0) + threadIdx.x;
             RowTile x = {};
