@@ -386,7 +386,9 @@ qkv_status prompt_attn(const qkv_plan* plan, const qkv_paged_kv* cache, const qk
     p.first = a->d_first;
     p.lens = a->d_lens;
     p.scale = a->scale;
-    p.window = a->window;
+    // one of the capacity or more hides nothing; a smaller one stays within 32 bits where it is taken off a token's end (which
+    // may lie below 0 by as many as nt)
+    p.window = a->window >= capacity(cache) ? 0 : a->window;
     p.out = a->out;
     p.out_stride = a->out_stride;
     p.lse = a->lse;

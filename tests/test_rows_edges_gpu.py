@@ -74,3 +74,26 @@ def test_a_decrease_far_before(qkv):
     want, _, bound, _ = ref.rows_ref(c.k, c.v, x[995:1000], places[995:1000], 0.125, nh, nkv, hd, False)
     close(got[995:1000], want, bound, "the long one")
     assert (got[1300:] == 77.0).all()
+
+
+@pytest.mark.parametrize("kv,hd", [("f16", 128), ("f32", 64)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40, 96, 95])
+def test_windows_as_large_as_the_cache(qkv, kv, hd, window):
+    """The capacity is 96 slots; some tokens' ends lie below 0."""
+    import torch
+    rng = np.random.default_rng(13)
+    nh, nkv, page, new, lens = 4, 2, 16, [70, 50], [20, 96]
+    c = paged_reference.Cache(rng, 2, nkv, hd, kv, page, 6, lens=lens)
+    plan = make_plan(nh, nkv, hd, kv)
+    cache = Q.PagedKv(plan, *pools_of(c), dev(c.table))
+    first, nt = np.int32([0, 70, 120]), 120
+    x = rng.standard_normal((nt, nh * hd)).astype(np.float32)
+    q, o = buffers(nt, nh * hd, x, "f32", 0)
+    lse = torch.full((nt, nh), 55.0, device="cuda")
+    ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, nt), dtype=torch.uint8, device="cuda")
+    Q.qkv_prompt_attn_step(plan, cache, q, dev(first), dev(c.lens), 0.1, o, ws, window=window, lse=lse)
+    torch.cuda.synchronize()
+    assert Q.qkv_check_device_error()[0] == 0
+    want, wl, bound, bl = ref.rows_ref(c.k, c.v, x, ref.prompt_places(c, first, lens, nt, window), 0.1, nh, nkv, hd, False)
+    close(o.cpu().numpy(), want, bound, "out")
+    close(lse.cpu().numpy(), wl, bl, "lse")
