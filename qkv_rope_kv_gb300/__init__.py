@@ -99,6 +99,7 @@ class qkv_rope_desc(ctypes.Structure):
 # qkv_paged_store_args, qkv_attn_args and qkv_evict_args, field by field: packing one and passing its
 # bytes costs a third of converting as many ctypes arguments.
 _ROPE_ARGS = struct.Struct("@PqPqPiiii")
+_ROPE_DESC = struct.Struct("@iiiiddddddP")  # (a ctypes structure would cut a number that does not fit)
 _STORE_ARGS = struct.Struct("@PqiiPPPPPPPqf4x")
 _ATTN_ARGS = struct.Struct("@PqPPqPPNfiii")
 _PROMPT_ARGS = struct.Struct("@PqPPPqPPNfiii")
@@ -541,11 +542,14 @@ def qkv_rope_create(head_dim: int, theta: float, rot_dim: int | None = None, lay
     load()
     rot_dim = head_dim if rot_dim is None else rot_dim
     table = None
-    if divisors is not None:
-        table = (ctypes.c_double * len(divisors))(*divisors)
-        if len(divisors) != rot_dim // 2:
-            raise QkvError(QKV_ERR_INVALID_ARG, "divisors must be rot_dim/2 = %d numbers (got %d)" % (rot_dim // 2,
-                                                                                                 len(divisors)))
+    try:
+        _ROPE_DESC.pack(head_dim, rot_dim, layout, scaling, theta, factor, orig_ctx, low, high, magnitude, 0)
+        if divisors is not None:
+            table = (ctypes.c_double * len(divisors))(*divisors)
+    except (struct.error, OverflowError, TypeError) as e:
+        _unpackable(e)
+    if table is not None and len(table) != rot_dim // 2:
+        raise QkvError(QKV_ERR_INVALID_ARG, "divisors must be rot_dim/2 = %d numbers (got %d)" % (rot_dim // 2, len(table)))
     d = qkv_rope_desc(head_dim, rot_dim, layout, scaling, theta, factor, orig_ctx, low, high, magnitude,
                       ctypes.cast(table, ctypes.c_void_p))
     h = ctypes.c_void_p()
@@ -567,8 +571,11 @@ def qkv_rope_step(rope: Rope, x, positions, out, inverse: bool = False, stream=N
     nt, width = shape
     src, src_stride = _rows(x, "x", dtype, shape, dev)
     to, to_stride = _rows(out, "out", dtype, shape, dev)
-    args = _ROPE_ARGS.pack(src, src_stride, to, to_stride, _tensor(positions, "positions", rope.index_type, (nt,), dev),
-                           kind, nt, width // rope.head_dim, bool(inverse))
+    try:
+        args = _ROPE_ARGS.pack(src, src_stride, to, to_stride, _tensor(positions, "positions", rope.index_type, (nt,), dev),
+                               kind, nt, width // rope.head_dim, bool(inverse))
+    except (struct.error, OverflowError) as e:
+        _unpackable(e)
     _check(_lib.qkv_rope_step(rope.handle, args, rope.current_stream(dev) if stream is None else _stream(stream)))
 
 
@@ -686,6 +693,10 @@ def qkv_attn_step(plan: Plan, cache: PagedKv, q, lens, scale: float, out, worksp
 
 def qkv_prompt_attn_workspace_bytes(plan: Plan, cache: PagedKv, nt: int) -> int:
     out = ctypes.c_size_t()
+    try:
+        struct.pack("@i", nt)
+    except struct.error as e:
+        _unpackable(e)
     _check(_lib.qkv_prompt_attn_workspace_bytes(plan.handle, cache.address, nt, ctypes.byref(out)))
     return out.value
 
