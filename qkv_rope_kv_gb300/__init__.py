@@ -663,6 +663,8 @@ def qkv_paged_store_step(plan: Plan, cache: PagedKv, Y, bias, q_norm_w, k_norm_w
 def qkv_paged_store_rope_step(plan: Plan, cache: PagedKv, rope: Rope, Y, bias, q_norm_w, k_norm_w, eps: float, positions,
                               seqs, slots, q, stream=None):
     """qkv_paged_store_step with ``rope`` in place of the plan's rotation."""
+    if rope is None:
+        raise QkvError(QKV_ERR_INVALID_ARG, "rope is None")
     qkv_paged_store_step(plan, cache, Y, bias, q_norm_w, k_norm_w, eps, positions, seqs, slots, q, stream, rope)
 
 

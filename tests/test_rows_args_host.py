@@ -51,3 +51,9 @@ def test_workspace_of_too_many_tokens(nt):
     assert q.qkv_prompt_attn_workspace_bytes(plan(), paged, 5) > 0
     with pytest.raises(q.QkvError):
         q.qkv_prompt_attn_workspace_bytes(plan(), paged, nt)
+
+
+def test_store_with_no_rope():
+    """None is not the plan's rotation here."""
+    with pytest.raises(q.QkvError):
+        q.qkv_paged_store_rope_step(plan(), None, None, None, None, None, None, 0.0, None, None, None, None)
