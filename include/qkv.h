@@ -576,8 +576,9 @@ qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const 
  * Scores, softmax and sums are f32.  With out F32, q, the softmax weights and an f32 cache's rows keep 22 bits or more;
  * with out BF16 and an f16 cache, q (scaled by a power of two for each row) and the softmax weights are rounded to f16,
  * 2^-11 of themselves at most: less than out's own rounding as long as |scale| * sum_d |q_d K_d| stays below about 8.
- * On an f16 cache the tensor cores make the sums, in f32 but cut off towards zero at each 16 products (out F32: 256
- * slots at a time, whose sums are added to each other rounded to nearest; 1e-6 of the result over 30000 slots).
+ * On an f16 cache the tensor cores make the sums, in f32 but cut off towards zero at each 16 products.  Out F32 has 256 slots
+ * in one such sum, out BF16 32768, of which less than 2^-12 is lost; they are added to each other rounded to nearest
+ * (out F32: 1e-6 of the result over 30000 slots).
  * |V| (f32) times the number of slots is to stay below the largest f32.
  * Work is split over the GPU and joined in a fixed order: results do not depend on timing.  The workspace may hold
  * anything and is not shared by calls that overlap on the GPU; its first 4096 bytes are left as they are, so it may be that of

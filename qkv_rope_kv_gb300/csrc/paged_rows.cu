@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
     const bool q_vec = ((reinterpret_cast<uintptr_t>(p.q) | static_cast<uintptr_t>(p.q_stride * 4) | static_cast<uintptr_t>(p.hd * 4)) & 15u) == 0;
     using B = Block<KT, HDP>;
     constexpr bool kAhead = B::kPieces <= 4;  // there are registers for it
-    Walk w;
+    Walk<> w;
     if (!w.begin(p)) return;
     if (tid == 0) note_none(p);
     Piece piece;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HDP>::kCtas) paged_rows_any_ke
             const int r = ty + 16 * i;
             const int row = t.row0 + r / p.per_block, g = r % p.per_block, h = kv * G + g0 + g;
             if (r >= rows || g >= heads) continue;
-            if (piece.whole()) {
+            if (w.whole(piece)) {
                 const bool empty = lo_s[r] >= hi_s[r];
                 const float inv = empty ? 0.f : 1.f / l[i];
                 const int64_t at = p.first ? row * p.out_stride + static_cast<int64_t>(h) * p.hd

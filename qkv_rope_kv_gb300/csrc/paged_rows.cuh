@@ -28,7 +28,7 @@ struct Piece {
     int tile, head;  // head: kv head and block of its q heads
     int from, to;
     bool first;      // the tile lies over the CTA's beginning
-    __device__ __forceinline__ bool whole() const { return from == 0 && to == t.units; }
+    bool begin, end, all;  // where pieces are limited: the first, the last of the tile's units in the CTA; these are all it has
 };
 
 __device__ __forceinline__ RowTile load_tile(const PagedRowsParams& p, int i) {
@@ -42,10 +42,15 @@ __device__ __forceinline__ RowTile load_tile(const PagedRowsParams& p, int i) {
     return t;
 }
 
-// The units of one CTA, piece by piece.  Every warp walks for itself; all its lanes call together.
+// The units of one CTA, piece by piece, of MOST units at most.  Every warp walks for itself; all its lanes call together.
+template <int MOST = 0x7fffffff>
 struct Walk {
+    static constexpr bool kLimited = MOST < 0x7fffffff;
     int64_t at, end, per_head, share;
     int tiles, tile, head;
+    // Whether the CTA has all of the tile; and this piece is the last of it.
+    static __device__ __forceinline__ bool all(const Piece& x) { return kLimited ? x.all : x.from == 0 && x.to == x.t.units; }
+    static __device__ __forceinline__ bool whole(const Piece& x) { return all(x) && (!kLimited || x.end); }
     __device__ __forceinline__ bool begin(const PagedRowsParams& p) {
         per_head = __ldcg(p.total);
         tiles = static_cast<int>(__ldcg(p.total + 1));
@@ -80,9 +85,20 @@ struct Walk {
             x.tile = tile++;
             if (x.t.units == 0) continue;
             x.head = head;
+            const int stop = static_cast<int>(min(static_cast<int64_t>(x.t.units), end - start));
             x.from = static_cast<int>(min(at - start, static_cast<int64_t>(x.t.units)));
-            x.to = static_cast<int>(min(static_cast<int64_t>(x.t.units), end - start));
+            x.to = kLimited && stop - x.from > MOST ? x.from + MOST : stop;
             x.first = start <= share * blockIdx.x;
+            if (kLimited) {
+                x.begin = at == max(start, share * blockIdx.x);
+                x.end = x.to == stop;
+                x.all = start >= share * blockIdx.x && stop == x.t.units;
+                if (!x.end) {  // the same tile again
+                    at = start + x.to;
+                    --tile;
+                    return true;
+                }
+            }
             at = start + x.t.units + tile_cost(p, x.t);
             if (x.from < x.to) return true;  // else only the tile's end is this CTA's
         }
@@ -118,8 +134,9 @@ __device__ __forceinline__ float* part_o(const PagedRowsParams& p, float* part, 
 
 // For the join: the CTA in which a tile begins notes how many CTAs have parts of it; one thread, first for no piece.
 __device__ __forceinline__ void note_none(const PagedRowsParams& p) { p.pieces[blockIdx.x].parts = 0; }
-__device__ __forceinline__ void note_piece(const PagedRowsParams& p, const Walk& w, const Piece& x) {
-    if (x.from > 0 || x.to == x.t.units) return;
+template <typename W>
+__device__ __forceinline__ void note_piece(const PagedRowsParams& p, const W& w, const Piece& x) {
+    if (x.from > 0 || w.all(x)) return;
     RowPiece r = {};
     r.start = x.head * w.per_head + x.t.start;
     r.tile = x.tile;

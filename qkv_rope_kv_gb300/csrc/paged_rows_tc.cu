@@ -52,6 +52,9 @@ constexpr int kControlBytes = 2560;  // barriers and small tables, behind the ch
 // largest are not).
 constexpr float kMostWeight = 60000.f;
 constexpr int kFold = 2;       // SPLIT: blocks that are summed in one accumulator before it is added to the others' sum
+// out BF16: blocks of a piece, whose sums are added to those of the tile's pieces before it.  One accumulator for 262144
+// slots of values above zero made results 1e-3 too small, as much as the rounding to bf16 is off; 32768 slots lose 1.3e-4.
+constexpr int kMostBlocks = 256;
 // Units that a tile's beginning and end take for 128 rows.  (0, 3 and 6 gave 71, 60 and 65 us for 32 sequences of four tokens;
 // 0, 3 and 5 of them 679, 550 and 566 for 8191 tokens, whose tiles have twice as many rows.)
 constexpr int kTileCost = 3;
@@ -482,6 +485,30 @@ __device__ __noinline__ void mend_rows(const PagedRowsParams& p, int warps, int 
     }
 }
 
+// out BF16: to a row's sums (of V in tensor memory, l) and maximum, those of the tile's pieces before this one, which are where
+// its part would be.  The warp's lanes together.
+__device__ __noinline__ float2 add_before(const PagedRowsParams& p, float* part, int row, uint32_t o_at, float m, float l, bool mine) {
+    const float2 ml = mine ? *part_ml(part, row) : make_float2(-CUDART_INF_F, 0.f);
+    const float4* sum = reinterpret_cast<const float4*>(part_o(p, part, row));
+    const float top = fmaxf(m, ml.x), keep = m == top ? 1.f : ex2(m - top), f = ml.x == top ? 1.f : ex2(ml.x - top);
+    for (int c = 0; c < p.hd; c += 16) {
+        uint32_t v[16];
+        tm_ld16(o_at + c, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 y = mine ? sum[c / 4 + k] : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[4 * k] = __float_as_uint(fmaf(y.x, f, __uint_as_float(v[4 * k]) * keep));
+            v[4 * k + 1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(v[4 * k + 1]) * keep));
+            v[4 * k + 2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(v[4 * k + 2]) * keep));
+            v[4 * k + 3] = __float_as_uint(fmaf(y.w, f, __uint_as_float(v[4 * k + 3]) * keep));
+        }
+        tm_st16(o_at + c, v);
+    }
+    tc_wait_st();
+    return make_float2(top, fmaf(ml.y, f, l * keep));
+}
+
 template <bool SPLIT, int NCH>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_rows_tc_kernel(const __grid_constant__ PagedRowsParams p, const __grid_constant__ CUtensorMap map_k,
@@ -536,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
 
     const int G = p.nh / p.nkv;
-    Walk w;
+    Walk<SPLIT ? 0x7fffffff : kMostBlocks> w;
     Piece x;
     const bool work = w.begin(p);
     if (work && tid == 0) note_none(p);
@@ -736,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pair_any(quarter, false);
                 l += ctl.top[side ^ 1][r];
                 const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
-                const bool whole = x.whole(), empty = see_lo >= see_hi;
+                const bool whole = w.whole(x), empty = see_lo >= see_hi;
                 const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
                 float* part = part_of(p, blockIdx.x, x.first);
                 if (!whole) to = part_o(p, part, r);
@@ -933,9 +960,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (busy) {
                 const bool put = mine && ok;  // (nothing is written where a wait ran out)
                 const bool poison = ctl.poison[piece % kPoisonRing] == static_cast<uint32_t>(piece);
-                const bool whole = x.whole(), empty = see_lo >= see_hi;
-                const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
+                const bool whole = w.whole(x), empty = see_lo >= see_hi;
                 float* part = part_of(p, blockIdx.x, x.first);
+                m -= kShift;
+                if (!x.begin) {
+                    const float2 ml = add_before(p, part, t * kHalf + r, o_at, m, l, mine);
+                    m = ml.x;
+                    l = ml.y;
+                }
+                const float inv = !whole ? 1.f : empty ? 0.f : 1.f / l;  // (a row that sees nothing has sums of zero)
                 // Results go to memory through q's place, by rows of a warp: 16 bytes a lane of neighbouring lanes instead of a
                 // row a lane, which took 7000 cycles of a tile.
                 const int es = whole && p.first && p.out_bf16 ? 2 : 4;
@@ -1000,8 +1033,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           live ? min(see_hi, tile.lo + x.to * kBlock) : 0, to, es);
                 if (put) {
                     float* lse = p.first ? p.lse : p.prefix_lse;
-                    if (!whole) *part_ml(part, t * kHalf + r) = make_float2(m - kShift, l);
-                    else if (lse) lse[static_cast<int64_t>(row) * p.nh + h_row] = lse_of(m - kShift, l, empty);
+                    if (!whole) *part_ml(part, t * kHalf + r) = make_float2(m, l);
+                    else if (lse) lse[static_cast<int64_t>(row) * p.nh + h_row] = lse_of(m, l, empty);
                 }
                 tc_fence_before();
             }

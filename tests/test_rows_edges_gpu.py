@@ -97,3 +97,105 @@ def test_windows_as_large_as_the_cache(qkv, kv, hd, window):
     want, wl, bound, bl = ref.rows_ref(c.k, c.v, x, ref.prompt_places(c, first, lens, nt, window), 0.1, nh, nkv, hd, False)
     close(o.cpu().numpy(), want, bound, "out")
     close(lse.cpu().numpy(), wl, bl, "lse")
+
+
+@pytest.mark.parametrize("page", [64, 12])  # copied by boxes, and row by row
+@pytest.mark.parametrize("slots,grow", [(262144, 1.0), (65536, 1.0), (65536 + 128, 3.0)])
+def test_many_slots_in_one_piece(qkv, slots, grow, page):
+    """Out bf16, values above zero: the tensor cores cut less than 2^-23 of a sum off at each 16 slots, always towards zero, so
+    2^-12 is lost over the 32768 that are summed in one accumulator, and no more over any number.  That is looked for in
+    the mean distance from the exact values' own roundings to bf16; other errors, which may move a value by 2^-8 across a
+    rounding's border to either side, leave 2^-8 / sqrt(values) of a mean; 4 times that is allowed."""
+    import torch
+    torch.manual_seed(0)
+    hd, new = 64, 256 * 152                   # every CTA has a whole tile
+    plan = make_plan(1, 1, hd, "f16")
+    per = -(-slots // page)
+    k, v = (torch.randn(per, page, hd, device="cuda").half() for _ in range(2))
+    v.copy_(v.abs())
+    k[per // 2:] *= grow                      # maxima move on the way
+    table = torch.randperm(per, device="cuda").int()[None].contiguous()
+    cache = Q.PagedKv(plan, k, v, table)
+    q = torch.randn(new, hd, device="cuda")
+    o = torch.empty(new, hd, device="cuda", dtype=torch.bfloat16)
+    lse = torch.empty(new, 1, device="cuda")
+    ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, new), dtype=torch.uint8, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    Q.qkv_prompt_attn_step(plan, cache, q, i32(0, new), i32(slots), hd ** -0.5, o, ws, lse=lse)
+    assert Q.qkv_check_device_error()[0] == 0
+    at = torch.arange(7, new, 151, device="cuda")
+    K, V = (x[table[0].long()].view(-1, hd)[:slots].double() for x in (k, v))
+    want = torch.empty(len(at), hd, device="cuda", dtype=torch.float64)
+    most, off = (torch.empty(len(at), 1, device="cuda", dtype=torch.float64) for _ in range(2))
+    for i in range(0, len(at), 32):
+        t = at[i:i + 32]
+        s = q[t].double() @ K.T * hd ** -0.5
+        s.masked_fill_(torch.arange(slots, device="cuda") >= (slots - new + 1 + t)[:, None], -float("inf"))
+        most[i:i + 32] = torch.logsumexp(s, -1, keepdim=True)
+        want[i:i + 32] = torch.softmax(s, -1) @ V
+        # each q element is rounded to f16 (2^-11 of it at most), so a score may be off by 2^-11 scale sum |q_d K_d|, besides the
+        # f32 sums' (hd + 16) 2^-23 of that; log sum exp is off by no more than the scores are, and its own sum's error
+        off[i:i + 32] = (q[t].double().abs() @ K.abs().T).amax(-1, keepdim=True) * hd ** -0.5 * (2.0 ** -11 + (hd + 16) * 2.0 ** -23)
+    got = o[at].double()
+    shrink = ((got - want.bfloat16().double()) * want).sum().item() / (want * want).sum().item()
+    assert abs(shrink) <= 2.0 ** -12 + 4 * 2.0 ** -8 / want.numel() ** 0.5, shrink
+    assert (got - want).norm() <= 2.0 ** -9 * want.norm()  # roundings of all kinds, not only towards zero
+    assert ((lse[at].double() - most).abs() <= off + (slots / 8 + 64) * 2.0 ** -23).all()
+
+
+def test_infinities_in_long_pieces(qkv):
+    """Pieces that are summed in several goes: an infinity of an earlier or a later go reaches all rows, other columns keep
+    their bits."""
+    import torch
+    torch.manual_seed(1)
+    hd, new, slots, page = 64, 256 * 152, 65536, 64
+    plan = make_plan(1, 1, hd, "f16")
+    k, v = (torch.randn(slots // page, page, hd, device="cuda").half() for _ in range(2))
+    cache = Q.PagedKv(plan, k, v, torch.arange(slots // page, device="cuda").int()[None].contiguous())
+    q = torch.randn(new, hd, device="cuda")
+    ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, new), dtype=torch.uint8, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def run():
+        o = torch.empty(new, hd, device="cuda", dtype=torch.bfloat16)
+        Q.qkv_prompt_attn_step(plan, cache, q, i32(0, new), i32(slots), hd ** -0.5, o, ws)
+        assert Q.qkv_check_device_error()[0] == 0
+        return o
+    want = run()
+    first = slots - new                          # the first token's own slot
+    for slot, d, value in ((5, 1, float("inf")), (first - 3, 2, -float("inf")), (first - 2, 60, float("nan")), (7, 61, float("inf")),
+                           (first - 4, 61, -float("inf"))):
+        v.view(-1, hd)[slot, d] = value
+    got = run()
+    assert (got[:, 1] == float("inf")).all() and (got[:, 2] == -float("inf")).all() and torch.isnan(got[:, 60:62]).all()
+    keep = [d for d in range(hd) if d not in (1, 2, 60, 61)]
+    assert torch.equal(got[:, keep].view(torch.int16), want[:, keep].view(torch.int16))
+
+
+def test_long_shared_prefix_in_one_piece(qkv):
+    """The same for sequences on a shared prefix: out bf16 against out f32, whose sums are never in one accumulator for long."""
+    import torch
+    torch.manual_seed(2)
+    nkv, hd, page, B, P = 8, 64, 64, 19 * 256, 131072
+    plan = make_plan(nkv, nkv, hd, "f16")
+    per = P // page
+    k, v = (torch.randn(per + 1, page, nkv * hd, device="cuda").half() for _ in range(2))
+    v.copy_(v.abs())
+    k[per // 2:] *= 2
+    table = torch.full((B, per + 1), -1, dtype=torch.int32, device="cuda")
+    table[0, :per] = torch.randperm(per, device="cuda").int()
+    table[:, per] = per
+    cache = Q.PagedKv(plan, k, v, table)
+    ws = torch.zeros(Q.qkv_prefix_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+    q = torch.randn(B, nkv * hd, device="cuda")
+    full = lambda x: torch.full((B,), x, dtype=torch.int32, device="cuda")  # noqa: E731
+    outs = []
+    for dtype in (torch.float32, torch.bfloat16):
+        o = torch.empty(B, nkv * hd, device="cuda", dtype=dtype)
+        Q.qkv_prefix_attn_step(plan, cache, q, full(P + 9), full(0), full(P), hd ** -0.5, o, ws)
+        assert Q.qkv_check_device_error()[0] == 0
+        outs.append(o.double())
+    want, got = outs
+    shrink = ((got - want.bfloat16().double()) * want).sum().item() / (want * want).sum().item()
+    assert abs(shrink) <= 2.0 ** -12 + 4 * 2.0 ** -8 / want.numel() ** 0.5, shrink
+    assert (got - want).norm() <= 2.0 ** -8 * want.norm()
