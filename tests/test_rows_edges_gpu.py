@@ -6,7 +6,7 @@ import paged_reference
 import qkv_rope_kv_gb300 as Q
 import rows_reference as ref
 from test_paged_gpu import close, dev, make_plan
-from test_rows_gpu import buffers, pools_of
+from test_rows_gpu import attend64, buffers, pools_of
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +199,41 @@ def test_long_shared_prefix_in_one_piece(qkv):
     shrink = ((got - want.bfloat16().double()) * want).sum().item() / (want * want).sum().item()
     assert abs(shrink) <= 2.0 ** -12 + 4 * 2.0 ** -8 / want.numel() ** 0.5, shrink
     assert (got - want).norm() <= 2.0 ** -8 * want.norm()
+
+
+@pytest.mark.parametrize("kind", ["prompt", "prefix"])
+@pytest.mark.parametrize("q_scale", [2.0, 8.0, 32.0])
+def test_rounded_q_and_weights(qkv, q_scale, kind):
+    """Out bf16 on an f16 cache, scores of standard deviation 2 to 32.  q's elements are off by 2^-11 of themselves at most, to
+    either side, so a score by 2^-11 / sqrt(3) scale |q o K| (2-norm) as a mean square, twice that with the others of its
+    row; a weight by 2^-11 / sqrt(3); the result by 2^-8 / sqrt(3) as bf16.  Out f32 has none of these."""
+    import torch
+    torch.manual_seed(5)
+    nh, nkv, hd, page, n = 8, 1, 128, 64, 4096
+    new = 256 if kind == "prompt" else 32
+    plan = make_plan(nh, nkv, hd, "f16")
+    k, v = (torch.randn(n // page + new, page, hd, device="cuda").half() for _ in range(2))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = q_scale * torch.randn(new, nh * hd, device="cuda")
+    outs = []
+    for dtype in (torch.bfloat16, torch.float32):
+        o = torch.empty(new, nh * hd, device="cuda", dtype=dtype)
+        if kind == "prompt":
+            cache = Q.PagedKv(plan, k, v, torch.arange(n // page, device="cuda").int()[None].contiguous())
+            ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, new), dtype=torch.uint8, device="cuda")
+            Q.qkv_prompt_attn_step(plan, cache, q, i32([0, new]), i32([n]), hd ** -0.5, o, ws)
+            hi = torch.arange(n - new + 1, n + 1, device="cuda")
+        else:  # every sequence has the prefix only
+            table = torch.arange(n // page, device="cuda").int()[None].repeat(new, 1).contiguous()
+            cache = Q.PagedKv(plan, k, v, table)
+            ws = torch.zeros(Q.qkv_prefix_attn_workspace_bytes(plan, cache), dtype=torch.uint8, device="cuda")
+            Q.qkv_prefix_attn_step(plan, cache, q, i32([n] * new), i32([0] * new), i32([n] * new), hd ** -0.5, o, ws)
+            hi = torch.full((new,), n, device="cuda")
+        assert Q.qkv_check_device_error()[0] == 0
+        outs.append(o.view(new, nh, hd).double())
+    K, V = (x[:n // page].view(-1, hd) for x in (k, v))
+    want, most, size = attend64(q.view(new, nh, hd), K, V, hi, hd ** -0.5)
+    spread = ((q.view(new, nh, hd).double() ** 2) @ (K.double() ** 2).T).mean().sqrt().item() * hd ** -0.5
+    rms = (2.0 ** -8 + 2.0 ** -11 + 2 * 2.0 ** -11 * spread) / 3 ** 0.5
+    assert (outs[0] - want).norm() <= rms * want.norm()
+    assert (outs[1] - want).norm() <= (n ** 0.5 + hd ** 0.5 * size.max()) * ref.U * most.norm()  # as in test_long_prompts
