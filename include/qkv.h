@@ -574,8 +574,11 @@ qkv_status qkv_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache, const 
  * another sequence's) is flagged (bit 2) and its sequence skipped.
  * Rows before d_first[0] and from d_first[n_seq] on are left as they were.
  * Scores, softmax and sums are f32.  With out F32, q, the softmax weights and an f32 cache's rows keep 22 bits or more;
- * with out BF16 and an f16 cache, q (scaled by a power of two for each row) and the softmax weights are rounded to f16,
- * 2^-11 of themselves at most: less than out's own rounding as long as |scale| * sum_d |q_d K_d| stays below about 8.
+ * with out BF16 and an f16 cache, q (scaled by a power of two for each row) and the softmax weights are rounded to f16, by
+ * 2^-11 of themselves at most (or 2^-38 of the row's largest q, 2^-31 of its largest weight).  At most a score is then off by
+ * 2^-11 |scale| sum_d |q_d K_d|, which passes out's own rounding (2^-8) at a sum of 8; but most of it cancels: over 4096 slots of
+ * normal numbers it adds 4e-4 of the result (2-norm) where that sum is 15, 7e-4 at 60 and 1.3e-3 at 240, and the rounding to
+ * bf16 takes 1.7e-3.  Out F32 is the form without it (qkv_attn_step keeps 23 bits with either).
  * On an f16 cache the tensor cores make the sums, in f32 but cut off towards zero at each 16 products.  Out F32 has 256 slots
  * in one such sum, out BF16 32768, of which less than 2^-12 is lost; they are added to each other rounded to nearest
  * (out F32: 1e-6 of the result over 30000 slots).
@@ -604,8 +607,10 @@ qkv_status qkv_prompt_attn_step(const qkv_plan* plan, const qkv_paged_kv* cache,
                                 void* stream);
 
 /* qkv_attn_step (without window and add_weight) for sequences that begin alike: the first d_prefix_len[b] slots of
- * sequence b are those of sequence d_share[b] and are read through that one's row of the page table, once for all
- * neighbouring sequences with the same d_share (a sequence that shares nothing names itself, with any prefix length).
+ * sequence b are those of sequence d_share[b] and are read through that one's row of the page table, for neighbouring
+ * sequences with the same d_share together (a sequence that shares nothing names itself, with any prefix length): once for as
+ * many of them as fill a tile of 128 q rows of a kv head (256 with out BF16; 64 where the tensor cores are not used: an f32
+ * cache, heads above 128 or not of a multiple of 16, pools that are not 16-byte aligned).
  * The slots from there to d_lens[b] are read through b's own row, whose entries below may hold anything.  A prefix
  * need not end on a page's border, nor a sequence's length reach its prefix's end: it then sees only so many of its slots.
  * A d_prefix_len outside [0, capacity] is flagged (bit 2) and counts as 0; a d_share outside [0, n_seq) is flagged and

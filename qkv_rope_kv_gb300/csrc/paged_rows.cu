@@ -4,7 +4,7 @@
 // s_j = scale * q.K_j, running maximum m and sum l of each row, out = sum p_j V_j / l, scores in log2 terms.  A tile of 64
 // rows goes over blocks of 64 slots: both products are made by plain f32 multiply-adds from shared memory, each thread 4 x 4
 // scores and 4 rows x hd / 16 columns of the sums.  Multiply-adds bound it (and their operands' reads from shared memory) where
-// there are many rows; a few, 17 tokens of 14 heads over 2, take 17.7 us with the plan and the join: a chain of latencies.
+// there are many rows; a few, 17 tokens of 14 heads over 2, take 17.5 us with the plan and the join: a chain of latencies.
 #include "paged_rows.cuh"
 
 namespace {

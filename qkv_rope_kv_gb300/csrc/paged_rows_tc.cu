@@ -9,8 +9,9 @@
 //   out F32, "SPLIT"  a tile has 128 rows, one stream, whose S is there twice: a block's scores are made during the softmax of
 //                     the last one's
 // SPLIT, q is kept as the sum of two f16 (rounded, and the remainder rounded), so are the weights, both
-// products are made twice, and 22 bits of each are kept.  For out BF16 everything is rounded once: 2^-11, an eighth of what
-// out's rounding takes.  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are 2^(s - m + kShift), m
+// products are made twice, and 22 bits of each are kept.  For out BF16 everything is rounded once, by 2^-11 at most, which adds
+// 4e-4 to the 1.7e-3 that out's rounding takes (scores of standard deviation 2) and halves the time (8191 tokens of 10 heads over 2:
+// 168 us and 316).  q is scaled by a power of two for each row, into [2^13, 2^14); the weights are 2^(s - m + kShift), m
 // being the maximum or up to some 2^9 below it.
 //   warps 0-3, 4-7   softmax: S out of tensor memory, P back into it, O rescaled where the maximum has to move; at the end O / l
 //                    to memory.  A row a thread of a stream each, P in two halves so that its product begins early; SPLIT: a
@@ -20,9 +21,9 @@
 //                    Pages of a multiple of 8 slots: 12 asks for boxes of a page's rows by TMA, 13-15 hand them on and
 //                    look at V where that is needed.  Others: all four by cp.async, a row at a time.
 // An MMA of 128 x 128 x 16 takes 64 cycles, so a block of 128 rows takes 1024, and 2048 SPLIT.  What it takes in fact: 1800 for
-// 8191 new tokens of 40 heads over 8 (510 us; the tensor pipe is busy for 60 % of them), by the chain of a stream's S, softmax
+// 8191 new tokens of 40 heads over 8 (507 us; the tensor pipe is busy for 59 % of them), by the chain of a stream's S, softmax
 // (of which twice 230 cycles bring the scores, 600 make the weights, 270 hand them on) and products; SPLIT about 3800 for 96
-// rows over 32704 slots (79 us, 49 %), by the same chain and the warp that asks for copies.  A CTA's first piece begins some
+// rows over 32704 slots (80 us, 49 %), by the same chain and the warp that asks for copies.  A CTA's first piece begins some
 // 20000 cycles late: its instructions are in no cache yet.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -599,8 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = i < tile.ntok && g < heads;
             const int busy_pairs = (tile.ntok * p.per_block + 31) / 32;
             const bool busy = quarter < busy_pairs;
-            // The tensor cores cut bits off a score's sums too, each towards zero: 2^-23 of it are missing on average (128
-            // columns; log sum exp comes out 6e-7 too small), and given back here.
+            // The tensor cores cut bits off a score's sums too, each towards zero: 2^-23 of it are missing on average, and given
+            // back here.  (Log sum exp over 4096 slots of normal numbers, heads of 16 to 128 columns: off by -0.8 to -1.4 times
+            // 2^-23 of itself without, by -0.4 to 0.2 with it; where all products have one sign, by up to -2.2.)
             const float unscale = mine ? __ldcg(p.q_unscale + row * p.nh + h_row) * (1.f + 1.1920929e-7f) : 1.f;
             int see_lo = 0, see_hi = 0;
             if (mine) row_span(p, tile, i, see_lo, see_hi);

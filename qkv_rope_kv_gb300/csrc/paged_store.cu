@@ -8,8 +8,9 @@
 // Measured (GPU time): one token 2.5 us, 64 of 40 + 2 x 8 heads of 128 with norms 3.1 us, 8191 of them 60.2 us
 // (318.9 MB at 5.3 TB/s, 0.78 of the copy rate; issue slots are 72 % busy).  There, one token per CTA takes
 // 73 us, four 64.5, loads without a branch 73, seven warps 61.7.
-// With a qkv_rope, 8191 of them (pairs of neighbours, bf16) 68.9 us: its angles take a 64-bit product and a sine and cosine of
-// turns instead of a table's factor, and neighbours' pairs lie within a lane, whose sixteen-bit values are taken apart first.
+// With a qkv_rope, 32 tokens of 28 + 2 x 4 heads 2.9 us, 8191 of the above (halves, ramp) 68.8: its angles take a 64-bit product
+// and a sine and cosine of turns instead of a table's factor.  (Issue slots are 58 % busy, DRAM at 0.68 of the copy rate: what
+// bounds it is not established.)
 #include "epilogue_math.cuh"
 #include "paged_common.cuh"
 #include "ptx_sync.cuh"

@@ -3,9 +3,9 @@
 // Pairs (x0, x1) -> (x0 c - x1 s, x0 s + x1 c), every value read and written once, so memory bounds all but a few
 // rows.  A thread takes eight neighbouring values of a head, or four pairs whose halves are apart, and the same ones of
 // several heads of its row: the angles are made once for them, and all its loads are in flight together.
-// Measured (GPU time): one token of 14 + 2 heads of 64 5.0 us (a launch and one trip through position and angle), 1641 tokens of
-// 32 heads of 128 f16, half of each turned, 5.3 us (26.9 MB, in part from L2), 8191 of 48 bf16 heads 34.3 us (201 MB at 5.9 TB/s,
-// 0.87 of the copy rate; issue slots are 58 % busy).
+// Measured (GPU time in a graph): one token of 14 + 2 heads of 64 1.6 us (one trip through position and angle; a call takes the
+// host 5), 1641 tokens of 32 heads of 128 f16, half of each turned, 5.2 us (26.9 MB, in part from L2), 8191 of 48 bf16 heads 33.7
+// us (201 MB at 6.0 TB/s, 0.88 of the copy rate; issue slots are 58 % busy).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
