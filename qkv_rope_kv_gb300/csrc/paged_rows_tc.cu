@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ctl.tmem;
     griddep_wait();
     griddep_launch_dependents();
+    if (tid == 0) note_moved();  // (what came before may have taken long)
 
     const int G = p.nh / p.nkv;
     Walk<SPLIT ? 0x7fffffff : kMostBlocks> w;

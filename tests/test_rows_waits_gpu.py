@@ -58,6 +58,34 @@ def test_pieces_longer_than_the_limit(qkv, name, out):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_a_plan_longer_than_the_limit(qkv, out):
+    """200000 sequences, of which the first and the last have tokens: what comes before the attention does not count."""
+    import torch
+    torch.manual_seed(2)
+    nh, nkv, hd, page, B, n = 8, 4, 64, 16, 200000, 300
+    plan = make_plan(nh, nkv, hd, "f16")
+    per = -(-n // page)
+    k, v = (torch.randn(per, page, nkv * hd, device="cuda").half() for _ in range(2))
+    table = torch.arange(per, device="cuda").int()[None].repeat(B, 1).contiguous()
+    cache = Q.PagedKv(plan, k, v, table)
+    first = torch.full((B + 1,), n, dtype=torch.int32, device="cuda")
+    first[0], first[B] = 0, 2 * n
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = torch.randn(n, nh * hd, device="cuda").repeat(2, 1)
+    ws = torch.empty(Q.qkv_prompt_attn_workspace_bytes(plan, cache, 2 * n), dtype=torch.uint8, device="cuda")
+    o = torch.full((2 * n, nh * hd), float("nan"), dtype=dtypes(out), device="cuda")
+    Q.qkv_test_prompt_attn(plan, cache, q, first, lens, hd ** -0.5, o, ws, wait_limit_us=100)
+    torch.cuda.synchronize()
+    assert Q.qkv_check_device_error()[0] == 0
+    want = torch.empty_like(o[:n])
+    one = Q.PagedKv(plan, k, v, table[:1].contiguous())
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    Q.qkv_prompt_attn_step(plan, one, q[:n], i32(0, n), i32(n), hd ** -0.5, want, ws)
+    for got in (o[:n], o[n:]):  # (other CTAs may begin in the middle of a tile: the same up to the sums' order)
+        assert (got.float() - want.float()).norm() <= (2.0 ** -8 if out == "bf16" else 2.0 ** -18) * want.float().norm()
+
+
 @pytest.mark.parametrize("page", [64, 12])  # copied by boxes, and row by row
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_withheld_end_is_flagged(qkv, out, page):
